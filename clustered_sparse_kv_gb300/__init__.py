@@ -47,7 +47,20 @@ class wi_config(ctypes.Structure):
     ]
 
 
+class wi_paged_config(ctypes.Structure):
+    _fields_ = [
+        ("n_q_heads", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+        ("page_size", ctypes.c_int), ("n_pages", ctypes.c_int), ("max_batch", ctypes.c_int),
+        ("max_pages", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+        ("reserved", ctypes.c_int * 3),
+        ("eps", ctypes.c_double), ("rope_scale", ctypes.c_double),
+        ("inv_freq", ctypes.POINTER(ctypes.c_double)),
+    ]
+
+
 _vp = ctypes.c_void_p
+_i32 = ctypes.c_int
+_i64 = ctypes.c_longlong
 _ip = ctypes.POINTER(ctypes.c_int)
 _cfgp = ctypes.POINTER(wi_config)
 _SIGS = {
@@ -73,6 +86,12 @@ _SIGS = {
     "wi_tier_round": [_vp, _vp],
     "wi_tier_stats": [_vp, ctypes.POINTER(ctypes.c_longlong), ctypes.POINTER(ctypes.c_ulonglong), _ip, _ip],
     "wi_tier_tables": [_vp, _vp, _vp],
+    "wi_paged_create": [ctypes.POINTER(wi_paged_config), ctypes.POINTER(_vp)],
+    "wi_paged_check": [_vp],
+    "wi_paged_tables": [_vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp],
+    "wi_paged_write": [_vp, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "wi_paged_attention": [_vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "wi_paged_gather": [_vp, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp],
     "wi_lru_round": [_vp, _vp, ctypes.c_int, ctypes.c_longlong, _vp, _vp, _ip, _vp, _vp, _ip],
 }
 for _name, _args in _SIGS.items():
@@ -81,6 +100,8 @@ for _name, _args in _SIGS.items():
     _f.restype = ctypes.c_int
 lib.wi_free.argtypes = [_vp]
 lib.wi_free.restype = None
+lib.wi_paged_free.argtypes = [_vp]
+lib.wi_paged_free.restype = None
 lib.wi_last_error.argtypes = []
 lib.wi_last_error.restype = ctypes.c_char_p
 lib.wi_lru_new.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int]
@@ -88,7 +109,7 @@ lib.wi_lru_new.restype = _vp
 lib.wi_lru_free.argtypes = [_vp]
 lib.wi_lru_free.restype = None
 
-EXPORTED = sorted([*_SIGS, "wi_free", "wi_last_error", "wi_lru_new", "wi_lru_free"])
+EXPORTED = sorted([*_SIGS, "wi_free", "wi_paged_free", "wi_last_error", "wi_lru_new", "wi_lru_free"])
 
 
 def _check(rc: int):
@@ -118,6 +139,16 @@ def _stream(stream):
     return int(stream)
 
 
+def _new_on(stream, shape, dtype, device, make=torch.empty):
+    """A tensor made on `stream`, so that nothing enqueued elsewhere still uses its memory."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 def make_config(batch, layers, n_q_heads, n_kv_heads, n_ctx, seg_len=8192, clusters_per_seg=512, iters=10,
                 n_sink=4, local_window=64, max_append=0, budget_frac=0.018, budget_k=0, head_dim=128,
                 valsum_bf16=0) -> wi_config:
@@ -135,6 +166,24 @@ def config_from_workload(w, max_append: int | None = None, iters: int | None = N
                        w.iters if iters is None else iters, w.n_sink, w.local_window,
                        (w.decode_steps if w.append else 0) if max_append is None else max_append,
                        w.budget_frac, w.budget_k, w.head_dim)
+
+
+def make_paged_config(n_q_heads, n_kv_heads, page_size, n_pages, max_batch, max_pages, rotary_dim=128,
+                      interleaved=False, inv_freq=None, rope_theta=500000.0, rope_scale=1.0, eps=1e-6,
+                      head_dim=128) -> wi_paged_config:
+    """Shapes of a paged cache.  inv_freq: the rotation's rotary_dim // 2 angles per position (radians);
+    by default rope_theta ** (-2 i / rotary_dim)."""
+    c = wi_paged_config()
+    c.n_q_heads, c.n_kv_heads, c.head_dim = n_q_heads, n_kv_heads, head_dim
+    c.page_size, c.n_pages, c.max_batch, c.max_pages = page_size, n_pages, max_batch, max_pages
+    c.rotary_dim, c.interleaved, c.eps, c.rope_scale = rotary_dim, int(interleaved), eps, rope_scale
+    n = max(rotary_dim, 0) // 2
+    if inv_freq is None:
+        inv_freq = [rope_theta ** (-2.0 * i / rotary_dim) for i in range(n)]
+    if len(inv_freq) != n:
+        raise ValueError(f"inv_freq must have rotary_dim // 2 = {n} values (got {len(inv_freq)})")
+    c.inv_freq = (ctypes.c_double * n)(*[float(f) for f in inv_freq]) if n else None
+    return c
 
 
 # ----------------------------------------------------------- C-named calls ----
@@ -314,6 +363,18 @@ class WaveIndex:
     def adopt(cls, cfg: wi_config, k, v, counts, perm, mu, valsum, stream=None):
         return cls(cfg, k, v, wi_index_import(cfg, k, v, counts, perm, mu, valsum, stream))
 
+    @classmethod
+    def build_paged(cls, cfg: wi_config, cache: "PagedCache", k_pages, v_pages, block_table, kv_len,
+                    init_centroids=None, stream=None):
+        """Build from prompts prefilled into a paged cache: gathers positions [0, n_ctx) of every
+        request into contiguous tensors that the index owns (the pages may be given back once the
+        build has run) and clusters them.  k_pages, v_pages: cfg.layers pools; kv_len: device int32
+        [cfg.batch], each at least n_ctx."""
+        shape = (cfg.batch, cfg.layers, cfg.n_kv_heads, cfg.n_ctx, 128)
+        k, v = (_new_on(stream, shape, torch.bfloat16, k_pages.device) for _ in range(2))
+        cache.gather(k_pages, v_pages, block_table, kv_len, 0, k, v, stream)
+        return cls.build(cfg, k, v, init_centroids, stream)
+
     def decode(self, q: torch.Tensor, k_new=None, v_new=None, out=None, stream=None) -> torch.Tensor:
         if out is None:
             out = torch.empty((self.cfg.batch, self.cfg.layers, self.cfg.n_q_heads, 128), dtype=torch.float32,
@@ -388,3 +449,129 @@ class WaveIndex:
         except Exception:
             pass
 
+
+
+_BF16 = (torch.bfloat16, torch.int16)
+_INT32 = (torch.int32,)
+_FP32 = (torch.float32,)
+
+
+class PagedCache:
+    """Owns one paged-cache handle (wi_paged_*): pages and slots of a step from its requests' lengths,
+    norms and rotation written into the pools, attention over them, and the gather of their rows.
+
+    Made on the current CUDA device; tensors are the caller's, on that device, bf16 ones as
+    torch.bfloat16 or their int16 bit patterns.  One layer's pools are
+    k_pages, v_pages [n_pages][n_kv_heads][page_size][128]."""
+
+    def __init__(self, cfg: wi_paged_config):
+        self.handle = None
+        h = _vp()
+        _check(lib.wi_paged_create(ctypes.byref(cfg), ctypes.byref(h)))
+        self.handle = h.value
+        self.cfg = cfg
+        self.device = torch.cuda.current_device()
+        self.n_q_heads, self.n_kv_heads = cfg.n_q_heads, cfg.n_kv_heads
+        self.page_size, self.n_pages = cfg.page_size, cfg.n_pages
+        self.max_batch, self.max_pages = cfg.max_batch, cfg.max_pages
+        self._pool = (cfg.n_pages, cfg.n_kv_heads, cfg.page_size, 128)
+
+    def _arg(self, name, t, kinds, shape):
+        """Data pointer of a contiguous tensor of this device; None in `shape` stands for any size."""
+        if t.dtype not in kinds or t.get_device() != self.device or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {kinds[0]} tensor on cuda:{self.device} "
+                             f"(got {t.dtype} on {t.device}, strides {tuple(t.stride())})")
+        got = t.shape
+        if len(got) != len(shape) or any(a != b and b is not None for a, b in zip(got, shape)):
+            raise ValueError(f"{name} must have shape {shape} (got {tuple(got)})")
+        return t.data_ptr()
+
+    def _heads(self, name, t, heads, n):
+        """Data pointer and token stride of [n][heads][128] with contiguous heads."""
+        if (t.dtype not in _BF16 or t.get_device() != self.device or t.shape != (n, heads, 128) or
+                t.stride(2) != 1 or (heads > 1 and t.stride(1) != 128)):
+            raise ValueError(f"{name} must be a bf16 tensor [{n}][{heads}][128] with contiguous heads on "
+                             f"cuda:{self.device} (got {t.dtype} {tuple(t.shape)} on {t.device}, strides "
+                             f"{tuple(t.stride())})")
+        return t.data_ptr(), t.stride(0)
+
+    def tables(self, ctx_len, new_len, free_pages, n_free, block_table, kv_len, q_start, slots, positions,
+               n_free_out, stream=None):
+        """Pages, slots and positions of a step (wi_paged_tables); every argument an int32 tensor."""
+        a, b, n = self._arg, len(ctx_len), len(slots)
+        if len(block_table) < b:
+            raise ValueError(f"block_table must have a row for each of the {b} requests")
+        _check(lib.wi_paged_tables(
+            self.handle, b, a("ctx_len", ctx_len, _INT32, (b,)), a("new_len", new_len, _INT32, (b,)),
+            a("free_pages", free_pages, _INT32, (None,)), a("n_free", n_free, _INT32, (1,)), len(free_pages),
+            a("block_table", block_table, _INT32, (None, self.max_pages)), a("kv_len", kv_len, _INT32, (b,)),
+            a("q_start", q_start, _INT32, (b + 1,)), a("slots", slots, _INT32, (n,)),
+            a("positions", positions, _INT32, (n,)), n, a("n_free_out", n_free_out, _INT32, (1,)), _stream(stream)))
+
+    def write(self, q, k, v, positions, slots, k_pages, v_pages, q_out=None, q_weight=None, k_weight=None,
+              stream=None):
+        """Norms and rotation of q and k, keys and values into the pools (wi_paged_write); returns q_out
+        [n][n_q_heads][128].  q, k, v: [n][heads][128], views of a fused projection allowed.  slots None:
+        k_pages and v_pages are [n][n_kv_heads][128]."""
+        a, n = self._arg, len(q)
+        if q_out is None:
+            q_out = _new_on(stream, (n, self.n_q_heads, 128), q.dtype, q.device)
+        pool = (n, self.n_kv_heads, 128) if slots is None else self._pool
+        qp, qs = self._heads("q", q, self.n_q_heads, n)
+        kp, ks = self._heads("k", k, self.n_kv_heads, n)
+        vp, vs = self._heads("v", v, self.n_kv_heads, n)
+        _check(lib.wi_paged_write(
+            self.handle, n, qp, qs, kp, ks, vp, vs,
+            None if q_weight is None else a("q_weight", q_weight, _BF16, (128,)),
+            None if k_weight is None else a("k_weight", k_weight, _BF16, (128,)),
+            a("positions", positions, _INT32, (n,)), None if slots is None else a("slots", slots, _INT32, (n,)),
+            a("q_out", q_out, _BF16, (n, self.n_q_heads, 128)), a("k_pages", k_pages, _BF16, pool),
+            a("v_pages", v_pages, _BF16, pool), _stream(stream)))
+        return q_out
+
+    def attention(self, q, k_pages, v_pages, block_table, q_start, kv_len, out=None, lse=None, stream=None):
+        """Attention of a step's tokens over the cache (wi_paged_attention); returns out [n][n_q_heads][128]
+        (rows behind the last request are zero if out was not given)."""
+        a, b, shape = self._arg, len(kv_len), (len(q), self.n_q_heads, 128)
+        if out is None:
+            out = _new_on(stream, shape, q.dtype, q.device, torch.zeros)
+        if len(block_table) < b:
+            raise ValueError(f"block_table must have a row for each of the {b} requests")
+        _check(lib.wi_paged_attention(
+            self.handle, b, shape[0], a("q", q, _BF16, shape), a("k_pages", k_pages, _BF16, self._pool),
+            a("v_pages", v_pages, _BF16, self._pool),
+            a("block_table", block_table, _INT32, (None, self.max_pages)), a("q_start", q_start, _INT32, (b + 1,)),
+            a("kv_len", kv_len, _INT32, (b,)), a("out", out, _BF16, shape),
+            None if lse is None else a("lse", lse, _FP32, shape[:2]), _stream(stream)))
+        return out
+
+    def gather(self, k_pages, v_pages, block_table, kv_len, pos0, k_out, v_out, stream=None):
+        """Rows [pos0, pos0 + n) of every request to k_out, v_out [batch][layers][n_kv_heads][n][128]
+        (wi_paged_gather).  k_pages, v_pages: one pool, or [layers] of them."""
+        a, b = self._arg, len(kv_len)
+        if k_out.dim() != 5:
+            raise ValueError("k_out must have shape [batch][layers][n_kv_heads][n][128]")
+        layers, n = k_out.shape[1], k_out.shape[3]
+        pool = self._pool if k_pages.dim() == 4 and layers == 1 else (layers, *self._pool)
+        shape = (b, layers, self.n_kv_heads, n, 128)
+        if len(block_table) < b:
+            raise ValueError(f"block_table must have a row for each of the {b} requests")
+        _check(lib.wi_paged_gather(
+            self.handle, b, layers, a("k_pages", k_pages, _BF16, pool), a("v_pages", v_pages, _BF16, pool),
+            a("block_table", block_table, _INT32, (None, self.max_pages)), a("kv_len", kv_len, _INT32, (b,)),
+            pos0, n, a("k_out", k_out, _BF16, shape), a("v_out", v_out, _BF16, shape), _stream(stream)))
+        return k_out, v_out
+
+    def check(self):
+        _check(lib.wi_paged_check(self.handle))
+
+    def free(self):
+        if self.handle:
+            lib.wi_paged_free(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass

@@ -16,6 +16,9 @@ enum {
   WI_DEVERR_BAD_ROW = 4,
   WI_DEVERR_TOPK = 8,
   WI_DEVERR_MBAR_TIMEOUT = 16,
+  WI_DEVERR_BAD_PAGE = 32,     // paged cache: a page or slot number outside the pool
+  WI_DEVERR_BAD_LENGTH = 64,   // paged cache: a length or offset out of range
+  WI_DEVERR_NO_PAGES = 128,    // paged cache: a step needs more pages than are free
 };
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }

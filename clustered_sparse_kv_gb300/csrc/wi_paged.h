@@ -1,0 +1,84 @@
+// wi_paged.h -- host-side declarations shared by the paged-cache sources.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "wave_index.h"
+
+constexpr int kPagedMaxBatch = 4096;
+constexpr int kPagedMaxTokens = 1 << 24;  // of a step
+
+// Rotation of a head's pairs: the angle of pair i at position p is p * turn[i] / 2^64 turns, so the whole
+// turns drop out of a 64-bit product and nothing is lost at far positions.
+struct WiRope {
+  unsigned long long turn[64];
+  float scale;       // on cosine and sine
+  int rotary;        // rotated elements, a multiple of 8
+  int interleaved;
+};
+
+// Geometry of a paged cache, derived from wi_paged_config.
+struct WiPagedGeom {
+  int Hq, Hkv, G;    // query heads, kv heads, query heads per kv head
+  int page;          // positions per page
+  int n_pages;
+  int max_batch, max_pages;
+  float eps;
+  WiRope rope;
+};
+
+struct WiPagedTables {
+  const int32_t* ctx_len;
+  const int32_t* new_len;
+  const int32_t* free_pages;
+  const int32_t* n_free;
+  int32_t* block_table;
+  int32_t* kv_len;
+  int32_t* q_start;
+  int32_t* slots;
+  int32_t* positions;
+  int32_t* n_free_out;
+  int batch, free_cap, n_tokens;
+};
+cudaError_t wi_launch_paged_tables(const WiPagedGeom& g, const WiPagedTables& a, int sms, int* err, cudaStream_t st);
+
+struct WiPagedWrite {
+  const void* q;
+  const void* k;
+  const void* v;
+  long long q_stride, k_stride, v_stride;
+  const void* q_weight;
+  const void* k_weight;
+  const int32_t* positions;
+  const int32_t* slots;  // null: k_out / v_out are [n_tokens][Hkv][128]
+  void* q_out;
+  void* k_out;
+  void* v_out;
+  int n_tokens;
+};
+cudaError_t wi_launch_paged_write(const WiPagedGeom& g, const WiPagedWrite& a, int sms, int* err, cudaStream_t st);
+
+struct WiPagedGather {
+  const void* k_pages;
+  const void* v_pages;
+  const int32_t* block_table;
+  const int32_t* kv_len;
+  void* k_out;
+  void* v_out;
+  int batch, layers;
+  long long pos0, n;
+};
+cudaError_t wi_launch_paged_gather(const WiPagedGeom& g, const WiPagedGather& a, int* err, cudaStream_t st);
+
+struct WiPagedAttn {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  const int32_t* block_table;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  void* out;
+  float* lse;
+  int batch, n_tokens;
+};
+cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a, int sms, int* err, cudaStream_t st);

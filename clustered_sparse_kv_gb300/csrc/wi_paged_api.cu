@@ -1,0 +1,276 @@
+// wi_paged_api.cu -- the paged cache's part of the C ABI (include/wave_index.h): argument checks, the
+// handle and its scratch.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <new>
+
+#include "wi_common.cuh"
+#include "wi_internal.h"
+#include "wi_paged.h"
+
+struct wi_paged {
+  WiPagedGeom g{};
+  int device = 0;
+  int sms = 0;
+  int* err = nullptr;
+};
+
+namespace {
+
+int fail(int code, const char* fmt, ...) {
+  char buf[400];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  wi_set_error(buf);
+  return code;
+}
+
+#define WI_CUDA(call)                                                       \
+  do {                                                                      \
+    cudaError_t e_ = (call);                                                \
+    if (e_ != cudaSuccess) {                                                \
+      cudaGetLastError();                                                   \
+      return fail(WI_ECUDA, "%s: %s", #call, cudaGetErrorString(e_));      \
+    }                                                                       \
+  } while (0)
+
+bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
+
+// What every call checks first: the handle, and that its device is the current one.
+int enter(const wi_paged* pc) {
+  wi_set_error("");
+  if (!pc) return fail(WI_EINVAL, "paged cache handle is NULL");
+  int dev = 0;
+  WI_CUDA(cudaGetDevice(&dev));
+  if (dev != pc->device) return fail(WI_EINVAL, "the handle belongs to device %d, device %d is current", pc->device, dev);
+  return WI_OK;
+}
+
+int bad_batch(const wi_paged* pc, int batch) {
+  return fail(WI_EINVAL, "batch (%d) must be in [1, %d]", batch, pc->g.max_batch);
+}
+
+int geom_from_config(const wi_paged_config* c, WiPagedGeom* g) {
+  if (!c) return fail(WI_EINVAL, "config is NULL");
+  if (c->n_q_heads < 1 || c->n_kv_heads < 1 || c->n_q_heads % c->n_kv_heads)
+    return fail(WI_EINVAL, "n_q_heads (%d) must be a positive multiple of n_kv_heads (%d)", c->n_q_heads, c->n_kv_heads);
+  if (c->head_dim != WI_D) return fail(WI_EINVAL, "head_dim must be 128 (got %d)", c->head_dim);
+  if (c->page_size < 16 || c->page_size % 16)
+    return fail(WI_EINVAL, "page_size must be a positive multiple of 16 (got %d)", c->page_size);
+  if (c->n_pages < 1 || c->max_batch < 1 || c->max_pages < 1)
+    return fail(WI_EINVAL, "n_pages, max_batch and max_pages must be >= 1");
+  if (c->rotary_dim < 0 || c->rotary_dim > WI_D || c->rotary_dim % 8)
+    return fail(WI_EINVAL, "rotary_dim must be a multiple of 8 in [0, 128] (got %d)", c->rotary_dim);
+  if (c->interleaved != 0 && c->interleaved != 1) return fail(WI_EINVAL, "interleaved must be 0 or 1");
+  if (c->reserved[0] || c->reserved[1] || c->reserved[2]) return fail(WI_EINVAL, "reserved fields must be zero");
+  if (!(c->eps > 0.0) || !((float)c->eps > 0.f) || !std::isfinite((float)c->eps))
+    return fail(WI_EINVAL, "eps must be a positive fp32 number");
+  if (!std::isfinite((float)c->rope_scale)) return fail(WI_EINVAL, "rope_scale must be finite");
+  if (c->rotary_dim > 0 && !c->inv_freq) return fail(WI_EINVAL, "inv_freq is NULL with rotary_dim > 0");
+  if (c->n_q_heads / c->n_kv_heads > 8)
+    return fail(WI_EUNSUPPORTED, "query heads per kv head must be <= 8 (got %d)", c->n_q_heads / c->n_kv_heads);
+  if (c->n_q_heads > 1024) return fail(WI_EUNSUPPORTED, "n_q_heads must be <= 1024 (got %d)", c->n_q_heads);
+  if (c->max_batch > kPagedMaxBatch)
+    return fail(WI_EUNSUPPORTED, "max_batch must be <= %d (got %d)", kPagedMaxBatch, c->max_batch);
+  // row numbers of a pool and positions of a request are 32-bit
+  if ((double)c->n_pages * c->n_kv_heads * c->page_size >= 2147483648.0)
+    return fail(WI_EUNSUPPORTED, "n_pages * n_kv_heads * page_size must be < 2^31");
+  if ((double)c->max_pages * c->page_size >= 2147483648.0)
+    return fail(WI_EUNSUPPORTED, "max_pages * page_size must be < 2^31");
+  g->Hq = c->n_q_heads;
+  g->Hkv = c->n_kv_heads;
+  g->G = c->n_q_heads / c->n_kv_heads;
+  g->page = c->page_size;
+  g->n_pages = c->n_pages;
+  g->max_batch = c->max_batch;
+  g->max_pages = c->max_pages;
+  g->eps = (float)c->eps;
+  g->rope.scale = (float)c->rope_scale;
+  g->rope.rotary = c->rotary_dim;
+  g->rope.interleaved = c->interleaved;
+  for (int i = 0; i < c->rotary_dim / 2; ++i) {
+    const double f = c->inv_freq[i] / 6.283185307179586476925286766559;  // turns per position
+    if (!std::isfinite(f)) return fail(WI_EINVAL, "inv_freq[%d] is not finite", i);
+    const double part = f - std::floor(f);  // whole turns per position are no rotation
+    // a double's 53 bits fit the 64-bit fraction; 1.0 (a tiny negative f) is a whole turn again
+    g->rope.turn[i] = part >= 1.0 ? 0ull : (unsigned long long)std::ldexp(part, 64);
+  }
+  return WI_OK;
+}
+
+void destroy(wi_paged* pc) {
+  if (pc->err) cudaFree(pc->err);
+  delete pc;
+}
+
+int create_impl(const wi_paged_config* cfg, wi_paged** out) {
+  wi_set_error("");
+  if (!out) return fail(WI_EINVAL, "out is NULL");
+  *out = nullptr;
+  WiPagedGeom g{};
+  const int rc = geom_from_config(cfg, &g);
+  if (rc != WI_OK) return rc;
+  int dev = 0, sms = 0;
+  WI_CUDA(cudaGetDevice(&dev));
+  WI_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  wi_paged* pc = new wi_paged;
+  pc->g = g;
+  pc->device = dev;
+  pc->sms = sms;
+  if (cudaMalloc(reinterpret_cast<void**>(&pc->err), 4) != cudaSuccess ||
+      cudaMemset(pc->err, 0, 4) != cudaSuccess) {
+    cudaGetLastError();
+    destroy(pc);
+    return fail(WI_ENOMEM, "device allocation failed");
+  }
+  *out = pc;
+  return WI_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int wi_paged_create(const wi_paged_config* cfg, wi_paged** out) {
+  try {
+    return create_impl(cfg, out);
+  } catch (...) {
+    if (out) *out = nullptr;
+    return fail(WI_ENOMEM, "host allocation failed");
+  }
+}
+
+int wi_paged_check(wi_paged* pc) {
+  const int rc = enter(pc);
+  if (rc != WI_OK) return rc;
+  WI_CUDA(cudaDeviceSynchronize());
+  int herr = 0;
+  WI_CUDA(cudaMemcpy(&herr, pc->err, 4, cudaMemcpyDeviceToHost));
+  if (!herr) return WI_OK;
+  WI_CUDA(cudaMemset(pc->err, 0, 4));
+  return fail(WI_EDEVICE, "paged cache (flags 0x%x):%s%s%s%s", herr,
+              herr & WI_DEVERR_BAD_PAGE ? " a page or slot outside the pool;" : "",
+              herr & WI_DEVERR_BAD_LENGTH ? " a length or offset out of range;" : "",
+              herr & WI_DEVERR_NO_PAGES ? " more pages needed than are free;" : "",
+              herr & WI_DEVERR_MBAR_TIMEOUT ? " a wait timed out;" : "");
+}
+
+void wi_paged_free(wi_paged* pc) {
+  if (!pc) return;
+  cudaDeviceSynchronize();
+  destroy(pc);
+}
+
+int wi_paged_tables(wi_paged* pc, int batch, const int32_t* ctx_len, const int32_t* new_len,
+                    const int32_t* free_pages, const int32_t* n_free, int free_cap, int32_t* block_table,
+                    int32_t* kv_len, int32_t* q_start, int32_t* slots, int32_t* positions, int n_tokens,
+                    int32_t* n_free_out, void* stream) {
+  const int rc = enter(pc);
+  if (rc != WI_OK) return rc;
+  if (batch < 1 || batch > pc->g.max_batch) return bad_batch(pc, batch);
+  if (n_tokens < 0 || free_cap < 0) return fail(WI_EINVAL, "n_tokens and free_cap must be >= 0");
+  if (!ctx_len || !new_len || !n_free || !block_table || !kv_len || !q_start || !n_free_out ||
+      (free_cap > 0 && !free_pages) || (n_tokens > 0 && (!slots || !positions)))
+    return fail(WI_EINVAL, "a table pointer is NULL");
+  const void* in[4] = {ctx_len, new_len, free_pages, n_free};
+  const void* outs[6] = {block_table, kv_len, q_start, slots, positions, n_free_out};
+  for (int o = 0; o < 6; ++o) {
+    if (misaligned(outs[o], 4)) return fail(WI_EINVAL, "the tables must be 4-byte aligned");
+    for (int i = 0; i < 4; ++i) {
+      if (misaligned(in[i], 4)) return fail(WI_EINVAL, "the tables must be 4-byte aligned");
+      if (outs[o] && outs[o] == in[i]) return fail(WI_EINVAL, "an output is an input's buffer");
+    }
+    for (int p = 0; p < o; ++p)
+      if (outs[o] && outs[o] == outs[p]) return fail(WI_EINVAL, "two outputs are one buffer");
+  }
+  const WiPagedTables a = {ctx_len, new_len, free_pages, n_free,    block_table, kv_len,  q_start,
+                           slots,   positions, n_free_out, batch, free_cap,    n_tokens};
+  const cudaError_t e = wi_launch_paged_tables(pc->g, a, pc->sms, pc->err, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(WI_ECUDA, "paged tables launch: %s", cudaGetErrorString(e));
+  return WI_OK;
+}
+
+int wi_paged_write(wi_paged* pc, int n_tokens, const void* q, long long q_stride, const void* k, long long k_stride,
+                   const void* v, long long v_stride, const void* q_weight, const void* k_weight,
+                   const int32_t* positions, const int32_t* slots, void* q_out, void* k_pages, void* v_pages,
+                   void* stream) {
+  const int rc = enter(pc);
+  if (rc != WI_OK) return rc;
+  const WiPagedGeom& g = pc->g;
+  if (n_tokens < 0) return fail(WI_EINVAL, "n_tokens must be >= 0");
+  if (n_tokens == 0) return WI_OK;
+  if (n_tokens > kPagedMaxTokens) return fail(WI_EUNSUPPORTED, "n_tokens must be <= %d (got %d)", kPagedMaxTokens, n_tokens);
+  if (!q || !k || !v || !positions || !q_out || !k_pages || !v_pages)
+    return fail(WI_EINVAL, "q, k, v, positions, q_out, k_pages and v_pages must be non-NULL");
+  if (misaligned(q, 16) || misaligned(k, 16) || misaligned(v, 16) || misaligned(q_weight, 16) ||
+      misaligned(k_weight, 16) || misaligned(q_out, 16) || misaligned(k_pages, 16) || misaligned(v_pages, 16))
+    return fail(WI_EINVAL, "q, k, v, the weights, q_out and the pools must be 16-byte aligned");
+  if (misaligned(positions, 4) || misaligned(slots, 4)) return fail(WI_EINVAL, "positions and slots must be 4-byte aligned");
+  const long long qw = (long long)g.Hq * WI_D, kw = (long long)g.Hkv * WI_D;
+  if (n_tokens > 1 && (q_stride < qw || k_stride < kw || v_stride < kw || q_stride % 8 || k_stride % 8 || v_stride % 8))
+    return fail(WI_EINVAL, "token strides must be multiples of 8 and at least a token's heads");
+  if (q_out == q && n_tokens > 1 && q_stride != qw)
+    return fail(WI_EINVAL, "q_out may be q only where q's tokens are contiguous");
+  if (k_pages == v_pages) return fail(WI_EINVAL, "k_pages and v_pages are one buffer");
+  const WiPagedWrite a = {q,     k,     v,       q_stride, k_stride, v_stride, q_weight, k_weight, positions,
+                          slots, q_out, k_pages, v_pages,  n_tokens};
+  const cudaError_t e = wi_launch_paged_write(g, a, pc->sms, pc->err, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(WI_ECUDA, "paged write launch: %s", cudaGetErrorString(e));
+  return WI_OK;
+}
+
+int wi_paged_attention(wi_paged* pc, int batch, int n_tokens, const void* q, const void* k_pages,
+                       const void* v_pages, const int32_t* block_table, const int32_t* q_start,
+                       const int32_t* kv_len, void* out, float* lse, void* stream) {
+  const int rc = enter(pc);
+  if (rc != WI_OK) return rc;
+  if (batch < 1 || batch > pc->g.max_batch) return bad_batch(pc, batch);
+  if (n_tokens < 0) return fail(WI_EINVAL, "n_tokens must be >= 0");
+  if (n_tokens == 0) return WI_OK;
+  if (n_tokens > kPagedMaxTokens) return fail(WI_EUNSUPPORTED, "n_tokens must be <= %d (got %d)", kPagedMaxTokens, n_tokens);
+  if (!q || !k_pages || !v_pages || !block_table || !q_start || !kv_len || !out)
+    return fail(WI_EINVAL, "q, the pools, block_table, q_start, kv_len and out must be non-NULL");
+  if (misaligned(q, 16) || misaligned(k_pages, 16) || misaligned(v_pages, 16) || misaligned(out, 16))
+    return fail(WI_EINVAL, "q, the pools and out must be 16-byte aligned");
+  if (misaligned(block_table, 4) || misaligned(q_start, 4) || misaligned(kv_len, 4) || misaligned(lse, 4))
+    return fail(WI_EINVAL, "the tables and lse must be 4-byte aligned");
+  if (out == q) return fail(WI_EINVAL, "out may not be q");
+  const WiPagedAttn a = {q, k_pages, v_pages, block_table, q_start, kv_len, out, lse, batch, n_tokens};
+  const cudaError_t e = wi_launch_paged_attention(pc->g, a, pc->sms, pc->err, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(WI_ECUDA, "paged attention launch: %s", cudaGetErrorString(e));
+  return WI_OK;
+}
+
+int wi_paged_gather(wi_paged* pc, int batch, int layers, const void* k_pages, const void* v_pages,
+                    const int32_t* block_table, const int32_t* kv_len, long long pos0, long long n, void* k_out,
+                    void* v_out, void* stream) {
+  const int rc = enter(pc);
+  if (rc != WI_OK) return rc;
+  const WiPagedGeom& g = pc->g;
+  if (batch < 1 || batch > g.max_batch) return bad_batch(pc, batch);
+  if (layers < 1 || layers > 65536) return fail(WI_EINVAL, "layers (%d) must be in [1, 65536]", layers);
+  const long long most = (long long)g.max_pages * g.page;
+  if (pos0 < 0 || n < 0 || pos0 > most || n > most - pos0)
+    return fail(WI_EINVAL, "positions [pos0, pos0 + n) must lie in [0, max_pages * page_size = %lld)", most);
+  if (n == 0) return WI_OK;
+  if ((double)batch * layers * g.Hkv * (double)n >= 137438953472.0)  // 64 rows a block, 2^31 blocks
+    return fail(WI_EUNSUPPORTED, "batch * layers * n_kv_heads * n must be < 2^37");
+  if (!k_pages || !v_pages || !block_table || !kv_len || !k_out || !v_out)
+    return fail(WI_EINVAL, "the pools, block_table, kv_len, k_out and v_out must be non-NULL");
+  if (misaligned(k_pages, 16) || misaligned(v_pages, 16) || misaligned(k_out, 16) || misaligned(v_out, 16))
+    return fail(WI_EINVAL, "the pools, k_out and v_out must be 16-byte aligned");
+  if (misaligned(block_table, 4) || misaligned(kv_len, 4)) return fail(WI_EINVAL, "the tables must be 4-byte aligned");
+  if (k_out == v_out || k_out == k_pages || k_out == v_pages || v_out == k_pages || v_out == v_pages)
+    return fail(WI_EINVAL, "k_out and v_out must be buffers of their own");
+  const WiPagedGather a = {k_pages, v_pages, block_table, kv_len, k_out, v_out, batch, layers, pos0, n};
+  const cudaError_t e = wi_launch_paged_gather(g, a, pc->err, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return fail(WI_ECUDA, "paged gather launch: %s", cudaGetErrorString(e));
+  return WI_OK;
+}
+
+}  // extern "C"

@@ -381,6 +381,135 @@ int wi_lru_round(void* policy, const int32_t* touched, int n, long long t, int32
                  int* n_ev, int32_t* ad_pages, int32_t* ad_slots, int* n_ad);
 void wi_lru_free(void* policy);
 
+/*
+ * Paged cache: where requests of different lengths are prefilled and decoded
+ * before (or beside) an index.  One layer's keys and values live in two pools
+ * of pages, k_pages and v_pages: device bf16 [n_pages][n_kv_heads][page_size]
+ * [128], caller-owned, 16-byte aligned; a model's layers are pools of their
+ * own that share one block table.  Row b of the block table (device int32
+ * [max_batch or more][max_pages]) lists request b's pages: position p is row
+ * p % page_size of page block_table[b][p / page_size], and its slot number is
+ * page * page_size + p % page_size.  One page per request with page_size = n_ctx is
+ * exactly the layout that wi_build_index takes.
+ * A step: wi_paged_tables (lengths -> pages, slots, positions),
+ * then in every layer wi_paged_write (norms and rotation, keys and values into
+ * the pools) and wi_paged_attention; wi_paged_gather copies rows out into the
+ * layout of wi_build_index or of wi_decode_step's k_new / v_new.
+ *
+ * Lengths and tables are read on the device only: no call synchronises, and
+ * every call may be captured in a CUDA graph and replayed over new contents.
+ * Kernels check what they read there (page numbers, lengths, offsets) before
+ * they use it: a bad value is never followed, sets a bit that
+ * wi_paged_check reports, and leaves the outputs of the request it belongs to
+ * unspecified but inside their buffers.
+ * Limits: at most 2^24 tokens in a step (WI_EUNSUPPORTED).
+ * A handle owns the attention's scratch and the error word and belongs to the
+ * device that was current when it was made (WI_EINVAL on another): order the
+ * attention calls on one handle (one stream); the other calls may overlap.
+ */
+typedef struct wi_paged wi_paged; /* opaque, library-owned */
+
+typedef struct {
+  int n_q_heads, n_kv_heads, head_dim; /* head_dim == 128; n_q_heads / n_kv_heads <= 8 */
+  int page_size;          /* positions per page: a multiple of 16 */
+  int n_pages;            /* pages in a pool; n_pages * n_kv_heads * page_size < 2^31 */
+  int max_batch;          /* requests per call, at most; <= 4096 */
+  int max_pages;          /* row width of the block table; max_pages * page_size < 2^31 */
+  int rotary_dim;         /* elements of a head that are rotated: 0 (none) .. 128, a multiple of 8 */
+  int interleaved;        /* 0: element i turns with i + rotary_dim / 2; 1: 2i with 2i + 1 */
+  int reserved[3];        /* must be zero */
+  double eps;             /* of the norms, > 0 */
+  double rope_scale;      /* factor on both cosine and sine (1 for plain rotation) */
+  const double* inv_freq; /* host, rotary_dim / 2 angles per position (radians), copied; NULL if none */
+} wi_paged_config;
+
+/* Make a handle on the current device (allocates the attention's scratch). */
+int wi_paged_create(const wi_paged_config* cfg, wi_paged** out);
+
+/* Synchronise the device and report what kernels of this handle's calls found wrong
+ * since the last check: WI_OK, or WI_EDEVICE with a message. */
+int wi_paged_check(wi_paged* pc);
+
+/* Release the handle.  NULL is a no-op.  Synchronises the device first. */
+void wi_paged_free(wi_paged* pc);
+
+/*
+ * Pages, slots and positions of a step from its requests' lengths.  ctx_len,
+ * new_len: device int32 [batch], positions in the cache before the step and
+ * tokens that the step adds (0 allowed).  Request b holds the first
+ * ceil(ctx_len / page_size) entries of its row; the pages that its new
+ * positions need on top are taken from the end of free_pages (device int32,
+ * the first *n_free of free_cap entries are free), request after request, a
+ * request's own in increasing position, and entered in its row.  Other entries
+ * of the block table stay as they were.  Written: kv_len [batch] = ctx_len +
+ * new_len; q_start [batch + 1], the running sum of new_len (the step's tokens
+ * lie request after request); slots and positions [n_tokens], of each token,
+ * -1 for those behind the last; *n_free_out, the free pages that are left
+ * (free_pages itself is not changed).  No output may be an input's
+ * buffer except block_table (WI_EINVAL for equal pointers).
+ * A length that is negative or beyond max_pages * page_size, more new tokens
+ * than n_tokens, or more pages than *n_free: an error bit is set, and the step
+ * takes no page and has no token (q_start all 0, kv_len = ctx_len, or 0 where
+ * that is out of range).  Idempotent as long as *n_free and the lengths stay.
+ */
+int wi_paged_tables(wi_paged* pc, int batch, const int32_t* ctx_len, const int32_t* new_len,
+                    const int32_t* free_pages, const int32_t* n_free, int free_cap, int32_t* block_table,
+                    int32_t* kv_len, int32_t* q_start, int32_t* slots, int32_t* positions, int n_tokens,
+                    int32_t* n_free_out, void* stream);
+
+/*
+ * Norms and rotation of a step's queries and keys, and their way into the
+ * cache, in one pass.  q [n_tokens][n_q_heads][128], k and v
+ * [n_tokens][n_kv_heads][128]: device bf16, heads contiguous, tokens
+ * q_stride, k_stride, v_stride elements apart (multiples of 8; a fused
+ * projection's rows can be passed as they are), 16-byte aligned.  Per head of
+ * q and k: x * rsqrt(mean(x^2) + eps) * weight with q_weight / k_weight device
+ * bf16 [128] (NULL: no norm), then each pair (a, b) of the rotated part by the
+ * angle positions[t] * inv_freq[i]: (a cos - b sin, b cos + a sin).  All in
+ * fp32 (the angle exact to 2^-32 of a turn at any position), rounded once.
+ * Queries go to q_out [n_tokens][n_q_heads][128] (q itself if
+ * q_stride = n_q_heads * 128), keys and values to slot slots[t] of the pools.
+ * A token with positions[t] < 0 is padding: nothing of it is written; one with
+ * slots[t] < 0 has its query written only.  Live tokens' slots are distinct.
+ * With slots NULL, k_pages and v_pages are [n_tokens][n_kv_heads][128] instead
+ * of pools: the layout of wi_decode_step's k_new and v_new (one layer).
+ */
+int wi_paged_write(wi_paged* pc, int n_tokens, const void* q, long long q_stride, const void* k, long long k_stride,
+                   const void* v, long long v_stride, const void* q_weight, const void* k_weight,
+                   const int32_t* positions, const int32_t* slots, void* q_out, void* k_pages, void* v_pages,
+                   void* stream);
+
+/*
+ * Attention of a step's tokens over the cache (their own keys and values
+ * already written).  q: device bf16 [n_tokens][n_q_heads][128], normed and
+ * rotated; q_start [batch + 1] and kv_len [batch] as wi_paged_tables writes
+ * them.  Token i of request b sits at position kv_len[b] - (tokens of b) + i
+ * and sees positions 0 .. its own: out = softmax(q K^T / sqrt(128)) V, bf16
+ * [n_tokens][n_q_heads][128]; lse (fp32 [n_tokens][n_q_heads], may be NULL)
+ * the natural logarithm of the row's sum of exponentials.  A token whose
+ * position is negative (kv_len smaller than the request's tokens) sees
+ * nothing: out 0, lse -infinity.  Rows at and behind q_start[batch] stay as
+ * they were.  What lies in the pools beyond a request's kv_len, or at
+ * positions that a token does not see, has no influence, not even infinities
+ * or NaN.  Fp32 accumulation and softmax; the weights are rounded to bf16 for
+ * the product with V (the row's sum is of the unrounded ones).  Same inputs,
+ * same bits.  Single tokens and chunks may be mixed freely in one call.
+ */
+int wi_paged_attention(wi_paged* pc, int batch, int n_tokens, const void* q, const void* k_pages,
+                       const void* v_pages, const int32_t* block_table, const int32_t* q_start,
+                       const int32_t* kv_len, void* out, float* lse, void* stream);
+
+/*
+ * Rows out of the cache: positions [pos0, pos0 + n) of every request and of
+ * `layers` consecutive pools (layer l's pools start l * n_pages * n_kv_heads *
+ * page_size * 128 elements into k_pages / v_pages), to k_out and v_out: device
+ * bf16 [batch][layers][n_kv_heads][n][128], as wi_build_index takes them, and with n = 1
+ * wi_decode_step's k_new and v_new.  Positions at or beyond kv_len[b] become zeros.
+ */
+int wi_paged_gather(wi_paged* pc, int batch, int layers, const void* k_pages, const void* v_pages,
+                    const int32_t* block_table, const int32_t* kv_len, long long pos0, long long n, void* k_out,
+                    void* v_out, void* stream);
+
 /* Error-path testing: with the environment variable WI_FAIL_ALLOC_AT=n (n >= 1),
  * the n-th device allocation made for any index fails as out-of-memory; the
  * call returns WI_ENOMEM having released what it had allocated.  Likewise

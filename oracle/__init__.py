@@ -35,6 +35,10 @@ Parity status per function (what pins it is in ``tests/test_oracle_pins.py``):
                               of the rounds over random traces; cache as
                               large as the working set never evicts, no
                               slots never admits)
+  paged               pinned in tests/test_oracle_paged.py (hand-worked page
+                              tables; rotation as a complex product and by
+                              relative positions; attention against
+                              full_attention and single rows)
 Approximation quality against full attention on synthetic data: parity
 unpinned (the summaries claim accuracy only on RULER / Needle-in-a-Haystack
 with trained models).
@@ -64,3 +68,4 @@ from .wave_index import (  # noqa: F401
     full_attention,
 )
 from .wave_buffer import LruPagePolicy, pages_of_rows  # noqa: F401
+from . import paged  # noqa: F401
