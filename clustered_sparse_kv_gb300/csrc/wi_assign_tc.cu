@@ -301,6 +301,19 @@ bool wi_encode_rows_sw128(CUtensorMap* map, const void* base, unsigned long long
   return encode_rows_impl(map, base, rows, box_rows);
 }
 
+bool wi_encode_heads_sw128(CUtensorMap* map, const void* base, unsigned long long tokens, unsigned heads,
+                           unsigned box_heads, unsigned box_tokens) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)WI_D, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)WI_D * 2, (cuuint64_t)heads * WI_D * 2};
+  const cuuint32_t box[3] = {64u, box_heads, box_tokens};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool wi_tensor_maps_available() { return get_encode() != nullptr; }
 
 bool wi_assign_tc_supported(const WiGeom& g) {

@@ -58,6 +58,9 @@ cudaError_t wi_launch_permute(const WiGeom& g, void* K, void* V, const int* perm
 size_t wi_assign_smem_bytes(const WiGeom& g);
 
 bool wi_encode_rows_sw128(CUtensorMap* map, const void* base, unsigned long long rows, unsigned box_rows);
+// 3-D bf16 tensor map over [tokens][heads][128], box = 64 columns x box_heads x box_tokens, 128-byte swizzle.
+bool wi_encode_heads_sw128(CUtensorMap* map, const void* base, unsigned long long tokens, unsigned heads,
+                           unsigned box_heads, unsigned box_tokens);
 
 // ---- tensor-core assignment (wi_assign_tc.cu)
 bool wi_assign_tc_supported(const WiGeom& g);

@@ -16,6 +16,8 @@ struct wi_paged {
   int device = 0;
   int sms = 0;
   int* err = nullptr;
+  void* scratch = nullptr;  // the attention's
+  size_t scratch_bytes = 0;
 };
 
 namespace {
@@ -105,6 +107,7 @@ int geom_from_config(const wi_paged_config* c, WiPagedGeom* g) {
 
 void destroy(wi_paged* pc) {
   if (pc->err) cudaFree(pc->err);
+  if (pc->scratch) cudaFree(pc->scratch);
   delete pc;
 }
 
@@ -122,8 +125,10 @@ int create_impl(const wi_paged_config* cfg, wi_paged** out) {
   pc->g = g;
   pc->device = dev;
   pc->sms = sms;
+  pc->scratch_bytes = wi_paged_attention_scratch(sms);
   if (cudaMalloc(reinterpret_cast<void**>(&pc->err), 4) != cudaSuccess ||
-      cudaMemset(pc->err, 0, 4) != cudaSuccess) {
+      cudaMalloc(&pc->scratch, pc->scratch_bytes) != cudaSuccess || cudaMemset(pc->err, 0, 4) != cudaSuccess ||
+      cudaMemset(pc->scratch, 0, kPagedTicketBytes) != cudaSuccess) {
     cudaGetLastError();
     destroy(pc);
     return fail(WI_ENOMEM, "device allocation failed");
@@ -153,6 +158,7 @@ int wi_paged_check(wi_paged* pc) {
   WI_CUDA(cudaMemcpy(&herr, pc->err, 4, cudaMemcpyDeviceToHost));
   if (!herr) return WI_OK;
   WI_CUDA(cudaMemset(pc->err, 0, 4));
+  if (herr & WI_DEVERR_MBAR_TIMEOUT) WI_CUDA(cudaMemset(pc->scratch, 0, kPagedTicketBytes));  // tickets left behind
   return fail(WI_EDEVICE, "paged cache (flags 0x%x):%s%s%s%s", herr,
               herr & WI_DEVERR_BAD_PAGE ? " a page or slot outside the pool;" : "",
               herr & WI_DEVERR_BAD_LENGTH ? " a length or offset out of range;" : "",
@@ -241,7 +247,7 @@ int wi_paged_attention(wi_paged* pc, int batch, int n_tokens, const void* q, con
     return fail(WI_EINVAL, "the tables and lse must be 4-byte aligned");
   if (out == q) return fail(WI_EINVAL, "out may not be q");
   const WiPagedAttn a = {q, k_pages, v_pages, block_table, q_start, kv_len, out, lse, batch, n_tokens};
-  const cudaError_t e = wi_launch_paged_attention(pc->g, a, pc->sms, pc->err, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = wi_launch_paged_attention(pc->g, a, pc->sms, pc->scratch, pc->err, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(WI_ECUDA, "paged attention launch: %s", cudaGetErrorString(e));
   return WI_OK;
 }

@@ -1,73 +1,849 @@
-// wi_paged_attn.cu -- attention of new tokens over the paged cache.
+// wi_paged_attn.cu -- attention of new tokens over the paged cache on the
+// 5th-generation tensor cores.
+//
+// out = softmax(q K^T / sqrt(128)) V over the positions a token sees, for
+// every (token, query head).  The query heads of a kv head share its keys, so
+// the rows of a tile are (token, query head of the group) pairs: floor(128/G)
+// tokens to a tile of 128 rows.
+//
+// Work.  An item is one (request, kv head, pair of tiles); its key blocks of
+// 128 positions run from 0 to the last position that a row sees.  A unit is
+// one block of one item; all units of the call, item after item, are cut into
+// equal runs, one per CTA (one CTA per SM), so single tokens over long
+// contexts split over the machine and ragged chunks balance without a plan
+// made on the host.  Lengths live on the device: each CTA sums the units of
+// all requests itself (closed form per request) and finds its run's start.
+// An item cut between CTAs leaves partial results (maximum, sum, O) in the
+// scratch; the last of its CTAs merges them in CTA order, so results do not
+// depend on timing.
+//
+// A CTA (384 threads) processes its items' blocks in roles:
+//   warps 0-3, 4-7  softmax, one thread per row of chain 0 / chain 1
+//   warp 8          TMA: queries, key and value blocks (box by box, through
+//                   the block table) into a ring of five 32 KB stages
+//   warp 9          issues tcgen05.mma: S = Q K^T (both operands in shared
+//                   memory), O += P V (P in tensor memory, V N-major)
+//   warps 10-11     clean value rows of blocks that not every row sees whole
+// The two chains have their own S (P takes S's place) and O in tensor memory
+// (all 512 columns), so that one chain's softmax runs while the tensor cores
+// work on the other.  In an item of two tiles the chains are the tiles, and
+// share the key and value blocks; an item of one tile (single tokens above
+// all) gives the chains alternate blocks of the same tile and adds their
+// results at the end.
+//
+// Masked positions.  Keys of unseen positions may hold anything: their scores
+// are replaced, not added to.  Values are different: 0 * Inf is NaN inside the
+// product.  In blocks that not every row sees whole, rows behind the request's
+// end are zeroed in shared memory, and so are infinite and NaN elements, which
+// the end of the item then adds to the rows that do see them.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cstddef>
+
 #include "wi_common.cuh"
+#include "wi_internal.h"
 #include "wi_paged.h"
+#include "wi_pipe.cuh"
+#include "wi_tc.cuh"
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kRows = 128;                     // rows of a tile, and positions of a block
+constexpr int kStages = 5;
+constexpr int kTileBytes = kRows * WI_D * 2;   // 32 KB: two halves of 64 columns
+constexpr int kHalfBytes = kTileBytes / 2;
+constexpr int kSoftWarps = 8;
+constexpr int kThreads = 32 * (kSoftWarps + 4);
+constexpr int kFixWarps = 2;
+constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
+constexpr float kLn2 = 0.6931471805599453f;
+// A row's reference maximum follows its true maximum only when that is more than 2^8 larger: the weights stay
+// below 256, which costs neither bf16 nor fp32 any precision, and O is rescaled a few times per item at most.
+constexpr float kLazy = 8.f;
 
-// The plain form on the CUDA cores: a warp per (token, query head), one pass over its keys with the running
-// maximum and sum of the softmax; a lane holds four of the 128 elements.
-__global__ void __launch_bounds__(kWarps * 32) k_paged_attention(WiPagedAttn A, int Hq, int Hkv, int page, int n_pages,
-                                                                int max_pages, int* err) {
-  const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b < A.batch; b += kWarps * 32)
-      if (A.q_start[b] < 0 || A.q_start[b + 1] < A.q_start[b] || A.q_start[b + 1] > A.n_tokens)
-        atomicOr(err, WI_DEVERR_BAD_LENGTH);
-  const long long row = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int t = (int)(row / Hq), h = (int)(row % Hq);
-  if (t >= A.n_tokens) return;
-  int lo = 0, hi = A.batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (A.q_start[mid] <= t) lo = mid; else hi = mid - 1;
+// A partial result: m and l of 256 rows, then O of two tiles, column-major (a thread owns a row, so column-major
+// stores of a warp are contiguous).
+constexpr int kPartFloats = 2 * 256 + 2 * WI_D * kRows;
+
+struct Smem {
+  uint64_t full[kStages], empty[kStages];
+  uint64_t to_fix[kStages], fixed[kStages];  // a value block that is to be cleaned was asked for; has been cleaned
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_ready[2], o_full[2];
+  uint64_t drained;
+  uint32_t tmem_base;
+  int last;                 // the merge is this CTA's
+  int poison[8];            // segment number + 1 of the last segment (modulo 8) with an infinite or NaN value
+  long long scan[kThreads / 32];
+  int start[4];             // the run's first request, kv head, tile pair, block
+  float xm[kRows], xl[kRows];  // chain 1's maximum and sum, for chain 0
+  unsigned char pad[2048 - (4 * kStages + 9) * 8 - 8 - 32 - kThreads / 32 * 8 - 16 - 2 * kRows * 4];
+  unsigned char q[2][kTileBytes];          // [k half][128 rows][128 B]
+  unsigned char ring[kStages][kTileBytes]; // [k half][128 rows][128 B]
+};
+static_assert(offsetof(Smem, q) == 2048, "tiles must start 1024-byte aligned");
+static_assert(sizeof(Smem) <= 232448, "shared memory");
+
+struct Params {
+  WiPagedAttn a;
+  int Hq, Hkv, G, tq;       // tq = tokens per tile
+  int page, n_pages, max_pages, box;
+  float* parts;
+  unsigned* tickets;
+  int* err;
+};
+
+// Request b as the kernel reads it; a request with impossible numbers has no tokens (CTA 0 reports it).
+struct Req {
+  int s0, n, kv, ok;
+};
+__device__ __forceinline__ Req load_req(const Params& P, int b) {
+  Req r;
+  r.s0 = P.a.q_start[b];
+  const int s1 = P.a.q_start[b + 1];
+  r.kv = P.a.kv_len[b];
+  r.ok = r.s0 >= 0 && s1 >= r.s0 && s1 <= P.a.n_tokens && r.kv >= 0 && (long long)r.kv <= (long long)P.max_pages * P.page;
+  r.n = r.ok ? s1 - r.s0 : 0;
+  return r;
+}
+
+// Blocks of the tile pair that ends before token `end` of a request whose token 0 sits at p0: at least one,
+// so that rows that see nothing are visited too.
+__device__ __forceinline__ int blocks_to(long long p0, long long end) {
+  const long long e = p0 + end;
+  return e <= kRows ? 1 : (int)((e + kRows - 1) / kRows);
+}
+
+// Sum over i < n of floor((a i + b) / m), a, b >= 0: whole multiples of m are taken out of a and b, and what is
+// left counts lattice points under a line, which is the same problem with a and m exchanged.
+__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
+  long long s = 0;
+  while (n > 0) {
+    s += (n - 1) * n / 2 * (a / m) + n * (b / m);
+    a %= m;
+    b %= m;
+    const long long y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const long long t = a;
+    a = m;
+    m = t;
   }
-  const int s0 = A.q_start[lo], s1 = A.q_start[lo + 1], kv = A.kv_len[lo];
-  if (t < s0 || t >= s1) return;  // behind the last request
-  if (kv < 0 || (long long)kv > (long long)max_pages * page) {
-    if (lane == 0) atomicOr(err, WI_DEVERR_BAD_LENGTH);
+  return s;
+}
+
+// Blocks of the first `m` tile pairs (none of them the last one, which may be shorter).
+__device__ long long blocks_before(long long p0, int tp, int m) {
+  long long z = p0 < 0 ? -p0 / tp : 0;  // pairs that end at or before position 0: one block each
+  if (z > m) z = m;
+  return z + floor_sum(m - z, kRows, tp, p0 + (z + 1) * tp + kRows - 1);
+}
+
+// Where a CTA stands in its run: one item's part after the other.
+struct Walk {
+  int b, kh, tile, blk;   // blk: the next block of the item
+  long long left;         // units of the run still to come
+  Req r;
+  int tp, tiles;
+  // the current segment
+  int cnt, single, nblk, b0, nb;   // tokens, one tile, blocks of the item, first block, blocks of the segment
+  long long p0;           // position of the request's token 0
+
+  __device__ __forceinline__ void begin(const Params& P, const Smem& sm, long long units) {
+    b = sm.start[0];
+    kh = sm.start[1];
+    tile = sm.start[2];
+    blk = sm.start[3];
+    left = units;
+    tp = 2 * P.tq;
+    if (left > 0) set(P);
+  }
+  __device__ __forceinline__ void set(const Params& P) {
+    r = load_req(P, b);
+    p0 = (long long)r.kv - r.n;
+    tiles = (r.n + tp - 1) / tp;
+  }
+  // The next segment of the run; false at its end.
+  __device__ __forceinline__ bool next(const Params& P) {
+    if (left <= 0) return false;
+    while (tile >= tiles) {   // past the request's last pair: next kv head, next request with tokens
+      tile = 0;
+      if (r.n == 0 || ++kh == P.Hkv) {
+        kh = 0;
+        if (++b >= P.a.batch) return false;
+        set(P);
+      }
+    }
+    cnt = min(tp, r.n - tile * tp);
+    single = cnt <= P.tq;
+    nblk = blocks_to(p0, (long long)tile * tp + cnt);
+    b0 = blk;
+    nb = (int)min((long long)(nblk - blk), left);
+    return true;
+  }
+  __device__ __forceinline__ void advance() {
+    left -= nb;
+    blk += nb;
+    if (blk >= nblk) {
+      blk = 0;
+      ++tile;
+    }
+  }
+  __device__ __forceinline__ int first_pos() const { return (int)(p0 + (long long)tile * tp); }
+  // The item's first block that not all of its rows see whole.
+  __device__ __forceinline__ int first_fix() const {
+    const int f = first_pos();
+    return f < 0 ? 0 : (f + 1) / kRows;
+  }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 w = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&w);
+}
+
+__device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory"); }
+
+__device__ __forceinline__ bool nonfinite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
+
+// Add the infinite and NaN values that a row sees in blocks [f0, f1) to 32 columns of its O.
+__device__ __forceinline__ void add_poison(const Params& P, int b, int kh, int f0, int f1, int kv, int limit, int c0,
+                                           float (&o)[32]) {
+  const int end = min(min(f1 * kRows, kv), limit + 1);
+#pragma unroll 1
+  for (int p = f0 * kRows; p < end; ++p) {
+    const int j = p / P.page, pg = P.a.block_table[(long long)b * P.max_pages + j];
+    if (pg < 0 || pg >= P.n_pages) continue;
+    const uint32_t* v = static_cast<const uint32_t*>(P.a.v_pages) +
+                        ((((long long)pg * P.Hkv + kh) * P.page + (p - j * P.page)) * WI_D + c0) / 2;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t w = v[i];
+      if (nonfinite16(w)) o[2 * i] += bf16_lo(w);
+      if (nonfinite16(w >> 16)) o[2 * i + 1] += bf16_hi(w);
+    }
+  }
+}
+
+// The CTA whose run holds unit u of `total`, cut into `ctas` runs.
+__device__ __forceinline__ int cta_of(long long u, long long total, int ctas) {
+  return (int)(((u + 1) * ctas - 1) / total);
+}
+
+// Merge the partial results of one item, made by CTAs c0 .. c1, in that order: a thread takes a column, eight
+// rows at a time.
+__device__ void merge_parts(const Params& P, const Walk& w, int c0, int c1) {
+  const int tid = threadIdx.x, d = tid & 127;
+  const int rows_tile = P.tq * P.G;
+  const int div = (65536 + P.G - 1) / P.G;  // r / G for r < 128
+  for (int t = 0; t < (w.single ? 1 : 2); ++t) {
+    const int rows = min(rows_tile, (w.cnt - t * P.tq) * P.G);
+    for (int r0 = (tid >> 7) * 8; r0 < rows; r0 += 16) {
+      float M[8], L[8], acc[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        M[i] = -INFINITY;
+        L[i] = acc[i] = 0.f;
+      }
+      for (int c = c0; c <= c1; ++c) {
+        const float* s = P.parts + (long long)(2 * c + (c == c0 ? 1 : 0)) * kPartFloats + t * kRows + r0;
+        const float4 a = __ldcg(reinterpret_cast<const float4*>(s)), b = __ldcg(reinterpret_cast<const float4*>(s + 4));
+        const float m[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) M[i] = fmaxf(M[i], m[i]);
+      }
+#pragma unroll 2
+      for (int c = c0; c <= c1; ++c) {
+        const float* s = P.parts + (long long)(2 * c + (c == c0 ? 1 : 0)) * kPartFloats;
+        const float4* ps = reinterpret_cast<const float4*>(s + t * kRows + r0);
+        const float4* pl = reinterpret_cast<const float4*>(s + 256 + t * kRows + r0);
+        const float4* po = reinterpret_cast<const float4*>(s + 512 + (t * WI_D + d) * kRows + r0);
+        const float4 m0 = __ldcg(ps), m1 = __ldcg(ps + 1), l0 = __ldcg(pl), l1 = __ldcg(pl + 1), o0 = __ldcg(po),
+                     o1 = __ldcg(po + 1);
+        const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+        const float l[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
+        const float o[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float f = ex2(m[i] - (M[i] == -INFINITY ? 0.f : M[i]));
+          L[i] += f * l[i];
+          acc[i] += f * o[i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + i;
+        if (r >= rows) break;
+        const int tok = (r * div) >> 16, h = r - tok * P.G;
+        const long long at = (long long)(w.r.s0 + w.tile * w.tp + t * P.tq + tok) * P.Hq + w.kh * P.G + h;
+        const float inv = L[i] == 0.f ? 0.f : 1.f / L[i];
+        static_cast<bf16*>(P.a.out)[at * WI_D + d] = __float2bfloat16_rn(acc[i] * inv);
+        if (P.a.lse && d == 0) P.a.lse[at] = L[i] == 0.f ? -INFINITY : M[i] * kLn2 + logf(L[i]);
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_constant__ CUtensorMap map_q,
+                                                                const __grid_constant__ CUtensorMap map_k,
+                                                                const __grid_constant__ CUtensorMap map_v,
+                                                                const __grid_constant__ Params P) {
+  extern __shared__ __align__(1024) unsigned char raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (smem_addr(raw) & 1023u) {  // the swizzled tiles need 1024-byte alignment; never run misaligned
+    if (tid == 0) atomicOr(P.err, WI_DEVERR_BAD_ROW);
     return;
   }
-  const int last = kv - (s1 - s0) + (t - s0);
-  const int kh = h / (Hq / Hkv);
-  float q[4], o[4] = {0.f, 0.f, 0.f, 0.f};
-  load_bf16x4(static_cast<const bf16*>(A.q) + row * WI_D + 4 * lane, q);
-  float m = -INFINITY, z = 0.f;
-  for (int p = 0; p <= last; ++p) {
-    const int pg = A.block_table[(long long)lo * max_pages + p / page];
-    if (pg < 0 || pg >= n_pages) {
-      if (lane == 0) atomicOr(err, WI_DEVERR_BAD_PAGE);
-      continue;
-    }
-    const long long at = (((long long)pg * Hkv + kh) * page + p % page) * WI_D + 4 * lane;
-    float k[4], v[4];
-    load_bf16x4(static_cast<const bf16*>(A.k_pages) + at, k);
-    load_bf16x4(static_cast<const bf16*>(A.v_pages) + at, v);
-    const float s = warp_sum(q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3]) * 0.08838834764831845f;
-    const float top = fmaxf(m, s), keep = expf(m - top), w = expf(s - top);
-    m = top;
-    z = z * keep + w;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = o[i] * keep + w * v[i];
+
+  // ---- this CTA's run of units
+  const int per = (P.a.batch + kThreads - 1) / kThreads;
+  const int rb0 = min(tid * per, P.a.batch), rb1 = min(rb0 + per, P.a.batch);
+  const int tp = 2 * P.tq;
+  long long mine = 0;
+  for (int b = rb0; b < rb1; ++b) {
+    const Req r = load_req(P, b);
+    if (!r.ok && blockIdx.x == 0) atomicOr(P.err, WI_DEVERR_BAD_LENGTH);
+    if (r.n == 0) continue;
+    const int tiles = (r.n + tp - 1) / tp;
+    mine += P.Hkv * (blocks_before((long long)r.kv - r.n, tp, tiles - 1) + blocks_to((long long)r.kv - r.n, r.n));
   }
-  const float inv = z > 0.f ? 1.f / z : 0.f;
-  const __nv_bfloat162 a = __floats2bfloat162_rn(o[0] * inv, o[1] * inv), b = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
-  uint2 w;
-  w.x = *reinterpret_cast<const uint32_t*>(&a);
-  w.y = *reinterpret_cast<const uint32_t*>(&b);
-  *reinterpret_cast<uint2*>(static_cast<bf16*>(A.out) + row * WI_D + 4 * lane) = w;
-  if (A.lse && lane == 0) A.lse[row] = z > 0.f ? m + logf(z) : -INFINITY;
+  long long before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += t;
+  }
+  if (lane == 31) sm.scan[warp] = before;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.to_fix[s], 1);
+      mbar_init(&sm.fixed[s], kFixWarps);
+    }
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sm.s_full[t], 1);
+      mbar_init(&sm.p_ready[t], 4);
+      mbar_init(&sm.o_full[t], 1);
+    }
+    mbar_init(&sm.drained, 1);
+    for (int i = 0; i < 8; ++i) sm.poison[i] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+  long long total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) before += total;
+    total += sm.scan[w];
+  }
+  before -= mine;
+  const int ctas = (int)min((long long)gridDim.x, total);
+  if ((int)blockIdx.x >= ctas) return;  // fewer units than CTAs (the whole CTA leaves)
+  const long long u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
+  if (u0 >= before && u0 < before + mine) {  // one thread's requests hold the run's first unit
+    long long rem = u0 - before;
+    for (int b = rb0; b < rb1; ++b) {
+      const Req r = load_req(P, b);
+      if (r.n == 0) continue;
+      const int tiles = (r.n + tp - 1) / tp;
+      const long long p0 = (long long)r.kv - r.n;
+      const long long c = blocks_before(p0, tp, tiles - 1) + blocks_to(p0, r.n);
+      if (rem >= c * P.Hkv) {
+        rem -= c * P.Hkv;
+        continue;
+      }
+      const int kh = (int)(rem / c);
+      rem -= c * kh;
+      int lo = 0, hi = tiles - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (blocks_before(p0, tp, mid) <= rem) lo = mid; else hi = mid - 1;
+      }
+      sm.start[0] = b;
+      sm.start[1] = kh;
+      sm.start[2] = lo;
+      sm.start[3] = (int)(rem - blocks_before(p0, tp, lo));
+      break;
+    }
+  }
+  if (P.tq * P.G < kRows) {  // rows of the query tiles that no box fills: zero, not whatever was there
+    for (int i = tid; i < 2 * kTileBytes / 16; i += kThreads)
+      reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;  // S0, S1 at columns 0, 128; O0, O1 at 256, 384
+
+  Walk w;
+  w.begin(P, sm, u1 - u0);
+
+  if (warp < kSoftWarps) {
+    // ---------------- softmax
+    const int chain = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + (uint32_t)chain * kRows;
+    const uint32_t to = tmem + lanes + 256u + (uint32_t)chain * WI_D;
+    const int tok = (row * ((65536 + P.G - 1) / P.G)) >> 16, head = row - tok * P.G;
+    uint32_t s_par = 0, o_par0 = 0, o_par1 = 0;
+    bool ok = true;  // after one timed-out wait the warp waits no more and writes nothing, but meets every barrier
+    long long done = 0;
+    for (int seg = 0; w.next(P); ++seg) {
+      const int own_tile = w.single ? 0 : chain;
+      const int ti = w.tile * w.tp + own_tile * P.tq + tok;
+      const bool live = tok < P.tq && ti < w.r.n;
+      const int limit = live ? (int)(w.p0 + ti) : -1;   // the last position that the row sees
+      const int whole = (int)(w.p0 + w.tile * w.tp + own_tile * P.tq);  // ... that all rows of the tile see
+      float m = -INFINITY, l = 0.f;
+      bool first = true;
+      for (int j = w.single ? chain : 0; j < w.nb; j += w.single ? 2 : 1) {
+        const int k0 = (w.b0 + j) * kRows;
+        if (ok) ok = mbar_wait(&sm.s_full[chain], s_par, P.err);
+        s_par ^= 1;
+        tc_fence_after();
+        uint32_t raw_s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_nowait(ts + 32 * c, raw_s[c]);
+        tmem_wait_ld();
+        float s[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) s[i] = __uint_as_float(raw_s[i >> 5][i & 31]);
+        if (k0 + kRows - 1 > whole) {
+#pragma unroll
+          for (int i = 0; i < kRows; ++i)
+            if (k0 + i > limit) s[i] = -INFINITY;
+        }
+        float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
+#pragma unroll
+        for (int i = 4; i < kRows; i += 4) {
+          t0 = fmaxf(t0, s[i]);
+          t1 = fmaxf(t1, s[i + 1]);
+          t2 = fmaxf(t2, s[i + 2]);
+          t3 = fmaxf(t3, s[i + 3]);
+        }
+        const float top = fmaxf(fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)), -INFINITY) * kScaleLog2;
+        if (first) {
+          m = top;
+        } else {
+          const bool need = top > m + kLazy;
+          if (__any_sync(0xffffffffu, need)) {
+            // the chain's products so far are done: S of this block was issued behind them
+            const float f = need ? ex2(m - top) : 1.f;
+            if (need) m = top;
+            l *= f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld32_nowait(to + 32 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32_nowait(to + 32 * c, o);
+            }
+          }
+        }
+        first = false;
+        const float ref = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 2^-inf = 0
+        float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t p[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float a = ex2(fmaf(s[64 * c + 2 * i], kScaleLog2, -ref));
+            const float b = ex2(fmaf(s[64 * c + 2 * i + 1], kScaleLog2, -ref));
+            l0 += a;
+            l1 += b;
+            p[i] = pack2(a, b);
+          }
+          tmem_st32_nowait(ts + 32 * c, p);
+        }
+        l += l0 + l1;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_ready[chain]);
+      }
+
+      // ---- the segment's end
+      const bool both = !w.single || w.nb > 1;  // chain 1 had blocks
+      if (w.single && chain == 1) {
+        sm.xm[row] = m;
+        sm.xl[row] = l;
+      }
+      if (ok && (chain == 0 || !both)) ok = mbar_wait(&sm.o_full[0], o_par0, P.err);
+      if (ok && both && (chain == 1 || w.single)) ok = mbar_wait(&sm.o_full[1], o_par1, P.err);
+      o_par0 ^= 1;
+      if (both) o_par1 ^= 1;
+      tc_fence_after();
+      const bool part = w.b0 > 0 || w.nb < w.nblk;
+      if (w.single) soft_barrier();
+      float f0 = 1.f, f1 = 0.f;
+      const bool writer = !w.single || chain == 0;
+      if (w.single && chain == 0 && both) {
+        const float m1 = sm.xm[row], M = fmaxf(m, m1), ref = M == -INFINITY ? 0.f : M;
+        f0 = ex2(m - ref);
+        f1 = ex2(m1 - ref);
+        l = l * f0 + sm.xl[row] * f1;
+        m = M;
+      }
+      const long long at = (long long)(w.r.s0 + ti) * P.Hq + w.kh * P.G + head;
+      const int slot = 2 * (int)blockIdx.x + (w.b0 == 0 ? 1 : 0);
+      float* dst = P.parts + (long long)slot * kPartFloats;
+      const bool poison = *reinterpret_cast<volatile int*>(&sm.poison[seg & 7]) == seg + 1;
+      if (writer) {
+        const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          __syncwarp();
+          uint32_t raw_o[32];
+          tmem_ld32_nowait(to + 32 * c, raw_o);
+          tmem_wait_ld();
+          float o[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(raw_o[i]);
+          if (w.single && both) {
+            tmem_ld32_nowait(to + WI_D + 32 * c, raw_o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = o[i] * f0 + __uint_as_float(raw_o[i]) * f1;
+          }
+          if (poison && live)
+            add_poison(P, w.b, w.kh, max(w.b0, w.first_fix()), w.b0 + w.nb, w.r.kv, limit, 32 * c, o);
+          if (ok && live) {
+            if (part) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) __stcg(dst + 512 + (own_tile * WI_D + 32 * c + i) * kRows + row, o[i]);
+            } else {
+              uint4* q = reinterpret_cast<uint4*>(static_cast<bf16*>(P.a.out) + at * WI_D + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint4 x;
+                x.x = pack2(o[8 * i] * inv, o[8 * i + 1] * inv);
+                x.y = pack2(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
+                x.z = pack2(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
+                x.w = pack2(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
+                q[i] = x;
+              }
+            }
+          }
+        }
+        if (ok && live) {
+          if (part) {
+            __stcg(dst + own_tile * kRows + row, m);
+            __stcg(dst + 256 + own_tile * kRows + row, l);
+          } else if (P.a.lse) {
+            P.a.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+          }
+        }
+      }
+      tc_fence_before();  // O is read: the next segment may write it
+      if (part) {
+        // the last CTA to bring its part of the item merges all of them
+        const long long item = u0 + done - w.b0;  // the item's first unit
+        const int c0 = cta_of(item, total, ctas), c1 = cta_of(item + w.nblk - 1, total, ctas);
+        __threadfence();
+        soft_barrier();
+        if (tid == 0) {
+          sm.last = 0;
+          if (ok) {
+            sm.last = ticket_acq_rel(P.tickets + c0) == (unsigned)(c1 - c0);
+            if (sm.last) P.tickets[c0] = 0;
+          }
+          __threadfence();
+        }
+        soft_barrier();
+        if (sm.last) merge_parts(P, w, c0, c1);
+        soft_barrier();
+      } else if (w.single) {
+        soft_barrier();  // chain 1's O has been read
+      }
+      done += w.nb;
+      w.advance();
+    }
+  } else if (warp == 8) {
+    // ---------------- TMA: queries, keys, values
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
+    }
+    const int boxes = kRows / P.box;  // boxes of a block, one lane each
+    const uint32_t q_half = (uint32_t)(P.tq * P.G) * 128u;
+    long long issued = 0;             // ring stages filled
+    int q_loads = 0;
+    bool ok = true;
+    for (int seg = 0; ok && w.next(P); ++seg) {
+      // queries, once the products of the segment before have read theirs
+      if (seg > 0) ok = mbar_wait(&sm.q_empty, (seg - 1) & 1, P.err);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      if (lane == 0) {
+        const int n = w.single ? 1 : 2;
+        mbar_arrive_expect_tx(&sm.q_full, 2u * q_half * n);
+        for (int t = 0; t < n; ++t) {
+          const int tk = w.r.s0 + w.tile * w.tp + t * P.tq;
+          tma_load_3d(sm.q[t], &map_q, 0, w.kh * P.G, tk, &sm.q_full);
+          tma_load_3d(sm.q[t] + kHalfBytes, &map_q, 64, w.kh * P.G, tk, &sm.q_full);
+        }
+      }
+      ++q_loads;
+      const int ahead = w.single ? 2 : 1;
+      // the pool row of this lane's box of block j (of the segment); -1 behind the request's end
+      auto row_of = [&](int j) -> int {
+        const int p = (w.b0 + j) * kRows + lane * P.box;
+        if (j >= w.nb || lane >= boxes || p >= w.r.kv) return -1;
+        const int pj = p / P.page;
+        int pg = __ldg(P.a.block_table + (long long)w.b * P.max_pages + pj);
+        if (pg < 0 || pg >= P.n_pages) {
+          atomicOr(P.err, WI_DEVERR_BAD_PAGE);
+          pg = 0;
+        }
+        return (pg * P.Hkv + w.kh) * P.page + (p - pj * P.page);
+      };
+      auto fill = [&](const CUtensorMap* map, int rowi) -> bool {
+        const int s = (int)(issued % kStages);
+        const long long round = issued / kStages;
+        bool got = true;
+        if (round > 0) got = mbar_wait(&sm.empty[s], (uint32_t)(round - 1) & 1u, P.err);
+        if (!__all_sync(0xffffffffu, got)) return false;
+        const unsigned on = __ballot_sync(0xffffffffu, rowi >= 0);
+        if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)__popc(on) * P.box * 256u);
+        __syncwarp();
+        if (rowi >= 0) {
+          unsigned char* dst = sm.ring[s] + lane * P.box * 128;
+          tma_load_2d(dst, map, 0, rowi, &sm.full[s]);
+          tma_load_2d(dst + kHalfBytes, map, 64, rowi, &sm.full[s]);
+        }
+        ++issued;
+        return true;
+      };
+      int r0 = row_of(0), r1 = row_of(1), r2 = row_of(2);
+      ok = fill(&map_k, r0);
+      if (ok && ahead == 2 && w.nb > 1) ok = fill(&map_k, r1);
+      for (int j = 0; ok && j < w.nb; ++j) {
+        const int r3 = row_of(j + 3);
+        ok = fill(&map_v, r0);
+        if (ok && lane == 0 && w.b0 + j >= w.first_fix()) mbar_arrive(&sm.to_fix[(issued - 1) % kStages]);
+        if (ok && j + ahead < w.nb) ok = fill(&map_k, ahead == 2 ? r2 : r1);
+        r0 = r1;
+        r1 = r2;
+        r2 = r3;
+      }
+      w.advance();
+    }
+    // no copy is in flight when the CTA's shared memory goes (after a timed-out wait the tensor cores may not have
+    // waited for them)
+    if (q_loads > 0) mbar_wait(&sm.q_full, (uint32_t)(q_loads - 1) & 1u, P.err);
+    for (int s = 0; s < kStages && s < issued; ++s)
+      mbar_wait(&sm.full[s], (uint32_t)((issued - 1 - s) / kStages) & 1u, P.err);
+  } else if (warp == 9) {
+    // ---------------- tensor cores: one thread issues
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = make_idesc(kRows, kRows);
+      constexpr uint32_t idesc_o = make_idesc(kRows, WI_D) | kIdescNMajorB;
+      long long used = 0;        // ring stages consumed
+      uint32_t p_par[2] = {0, 0}, fix_par = 0;
+      bool ok = true;
+      auto scores = [&](int t, int q, int s) {
+        const uint32_t a0 = smem_addr(sm.q[q]), b0 = smem_addr(sm.ring[s]);
+#pragma unroll
+        for (int kk = 0; kk < WI_D / 16; ++kk) {
+          const uint32_t off = (uint32_t)(kk >> 2) * kHalfBytes + (uint32_t)(kk & 3) * 32;
+          mma_bf16(tmem + (uint32_t)t * kRows, make_desc_sw128(a0 + off), make_desc_sw128(b0 + off), idesc_s, kk > 0);
+        }
+        mma_commit(&sm.s_full[t]);
+      };
+      auto values = [&](int t, int s, bool add) {
+        const uint32_t b0 = smem_addr(sm.ring[s]);
+#pragma unroll
+        for (int kk = 0; kk < kRows / 16; ++kk)
+          mma_bf16_ta(tmem + 256u + (uint32_t)t * WI_D, tmem + (uint32_t)t * kRows + (uint32_t)kk * 8,
+                      make_desc_sw128_nmajor(b0 + (uint32_t)kk * 2048, kHalfBytes), idesc_o, add || kk > 0);
+      };
+      auto take = [&](int* s) -> bool {  // the next ring stage, once it is full
+        *s = (int)(used % kStages);
+        const bool got = mbar_wait(&sm.full[*s], (uint32_t)(used / kStages) & 1u, P.err);
+        ++used;
+        tc_fence_after();
+        return got;
+      };
+      for (int seg = 0; ok && w.next(P); ++seg) {
+        ok = mbar_wait(&sm.q_full, seg & 1, P.err);
+        if (!ok) break;
+        tc_fence_after();
+        const int fix = w.first_fix() - w.b0;  // from this block of the segment on, values are cleaned first
+        int ks, vs;
+        if (!(ok = take(&ks))) break;
+        scores(0, 0, ks);
+        if (w.single) {
+          mma_commit(&sm.empty[ks]);
+          if (w.nb > 1) {
+            if (!(ok = take(&ks))) break;
+            scores(1, 0, ks);
+            mma_commit(&sm.empty[ks]);
+          }
+        } else {
+          scores(1, 1, ks);
+          mma_commit(&sm.empty[ks]);
+        }
+        if (w.nb <= (w.single ? 2 : 1)) mma_commit(&sm.q_empty);
+        for (int j = 0; j < w.nb; ++j) {
+          if (!(ok = take(&vs))) break;
+          if (j >= fix) {
+            ok = mbar_wait(&sm.fixed[vs], (fix_par >> vs) & 1u, P.err);
+            fix_par ^= 1u << vs;
+            if (!ok) break;
+          }
+          if (w.single) {
+            const int t = j & 1;
+            if (!(ok = mbar_wait(&sm.p_ready[t], p_par[t], P.err))) break;
+            p_par[t] ^= 1;
+            tc_fence_after();
+            values(t, vs, j >= 2);
+            mma_commit(&sm.empty[vs]);
+            if (j + 2 >= w.nb) {
+              mma_commit(&sm.o_full[t]);
+            } else {
+              if (!(ok = take(&ks))) break;
+              scores(t, 0, ks);
+              mma_commit(&sm.empty[ks]);
+              if (j + 3 >= w.nb) mma_commit(&sm.q_empty);
+            }
+          } else {
+            const bool more = j + 1 < w.nb;
+            if (!(ok = mbar_wait(&sm.p_ready[0], p_par[0], P.err))) break;
+            p_par[0] ^= 1;
+            tc_fence_after();
+            values(0, vs, j > 0);
+            if (more) {
+              if (!(ok = take(&ks))) break;
+              scores(0, 0, ks);
+            } else {
+              mma_commit(&sm.o_full[0]);
+            }
+            if (!(ok = mbar_wait(&sm.p_ready[1], p_par[1], P.err))) break;
+            p_par[1] ^= 1;
+            tc_fence_after();
+            values(1, vs, j > 0);
+            mma_commit(&sm.empty[vs]);
+            if (more) {
+              scores(1, 1, ks);
+              mma_commit(&sm.empty[ks]);
+              if (j + 2 >= w.nb) mma_commit(&sm.q_empty);
+            } else {
+              mma_commit(&sm.o_full[1]);
+            }
+          }
+        }
+        if (!ok) break;
+        w.advance();
+      }
+      // every product is done before the tensor memory goes
+      mma_commit(&sm.drained);
+      mbar_wait(&sm.drained, 0, P.err);
+    }
+  } else {
+    // ---------------- clean the value rows of blocks that not every row sees whole
+    const int half = warp - 10;  // 64 columns each
+    long long at = 0;            // the segment's first ring stage
+    uint32_t fix_par = 0;
+    bool ok = true;
+    for (int seg = 0; ok && w.next(P); ++seg) {
+      const int ahead = w.single ? 2 : 1;
+      const int lead = min(ahead, w.nb);  // key blocks in front of the first value block
+      for (int j = max(0, w.first_fix() - w.b0); j < w.nb; ++j) {
+        // stages in front of value block j: the leading key blocks, j value blocks and the key blocks among them
+        const long long use = at + lead + j + max(0, min(j, w.nb - ahead));
+        const int s = (int)(use % kStages);
+        // only once the copy has been asked for does the stage's phase stand at this use
+        if (!(ok = mbar_wait(&sm.to_fix[s], (fix_par >> s) & 1u, P.err))) break;
+        fix_par ^= 1u << s;
+        if (!(ok = mbar_wait(&sm.full[s], (uint32_t)(use / kStages) & 1u, P.err))) break;
+        const int seen = w.r.kv - (w.b0 + j) * kRows;  // rows of the block that the request holds
+        uint4* v = reinterpret_cast<uint4*>(sm.ring[s] + half * kHalfBytes);
+        bool found = false;
+        for (int i = lane; i < kHalfBytes / 16; i += 32) {
+          if ((i >> 3) >= seen) {  // eight 16-byte pieces to a row (the swizzle moves them inside it only)
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+          }
+          const uint4 x = v[i];
+          uint32_t e[4] = {x.x, x.y, x.z, x.w};
+          bool hit = false;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (nonfinite16(e[k])) { e[k] &= 0xFFFF0000u; hit = true; }
+            if (nonfinite16(e[k] >> 16)) { e[k] &= 0x0000FFFFu; hit = true; }
+          }
+          if (hit) v[i] = make_uint4(e[0], e[1], e[2], e[3]);
+          found |= hit;
+        }
+        if (found) *reinterpret_cast<volatile int*>(&sm.poison[seg & 7]) = seg + 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.fixed[s]);
+      }
+      at += 2LL * w.nb;
+      w.advance();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
 }
 
 }  // namespace
 
-cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a, int sms, int* err, cudaStream_t st) {
-  (void)sms;
-  const long long rows = (long long)a.n_tokens * g.Hq;
-  k_paged_attention<<<(unsigned)((rows + kWarps - 1) / kWarps), kWarps * 32, 0, st>>>(a, g.Hq, g.Hkv, g.page, g.n_pages,
-                                                                                   g.max_pages, err);
+size_t wi_paged_attention_scratch(int sms) { return kPagedTicketBytes + (size_t)sms * 2 * kPartFloats * 4; }
+
+cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a, int sms, void* scratch, int* err,
+                                      cudaStream_t st) {
+  Params P;
+  P.a = a;
+  P.Hq = g.Hq;
+  P.Hkv = g.Hkv;
+  P.G = g.G;
+  P.tq = kRows / g.G;
+  P.page = g.page;
+  P.n_pages = g.n_pages;
+  P.max_pages = g.max_pages;
+  // a box of a block lies inside one page: the largest power of two that divides the page, 128 at most
+  P.box = g.page & -g.page;
+  if (P.box > kRows) P.box = kRows;
+  P.tickets = static_cast<unsigned*>(scratch);
+  P.parts = reinterpret_cast<float*>(static_cast<char*>(scratch) + kPagedTicketBytes);
+  P.err = err;
+  CUtensorMap map_q, map_k, map_v;
+  const unsigned long long rows = (unsigned long long)g.n_pages * g.Hkv * g.page;
+  if (!wi_encode_heads_sw128(&map_q, a.q, (unsigned long long)a.n_tokens, (unsigned)g.Hq, (unsigned)g.G,
+                             (unsigned)P.tq) ||
+      !wi_encode_rows_sw128(&map_k, a.k_pages, rows, (unsigned)P.box) ||
+      !wi_encode_rows_sw128(&map_v, a.v_pages, rows, (unsigned)P.box))
+    return cudaErrorInvalidValue;
+  static int smem_set[kWiSmemDevices] = {};
+  const cudaError_t e = wi_ensure_smem(k_paged_attention, sizeof(Smem), smem_set);
+  if (e != cudaSuccess) return e;
+  k_paged_attention<<<sms < kPagedMaxSms ? sms : kPagedMaxSms, kThreads, sizeof(Smem), st>>>(map_q, map_k, map_v, P);
   return cudaGetLastError();
 }
