@@ -205,6 +205,32 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
+// Two fp32 values in one 64-bit register pair.
+__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(a), "r"(b));
+  return x;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) { return pair(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 w = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&w);
@@ -395,6 +421,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
   Walk w;
   w.begin(P, sm, u1 - u0);
 
+  // a softmax lane holds a row of scores; the registers that the other warps do not need go to those
+  // (208 * 8 + 88 * 4 = 168 * 12, what the launch has)
+  if (warp < kSoftWarps)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp < kSoftWarps) {
     // ---------------- softmax
     const int chain = warp >> 2;
@@ -419,27 +451,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         if (ok) ok = mbar_wait(&sm.s_full[chain], s_par, P.err);
         s_par ^= 1;
         tc_fence_after();
-        uint32_t raw_s[4][32];
+        uint32_t s[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_nowait(ts + 32 * c, raw_s[c]);
+        for (int c = 0; c < 4; ++c) tmem_ld32_nowait(ts + 32 * c, s[c]);
         tmem_wait_ld();
-        float s[kRows];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) s[i] = __uint_as_float(raw_s[i >> 5][i & 31]);
         if (k0 + kRows - 1 > whole) {
+          const int seen = limit - k0;  // the row sees columns 0 .. seen of this block
 #pragma unroll
           for (int i = 0; i < kRows; ++i)
-            if (k0 + i > limit) s[i] = -INFINITY;
+            if (i > seen) s[i >> 5][i & 31] = 0xFF800000u;  // -infinity
         }
-        float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
+        float t[4];
 #pragma unroll
-        for (int i = 4; i < kRows; i += 4) {
-          t0 = fmaxf(t0, s[i]);
-          t1 = fmaxf(t1, s[i + 1]);
-          t2 = fmaxf(t2, s[i + 2]);
-          t3 = fmaxf(t3, s[i + 3]);
+        for (int c = 0; c < 4; ++c) {
+          t[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+          for (int i = 2; i < 32; i += 2) t[c] = max3(t[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
         }
-        const float top = fmaxf(fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)), -INFINITY) * kScaleLog2;
+        const float top = fmaxf(max3(t[0], t[1], max3(t[2], t[3], -INFINITY)), -INFINITY) * kScaleLog2;
         if (first) {
           m = top;
         } else {
@@ -449,34 +478,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
             const float f = need ? ex2(m - top) : 1.f;
             if (need) m = top;
             l *= f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tmem_ld32_nowait(to + 32 * c, o);
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tmem_ld16_nowait(to + 16 * c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32_nowait(to + 32 * c, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st16_nowait(to + 16 * c, o);
             }
           }
         }
         first = false;
         const float ref = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 2^-inf = 0
-        float l0 = 0.f, l1 = 0.f;
+        const uint64_t scale2 = pair(kScaleLog2, kScaleLog2), ref2 = pair(-ref, -ref);
+        uint64_t l2[2] = {pair(l, 0.f), 0ull};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t p[32];
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float a = ex2(fmaf(s[64 * c + 2 * i], kScaleLog2, -ref));
-            const float b = ex2(fmaf(s[64 * c + 2 * i + 1], kScaleLog2, -ref));
-            l0 += a;
-            l1 += b;
+          for (int i = 0; i < 16; ++i) {
+            const uint64_t x = fma2(pair(s[c][2 * i], s[c][2 * i + 1]), scale2, ref2);
+            const float a = ex2(lo_of(x)), b = ex2(hi_of(x));
+            l2[i & 1] = add2(l2[i & 1], pair(a, b));
             p[i] = pack2(a, b);
           }
-          tmem_st32_nowait(ts + 32 * c, p);
+          tmem_st16_nowait(ts + 16 * c, p);
         }
-        l += l0 + l1;
+        const uint64_t ls = add2(l2[0], l2[1]);
+        l = lo_of(ls) + hi_of(ls);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
