@@ -17,13 +17,14 @@
 // scratch; the last of its CTAs merges them in CTA order, so results do not
 // depend on timing.
 //
-// A CTA (384 threads) processes its items' blocks in roles:
-//   warps 0-3, 4-7  softmax, one thread per row of chain 0 / chain 1
-//   warp 8          TMA: queries, key and value blocks (box by box, through
+// A CTA (640 threads) processes its items' blocks in roles:
+//   warps 0-15      softmax: eight warps for each of two chains, two threads
+//                   per row (64 of the block's 128 positions each)
+//   warp 16         TMA: queries, key and value blocks (box by box, through
 //                   the block table) into a ring of five 32 KB stages
-//   warp 9          issues tcgen05.mma: S = Q K^T (both operands in shared
+//   warp 17         issues tcgen05.mma: S = Q K^T (both operands in shared
 //                   memory), O += P V (P in tensor memory, V N-major)
-//   warps 10-11     clean value rows of blocks that not every row sees whole
+//   warps 18-19     clean value rows of blocks that not every row sees whole
 // The two chains have their own S (P takes S's place) and O in tensor memory
 // (all 512 columns), so that one chain's softmax runs while the tensor cores
 // work on the other.  In an item of two tiles the chains are the tiles, and
@@ -53,7 +54,7 @@ constexpr int kRows = 128;                     // rows of a tile, and positions 
 constexpr int kStages = 5;
 constexpr int kTileBytes = kRows * WI_D * 2;   // 32 KB: two halves of 64 columns
 constexpr int kHalfBytes = kTileBytes / 2;
-constexpr int kSoftWarps = 8;
+constexpr int kSoftWarps = 16;
 constexpr int kThreads = 32 * (kSoftWarps + 4);
 constexpr int kFixWarps = 2;
 constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
@@ -77,13 +78,32 @@ struct Smem {
   int poison[8];            // segment number + 1 of the last segment (modulo 8) with an infinite or NaN value
   long long scan[kThreads / 32];
   int start[4];             // the run's first request, kv head, tile pair, block
-  float xm[kRows], xl[kRows];  // chain 1's maximum and sum, for chain 0
-  unsigned char pad[2048 - (4 * kStages + 9) * 8 - 8 - 32 - kThreads / 32 * 8 - 16 - 2 * kRows * 4];
+  float xch[2][2][kRows];   // between the two threads of a row: [chain][half]
+  unsigned char pad[3072 - (4 * kStages + 9) * 8 - 8 - 32 - kThreads / 32 * 8 - 16 - 4 * kRows * 4];
   unsigned char q[2][kTileBytes];          // [k half][128 rows][128 B]
   unsigned char ring[kStages][kTileBytes]; // [k half][128 rows][128 B]
 };
-static_assert(offsetof(Smem, q) == 2048, "tiles must start 1024-byte aligned");
+static_assert(offsetof(Smem, q) == 3072, "tiles must start 1024-byte aligned");
 static_assert(sizeof(Smem) <= 232448, "shared memory");
+
+// A position in the ring: the stage, and the parity of its current use.
+struct Ring {
+  int s = 0;
+  uint32_t par = 0;
+  __device__ __forceinline__ void step() {
+    if (++s == kStages) {
+      s = 0;
+      par ^= 1;
+    }
+  }
+  __device__ __forceinline__ void step(int n) {  // n < kStages
+    s += n;
+    if (s >= kStages) {
+      s -= kStages;
+      par ^= 1;
+    }
+  }
+};
 
 struct Params {
   WiPagedAttn a;
@@ -238,11 +258,16 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 
 __device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory"); }
 
+// The two warps that share 32 rows of a chain.
+__device__ __forceinline__ void rows_barrier(int chain, int quarter) {
+  asm volatile("bar.sync %0, 64;" ::"r"(2 + chain * 4 + quarter) : "memory");
+}
+
 __device__ __forceinline__ bool nonfinite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
-// Add the infinite and NaN values that a row sees in blocks [f0, f1) to 32 columns of its O.
+// Add the infinite and NaN values that a row sees in blocks [f0, f1) to 16 columns of its O.
 __device__ __forceinline__ void add_poison(const Params& P, int b, int kh, int f0, int f1, int kv, int limit, int c0,
-                                           float (&o)[32]) {
+                                           float (&o)[16]) {
   const int end = min(min(f1 * kRows, kv), limit + 1);
 #pragma unroll 1
   for (int p = f0 * kRows; p < end; ++p) {
@@ -251,7 +276,7 @@ __device__ __forceinline__ void add_poison(const Params& P, int b, int kh, int f
     const uint32_t* v = static_cast<const uint32_t*>(P.a.v_pages) +
                         ((((long long)pg * P.Hkv + kh) * P.page + (p - j * P.page)) * WI_D + c0) / 2;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const uint32_t w = v[i];
       if (nonfinite16(w)) o[2 * i] += bf16_lo(w);
       if (nonfinite16(w >> 16)) o[2 * i + 1] += bf16_hi(w);
@@ -272,7 +297,7 @@ __device__ void merge_parts(const Params& P, const Walk& w, int c0, int c1) {
   const int div = (65536 + P.G - 1) / P.G;  // r / G for r < 128
   for (int t = 0; t < (w.single ? 1 : 2); ++t) {
     const int rows = min(rows_tile, (w.cnt - t * P.tq) * P.G);
-    for (int r0 = (tid >> 7) * 8; r0 < rows; r0 += 16) {
+    for (int r0 = (tid >> 7) * 8; r0 < rows; r0 += kSoftWarps * 2) {
       float M[8], L[8], acc[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -360,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     mbar_init(&sm.q_empty, 1);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm.s_full[t], 1);
-      mbar_init(&sm.p_ready[t], 4);
+      mbar_init(&sm.p_ready[t], kSoftWarps / 2);
       mbar_init(&sm.o_full[t], 1);
     }
     mbar_init(&sm.drained, 1);
@@ -408,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
   }
-  if (warp == 9) {
+  if (warp == kSoftWarps + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem_base))
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -421,19 +446,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
   Walk w;
   w.begin(P, sm, u1 - u0);
 
-  // a softmax lane holds a row of scores; the registers that the other warps do not need go to those
-  // (208 * 8 + 88 * 4 = 168 * 12, what the launch has)
+  // a softmax lane holds half a row of scores; the registers that the other warps do not need go to those
+  // (104 * 16 + 64 * 4 = 96 * 20, what the launch has)
   if (warp < kSoftWarps)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
   else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   if (warp < kSoftWarps) {
     // ---------------- softmax
-    const int chain = warp >> 2;
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int chain = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t ts = tmem + lanes + (uint32_t)chain * kRows;
-    const uint32_t to = tmem + lanes + 256u + (uint32_t)chain * WI_D;
     const int tok = (row * ((65536 + P.G - 1) / P.G)) >> 16, head = row - tok * P.G;
     uint32_t s_par = 0, o_par0 = 0, o_par1 = 0;
     bool ok = true;  // after one timed-out wait the warp waits no more and writes nothing, but meets every barrier
@@ -444,32 +468,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       const bool live = tok < P.tq && ti < w.r.n;
       const int limit = live ? (int)(w.p0 + ti) : -1;   // the last position that the row sees
       const int whole = (int)(w.p0 + w.tile * w.tp + own_tile * P.tq);  // ... that all rows of the tile see
-      float m = -INFINITY, l = 0.f;
-      bool first = true;
+      float m = -INFINITY, l = 0.f;  // the row's reference maximum, and the sum of this thread's half
       for (int j = w.single ? chain : 0; j < w.nb; j += w.single ? 2 : 1) {
         const int k0 = (w.b0 + j) * kRows;
         if (ok) ok = mbar_wait(&sm.s_full[chain], s_par, P.err);
         s_par ^= 1;
         tc_fence_after();
-        uint32_t s[4][32];
+        uint32_t s[2][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_nowait(ts + 32 * c, s[c]);
+        for (int c = 0; c < 2; ++c) tmem_ld32_nowait(ts + 64 * half + 32 * c, s[c]);
         tmem_wait_ld();
         if (k0 + kRows - 1 > whole) {
-          const int seen = limit - k0;  // the row sees columns 0 .. seen of this block
+          const int seen = limit - k0 - 64 * half;  // the row sees columns 0 .. seen of this half
 #pragma unroll
-          for (int i = 0; i < kRows; ++i)
+          for (int i = 0; i < 64; ++i)
             if (i > seen) s[i >> 5][i & 31] = 0xFF800000u;  // -infinity
         }
         float t[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          t[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+          const int o = (c & 1) * 16;
+          t[c] = fmaxf(__uint_as_float(s[c >> 1][o]), __uint_as_float(s[c >> 1][o + 1]));
 #pragma unroll
-          for (int i = 2; i < 32; i += 2) t[c] = max3(t[c], __uint_as_float(s[c][i]), __uint_as_float(s[c][i + 1]));
+          for (int i = 2; i < 16; i += 2)
+            t[c] = max3(t[c], __uint_as_float(s[c >> 1][o + i]), __uint_as_float(s[c >> 1][o + i + 1]));
         }
-        const float top = fmaxf(max3(t[0], t[1], max3(t[2], t[3], -INFINITY)), -INFINITY) * kScaleLog2;
-        if (first) {
+        float top = fmaxf(max3(t[0], t[1], max3(t[2], t[3], -INFINITY)), -INFINITY) * kScaleLog2;
+        // The other half's maximum.  Past the barrier both threads have their scores in registers, so P may take
+        // S's place.  The slots are free again once the next scores of the chain are there: those wait for P.
+        sm.xch[chain][half][row] = top;
+        tc_fence_before();
+        rows_barrier(chain, quarter);
+        tc_fence_after();
+        top = fmaxf(top, sm.xch[chain][half ^ 1][row]);
+        if (j < 2 && (j == 0 || w.single)) {  // the chain's first block
           m = top;
         } else {
           const bool need = top > m + kLazy;
@@ -478,8 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
             const float f = need ? ex2(m - top) : 1.f;
             if (need) m = top;
             l *= f;
+            const uint32_t to = tmem + lanes + 256u + (uint32_t)chain * WI_D + 64u * half;
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < 4; ++c) {
               uint32_t o[16];
               tmem_ld16_nowait(to + 16 * c, o);
               tmem_wait_ld();
@@ -489,12 +522,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
             }
           }
         }
-        first = false;
         const float ref = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 2^-inf = 0
         const uint64_t scale2 = pair(kScaleLog2, kScaleLog2), ref2 = pair(-ref, -ref);
         uint64_t l2[2] = {pair(l, 0.f), 0ull};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t p[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -503,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
             l2[i & 1] = add2(l2[i & 1], pair(a, b));
             p[i] = pack2(a, b);
           }
-          tmem_st16_nowait(ts + 16 * c, p);
+          tmem_st16_nowait(ts + 32 * half + 16 * c, p);
         }
         const uint64_t ls = add2(l2[0], l2[1]);
         l = lo_of(ls) + hi_of(ls);
@@ -513,76 +545,82 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         if (lane == 0) mbar_arrive(&sm.p_ready[chain]);
       }
 
-      // ---- the segment's end
+      // ---- the segment's end: the sums of both halves, of both chains where they had one tile, then O
       const bool both = !w.single || w.nb > 1;  // chain 1 had blocks
-      if (w.single && chain == 1) {
-        sm.xm[row] = m;
-        sm.xl[row] = l;
-      }
-      if (ok && (chain == 0 || !both)) ok = mbar_wait(&sm.o_full[0], o_par0, P.err);
-      if (ok && both && (chain == 1 || w.single)) ok = mbar_wait(&sm.o_full[1], o_par1, P.err);
+      const bool part = w.b0 > 0 || w.nb < w.nblk;
+      if (ok && (w.single || chain == 0)) ok = mbar_wait(&sm.o_full[0], o_par0, P.err);
+      if (ok && both && (w.single || chain == 1)) ok = mbar_wait(&sm.o_full[1], o_par1, P.err);
       o_par0 ^= 1;
       if (both) o_par1 ^= 1;
       tc_fence_after();
-      const bool part = w.b0 > 0 || w.nb < w.nblk;
-      if (w.single) soft_barrier();
+      // half 1 gives its sum, half 0 the total (and the maximum) back; O is complete, so nobody reads a block's
+      // maximum from the slots any more
+      if (half == 1) sm.xch[chain][1][row] = l;
+      if (w.single) soft_barrier(); else rows_barrier(chain, quarter);
+      if (half == 0) {
+        l += sm.xch[chain][1][row];
+        sm.xch[chain][1][row] = l;
+        sm.xch[chain][0][row] = m;
+      }
+      if (w.single) soft_barrier(); else rows_barrier(chain, quarter);
+      l = sm.xch[chain][1][row];
       float f0 = 1.f, f1 = 0.f;
-      const bool writer = !w.single || chain == 0;
-      if (w.single && chain == 0 && both) {
-        const float m1 = sm.xm[row], M = fmaxf(m, m1), ref = M == -INFINITY ? 0.f : M;
-        f0 = ex2(m - ref);
+      if (w.single) {
+        const float m0 = sm.xch[0][0][row], m1 = sm.xch[1][0][row];
+        m = fmaxf(m0, m1);
+        const float ref = m == -INFINITY ? 0.f : m;
+        f0 = ex2(m0 - ref);
         f1 = ex2(m1 - ref);
-        l = l * f0 + sm.xl[row] * f1;
-        m = M;
+        l = sm.xch[0][1][row] * f0 + sm.xch[1][1][row] * f1;
       }
       const long long at = (long long)(w.r.s0 + ti) * P.Hq + w.kh * P.G + head;
       const int slot = 2 * (int)blockIdx.x + (w.b0 == 0 ? 1 : 0);
       float* dst = P.parts + (long long)slot * kPartFloats;
       const bool poison = *reinterpret_cast<volatile int*>(&sm.poison[seg & 7]) == seg + 1;
-      if (writer) {
-        const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+      const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+      const uint32_t to = tmem + lanes + 256u + (w.single ? 0u : (uint32_t)chain * WI_D);
+      const int ca = w.single ? 32 * (2 * chain + half) : 64 * half, cb = ca + (w.single ? 32 : 64);
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          __syncwarp();
-          uint32_t raw_o[32];
-          tmem_ld32_nowait(to + 32 * c, raw_o);
+      for (int c = ca; c < cb; c += 16) {
+        __syncwarp();
+        uint32_t raw_o[16];
+        tmem_ld16_nowait(to + c, raw_o);
+        tmem_wait_ld();
+        float o[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(raw_o[i]);
+        if (w.single && both) {
+          tmem_ld16_nowait(to + WI_D + c, raw_o);
           tmem_wait_ld();
-          float o[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(raw_o[i]);
-          if (w.single && both) {
-            tmem_ld32_nowait(to + WI_D + 32 * c, raw_o);
-            tmem_wait_ld();
+          for (int i = 0; i < 16; ++i) o[i] = o[i] * f0 + __uint_as_float(raw_o[i]) * f1;
+        }
+        if (poison && live)
+          add_poison(P, w.b, w.kh, max(w.b0, w.first_fix()), w.b0 + w.nb, w.r.kv, limit, c, o);
+        if (ok && live) {
+          if (part) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = o[i] * f0 + __uint_as_float(raw_o[i]) * f1;
-          }
-          if (poison && live)
-            add_poison(P, w.b, w.kh, max(w.b0, w.first_fix()), w.b0 + w.nb, w.r.kv, limit, 32 * c, o);
-          if (ok && live) {
-            if (part) {
+            for (int i = 0; i < 16; ++i) __stcg(dst + 512 + (own_tile * WI_D + c + i) * kRows + row, o[i]);
+          } else {
+            uint4* q = reinterpret_cast<uint4*>(static_cast<bf16*>(P.a.out) + at * WI_D + c);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) __stcg(dst + 512 + (own_tile * WI_D + 32 * c + i) * kRows + row, o[i]);
-            } else {
-              uint4* q = reinterpret_cast<uint4*>(static_cast<bf16*>(P.a.out) + at * WI_D + 32 * c);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint4 x;
-                x.x = pack2(o[8 * i] * inv, o[8 * i + 1] * inv);
-                x.y = pack2(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
-                x.z = pack2(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
-                x.w = pack2(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
-                q[i] = x;
-              }
+            for (int i = 0; i < 2; ++i) {
+              uint4 x;
+              x.x = pack2(o[8 * i] * inv, o[8 * i + 1] * inv);
+              x.y = pack2(o[8 * i + 2] * inv, o[8 * i + 3] * inv);
+              x.z = pack2(o[8 * i + 4] * inv, o[8 * i + 5] * inv);
+              x.w = pack2(o[8 * i + 6] * inv, o[8 * i + 7] * inv);
+              q[i] = x;
             }
           }
         }
-        if (ok && live) {
-          if (part) {
-            __stcg(dst + own_tile * kRows + row, m);
-            __stcg(dst + 256 + own_tile * kRows + row, l);
-          } else if (P.a.lse) {
-            P.a.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-          }
+      }
+      if (ok && live && half == 0 && (chain == 0 || !w.single)) {
+        if (part) {
+          __stcg(dst + own_tile * kRows + row, m);
+          __stcg(dst + 256 + own_tile * kRows + row, l);
+        } else if (P.a.lse) {
+          P.a.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
         }
       }
       tc_fence_before();  // O is read: the next segment may write it
@@ -604,12 +642,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         if (sm.last) merge_parts(P, w, c0, c1);
         soft_barrier();
       } else if (w.single) {
-        soft_barrier();  // chain 1's O has been read
+        soft_barrier();  // both chains' O, maxima and sums have been read
       }
       done += w.nb;
       w.advance();
     }
-  } else if (warp == 8) {
+  } else if (warp == kSoftWarps) {
     // ---------------- TMA: queries, keys, values
     if (lane == 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
@@ -618,8 +656,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     }
     const int boxes = kRows / P.box;  // boxes of a block, one lane each
     const uint32_t q_half = (uint32_t)(P.tq * P.G) * 128u;
-    long long issued = 0;             // ring stages filled
-    int q_loads = 0;
+    Ring at;                          // the next ring stage to fill
+    int filled = 0;                   // stages filled so far, counted up to the ring's length
+    int q_loads = 0, last = 0;        // last: the stage filled last
     bool ok = true;
     for (int seg = 0; ok && w.next(P); ++seg) {
       // queries, once the products of the segment before have read theirs
@@ -649,20 +688,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         return (pg * P.Hkv + w.kh) * P.page + (p - pj * P.page);
       };
       auto fill = [&](const CUtensorMap* map, int rowi) -> bool {
-        const int s = (int)(issued % kStages);
-        const long long round = issued / kStages;
         bool got = true;
-        if (round > 0) got = mbar_wait(&sm.empty[s], (uint32_t)(round - 1) & 1u, P.err);
+        if (filled == kStages) got = mbar_wait(&sm.empty[at.s], at.par ^ 1u, P.err);
         if (!__all_sync(0xffffffffu, got)) return false;
         const unsigned on = __ballot_sync(0xffffffffu, rowi >= 0);
-        if (lane == 0) mbar_arrive_expect_tx(&sm.full[s], (uint32_t)__popc(on) * P.box * 256u);
+        if (lane == 0) mbar_arrive_expect_tx(&sm.full[at.s], (uint32_t)__popc(on) * P.box * 256u);
         __syncwarp();
         if (rowi >= 0) {
-          unsigned char* dst = sm.ring[s] + lane * P.box * 128;
-          tma_load_2d(dst, map, 0, rowi, &sm.full[s]);
-          tma_load_2d(dst + kHalfBytes, map, 64, rowi, &sm.full[s]);
+          unsigned char* dst = sm.ring[at.s] + lane * P.box * 128;
+          tma_load_2d(dst, map, 0, rowi, &sm.full[at.s]);
+          tma_load_2d(dst + kHalfBytes, map, 64, rowi, &sm.full[at.s]);
         }
-        ++issued;
+        last = at.s;
+        at.step();
+        if (filled < kStages) ++filled;
         return true;
       };
       int r0 = row_of(0), r1 = row_of(1), r2 = row_of(2);
@@ -671,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       for (int j = 0; ok && j < w.nb; ++j) {
         const int r3 = row_of(j + 3);
         ok = fill(&map_v, r0);
-        if (ok && lane == 0 && w.b0 + j >= w.first_fix()) mbar_arrive(&sm.to_fix[(issued - 1) % kStages]);
+        if (ok && lane == 0 && w.b0 + j >= w.first_fix()) mbar_arrive(&sm.to_fix[last]);
         if (ok && j + ahead < w.nb) ok = fill(&map_k, ahead == 2 ? r2 : r1);
         r0 = r1;
         r1 = r2;
@@ -682,41 +721,49 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     // no copy is in flight when the CTA's shared memory goes (after a timed-out wait the tensor cores may not have
     // waited for them)
     if (q_loads > 0) mbar_wait(&sm.q_full, (uint32_t)(q_loads - 1) & 1u, P.err);
-    for (int s = 0; s < kStages && s < issued; ++s)
-      mbar_wait(&sm.full[s], (uint32_t)((issued - 1 - s) / kStages) & 1u, P.err);
-  } else if (warp == 9) {
-    // ---------------- tensor cores: one thread issues
-    if (lane == 0) {
+    for (int s = 0; s < filled; ++s)  // the last use of each stage: this turn's in front of `at`, else the turn before
+      mbar_wait(&sm.full[s], s < at.s ? at.par : at.par ^ 1u, P.err);
+  } else if (warp == kSoftWarps + 1) {
+    // ---------------- tensor cores: one lane issues, the whole warp computes what it issues
+    {
+      const uint32_t on = elect_one();
       constexpr uint32_t idesc_s = make_idesc(kRows, kRows);
       constexpr uint32_t idesc_o = make_idesc(kRows, WI_D) | kIdescNMajorB;
-      long long used = 0;        // ring stages consumed
-      uint32_t p_par[2] = {0, 0}, fix_par = 0;
+      Ring at;                   // the next ring stage to consume
+      uint32_t p_par = 0, fix_par = 0;
       bool ok = true;
+      auto all_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, P.err));
+      };
       auto scores = [&](int t, int q, int s) {
-        const uint32_t a0 = smem_addr(sm.q[q]), b0 = smem_addr(sm.ring[s]);
+        const uint32_t d = __shfl_sync(0xffffffffu, tmem + (uint32_t)t * kRows, 0);
+        const uint32_t a0 = __shfl_sync(0xffffffffu, desc_lo_kmajor(smem_addr(sm.q[q])), 0);
+        const uint32_t b0 = __shfl_sync(0xffffffffu, desc_lo_kmajor(smem_addr(sm.ring[s])), 0);
 #pragma unroll
         for (int kk = 0; kk < WI_D / 16; ++kk) {
-          const uint32_t off = (uint32_t)(kk >> 2) * kHalfBytes + (uint32_t)(kk & 3) * 32;
-          mma_bf16(tmem + (uint32_t)t * kRows, make_desc_sw128(a0 + off), make_desc_sw128(b0 + off), idesc_s, kk > 0);
+          const uint32_t off = ((uint32_t)(kk >> 2) * kHalfBytes + (uint32_t)(kk & 3) * 32) / 16;
+          mma_bf16_warp(on, d, a0 + off, b0 + off, idesc_s, kk > 0);
         }
-        mma_commit(&sm.s_full[t]);
+        mma_commit_warp(on, &sm.s_full[t]);
       };
       auto values = [&](int t, int s, bool add) {
-        const uint32_t b0 = smem_addr(sm.ring[s]);
+        const uint32_t p = __shfl_sync(0xffffffffu, tmem + (uint32_t)t * kRows, 0);
+        const uint32_t b0 = __shfl_sync(0xffffffffu, desc_lo_nmajor(smem_addr(sm.ring[s]), kHalfBytes), 0);
+        const uint32_t more = __shfl_sync(0xffffffffu, (uint32_t)add, 0);
+        const uint32_t d = __shfl_sync(0xffffffffu, tmem + 256u + (uint32_t)t * WI_D, 0);
 #pragma unroll
         for (int kk = 0; kk < kRows / 16; ++kk)
-          mma_bf16_ta(tmem + 256u + (uint32_t)t * WI_D, tmem + (uint32_t)t * kRows + (uint32_t)kk * 8,
-                      make_desc_sw128_nmajor(b0 + (uint32_t)kk * 2048, kHalfBytes), idesc_o, add || kk > 0);
+          mma_bf16_ta_warp(on, d, p + (uint32_t)kk * 8, b0 + (uint32_t)kk * (2048 / 16), idesc_o, kk > 0 ? 1u : more);
       };
-      auto take = [&](int* s) -> bool {  // the next ring stage, once it is full
-        *s = (int)(used % kStages);
-        const bool got = mbar_wait(&sm.full[*s], (uint32_t)(used / kStages) & 1u, P.err);
-        ++used;
+      auto take = [&](int* st) -> bool {  // the next ring stage, once it is full
+        *st = at.s;
+        const bool got = all_wait(&sm.full[at.s], at.par);
+        at.step();
         tc_fence_after();
         return got;
       };
       for (int seg = 0; ok && w.next(P); ++seg) {
-        ok = mbar_wait(&sm.q_full, seg & 1, P.err);
+        ok = all_wait(&sm.q_full, seg & 1);
         if (!ok) break;
         tc_fence_after();
         const int fix = w.first_fix() - w.b0;  // from this block of the segment on, values are cleaned first
@@ -724,62 +771,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         if (!(ok = take(&ks))) break;
         scores(0, 0, ks);
         if (w.single) {
-          mma_commit(&sm.empty[ks]);
+          mma_commit_warp(on, &sm.empty[ks]);
           if (w.nb > 1) {
             if (!(ok = take(&ks))) break;
             scores(1, 0, ks);
-            mma_commit(&sm.empty[ks]);
+            mma_commit_warp(on, &sm.empty[ks]);
           }
         } else {
           scores(1, 1, ks);
-          mma_commit(&sm.empty[ks]);
+          mma_commit_warp(on, &sm.empty[ks]);
         }
-        if (w.nb <= (w.single ? 2 : 1)) mma_commit(&sm.q_empty);
+        if (w.nb <= (w.single ? 2 : 1)) mma_commit_warp(on, &sm.q_empty);
         for (int j = 0; j < w.nb; ++j) {
           if (!(ok = take(&vs))) break;
           if (j >= fix) {
-            ok = mbar_wait(&sm.fixed[vs], (fix_par >> vs) & 1u, P.err);
+            ok = all_wait(&sm.fixed[vs], (fix_par >> vs) & 1u);
             fix_par ^= 1u << vs;
             if (!ok) break;
           }
           if (w.single) {
             const int t = j & 1;
-            if (!(ok = mbar_wait(&sm.p_ready[t], p_par[t], P.err))) break;
-            p_par[t] ^= 1;
+            if (!(ok = all_wait(&sm.p_ready[t], (p_par >> t) & 1u))) break;
+            p_par ^= 1u << t;
             tc_fence_after();
             values(t, vs, j >= 2);
-            mma_commit(&sm.empty[vs]);
+            mma_commit_warp(on, &sm.empty[vs]);
             if (j + 2 >= w.nb) {
-              mma_commit(&sm.o_full[t]);
+              mma_commit_warp(on, &sm.o_full[t]);
             } else {
               if (!(ok = take(&ks))) break;
               scores(t, 0, ks);
-              mma_commit(&sm.empty[ks]);
-              if (j + 3 >= w.nb) mma_commit(&sm.q_empty);
+              mma_commit_warp(on, &sm.empty[ks]);
+              if (j + 3 >= w.nb) mma_commit_warp(on, &sm.q_empty);
             }
           } else {
             const bool more = j + 1 < w.nb;
-            if (!(ok = mbar_wait(&sm.p_ready[0], p_par[0], P.err))) break;
-            p_par[0] ^= 1;
+            if (!(ok = all_wait(&sm.p_ready[0], (p_par >> 0) & 1u))) break;
+            p_par ^= 1u;
             tc_fence_after();
             values(0, vs, j > 0);
             if (more) {
               if (!(ok = take(&ks))) break;
               scores(0, 0, ks);
             } else {
-              mma_commit(&sm.o_full[0]);
+              mma_commit_warp(on, &sm.o_full[0]);
             }
-            if (!(ok = mbar_wait(&sm.p_ready[1], p_par[1], P.err))) break;
-            p_par[1] ^= 1;
+            if (!(ok = all_wait(&sm.p_ready[1], (p_par >> 1) & 1u))) break;
+            p_par ^= 2u;
             tc_fence_after();
             values(1, vs, j > 0);
-            mma_commit(&sm.empty[vs]);
+            mma_commit_warp(on, &sm.empty[vs]);
             if (more) {
               scores(1, 1, ks);
-              mma_commit(&sm.empty[ks]);
-              if (j + 2 >= w.nb) mma_commit(&sm.q_empty);
+              mma_commit_warp(on, &sm.empty[ks]);
+              if (j + 2 >= w.nb) mma_commit_warp(on, &sm.q_empty);
             } else {
-              mma_commit(&sm.o_full[1]);
+              mma_commit_warp(on, &sm.o_full[1]);
             }
           }
         }
@@ -787,26 +834,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         w.advance();
       }
       // every product is done before the tensor memory goes
-      mma_commit(&sm.drained);
+      mma_commit_warp(on, &sm.drained);
       mbar_wait(&sm.drained, 0, P.err);
     }
   } else {
     // ---------------- clean the value rows of blocks that not every row sees whole
-    const int half = warp - 10;  // 64 columns each
-    long long at = 0;            // the segment's first ring stage
+    const int half = warp - kSoftWarps - 2;  // 64 columns each
+    Ring at;                     // the ring stage of the next block in turn
     uint32_t fix_par = 0;
     bool ok = true;
     for (int seg = 0; ok && w.next(P); ++seg) {
-      const int ahead = w.single ? 2 : 1;
-      const int lead = min(ahead, w.nb);  // key blocks in front of the first value block
-      for (int j = max(0, w.first_fix() - w.b0); j < w.nb; ++j) {
-        // stages in front of value block j: the leading key blocks, j value blocks and the key blocks among them
-        const long long use = at + lead + j + max(0, min(j, w.nb - ahead));
-        const int s = (int)(use % kStages);
+      // stages in front of value block 0: the leading key blocks; between two: a value and a key block, where there
+      // still is one
+      const int ahead = w.single ? 2 : 1, from = w.first_fix() - w.b0;
+      at.step(min(ahead, w.nb));
+      for (int j = 0; j < w.nb; ++j, at.step(j + ahead - 1 < w.nb ? 2 : 1)) {
+        if (j < from) continue;
+        const int s = at.s;
         // only once the copy has been asked for does the stage's phase stand at this use
         if (!(ok = mbar_wait(&sm.to_fix[s], (fix_par >> s) & 1u, P.err))) break;
         fix_par ^= 1u << s;
-        if (!(ok = mbar_wait(&sm.full[s], (uint32_t)(use / kStages) & 1u, P.err))) break;
+        if (!(ok = mbar_wait(&sm.full[s], at.par, P.err))) break;
         const int seen = w.r.kv - (w.b0 + j) * kRows;  // rows of the block that the request holds
         uint4* v = reinterpret_cast<uint4*>(sm.ring[s] + half * kHalfBytes);
         bool found = false;
@@ -831,13 +879,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.fixed[s]);
       }
-      at += 2LL * w.nb;
       w.advance();
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kSoftWarps + 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }

@@ -54,30 +54,61 @@ __device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t adesc, uint64
       : "memory");
 }
 
-// The same product with A (K-major, two bf16 per 32-bit column) in tensor memory.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // Instruction descriptor bit of a B operand whose N elements are contiguous (N-major).
 constexpr uint32_t kIdescNMajorB = 1u << 16;
 
-// Shared-memory matrix descriptor of an N-major operand with the 128-byte swizzle: 64 N elements to a 128-byte
-// row, rows one k apart; `lbo` bytes to the next 64 N elements, 1024 (eight rows) to the next eight k.
-__device__ __forceinline__ uint64_t make_desc_sw128_nmajor(uint32_t saddr, uint32_t lbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
-  d |= (uint64_t)(lbo >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// The two words of a shared-memory matrix descriptor with the 128-byte swizzle, for code that the whole warp runs
+// with values it shares (the low word steps by bytes / 16 from one k step to the next).  K-major as in
+// make_desc_sw128; N-major: 64 N elements to a 128-byte row, rows one k apart, `lbo` bytes to the next 64 N
+// elements, 1024 (eight rows) to the next eight k.
+constexpr uint32_t kDescHiSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo_kmajor(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_lo_nmajor(uint32_t saddr, uint32_t lbo) {
+  return (saddr >> 4) | ((lbo >> 4) << 16);
+}
+
+// D (+)= A B issued by the lane with on != 0, A and B in shared memory.  Every lane runs the instruction's setup,
+// so the operands stay in uniform registers; under a branch on the lane each would be moved there again.
+__device__ __forceinline__ void mma_bf16_warp(uint32_t on, uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %6, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHiSw128), "r"(on)
+      : "memory");
+}
+
+// The same with A (K-major, two bf16 to a 32-bit column) in tensor memory.
+__device__ __forceinline__ void mma_bf16_ta_warp(uint32_t on, uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo,
+                                                 uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %6, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHiSw128), "r"(on)
+      : "memory");
+}
+
+// mma_commit by the lane with on != 0.
+__device__ __forceinline__ void mma_commit_warp(uint32_t on, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(on)
+      : "memory");
+}
+
+// One lane of the converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t on;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+  return on;
 }
 
 // Arrive on `bar` once every tcgen05 operation issued so far by this thread has completed.
