@@ -314,6 +314,18 @@ bool wi_encode_heads_sw128(CUtensorMap* map, const void* base, unsigned long lon
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool wi_encode_pages_sw128(CUtensorMap* map, const void* base, unsigned long long rows, unsigned box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {64u, 8u, 2u, (cuuint64_t)rows / 8};
+  const cuuint64_t strides[3] = {WI_D * 2, 128u, 8 * WI_D * 2};
+  const cuuint32_t box[4] = {64u, 8u, 2u, box_rows / 8};
+  const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool wi_tensor_maps_available() { return get_encode() != nullptr; }
 
 bool wi_assign_tc_supported(const WiGeom& g) {

@@ -82,9 +82,8 @@ struct WiPagedAttn {
   int batch, n_tokens;
 };
 constexpr int kPagedMaxSms = 1024;
-constexpr size_t kPagedTicketBytes = kPagedMaxSms * 4;  // at the start of the scratch, zero between calls
 // Scratch of the attention, part of the handle: two partial results per CTA (of an item that the CTA before began,
-// and of one that the CTA after ends) and the tickets of the merge.
+// and of one that the CTA after goes on with) and what the merge needs to know of the latter.
 size_t wi_paged_attention_scratch(int sms);
 cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a, int sms, void* scratch, int* err,
                                       cudaStream_t st);

@@ -8,14 +8,14 @@
 //
 // Work.  An item is one (request, kv head, pair of tiles); its key blocks of
 // 128 positions run from 0 to the last position that a row sees.  A unit is
-// one block of one item; all units of the call, item after item, are cut into
+// one block of one item, or one of two more for its start and end; all units
+// of the call, item after item, are cut into
 // equal runs, one per CTA (one CTA per SM), so single tokens over long
 // contexts split over the machine and ragged chunks balance without a plan
 // made on the host.  Lengths live on the device: each CTA sums the units of
 // all requests itself (closed form per request) and finds its run's start.
 // An item cut between CTAs leaves partial results (maximum, sum, O) in the
-// scratch; the last of its CTAs merges them in CTA order, so results do not
-// depend on timing.
+// scratch, which k_paged_merge adds up in CTA order.
 //
 // A CTA (640 threads) processes its items' blocks in roles:
 //   warps 0-15      softmax: eight warps for each of two chains, two threads
@@ -59,6 +59,8 @@ constexpr int kThreads = 32 * (kSoftWarps + 4);
 constexpr int kFixWarps = 2;
 constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
 constexpr float kLn2 = 0.6931471805599453f;
+// Units in front of an item's blocks, for what its start and end cost.
+constexpr int kLead = 2;
 // A row's reference maximum follows its true maximum only when that is more than 2^8 larger: the weights stay
 // below 256, which costs neither bf16 nor fp32 any precision, and O is rescaled a few times per item at most.
 constexpr float kLazy = 8.f;
@@ -74,14 +76,14 @@ struct Smem {
   uint64_t s_full[2], p_ready[2], o_full[2];
   uint64_t drained;
   uint32_t tmem_base;
-  int last;                 // the merge is this CTA's
+  int spare;                // keeps scan aligned
   int poison[8];            // segment number + 1 of the last segment (modulo 8) with an infinite or NaN value
   long long scan[kThreads / 32];
   int start[4];             // the run's first request, kv head, tile pair, block
   float xch[2][2][kRows];   // between the two threads of a row: [chain][half]
-  unsigned char pad[3072 - (4 * kStages + 9) * 8 - 8 - 32 - kThreads / 32 * 8 - 16 - 4 * kRows * 4];
+  unsigned char pad[3072 - (4 * kStages + 9) * 8 - 4 - 32 - 4 - kThreads / 32 * 8 - 16 - 4 * kRows * 4];
   unsigned char q[2][kTileBytes];          // [k half][128 rows][128 B]
-  unsigned char ring[kStages][kTileBytes]; // [k half][128 rows][128 B]
+  unsigned char ring[kStages][kTileBytes]; // [group of 8 rows][k half][8 rows][128 B]
 };
 static_assert(offsetof(Smem, q) == 3072, "tiles must start 1024-byte aligned");
 static_assert(sizeof(Smem) <= 232448, "shared memory");
@@ -105,12 +107,17 @@ struct Ring {
   }
 };
 
+// An item that CTA c begins and others go on with: what the merge needs of it.  last < 0: there is none.
+struct Split {
+  int row0, kh, cnt, last;  // first token (row of q), kv head, tokens, the item's last CTA
+};
+
 struct Params {
   WiPagedAttn a;
   int Hq, Hkv, G, tq;       // tq = tokens per tile
   int page, n_pages, max_pages, box;
   float* parts;
-  unsigned* tickets;
+  Split* splits;
   int* err;
 };
 
@@ -135,79 +142,90 @@ __device__ __forceinline__ int blocks_to(long long p0, long long end) {
   return e <= kRows ? 1 : (int)((e + kRows - 1) / kRows);
 }
 
-// Sum over i < n of floor((a i + b) / m), a, b >= 0: whole multiples of m are taken out of a and b, and what is
-// left counts lattice points under a line, which is the same problem with a and m exchanged.
-__device__ long long floor_sum(long long n, long long m, long long a, long long b) {
-  long long s = 0;
-  while (n > 0) {
-    s += (n - 1) * n / 2 * (a / m) + n * (b / m);
-    a %= m;
-    b %= m;
-    const long long y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y % m;
-    const long long t = a;
-    a = m;
+// Sum over i < n of floor((a i + b) / 128), a, b >= 0: whole multiples of the divisor m are taken out of a and b, and
+// what is left counts lattice points under a line, which is the same problem with a and m exchanged (n <= 2^19, so
+// that after the first step everything but the sum fits 32 bits).
+__device__ long long floor_sum(int n, int a, long long b) {
+  if (n <= 0) return 0;
+  long long s = (long long)n * (n - 1) / 2 * (a >> 7) + n * (b >> 7);
+  uint32_t k = (uint32_t)n, m = 128, u = (uint32_t)a & 127u, v = (uint32_t)b & 127u;
+  for (;;) {
+    const uint32_t y = u * k + v;
+    if (y < m) return s;
+    k = y / m;
+    v = y % m;
+    const uint32_t t = u;
+    u = m;
     m = t;
+    s += (long long)k * (k - 1) / 2 * (u / m) + (long long)k * (v / m);
+    u %= m;
+    v %= m;
   }
-  return s;
 }
 
-// Blocks of the first `m` tile pairs (none of them the last one, which may be shorter).
-__device__ long long blocks_before(long long p0, int tp, int m) {
-  long long z = p0 < 0 ? -p0 / tp : 0;  // pairs that end at or before position 0: one block each
-  if (z > m) z = m;
-  return z + floor_sum(m - z, kRows, tp, p0 + (z + 1) * tp + kRows - 1);
+// Units of the first `m` tile pairs (none of them the last one, which may be shorter).
+__device__ long long units_before(long long p0, int tp, int m) {
+  long long z = 0;  // pairs that end at or before position 0: one block each
+  if (p0 < 0) z = min(-p0 / tp, (long long)m);
+  return z + floor_sum((int)(m - z), tp, p0 + (z + 1) * tp + kRows - 1) + (long long)kLead * m;
+}
+
+// a / b; 64-bit division only where 32 bits do not do.
+__device__ __forceinline__ long long quot(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // Where a CTA stands in its run: one item's part after the other.
 struct Walk {
-  int b, kh, tile, blk;   // blk: the next block of the item
+  int b, kh, tile, at;    // at: the next unit of the item (its first kLead units stand for no block)
   long long left;         // units of the run still to come
   Req r;
   int tp, tiles;
-  // the current segment
-  int cnt, single, nblk, b0, nb;   // tokens, one tile, blocks of the item, first block, blocks of the segment
+  // the current segment: what the run holds of one item
+  int cnt, single, nblk, b0, nb, took;   // tokens, one tile, blocks of the item, first block, blocks, units
   long long p0;           // position of the request's token 0
 
   __device__ __forceinline__ void begin(const Params& P, const Smem& sm, long long units) {
     b = sm.start[0];
     kh = sm.start[1];
     tile = sm.start[2];
-    blk = sm.start[3];
+    at = sm.start[3];
     left = units;
     tp = 2 * P.tq;
-    if (left > 0) set(P);
+    set(P);
   }
   __device__ __forceinline__ void set(const Params& P) {
     r = load_req(P, b);
     p0 = (long long)r.kv - r.n;
     tiles = (r.n + tp - 1) / tp;
   }
-  // The next segment of the run; false at its end.
+  // The next segment of the run that has blocks; false at the run's end.
   __device__ __forceinline__ bool next(const Params& P) {
-    if (left <= 0) return false;
-    while (tile >= tiles) {   // past the request's last pair: next kv head, next request with tokens
-      tile = 0;
-      if (r.n == 0 || ++kh == P.Hkv) {
-        kh = 0;
-        if (++b >= P.a.batch) return false;
-        set(P);
+    while (left > 0) {
+      while (tile >= tiles) {   // past the request's last pair: next kv head, next request with tokens
+        tile = 0;
+        if (r.n == 0 || ++kh == P.Hkv) {
+          kh = 0;
+          if (++b >= P.a.batch) return false;
+          set(P);
+        }
       }
+      cnt = min(tp, r.n - tile * tp);
+      single = cnt <= P.tq;
+      nblk = blocks_to(p0, (long long)tile * tp + cnt);
+      took = (int)min((long long)(nblk + kLead - at), left);
+      b0 = max(0, at - kLead);
+      nb = max(0, at + took - kLead) - b0;
+      if (nb > 0) return true;
+      advance();
     }
-    cnt = min(tp, r.n - tile * tp);
-    single = cnt <= P.tq;
-    nblk = blocks_to(p0, (long long)tile * tp + cnt);
-    b0 = blk;
-    nb = (int)min((long long)(nblk - blk), left);
-    return true;
+    return false;
   }
   __device__ __forceinline__ void advance() {
-    left -= nb;
-    blk += nb;
-    if (blk >= nblk) {
-      blk = 0;
+    left -= took;
+    at += took;
+    if (at >= nblk + kLead) {
+      at = 0;
       ++tile;
     }
   }
@@ -286,61 +304,7 @@ __device__ __forceinline__ void add_poison(const Params& P, int b, int kh, int f
 
 // The CTA whose run holds unit u of `total`, cut into `ctas` runs.
 __device__ __forceinline__ int cta_of(long long u, long long total, int ctas) {
-  return (int)(((u + 1) * ctas - 1) / total);
-}
-
-// Merge the partial results of one item, made by CTAs c0 .. c1, in that order: a thread takes a column, eight
-// rows at a time.
-__device__ void merge_parts(const Params& P, const Walk& w, int c0, int c1) {
-  const int tid = threadIdx.x, d = tid & 127;
-  const int rows_tile = P.tq * P.G;
-  const int div = (65536 + P.G - 1) / P.G;  // r / G for r < 128
-  for (int t = 0; t < (w.single ? 1 : 2); ++t) {
-    const int rows = min(rows_tile, (w.cnt - t * P.tq) * P.G);
-    for (int r0 = (tid >> 7) * 8; r0 < rows; r0 += kSoftWarps * 2) {
-      float M[8], L[8], acc[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        M[i] = -INFINITY;
-        L[i] = acc[i] = 0.f;
-      }
-      for (int c = c0; c <= c1; ++c) {
-        const float* s = P.parts + (long long)(2 * c + (c == c0 ? 1 : 0)) * kPartFloats + t * kRows + r0;
-        const float4 a = __ldcg(reinterpret_cast<const float4*>(s)), b = __ldcg(reinterpret_cast<const float4*>(s + 4));
-        const float m[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) M[i] = fmaxf(M[i], m[i]);
-      }
-#pragma unroll 2
-      for (int c = c0; c <= c1; ++c) {
-        const float* s = P.parts + (long long)(2 * c + (c == c0 ? 1 : 0)) * kPartFloats;
-        const float4* ps = reinterpret_cast<const float4*>(s + t * kRows + r0);
-        const float4* pl = reinterpret_cast<const float4*>(s + 256 + t * kRows + r0);
-        const float4* po = reinterpret_cast<const float4*>(s + 512 + (t * WI_D + d) * kRows + r0);
-        const float4 m0 = __ldcg(ps), m1 = __ldcg(ps + 1), l0 = __ldcg(pl), l1 = __ldcg(pl + 1), o0 = __ldcg(po),
-                     o1 = __ldcg(po + 1);
-        const float m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
-        const float l[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w};
-        const float o[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float f = ex2(m[i] - (M[i] == -INFINITY ? 0.f : M[i]));
-          L[i] += f * l[i];
-          acc[i] += f * o[i];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = r0 + i;
-        if (r >= rows) break;
-        const int tok = (r * div) >> 16, h = r - tok * P.G;
-        const long long at = (long long)(w.r.s0 + w.tile * w.tp + t * P.tq + tok) * P.Hq + w.kh * P.G + h;
-        const float inv = L[i] == 0.f ? 0.f : 1.f / L[i];
-        static_cast<bf16*>(P.a.out)[at * WI_D + d] = __float2bfloat16_rn(acc[i] * inv);
-        if (P.a.lse && d == 0) P.a.lse[at] = L[i] == 0.f ? -INFINITY : M[i] * kLn2 + logf(L[i]);
-      }
-    }
-  }
+  return (int)quot((u + 1) * ctas - 1, total);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_constant__ CUtensorMap map_q,
@@ -348,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
                                                                 const __grid_constant__ CUtensorMap map_v,
                                                                 const __grid_constant__ Params P) {
   extern __shared__ __align__(1024) unsigned char raw[];
+  pdl_trigger();  // k_paged_merge may take the SMs as they fall free; it waits for this grid before it reads
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (smem_addr(raw) & 1023u) {  // the swizzled tiles need 1024-byte alignment; never run misaligned
@@ -359,13 +324,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
   const int per = (P.a.batch + kThreads - 1) / kThreads;
   const int rb0 = min(tid * per, P.a.batch), rb1 = min(rb0 + per, P.a.batch);
   const int tp = 2 * P.tq;
-  long long mine = 0;
+  long long mine = 0, cost = 0;  // cost: of one kv head of the last request looked at
   for (int b = rb0; b < rb1; ++b) {
     const Req r = load_req(P, b);
     if (!r.ok && blockIdx.x == 0) atomicOr(P.err, WI_DEVERR_BAD_LENGTH);
     if (r.n == 0) continue;
     const int tiles = (r.n + tp - 1) / tp;
-    mine += P.Hkv * (blocks_before((long long)r.kv - r.n, tp, tiles - 1) + blocks_to((long long)r.kv - r.n, r.n));
+    cost = units_before((long long)r.kv - r.n, tp, tiles - 1) + kLead + blocks_to((long long)r.kv - r.n, r.n);
+    mine += P.Hkv * cost;
   }
   long long before = mine;
 #pragma unroll
@@ -400,8 +366,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
   }
   before -= mine;
   const int ctas = (int)min((long long)gridDim.x, total);
-  if ((int)blockIdx.x >= ctas) return;  // fewer units than CTAs (the whole CTA leaves)
-  const long long u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
+  if ((int)blockIdx.x >= ctas) {  // fewer units than CTAs (the whole CTA leaves)
+    if (tid == 0) P.splits[blockIdx.x].last = -1;
+    return;
+  }
+  const long long u0 = quot(total * blockIdx.x, ctas), u1 = quot(total * (blockIdx.x + 1), ctas);
   if (u0 >= before && u0 < before + mine) {  // one thread's requests hold the run's first unit
     long long rem = u0 - before;
     for (int b = rb0; b < rb1; ++b) {
@@ -409,22 +378,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       if (r.n == 0) continue;
       const int tiles = (r.n + tp - 1) / tp;
       const long long p0 = (long long)r.kv - r.n;
-      const long long c = blocks_before(p0, tp, tiles - 1) + blocks_to(p0, r.n);
-      if (rem >= c * P.Hkv) {
-        rem -= c * P.Hkv;
+      if (per > 1) cost = units_before(p0, tp, tiles - 1) + kLead + blocks_to(p0, r.n);
+      if (rem >= cost * P.Hkv) {
+        rem -= cost * P.Hkv;
         continue;
       }
-      const int kh = (int)(rem / c);
-      rem -= c * kh;
+      const int kh = (int)quot(rem, cost);
+      rem -= cost * kh;
       int lo = 0, hi = tiles - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (blocks_before(p0, tp, mid) <= rem) lo = mid; else hi = mid - 1;
+        if (units_before(p0, tp, mid) <= rem) lo = mid; else hi = mid - 1;
       }
       sm.start[0] = b;
       sm.start[1] = kh;
       sm.start[2] = lo;
-      sm.start[3] = (int)(rem - blocks_before(p0, tp, lo));
+      sm.start[3] = (int)(rem - units_before(p0, tp, lo));
       break;
     }
   }
@@ -461,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     const int tok = (row * ((65536 + P.G - 1) / P.G)) >> 16, head = row - tok * P.G;
     uint32_t s_par = 0, o_par0 = 0, o_par1 = 0;
     bool ok = true;  // after one timed-out wait the warp waits no more and writes nothing, but meets every barrier
-    long long done = 0;
+    bool split = false;  // the run's last item goes on in the next CTA
     for (int seg = 0; w.next(P); ++seg) {
       const int own_tile = w.single ? 0 : chain;
       const int ti = w.tile * w.tp + own_tile * P.tq + tok;
@@ -624,29 +593,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         }
       }
       tc_fence_before();  // O is read: the next segment may write it
-      if (part) {
-        // the last CTA to bring its part of the item merges all of them
-        const long long item = u0 + done - w.b0;  // the item's first unit
-        const int c0 = cta_of(item, total, ctas), c1 = cta_of(item + w.nblk - 1, total, ctas);
-        __threadfence();
-        soft_barrier();
-        if (tid == 0) {
-          sm.last = 0;
-          if (ok) {
-            sm.last = ticket_acq_rel(P.tickets + c0) == (unsigned)(c1 - c0);
-            if (sm.last) P.tickets[c0] = 0;
-          }
-          __threadfence();
-        }
-        soft_barrier();
-        if (sm.last) merge_parts(P, w, c0, c1);
-        soft_barrier();
-      } else if (w.single) {
-        soft_barrier();  // both chains' O, maxima and sums have been read
+      if (part && w.b0 == 0 && tid == 0) {
+        split = true;
+        P.splits[blockIdx.x] = {w.r.s0 + w.tile * w.tp, w.kh, w.cnt, cta_of(u1 - w.left - w.at + kLead + w.nblk - 1, total, ctas)};
       }
-      done += w.nb;
+      if (w.single) soft_barrier();  // both chains' O, maxima and sums have been read
       w.advance();
     }
+    if (tid == 0 && !split) P.splits[blockIdx.x].last = -1;
   } else if (warp == kSoftWarps) {
     // ---------------- TMA: queries, keys, values
     if (lane == 0) {
@@ -654,7 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
     }
-    const int boxes = kRows / P.box;  // boxes of a block, one lane each
+    const uint32_t on = elect_one();
+    const int boxes = kRows / P.box;  // boxes of a block, one lane finds the page of each
     const uint32_t q_half = (uint32_t)(P.tq * P.G) * 128u;
     Ring at;                          // the next ring stage to fill
     int filled = 0;                   // stages filled so far, counted up to the ring's length
@@ -691,14 +646,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         bool got = true;
         if (filled == kStages) got = mbar_wait(&sm.empty[at.s], at.par ^ 1u, P.err);
         if (!__all_sync(0xffffffffu, got)) return false;
-        const unsigned on = __ballot_sync(0xffffffffu, rowi >= 0);
-        if (lane == 0) mbar_arrive_expect_tx(&sm.full[at.s], (uint32_t)__popc(on) * P.box * 256u);
+        // boxes behind the request's end are left out: always the last ones
+        const int n = __popc(__ballot_sync(0xffffffffu, rowi >= 0));
+        if (on) mbar_arrive_expect_tx(&sm.full[at.s], (uint32_t)(n * P.box) * 256u);
         __syncwarp();
-        if (rowi >= 0) {
-          unsigned char* dst = sm.ring[at.s] + lane * P.box * 128;
-          tma_load_2d(dst, map, 0, rowi, &sm.full[at.s]);
-          tma_load_2d(dst + kHalfBytes, map, 64, rowi, &sm.full[at.s]);
-        }
+        const uint32_t dst = smem_addr(sm.ring[at.s]);
+        for (int i = 0; i < n; ++i)
+          tma_load_4d_warp(on, dst + (uint32_t)(i * P.box) * 256u, map, 0, 0, 0, __shfl_sync(0xffffffffu, rowi, i) >> 3,
+                           &sm.full[at.s]);
         last = at.s;
         at.step();
         if (filled < kStages) ++filled;
@@ -742,18 +697,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
 #pragma unroll
         for (int kk = 0; kk < WI_D / 16; ++kk) {
           const uint32_t off = ((uint32_t)(kk >> 2) * kHalfBytes + (uint32_t)(kk & 3) * 32) / 16;
-          mma_bf16_warp(on, d, a0 + off, b0 + off, idesc_s, kk > 0);
+          const uint32_t offb = ((uint32_t)(kk >> 2) * 1024 + (uint32_t)(kk & 3) * 32) / 16;
+          mma_bf16_warp(on, d, a0 + off, desc_hi_sw128(1024), b0 + offb, desc_hi_sw128(2048), idesc_s, kk > 0);
         }
         mma_commit_warp(on, &sm.s_full[t]);
       };
       auto values = [&](int t, int s, bool add) {
         const uint32_t p = __shfl_sync(0xffffffffu, tmem + (uint32_t)t * kRows, 0);
-        const uint32_t b0 = __shfl_sync(0xffffffffu, desc_lo_nmajor(smem_addr(sm.ring[s]), kHalfBytes), 0);
+        const uint32_t b0 = __shfl_sync(0xffffffffu, desc_lo_nmajor(smem_addr(sm.ring[s]), 1024), 0);
         const uint32_t more = __shfl_sync(0xffffffffu, (uint32_t)add, 0);
         const uint32_t d = __shfl_sync(0xffffffffu, tmem + 256u + (uint32_t)t * WI_D, 0);
 #pragma unroll
         for (int kk = 0; kk < kRows / 16; ++kk)
-          mma_bf16_ta_warp(on, d, p + (uint32_t)kk * 8, b0 + (uint32_t)kk * (2048 / 16), idesc_o, kk > 0 ? 1u : more);
+          mma_bf16_ta_warp(on, d, p + (uint32_t)kk * 8, b0 + (uint32_t)kk * (4096 / 16), desc_hi_sw128(2048), idesc_o,
+                           kk > 0 ? 1u : more);
       };
       auto take = [&](int* st) -> bool {  // the next ring stage, once it is full
         *st = at.s;
@@ -839,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     }
   } else {
     // ---------------- clean the value rows of blocks that not every row sees whole
-    const int half = warp - kSoftWarps - 2;  // 64 columns each
+    const int half = warp - kSoftWarps - 2;  // 64 rows each
     Ring at;                     // the ring stage of the next block in turn
     uint32_t fix_par = 0;
     bool ok = true;
@@ -856,10 +813,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         fix_par ^= 1u << s;
         if (!(ok = mbar_wait(&sm.full[s], at.par, P.err))) break;
         const int seen = w.r.kv - (w.b0 + j) * kRows;  // rows of the block that the request holds
-        uint4* v = reinterpret_cast<uint4*>(sm.ring[s] + half * kHalfBytes);
+        uint4* v = reinterpret_cast<uint4*>(sm.ring[s] + half * kHalfBytes);  // 64 rows: [8 groups][2][8 rows][8 pieces]
         bool found = false;
         for (int i = lane; i < kHalfBytes / 16; i += 32) {
-          if ((i >> 3) >= seen) {  // eight 16-byte pieces to a row (the swizzle moves them inside it only)
+          if (half * 64 + (i >> 7) * 8 + ((i >> 3) & 7) >= seen) {  // (the swizzle moves pieces inside a row only)
             v[i] = make_uint4(0u, 0u, 0u, 0u);
             continue;
           }
@@ -890,9 +847,107 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
   }
 }
 
+// ---------------------------------------------------------------- merge of cut items
+//
+// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over the CTAs c that worked on an item, in CTA order.  A block
+// takes 64 rows of one cut item: first each row's maximum and sum, then O, a thread per column and eight rows.  Up to
+// eight rows (single tokens), whose item may be cut into as many parts as there are SMs, the block's eight groups
+// share the parts out instead.
+constexpr int kMergeThreads = 512;
+constexpr int kMergeRows = 64;
+constexpr int kMergeGroups = kMergeThreads / WI_D;
+
+__global__ void __launch_bounds__(kMergeThreads) k_paged_merge(const __grid_constant__ Params P) {
+  constexpr int kParts = kMergeThreads / kMergeRows;  // threads that share a row's maximum and sum
+  __shared__ float pm[kParts][kMergeRows], pl[kParts][kMergeRows];
+  __shared__ float acc_s[kMergeGroups][8][WI_D];
+  pdl_wait();
+  const Split sp = P.splits[blockIdx.x];
+  if (sp.last < 0) return;
+  const int tid = threadIdx.x, c0 = blockIdx.x, parts = sp.last - c0 + 1;
+  // the item's rows: tile 0's tq * G, then tile 1's; row x of the partials lies in tile x / 128
+  const int t = blockIdx.y >> 1, base = (blockIdx.y & 1) * kMergeRows;
+  const int rows = min(P.tq, sp.cnt - t * P.tq) * P.G - base;  // rows of the tile from `base` on
+  if (rows <= 0) return;
+  auto part = [&](int i) -> const float* { return P.parts + (long long)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kPartFloats; };
+  auto store = [&](int r, int d, float v) {
+    const int x = base + r, tok = x / P.G;
+    static_cast<bf16*>(P.a.out)[((long long)(sp.row0 + t * P.tq + tok) * P.Hq + sp.kh * P.G + x - tok * P.G) * WI_D + d] =
+        __float2bfloat16_rn(v);
+  };
+  {
+    const int r = tid & 63, g = tid >> 6;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 2
+    for (int i = g; i < parts; i += kParts) {
+      const float* s = part(i) + t * kRows + base + r;
+      const float mi = s[0], li = s[256], M = fmaxf(m, mi), ref = M == -INFINITY ? 0.f : M;
+      l = l * ex2(m - ref) + li * ex2(mi - ref);
+      m = M;
+    }
+    pm[g][r] = m;
+    pl[g][r] = l;
+  }
+  __syncthreads();
+  if (tid < kMergeRows) {
+    float M = -INFINITY, L = 0.f;
+    for (int g = 0; g < kParts; ++g) M = fmaxf(M, pm[g][tid]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    for (int g = 0; g < kParts; ++g) L += pl[g][tid] * ex2(pm[g][tid] - ref);
+    pm[0][tid] = ref;
+    pl[0][tid] = L == 0.f ? 0.f : 1.f / L;
+    if (P.a.lse && tid < rows) {
+      const int r = base + tid, tok = r / P.G;
+      P.a.lse[(long long)(sp.row0 + t * P.tq + tok) * P.Hq + sp.kh * P.G + r - tok * P.G] =
+          L == 0.f ? -INFINITY : M * kLn2 + logf(L);
+    }
+  }
+  __syncthreads();
+  const int d = tid & 127, g = tid >> 7;
+  const bool few = rows <= 8;
+  for (int r0 = few ? 0 : g * 8; r0 < rows && r0 < kMergeRows; r0 += kMergeGroups * 8) {
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float ref[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) ref[k] = pm[0][r0 + k];
+#pragma unroll 4
+    for (int i = few ? g : 0; i < parts; i += few ? kMergeGroups : 1) {
+      const float* s = part(i);
+      const float4* ps = reinterpret_cast<const float4*>(s + t * kRows + base + r0);
+      const float4* po = reinterpret_cast<const float4*>(s + 512 + (t * WI_D + d) * kRows + base + r0);
+      const float4 m0 = ps[0], m1 = ps[1], o0 = po[0], o1 = po[1];
+      acc[0] += ex2(m0.x - ref[0]) * o0.x;
+      acc[1] += ex2(m0.y - ref[1]) * o0.y;
+      acc[2] += ex2(m0.z - ref[2]) * o0.z;
+      acc[3] += ex2(m0.w - ref[3]) * o0.w;
+      acc[4] += ex2(m1.x - ref[4]) * o1.x;
+      acc[5] += ex2(m1.y - ref[5]) * o1.y;
+      acc[6] += ex2(m1.z - ref[6]) * o1.z;
+      acc[7] += ex2(m1.w - ref[7]) * o1.w;
+    }
+    if (few) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc_s[g][k][d] = acc[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (r0 + k < rows) store(r0 + k, d, acc[k] * pl[0][r0 + k]);
+    }
+  }
+  if (few) {
+    __syncthreads();
+    for (int r = g; r < rows; r += kMergeGroups) {
+      float a = 0.f;
+      for (int i = 0; i < kMergeGroups; ++i) a += acc_s[i][r][d];
+      store(r, d, a * pl[0][r]);
+    }
+  }
+}
+
 }  // namespace
 
-size_t wi_paged_attention_scratch(int sms) { return kPagedTicketBytes + (size_t)sms * 2 * kPartFloats * 4; }
+constexpr size_t kSplitBytes = kPagedMaxSms * sizeof(Split);
+size_t wi_paged_attention_scratch(int sms) { return kSplitBytes + (size_t)sms * 2 * kPartFloats * 4; }
 
 cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a, int sms, void* scratch, int* err,
                                       cudaStream_t st) {
@@ -908,19 +963,30 @@ cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a
   // a box of a block lies inside one page: the largest power of two that divides the page, 128 at most
   P.box = g.page & -g.page;
   if (P.box > kRows) P.box = kRows;
-  P.tickets = static_cast<unsigned*>(scratch);
-  P.parts = reinterpret_cast<float*>(static_cast<char*>(scratch) + kPagedTicketBytes);
+  P.splits = static_cast<Split*>(scratch);
+  P.parts = reinterpret_cast<float*>(static_cast<char*>(scratch) + kSplitBytes);
   P.err = err;
   CUtensorMap map_q, map_k, map_v;
   const unsigned long long rows = (unsigned long long)g.n_pages * g.Hkv * g.page;
   if (!wi_encode_heads_sw128(&map_q, a.q, (unsigned long long)a.n_tokens, (unsigned)g.Hq, (unsigned)g.G,
                              (unsigned)P.tq) ||
-      !wi_encode_rows_sw128(&map_k, a.k_pages, rows, (unsigned)P.box) ||
-      !wi_encode_rows_sw128(&map_v, a.v_pages, rows, (unsigned)P.box))
+      !wi_encode_pages_sw128(&map_k, a.k_pages, rows, (unsigned)P.box) ||
+      !wi_encode_pages_sw128(&map_v, a.v_pages, rows, (unsigned)P.box))
     return cudaErrorInvalidValue;
   static int smem_set[kWiSmemDevices] = {};
-  const cudaError_t e = wi_ensure_smem(k_paged_attention, sizeof(Smem), smem_set);
+  cudaError_t e = wi_ensure_smem(k_paged_attention, sizeof(Smem), smem_set);
   if (e != cudaSuccess) return e;
-  k_paged_attention<<<sms < kPagedMaxSms ? sms : kPagedMaxSms, kThreads, sizeof(Smem), st>>>(map_q, map_k, map_v, P);
-  return cudaGetLastError();
+  const int grid = sms < kPagedMaxSms ? sms : kPagedMaxSms;
+  k_paged_attention<<<grid, kThreads, sizeof(Smem), st>>>(map_q, map_k, map_v, P);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((unsigned)grid, 2 * kRows / kMergeRows);
+  lc.blockDim = dim3(kMergeThreads);
+  lc.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, k_paged_merge, P);
 }

@@ -44,6 +44,17 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// A 4-D box by the lane with on != 0 (every lane runs the setup, as for mma_bf16_warp).
+__device__ __forceinline__ void tma_load_4d_warp(uint32_t on, uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                                 int w, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %7, 0;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+      "%5}], [%6];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar)), "r"(on)
+      : "memory");
+}
+
 __device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
@@ -58,10 +69,12 @@ __device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t adesc, uint64
 constexpr uint32_t kIdescNMajorB = 1u << 16;
 
 // The two words of a shared-memory matrix descriptor with the 128-byte swizzle, for code that the whole warp runs
-// with values it shares (the low word steps by bytes / 16 from one k step to the next).  K-major as in
-// make_desc_sw128; N-major: 64 N elements to a 128-byte row, rows one k apart, `lbo` bytes to the next 64 N
-// elements, 1024 (eight rows) to the next eight k.
-constexpr uint32_t kDescHiSw128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+// with values it shares (the low word steps by bytes / 16 from one k step to the next).  K-major: `group` bytes from
+// eight rows to the next eight.  N-major (64 N elements to a 128-byte row, rows one k apart): `group` bytes from
+// eight k to the next eight, `lbo` bytes to the next 64 N elements.
+__device__ __forceinline__ constexpr uint32_t desc_hi_sw128(uint32_t group) {
+  return (group >> 4) | (1u << 14) | (2u << 29);
+}
 __device__ __forceinline__ uint32_t desc_lo_kmajor(uint32_t saddr) { return (saddr >> 4) | (1u << 16); }
 __device__ __forceinline__ uint32_t desc_lo_nmajor(uint32_t saddr, uint32_t lbo) {
   return (saddr >> 4) | ((lbo >> 4) << 16);
@@ -69,29 +82,29 @@ __device__ __forceinline__ uint32_t desc_lo_nmajor(uint32_t saddr, uint32_t lbo)
 
 // D (+)= A B issued by the lane with on != 0, A and B in shared memory.  Every lane runs the instruction's setup,
 // so the operands stay in uniform registers; under a branch on the lane each would be moved there again.
-__device__ __forceinline__ void mma_bf16_warp(uint32_t on, uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo,
-                                              uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_bf16_warp(uint32_t on, uint32_t tmem_d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                              uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %6, 0;\n\t"
+      "setp.ne.b32 e, %7, 0;\n\t"
       "mov.b64 a, {%1, %5};\n\t"
-      "mov.b64 b, {%2, %5};\n\t"
+      "mov.b64 b, {%2, %6};\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHiSw128), "r"(on)
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(a_hi), "r"(b_hi), "r"(on)
       : "memory");
 }
 
 // The same with A (K-major, two bf16 to a 32-bit column) in tensor memory.
 __device__ __forceinline__ void mma_bf16_ta_warp(uint32_t on, uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo,
-                                                 uint32_t idesc, uint32_t accumulate) {
+                                                 uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "setp.ne.b32 e, %6, 0;\n\t"
       "mov.b64 b, {%2, %5};\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHiSw128), "r"(on)
+      "r"(tmem_a), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(b_hi), "r"(on)
       : "memory");
 }
 
