@@ -8,9 +8,9 @@
 //
 // Work.  An item is one (request, kv head, pair of tiles); its key blocks of
 // 128 positions run from 0 to the last position that a row sees.  A unit is
-// one block of one item, or one of two more for its start and end; all units
-// of the call, item after item, are cut into
-// equal runs, one per CTA (one CTA per SM), so single tokens over long
+// one block of one item, or one of four more for its start and end; all units
+// of the call, item after item, are cut into equal runs, one per CTA (one CTA
+// per SM), so single tokens over long
 // contexts split over the machine and ragged chunks balance without a plan
 // made on the host.  Lengths live on the device: each CTA sums the units of
 // all requests itself (closed form per request) and finds its run's start.
@@ -59,8 +59,9 @@ constexpr int kThreads = 32 * (kSoftWarps + 4);
 constexpr int kFixWarps = 2;
 constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
 constexpr float kLn2 = 0.6931471805599453f;
-// Units in front of an item's blocks, for what its start and end cost.
-constexpr int kLead = 2;
+// Units in front of an item's blocks, for what its start and end cost (8192 fresh tokens, 32 / 8 heads: 542, 502, 466,
+// 439, 444 us at 1, 2, 3, 4, 6; longer contexts and single tokens do not care).
+constexpr int kLead = 4;
 // A row's reference maximum follows its true maximum only when that is more than 2^8 larger: the weights stay
 // below 256, which costs neither bf16 nor fp32 any precision, and O is rescaled a few times per item at most.
 constexpr float kLazy = 8.f;
@@ -849,97 +850,136 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
 
 // ---------------------------------------------------------------- merge of cut items
 //
-// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over the CTAs c that worked on an item, in CTA order.  A block
-// takes 64 rows of one cut item: first each row's maximum and sum, then O, a thread per column and eight rows.  Up to
-// eight rows (single tokens), whose item may be cut into as many parts as there are SMs, the block's eight groups
-// share the parts out instead.
+// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over the CTAs c that worked on an item: one pass over the parts
+// with the running maximum, in a fixed order.  A block takes 32 rows of one cut item.  What counts is latency: a few
+// parts of many rows are read with a lane to a row, as they were written, every load issued before the first is used,
+// and turned in shared memory for the way out; many parts (single tokens over a long context, cut into as many as
+// there are SMs) with four lanes sharing them out, four rows at a time.
 constexpr int kMergeThreads = 512;
-constexpr int kMergeRows = 64;
-constexpr int kMergeGroups = kMergeThreads / WI_D;
+constexpr int kMergeRows = 32;
+constexpr int kMergeWide = 4;  // parts up to which a lane reads them all
 
-__global__ void __launch_bounds__(kMergeThreads) k_paged_merge(const __grid_constant__ Params P) {
-  constexpr int kParts = kMergeThreads / kMergeRows;  // threads that share a row's maximum and sum
-  __shared__ float pm[kParts][kMergeRows], pl[kParts][kMergeRows];
-  __shared__ float acc_s[kMergeGroups][8][WI_D];
+template <int N>
+struct RowSums {
+  float m[N], l[N], o[N];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      m[k] = -INFINITY;
+      l[k] = o[k] = 0.f;
+    }
+  }
+  __device__ __forceinline__ void add(int k, float mi, float li, float oi) {
+    const float M = fmaxf(m[k], mi), ref = M == -INFINITY ? 0.f : M;
+    const float a = ex2(m[k] - ref), b = ex2(mi - ref);
+    m[k] = M;
+    l[k] = l[k] * a + li * b;
+    o[k] = o[k] * a + oi * b;
+  }
+  __device__ __forceinline__ void add4(int k, const float* pm, const float* po) {
+    const float4 a = __ldcg(reinterpret_cast<const float4*>(pm)), b = __ldcg(reinterpret_cast<const float4*>(pm + 256)),
+                 c = __ldcg(reinterpret_cast<const float4*>(po));
+    add(k, a.x, b.x, c.x);
+    add(k + 1, a.y, b.y, c.y);
+    add(k + 2, a.z, b.z, c.z);
+    add(k + 3, a.w, b.w, c.w);
+  }
+};
+
+__global__ void __launch_bounds__(kMergeThreads, 2) k_paged_merge(const __grid_constant__ Params P) {
   pdl_wait();
   const Split sp = P.splits[blockIdx.x];
   if (sp.last < 0) return;
-  const int tid = threadIdx.x, c0 = blockIdx.x, parts = sp.last - c0 + 1;
-  // the item's rows: tile 0's tq * G, then tile 1's; row x of the partials lies in tile x / 128
-  const int t = blockIdx.y >> 1, base = (blockIdx.y & 1) * kMergeRows;
-  const int rows = min(P.tq, sp.cnt - t * P.tq) * P.G - base;  // rows of the tile from `base` on
-  if (rows <= 0) return;
+  static_assert(kMergeThreads / 32 * 8 == WI_D && kMergeThreads / 16 == kMergeRows, "thread maps");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x, parts = sp.last - c0 + 1;
+  // the partials' rows: tile 0's, then from 128 on tile 1's
+  const int t = blockIdx.y / (kRows / kMergeRows), base = blockIdx.y % (kRows / kMergeRows) * kMergeRows;
+  const int rows = min(P.tq, sp.cnt - t * P.tq) * P.G;  // rows of the tile
+  if (base >= rows) return;
   auto part = [&](int i) -> const float* { return P.parts + (long long)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kPartFloats; };
-  auto store = [&](int r, int d, float v) {
-    const int x = base + r, tok = x / P.G;
-    static_cast<bf16*>(P.a.out)[((long long)(sp.row0 + t * P.tq + tok) * P.Hq + sp.kh * P.G + x - tok * P.G) * WI_D + d] =
-        __float2bfloat16_rn(v);
+  auto store = [&](int r, int d, float m, float l, float o) {
+    if (r >= rows) return;
+    const int tok = r / P.G;
+    const long long at = (long long)(sp.row0 + t * P.tq + tok) * P.Hq + sp.kh * P.G + r - tok * P.G;
+    static_cast<bf16*>(P.a.out)[at * WI_D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+    if (P.a.lse && d == 0) P.a.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
   };
-  {
-    const int r = tid & 63, g = tid >> 6;
-    float m = -INFINITY, l = 0.f;
-#pragma unroll 2
-    for (int i = g; i < parts; i += kParts) {
-      const float* s = part(i) + t * kRows + base + r;
-      const float mi = s[0], li = s[256], M = fmaxf(m, mi), ref = M == -INFINITY ? 0.f : M;
-      l = l * ex2(m - ref) + li * ex2(mi - ref);
-      m = M;
+  if (parts <= kMergeWide) {
+    __shared__ __align__(16) bf16 turn[kMergeRows][WI_D + 8];
+    const int r = base + lane, d0 = warp * 8;  // sixteen warps take eight columns each
+    float m[kMergeWide], l[kMergeWide], o[kMergeWide][8];
+#pragma unroll
+    for (int i = 0; i < kMergeWide; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      if (i < parts) {
+        const float* p = part(i) + t * kRows + r;
+        m[i] = __ldcg(p);
+        l[i] = __ldcg(p + 256);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[i][k] = __ldcg(part(i) + 512 + (t * WI_D + d0 + k) * kRows + r);
+      }
     }
-    pm[g][r] = m;
-    pl[g][r] = l;
-  }
-  __syncthreads();
-  if (tid < kMergeRows) {
-    float M = -INFINITY, L = 0.f;
-    for (int g = 0; g < kParts; ++g) M = fmaxf(M, pm[g][tid]);
+    float M = m[0], L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 1; i < kMergeWide; ++i) M = fmaxf(M, m[i]);
     const float ref = M == -INFINITY ? 0.f : M;
-    for (int g = 0; g < kParts; ++g) L += pl[g][tid] * ex2(pm[g][tid] - ref);
-    pm[0][tid] = ref;
-    pl[0][tid] = L == 0.f ? 0.f : 1.f / L;
-    if (P.a.lse && tid < rows) {
-      const int r = base + tid, tok = r / P.G;
+#pragma unroll
+    for (int i = 0; i < kMergeWide; ++i)
+      if (i < parts) {
+        const float f = ex2(m[i] - ref);
+        L += l[i] * f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] += o[i][k] * f;
+      }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    uint4 x;
+    x.x = pack2(acc[0] * inv, acc[1] * inv);
+    x.y = pack2(acc[2] * inv, acc[3] * inv);
+    x.z = pack2(acc[4] * inv, acc[5] * inv);
+    x.w = pack2(acc[6] * inv, acc[7] * inv);
+    *reinterpret_cast<uint4*>(&turn[lane][d0]) = x;
+    __syncthreads();
+    const int q = base + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 8;  // sixteen threads store a row
+    if (q < rows) {
+      const int tok = q / P.G;
+      const long long at = (long long)(sp.row0 + t * P.tq + tok) * P.Hq + sp.kh * P.G + q - tok * P.G;
+      *reinterpret_cast<uint4*>(static_cast<bf16*>(P.a.out) + at * WI_D + c) =
+          *reinterpret_cast<const uint4*>(&turn[q - base][c]);
+    }
+    if (P.a.lse && warp == 0 && r < rows) {
+      const int tok = r / P.G;
       P.a.lse[(long long)(sp.row0 + t * P.tq + tok) * P.Hq + sp.kh * P.G + r - tok * P.G] =
           L == 0.f ? -INFINITY : M * kLn2 + logf(L);
     }
-  }
-  __syncthreads();
-  const int d = tid & 127, g = tid >> 7;
-  const bool few = rows <= 8;
-  for (int r0 = few ? 0 : g * 8; r0 < rows && r0 < kMergeRows; r0 += kMergeGroups * 8) {
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    float ref[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) ref[k] = pm[0][r0 + k];
+  } else {
+    const int d = warp * 8 + (lane & 7), g = lane >> 3;  // sixteen warps take eight columns each
+    for (int r0 = base; r0 < rows && r0 < base + kMergeRows; r0 += 4) {
+      RowSums<4> s;
+      s.clear();
 #pragma unroll 4
-    for (int i = few ? g : 0; i < parts; i += few ? kMergeGroups : 1) {
-      const float* s = part(i);
-      const float4* ps = reinterpret_cast<const float4*>(s + t * kRows + base + r0);
-      const float4* po = reinterpret_cast<const float4*>(s + 512 + (t * WI_D + d) * kRows + base + r0);
-      const float4 m0 = ps[0], m1 = ps[1], o0 = po[0], o1 = po[1];
-      acc[0] += ex2(m0.x - ref[0]) * o0.x;
-      acc[1] += ex2(m0.y - ref[1]) * o0.y;
-      acc[2] += ex2(m0.z - ref[2]) * o0.z;
-      acc[3] += ex2(m0.w - ref[3]) * o0.w;
-      acc[4] += ex2(m1.x - ref[4]) * o1.x;
-      acc[5] += ex2(m1.y - ref[5]) * o1.y;
-      acc[6] += ex2(m1.z - ref[6]) * o1.z;
-      acc[7] += ex2(m1.w - ref[7]) * o1.w;
-    }
-    if (few) {
+      for (int i = g; i < parts; i += 4) {
+        const float* p = part(i);
+        s.add4(0, p + t * kRows + r0, p + 512 + (t * WI_D + d) * kRows + r0);
+      }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) acc_s[g][k][d] = acc[k];
-    } else {
+      for (int o = 8; o <= 16; o <<= 1)
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (r0 + k < rows) store(r0 + k, d, acc[k] * pl[0][r0 + k]);
-    }
-  }
-  if (few) {
-    __syncthreads();
-    for (int r = g; r < rows; r += kMergeGroups) {
-      float a = 0.f;
-      for (int i = 0; i < kMergeGroups; ++i) a += acc_s[i][r][d];
-      store(r, d, a * pl[0][r]);
+        for (int k = 0; k < 4; ++k) {
+          const float m = __shfl_xor_sync(0xffffffffu, s.m[k], o), l = __shfl_xor_sync(0xffffffffu, s.l[k], o),
+                      x = __shfl_xor_sync(0xffffffffu, s.o[k], o);
+          s.add(k, m, l, x);
+        }
+      // lane group g holds every row; it stores row g
+      float m = s.m[0], l = s.l[0], x = s.o[0];
+#pragma unroll
+      for (int k = 1; k < 4; ++k)
+        if (g == k) {
+          m = s.m[k];
+          l = s.l[k];
+          x = s.o[k];
+        }
+      store(r0 + g, d, m, l, x);
     }
   }
 }
