@@ -144,159 +144,214 @@ __global__ void __launch_bounds__(kTabThreads) k_paged_tables(WiPagedTables A, i
 
 // --------------------------------------------------- norms, rotation, cache write
 //
-// Sixteen lanes hold one head row of 128 elements, eight each, as two groups
-// of four: where the rotation pairs element i with i + R / 2, a lane's groups
-// are four pairs (4l .. 4l+3 and R/2 further), so that norm and rotation need
-// no exchange but the sum of squares.  The lane's four angles are computed
-// once for all the rows that it takes from one token.
+// A warp takes heads of one token in batches of eight: sixteen lanes hold one
+// head row of 128 elements, eight each, as two groups of four.  Where the
+// rotation pairs element i with i + R / 2, a lane's groups are four pairs
+// (4l .. 4l+3 and R/2 further), so norm and rotation need no exchange but the
+// sum of squares.  With the norm's weight w folded into the angle's cosine and
+// sine once per token, a row costs
+//   a' = (a / rms) (w_a cos) - (b / rms) (w_b sin), b' likewise,
+// in packed fp32; the four sums of squares that a lane group has in flight are
+// reduced together (each of sixteen lanes ends with a quarter of them).  The
+// first rows are loaded before the token's position and slot are known (the
+// rows of a padding token exist too), every batch while the one before it is
+// worked on.  8192 tokens of 32 + 8 + 8 heads: 38.1 us (5.3 TB/s); with the
+// operations one by one, a row to sixteen lanes, instruction issue bounds it
+// (194 instructions for two rows, 48 us).
 constexpr int kWrThreads = 256;
-constexpr int kWrRows = 4;  // rows in flight per 16 lanes
+constexpr int kWrPerSm = 16;    // warps per SM that a launch aims at (1531 tokens: 11.5, 9.5, 10.7 us at 8, 16, 24)
 
-struct Lane8 {
-  uint2 a, b;
-};
-
-// Offsets of a lane's two groups inside a head row.
-__device__ __forceinline__ void lane_groups(int l, const WiRope& r, int& o0, int& o1) {
-  const int half = r.rotary >> 1;
-  if (!r.interleaved && 4 * l < half) {
-    o0 = 4 * l;
-    o1 = 4 * l + half;
-  } else {
-    o0 = 8 * l;
-    o1 = 8 * l + 4;
-  }
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  return x;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(x));
+  return v;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t unpack2(uint32_t w) { return pair2(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ uint32_t repack2(uint64_t x) {
+  const float2 v = unpair(x);
+  const __nv_bfloat162 w = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&w);
+}
+__device__ __forceinline__ uint64_t swap2(uint64_t x) {
+  const float2 v = unpair(x);
+  return pair2(v.y, v.x);
 }
 
-__device__ __forceinline__ uint2 pack4(const float (&x)[4]) {
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
-  uint2 w;
-  w.x = *reinterpret_cast<const uint32_t*>(&lo);
-  w.y = *reinterpret_cast<const uint32_t*>(&hi);
-  return w;
-}
-
-__global__ void __launch_bounds__(kWrThreads) k_paged_write(const __grid_constant__ WiPagedWrite A,
-                                                           const __grid_constant__ WiRope R, int Hq, int Hkv, int page,
-                                                           int n_slots, float eps, int parts, int* err) {
-  const int l = threadIdx.x & 15;
-  const long long unit = (long long)blockIdx.x * (kWrThreads / 16) + (threadIdx.x >> 4);
-  const int t = (int)(unit / parts), part = (int)(unit % parts);
-  // whole warps stay together for the shuffles: lanes without a token run along with nothing to do
-  const bool on = t < A.n_tokens;
-  const int pos = on ? A.positions[t] : -1;
-  int slot = -1;
-  if (pos >= 0) {
-    slot = A.slots ? A.slots[t] : t;
-    if (A.slots && slot >= n_slots) {
-      if (l == 0) atomicOr(err, WI_DEVERR_BAD_PAGE);
-      slot = -1;
+// INTER: pairs (2i, 2i + 1).  FULL: the whole head is rotated (no lane holds elements that are only scaled).
+template <bool INTER, bool FULL>
+__global__ void __launch_bounds__(kWrThreads, 3) k_paged_write(const __grid_constant__ WiPagedWrite A,
+                                                              const __grid_constant__ WiRope R, int Hq, int Hkv, int page,
+                                                              int n_slots, float eps, int parts, int* err) {
+  const int lane = threadIdx.x & 31, l = lane & 15, row1 = lane >> 4;
+  const long long unit = (long long)blockIdx.x * (kWrThreads / 32) + (threadIdx.x >> 5);
+  const long long tl = unit / parts;
+  if (tl >= A.n_tokens) return;  // the whole warp
+  const int t = (int)tl, part = (int)(unit - tl * parts);
+  const int half = R.rotary >> 1, bq = (Hq + 7) >> 3, bk = (Hkv + 7) >> 3, batches = bq + 2 * bk;
+  const bool turned = FULL || (INTER ? 8 * l < R.rotary : 4 * l < half);
+  const int o0 = !INTER && turned ? 4 * l : 8 * l, o1 = !INTER && turned ? 4 * l + half : 8 * l + 4;
+  uint2 xa[4], xb[4];
+  auto fetch = [&](int i) {
+    const int kind = i < bq ? 0 : i < bq + bk ? 1 : 2;
+    const int h0 = 8 * (kind == 0 ? i : kind == 1 ? i - bq : i - bq - bk) + row1;
+    const bf16* from = kind == 0   ? static_cast<const bf16*>(A.q) + (long long)t * A.q_stride
+                       : kind == 1 ? static_cast<const bf16*>(A.k) + (long long)t * A.k_stride
+                                   : static_cast<const bf16*>(A.v) + (long long)t * A.v_stride;
+    const int H = kind == 0 ? Hq : Hkv;
+    from += h0 * WI_D;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      xa[k] = xb[k] = make_uint2(0u, 0u);
+      if (h0 + 2 * k < H) {
+        xa[k] = *reinterpret_cast<const uint2*>(from + 2 * k * WI_D + o0);
+        xb[k] = *reinterpret_cast<const uint2*>(from + 2 * k * WI_D + o1);
+      }
     }
+  };
+  if (part < batches) fetch(part);
+  const int pos = A.positions[t];
+  int slot = A.slots ? A.slots[t] : t;
+  if (pos < 0) return;  // padding
+  if (A.slots && slot >= n_slots) {
+    if (lane == 0) atomicOr(err, WI_DEVERR_BAD_PAGE);
+    slot = -1;
   }
-  int o0, o1;
-  lane_groups(l, R, o0, o1);
-  const bool turned = R.interleaved ? 8 * l < R.rotary : 4 * l < (R.rotary >> 1);
+  const int end = slot < 0 ? bq : batches;  // without a slot the query alone is wanted
   float cs[4], sn[4];
+  {
+    // the two lane groups need the same four angles: each computes two of them
+    float c[2] = {1.f, 1.f}, s[2] = {0.f, 0.f};
+    if (turned) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    cs[i] = 1.f;
-    sn[i] = 0.f;
-    if (turned && pos >= 0) {
-      // the product's low 64 bits are the fraction of a turn; signed, it is the angle in (-1/2, 1/2] turns
-      const long long a = (long long)(R.turn[4 * l + i] * (unsigned long long)pos);
-      sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &sn[i], &cs[i]);  // 2^-31: half turns
-      cs[i] *= R.scale;
-      sn[i] *= R.scale;
+      for (int i = 0; i < 2; ++i) {
+        // the product's low 64 bits are the fraction of a turn; signed, it is the angle in [-1/2, 1/2) turns
+        const long long a = (long long)(R.turn[4 * l + 2 * row1 + i] * (unsigned long long)pos);
+        sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &s[i], &c[i]);  // 2^-31: half turns
+        c[i] *= R.scale;
+        s[i] *= R.scale;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float co = __shfl_xor_sync(0xffffffffu, c[i], 16), so = __shfl_xor_sync(0xffffffffu, s[i], 16);
+      cs[i] = row1 ? co : c[i];
+      sn[i] = row1 ? so : s[i];
+      cs[2 + i] = row1 ? c[i] : co;
+      sn[2 + i] = row1 ? s[i] : so;
     }
   }
-  const long long k_row = A.slots ? (long long)(slot / page) * Hkv * page + slot % page : (long long)slot * Hkv;
-  const int k_step = A.slots ? page : 1;  // rows between a token's kv heads
-  const int rows = Hq + 2 * Hkv;
-  const int r0 = (int)((long long)rows * part / parts), r1 = (int)((long long)rows * (part + 1) / parts);
-  const int most = (rows + parts - 1) / parts;
-  for (int base = 0; base < most; base += kWrRows) {
-    Lane8 x[kWrRows];
-    bf16* to[kWrRows];
+  // elements between a token's kv heads in k_out / v_out, and its first
+  const long long k_step = (A.slots ? page : 1) * (long long)WI_D;
+  const long long k_at = (A.slots ? (long long)(slot / page) * Hkv * page + slot % page : (long long)slot * Hkv) * WI_D;
+  uint64_t ca[2], cb[2], sa[2], sb[2];  // factors of a in a', of b in b', of a in b', of b in a'
+  int have = -1;
+  for (int i = part; i < end; i += parts) {
+    uint2 ya[4], yb[4];
 #pragma unroll
-    for (int i = 0; i < kWrRows; ++i) {
-      const int r = r0 + base + i;
-      const bf16* from = nullptr;
-      to[i] = nullptr;
-      if (r < r1 && pos >= 0) {
-        if (r < Hq) {
-          from = static_cast<const bf16*>(A.q) + (long long)t * A.q_stride + (long long)r * WI_D;
-          to[i] = static_cast<bf16*>(A.q_out) + ((long long)t * Hq + r) * WI_D;
-        } else if (slot >= 0) {
-          const int h = r < Hq + Hkv ? r - Hq : r - Hq - Hkv;
-          const long long row = (k_row + (long long)h * k_step) * WI_D;
-          if (r < Hq + Hkv) {
-            from = static_cast<const bf16*>(A.k) + (long long)t * A.k_stride + (long long)h * WI_D;
-            to[i] = static_cast<bf16*>(A.k_out) + row;
-          } else {
-            from = static_cast<const bf16*>(A.v) + (long long)t * A.v_stride + (long long)h * WI_D;
-            to[i] = static_cast<bf16*>(A.v_out) + row;
-          }
-        }
-      }
-      x[i].a = x[i].b = make_uint2(0u, 0u);
-      if (to[i]) {
-        x[i].a = *reinterpret_cast<const uint2*>(from + o0);
-        x[i].b = *reinterpret_cast<const uint2*>(from + o1);
-      }
+    for (int k = 0; k < 4; ++k) {
+      ya[k] = xa[k];
+      yb[k] = xb[k];
     }
-#pragma unroll
-    for (int i = 0; i < kWrRows; ++i) {
-      const int r = r0 + base + i;
-      if (r < Hq + Hkv) {
-        float a[4], b[4];
-        unpack_bf16x4(x[i].a, a);
-        unpack_bf16x4(x[i].b, b);
-        const bf16* w = static_cast<const bf16*>(r < Hq ? A.q_weight : A.k_weight);
+    if (i + parts < end) fetch(i + parts);
+    const int kind = i < bq ? 0 : i < bq + bk ? 1 : 2;
+    const int h0 = 8 * (kind == 0 ? i : kind == 1 ? i - bq : i - bq - bk) + row1;
+    const int H = kind == 0 ? Hq : Hkv;
+    bf16* to = kind == 0 ? static_cast<bf16*>(A.q_out) + ((long long)t * Hq + h0) * WI_D
+                         : static_cast<bf16*>(kind == 1 ? A.k_out : A.v_out) + k_at + h0 * k_step;
+    const long long step = 2 * (kind == 0 ? (long long)WI_D : k_step);
+    const int pairs = (min(8, H - (h0 - row1)) + 1) >> 1;  // rows of the batch, two by two
+    if (kind < 2) {
+      const bf16* w = static_cast<const bf16*>(kind == 0 ? A.q_weight : A.k_weight);
+      if (kind != have) {
+        have = kind;
+        float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
         if (w) {
-          float ss = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) ss += a[j] * a[j] + b[j] * b[j];
-          // both halves of a warp may hold rows of different kinds: each sums over its own sixteen lanes
-          const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-          const float inv = rsqrtf(ss * (1.f / WI_D) + eps);
-          float wa[4], wb[4];
           load_bf16x4(w + o0, wa);
           load_bf16x4(w + o1, wb);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            a[j] = a[j] * inv * wa[j];
-            b[j] = b[j] * inv * wb[j];
-          }
         }
-        if (turned) {
-          if (R.interleaved) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float a0 = a[2 * j], a1 = a[2 * j + 1], b0 = b[2 * j], b1 = b[2 * j + 1];
-              a[2 * j] = a0 * cs[j] - a1 * sn[j];
-              a[2 * j + 1] = a1 * cs[j] + a0 * sn[j];
-              b[2 * j] = b0 * cs[2 + j] - b1 * sn[2 + j];
-              b[2 * j + 1] = b1 * cs[2 + j] + b0 * sn[2 + j];
-            }
+        for (int k = 0; k < 2; ++k) {
+          if (INTER) {  // a = (x0, x1), (x2, x3): both groups hold whole pairs, turned with their own neighbour
+            ca[k] = pair2(wa[2 * k] * cs[k], wa[2 * k + 1] * cs[k]);
+            sa[k] = pair2(-wa[2 * k + 1] * sn[k], wa[2 * k] * sn[k]);
+            cb[k] = pair2(wb[2 * k] * cs[2 + k], wb[2 * k + 1] * cs[2 + k]);
+            sb[k] = pair2(-wb[2 * k + 1] * sn[2 + k], wb[2 * k] * sn[2 + k]);
           } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float p = a[j], s = b[j];
-              a[j] = p * cs[j] - s * sn[j];
-              b[j] = s * cs[j] + p * sn[j];
-            }
+            ca[k] = pair2(wa[2 * k] * cs[2 * k], wa[2 * k + 1] * cs[2 * k + 1]);
+            cb[k] = pair2(wb[2 * k] * cs[2 * k], wb[2 * k + 1] * cs[2 * k + 1]);
+            sa[k] = pair2(wa[2 * k] * sn[2 * k], wa[2 * k + 1] * sn[2 * k + 1]);
+            sb[k] = pair2(-wb[2 * k] * sn[2 * k], -wb[2 * k + 1] * sn[2 * k + 1]);
           }
         }
-        x[i].a = pack4(a);
-        x[i].b = pack4(b);
       }
-      if (to[i]) {
-        *reinterpret_cast<uint2*>(to[i] + o0) = x[i].a;
-        *reinterpret_cast<uint2*>(to[i] + o1) = x[i].b;
+      float inv[4] = {1.f, 1.f, 1.f, 1.f};
+      if (w) {
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[k] = 0.f;
+          if (k >= pairs) continue;
+          const uint64_t a0 = unpack2(ya[k].x), a1 = unpack2(ya[k].y), b0 = unpack2(yb[k].x), b1 = unpack2(yb[k].y);
+          const float2 ss = unpair(fma2(a0, a0, fma2(a1, a1, fma2(b0, b0, mul2(b1, b1)))));
+          v[k] = ss.x + ss.y;
+        }
+        const bool up8 = l & 8, up4 = l & 4;
+        float s0 = up8 ? v[0] : v[2], s1 = up8 ? v[1] : v[3];
+        float k0 = up8 ? v[2] : v[0], k1 = up8 ? v[3] : v[1];
+        k0 += __shfl_xor_sync(0xffffffffu, s0, 8);
+        k1 += __shfl_xor_sync(0xffffffffu, s1, 8);
+        float r = (up4 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, up4 ? k0 : k1, 4);
+        r += __shfl_xor_sync(0xffffffffu, r, 2);
+        r += __shfl_xor_sync(0xffffffffu, r, 1);
+        r = rsqrtf(r * (1.f / WI_D) + eps);  // of the row that lanes 4k .. 4k + 3 summed
+#pragma unroll
+        for (int k = 0; k < 4; ++k) inv[k] = __shfl_sync(0xffffffffu, r, (lane & 16) + 4 * k);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k >= pairs) continue;
+        uint64_t a[2] = {unpack2(ya[k].x), unpack2(ya[k].y)}, b[2] = {unpack2(yb[k].x), unpack2(yb[k].y)};
+        if (w) {
+          const uint64_t f = pair2(inv[k], inv[k]);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            a[c] = mul2(a[c], f);
+            b[c] = mul2(b[c], f);
+          }
+        }
+        uint32_t ra[2], rb[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint64_t pa = INTER ? swap2(a[c]) : b[c], pb = INTER ? swap2(b[c]) : a[c];
+          if (!FULL && !turned) pa = pb = 0;  // nothing of the partner, an infinite one included
+          ra[c] = repack2(fma2(a[c], ca[c], mul2(pa, INTER ? sa[c] : sb[c])));
+          rb[c] = repack2(fma2(b[c], cb[c], mul2(pb, INTER ? sb[c] : sa[c])));
+        }
+        ya[k] = make_uint2(ra[0], ra[1]);
+        yb[k] = make_uint2(rb[0], rb[1]);
       }
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (h0 + 2 * k < H) {
+        *reinterpret_cast<uint2*>(to + k * step + o0) = ya[k];
+        *reinterpret_cast<uint2*>(to + k * step + o1) = yb[k];
+      }
   }
 }
 
@@ -382,17 +437,17 @@ cudaError_t wi_launch_paged_tables(const WiPagedGeom& g, const WiPagedTables& a,
 }
 
 cudaError_t wi_launch_paged_write(const WiPagedGeom& g, const WiPagedWrite& a, int sms, int* err, cudaStream_t st) {
-  // rows per sixteen lanes: as many as leave eight warps per SM, so that few tokens spread over the
-  // machine and many share each token's angles among all of its rows
-  const int rows = g.Hq + 2 * g.Hkv;
-  const long long groups = 16LL * sms;
-  long long parts = (groups + a.n_tokens - 1) / a.n_tokens;
-  const int widest = (rows + kWrRows - 1) / kWrRows;
-  if (parts > widest) parts = widest;
-  const long long units = parts * a.n_tokens;
-  const long long grid = (units + kWrThreads / 16 - 1) / (kWrThreads / 16);
-  k_paged_write<<<(unsigned)grid, kWrThreads, 0, st>>>(a, g.rope, g.Hq, g.Hkv, g.page, g.n_pages * g.page, g.eps,
-                                                      (int)parts, err);
+  // warps that share a token's batches: enough to fill the machine, no more than there are batches (each computes
+  // the token's angles again)
+  const int batches = (g.Hq + 7) / 8 + 2 * ((g.Hkv + 7) / 8);
+  long long parts = ((long long)kWrPerSm * sms + a.n_tokens - 1) / a.n_tokens;
+  if (parts > batches) parts = batches;
+  const long long grid = (parts * a.n_tokens + kWrThreads / 32 - 1) / (kWrThreads / 32);
+  const bool full = g.rope.rotary == WI_D;
+  auto* kernel = g.rope.interleaved ? (full ? k_paged_write<true, true> : k_paged_write<true, false>)
+                                    : (full ? k_paged_write<false, true> : k_paged_write<false, false>);
+  kernel<<<(unsigned)grid, kWrThreads, 0, st>>>(a, g.rope, g.Hq, g.Hkv, g.page, g.n_pages * g.page, g.eps, (int)parts,
+                                                err);
   return cudaGetLastError();
 }
 
