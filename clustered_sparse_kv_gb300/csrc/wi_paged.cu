@@ -3,6 +3,7 @@
 
 #include "wi_common.cuh"
 #include "wi_paged.h"
+#include "wi_pipe.cuh"
 
 namespace {
 
@@ -64,6 +65,8 @@ __global__ void __launch_bounds__(kTabThreads) k_paged_tables(WiPagedTables A, i
   extern __shared__ TabReq req[];  // [batch + 1]
   __shared__ long long tmp[2 * (kTabThreads / 32)];
   const int tid = threadIdx.x;
+  pdl_trigger();
+  pdl_wait();
   const int per = (A.batch + kTabThreads - 1) / kTabThreads;  // consecutive requests per thread
   const int b0 = min(tid * per, A.batch), b1 = min(b0 + per, A.batch);
   const long long most = (long long)max_pages * page;
@@ -198,6 +201,8 @@ __global__ void __launch_bounds__(kWrThreads, 3) k_paged_write(const __grid_cons
                                                               const __grid_constant__ WiRope R, int Hq, int Hkv, int page,
                                                               int n_slots, float eps, int parts, int* err) {
   const int lane = threadIdx.x & 31, l = lane & 15, row1 = lane >> 4;
+  pdl_trigger();
+  pdl_wait();
   const long long unit = (long long)blockIdx.x * (kWrThreads / 32) + (threadIdx.x >> 5);
   const long long tl = unit / parts;
   if (tl >= A.n_tokens) return;  // the whole warp
@@ -367,6 +372,8 @@ constexpr int kGaRows = 4;
 __global__ void __launch_bounds__(kGaThreads) k_paged_gather(WiPagedGather A, long long rows, int Hkv, int page,
                                                             int n_pages, int max_pages, int* err) {
   constexpr int kStep = kGaThreads / 16;
+  pdl_trigger();
+  pdl_wait();
   const int l = threadIdx.x & 15;
   const int most = max_pages * page, n = (int)A.n;
   const long long r0 = (long long)blockIdx.x * (kStep * kGaRows);
@@ -432,8 +439,8 @@ cudaError_t wi_launch_paged_tables(const WiPagedGeom& g, const WiPagedTables& a,
   }
   const long long want = ((long long)a.n_tokens + kTabThreads - 1) / kTabThreads;
   const int grid = want < 1 ? 1 : want > sms ? sms : (int)want;
-  k_paged_tables<<<grid, kTabThreads, smem, st>>>(a, g.page, g.n_pages, g.max_pages, err);
-  return cudaGetLastError();
+  return wi_launch_chained(k_paged_tables, dim3((unsigned)grid), kTabThreads, smem, st, a, g.page, g.n_pages,
+                           g.max_pages, err);
 }
 
 cudaError_t wi_launch_paged_write(const WiPagedGeom& g, const WiPagedWrite& a, int sms, int* err, cudaStream_t st) {
@@ -446,15 +453,14 @@ cudaError_t wi_launch_paged_write(const WiPagedGeom& g, const WiPagedWrite& a, i
   const bool full = g.rope.rotary == WI_D;
   auto* kernel = g.rope.interleaved ? (full ? k_paged_write<true, true> : k_paged_write<true, false>)
                                     : (full ? k_paged_write<false, true> : k_paged_write<false, false>);
-  kernel<<<(unsigned)grid, kWrThreads, 0, st>>>(a, g.rope, g.Hq, g.Hkv, g.page, g.n_pages * g.page, g.eps, (int)parts,
-                                                err);
-  return cudaGetLastError();
+  return wi_launch_chained(kernel, dim3((unsigned)grid), kWrThreads, 0, st, a, g.rope, g.Hq, g.Hkv, g.page,
+                           g.n_pages * g.page, g.eps, (int)parts, err);
 }
 
 cudaError_t wi_launch_paged_gather(const WiPagedGeom& g, const WiPagedGather& a, int* err, cudaStream_t st) {
   const int per = kGaThreads / 16 * kGaRows;
   const long long rows = (long long)a.batch * a.layers * g.Hkv * a.n, grid = (rows + per - 1) / per;
   if (grid > 2147483647LL) return cudaErrorInvalidConfiguration;
-  k_paged_gather<<<(unsigned)grid, kGaThreads, 0, st>>>(a, rows, g.Hkv, g.page, g.n_pages, g.max_pages, err);
-  return cudaGetLastError();
+  return wi_launch_chained(k_paged_gather, dim3((unsigned)grid), kGaThreads, 0, st, a, rows, g.Hkv, g.page, g.n_pages,
+                           g.max_pages, err);
 }

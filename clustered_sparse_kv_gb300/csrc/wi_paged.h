@@ -5,6 +5,24 @@
 
 #include "wave_index.h"
 
+// Launch that may be scheduled while the kernel before it in the stream drains (the kernel waits with pdl_wait
+// before it reads or writes anything that another one touches).
+template <typename... K, typename... A>
+inline cudaError_t wi_launch_chained(void (*kernel)(K...), dim3 grid, int threads, size_t smem, cudaStream_t st,
+                                     const A&... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = dim3((unsigned)threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  lc.attrs = at;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, args...);
+}
+
 constexpr int kPagedMaxBatch = 4096;
 constexpr int kPagedMaxTokens = 1 << 24;  // of a step
 
@@ -82,7 +100,8 @@ struct WiPagedAttn {
   int batch, n_tokens;
 };
 constexpr int kPagedMaxSms = 1024;
-// Scratch of the attention, part of the handle: two partial results per CTA (of an item that the CTA before began,
+constexpr size_t kPagedTicketBytes = kPagedMaxSms * 4;  // at the start of the scratch, zero between calls
+// Scratch of the attention, part of the handle: tickets, two partial results per CTA (of an item that the CTA before began,
 // and of one that the CTA after goes on with) and what the merge needs to know of the latter.
 size_t wi_paged_attention_scratch(int sms);
 cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a, int sms, void* scratch, int* err,

@@ -126,7 +126,7 @@ int create_impl(const wi_paged_config* cfg, wi_paged** out) {
   pc->sms = sms;
   if (cudaMalloc(reinterpret_cast<void**>(&pc->err), 4) != cudaSuccess ||
       cudaMalloc(&pc->scratch, wi_paged_attention_scratch(sms)) != cudaSuccess ||
-      cudaMemset(pc->err, 0, 4) != cudaSuccess) {
+      cudaMemset(pc->err, 0, 4) != cudaSuccess || cudaMemset(pc->scratch, 0, kPagedTicketBytes) != cudaSuccess) {
     cudaGetLastError();
     destroy(pc);
     return fail(WI_ENOMEM, "device allocation failed");
@@ -156,6 +156,7 @@ int wi_paged_check(wi_paged* pc) {
   WI_CUDA(cudaMemcpy(&herr, pc->err, 4, cudaMemcpyDeviceToHost));
   if (!herr) return WI_OK;
   WI_CUDA(cudaMemset(pc->err, 0, 4));
+  if (herr & WI_DEVERR_MBAR_TIMEOUT) WI_CUDA(cudaMemset(pc->scratch, 0, kPagedTicketBytes));  // tickets left behind
   return fail(WI_EDEVICE, "paged cache (flags 0x%x):%s%s%s%s", herr,
               herr & WI_DEVERR_BAD_PAGE ? " a page or slot outside the pool;" : "",
               herr & WI_DEVERR_BAD_LENGTH ? " a length or offset out of range;" : "",

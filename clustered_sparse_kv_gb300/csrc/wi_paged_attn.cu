@@ -15,7 +15,10 @@
 // made on the host.  Lengths live on the device: each CTA sums the units of
 // all requests itself (closed form per request) and finds its run's start.
 // An item cut between CTAs leaves partial results (maximum, sum, O) in the
-// scratch, which k_paged_merge adds up in CTA order.
+// scratch, added up in CTA order: those of an item of one tile by the last of
+// its CTAs, those of two tiles by k_paged_merge, which spreads them over the
+// machine and is launched only where the call may hold such an item (a single
+// token over 131K, 8 kv heads: 8-10 us less than with the second kernel).
 //
 // A CTA (640 threads) processes its items' blocks in roles:
 //   warps 0-15      softmax: eight warps for each of two chains, two threads
@@ -77,7 +80,7 @@ struct Smem {
   uint64_t s_full[2], p_ready[2], o_full[2];
   uint64_t drained;
   uint32_t tmem_base;
-  int spare;                // keeps scan aligned
+  int last;                 // this CTA merges the item that it just added to
   int poison[8];            // segment number + 1 of the last segment (modulo 8) with an infinite or NaN value
   long long scan[kThreads / 32];
   int start[4];             // the run's first request, kv head, tile pair, block
@@ -119,6 +122,7 @@ struct Params {
   int page, n_pages, max_pages, box;
   float* parts;
   Split* splits;
+  unsigned* tickets;        // of items of one tile, at the CTA that begins them; zero between calls
   int* err;
 };
 
@@ -308,18 +312,190 @@ __device__ __forceinline__ int cta_of(long long u, long long total, int ctas) {
   return (int)quot((u + 1) * ctas - 1, total);
 }
 
+// ---- merge of an item that was cut between CTAs
+//
+// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over the CTAs c that worked on it: one pass over the parts with
+// the running maximum, in a fixed order, by sixteen warps, 32 rows of a tile at a time.  What counts is latency: a few
+// parts of many rows are read with a lane to a row, as they were written, every load issued before the first is used
+// (TURN: the results go out through shared memory, whole rows at a time); many parts (single tokens over a long
+// context, cut into as many as there are SMs) with four lanes sharing them out, four rows at a time.
+constexpr int kMergeRows = 32;
+constexpr int kMergeWide = 4;  // parts up to which a lane reads them all
+
+struct RowSums {
+  float m[4], l[4], o[4];
+  __device__ __forceinline__ void add(int k, float mi, float li, float oi) {
+    const float M = fmaxf(m[k], mi), ref = M == -INFINITY ? 0.f : M;
+    const float a = ex2(m[k] - ref), b = ex2(mi - ref);
+    m[k] = M;
+    l[k] = l[k] * a + li * b;
+    o[k] = o[k] * a + oi * b;
+  }
+};
+
+// Rows of an item's tile t.
+__device__ __forceinline__ int tile_rows(const Params& P, const Split& sp, int t) {
+  return min(P.tq, sp.cnt - t * P.tq) * P.G;
+}
+
+template <bool TURN>
+__device__ __forceinline__ void merge_rows(const Params& P, const Split& sp, int c0, int t, int base,
+                                           bf16 (*turn)[WI_D + 8]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, parts = sp.last - c0 + 1, rows = tile_rows(P, sp, t);
+  auto part = [&](int i) -> const float* { return P.parts + (long long)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kPartFloats; };
+  auto place = [&](int r) -> long long {  // (token, query head) of a row
+    const int tok = r / P.G;
+    return (long long)(sp.row0 + t * P.tq + tok) * P.Hq + sp.kh * P.G + r - tok * P.G;
+  };
+  if (parts <= kMergeWide) {
+    const int r = base + lane, d0 = warp * 8;  // sixteen warps take eight columns each
+    float m[kMergeWide], l[kMergeWide], o[kMergeWide][8];
+#pragma unroll
+    for (int i = 0; i < kMergeWide; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      if (i < parts) {
+        const float* p = part(i) + t * kRows + r;
+        m[i] = __ldcg(p);
+        l[i] = __ldcg(p + 256);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[i][k] = __ldcg(part(i) + 512 + (t * WI_D + d0 + k) * kRows + r);
+      }
+    }
+    float M = m[0], L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 1; i < kMergeWide; ++i) M = fmaxf(M, m[i]);
+    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int i = 0; i < kMergeWide; ++i)
+      if (i < parts) {
+        const float f = ex2(m[i] - ref);
+        L += l[i] * f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] += o[i][k] * f;
+      }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    uint4 x;
+    x.x = pack2(acc[0] * inv, acc[1] * inv);
+    x.y = pack2(acc[2] * inv, acc[3] * inv);
+    x.z = pack2(acc[4] * inv, acc[5] * inv);
+    x.w = pack2(acc[6] * inv, acc[7] * inv);
+    bf16* out = static_cast<bf16*>(P.a.out);
+    if (TURN) {
+      *reinterpret_cast<uint4*>(&turn[lane][d0]) = x;
+      __syncthreads();
+      const int q = threadIdx.x >> 4, c = (threadIdx.x & 15) * 8;  // sixteen threads store a row
+      if (base + q < rows)
+        *reinterpret_cast<uint4*>(out + place(base + q) * WI_D + c) = *reinterpret_cast<const uint4*>(&turn[q][c]);
+    } else if (r < rows) {
+      *reinterpret_cast<uint4*>(out + place(r) * WI_D + d0) = x;
+    }
+    if (P.a.lse && warp == 0 && r < rows) P.a.lse[place(r)] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
+  } else {
+    const int d = warp * 8 + (lane & 7), g = lane >> 3;
+    for (int r0 = base; r0 < rows && r0 < base + kMergeRows; r0 += 4) {
+      RowSums s;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        s.m[k] = -INFINITY;
+        s.l[k] = s.o[k] = 0.f;
+      }
+      constexpr int kAtOnce = 5;  // parts that a lane has in flight: all of them up to 20 parts
+      for (int i0 = g; i0 < parts; i0 += 4 * kAtOnce) {
+        float4 a[kAtOnce], b[kAtOnce], c[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          a[k] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          b[k] = c[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i0 + 4 * k < parts) {
+            const float* p = part(i0 + 4 * k) + t * kRows + r0;
+            a[k] = __ldcg(reinterpret_cast<const float4*>(p));
+            b[k] = __ldcg(reinterpret_cast<const float4*>(p + 256));
+            c[k] = __ldcg(reinterpret_cast<const float4*>(p - t * kRows + 512 + (t * WI_D + d) * kRows));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          s.add(0, a[k].x, b[k].x, c[k].x);
+          s.add(1, a[k].y, b[k].y, c[k].y);
+          s.add(2, a[k].z, b[k].z, c[k].z);
+          s.add(3, a[k].w, b[k].w, c[k].w);
+        }
+      }
+#pragma unroll
+      for (int o = 8; o <= 16; o <<= 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float m = __shfl_xor_sync(0xffffffffu, s.m[k], o), l = __shfl_xor_sync(0xffffffffu, s.l[k], o),
+                      x = __shfl_xor_sync(0xffffffffu, s.o[k], o);
+          s.add(k, m, l, x);
+        }
+      // every lane group holds all four rows; group g stores row g
+      float m = s.m[0], l = s.l[0], x = s.o[0];
+#pragma unroll
+      for (int k = 1; k < 4; ++k)
+        if (g == k) {
+          m = s.m[k];
+          l = s.l[k];
+          x = s.o[k];
+        }
+      const int r = r0 + g;
+      if (r < rows) {
+        static_cast<bf16*>(P.a.out)[place(r) * WI_D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
+        if (P.a.lse && d == 0) P.a.lse[place(r)] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+      }
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_constant__ CUtensorMap map_q,
                                                                 const __grid_constant__ CUtensorMap map_k,
                                                                 const __grid_constant__ CUtensorMap map_v,
                                                                 const __grid_constant__ Params P) {
   extern __shared__ __align__(1024) unsigned char raw[];
-  pdl_trigger();  // k_paged_merge may take the SMs as they fall free; it waits for this grid before it reads
+  pdl_trigger();  // the next kernel may take the SMs as they fall free; it waits for this grid before it reads
   Smem& sm = *reinterpret_cast<Smem*>(raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (smem_addr(raw) & 1023u) {  // the swizzled tiles need 1024-byte alignment; never run misaligned
     if (tid == 0) atomicOr(P.err, WI_DEVERR_BAD_ROW);
     return;
   }
+
+  // ---- what needs nothing of the kernels before this one
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+      mbar_init(&sm.to_fix[s], 1);
+      mbar_init(&sm.fixed[s], kFixWarps);
+    }
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sm.s_full[t], 1);
+      mbar_init(&sm.p_ready[t], kSoftWarps / 2);
+      mbar_init(&sm.o_full[t], 1);
+    }
+    mbar_init(&sm.drained, 1);
+    for (int i = 0; i < 8; ++i) sm.poison[i] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kSoftWarps + 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == kSoftWarps && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
+  }
+  if (P.tq * P.G < kRows) {  // rows of the query tiles that no box fills: zero, not whatever was there
+    for (int i = tid; i < 2 * kTileBytes / 16; i += kThreads)
+      reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
+  pdl_wait();
 
   // ---- this CTA's run of units
   const int per = (P.a.batch + kThreads - 1) / kThreads;
@@ -341,25 +517,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     if (lane >= o) before += t;
   }
   if (lane == 31) sm.scan[warp] = before;
-  if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], 1);
-      mbar_init(&sm.to_fix[s], 1);
-      mbar_init(&sm.fixed[s], kFixWarps);
-    }
-    mbar_init(&sm.q_full, 1);
-    mbar_init(&sm.q_empty, 1);
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(&sm.s_full[t], 1);
-      mbar_init(&sm.p_ready[t], kSoftWarps / 2);
-      mbar_init(&sm.o_full[t], 1);
-    }
-    mbar_init(&sm.drained, 1);
-    for (int i = 0; i < 8; ++i) sm.poison[i] = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;  // S0, S1 at columns 0, 128; O0, O1 at 256, 384
   long long total = 0;
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w == warp) before += total;
@@ -369,6 +530,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
   const int ctas = (int)min((long long)gridDim.x, total);
   if ((int)blockIdx.x >= ctas) {  // fewer units than CTAs (the whole CTA leaves)
     if (tid == 0) P.splits[blockIdx.x].last = -1;
+    if (warp == kSoftWarps + 1)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     return;
   }
   const long long u0 = quot(total * blockIdx.x, ctas), u1 = quot(total * (blockIdx.x + 1), ctas);
@@ -398,20 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       break;
     }
   }
-  if (P.tq * P.G < kRows) {  // rows of the query tiles that no box fills: zero, not whatever was there
-    for (int i = tid; i < 2 * kTileBytes / 16; i += kThreads)
-      reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0u, 0u, 0u, 0u);
-    fence_proxy_async_smem();
-  }
-  if (warp == kSoftWarps + 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem_base))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;  // S0, S1 at columns 0, 128; O0, O1 at 256, 384
 
   Walk w;
   w.begin(P, sm, u1 - u0);
@@ -594,21 +744,38 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         }
       }
       tc_fence_before();  // O is read: the next segment may write it
-      if (part && w.b0 == 0 && tid == 0) {
-        split = true;
-        P.splits[blockIdx.x] = {w.r.s0 + w.tile * w.tp, w.kh, w.cnt, cta_of(u1 - w.left - w.at + kLead + w.nblk - 1, total, ctas)};
+      if (!w.single) {
+        if (part && w.b0 == 0 && tid == 0) {
+          split = true;
+          P.splits[blockIdx.x] = {w.r.s0 + w.tile * w.tp, w.kh, w.cnt,
+                                  cta_of(u1 - w.left - w.at + kLead + w.nblk - 1, total, ctas)};
+        }
+      } else if (part) {
+        const long long item = u1 - w.left - w.at + kLead;  // the unit of the item's first block
+        const int c0 = cta_of(item, total, ctas), c1 = cta_of(item + w.nblk - 1, total, ctas);
+        soft_barrier();  // then thread 0's release covers what all of them stored
+        if (tid == 0) {
+          sm.last = 0;
+          if (ok && ticket_acq_rel(P.tickets + c0) == (unsigned)(c1 - c0)) {
+            P.tickets[c0] = 0;
+            sm.last = 1;
+          }
+        }
+        soft_barrier();
+        if (sm.last) {
+          const Split sp = {w.r.s0 + w.tile * w.tp, w.kh, w.cnt, c1};
+          for (int base = 0; base < tile_rows(P, sp, 0); base += kMergeRows)
+            merge_rows<false>(P, sp, c0, 0, base, nullptr);
+        }
+        soft_barrier();
+      } else {
+        soft_barrier();  // both chains' O, maxima and sums have been read
       }
-      if (w.single) soft_barrier();  // both chains' O, maxima and sums have been read
       w.advance();
     }
     if (tid == 0 && !split) P.splits[blockIdx.x].last = -1;
   } else if (warp == kSoftWarps) {
     // ---------------- TMA: queries, keys, values
-    if (lane == 0) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
-    }
     const uint32_t on = elect_one();
     const int boxes = kRows / P.box;  // boxes of a block, one lane finds the page of each
     const uint32_t q_half = (uint32_t)(P.tq * P.G) * 128u;
@@ -848,146 +1015,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
   }
 }
 
-// ---------------------------------------------------------------- merge of cut items
-//
-// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over the CTAs c that worked on an item: one pass over the parts
-// with the running maximum, in a fixed order.  A block takes 32 rows of one cut item.  What counts is latency: a few
-// parts of many rows are read with a lane to a row, as they were written, every load issued before the first is used,
-// and turned in shared memory for the way out; many parts (single tokens over a long context, cut into as many as
-// there are SMs) with four lanes sharing them out, four rows at a time.
+// ---------------------------------------------------------------- merge of cut items of two tiles
 constexpr int kMergeThreads = 512;
-constexpr int kMergeRows = 32;
-constexpr int kMergeWide = 4;  // parts up to which a lane reads them all
-
-template <int N>
-struct RowSums {
-  float m[N], l[N], o[N];
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      m[k] = -INFINITY;
-      l[k] = o[k] = 0.f;
-    }
-  }
-  __device__ __forceinline__ void add(int k, float mi, float li, float oi) {
-    const float M = fmaxf(m[k], mi), ref = M == -INFINITY ? 0.f : M;
-    const float a = ex2(m[k] - ref), b = ex2(mi - ref);
-    m[k] = M;
-    l[k] = l[k] * a + li * b;
-    o[k] = o[k] * a + oi * b;
-  }
-  __device__ __forceinline__ void add4(int k, const float* pm, const float* po) {
-    const float4 a = __ldcg(reinterpret_cast<const float4*>(pm)), b = __ldcg(reinterpret_cast<const float4*>(pm + 256)),
-                 c = __ldcg(reinterpret_cast<const float4*>(po));
-    add(k, a.x, b.x, c.x);
-    add(k + 1, a.y, b.y, c.y);
-    add(k + 2, a.z, b.z, c.z);
-    add(k + 3, a.w, b.w, c.w);
-  }
-};
 
 __global__ void __launch_bounds__(kMergeThreads, 2) k_paged_merge(const __grid_constant__ Params P) {
+  __shared__ __align__(16) bf16 turn[kMergeRows][WI_D + 8];
   pdl_wait();
   const Split sp = P.splits[blockIdx.x];
   if (sp.last < 0) return;
-  static_assert(kMergeThreads / 32 * 8 == WI_D && kMergeThreads / 16 == kMergeRows, "thread maps");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x, parts = sp.last - c0 + 1;
-  // the partials' rows: tile 0's, then from 128 on tile 1's
   const int t = blockIdx.y / (kRows / kMergeRows), base = blockIdx.y % (kRows / kMergeRows) * kMergeRows;
-  const int rows = min(P.tq, sp.cnt - t * P.tq) * P.G;  // rows of the tile
-  if (base >= rows) return;
-  auto part = [&](int i) -> const float* { return P.parts + (long long)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kPartFloats; };
-  auto store = [&](int r, int d, float m, float l, float o) {
-    if (r >= rows) return;
-    const int tok = r / P.G;
-    const long long at = (long long)(sp.row0 + t * P.tq + tok) * P.Hq + sp.kh * P.G + r - tok * P.G;
-    static_cast<bf16*>(P.a.out)[at * WI_D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
-    if (P.a.lse && d == 0) P.a.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-  };
-  if (parts <= kMergeWide) {
-    __shared__ __align__(16) bf16 turn[kMergeRows][WI_D + 8];
-    const int r = base + lane, d0 = warp * 8;  // sixteen warps take eight columns each
-    float m[kMergeWide], l[kMergeWide], o[kMergeWide][8];
-#pragma unroll
-    for (int i = 0; i < kMergeWide; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-      if (i < parts) {
-        const float* p = part(i) + t * kRows + r;
-        m[i] = __ldcg(p);
-        l[i] = __ldcg(p + 256);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[i][k] = __ldcg(part(i) + 512 + (t * WI_D + d0 + k) * kRows + r);
-      }
-    }
-    float M = m[0], L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 1; i < kMergeWide; ++i) M = fmaxf(M, m[i]);
-    const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-    for (int i = 0; i < kMergeWide; ++i)
-      if (i < parts) {
-        const float f = ex2(m[i] - ref);
-        L += l[i] * f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] += o[i][k] * f;
-      }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    uint4 x;
-    x.x = pack2(acc[0] * inv, acc[1] * inv);
-    x.y = pack2(acc[2] * inv, acc[3] * inv);
-    x.z = pack2(acc[4] * inv, acc[5] * inv);
-    x.w = pack2(acc[6] * inv, acc[7] * inv);
-    *reinterpret_cast<uint4*>(&turn[lane][d0]) = x;
-    __syncthreads();
-    const int q = base + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 8;  // sixteen threads store a row
-    if (q < rows) {
-      const int tok = q / P.G;
-      const long long at = (long long)(sp.row0 + t * P.tq + tok) * P.Hq + sp.kh * P.G + q - tok * P.G;
-      *reinterpret_cast<uint4*>(static_cast<bf16*>(P.a.out) + at * WI_D + c) =
-          *reinterpret_cast<const uint4*>(&turn[q - base][c]);
-    }
-    if (P.a.lse && warp == 0 && r < rows) {
-      const int tok = r / P.G;
-      P.a.lse[(long long)(sp.row0 + t * P.tq + tok) * P.Hq + sp.kh * P.G + r - tok * P.G] =
-          L == 0.f ? -INFINITY : M * kLn2 + logf(L);
-    }
-  } else {
-    const int d = warp * 8 + (lane & 7), g = lane >> 3;  // sixteen warps take eight columns each
-    for (int r0 = base; r0 < rows && r0 < base + kMergeRows; r0 += 4) {
-      RowSums<4> s;
-      s.clear();
-#pragma unroll 4
-      for (int i = g; i < parts; i += 4) {
-        const float* p = part(i);
-        s.add4(0, p + t * kRows + r0, p + 512 + (t * WI_D + d) * kRows + r0);
-      }
-#pragma unroll
-      for (int o = 8; o <= 16; o <<= 1)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float m = __shfl_xor_sync(0xffffffffu, s.m[k], o), l = __shfl_xor_sync(0xffffffffu, s.l[k], o),
-                      x = __shfl_xor_sync(0xffffffffu, s.o[k], o);
-          s.add(k, m, l, x);
-        }
-      // lane group g holds every row; it stores row g
-      float m = s.m[0], l = s.l[0], x = s.o[0];
-#pragma unroll
-      for (int k = 1; k < 4; ++k)
-        if (g == k) {
-          m = s.m[k];
-          l = s.l[k];
-          x = s.o[k];
-        }
-      store(r0 + g, d, m, l, x);
-    }
-  }
+  if (base < tile_rows(P, sp, t)) merge_rows<true>(P, sp, blockIdx.x, t, base, turn);
 }
 
 }  // namespace
 
 constexpr size_t kSplitBytes = kPagedMaxSms * sizeof(Split);
-size_t wi_paged_attention_scratch(int sms) { return kSplitBytes + (size_t)sms * 2 * kPartFloats * 4; }
+size_t wi_paged_attention_scratch(int sms) {
+  return kPagedTicketBytes + kSplitBytes + (size_t)sms * 2 * kPartFloats * 4;
+}
 
 cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a, int sms, void* scratch, int* err,
                                       cudaStream_t st) {
@@ -1003,8 +1048,9 @@ cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a
   // a box of a block lies inside one page: the largest power of two that divides the page, 128 at most
   P.box = g.page & -g.page;
   if (P.box > kRows) P.box = kRows;
-  P.splits = static_cast<Split*>(scratch);
-  P.parts = reinterpret_cast<float*>(static_cast<char*>(scratch) + kSplitBytes);
+  P.tickets = static_cast<unsigned*>(scratch);
+  P.splits = reinterpret_cast<Split*>(static_cast<char*>(scratch) + kPagedTicketBytes);
+  P.parts = reinterpret_cast<float*>(static_cast<char*>(scratch) + kPagedTicketBytes + kSplitBytes);
   P.err = err;
   CUtensorMap map_q, map_k, map_v;
   const unsigned long long rows = (unsigned long long)g.n_pages * g.Hkv * g.page;
@@ -1017,16 +1063,9 @@ cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a
   cudaError_t e = wi_ensure_smem(k_paged_attention, sizeof(Smem), smem_set);
   if (e != cudaSuccess) return e;
   const int grid = sms < kPagedMaxSms ? sms : kPagedMaxSms;
-  k_paged_attention<<<grid, kThreads, sizeof(Smem), st>>>(map_q, map_k, map_v, P);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((unsigned)grid, 2 * kRows / kMergeRows);
-  lc.blockDim = dim3(kMergeThreads);
-  lc.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = at;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, k_paged_merge, P);
+  if ((e = wi_launch_chained(k_paged_attention, dim3((unsigned)grid), kThreads, sizeof(Smem), st, map_q, map_k, map_v,
+                             P)) != cudaSuccess)
+    return e;
+  if (a.n_tokens <= P.tq) return cudaSuccess;  // no item has two tiles
+  return wi_launch_chained(k_paged_merge, dim3((unsigned)grid, 2 * kRows / kMergeRows), kMergeThreads, 0, st, P);
 }
