@@ -15,10 +15,9 @@
 // made on the host.  Lengths live on the device: each CTA sums the units of
 // all requests itself (closed form per request) and finds its run's start.
 // An item cut between CTAs leaves partial results (maximum, sum, O) in the
-// scratch, added up in CTA order: those of an item of one tile by the last of
-// its CTAs, those of two tiles by k_paged_merge, which spreads them over the
-// machine and is launched only where the call may hold such an item (a single
-// token over 131K, 8 kv heads: 8-10 us less than with the second kernel).
+// scratch, added up in CTA order: by the last of its CTAs where the call has
+// eight rows per kv head at most (single tokens of one request), else by
+// k_paged_merge, which spreads the rows over the machine.
 //
 // A CTA (640 threads) processes its items' blocks in roles:
 //   warps 0-15      softmax: eight warps for each of two chains, two threads
@@ -69,9 +68,21 @@ constexpr int kLead = 4;
 // below 256, which costs neither bf16 nor fp32 any precision, and O is rescaled a few times per item at most.
 constexpr float kLazy = 8.f;
 
-// A partial result: m and l of 256 rows, then O of two tiles, column-major (a thread owns a row, so column-major
-// stores of a warp are contiguous).
-constexpr int kPartFloats = 2 * 256 + 2 * WI_D * kRows;
+// A partial result: m, then l, of every row, then O, column-major (a thread owns a row, so column-major stores of a
+// warp are contiguous).  Two tiles of 128 rows, or, where a call has no more, one of kMergeHere: those of all CTAs lie
+// within 1.3 MB then, which the merge of single tokens reads with fewer address translations.
+constexpr int kMergeHere = 8;  // rows per kv head of a call up to which the attention kernel merges itself
+struct Parts {
+  float* base;
+  int rows, tiles;
+  __device__ __forceinline__ float* slot(int i) const {
+    return base + (long long)i * (tiles * rows * (2 + WI_D));
+  }
+  __device__ __forceinline__ int m(int t, int r) const { return t * rows + r; }
+  __device__ __forceinline__ int l(int t, int r) const { return (tiles + t) * rows + r; }
+  __device__ __forceinline__ int o(int t, int d, int r) const { return (2 * tiles + t * WI_D + d) * rows + r; }
+};
+constexpr size_t kPartBytes = 2 * kRows * (2 + WI_D) * 4;
 
 struct Smem {
   uint64_t full[kStages], empty[kStages];
@@ -120,9 +131,9 @@ struct Params {
   WiPagedAttn a;
   int Hq, Hkv, G, tq;       // tq = tokens per tile
   int page, n_pages, max_pages, box;
-  float* parts;
+  Parts parts;
   Split* splits;
-  unsigned* tickets;        // of items of one tile, at the CTA that begins them; zero between calls
+  unsigned* tickets;        // of the items, at the CTA that begins each; zero between calls; null: k_paged_merge merges
   int* err;
 };
 
@@ -314,137 +325,62 @@ __device__ __forceinline__ int cta_of(long long u, long long total, int ctas) {
 
 // ---- merge of an item that was cut between CTAs
 //
-// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over the CTAs c that worked on it: one pass over the parts with
-// the running maximum, in a fixed order, by sixteen warps, 32 rows of a tile at a time.  What counts is latency: a few
-// parts of many rows are read with a lane to a row, as they were written, every load issued before the first is used
-// (TURN: the results go out through shared memory, whole rows at a time); many parts (single tokens over a long
-// context, cut into as many as there are SMs) with four lanes sharing them out, four rows at a time.
-constexpr int kMergeRows = 32;
-constexpr int kMergeWide = 4;  // parts up to which a lane reads them all
-
-struct RowSums {
-  float m[4], l[4], o[4];
-  __device__ __forceinline__ void add(int k, float mi, float li, float oi) {
-    const float M = fmaxf(m[k], mi), ref = M == -INFINITY ? 0.f : M;
-    const float a = ex2(m[k] - ref), b = ex2(mi - ref);
-    m[k] = M;
-    l[k] = l[k] * a + li * b;
-    o[k] = o[k] * a + oi * b;
-  }
-};
+// out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c over the CTAs c that worked on it, in their order.
+constexpr int kMergeThreads = 512;
 
 // Rows of an item's tile t.
 __device__ __forceinline__ int tile_rows(const Params& P, const Split& sp, int t) {
   return min(P.tq, sp.cnt - t * P.tq) * P.G;
 }
 
-template <bool TURN>
-__device__ __forceinline__ void merge_rows(const Params& P, const Split& sp, int c0, int t, int base,
-                                           bf16 (*turn)[WI_D + 8]) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, parts = sp.last - c0 + 1, rows = tile_rows(P, sp, t);
-  auto part = [&](int i) -> const float* { return P.parts + (long long)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kPartFloats; };
-  auto place = [&](int r) -> long long {  // (token, query head) of a row
-    const int tok = r / P.G;
-    return (long long)(sp.row0 + t * P.tq + tok) * P.Hq + sp.kh * P.G + r - tok * P.G;
-  };
-  if (parts <= kMergeWide) {
-    const int r = base + lane, d0 = warp * 8;  // sixteen warps take eight columns each
-    float m[kMergeWide], l[kMergeWide], o[kMergeWide][8];
+// The partial result of the i-th CTA that worked on the item that CTA c0 begins.
+__device__ __forceinline__ const float* part_of(const Params& P, int c0, int i) {
+  return P.parts.slot(2 * (c0 + i) + (i == 0 ? 1 : 0));
+}
+
+// (token, query head) of a row of tile t.
+__device__ __forceinline__ long long place_of(const Params& P, const Split& sp, int t, int r) {
+  const int tok = r / P.G;
+  return (long long)(sp.row0 + t * P.tq + tok) * P.Hq + sp.kh * P.G + r - tok * P.G;
+}
+
+// Rows [r0, r0 + 4) of tile t by 512 threads, each one row of one column: the parts eight at a time, with the running
+// maximum.
+__device__ __noinline__ void merge_four(const Params& P, const Split& sp, int c0, int t, int r0) {
+  const int r = r0 + (threadIdx.x & 3), d = threadIdx.x >> 2, parts = sp.last - c0 + 1;
+  float M = -INFINITY, L = 0.f, acc = 0.f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < parts; i0 += 8) {
+    float m[8], l[8], o[8];
 #pragma unroll
-    for (int i = 0; i < kMergeWide; ++i) {
-      m[i] = -INFINITY;
-      l[i] = 0.f;
-      if (i < parts) {
-        const float* p = part(i) + t * kRows + r;
-        m[i] = __ldcg(p);
-        l[i] = __ldcg(p + 256);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o[i][k] = __ldcg(part(i) + 512 + (t * WI_D + d0 + k) * kRows + r);
+    for (int k = 0; k < 8; ++k) {
+      m[k] = -INFINITY;
+      l[k] = o[k] = 0.f;
+      if (i0 + k < parts) {
+        const float* p = part_of(P, c0, i0 + k);
+        m[k] = __ldcg(p + P.parts.m(t, r));
+        l[k] = __ldcg(p + P.parts.l(t, r));
+        o[k] = __ldcg(p + P.parts.o(t, d, r));
       }
     }
-    float M = m[0], L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float top = M;
 #pragma unroll
-    for (int i = 1; i < kMergeWide; ++i) M = fmaxf(M, m[i]);
-    const float ref = M == -INFINITY ? 0.f : M;
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, m[k]);
+    const float ref = top == -INFINITY ? 0.f : top, f = ex2(M - ref);
+    M = top;
+    L *= f;
+    acc *= f;
 #pragma unroll
-    for (int i = 0; i < kMergeWide; ++i)
-      if (i < parts) {
-        const float f = ex2(m[i] - ref);
-        L += l[i] * f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) acc[k] += o[i][k] * f;
-      }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    uint4 x;
-    x.x = pack2(acc[0] * inv, acc[1] * inv);
-    x.y = pack2(acc[2] * inv, acc[3] * inv);
-    x.z = pack2(acc[4] * inv, acc[5] * inv);
-    x.w = pack2(acc[6] * inv, acc[7] * inv);
-    bf16* out = static_cast<bf16*>(P.a.out);
-    if (TURN) {
-      *reinterpret_cast<uint4*>(&turn[lane][d0]) = x;
-      __syncthreads();
-      const int q = threadIdx.x >> 4, c = (threadIdx.x & 15) * 8;  // sixteen threads store a row
-      if (base + q < rows)
-        *reinterpret_cast<uint4*>(out + place(base + q) * WI_D + c) = *reinterpret_cast<const uint4*>(&turn[q][c]);
-    } else if (r < rows) {
-      *reinterpret_cast<uint4*>(out + place(r) * WI_D + d0) = x;
+    for (int k = 0; k < 8; ++k) {
+      const float g = ex2(m[k] - ref);
+      L += g * l[k];
+      if (i0 + k < parts) acc += g * o[k];
     }
-    if (P.a.lse && warp == 0 && r < rows) P.a.lse[place(r)] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
-  } else {
-    const int d = warp * 8 + (lane & 7), g = lane >> 3;
-    for (int r0 = base; r0 < rows && r0 < base + kMergeRows; r0 += 4) {
-      RowSums s;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        s.m[k] = -INFINITY;
-        s.l[k] = s.o[k] = 0.f;
-      }
-      constexpr int kAtOnce = 5;  // parts that a lane has in flight: all of them up to 20 parts
-      for (int i0 = g; i0 < parts; i0 += 4 * kAtOnce) {
-        float4 a[kAtOnce], b[kAtOnce], c[kAtOnce];
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          a[k] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-          b[k] = c[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (i0 + 4 * k < parts) {
-            const float* p = part(i0 + 4 * k) + t * kRows + r0;
-            a[k] = __ldcg(reinterpret_cast<const float4*>(p));
-            b[k] = __ldcg(reinterpret_cast<const float4*>(p + 256));
-            c[k] = __ldcg(reinterpret_cast<const float4*>(p - t * kRows + 512 + (t * WI_D + d) * kRows));
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          s.add(0, a[k].x, b[k].x, c[k].x);
-          s.add(1, a[k].y, b[k].y, c[k].y);
-          s.add(2, a[k].z, b[k].z, c[k].z);
-          s.add(3, a[k].w, b[k].w, c[k].w);
-        }
-      }
-#pragma unroll
-      for (int o = 8; o <= 16; o <<= 1)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float m = __shfl_xor_sync(0xffffffffu, s.m[k], o), l = __shfl_xor_sync(0xffffffffu, s.l[k], o),
-                      x = __shfl_xor_sync(0xffffffffu, s.o[k], o);
-          s.add(k, m, l, x);
-        }
-      // every lane group holds all four rows; group g stores row g
-      float m = s.m[0], l = s.l[0], x = s.o[0];
-#pragma unroll
-      for (int k = 1; k < 4; ++k)
-        if (g == k) {
-          m = s.m[k];
-          l = s.l[k];
-          x = s.o[k];
-        }
-      const int r = r0 + g;
-      if (r < rows) {
-        static_cast<bf16*>(P.a.out)[place(r) * WI_D + d] = __float2bfloat16_rn(l == 0.f ? 0.f : x / l);
-        if (P.a.lse && d == 0) P.a.lse[place(r)] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
-      }
-    }
+  }
+  if (r < tile_rows(P, sp, t)) {
+    const long long at = place_of(P, sp, t, r);
+    static_cast<bf16*>(P.a.out)[at * WI_D + d] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
+    if (P.a.lse && d == 0) P.a.lse[at] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
   }
 }
 
@@ -589,8 +525,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       const int limit = live ? (int)(w.p0 + ti) : -1;   // the last position that the row sees
       const int whole = (int)(w.p0 + w.tile * w.tp + own_tile * P.tq);  // ... that all rows of the tile see
       float m = -INFINITY, l = 0.f;  // the row's reference maximum, and the sum of this thread's half
-      for (int j = w.single ? chain : 0; j < w.nb; j += w.single ? 2 : 1) {
-        const int k0 = (w.b0 + j) * kRows;
+      const int nb = w.nb, step = w.single ? 2 : 1, from = w.single ? chain : 0, base = w.b0 * kRows;
+      for (int j = from; j < nb; j += step) {
+        const int k0 = base + j * kRows;
         if (ok) ok = mbar_wait(&sm.s_full[chain], s_par, P.err);
         s_par ^= 1;
         tc_fence_after();
@@ -621,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         rows_barrier(chain, quarter);
         tc_fence_after();
         top = fmaxf(top, sm.xch[chain][half ^ 1][row]);
-        if (j < 2 && (j == 0 || w.single)) {  // the chain's first block
+        if (j == from) {  // the chain's first block
           m = top;
         } else {
           const bool need = top > m + kLazy;
@@ -695,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       }
       const long long at = (long long)(w.r.s0 + ti) * P.Hq + w.kh * P.G + head;
       const int slot = 2 * (int)blockIdx.x + (w.b0 == 0 ? 1 : 0);
-      float* dst = P.parts + (long long)slot * kPartFloats;
+      float* dst = P.parts.slot(slot);
       const bool poison = *reinterpret_cast<volatile int*>(&sm.poison[seg & 7]) == seg + 1;
       const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
       const uint32_t to = tmem + lanes + 256u + (w.single ? 0u : (uint32_t)chain * WI_D);
@@ -720,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         if (ok && live) {
           if (part) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) __stcg(dst + 512 + (own_tile * WI_D + c + i) * kRows + row, o[i]);
+            for (int i = 0; i < 16; ++i) __stcg(dst + P.parts.o(own_tile, c + i, row), o[i]);
           } else {
             uint4* q = reinterpret_cast<uint4*>(static_cast<bf16*>(P.a.out) + at * WI_D + c);
 #pragma unroll
@@ -737,20 +674,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       }
       if (ok && live && half == 0 && (chain == 0 || !w.single)) {
         if (part) {
-          __stcg(dst + own_tile * kRows + row, m);
-          __stcg(dst + 256 + own_tile * kRows + row, l);
+          __stcg(dst + P.parts.m(own_tile, row), m);
+          __stcg(dst + P.parts.l(own_tile, row), l);
         } else if (P.a.lse) {
           P.a.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
         }
       }
       tc_fence_before();  // O is read: the next segment may write it
-      if (!w.single) {
-        if (part && w.b0 == 0 && tid == 0) {
-          split = true;
-          P.splits[blockIdx.x] = {w.r.s0 + w.tile * w.tp, w.kh, w.cnt,
-                                  cta_of(u1 - w.left - w.at + kLead + w.nblk - 1, total, ctas)};
-        }
-      } else if (part) {
+      if (part && P.tickets) {
         const long long item = u1 - w.left - w.at + kLead;  // the unit of the item's first block
         const int c0 = cta_of(item, total, ctas), c1 = cta_of(item + w.nblk - 1, total, ctas);
         soft_barrier();  // then thread 0's release covers what all of them stored
@@ -764,13 +695,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         soft_barrier();
         if (sm.last) {
           const Split sp = {w.r.s0 + w.tile * w.tp, w.kh, w.cnt, c1};
-          for (int base = 0; base < tile_rows(P, sp, 0); base += kMergeRows)
-            merge_rows<false>(P, sp, c0, 0, base, nullptr);
+#pragma unroll 1
+          for (int r0 = 0; r0 < tile_rows(P, sp, 0); r0 += 4) merge_four(P, sp, c0, 0, r0);
         }
-        soft_barrier();
-      } else {
-        soft_barrier();  // both chains' O, maxima and sums have been read
+      } else if (part && w.b0 == 0 && tid == 0) {
+        split = true;
+        P.splits[blockIdx.x] = {w.r.s0 + w.tile * w.tp, w.kh, w.cnt,
+                                cta_of(u1 - w.left - w.at + kLead + w.nblk - 1, total, ctas)};
       }
+      if (w.single) soft_barrier();  // both chains' O, maxima and sums have been read
       w.advance();
     }
     if (tid == 0 && !split) P.splits[blockIdx.x].last = -1;
@@ -1015,23 +948,73 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
   }
 }
 
-// ---------------------------------------------------------------- merge of cut items of two tiles
-constexpr int kMergeThreads = 512;
+// The merge as a kernel of its own: a block takes 32 rows of one cut item.  What counts is latency.  Up to kMergeWide
+// parts are read with a lane to a row, as they were written, every load issued before the first is used, and turned in
+// shared memory for the way out; more parts four rows at a time.
+constexpr int kMergeRows = 32;
+constexpr int kMergeWide = 4;
 
 __global__ void __launch_bounds__(kMergeThreads, 2) k_paged_merge(const __grid_constant__ Params P) {
   __shared__ __align__(16) bf16 turn[kMergeRows][WI_D + 8];
   pdl_wait();
-  const Split sp = P.splits[blockIdx.x];
+  const int c0 = blockIdx.x;
+  const Split sp = P.splits[c0];
   if (sp.last < 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, parts = sp.last - c0 + 1;
   const int t = blockIdx.y / (kRows / kMergeRows), base = blockIdx.y % (kRows / kMergeRows) * kMergeRows;
-  if (base < tile_rows(P, sp, t)) merge_rows<true>(P, sp, blockIdx.x, t, base, turn);
+  const int rows = tile_rows(P, sp, t);
+  if (base >= rows) return;
+  if (parts > kMergeWide) {
+    for (int r0 = base; r0 < rows && r0 < base + kMergeRows; r0 += 4) merge_four(P, sp, c0, t, r0);
+    return;
+  }
+  const int r = base + lane, d0 = warp * 8;  // sixteen warps take eight columns each
+  float m[kMergeWide], l[kMergeWide], o[kMergeWide][8];
+#pragma unroll
+  for (int i = 0; i < kMergeWide; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+    if (i < parts) {
+      const float* p = part_of(P, c0, i);
+      m[i] = __ldcg(p + P.parts.m(t, r));
+      l[i] = __ldcg(p + P.parts.l(t, r));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[i][k] = __ldcg(p + P.parts.o(t, d0 + k, r));
+    }
+  }
+  float M = m[0], L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 1; i < kMergeWide; ++i) M = fmaxf(M, m[i]);
+  const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+  for (int i = 0; i < kMergeWide; ++i)
+    if (i < parts) {
+      const float f = ex2(m[i] - ref);
+      L += l[i] * f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] += o[i][k] * f;
+    }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint4 x;
+  x.x = pack2(acc[0] * inv, acc[1] * inv);
+  x.y = pack2(acc[2] * inv, acc[3] * inv);
+  x.z = pack2(acc[4] * inv, acc[5] * inv);
+  x.w = pack2(acc[6] * inv, acc[7] * inv);
+  *reinterpret_cast<uint4*>(&turn[lane][d0]) = x;
+  __syncthreads();
+  static_assert(kMergeThreads / 32 * 8 == WI_D && kMergeThreads / 16 == kMergeRows, "thread maps");
+  const int q = threadIdx.x >> 4, c = (threadIdx.x & 15) * 8;  // sixteen threads store a row
+  if (base + q < rows)
+    *reinterpret_cast<uint4*>(static_cast<bf16*>(P.a.out) + place_of(P, sp, t, base + q) * WI_D + c) =
+        *reinterpret_cast<const uint4*>(&turn[q][c]);
+  if (P.a.lse && warp == 0 && r < rows) P.a.lse[place_of(P, sp, t, r)] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
 }
 
 }  // namespace
 
 constexpr size_t kSplitBytes = kPagedMaxSms * sizeof(Split);
 size_t wi_paged_attention_scratch(int sms) {
-  return kPagedTicketBytes + kSplitBytes + (size_t)sms * 2 * kPartFloats * 4;
+  return kPagedTicketBytes + kSplitBytes + (size_t)sms * 2 * kPartBytes;
 }
 
 cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a, int sms, void* scratch, int* err,
@@ -1048,9 +1031,11 @@ cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a
   // a box of a block lies inside one page: the largest power of two that divides the page, 128 at most
   P.box = g.page & -g.page;
   if (P.box > kRows) P.box = kRows;
-  P.tickets = static_cast<unsigned*>(scratch);
+  const bool here = (long long)a.n_tokens * g.G <= kMergeHere;
+  P.tickets = here ? static_cast<unsigned*>(scratch) : nullptr;
   P.splits = reinterpret_cast<Split*>(static_cast<char*>(scratch) + kPagedTicketBytes);
-  P.parts = reinterpret_cast<float*>(static_cast<char*>(scratch) + kPagedTicketBytes + kSplitBytes);
+  P.parts = {reinterpret_cast<float*>(static_cast<char*>(scratch) + kPagedTicketBytes + kSplitBytes),
+             here ? kMergeHere : kRows, here ? 1 : 2};
   P.err = err;
   CUtensorMap map_q, map_k, map_v;
   const unsigned long long rows = (unsigned long long)g.n_pages * g.Hkv * g.page;
@@ -1066,6 +1051,6 @@ cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a
   if ((e = wi_launch_chained(k_paged_attention, dim3((unsigned)grid), kThreads, sizeof(Smem), st, map_q, map_k, map_v,
                              P)) != cudaSuccess)
     return e;
-  if (a.n_tokens <= P.tq) return cudaSuccess;  // no item has two tiles
+  if (here) return cudaSuccess;
   return wi_launch_chained(k_paged_merge, dim3((unsigned)grid, 2 * kRows / kMergeRows), kMergeThreads, 0, st, P);
 }
