@@ -412,8 +412,8 @@ __global__ void __launch_bounds__(kGaThreads) k_paged_gather(WiPagedGather A, lo
         flags |= WI_DEVERR_BAD_PAGE;
       } else {
         const long long src = (pool + ((long long)pg * Hkv + h) * page + (p - j * page)) * 16 + l;
-        kr[k] = __ldg(static_cast<const uint4*>(A.k_pages) + src);
-        vr[k] = __ldg(static_cast<const uint4*>(A.v_pages) + src);
+        kr[k] = __ldcg(static_cast<const uint4*>(A.k_pages) + src);
+        vr[k] = __ldcg(static_cast<const uint4*>(A.v_pages) + src);
       }
     }
   }

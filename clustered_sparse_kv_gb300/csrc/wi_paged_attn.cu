@@ -19,14 +19,13 @@
 // eight rows per kv head at most (single tokens of one request), else by
 // k_paged_merge, which spreads the rows over the machine.
 //
-// A CTA (640 threads) processes its items' blocks in roles:
-//   warps 0-15      softmax: eight warps for each of two chains, two threads
-//                   per row (64 of the block's 128 positions each)
-//   warp 16         TMA: queries, key and value blocks (box by box, through
+// A CTA (384 threads) processes its items' blocks in roles:
+//   warps 0-3, 4-7  softmax, one thread per row of chain 0 / chain 1
+//   warp 8          TMA: queries, key and value blocks (box by box, through
 //                   the block table) into a ring of five 32 KB stages
-//   warp 17         issues tcgen05.mma: S = Q K^T (both operands in shared
+//   warp 9          issues tcgen05.mma: S = Q K^T (both operands in shared
 //                   memory), O += P V (P in tensor memory, V N-major)
-//   warps 18-19     clean value rows of blocks that not every row sees whole
+//   warps 10-11     clean value rows of blocks that not every row sees whole
 // The two chains have their own S (P takes S's place) and O in tensor memory
 // (all 512 columns), so that one chain's softmax runs while the tensor cores
 // work on the other.  In an item of two tiles the chains are the tiles, and
@@ -56,7 +55,7 @@ constexpr int kRows = 128;                     // rows of a tile, and positions 
 constexpr int kStages = 5;
 constexpr int kTileBytes = kRows * WI_D * 2;   // 32 KB: two halves of 64 columns
 constexpr int kHalfBytes = kTileBytes / 2;
-constexpr int kSoftWarps = 16;
+constexpr int kSoftWarps = 8;
 constexpr int kThreads = 32 * (kSoftWarps + 4);
 constexpr int kFixWarps = 2;
 constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
@@ -64,9 +63,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Units in front of an item's blocks, for what its start and end cost (8192 fresh tokens, 32 / 8 heads: 542, 502, 466,
 // 439, 444 us at 1, 2, 3, 4, 6; longer contexts and single tokens do not care).
 constexpr int kLead = 4;
-// A row's reference maximum follows its true maximum only when that is more than 2^8 larger: the weights stay
-// below 256, which costs neither bf16 nor fp32 any precision, and O is rescaled a few times per item at most.
-constexpr float kLazy = 8.f;
+// A row's weights are 2^(score - m) with m the row's maximum in the first block of its part, which no later block needs
+// to know its own maximum for: only when a block's weights add up to more than this (one of them is 2^9 at least), or to
+// no number, the block is done again with the maximum so far, and O rescaled.  Weights below 2^16 cost neither bf16 nor
+// fp32 any precision.
+constexpr float kAgain = 65536.f;
 
 // A partial result: m, then l, of every row, then O, column-major (a thread owns a row, so column-major stores of a
 // warp are contiguous).  Two tiles of 128 rows, or, where a call has no more, one of kMergeHere: those of all CTAs lie
@@ -84,6 +85,17 @@ struct Parts {
 };
 constexpr size_t kPartBytes = 2 * kRows * (2 + WI_D) * 4;
 
+// Request b as the kernel reads it; a request with impossible numbers has no tokens (CTA 0 reports it).
+struct Req {
+  int s0, n, kv, ok;
+};
+
+// Where a CTA stands in its run: request, kv head, tile pair, the next unit of that item (its first kLead units stand
+// for no block), and the units of the run still to come.
+struct Cursor {
+  int b, kh, tile, at, left;
+};
+
 struct Smem {
   uint64_t full[kStages], empty[kStages];
   uint64_t to_fix[kStages], fixed[kStages];  // a value block that is to be cleaned was asked for; has been cleaned
@@ -94,9 +106,13 @@ struct Smem {
   int last;                 // this CTA merges the item that it just added to
   int poison[8];            // segment number + 1 of the last segment (modulo 8) with an infinite or NaN value
   long long scan[kThreads / 32];
-  int start[4];             // the run's first request, kv head, tile pair, block
-  float xch[2][2][kRows];   // between the two threads of a row: [chain][half]
-  unsigned char pad[3072 - (4 * kStages + 9) * 8 - 4 - 32 - 4 - kThreads / 32 * 8 - 16 - 4 * kRows * 4];
+  long long run_end, total;  // the unit behind this CTA's run, all units
+  int ctas;                 // CTAs with units
+  int spare;
+  Cursor start;             // of the run
+  Req req;                  // start.b's
+  float xch[2][2][kRows];   // maximum and sum of a row, from chain to chain: [chain][m, l]
+  unsigned char pad[3072 - (4 * kStages + 9) * 8 - 4 - 32 - 4 - kThreads / 32 * 8 - 24 - 20 - 16 - 4 * kRows * 4];
   unsigned char q[2][kTileBytes];          // [k half][128 rows][128 B]
   unsigned char ring[kStages][kTileBytes]; // [group of 8 rows][k half][8 rows][128 B]
 };
@@ -137,10 +153,6 @@ struct Params {
   int* err;
 };
 
-// Request b as the kernel reads it; a request with impossible numbers has no tokens (CTA 0 reports it).
-struct Req {
-  int s0, n, kv, ok;
-};
 __device__ __forceinline__ Req load_req(const Params& P, int b) {
   Req r;
   r.s0 = P.a.q_start[b];
@@ -191,27 +203,21 @@ __device__ __forceinline__ long long quot(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// Where a CTA stands in its run: one item's part after the other.
-struct Walk {
-  int b, kh, tile, at;    // at: the next unit of the item (its first kLead units stand for no block)
-  long long left;         // units of the run still to come
+// The run, one item's part after the other.
+struct Walk : Cursor {
   Req r;
   int tp, tiles;
   // the current segment: what the run holds of one item
   int cnt, single, nblk, b0, nb, took;   // tokens, one tile, blocks of the item, first block, blocks, units
   long long p0;           // position of the request's token 0
 
-  __device__ __forceinline__ void begin(const Params& P, const Smem& sm, long long units) {
-    b = sm.start[0];
-    kh = sm.start[1];
-    tile = sm.start[2];
-    at = sm.start[3];
-    left = units;
+  __device__ __forceinline__ Walk(const Params& P, const Cursor& c, const Req& q) : Cursor(c) {
     tp = 2 * P.tq;
-    set(P);
+    set(q);
   }
-  __device__ __forceinline__ void set(const Params& P) {
-    r = load_req(P, b);
+  __device__ __forceinline__ Walk(const Params& P, const Cursor& c) : Walk(P, c, load_req(P, c.b)) {}
+  __device__ __forceinline__ void set(const Req& q) {
+    r = q;
     p0 = (long long)r.kv - r.n;
     tiles = (r.n + tp - 1) / tp;
   }
@@ -223,13 +229,13 @@ struct Walk {
         if (r.n == 0 || ++kh == P.Hkv) {
           kh = 0;
           if (++b >= P.a.batch) return false;
-          set(P);
+          set(load_req(P, b));
         }
       }
       cnt = min(tp, r.n - tile * tp);
       single = cnt <= P.tq;
       nblk = blocks_to(p0, (long long)tile * tp + cnt);
-      took = (int)min((long long)(nblk + kLead - at), left);
+      took = min(nblk + kLead - at, left);
       b0 = max(0, at - kLead);
       nb = max(0, at + took - kLead) - b0;
       if (nb > 0) return true;
@@ -290,12 +296,40 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&w);
 }
 
-__device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory"); }
-
-// The two warps that share 32 rows of a chain.
-__device__ __forceinline__ void rows_barrier(int chain, int quarter) {
-  asm volatile("bar.sync %0, 64;" ::"r"(2 + chain * 4 + quarter) : "memory");
+// Scores behind column `seen` of 64 are not seen.
+__device__ __forceinline__ void mask_scores(uint32_t (&s)[2][32], int seen) {
+#pragma unroll
+  for (int i = 0; i < 64; ++i)
+    if (i > seen) s[i >> 5][i & 31] = 0xFF800000u;  // -infinity
 }
+
+__device__ __forceinline__ float top_score(const uint32_t (&s)[2][32]) {
+  float t[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const uint32_t* x = s[c >> 1] + (c & 1) * 16;
+    t[c] = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+#pragma unroll
+    for (int i = 2; i < 16; i += 2) t[c] = max3(t[c], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+  }
+  return fmaxf(max3(t[0], t[1], max3(t[2], t[3], -INFINITY)), -INFINITY);
+}
+
+// 32 scores to weights 2^(score * log2(e) / sqrt(128) - ref): added to `sum`, and as bf16 to 16 columns of P.
+__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t tp, float ref, uint64_t (&sum)[2]) {
+  const uint64_t scale2 = pair(kScaleLog2, kScaleLog2), ref2 = pair(-ref, -ref);
+  uint32_t p[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint64_t x = fma2(pair(s[2 * i], s[2 * i + 1]), scale2, ref2);
+    const float a = ex2(lo_of(x)), b = ex2(hi_of(x));
+    sum[i & 1] = add2(sum[i & 1], pair(a, b));
+    p[i] = pack2(a, b);
+  }
+  tmem_st16_nowait(tp, p);
+}
+
+__device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory"); }
 
 __device__ __forceinline__ bool nonfinite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
@@ -344,44 +378,54 @@ __device__ __forceinline__ long long place_of(const Params& P, const Split& sp, 
   return (long long)(sp.row0 + t * P.tq + tok) * P.Hq + sp.kh * P.G + r - tok * P.G;
 }
 
-// Rows [r0, r0 + 4) of tile t by 512 threads, each one row of one column: the parts eight at a time, with the running
-// maximum.
-__device__ __noinline__ void merge_four(const Params& P, const Split& sp, int c0, int t, int r0) {
-  const int r = r0 + (threadIdx.x & 3), d = threadIdx.x >> 2, parts = sp.last - c0 + 1;
-  float M = -INFINITY, L = 0.f, acc = 0.f;
+// Rows of tile t from r0 on by THREADS threads, each two rows of one column (2 * THREADS / 128 rows in all): the parts
+// ten at a time, with the running maximum.
+template <int THREADS>
+__device__ __noinline__ void merge_some(const Params& P, const Split& sp, int c0, int t, int r0) {
+  constexpr int kPairs = THREADS / WI_D, kAtOnce = 10;
+  const int r = r0 + 2 * (threadIdx.x % kPairs), d = threadIdx.x / kPairs, parts = sp.last - c0 + 1;
+  float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, acc[2] = {0.f, 0.f};
 #pragma unroll 1
-  for (int i0 = 0; i0 < parts; i0 += 8) {
-    float m[8], l[8], o[8];
+  for (int i0 = 0; i0 < parts; i0 += kAtOnce) {
+    float2 m[kAtOnce], l[kAtOnce], o[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      m[k] = -INFINITY;
-      l[k] = o[k] = 0.f;
+    for (int k = 0; k < kAtOnce; ++k) {
+      m[k] = make_float2(-INFINITY, -INFINITY);
+      l[k] = o[k] = make_float2(0.f, 0.f);
       if (i0 + k < parts) {
         const float* p = part_of(P, c0, i0 + k);
-        m[k] = __ldcg(p + P.parts.m(t, r));
-        l[k] = __ldcg(p + P.parts.l(t, r));
-        o[k] = __ldcg(p + P.parts.o(t, d, r));
+        m[k] = __ldcg(reinterpret_cast<const float2*>(p + P.parts.m(t, r)));
+        l[k] = __ldcg(reinterpret_cast<const float2*>(p + P.parts.l(t, r)));
+        o[k] = __ldcg(reinterpret_cast<const float2*>(p + P.parts.o(t, d, r)));
       }
     }
-    float top = M;
+    float2 top = make_float2(M[0], M[1]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = fmaxf(top, m[k]);
-    const float ref = top == -INFINITY ? 0.f : top, f = ex2(M - ref);
-    M = top;
-    L *= f;
-    acc *= f;
+    for (int k = 0; k < kAtOnce; ++k) top = make_float2(fmaxf(top.x, m[k].x), fmaxf(top.y, m[k].y));
+    const float ref0 = top.x == -INFINITY ? 0.f : top.x, ref1 = top.y == -INFINITY ? 0.f : top.y;
+    const float f0 = ex2(M[0] - ref0), f1 = ex2(M[1] - ref1);
+    M[0] = top.x;
+    M[1] = top.y;
+    L[0] *= f0;
+    L[1] *= f1;
+    acc[0] *= f0;
+    acc[1] *= f1;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float g = ex2(m[k] - ref);
-      L += g * l[k];
-      if (i0 + k < parts) acc += g * o[k];
+    for (int k = 0; k < kAtOnce; ++k) {
+      const float g0 = ex2(m[k].x - ref0), g1 = ex2(m[k].y - ref1);
+      L[0] += g0 * l[k].x;
+      L[1] += g1 * l[k].y;
+      acc[0] += g0 * o[k].x;
+      acc[1] += g1 * o[k].y;
     }
   }
-  if (r < tile_rows(P, sp, t)) {
-    const long long at = place_of(P, sp, t, r);
-    static_cast<bf16*>(P.a.out)[at * WI_D + d] = __float2bfloat16_rn(L == 0.f ? 0.f : acc / L);
-    if (P.a.lse && d == 0) P.a.lse[at] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
-  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (r + k < tile_rows(P, sp, t)) {
+      const long long at = place_of(P, sp, t, r + k);
+      static_cast<bf16*>(P.a.out)[at * WI_D + d] = __float2bfloat16_rn(L[k] == 0.f ? 0.f : acc[k] / L[k]);
+      if (P.a.lse && d == 0) P.a.lse[at] = L[k] == 0.f ? -INFINITY : M[k] * kLn2 + logf(L[k]);
+    }
 }
 
 __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_constant__ CUtensorMap map_q,
@@ -438,8 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
   const int rb0 = min(tid * per, P.a.batch), rb1 = min(rb0 + per, P.a.batch);
   const int tp = 2 * P.tq;
   long long mine = 0, cost = 0;  // cost: of one kv head of the last request looked at
+  Req r = {0, 0, 0, 1};
   for (int b = rb0; b < rb1; ++b) {
-    const Req r = load_req(P, b);
+    r = load_req(P, b);
     if (!r.ok && blockIdx.x == 0) atomicOr(P.err, WI_DEVERR_BAD_LENGTH);
     if (r.n == 0) continue;
     const int tiles = (r.n + tp - 1) / tp;
@@ -474,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
   if (u0 >= before && u0 < before + mine) {  // one thread's requests hold the run's first unit
     long long rem = u0 - before;
     for (int b = rb0; b < rb1; ++b) {
-      const Req r = load_req(P, b);
+      if (per > 1) r = load_req(P, b);  // else the one request is at hand
       if (r.n == 0) continue;
       const int tiles = (r.n + tp - 1) / tp;
       const long long p0 = (long long)r.kv - r.n;
@@ -490,119 +535,120 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         const int mid = (lo + hi + 1) >> 1;
         if (units_before(p0, tp, mid) <= rem) lo = mid; else hi = mid - 1;
       }
-      sm.start[0] = b;
-      sm.start[1] = kh;
-      sm.start[2] = lo;
-      sm.start[3] = (int)(rem - units_before(p0, tp, lo));
+      if (lo > 0) rem -= units_before(p0, tp, lo);
+      sm.start = {b, kh, lo, (int)rem, (int)(u1 - u0)};
+      sm.req = r;
+      sm.run_end = u1;
+      sm.total = total;
+      sm.ctas = ctas;
       break;
     }
   }
   __syncthreads();
 
-  Walk w;
-  w.begin(P, sm, u1 - u0);
-
-  // a softmax lane holds half a row of scores; the registers that the other warps do not need go to those
-  // (104 * 16 + 64 * 4 = 96 * 20, what the launch has)
+  // a softmax lane holds a row of scores; the registers that the other warps do not need go to those
+  // (208 * 8 + 88 * 4 = 168 * 12, what the launch has)
   if (warp < kSoftWarps)
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
   else
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp < kSoftWarps) {
     // ---------------- softmax
-    const int chain = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
-    const int row = quarter * 32 + lane;
-    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const int chain = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + (uint32_t)chain * kRows;
     const int tok = (row * ((65536 + P.G - 1) / P.G)) >> 16, head = row - tok * P.G;
     uint32_t s_par = 0, o_par0 = 0, o_par1 = 0;
     bool ok = true;  // after one timed-out wait the warp waits no more and writes nothing, but meets every barrier
     bool split = false;  // the run's last item goes on in the next CTA
-    for (int seg = 0; w.next(P); ++seg) {
-      const int own_tile = w.single ? 0 : chain;
-      const int ti = w.tile * w.tp + own_tile * P.tq + tok;
-      const bool live = tok < P.tq && ti < w.r.n;
-      const int limit = live ? (int)(w.p0 + ti) : -1;   // the last position that the row sees
-      const int whole = (int)(w.p0 + w.tile * w.tp + own_tile * P.tq);  // ... that all rows of the tile see
-      float m = -INFINITY, l = 0.f;  // the row's reference maximum, and the sum of this thread's half
-      const int nb = w.nb, step = w.single ? 2 : 1, from = w.single ? chain : 0, base = w.b0 * kRows;
+    // Only the cursor lives through a segment's blocks, beside the scores; the rest is worked out again behind them.
+    Cursor cur = sm.start;
+    for (int seg = 0;; ++seg) {
+      int nb, step, from, base, limit, whole;
+      {
+        Walk w(P, cur);
+        if (!w.next(P)) break;
+        cur = w;
+        const int own_tile = w.single ? 0 : chain, ti = w.tile * w.tp + own_tile * P.tq + tok;
+        limit = tok < P.tq && ti < w.r.n ? (int)(w.p0 + ti) : -1;     // the last position that the row sees
+        whole = (int)(w.p0 + w.tile * w.tp + own_tile * P.tq);       // ... that all rows of the tile see
+        nb = w.nb;
+        step = w.single ? 2 : 1;
+        from = w.single ? chain : 0;
+        base = w.b0 * kRows;
+      }
+      float m = -INFINITY, l = 0.f;  // the row's reference maximum and its sum
       for (int j = from; j < nb; j += step) {
-        const int k0 = base + j * kRows;
         if (ok) ok = mbar_wait(&sm.s_full[chain], s_par, P.err);
         s_par ^= 1;
         tc_fence_after();
-        uint32_t s[2][32];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) tmem_ld32_nowait(ts + 64 * half + 32 * c, s[c]);
+        // The second half of the scores comes while the first is worked on; P then takes the place of the first half,
+        // which stays in registers, so that the block can be done again.
+        uint32_t a[2][32], b[2][32];
+        tmem_ld32_nowait(ts, a[0]);
+        tmem_ld32_nowait(ts + 32, a[1]);
         tmem_wait_ld();
-        if (k0 + kRows - 1 > whole) {
-          const int seen = limit - k0 - 64 * half;  // the row sees columns 0 .. seen of this half
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (i > seen) s[i >> 5][i & 31] = 0xFF800000u;  // -infinity
-        }
-        float t[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int o = (c & 1) * 16;
-          t[c] = fmaxf(__uint_as_float(s[c >> 1][o]), __uint_as_float(s[c >> 1][o + 1]));
-#pragma unroll
-          for (int i = 2; i < 16; i += 2)
-            t[c] = max3(t[c], __uint_as_float(s[c >> 1][o + i]), __uint_as_float(s[c >> 1][o + i + 1]));
-        }
-        float top = fmaxf(max3(t[0], t[1], max3(t[2], t[3], -INFINITY)), -INFINITY) * kScaleLog2;
-        // The other half's maximum.  Past the barrier both threads have their scores in registers, so P may take
-        // S's place.  The slots are free again once the next scores of the chain are there: those wait for P.
-        sm.xch[chain][half][row] = top;
-        tc_fence_before();
-        rows_barrier(chain, quarter);
-        tc_fence_after();
-        top = fmaxf(top, sm.xch[chain][half ^ 1][row]);
-        if (j == from) {  // the chain's first block
-          m = top;
-        } else {
-          const bool need = top > m + kLazy;
-          if (__any_sync(0xffffffffu, need)) {
-            // the chain's products so far are done: S of this block was issued behind them
-            const float f = need ? ex2(m - top) : 1.f;
-            if (need) m = top;
-            l *= f;
-            const uint32_t to = tmem + lanes + 256u + (uint32_t)chain * WI_D + 64u * half;
+        tmem_ld32_nowait(ts + 64, b[0]);
+        tmem_ld32_nowait(ts + 96, b[1]);
+        const bool masked = base + j * kRows + kRows - 1 > whole;
+        const int seen = limit - base - j * kRows;  // the row sees columns 0 .. seen of this block
+        if (masked) mask_scores(a, seen);
+        bool again = j == from;
+        for (;;) {
+          if (again) {  // the first block, or the reference is far too small
+            tmem_wait_st();
+            tmem_wait_ld();
+            tmem_ld32_nowait(ts + 64, b[0]);
+            tmem_ld32_nowait(ts + 96, b[1]);
+            tmem_wait_ld();
+            if (masked) mask_scores(b, seen - 64);
+            const float top = fmaxf(m, fmaxf(top_score(a), top_score(b)) * kScaleLog2);
+            if (j != from) {
+              // the chain's products so far are done: S of this block was issued behind them
+              const float f = m == top ? 1.f : ex2(m - top);
+              l *= f;
+              const uint32_t to = tmem + lanes + 256u + (uint32_t)chain * WI_D;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[16];
-              tmem_ld16_nowait(to + 16 * c, o);
-              tmem_wait_ld();
+              for (int c = 0; c < 8; ++c) {
+                uint32_t o[16];
+                tmem_ld16_nowait(to + 16 * c, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st16_nowait(to + 16 * c, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st16_nowait(to + 16 * c, o);
+              }
             }
+            m = top;
           }
-        }
-        const float ref = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 2^-inf = 0
-        const uint64_t scale2 = pair(kScaleLog2, kScaleLog2), ref2 = pair(-ref, -ref);
-        uint64_t l2[2] = {pair(l, 0.f), 0ull};
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint64_t x = fma2(pair(s[c][2 * i], s[c][2 * i + 1]), scale2, ref2);
-            const float a = ex2(lo_of(x)), b = ex2(hi_of(x));
-            l2[i & 1] = add2(l2[i & 1], pair(a, b));
-            p[i] = pack2(a, b);
+          const float ref = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 2^-inf = 0
+          uint64_t sum[2] = {0ull, 0ull};
+          weights(a[0], ts, ref, sum);
+          weights(a[1], ts + 16, ref, sum);
+          tmem_wait_ld();
+          if (masked && !again) mask_scores(b, seen - 64);
+          weights(b[0], ts + 32, ref, sum);
+          weights(b[1], ts + 48, ref, sum);
+          const uint64_t both = add2(sum[0], sum[1]);
+          const float z = lo_of(both) + hi_of(both);
+          // (a row that had seen nothing takes its reference from the first block that it sees something of)
+          if (again || !__any_sync(0xffffffffu, !(z <= kAgain) || (m == -INFINITY && z > 0.f))) {
+            l += z;
+            break;
           }
-          tmem_st16_nowait(ts + 32 * half + 16 * c, p);
+          again = true;
         }
-        const uint64_t ls = add2(l2[0], l2[1]);
-        l = lo_of(ls) + hi_of(ls);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_ready[chain]);
       }
 
-      // ---- the segment's end: the sums of both halves, of both chains where they had one tile, then O
+      // ---- the segment's end: maximum and sum over both chains where they had one tile, then O
+      Walk w(P, cur);
+      w.next(P);
+      const int own_tile = w.single ? 0 : chain, ti = w.tile * w.tp + own_tile * P.tq + tok;
+      const bool live = tok < P.tq && ti < w.r.n;
       const bool both = !w.single || w.nb > 1;  // chain 1 had blocks
       const bool part = w.b0 > 0 || w.nb < w.nblk;
       if (ok && (w.single || chain == 0)) ok = mbar_wait(&sm.o_full[0], o_par0, P.err);
@@ -610,19 +656,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       o_par0 ^= 1;
       if (both) o_par1 ^= 1;
       tc_fence_after();
-      // half 1 gives its sum, half 0 the total (and the maximum) back; O is complete, so nobody reads a block's
-      // maximum from the slots any more
-      if (half == 1) sm.xch[chain][1][row] = l;
-      if (w.single) soft_barrier(); else rows_barrier(chain, quarter);
-      if (half == 0) {
-        l += sm.xch[chain][1][row];
-        sm.xch[chain][1][row] = l;
-        sm.xch[chain][0][row] = m;
-      }
-      if (w.single) soft_barrier(); else rows_barrier(chain, quarter);
-      l = sm.xch[chain][1][row];
       float f0 = 1.f, f1 = 0.f;
       if (w.single) {
+        sm.xch[chain][0][row] = m;
+        sm.xch[chain][1][row] = l;
+        soft_barrier();
         const float m0 = sm.xch[0][0][row], m1 = sm.xch[1][0][row];
         m = fmaxf(m0, m1);
         const float ref = m == -INFINITY ? 0.f : m;
@@ -636,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       const bool poison = *reinterpret_cast<volatile int*>(&sm.poison[seg & 7]) == seg + 1;
       const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
       const uint32_t to = tmem + lanes + 256u + (w.single ? 0u : (uint32_t)chain * WI_D);
-      const int ca = w.single ? 32 * (2 * chain + half) : 64 * half, cb = ca + (w.single ? 32 : 64);
+      const int ca = w.single ? 64 * chain : 0, cb = w.single ? ca + 64 : WI_D;  // the columns that this thread takes
 #pragma unroll 1
       for (int c = ca; c < cb; c += 16) {
         __syncwarp();
@@ -672,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
           }
         }
       }
-      if (ok && live && half == 0 && (chain == 0 || !w.single)) {
+      if (ok && live && (chain == 0 || !w.single)) {
         if (part) {
           __stcg(dst + P.parts.m(own_tile, row), m);
           __stcg(dst + P.parts.l(own_tile, row), l);
@@ -682,8 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       }
       tc_fence_before();  // O is read: the next segment may write it
       if (part && P.tickets) {
-        const long long item = u1 - w.left - w.at + kLead;  // the unit of the item's first block
-        const int c0 = cta_of(item, total, ctas), c1 = cta_of(item + w.nblk - 1, total, ctas);
+        const long long item = sm.run_end - w.left - w.at + kLead;  // the unit of the item's first block
+        const int c0 = cta_of(item, sm.total, sm.ctas), c1 = cta_of(item + w.nblk - 1, sm.total, sm.ctas);
         soft_barrier();  // then thread 0's release covers what all of them stored
         if (tid == 0) {
           sm.last = 0;
@@ -696,18 +734,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         if (sm.last) {
           const Split sp = {w.r.s0 + w.tile * w.tp, w.kh, w.cnt, c1};
 #pragma unroll 1
-          for (int r0 = 0; r0 < tile_rows(P, sp, 0); r0 += 4) merge_four(P, sp, c0, 0, r0);
+          for (int r0 = 0; r0 < tile_rows(P, sp, 0); r0 += 2 * kSoftWarps * 32 / WI_D)
+            merge_some<kSoftWarps * 32>(P, sp, c0, 0, r0);
         }
       } else if (part && w.b0 == 0 && tid == 0) {
         split = true;
         P.splits[blockIdx.x] = {w.r.s0 + w.tile * w.tp, w.kh, w.cnt,
-                                cta_of(u1 - w.left - w.at + kLead + w.nblk - 1, total, ctas)};
+                                cta_of(sm.run_end - w.left - w.at + kLead + w.nblk - 1, sm.total, sm.ctas)};
       }
       if (w.single) soft_barrier();  // both chains' O, maxima and sums have been read
       w.advance();
+      cur = w;
     }
     if (tid == 0 && !split) P.splits[blockIdx.x].last = -1;
   } else if (warp == kSoftWarps) {
+    Walk w(P, sm.start, sm.req);
     // ---------------- TMA: queries, keys, values
     const uint32_t on = elect_one();
     const int boxes = kRows / P.box;  // boxes of a block, one lane finds the page of each
@@ -717,6 +758,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     int q_loads = 0, last = 0;        // last: the stage filled last
     bool ok = true;
     for (int seg = 0; ok && w.next(P); ++seg) {
+      const int ahead = w.single ? 2 : 1;
+      // This lane's box of block j of the segment: its page as the table has it, looked up blocks ahead and looked at
+      // when the copy is due (kNone: behind the request's end).
+      constexpr int kNone = -0x7fffffff - 1;
+      auto page_of = [&](int j) -> int {
+        const int p = (w.b0 + j) * kRows + lane * P.box;
+        if (j >= w.nb || lane >= boxes || p >= w.r.kv) return kNone;
+        return P.a.block_table[(long long)w.b * P.max_pages + p / P.page];
+      };
+      auto row_of = [&](int pg, int j) -> int {
+        if (pg == kNone) return -1;
+        if (pg < 0 || pg >= P.n_pages) {
+          atomicOr(P.err, WI_DEVERR_BAD_PAGE);
+          pg = 0;
+        }
+        return (pg * P.Hkv + w.kh) * P.page + ((w.b0 + j) * kRows + lane * P.box) % P.page;
+      };
+      int g0 = page_of(0), g1 = page_of(1), g2 = page_of(2);
       // queries, once the products of the segment before have read theirs
       if (seg > 0) ok = mbar_wait(&sm.q_empty, (seg - 1) & 1, P.err);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -730,20 +789,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         }
       }
       ++q_loads;
-      const int ahead = w.single ? 2 : 1;
-      // the pool row of this lane's box of block j (of the segment); -1 behind the request's end
-      auto row_of = [&](int j) -> int {
-        const int p = (w.b0 + j) * kRows + lane * P.box;
-        if (j >= w.nb || lane >= boxes || p >= w.r.kv) return -1;
-        const int pj = p / P.page;
-        int pg = __ldg(P.a.block_table + (long long)w.b * P.max_pages + pj);
-        if (pg < 0 || pg >= P.n_pages) {
-          atomicOr(P.err, WI_DEVERR_BAD_PAGE);
-          pg = 0;
-        }
-        return (pg * P.Hkv + w.kh) * P.page + (p - pj * P.page);
-      };
-      auto fill = [&](const CUtensorMap* map, int rowi) -> bool {
+      auto fill = [&](const CUtensorMap* map, int pg, int j) -> bool {
+        const int rowi = row_of(pg, j);
         bool got = true;
         if (filled == kStages) got = mbar_wait(&sm.empty[at.s], at.par ^ 1u, P.err);
         if (!__all_sync(0xffffffffu, got)) return false;
@@ -760,17 +807,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         if (filled < kStages) ++filled;
         return true;
       };
-      int r0 = row_of(0), r1 = row_of(1), r2 = row_of(2);
-      ok = fill(&map_k, r0);
-      if (ok && ahead == 2 && w.nb > 1) ok = fill(&map_k, r1);
+      ok = fill(&map_k, g0, 0);
+      if (ok && ahead == 2 && w.nb > 1) ok = fill(&map_k, g1, 1);
       for (int j = 0; ok && j < w.nb; ++j) {
-        const int r3 = row_of(j + 3);
-        ok = fill(&map_v, r0);
+        const int g3 = page_of(j + 3);
+        ok = fill(&map_v, g0, j);
         if (ok && lane == 0 && w.b0 + j >= w.first_fix()) mbar_arrive(&sm.to_fix[last]);
-        if (ok && j + ahead < w.nb) ok = fill(&map_k, ahead == 2 ? r2 : r1);
-        r0 = r1;
-        r1 = r2;
-        r2 = r3;
+        if (ok && j + ahead < w.nb) ok = fill(&map_k, ahead == 2 ? g2 : g1, j + ahead);
+        g0 = g1;
+        g1 = g2;
+        g2 = g3;
       }
       w.advance();
     }
@@ -780,6 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     for (int s = 0; s < filled; ++s)  // the last use of each stage: this turn's in front of `at`, else the turn before
       mbar_wait(&sm.full[s], s < at.s ? at.par : at.par ^ 1u, P.err);
   } else if (warp == kSoftWarps + 1) {
+    Walk w(P, sm.start, sm.req);
     // ---------------- tensor cores: one lane issues, the whole warp computes what it issues
     {
       const uint32_t on = elect_one();
@@ -896,6 +943,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       mbar_wait(&sm.drained, 0, P.err);
     }
   } else {
+    Walk w(P, sm.start, sm.req);
     // ---------------- clean the value rows of blocks that not every row sees whole
     const int half = warp - kSoftWarps - 2;  // 64 rows each
     Ring at;                     // the ring stage of the next block in turn
@@ -950,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
 
 // The merge as a kernel of its own: a block takes 32 rows of one cut item.  What counts is latency.  Up to kMergeWide
 // parts are read with a lane to a row, as they were written, every load issued before the first is used, and turned in
-// shared memory for the way out; more parts four rows at a time.
+// shared memory for the way out; more parts eight rows at a time.
 constexpr int kMergeRows = 32;
 constexpr int kMergeWide = 4;
 
@@ -965,7 +1013,8 @@ __global__ void __launch_bounds__(kMergeThreads, 2) k_paged_merge(const __grid_c
   const int rows = tile_rows(P, sp, t);
   if (base >= rows) return;
   if (parts > kMergeWide) {
-    for (int r0 = base; r0 < rows && r0 < base + kMergeRows; r0 += 4) merge_four(P, sp, c0, t, r0);
+    for (int r0 = base; r0 < rows && r0 < base + kMergeRows; r0 += 2 * kMergeThreads / WI_D)
+      merge_some<kMergeThreads>(P, sp, c0, t, r0);
     return;
   }
   const int r = base + lane, d0 = warp * 8;  // sixteen warps take eight columns each
