@@ -257,6 +257,8 @@ struct Walk : Cursor {
     const int f = first_pos();
     return f < 0 ? 0 : (f + 1) / kRows;
   }
+  // The first position whose value row is cleaned: what all rows see stays as it is, in whole groups of eight.
+  __device__ __forceinline__ int first_clean() const { return max(0, first_pos() + 1) & ~7; }
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -332,13 +334,16 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t tp, fl
 __device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory"); }
 
 __device__ __forceinline__ bool nonfinite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
+// Two bf16 values at once: bit 15 / 31 set where the exponent is all ones (one more in its last place carries over it).
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
 
-// Add the infinite and NaN values that a row sees in blocks [f0, f1) to 16 columns of its O.
-__device__ __forceinline__ void add_poison(const Params& P, int b, int kh, int f0, int f1, int kv, int limit, int c0,
+// Add the infinite and NaN values that a row sees at positions [from, to), where they were taken out, to 16 columns of
+// its O.
+__device__ __forceinline__ void add_poison(const Params& P, int b, int kh, int from, int to, int limit, int c0,
                                            float (&o)[16]) {
-  const int end = min(min(f1 * kRows, kv), limit + 1);
+  const int end = min(to, limit + 1);
 #pragma unroll 1
-  for (int p = f0 * kRows; p < end; ++p) {
+  for (int p = from; p < end; ++p) {
     const int j = p / P.page, pg = P.a.block_table[(long long)b * P.max_pages + j];
     if (pg < 0 || pg >= P.n_pages) continue;
     const uint32_t* v = static_cast<const uint32_t*>(P.a.v_pages) +
@@ -691,7 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
           for (int i = 0; i < 16; ++i) o[i] = o[i] * f0 + __uint_as_float(raw_o[i]) * f1;
         }
         if (poison && live)
-          add_poison(P, w.b, w.kh, max(w.b0, w.first_fix()), w.b0 + w.nb, w.r.kv, limit, c, o);
+          add_poison(P, w.b, w.kh, max(max(w.b0, w.first_fix()) * kRows, w.first_clean()),
+                     min((w.b0 + w.nb) * kRows, w.r.kv), limit, c, o);
         if (ok && live) {
           if (part) {
 #pragma unroll
@@ -945,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
   } else {
     Walk w(P, sm.start, sm.req);
     // ---------------- clean the value rows of blocks that not every row sees whole
-    const int half = warp - kSoftWarps - 2;  // 64 rows each
+    const int fixer = warp - kSoftWarps - 2;
     Ring at;                     // the ring stage of the next block in turn
     uint32_t fix_par = 0;
     bool ok = true;
@@ -961,24 +967,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         if (!(ok = mbar_wait(&sm.to_fix[s], (fix_par >> s) & 1u, P.err))) break;
         fix_par ^= 1u << s;
         if (!(ok = mbar_wait(&sm.full[s], at.par, P.err))) break;
-        const int seen = w.r.kv - (w.b0 + j) * kRows;  // rows of the block that the request holds
-        uint4* v = reinterpret_cast<uint4*>(sm.ring[s] + half * kHalfBytes);  // 64 rows: [8 groups][2][8 rows][8 pieces]
+        const int k0 = (w.b0 + j) * kRows, seen = w.r.kv - k0;  // rows of the block that the request holds
+        uint4* v = reinterpret_cast<uint4*>(sm.ring[s]);  // [16 groups][2][8 rows][8 pieces]
         bool found = false;
-        for (int i = lane; i < kHalfBytes / 16; i += 32) {
-          if (half * 64 + (i >> 7) * 8 + ((i >> 3) & 7) >= seen) {  // (the swizzle moves pieces inside a row only)
+        for (int i = max(0, w.first_clean() - k0) * 16 + fixer * 32 + lane; i < kRows * 16; i += 64) {
+          if ((i >> 7) * 8 + ((i >> 3) & 7) >= seen) {  // (the swizzle moves pieces inside a row only)
             v[i] = make_uint4(0u, 0u, 0u, 0u);
             continue;
           }
           const uint4 x = v[i];
-          uint32_t e[4] = {x.x, x.y, x.z, x.w};
-          bool hit = false;
+          if ((nonfinite2(x.x) | nonfinite2(x.y) | nonfinite2(x.z) | nonfinite2(x.w)) & 0x80008000u) {
+            uint32_t e[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (nonfinite16(e[k])) { e[k] &= 0xFFFF0000u; hit = true; }
-            if (nonfinite16(e[k] >> 16)) { e[k] &= 0x0000FFFFu; hit = true; }
+            for (int k = 0; k < 4; ++k) {
+              if (nonfinite16(e[k])) e[k] &= 0xFFFF0000u;
+              if (nonfinite16(e[k] >> 16)) e[k] &= 0x0000FFFFu;
+            }
+            v[i] = make_uint4(e[0], e[1], e[2], e[3]);
+            found = true;
           }
-          if (hit) v[i] = make_uint4(e[0], e[1], e[2], e[3]);
-          found |= hit;
         }
         if (found) *reinterpret_cast<volatile int*>(&sm.poison[seg & 7]) = seg + 1;
         fence_proxy_async_smem();

@@ -67,6 +67,8 @@ __device__ __forceinline__ void mma_bf16(uint32_t tmem_d, uint64_t adesc, uint64
 
 // Instruction descriptor bit of a B operand whose N elements are contiguous (N-major).
 constexpr uint32_t kIdescNMajorB = 1u << 16;
+// ... and of an A operand whose M elements are contiguous (M-major).
+constexpr uint32_t kIdescMMajorA = 1u << 15;
 
 // The two words of a shared-memory matrix descriptor with the 128-byte swizzle, for code that the whole warp runs
 // with values it shares (the low word steps by bytes / 16 from one k step to the next).  K-major: `group` bytes from
