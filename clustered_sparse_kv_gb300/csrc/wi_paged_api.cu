@@ -42,6 +42,31 @@ int fail(int code, const char* fmt, ...) {
 
 bool misaligned(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
+// Bytes of device memory that an argument covers.
+struct Span {
+  const void* at;
+  long long bytes;
+};
+
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.at && b.at && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+
+// Whether an output shares memory with an input or with another output.
+template <int N, int M>
+bool clash(const Span (&outs)[N], const Span (&ins)[M]) {
+  for (int o = 0; o < N; ++o) {
+    for (int i = 0; i < M; ++i)
+      if (overlap(outs[o], ins[i])) return true;
+    for (int q = 0; q < o; ++q)
+      if (overlap(outs[o], outs[q])) return true;
+  }
+  return false;
+}
+
+long long pool_bytes(const WiPagedGeom& g) { return (long long)g.n_pages * g.Hkv * g.page * WI_D * 2; }
+
 // What every call checks first: the handle, and that its device is the current one.
 int enter(const wi_paged* pc) {
   wi_set_error("");
@@ -166,8 +191,11 @@ int wi_paged_check(wi_paged* pc) {
 
 void wi_paged_free(wi_paged* pc) {
   if (!pc) return;
+  int dev = -1;
+  const bool other = cudaGetDevice(&dev) == cudaSuccess && dev != pc->device && cudaSetDevice(pc->device) == cudaSuccess;
   cudaDeviceSynchronize();
   destroy(pc);
+  if (other) cudaSetDevice(dev);
 }
 
 int wi_paged_tables(wi_paged* pc, int batch, const int32_t* ctx_len, const int32_t* new_len,
@@ -181,17 +209,15 @@ int wi_paged_tables(wi_paged* pc, int batch, const int32_t* ctx_len, const int32
   if (!ctx_len || !new_len || !n_free || !block_table || !kv_len || !q_start || !n_free_out ||
       (free_cap > 0 && !free_pages) || (n_tokens > 0 && (!slots || !positions)))
     return fail(WI_EINVAL, "a table pointer is NULL");
-  const void* in[4] = {ctx_len, new_len, free_pages, n_free};
-  const void* outs[6] = {block_table, kv_len, q_start, slots, positions, n_free_out};
-  for (int o = 0; o < 6; ++o) {
-    if (misaligned(outs[o], 4)) return fail(WI_EINVAL, "the tables must be 4-byte aligned");
-    for (int i = 0; i < 4; ++i) {
-      if (misaligned(in[i], 4)) return fail(WI_EINVAL, "the tables must be 4-byte aligned");
-      if (outs[o] && outs[o] == in[i]) return fail(WI_EINVAL, "an output is an input's buffer");
-    }
-    for (int p = 0; p < o; ++p)
-      if (outs[o] && outs[o] == outs[p]) return fail(WI_EINVAL, "two outputs are one buffer");
-  }
+  const long long B = batch;
+  const Span in[4] = {{ctx_len, 4 * B}, {new_len, 4 * B}, {free_pages, 4LL * free_cap}, {n_free, 4}};
+  const Span outs[6] = {{block_table, 4 * B * pc->g.max_pages}, {kv_len, 4 * B}, {q_start, 4 * (B + 1)},
+                        {slots, 4LL * n_tokens}, {positions, 4LL * n_tokens}, {n_free_out, 4}};
+  for (const Span& x : in)
+    if (misaligned(x.at, 4)) return fail(WI_EINVAL, "the tables must be 4-byte aligned");
+  for (const Span& x : outs)
+    if (misaligned(x.at, 4)) return fail(WI_EINVAL, "the tables must be 4-byte aligned");
+  if (clash(outs, in)) return fail(WI_EINVAL, "an output shares memory with an input or another output");
   const WiPagedTables a = {ctx_len, new_len, free_pages, n_free,    block_table, kv_len,  q_start,
                            slots,   positions, n_free_out, batch, free_cap,    n_tokens};
   const cudaError_t e = wi_launch_paged_tables(pc->g, a, pc->sms, pc->err, static_cast<cudaStream_t>(stream));
@@ -218,9 +244,15 @@ int wi_paged_write(wi_paged* pc, int n_tokens, const void* q, long long q_stride
   const long long qw = (long long)g.Hq * WI_D, kw = (long long)g.Hkv * WI_D;
   if (n_tokens > 1 && (q_stride < qw || k_stride < kw || v_stride < kw || q_stride % 8 || k_stride % 8 || v_stride % 8))
     return fail(WI_EINVAL, "token strides must be multiples of 8 and at least a token's heads");
-  if (q_out == q && n_tokens > 1 && q_stride != qw)
-    return fail(WI_EINVAL, "q_out may be q only where q's tokens are contiguous");
-  if (k_pages == v_pages) return fail(WI_EINVAL, "k_pages and v_pages are one buffer");
+  const long long n1 = n_tokens - 1, kb = slots ? pool_bytes(g) : 2 * kw * n_tokens;
+  const bool in_place = q_out == q && (n_tokens == 1 || q_stride == qw);
+  const Span in[7] = {{in_place ? nullptr : q, 2 * (n1 * q_stride + qw)}, {k, 2 * (n1 * k_stride + kw)},
+                      {v, 2 * (n1 * v_stride + kw)}, {q_weight, 2 * WI_D}, {k_weight, 2 * WI_D},
+                      {positions, 4LL * n_tokens}, {slots, 4LL * n_tokens}};
+  const Span outs[3] = {{q_out, 2 * qw * n_tokens}, {k_pages, kb}, {v_pages, kb}};
+  if (clash(outs, in))
+    return fail(WI_EINVAL, "an output shares memory with an input or another output (q_out may be q itself where q's "
+                           "tokens are contiguous)");
   const WiPagedWrite a = {q,     k,     v,       q_stride, k_stride, v_stride, q_weight, k_weight, positions,
                           slots, q_out, k_pages, v_pages,  n_tokens};
   const cudaError_t e = wi_launch_paged_write(g, a, pc->sms, pc->err, static_cast<cudaStream_t>(stream));
@@ -243,7 +275,12 @@ int wi_paged_attention(wi_paged* pc, int batch, int n_tokens, const void* q, con
     return fail(WI_EINVAL, "q, the pools and out must be 16-byte aligned");
   if (misaligned(block_table, 4) || misaligned(q_start, 4) || misaligned(kv_len, 4) || misaligned(lse, 4))
     return fail(WI_EINVAL, "the tables and lse must be 4-byte aligned");
-  if (out == q) return fail(WI_EINVAL, "out may not be q");
+  const WiPagedGeom& g = pc->g;
+  const long long qb = 2LL * n_tokens * g.Hq * WI_D;
+  const Span in[6] = {{q, qb}, {k_pages, pool_bytes(g)}, {v_pages, pool_bytes(g)}, {block_table, 4LL * batch * g.max_pages},
+                      {q_start, 4LL * (batch + 1)}, {kv_len, 4LL * batch}};
+  const Span outs[2] = {{out, qb}, {lse, 4LL * n_tokens * g.Hq}};
+  if (clash(outs, in)) return fail(WI_EINVAL, "out or lse shares memory with an input or with the other");
   const WiPagedAttn a = {q, k_pages, v_pages, block_table, q_start, kv_len, out, lse, batch, n_tokens};
   const cudaError_t e = wi_launch_paged_attention(pc->g, a, pc->sms, pc->scratch, pc->err, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(WI_ECUDA, "paged attention launch: %s", cudaGetErrorString(e));
@@ -269,8 +306,11 @@ int wi_paged_gather(wi_paged* pc, int batch, int layers, const void* k_pages, co
   if (misaligned(k_pages, 16) || misaligned(v_pages, 16) || misaligned(k_out, 16) || misaligned(v_out, 16))
     return fail(WI_EINVAL, "the pools, k_out and v_out must be 16-byte aligned");
   if (misaligned(block_table, 4) || misaligned(kv_len, 4)) return fail(WI_EINVAL, "the tables must be 4-byte aligned");
-  if (k_out == v_out || k_out == k_pages || k_out == v_pages || v_out == k_pages || v_out == v_pages)
-    return fail(WI_EINVAL, "k_out and v_out must be buffers of their own");
+  const long long ob = 2LL * batch * layers * g.Hkv * n * WI_D;
+  const Span in[4] = {{k_pages, layers * pool_bytes(g)}, {v_pages, layers * pool_bytes(g)},
+                      {block_table, 4LL * batch * g.max_pages}, {kv_len, 4LL * batch}};
+  const Span outs[2] = {{k_out, ob}, {v_out, ob}};
+  if (clash(outs, in)) return fail(WI_EINVAL, "k_out or v_out shares memory with an input or with the other");
   const WiPagedGather a = {k_pages, v_pages, block_table, kv_len, k_out, v_out, batch, layers, pos0, n};
   const cudaError_t e = wi_launch_paged_gather(g, a, pc->err, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return fail(WI_ECUDA, "paged gather launch: %s", cudaGetErrorString(e));

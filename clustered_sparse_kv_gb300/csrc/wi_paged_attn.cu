@@ -513,6 +513,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     total += sm.scan[w];
   }
   before -= mine;
+  // (lengths that add up to more than a run can count, through pages shared by many requests: nothing is done)
+  if (total > (long long)gridDim.x * 0x3fffffff) {
+    if (blockIdx.x == 0 && tid == 0) atomicOr(P.err, WI_DEVERR_BAD_LENGTH);
+    total = 0;
+  }
   const int ctas = (int)min((long long)gridDim.x, total);
   if ((int)blockIdx.x >= ctas) {  // fewer units than CTAs (the whole CTA leaves)
     if (tid == 0) P.splits[blockIdx.x].last = -1;

@@ -423,7 +423,7 @@ typedef struct {
   const double* inv_freq; /* host, rotary_dim / 2 angles per position (radians), copied; NULL if none */
 } wi_paged_config;
 
-/* Make a handle on the current device (allocates the attention's scratch). */
+/* Make a handle on the current device (allocates the attention's scratch, about 270 KB per SM). */
 int wi_paged_create(const wi_paged_config* cfg, wi_paged** out);
 
 /* Synchronise the device and report what kernels of this handle's calls found wrong
@@ -445,8 +445,8 @@ void wi_paged_free(wi_paged* pc);
  * new_len; q_start [batch + 1], the running sum of new_len (the step's tokens
  * lie request after request); slots and positions [n_tokens], of each token,
  * -1 for those behind the last; *n_free_out, the free pages that are left
- * (free_pages itself is not changed).  No output may be an input's
- * buffer except block_table (WI_EINVAL for equal pointers).
+ * (free_pages itself is not changed).  No output may share memory with an
+ * input or another output (WI_EINVAL).
  * A length that is negative or beyond max_pages * page_size, more new tokens
  * than n_tokens, or more pages than *n_free: an error bit is set, and the step
  * takes no page and has no token (q_start all 0, kv_len = ctx_len, or 0 where
@@ -468,7 +468,8 @@ int wi_paged_tables(wi_paged* pc, int batch, const int32_t* ctx_len, const int32
  * angle positions[t] * inv_freq[i]: (a cos - b sin, b cos + a sin).  All in
  * fp32 (the angle exact to 2^-32 of a turn at any position), rounded once.
  * Queries go to q_out [n_tokens][n_q_heads][128] (q itself if
- * q_stride = n_q_heads * 128), keys and values to slot slots[t] of the pools.
+ * q_stride = n_q_heads * 128; outputs share no memory otherwise, WI_EINVAL),
+ * keys and values to slot slots[t] of the pools.
  * A token with positions[t] < 0 is padding: nothing of it is written; one with
  * slots[t] < 0 has its query written only.  Live tokens' slots are distinct.
  * With slots NULL, k_pages and v_pages are [n_tokens][n_kv_heads][128] instead

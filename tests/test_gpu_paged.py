@@ -747,3 +747,154 @@ def test_captured_step_replays_over_new_contents(wi):
     del graph
     for s in (a, b):
         s["pc"].free()
+
+
+# ------------------------------------------------------------ calls that overlap, repeat and share ----
+
+def test_attention_long_chunks(wi):
+    """More blocks than one CTA takes, several items to a CTA, items cut in two and in many."""
+    attention_case(wi, 8, 2, 64, [700, 1, 513], [5700, 9000, 3513], seed=30)
+    attention_case(wi, 4, 1, 16, [64], [20064], seed=31)
+    attention_case(wi, 28, 4, 128, [37, 300], [4037, 6300], seed=32)
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "late"])
+def test_attention_maxima_that_move_far(wi, order):
+    """Scores that outgrow everything before them block after block (by thousands), fall, or come late: the weights'
+    reference has to follow."""
+    hq, hkv, n, kv, page = 4, 1, 40, 900, 16
+    rng = np.random.default_rng(33)
+    table, n_pages = lay_out([kv], page, rng)
+    base = rng.normal(size=128)
+    q, Q = bf(np.broadcast_to(base * 4, (n, hq, 128)) + rng.normal(size=(n, hq, 128)))
+    size = {"rising": np.linspace(-3, 3, kv) ** 3, "falling": -np.linspace(-3, 3, kv) ** 3,
+            "late": np.where(np.arange(kv) < 700, -20.0, 1.0)}[order]
+    K = base * size[:, None] + 0.1 * rng.normal(size=(kv, 128))
+    Kp, Vp = np.zeros((n_pages, hkv, page, 128)), rng.normal(size=(n_pages, hkv, page, 128))
+    for p in range(kv):
+        Kp[table[0, p // page], 0, p % page] = K[p]
+    k, Kr = bf(Kp)
+    v, Vr = bf(Vp)
+    pc = wi.PagedCache(wi.make_paged_config(hq, hkv, page, n_pages, 1, table.shape[1]))
+    lse = torch.empty((n, hq), device=DEV)
+    out = pc.attention(q, k, v, i32(table), i32([0, n]), i32([kv]), lse=lse)
+    pc.check()
+    ref, rlse, spread = paged.attention(Q, Kr, Vr, table, [0, n], [kv])
+    top = np.linalg.norm(Q, axis=-1) * np.sqrt((Kr ** 2).sum(-1).max()) / np.sqrt(128)
+    ds = 128 * 2.0 ** -24 * top + 2.0 ** -20
+    tol = 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -7) * spread * (2.0 ** -8 + 2 * ds + kv * 2.0 ** -23)[..., None]
+    assert (np.abs(f64(out) - ref) <= tol).all()
+    assert (np.abs(f64(lse) - rlse) <= ds + kv * 2.0 ** -24 + 2.0 ** -22 * np.abs(rlse) + 2.0 ** -20).all()
+    pc.free()
+
+
+def test_attention_requests_that_share_pages(wi):
+    """Two requests with a common prefix held once."""
+    rng = np.random.default_rng(34)
+    k, K = bf(rng.normal(size=(12, 2, 16, 128)))
+    v, V = bf(rng.normal(size=(12, 2, 16, 128)))
+    table = [[3, 1, 4, 5, 9], [3, 1, 4, 2, 6], [3, 1, 4, 5, 9]]
+    q, Q = bf(rng.normal(size=(22, 8, 128)))
+    pc = wi.PagedCache(wi.make_paged_config(8, 2, 16, 12, 3, 5))
+    out = pc.attention(q, k, v, i32(table), i32([0, 20, 21, 22]), i32([70, 66, 51]))
+    pc.check()
+    ref, _, spread = paged.attention(Q, K, V, table, [0, 20, 21, 22], [70, 66, 51])
+    assert (np.abs(f64(out) - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -7 * spread).all()
+    pc.free()
+
+
+def test_attention_calls_in_turn_and_on_two_streams(wi):
+    """One handle used for single tokens and chunks in turn, many times, and two handles at once on two streams:
+    always the same bits."""
+    rng = np.random.default_rng(35)
+    kv = [3000, 2000, 700]
+    table, n_pages = lay_out(kv, 16, rng)
+    k, v = (bf(rng.normal(size=(n_pages, 2, 16, 128)))[0] for _ in range(2))
+    pcs = [wi.PagedCache(wi.make_paged_config(8, 2, 16, n_pages, 3, table.shape[1])) for _ in range(2)]
+    jobs = []
+    for new in [(1, 0, 0), (1, 1, 1), (0, 200, 90), (2, 0, 0), (150, 1, 33)]:
+        q = bf(rng.normal(size=(sum(new), 8, 128)))[0]
+        jobs.append((q, k, v, i32(table), i32(np.concatenate([[0], np.cumsum(new)])), i32(kv)))
+    first = [pcs[0].attention(*j) for j in jobs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for j, f in zip(jobs, first):
+            assert torch.equal(pcs[0].attention(*j), f)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.zeros_like(f) for _ in range(10) for f in first] for _ in range(2)]
+    for i in range(len(outs[0])):
+        for s in range(2):
+            n = i if s == 0 else len(outs[0]) - 1 - i   # different jobs at the same time
+            pcs[s].attention(*jobs[n % len(jobs)], out=outs[s][n], stream=streams[s])
+    torch.cuda.synchronize()
+    for s in range(2):
+        for n, o in enumerate(outs[s]):
+            assert torch.equal(o, first[n % len(jobs)])
+        pcs[s].check()
+        pcs[s].free()
+
+
+def test_calls_refuse_shared_memory(wi):
+    pc = wi.PagedCache(wi.make_paged_config(4, 2, 16, 8, 2, 4))
+    bf16 = dict(dtype=torch.bfloat16, device=DEV)
+    x = torch.zeros((4, 8 * 128), **bf16)
+    q, k, v = (t.view(4, -1, 128) for t in x.split([512, 256, 256], 1))
+    pools = [torch.zeros((8, 2, 16, 128), **bf16) for _ in range(2)]
+    neg, flat = i32([-1] * 4), torch.zeros(4 * 1024, **bf16)
+    for kw in (dict(q_out=x.view(-1)[:2048].view(4, 4, 128)),            # the fused rows, other strides
+               dict(q_out=pools[0].view(-1)[:2048].view(4, 4, 128))):
+        with pytest.raises(wi.WiError, match="shares memory"):
+            pc.write(q, k, v, neg, neg, *pools, **kw)
+    kn = flat[:1024].view(4, 2, 128)
+    with pytest.raises(wi.WiError, match="shares memory"):               # keys and values half a buffer apart
+        pc.write(q, k, v, neg, None, kn, flat[512:1536].view(4, 2, 128))
+    table, start, kv = i32([[0] * 4]), i32([0, 4]), i32([4])
+    qc = torch.zeros((4, 4, 128), **bf16)
+    with pytest.raises(wi.WiError, match="shares memory"):
+        pc.attention(qc, *pools, table, start, kv, out=pools[1].view(-1)[:2048].view(4, 4, 128))
+    with pytest.raises(wi.WiError, match="shares memory"):
+        pc.attention(qc, *pools, table, start, kv, lse=qc.view(torch.float32).view(-1)[:16].view(4, 4))
+    big = torch.zeros((1, 1, 2, 8, 128), **bf16)
+    with pytest.raises(wi.WiError, match="shares memory"):
+        pc.gather(*pools, table, kv, 0, big, pools[0].view(-1)[2048:4096].view(1, 1, 2, 8, 128))
+    i = i32(range(40))
+    with pytest.raises(wi.WiError, match="shares memory"):
+        pc.tables(i[0:1], i[1:2], i[2:4], i[4:5], i[5:9].view(1, 4), i[9:10], i[10:12], i[12:14], i[13:15], i[20:21])
+    pc.check()
+    pc.free()
+
+
+def test_write_then_attention_of_one_token_many_times(wi):
+    """A decode loop without any wait in between: each step's token is written and attended to before the next one,
+    kernel chained to kernel; against the same loop with a wait after every call."""
+    rng = np.random.default_rng(36)
+    hq, hkv, page, steps = 8, 2, 16, 60
+    cfg = wi.make_paged_config(hq, hkv, page, 40, 2, 20)
+    w = torch.ones(128, dtype=torch.bfloat16, device=DEV)
+    x = torch.from_numpy(rng.normal(size=(steps, 2, (hq + 2 * hkv) * 128)).astype(np.float32)).to(DEV).bfloat16()
+
+    def loop(wait):
+        pc = wi.PagedCache(cfg)
+        pools = [torch.zeros((40, hkv, page, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        table, free = i32(np.full((2, 20), -1)), i32(np.random.default_rng(1).permutation(40))
+        ctx, left = [i32([200, 7]), i32([0, 0])], [i32([40]), i32([0])]
+        start, slots, pos, one = i32([0, 0, 0]), i32([0, 0]), i32([0, 0]), i32([1, 1])
+        # the positions before the first step: their pages, and zeros in them
+        pc.tables(i32([0, 0]), ctx[0], free, left[0], table, ctx[1], i32([0, 0, 0]), i32([0] * 207), i32([0] * 207), left[1])
+        left.reverse()
+        outs = []
+        for t in range(steps):
+            pc.tables(ctx[0], one, free, left[0], table, ctx[1], start, slots, pos, left[1])
+            q, k, v = x[t].split([hq * 128, hkv * 128, hkv * 128], 1)
+            q = pc.write(q.view(2, hq, 128), k.view(2, hkv, 128), v.view(2, hkv, 128), pos, slots, *pools, None, w, w)
+            outs.append(pc.attention(q, *pools, table, start, ctx[1]))
+            ctx.reverse()
+            left.reverse()
+            if wait:
+                torch.cuda.synchronize()
+        pc.check()
+        pc.free()
+        return torch.stack(outs), pools
+
+    a, b = loop(False), loop(True)
+    assert torch.equal(a[0], b[0]) and all(torch.equal(u, v) for u, v in zip(a[1], b[1]))
