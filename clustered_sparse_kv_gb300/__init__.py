@@ -21,6 +21,7 @@ if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{_LIB_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
 
 lib = ctypes.CDLL(_LIB_PATH)
+from . import _paged  # noqa: E402  (the paged cache's argument checks; built with the library)
 
 WI_OK, WI_EINVAL, WI_ENOMEM, WI_ECUDA, WI_EUNSUPPORTED, WI_EDEVICE, WI_EFULL = 0, -1, -2, -3, -4, -5, -6
 _NAMES = {-1: "WI_EINVAL", -2: "WI_ENOMEM", -3: "WI_ECUDA", -4: "WI_EUNSUPPORTED", -5: "WI_EDEVICE",
@@ -455,10 +456,6 @@ class WaveIndex:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
-_BF16 = (torch.bfloat16, torch.int16)
-_INT32 = (torch.int32,)
-_FP32 = (torch.float32,)
-
 
 class PagedCache:
     """Owns one paged-cache handle (wi_paged_*): pages and slots of a step from its requests' lengths,
@@ -478,34 +475,8 @@ class PagedCache:
         self.n_q_heads, self.n_kv_heads = cfg.n_q_heads, cfg.n_kv_heads
         self.page_size, self.n_pages = cfg.page_size, cfg.n_pages
         self.max_batch, self.max_pages = cfg.max_batch, cfg.max_pages
-        self._pool = (cfg.n_pages, cfg.n_kv_heads, cfg.page_size, 128)
-
-    # The checks below run on every call of a decode step, whose kernels take a few microseconds: one comparison per
-    # property, shapes as tuples, the message put together only when something is wrong.
-
-    def _arg(self, name, t, kinds, shape):
-        """Data pointer of a contiguous tensor of this device with this shape."""
-        if t.dtype not in kinds or t.shape != shape or not t.is_contiguous() or t.get_device() != self.device:
-            raise ValueError(f"{name} must be a contiguous {kinds[0]} tensor of shape {tuple(shape)} on "
-                             f"cuda:{self.device} (got {t.dtype} {tuple(t.shape)} on {t.device}, strides "
-                             f"{tuple(t.stride())})")
-        return t.data_ptr()
-
-    def _heads(self, name, t, heads, n):
-        """Data pointer and token stride of [n][heads][128] with contiguous heads."""
-        s = t.stride()
-        if (t.dtype not in _BF16 or t.shape != (n, heads, 128) or s[2] != 1 or (heads > 1 and s[1] != 128) or
-                t.get_device() != self.device):
-            raise ValueError(f"{name} must be a bf16 tensor [{n}][{heads}][128] with contiguous heads on "
-                             f"cuda:{self.device} (got {t.dtype} {tuple(t.shape)} on {t.device}, strides {s})")
-        return t.data_ptr(), s[0]
-
-    def _table(self, t, b):
-        """Data pointer of a block table with at least b rows."""
-        rows = t.shape[0] if t.dim() == 2 else 0
-        if rows < b:
-            raise ValueError(f"block_table must have a row for each of the {b} requests (got {tuple(t.shape)})")
-        return self._arg("block_table", t, _INT32, (rows, self.max_pages))
+        self._ctx = _paged.context(self.handle, self.device, cfg.n_q_heads, cfg.n_kv_heads, cfg.page_size, cfg.n_pages,
+                                   cfg.max_pages)
 
     def _on(self, stream):
         return _raw_stream(self.device) if stream is None else _stream(stream)
@@ -513,13 +484,8 @@ class PagedCache:
     def tables(self, ctx_len, new_len, free_pages, n_free, block_table, kv_len, q_start, slots, positions,
                n_free_out, stream=None):
         """Pages, slots and positions of a step (wi_paged_tables); every argument an int32 tensor."""
-        a, b, n, cap = self._arg, ctx_len.shape[0], slots.shape[0], free_pages.shape[0]
-        rc = lib.wi_paged_tables(
-            self.handle, b, a("ctx_len", ctx_len, _INT32, (b,)), a("new_len", new_len, _INT32, (b,)),
-            a("free_pages", free_pages, _INT32, (cap,)), a("n_free", n_free, _INT32, (1,)), cap,
-            self._table(block_table, b), a("kv_len", kv_len, _INT32, (b,)),
-            a("q_start", q_start, _INT32, (b + 1,)), a("slots", slots, _INT32, (n,)),
-            a("positions", positions, _INT32, (n,)), n, a("n_free_out", n_free_out, _INT32, (1,)), self._on(stream))
+        rc = _paged.tables(self._ctx, ctx_len, new_len, free_pages, n_free, block_table, kv_len, q_start, slots,
+                           positions, n_free_out, self._on(stream))
         if rc:
             _check(rc)
 
@@ -528,21 +494,10 @@ class PagedCache:
         """Norms and rotation of q and k, keys and values into the pools (wi_paged_write); returns q_out
         [n][n_q_heads][128].  q, k, v: [n][heads][128], views of a fused projection allowed.  slots None:
         k_pages and v_pages are [n][n_kv_heads][128]."""
-        a, n = self._arg, q.shape[0]
-        shape = (n, self.n_q_heads, 128)
         if q_out is None:
-            q_out = _new_on(stream, shape, q.dtype, q.device)
-        pool = (n, self.n_kv_heads, 128) if slots is None else self._pool
-        qp, qs = self._heads("q", q, self.n_q_heads, n)
-        kp, ks = self._heads("k", k, self.n_kv_heads, n)
-        vp, vs = self._heads("v", v, self.n_kv_heads, n)
-        rc = lib.wi_paged_write(
-            self.handle, n, qp, qs, kp, ks, vp, vs,
-            None if q_weight is None else a("q_weight", q_weight, _BF16, (128,)),
-            None if k_weight is None else a("k_weight", k_weight, _BF16, (128,)),
-            a("positions", positions, _INT32, (n,)), None if slots is None else a("slots", slots, _INT32, (n,)),
-            a("q_out", q_out, _BF16, shape), a("k_pages", k_pages, _BF16, pool), a("v_pages", v_pages, _BF16, pool),
-            self._on(stream))
+            q_out = _new_on(stream, (q.shape[0], self.n_q_heads, 128), q.dtype, q.device)
+        rc = _paged.write(self._ctx, q, k, v, positions, slots, k_pages, v_pages, q_out, q_weight, k_weight,
+                          self._on(stream))
         if rc:
             _check(rc)
         return q_out
@@ -550,15 +505,9 @@ class PagedCache:
     def attention(self, q, k_pages, v_pages, block_table, q_start, kv_len, out=None, lse=None, stream=None):
         """Attention of a step's tokens over the cache (wi_paged_attention); returns out [n][n_q_heads][128]
         (rows behind the last request are zero if out was not given)."""
-        a, b, n = self._arg, kv_len.shape[0], q.shape[0]
-        shape = (n, self.n_q_heads, 128)
         if out is None:
-            out = _new_on(stream, shape, q.dtype, q.device, torch.zeros)
-        rc = lib.wi_paged_attention(
-            self.handle, b, n, a("q", q, _BF16, shape), a("k_pages", k_pages, _BF16, self._pool),
-            a("v_pages", v_pages, _BF16, self._pool), self._table(block_table, b),
-            a("q_start", q_start, _INT32, (b + 1,)), a("kv_len", kv_len, _INT32, (b,)), a("out", out, _BF16, shape),
-            None if lse is None else a("lse", lse, _FP32, (n, self.n_q_heads)), self._on(stream))
+            out = _new_on(stream, (q.shape[0], self.n_q_heads, 128), q.dtype, q.device, torch.zeros)
+        rc = _paged.attention(self._ctx, q, k_pages, v_pages, block_table, q_start, kv_len, out, lse, self._on(stream))
         if rc:
             _check(rc)
         return out
@@ -566,17 +515,7 @@ class PagedCache:
     def gather(self, k_pages, v_pages, block_table, kv_len, pos0, k_out, v_out, stream=None):
         """Rows [pos0, pos0 + n) of every request to k_out, v_out [batch][layers][n_kv_heads][n][128]
         (wi_paged_gather).  k_pages, v_pages: one pool, or [layers] of them."""
-        a, b = self._arg, kv_len.shape[0]
-        if k_out.dim() != 5:
-            raise ValueError("k_out must have shape [batch][layers][n_kv_heads][n][128]")
-        _, layers, _, n, _ = shape = k_out.shape
-        pool = self._pool if layers == 1 and k_pages.dim() == 4 else (layers, *self._pool)
-        if shape[0] != b or shape[2] != self.n_kv_heads or shape[4] != 128:
-            raise ValueError(f"k_out must have shape {(b, layers, self.n_kv_heads, n, 128)} (got {tuple(shape)})")
-        rc = lib.wi_paged_gather(
-            self.handle, b, layers, a("k_pages", k_pages, _BF16, pool), a("v_pages", v_pages, _BF16, pool),
-            self._table(block_table, b), a("kv_len", kv_len, _INT32, (b,)), pos0, n,
-            a("k_out", k_out, _BF16, shape), a("v_out", v_out, _BF16, shape), self._on(stream))
+        rc = _paged.gather(self._ctx, k_pages, v_pages, block_table, kv_len, pos0, k_out, v_out, self._on(stream))
         if rc:
             _check(rc)
         return k_out, v_out
@@ -586,6 +525,7 @@ class PagedCache:
 
     def free(self):
         if self.handle:
+            self._ctx = None
             lib.wi_paged_free(self.handle)
             self.handle = None
 

@@ -1,6 +1,7 @@
 """Build step of the CUDA library: nvcc, sm_103a only, objects compiled in parallel.
 
-Produces ``libwaveindex.so`` inside the package directory (in-tree, git-ignored).
+Produces ``libwaveindex.so`` and the extension module ``_paged.so`` (the paged cache's argument checks, host C++
+against this Python's torch) inside the package directory (in-tree, git-ignored).
 """
 from __future__ import annotations
 
@@ -15,6 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libwaveindex.so")
+EXT = os.path.join(PKG, "_paged.so")
 
 SOURCES = ["wi_api.cu", "wi_build.cu", "wi_decode.cu", "wi_dense.cu", "wi_assign_tc.cu", "wi_noalloc.cu",
            "wi_grow.cu", "wi_tier.cu", "wi_selftest.cu", "wi_paged_api.cu", "wi_paged.cu", "wi_paged_attn.cu"]
@@ -35,8 +37,37 @@ def _deps_mtime() -> float:
     return max(os.path.getmtime(f) for f in files)
 
 
+def _run(what: str, cmd: list[str]):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+
+
+def _compile_ext() -> str:
+    import sysconfig
+
+    from torch.utils import cpp_extension
+
+    obj = os.path.join(BUILD, "paged_binding.o")
+    dirs = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths()]
+    _run("g++ for paged_binding.cpp", ["g++", "-O2", "-std=c++17", "-fPIC", *[f"-I{d}" for d in dirs], "-c",
+                                       os.path.join(CSRC, "paged_binding.cpp"), "-o", obj])
+    return obj
+
+
+def _link_ext(obj: str):
+    from torch.utils import cpp_extension
+
+    dirs = cpp_extension.library_paths()
+    tmp = EXT + f".tmp{os.getpid()}"
+    _run("link of _paged.so", ["g++", "-shared", "-o", tmp, obj, f"-L{PKG}", "-l:libwaveindex.so", "-Wl,-rpath,$ORIGIN",
+                               *[f"-L{d}" for d in dirs], *[f"-Wl,-rpath,{d}" for d in dirs], "-ltorch_python",
+                               "-ltorch_cpu", "-lc10"])
+    os.replace(tmp, EXT)
+
+
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, EXT)):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -52,7 +83,8 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
             print(r.stdout, r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        ext = ex.submit(_compile_ext)
         objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-lpthread"]
@@ -60,6 +92,7 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_ext(ext.result())
     return LIB
 
 

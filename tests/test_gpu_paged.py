@@ -898,3 +898,16 @@ def test_write_then_attention_of_one_token_many_times(wi):
 
     a, b = loop(False), loop(True)
     assert torch.equal(a[0], b[0]) and all(torch.equal(u, v) for u, v in zip(a[1], b[1]))
+
+
+def test_a_freed_cache_refuses_its_calls(wi):
+    pc = wi.PagedCache(wi.make_paged_config(4, 2, 16, 8, 2, 4))
+    x = torch.zeros((8, 2, 16, 128), dtype=torch.bfloat16, device=DEV)
+    q = torch.zeros((1, 4, 128), dtype=torch.bfloat16, device=DEV)
+    args = (q, x, x.clone(), i32([[0] * 4]), i32([0, 1]), i32([1]))
+    pc.attention(*args)
+    pc.check()
+    pc.free()
+    with pytest.raises(ValueError, match="freed"):
+        pc.attention(*args)
+    pc.free()   # once more is no error

@@ -94,3 +94,30 @@ def test_config_layout_matches_binding(wi, tmp_path):
     assert int(out["size"]) == ctypes.sizeof(wi.wi_paged_config)
     for f in fields:
         assert int(out[f]) == getattr(wi.wi_paged_config, f).offset, f
+
+
+def test_python_calls_check_their_tensors_before_the_library(wi):
+    """The Python calls' checks, without a device: a context of handle 0 that no checked call reaches."""
+    import torch
+
+    from clustered_sparse_kv_gb300 import _paged
+    i = torch.zeros(4, dtype=torch.int32)
+    x = torch.zeros((4, 4, 128), dtype=torch.bfloat16)
+    ctx = _paged.context(0, 0, 4, 2, 16, 8, 4)
+    for c in (None, 3):
+        with pytest.raises(ValueError, match="freed"):
+            _paged.tables(c, i, i, i, i, i, i, i, i, i, i, 0)
+    with pytest.raises(TypeError, match="arguments"):
+        _paged.attention(ctx, x)
+    with pytest.raises(ValueError, match="ctx_len must be a tensor"):
+        _paged.tables(ctx, [1], i, i, i, i, i, i, i, i, i, 0)
+    with pytest.raises(ValueError, match="ctx_len .* on cuda:0 .*on cpu"):
+        _paged.tables(ctx, i, i, i, i, i, i, i, i, i, i, 0)
+    with pytest.raises(ValueError, match="dimension"):
+        _paged.tables(ctx, torch.zeros((), dtype=torch.int32), i, i, i, i, i, i, i, i, i, 0)
+    with pytest.raises(ValueError, match=r"q must be .*\(4, 4, 128\) .*on cpu"):
+        _paged.attention(ctx, x, x, x, i, i, i, x, None, 0)
+    with pytest.raises(ValueError, match="q must be .*contiguous heads"):
+        _paged.write(ctx, x.transpose(0, 1), x, x, i, i, x, x, x, None, None, 0)
+    with pytest.raises(ValueError, match="k_out must have shape"):
+        _paged.gather(ctx, x, x, i, i, 0, x, x, 0)
