@@ -32,44 +32,20 @@ __device__ __forceinline__ long long warp_scan64(long long v) {
   return v;
 }
 
-// Exclusive sums over the block of two values; 64 bits, since lengths that are in range each may add up to more.
-__device__ __forceinline__ void block_scan2(long long& a, long long& b, long long* tmp, long long* tot_a,
-                                            long long* tot_b) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int nw = kTabThreads / 32;
-  const long long ia = warp_scan64(a), ib = warp_scan64(b);
-  __syncthreads();
-  if (lane == 31) {
-    tmp[warp] = ia;
-    tmp[nw + warp] = ib;
-  }
-  __syncthreads();
-  long long ba = 0, bb = 0, ta = 0, tb = 0;
-#pragma unroll
-  for (int w = 0; w < nw; ++w) {
-    if (w == warp) {
-      ba = ta;
-      bb = tb;
-    }
-    ta += tmp[w];
-    tb += tmp[nw + w];
-  }
-  a = ba + ia - a;
-  b = bb + ib - b;
-  *tot_a = ta;
-  *tot_b = tb;
-}
-
 __global__ void __launch_bounds__(kTabThreads) k_paged_tables(WiPagedTables A, int page, int n_pages, int max_pages,
                                                              int* err) {
   extern __shared__ TabReq req[];  // [batch + 1]
-  __shared__ long long tmp[2 * (kTabThreads / 32)];
+  constexpr int kWarps = kTabThreads / 32;
+  __shared__ long long sum_t[kWarps], sum_p[kWarps];
+  __shared__ int sum_bad[kWarps];
   const int tid = threadIdx.x;
   pdl_trigger();
   pdl_wait();
   const int per = (A.batch + kTabThreads - 1) / kTabThreads;  // consecutive requests per thread
   const int b0 = min(tid * per, A.batch), b1 = min(b0 + per, A.batch);
-  const long long most = (long long)max_pages * page;
+  const long long most = (long long)max_pages * page;  // < 2^31
+  auto pages_of = [&](long long n) { return (int)(((unsigned)n + (unsigned)page - 1u) / (unsigned)page); };
+  const int free_now = *A.n_free;
   long long tokens = 0, pages = 0;
   int bad = 0;
   for (int b = b0; b < b1; ++b) {
@@ -78,14 +54,32 @@ __global__ void __launch_bounds__(kTabThreads) k_paged_tables(WiPagedTables A, i
       bad = 1;
     } else {
       tokens += n;
-      pages += (c + n + page - 1) / page - (c + page - 1) / page;
+      pages += pages_of(c + n) - pages_of(c);
     }
   }
-  long long all_tokens, all_pages;
-  long long at = tokens, first = pages;
-  block_scan2(at, first, tmp, &all_tokens, &all_pages);
-  const int free_now = *A.n_free;
-  int wrong = __syncthreads_or(bad) || all_tokens > A.n_tokens || free_now < 0 || free_now > A.free_cap
+  // exclusive sums over the block; 64 bits, since lengths that are in range each may add up to more
+  const int lane = tid & 31, warp = tid >> 5;
+  const long long it = warp_scan64(tokens), ip = warp_scan64(pages);
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 31) {
+    sum_t[warp] = it;
+    sum_p[warp] = ip;
+    sum_bad[warp] = bad;
+  }
+  __syncthreads();
+  long long at = it - tokens, first = ip - pages, all_tokens = 0, all_pages = 0;
+  bad = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w == warp) {
+      at += all_tokens;
+      first += all_pages;
+    }
+    all_tokens += sum_t[w];
+    all_pages += sum_p[w];
+    bad |= sum_bad[w];
+  }
+  int wrong = bad || all_tokens > A.n_tokens || free_now < 0 || free_now > A.free_cap
                   ? WI_DEVERR_BAD_LENGTH
                   : 0;
   if (all_pages > free_now) wrong |= WI_DEVERR_NO_PAGES;
@@ -100,7 +94,7 @@ __global__ void __launch_bounds__(kTabThreads) k_paged_tables(WiPagedTables A, i
       A.q_start[b] = wrong ? 0 : (int)at;
     }
     at += n;
-    first += (ctx + n + page - 1) / page - (ctx + page - 1) / page;
+    first += pages_of(ctx + n) - pages_of(ctx);
   }
   if (tid == 0) {
     req[A.batch] = {(int)all_tokens, (int)all_pages, 0};
@@ -122,7 +116,7 @@ __global__ void __launch_bounds__(kTabThreads) k_paged_tables(WiPagedTables A, i
         if (req[mid].q_start <= t) lo = mid; else hi = mid - 1;
       }
       pos = req[lo].ctx + (t - req[lo].q_start);
-      const int held = (int)(((long long)req[lo].ctx + page - 1) / page), j = pos / page;
+      const int held = pages_of(req[lo].ctx), j = pos / page;
       const int pg = j < held ? A.block_table[(long long)lo * max_pages + j]
                               : A.free_pages[free_now - 1 - (req[lo].first + j - held)];
       if (pg < 0 || pg >= n_pages) flags |= WI_DEVERR_BAD_PAGE;
@@ -137,7 +131,7 @@ __global__ void __launch_bounds__(kTabThreads) k_paged_tables(WiPagedTables A, i
       const int mid = (lo + hi + 1) >> 1;
       if (req[mid].first <= k) lo = mid; else hi = mid - 1;
     }
-    const int j = (int)(((long long)req[lo].ctx + page - 1) / page) + (k - req[lo].first);
+    const int j = pages_of(req[lo].ctx) + (k - req[lo].first);
     const int pg = A.free_pages[free_now - 1 - k];
     if (pg < 0 || pg >= n_pages) flags |= WI_DEVERR_BAD_PAGE;
     A.block_table[(long long)lo * max_pages + j] = pg;
@@ -369,6 +363,11 @@ __global__ void __launch_bounds__(kWrThreads, 3) k_paged_write(const __grid_cons
 constexpr int kGaThreads = 256;
 constexpr int kGaRows = 4;
 
+// a / b for a >= 0, b > 0; 64-bit division only where 32 bits do not do.
+__device__ __forceinline__ long long quot(long long a, int b) {
+  return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 __global__ void __launch_bounds__(kGaThreads) k_paged_gather(WiPagedGather A, long long rows, int Hkv, int page,
                                                             int n_pages, int max_pages, int* err) {
   constexpr int kStep = kGaThreads / 16;
@@ -377,7 +376,7 @@ __global__ void __launch_bounds__(kGaThreads) k_paged_gather(WiPagedGather A, lo
   const int l = threadIdx.x & 15;
   const int most = max_pages * page, n = (int)A.n;
   const long long r0 = (long long)blockIdx.x * (kStep * kGaRows);
-  const long long u0 = r0 / n;
+  const long long u0 = quot(r0, n);
   const unsigned i0 = (unsigned)(r0 - u0 * n) + (threadIdx.x >> 4);
   long long cur = -1, pool = 0;  // the unit of the last row, and where its layer's pool starts
   int b = 0, h = 0, len = 0, flags = 0;
@@ -395,19 +394,19 @@ __global__ void __launch_bounds__(kGaThreads) k_paged_gather(WiPagedGather A, lo
     }
     if (u != cur) {
       cur = u;
-      h = (int)(u % Hkv);
-      const long long bl = u / Hkv;
-      b = (int)(bl / A.layers);
-      pool = (bl % A.layers) * n_pages * (long long)Hkv * page;
+      const long long bl = quot(u, Hkv);
+      h = (int)(u - bl * Hkv);
+      b = (int)quot(bl, A.layers);
+      pool = (bl - (long long)b * A.layers) * n_pages * (long long)Hkv * page;
       len = A.kv_len[b];
       if (len < 0 || len > most) {
         flags |= WI_DEVERR_BAD_LENGTH;
         len = 0;
       }
     }
-    const int p = (int)A.pos0 + (int)i;
+    const int p = (int)A.pos0 + (int)i, j = p / page;
+    const int pg = A.block_table[(long long)b * max_pages + j];  // on its way beside the length: j < max_pages always
     if (p < len) {
-      const int j = p / page, pg = A.block_table[(long long)b * max_pages + j];
       if (pg < 0 || pg >= n_pages) {
         flags |= WI_DEVERR_BAD_PAGE;
       } else {
