@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         const bool masked = base + j * kRows + kRows - 1 > whole;
         const int seen = limit - base - j * kRows;  // the row sees columns 0 .. seen of this block
         if (masked) mask_scores(a, seen);
-        bool again = j == from;
+        bool again = j == from, grown = again;  // grown: this row takes a new reference (other rows keep theirs)
         for (;;) {
           if (again) {  // the first block, or the reference is far too small
             tmem_wait_st();
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
             tmem_ld32_nowait(ts + 96, b[1]);
             tmem_wait_ld();
             if (masked) mask_scores(b, seen - 64);
-            const float top = fmaxf(m, fmaxf(top_score(a), top_score(b)) * kScaleLog2);
+            const float top = grown ? fmaxf(m, fmaxf(top_score(a), top_score(b)) * kScaleLog2) : m;
             if (j != from) {
               // the chain's products so far are done: S of this block was issued behind them
               const float f = m == top ? 1.f : ex2(m - top);
@@ -642,7 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
           const uint64_t both = add2(sum[0], sum[1]);
           const float z = lo_of(both) + hi_of(both);
           // (a row that had seen nothing takes its reference from the first block that it sees something of)
-          if (again || !__any_sync(0xffffffffu, !(z <= kAgain) || (m == -INFINITY && z > 0.f))) {
+          grown = !(z <= kAgain) || (m == -INFINITY && z > 0.f);
+          if (again || !__any_sync(0xffffffffu, grown)) {
             l += z;
             break;
           }

@@ -911,3 +911,24 @@ def test_a_freed_cache_refuses_its_calls(wi):
     with pytest.raises(ValueError, match="freed"):
         pc.attention(*args)
     pc.free()   # once more is no error
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf, 3e38])
+def test_attention_rows_do_not_touch_each_other(wi, value):
+    """A token whose query is broken, or whose scores outgrow everything, leaves every other row's bits as they are."""
+    rng = np.random.default_rng(37)
+    kv = [700, 300]
+    table, n_pages = lay_out(kv, 16, rng)
+    k, v = (bf(rng.normal(size=(n_pages, 2, 16, 128)))[0] for _ in range(2))
+    q = bf(rng.normal(size=(151, 8, 128)))[0]
+    args = (k, v, i32(table), i32([0, 150, 151]), i32(kv))
+    pc = wi.PagedCache(wi.make_paged_config(8, 2, 16, n_pages, 2, table.shape[1]))
+    a = pc.attention(q, *args)
+    q2 = q.clone()
+    q2[77, 3] = value
+    b = pc.attention(q2, *args)
+    pc.check()
+    same = torch.ones((151, 8), dtype=torch.bool, device=DEV)
+    same[77, 3] = False
+    assert torch.equal(a[same], b[same]) and not torch.equal(a[77, 3], b[77, 3])
+    pc.free()
