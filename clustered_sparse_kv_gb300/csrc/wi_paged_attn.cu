@@ -10,10 +10,10 @@
 // 128 positions run from 0 to the last position that a row sees.  A unit is
 // one block of one item, or one of four more for its start and end; all units
 // of the call, item after item, are cut into equal runs, one per CTA (one CTA
-// per SM), so single tokens over long
-// contexts split over the machine and ragged chunks balance without a plan
-// made on the host.  Lengths live on the device: each CTA sums the units of
-// all requests itself (closed form per request) and finds its run's start.
+// per SM), so single tokens over long contexts split over the machine and
+// ragged chunks balance without a plan made on the host.  Lengths live on the
+// device: each CTA sums the units of all requests itself (closed form per
+// request) and finds its run's start.
 // An item cut between CTAs leaves partial results (maximum, sum, O) in the
 // scratch, added up in CTA order: by the last of its CTAs where the call has
 // eight rows per kv head at most (single tokens of one request), else by
@@ -38,6 +38,19 @@
 // product.  In blocks that not every row sees whole, rows behind the request's
 // end are zeroed in shared memory, and so are infinite and NaN elements, which
 // the end of the item then adds to the rows that do see them.
+//
+// What bounds it, 32 query and 8 kv heads on one GB300.  Chunks: the tensor
+// pipe, 72% active while a CTA runs; 2048 tokens behind 14K positions 316 us,
+// 1630 TFLOP/s, 0.87 of the measured bf16 peak (behind 129K 2.7 - 2.9 ms, 0.81
+// - 0.86; run for seconds, under the power cap, 3.1 - 3.3 ms).  Each role is
+// kept short: one thread computing the operands of tcgen05.mma under a branch
+// took 3345 of 4230 cycles a block (hence mma_bf16_warp), a maximum of every
+// block and two threads to a row 1750 cycles of softmax where 1100 do.  The
+// code's size matters as much: loops that were unrolled further, or a form of
+// its own for tiles of few rows, slowed every other loop of the kernel.
+// Single tokens: HBM; 131K positions in pages of 16 in 90 - 98 us, 5.5 - 6.0
+// TB/s, of which the start takes 6, the reads 70 (7.6 TB/s) and the merge of
+// twenty parts per head 5.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -61,7 +74,7 @@ constexpr int kFixWarps = 2;
 constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
 constexpr float kLn2 = 0.6931471805599453f;
 // Units in front of an item's blocks, for what its start and end cost (8192 fresh tokens, 32 / 8 heads: 542, 502, 466,
-// 439, 444 us at 1, 2, 3, 4, 6; longer contexts and single tokens do not care).
+// 439, 444 us at 1, 2, 3, 4, 6 in an earlier form; longer contexts and single tokens do not care).
 constexpr int kLead = 4;
 // A row's weights are 2^(score - m) with m the row's maximum in the first block of its part, which no later block needs
 // to know its own maximum for: only when a block's weights add up to more than this (one of them is 2^9 at least), or to
@@ -970,9 +983,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         if (j < from) continue;
         const int s = at.s;
         // only once the copy has been asked for does the stage's phase stand at this use
-        if (!(ok = mbar_wait(&sm.to_fix[s], (fix_par >> s) & 1u, P.err))) break;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.to_fix[s], (fix_par >> s) & 1u, P.err)))) break;
         fix_par ^= 1u << s;
-        if (!(ok = mbar_wait(&sm.full[s], at.par, P.err))) break;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[s], at.par, P.err)))) break;
         const int k0 = (w.b0 + j) * kRows, seen = w.r.kv - k0;  // rows of the block that the request holds
         uint4* v = reinterpret_cast<uint4*>(sm.ring[s]);  // [16 groups][2][8 rows][8 pieces]
         bool found = false;
