@@ -53,11 +53,11 @@ struct TcSmem {
   uint64_t tmem_full[2], tmem_empty[2];
   uint32_t tmem_base;
   int abort_flag;
-  unsigned char pad[3072 - (kGroups - 1) * kTM * 6 - (2 * kStagesA + 6) * 8 - 8];
+  unsigned char pad[3 * 1024 - (kGroups - 1) * kTM * 6 - (2 * kStagesA + 6) * 8 - 8];
   unsigned char b[kBBytes];                 // [k half][Cs rows][128 B]
   unsigned char a[kStagesA][kATileBytes];   // [k half][128 rows][128 B]
 };
-static_assert(offsetof(TcSmem, b) == 3072, "tile region must start 1024-byte aligned");
+static_assert(offsetof(TcSmem, b) == 3 * 1024, "tile region must start 1024-byte aligned");
 
 struct TcParams {
   int32_t* assign;

@@ -125,11 +125,11 @@ struct Smem {
   Cursor start;             // of the run
   Req req;                  // start.b's
   float xch[2][2][kRows];   // maximum and sum of a row, from chain to chain: [chain][m, l]
-  unsigned char pad[3072 - (4 * kStages + 9) * 8 - 4 - 32 - 4 - kThreads / 32 * 8 - 24 - 20 - 16 - 4 * kRows * 4];
+  unsigned char pad[3 * 1024 - (4 * kStages + 9) * 8 - 4 - 32 - 4 - kThreads / 32 * 8 - 24 - 20 - 16 - 4 * kRows * 4];
   unsigned char q[2][kTileBytes];          // [k half][128 rows][128 B]
   unsigned char ring[kStages][kTileBytes]; // [group of 8 rows][k half][8 rows][128 B]
 };
-static_assert(offsetof(Smem, q) == 3072, "tiles must start 1024-byte aligned");
+static_assert(offsetof(Smem, q) == 3 * 1024, "tiles must start 1024-byte aligned");
 static_assert(sizeof(Smem) <= 232448, "shared memory");
 
 // A position in the ring: the stage, and the parity of its current use.

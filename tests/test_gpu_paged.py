@@ -932,3 +932,164 @@ def test_attention_rows_do_not_touch_each_other(wi, value):
     same[77, 3] = False
     assert torch.equal(a[same], b[same]) and not torch.equal(a[77, 3], b[77, 3])
     pc.free()
+
+
+def test_captured_behind_copies_and_joins(wi):
+    """In a graph: behind a memory copy, behind a fork and a join of two streams, and the same eagerly behind events:
+    each kernel may be scheduled early, and still waits for what it reads."""
+    rng = np.random.default_rng(38)
+    hq, hkv, page, n = 8, 2, 16, 300
+    table, n_pages = lay_out([2300, 40], page, rng)
+    cfg = wi.make_paged_config(hq, hkv, page, n_pages, 2, table.shape[1])
+    bf16 = dict(dtype=torch.bfloat16, device=DEV)
+    src = bf(rng.normal(size=(n, (hq + 2 * hkv) * 128)))[0]
+    old = [bf(rng.normal(size=(n_pages, hkv, page, 128)))[0] for _ in range(2)]
+    slots = np.concatenate([[table[0, p // page] * page + p % page for p in range(2000, 2299)], [table[1, 2] * page + 7]])
+    pos = np.concatenate([np.arange(2000, 2299), [39]])
+    args = (i32(table), i32([0, 299, 300]), i32([2299, 40]))
+    pos, slots = i32(pos), i32(slots)
+
+    def make():
+        s = {"pc": wi.PagedCache(cfg), "x": torch.zeros_like(src), "pools": [torch.zeros_like(o) for o in old],
+             "q": torch.zeros((n, hq, 128), **bf16), "out": torch.zeros((n, hq, 128), **bf16),
+             "rows": [torch.zeros((2, 1, hkv, 40, 128), **bf16) for _ in range(2)]}
+        return s
+
+    def step(s, main, side):
+        for a, b in zip(s["pools"], old):
+            a.copy_(b)
+        s["x"].copy_(src)                                   # a copy, not a kernel
+        q, k, v = s["x"].split([hq * 128, hkv * 128, hkv * 128], 1)
+        s["pc"].write(q.view(n, hq, 128), k.view(n, hkv, 128), v.view(n, hkv, 128), pos, slots, *s["pools"], s["q"])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            s["pc"].gather(*s["pools"], args[0], args[2], 0, *s["rows"])
+        s["pc"].attention(s["q"], *s["pools"], *args, out=s["out"])
+        main.wait_stream(side)
+        # behind the join: over what both branches left
+        s["pc"].gather(*s["pools"], args[0], args[2], 0, *s["rows"])
+
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    eager, captured = make(), make()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        step(eager, main, side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        step(captured, main, side)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    plain = make()                                          # one call at a time
+    for a, b in zip(plain["pools"], old):
+        a.copy_(b)
+    q, k, v = src.split([hq * 128, hkv * 128, hkv * 128], 1)
+    for call in (lambda: plain["pc"].write(q.view(n, hq, 128), k.view(n, hkv, 128), v.view(n, hkv, 128), pos, slots,
+                                           *plain["pools"], plain["q"]),
+                 lambda: plain["pc"].attention(plain["q"], *plain["pools"], *args, out=plain["out"]),
+                 lambda: plain["pc"].gather(*plain["pools"], args[0], args[2], 0, *plain["rows"])):
+        torch.cuda.synchronize()
+        call()
+    torch.cuda.synchronize()
+    for s in (eager, captured):
+        s["pc"].check()
+        assert torch.equal(s["q"], plain["q"]) and torch.equal(s["out"], plain["out"])
+        for k in ("pools", "rows"):
+            assert all(torch.equal(a, b) for a, b in zip(s[k], plain[k]))
+    del graph
+    for s in (eager, captured, plain):
+        s["pc"].free()
+
+
+def test_written_tokens_feed_the_decode_step(wi):
+    """Steps of an index whose query and new row a cache's write makes just before, back to back and (without the
+    appended row: an appending step is not for a graph) captured, equal the same steps taken one call at a time."""
+    rng = np.random.default_rng(39)
+    hq, hkv, batch, ctx, steps = 8, 2, 2, 1024, 12
+    cfg = wi.make_config(batch, 1, hq, hkv, ctx, seg_len=512, clusters_per_seg=32, iters=2, max_append=2 * steps,
+                         budget_k=8)
+    ks, vs = (bf(rng.normal(size=(batch, 1, hkv, ctx, 128)))[0] for _ in range(2))
+    xs = [bf(rng.normal(size=(batch, (hq + 2 * hkv) * 128)))[0] for _ in range(steps)]
+    f = freqs(128)
+    results = []
+    for wait, append in ((True, True), (False, True), (True, False), ("graph", False)):
+        pc = wi.PagedCache(wi.make_paged_config(hq, hkv, 16, 4, batch, 4, inv_freq=f))
+        ix = wi.WaveIndex.build(cfg, ks.clone(), vs.clone())  # a build reorders the rows in place
+        qn = torch.zeros((batch, hq, 128), dtype=torch.bfloat16, device=DEV)
+        kn, vn = (torch.zeros((batch, hkv, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        pos, at = [i32([ctx + i] * batch) for i in range(steps)], i32([0] * batch)
+        buf = torch.zeros_like(xs[0])
+
+        def step(x, at):
+            q, k, v = x.split([hq * 128, hkv * 128, hkv * 128], 1)
+            pc.write(q.view(batch, hq, 128), k.view(batch, hkv, 128), v.view(batch, hkv, 128), at, None, kn, vn, qn)
+            if wait is True:
+                torch.cuda.synchronize()
+            return ix.decode(qn, kn, vn) if append else ix.decode(qn)
+
+        outs = []
+        if wait == "graph":
+            side = torch.cuda.Stream()
+            torch.cuda.synchronize()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=side):
+                out = step(buf, at)
+            for x, p in zip(xs, pos):
+                buf.copy_(x)
+                at.copy_(p)
+                graph.replay()
+                outs.append(out.clone())
+            torch.cuda.synchronize()
+            del graph
+        else:
+            outs = [step(x, p).clone() for x, p in zip(xs, pos)]
+        torch.cuda.synchronize()
+        ix.check()
+        pc.check()
+        results.append(torch.stack(outs))
+        ix.free()
+        pc.free()
+    assert results[0].isfinite().all() and results[2].isfinite().all() and not torch.equal(results[0], results[2])
+    assert torch.equal(results[0], results[1]) and torch.equal(results[2], results[3])
+
+
+def test_largest_batch(wi):
+    """4096 requests in one call of each operator that takes a batch, every fifth of them without a token."""
+    rng = np.random.default_rng(40)
+    batch, hq, hkv, page, width = 4096, 2, 1, 16, 3
+    n_pages = batch * width
+    kv = rng.integers(0, page * (width - 1), size=batch)
+    new = np.where(np.arange(batch) % 5 == 4, 0, rng.integers(1, 4, size=batch))
+    pc = wi.PagedCache(wi.make_paged_config(hq, hkv, page, n_pages, batch, width))
+    order = rng.permutation(n_pages)
+    have = -(-kv // page)
+    table = np.full((batch, width), -1)
+    at = 0
+    for b in range(batch):
+        table[b, :have[b]] = order[at:at + have[b]]
+        at += have[b]
+    n = int(new.sum())
+    t = {k: i32([0] * s) for k, s in (("kv", batch), ("qs", batch + 1), ("slots", n), ("pos", n), ("left", 1))}
+    T = i32(table)
+    pc.tables(i32(kv), i32(new), i32(order[at:]), i32([n_pages - at]), T, t["kv"], t["qs"], t["slots"], t["pos"], t["left"])
+    pc.check()
+    pools, F = zip(*(bf(rng.normal(size=(n_pages, hkv, page, 128))) for _ in range(2)))
+    q, Q = bf(rng.normal(size=(n, hq, 128)))
+    out = f64(pc.attention(q, *pools, T, t["qs"], t["kv"]))
+    pc.check()
+    TT, qs = T.cpu().numpy(), np.concatenate([[0], np.cumsum(new)])
+    assert (t["qs"].cpu().numpy() == qs).all() and (t["kv"].cpu().numpy() == kv + new).all()
+    for b in range(batch):
+        total = kv[b] + new[b]
+        K, V = (x.reshape(n_pages, page, 128)[TT[b, :-(-total // page)]].reshape(-1, 128)[:total] for x in F)
+        for i in range(new[b]):
+            see = kv[b] + i + 1
+            s = Q[qs[b] + i] @ K[:see].T / np.sqrt(128)
+            p = np.exp(s - s.max(1, keepdims=True))
+            p /= p.sum(1, keepdims=True)
+            # weights and result are rounded to bf16, each by at most half a step (2^-8); a score of at most 30 in 32
+            # bits is off by 128 2^-24 30 = 2^-12.1 at most, its weight by twice that
+            bound = (2.0 ** -7 + 2.0 ** -11) * (p @ np.abs(V[:see])) + 1e-6
+            assert (np.abs(out[qs[b] + i] - p @ V[:see]) <= bound).all(), b
+    pc.free()
