@@ -152,13 +152,17 @@ __global__ void __launch_bounds__(kTabThreads) k_paged_tables(WiPagedTables A, i
 //   a' = (a / rms) (w_a cos) - (b / rms) (w_b sin), b' likewise,
 // in packed fp32; the four sums of squares that a lane group has in flight are
 // reduced together (each of sixteen lanes ends with a quarter of them).  The
-// first rows are loaded before the token's position and slot are known (the
-// rows of a padding token exist too), every batch while the one before it is
-// worked on.  8192 tokens of 32 + 8 + 8 heads: 38.1 us (5.3 TB/s); with the
-// operations one by one, a row to sixteen lanes, instruction issue bounds it
-// (194 instructions for two rows, 48 us).
-constexpr int kWrThreads = 256;
-constexpr int kWrPerSm = 16;    // warps per SM that a launch aims at (1531 tokens: 11.5, 9.5, 10.7 us at 8, 16, 24)
+// rows come through shared memory, kWrStages batches ahead; the first are
+// asked for before the token's position and slot are known (the rows of a
+// padding token exist too).  8192 tokens of 32 + 8 + 8 heads: 34.1 us (5.9
+// TB/s; 35.1 and 34.7 with two and four stages); with the next batch in
+// registers, which left no room for more warps, 38.1; with the operations one
+// by one, a row to sixteen lanes, instruction issue bounds it (194 instructions
+// for two rows, 48 us).
+constexpr int kWrThreads = 128;
+constexpr int kWrStages = 3;
+constexpr int kWrBatch = 8 * WI_D * 2;  // bytes of a batch
+constexpr int kWrPerSm = 16;    // warps per SM that a launch aims at (1531 tokens: 12.2, 8.6, 10.0 us at 8, 16, 24)
 
 __device__ __forceinline__ uint64_t pair2(float a, float b) {
   uint64_t x;
@@ -193,7 +197,7 @@ __device__ __forceinline__ uint64_t swap2(uint64_t x) {
 
 // INTER: pairs (2i, 2i + 1).  FULL: the whole head is rotated (no lane holds elements that are only scaled).
 template <bool INTER, bool FULL>
-__global__ void __launch_bounds__(kWrThreads, 3) k_paged_write(const __grid_constant__ WiPagedWrite A,
+__global__ void __launch_bounds__(kWrThreads, 6) k_paged_write(const __grid_constant__ WiPagedWrite A,
                                                               const __grid_constant__ WiRope R, int Hq, int Hkv, int page,
                                                               int n_slots, float eps, int parts, int* err) {
   const int lane = threadIdx.x & 31, l = lane & 15, row1 = lane >> 4;
@@ -206,28 +210,36 @@ __global__ void __launch_bounds__(kWrThreads, 3) k_paged_write(const __grid_cons
   const int half = R.rotary >> 1, bq = (Hq + 7) >> 3, bk = (Hkv + 7) >> 3, batches = bq + 2 * bk;
   const bool turned = FULL || (INTER ? 8 * l < R.rotary : 4 * l < half);
   const int o0 = !INTER && turned ? 4 * l : 8 * l, o1 = !INTER && turned ? 4 * l + half : 8 * l + 4;
-  uint2 xa[4], xb[4];
-  auto fetch = [&](int i) {
-    const int kind = i < bq ? 0 : i < bq + bk ? 1 : 2;
-    const int h0 = 8 * (kind == 0 ? i : kind == 1 ? i - bq : i - bq - bk) + row1;
-    const bf16* from = kind == 0   ? static_cast<const bf16*>(A.q) + (long long)t * A.q_stride
-                       : kind == 1 ? static_cast<const bf16*>(A.k) + (long long)t * A.k_stride
-                                   : static_cast<const bf16*>(A.v) + (long long)t * A.v_stride;
-    const int H = kind == 0 ? Hq : Hkv;
-    from += h0 * WI_D;
+  // kWrStages batches of this warp are on their way or worked on; a row that does not exist is left as it is and
+  // touches no other
+  __shared__ __align__(16) unsigned char rows[kWrThreads / 32][kWrStages][kWrBatch];
+  unsigned char* const mine = rows[threadIdx.x >> 5][0];
+  auto fetch = [&](int i, int stage) {
+    if (i < batches) {
+      const int kind = i < bq ? 0 : i < bq + bk ? 1 : 2;
+      const int h0 = 8 * (kind == 0 ? i : kind == 1 ? i - bq : i - bq - bk) + row1;
+      const bf16* from = (kind == 0   ? static_cast<const bf16*>(A.q) + (long long)t * A.q_stride
+                          : kind == 1 ? static_cast<const bf16*>(A.k) + (long long)t * A.k_stride
+                                      : static_cast<const bf16*>(A.v) + (long long)t * A.v_stride) +
+                         h0 * WI_D + 8 * l;
+      const int H = kind == 0 ? Hq : Hkv;
+      const uint32_t to = smem_addr(mine) + stage * kWrBatch + row1 * (kWrBatch / 8) + 16 * l;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      xa[k] = xb[k] = make_uint2(0u, 0u);
-      if (h0 + 2 * k < H) {
-        xa[k] = *reinterpret_cast<const uint2*>(from + 2 * k * WI_D + o0);
-        xb[k] = *reinterpret_cast<const uint2*>(from + 2 * k * WI_D + o1);
-      }
+      for (int k = 0; k < 4; ++k)
+        if (h0 + 2 * k < H)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k * (kWrBatch / 4)), "l"(from + 2 * k * WI_D)
+                       : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (part < batches) fetch(part);
+#pragma unroll
+  for (int s = 0; s < kWrStages - 1; ++s) fetch(part + s * parts, s);
   const int pos = A.positions[t];
   int slot = A.slots ? A.slots[t] : t;
-  if (pos < 0) return;  // padding
+  if (pos < 0) {  // padding
+    asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives its warp
+    return;
+  }
   if (A.slots && slot >= n_slots) {
     if (lane == 0) atomicOr(err, WI_DEVERR_BAD_PAGE);
     slot = -1;
@@ -261,14 +273,14 @@ __global__ void __launch_bounds__(kWrThreads, 3) k_paged_write(const __grid_cons
   const long long k_at = (A.slots ? (long long)(slot / page) * Hkv * page + slot % page : (long long)slot * Hkv) * WI_D;
   uint64_t ca[2], cb[2], sa[2], sb[2];  // factors of a in a', of b in b', of a in b', of b in a'
   int have = -1;
+  int stage = 0;
   for (int i = part; i < end; i += parts) {
-    uint2 ya[4], yb[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      ya[k] = xa[k];
-      yb[k] = xb[k];
-    }
-    if (i + parts < end) fetch(i + parts);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kWrStages - 2) : "memory");
+    __syncwarp();  // the batch has come for every lane, and none reads the one before it any longer
+    const int ahead = i + (kWrStages - 1) * parts;
+    fetch(ahead < end ? ahead : batches, stage == 0 ? kWrStages - 1 : stage - 1);
+    const unsigned char* const here = mine + stage * kWrBatch + row1 * (kWrBatch / 8);
+    stage = stage + 1 == kWrStages ? 0 : stage + 1;
     const int kind = i < bq ? 0 : i < bq + bk ? 1 : 2;
     const int h0 = 8 * (kind == 0 ? i : kind == 1 ? i - bq : i - bq - bk) + row1;
     const int H = kind == 0 ? Hq : Hkv;
@@ -276,76 +288,88 @@ __global__ void __launch_bounds__(kWrThreads, 3) k_paged_write(const __grid_cons
                          : static_cast<bf16*>(kind == 1 ? A.k_out : A.v_out) + k_at + h0 * k_step;
     const long long step = 2 * (kind == 0 ? (long long)WI_D : k_step);
     const int pairs = (min(8, H - (h0 - row1)) + 1) >> 1;  // rows of the batch, two by two
-    if (kind < 2) {
-      const bf16* w = static_cast<const bf16*>(kind == 0 ? A.q_weight : A.k_weight);
-      if (kind != have) {
-        have = kind;
-        float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
-        if (w) {
-          load_bf16x4(w + o0, wa);
-          load_bf16x4(w + o1, wb);
-        }
+    if (kind == 2) {  // a copy
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (INTER) {  // a = (x0, x1), (x2, x3): both groups hold whole pairs, turned with their own neighbour
-            ca[k] = pair2(wa[2 * k] * cs[k], wa[2 * k + 1] * cs[k]);
-            sa[k] = pair2(-wa[2 * k + 1] * sn[k], wa[2 * k] * sn[k]);
-            cb[k] = pair2(wb[2 * k] * cs[2 + k], wb[2 * k + 1] * cs[2 + k]);
-            sb[k] = pair2(-wb[2 * k + 1] * sn[2 + k], wb[2 * k] * sn[2 + k]);
-          } else {
-            ca[k] = pair2(wa[2 * k] * cs[2 * k], wa[2 * k + 1] * cs[2 * k + 1]);
-            cb[k] = pair2(wb[2 * k] * cs[2 * k], wb[2 * k + 1] * cs[2 * k + 1]);
-            sa[k] = pair2(wa[2 * k] * sn[2 * k], wa[2 * k + 1] * sn[2 * k + 1]);
-            sb[k] = pair2(-wb[2 * k] * sn[2 * k], -wb[2 * k + 1] * sn[2 * k + 1]);
-          }
-        }
-      }
-      float inv[4] = {1.f, 1.f, 1.f, 1.f};
+      for (int k = 0; k < 4; ++k)
+        if (h0 + 2 * k < H)
+          *reinterpret_cast<uint4*>(to + k * step + 8 * l) =
+              *reinterpret_cast<const uint4*>(here + k * (kWrBatch / 4) + 16 * l);
+      continue;
+    }
+    uint2 ya[4], yb[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      ya[k] = *reinterpret_cast<const uint2*>(here + k * (kWrBatch / 4) + 2 * o0);
+      yb[k] = *reinterpret_cast<const uint2*>(here + k * (kWrBatch / 4) + 2 * o1);
+    }
+    const bf16* w = static_cast<const bf16*>(kind == 0 ? A.q_weight : A.k_weight);
+    if (kind != have) {
+      have = kind;
+      float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
       if (w) {
-        float v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[k] = 0.f;
-          if (k >= pairs) continue;
-          const uint64_t a0 = unpack2(ya[k].x), a1 = unpack2(ya[k].y), b0 = unpack2(yb[k].x), b1 = unpack2(yb[k].y);
-          const float2 ss = unpair(fma2(a0, a0, fma2(a1, a1, fma2(b0, b0, mul2(b1, b1)))));
-          v[k] = ss.x + ss.y;
-        }
-        const bool up8 = l & 8, up4 = l & 4;
-        float s0 = up8 ? v[0] : v[2], s1 = up8 ? v[1] : v[3];
-        float k0 = up8 ? v[2] : v[0], k1 = up8 ? v[3] : v[1];
-        k0 += __shfl_xor_sync(0xffffffffu, s0, 8);
-        k1 += __shfl_xor_sync(0xffffffffu, s1, 8);
-        float r = (up4 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, up4 ? k0 : k1, 4);
-        r += __shfl_xor_sync(0xffffffffu, r, 2);
-        r += __shfl_xor_sync(0xffffffffu, r, 1);
-        r = rsqrtf(r * (1.f / WI_D) + eps);  // of the row that lanes 4k .. 4k + 3 summed
-#pragma unroll
-        for (int k = 0; k < 4; ++k) inv[k] = __shfl_sync(0xffffffffu, r, (lane & 16) + 4 * k);
+        load_bf16x4(w + o0, wa);
+        load_bf16x4(w + o1, wb);
       }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (INTER) {  // a = (x0, x1), (x2, x3): both groups hold whole pairs, turned with their own neighbour
+          ca[k] = pair2(wa[2 * k] * cs[k], wa[2 * k + 1] * cs[k]);
+          sa[k] = pair2(-wa[2 * k + 1] * sn[k], wa[2 * k] * sn[k]);
+          cb[k] = pair2(wb[2 * k] * cs[2 + k], wb[2 * k + 1] * cs[2 + k]);
+          sb[k] = pair2(-wb[2 * k + 1] * sn[2 + k], wb[2 * k] * sn[2 + k]);
+        } else {
+          ca[k] = pair2(wa[2 * k] * cs[2 * k], wa[2 * k + 1] * cs[2 * k + 1]);
+          cb[k] = pair2(wb[2 * k] * cs[2 * k], wb[2 * k + 1] * cs[2 * k + 1]);
+          sa[k] = pair2(wa[2 * k] * sn[2 * k], wa[2 * k + 1] * sn[2 * k + 1]);
+          sb[k] = pair2(-wb[2 * k] * sn[2 * k], -wb[2 * k + 1] * sn[2 * k + 1]);
+        }
+      }
+    }
+    float inv[4] = {1.f, 1.f, 1.f, 1.f};
+    if (w) {
+      float v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        v[k] = 0.f;
         if (k >= pairs) continue;
-        uint64_t a[2] = {unpack2(ya[k].x), unpack2(ya[k].y)}, b[2] = {unpack2(yb[k].x), unpack2(yb[k].y)};
-        if (w) {
-          const uint64_t f = pair2(inv[k], inv[k]);
+        const uint64_t a0 = unpack2(ya[k].x), a1 = unpack2(ya[k].y), b0 = unpack2(yb[k].x), b1 = unpack2(yb[k].y);
+        const float2 ss = unpair(fma2(a0, a0, fma2(a1, a1, fma2(b0, b0, mul2(b1, b1)))));
+        v[k] = ss.x + ss.y;
+      }
+      const bool up8 = l & 8, up4 = l & 4;
+      float s0 = up8 ? v[0] : v[2], s1 = up8 ? v[1] : v[3];
+      float k0 = up8 ? v[2] : v[0], k1 = up8 ? v[3] : v[1];
+      k0 += __shfl_xor_sync(0xffffffffu, s0, 8);
+      k1 += __shfl_xor_sync(0xffffffffu, s1, 8);
+      float r = (up4 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, up4 ? k0 : k1, 4);
+      r += __shfl_xor_sync(0xffffffffu, r, 2);
+      r += __shfl_xor_sync(0xffffffffu, r, 1);
+      r = rsqrtf(r * (1.f / WI_D) + eps);  // of the row that lanes 4k .. 4k + 3 summed
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            a[c] = mul2(a[c], f);
-            b[c] = mul2(b[c], f);
-          }
-        }
-        uint32_t ra[2], rb[2];
+      for (int k = 0; k < 4; ++k) inv[k] = __shfl_sync(0xffffffffu, r, (lane & 16) + 4 * k);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= pairs) continue;
+      uint64_t a[2] = {unpack2(ya[k].x), unpack2(ya[k].y)}, b[2] = {unpack2(yb[k].x), unpack2(yb[k].y)};
+      if (w) {
+        const uint64_t f = pair2(inv[k], inv[k]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint64_t pa = INTER ? swap2(a[c]) : b[c], pb = INTER ? swap2(b[c]) : a[c];
-          if (!FULL && !turned) pa = pb = 0;  // nothing of the partner, an infinite one included
-          ra[c] = repack2(fma2(a[c], ca[c], mul2(pa, INTER ? sa[c] : sb[c])));
-          rb[c] = repack2(fma2(b[c], cb[c], mul2(pb, INTER ? sb[c] : sa[c])));
+          a[c] = mul2(a[c], f);
+          b[c] = mul2(b[c], f);
         }
-        ya[k] = make_uint2(ra[0], ra[1]);
-        yb[k] = make_uint2(rb[0], rb[1]);
       }
+      uint32_t ra[2], rb[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint64_t pa = INTER ? swap2(a[c]) : b[c], pb = INTER ? swap2(b[c]) : a[c];
+        if (!FULL && !turned) pa = pb = 0;  // nothing of the partner, an infinite one included
+        ra[c] = repack2(fma2(a[c], ca[c], mul2(pa, INTER ? sa[c] : sb[c])));
+        rb[c] = repack2(fma2(b[c], cb[c], mul2(pb, INTER ? sb[c] : sa[c])));
+      }
+      ya[k] = make_uint2(ra[0], ra[1]);
+      yb[k] = make_uint2(rb[0], rb[1]);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -354,6 +378,7 @@ __global__ void __launch_bounds__(kWrThreads, 3) k_paged_write(const __grid_cons
         *reinterpret_cast<uint2*>(to + k * step + o1) = yb[k];
       }
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- gather
