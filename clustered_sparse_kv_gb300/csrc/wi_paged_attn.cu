@@ -16,8 +16,10 @@
 // request) and finds its run's start.
 // An item cut between CTAs leaves partial results (maximum, sum, O) in the
 // scratch, added up in CTA order: by the last of its CTAs where the call has
-// eight rows per kv head at most (single tokens of one request), else by
-// k_paged_merge, which spreads the rows over the machine.
+// 32 rows per kv head at most (single tokens of a few requests, a few tokens
+// of one), else by k_paged_merge, which spreads the rows over the machine.
+// (Eight tokens over 1000 positions: 13.8 and 26.7 us, over 131K 94 and 121,
+// eight requests' single tokens over 4000 34.4 and 38.3.)
 //
 // A CTA (384 threads) processes its items' blocks in roles:
 //   warps 0-3, 4-7  softmax, one thread per row of chain 0 / chain 1
@@ -76,6 +78,9 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Units in front of an item's blocks, for what its start and end cost (8192 fresh tokens, 32 / 8 heads: 542, 502, 466,
 // 439, 444 us at 1, 2, 3, 4, 6 in an earlier form; longer contexts and single tokens do not care).
 constexpr int kLead = 4;
+// One request of few rows is not cut up to this many blocks: a merge costs 4 us, a block behind the first 0.7 (five
+// tokens over 305 positions 10.6 us whole, 12.4 cut; one over 500 11.3 and 12.1, over 800 15.7 and 12.9).
+constexpr int kWhole = 4;
 // A row's weights are 2^(score - m) with m the row's maximum in the first block of its part, which no later block needs
 // to know its own maximum for: only when a block's weights add up to more than this (one of them is 2^9 at least), or to
 // no number, the block is done again with the maximum so far, and O rescaled.  Weights below 2^16 cost neither bf16 nor
@@ -83,9 +88,10 @@ constexpr int kLead = 4;
 constexpr float kAgain = 65536.f;
 
 // A partial result: m, then l, of every row, then O, column-major (a thread owns a row, so column-major stores of a
-// warp are contiguous).  Two tiles of 128 rows, or, where a call has no more, one of kMergeHere: those of all CTAs lie
-// within 1.3 MB then, which the merge of single tokens reads with fewer address translations.
-constexpr int kMergeHere = 8;  // rows per kv head of a call up to which the attention kernel merges itself
+// warp are contiguous).  Two tiles of 128 rows, or, where a call has no more, one of kMergeHere or kFewRows: those of
+// all CTAs lie within 5 or 1.3 MB then, which a merge reads with fewer address translations.
+constexpr int kFewRows = 8;
+constexpr int kMergeHere = 32;  // rows per kv head of a call up to which the attention kernel merges itself
 struct Parts {
   float* base;
   int rows, tiles;
@@ -446,6 +452,75 @@ __device__ __noinline__ void merge_some(const Params& P, const Split& sp, int c0
     }
 }
 
+// COLS columns from d0 on of row r of tile t, added up: the parts four at a time, every load of them issued before the
+// first is used, with the running maximum (ONCE: no more than four).  A lane to a row, as they were written; ROWS,
+// TILES: the parts' layout.
+constexpr int kWideParts = 4;
+template <int COLS>
+struct Merged {
+  float M, L, acc[COLS];
+};
+template <int COLS, int ROWS, int TILES, bool ONCE = false>
+__device__ __forceinline__ Merged<COLS> merge_wide(const Params& P, const Split& sp, int c0, int t, int r, int d0) {
+  constexpr int kAtOnce = kWideParts;
+  const int parts = sp.last - c0 + 1;
+  Merged<COLS> x = {-INFINITY, 0.f, {}};
+#pragma unroll 1
+  for (int i0 = 0; i0 < (ONCE ? 1 : parts); i0 += kAtOnce) {
+    float m[kAtOnce], l[kAtOnce], o[kAtOnce][COLS];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      m[k] = -INFINITY;
+      l[k] = 0.f;
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) o[k][c] = 0.f;
+      if (i0 + k < parts) {
+        const float* p = part_of(P, c0, i0 + k) + r;
+        m[k] = __ldcg(p + t * ROWS);
+        l[k] = __ldcg(p + (TILES + t) * ROWS);
+        p += (2 * TILES + t * WI_D + d0) * ROWS;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) o[k][c] = __ldcg(p + c * ROWS);
+      }
+    }
+    float top = x.M;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, m[k]);
+    const float ref = top == -INFINITY ? 0.f : top, f = ex2(x.M - ref);
+    x.M = top;
+    x.L *= f;
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) x.acc[c] *= f;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const float g = ex2(m[k] - ref);
+      x.L += g * l[k];
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) x.acc[c] += g * o[k][c];
+    }
+  }
+  const float inv = x.L == 0.f ? 0.f : 1.f / x.L;
+#pragma unroll
+  for (int c = 0; c < COLS; ++c) x.acc[c] *= inv;
+  return x;
+}
+
+// All rows (32 at most) of an item of one tile by the softmax warps, sixteen columns each.
+__device__ __noinline__ void merge_tile(const Params& P, const Split& sp, int c0) {
+  constexpr int kCols = WI_D / kSoftWarps;
+  const int r = threadIdx.x & 31, d0 = (threadIdx.x >> 5) * kCols;
+  if (r >= tile_rows(P, sp, 0)) return;
+  const Merged<kCols> x = merge_wide<kCols, kMergeHere, 1>(P, sp, c0, 0, r, d0);
+  const long long at = place_of(P, sp, 0, r);
+  uint4* out = reinterpret_cast<uint4*>(static_cast<bf16*>(P.a.out) + at * WI_D + d0);
+#pragma unroll
+  for (int i = 0; i < kCols / 8; ++i) {
+    const float* a = x.acc + 8 * i;
+    out[i] = make_uint4(pack2(a[0], a[1]), pack2(a[2], a[3]), pack2(a[4], a[5]), pack2(a[6], a[7]));
+  }
+  if (P.a.lse && d0 == 0) P.a.lse[at] = x.L == 0.f ? -INFINITY : x.M * kLn2 + logf(x.L);
+}
+
 __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_constant__ CUtensorMap map_q,
                                                                 const __grid_constant__ CUtensorMap map_k,
                                                                 const __grid_constant__ CUtensorMap map_v,
@@ -531,7 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     if (blockIdx.x == 0 && tid == 0) atomicOr(P.err, WI_DEVERR_BAD_LENGTH);
     total = 0;
   }
-  const int ctas = (int)min((long long)gridDim.x, total);
+  int ctas = (int)min((long long)gridDim.x, total);
+  if (P.tickets && P.a.batch == 1 && ctas > P.Hkv && total <= (long long)P.Hkv * (kLead + kWhole)) ctas = P.Hkv;
   if ((int)blockIdx.x >= ctas) {  // fewer units than CTAs (the whole CTA leaves)
     if (tid == 0) P.splits[blockIdx.x].last = -1;
     if (warp == kSoftWarps + 1)
@@ -758,9 +834,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         soft_barrier();
         if (sm.last) {
           const Split sp = {w.r.s0 + w.tile * w.tp, w.kh, w.cnt, c1};
+          if (P.parts.rows > kFewRows) {
+            merge_tile(P, sp, c0);
+          } else {
 #pragma unroll 1
-          for (int r0 = 0; r0 < tile_rows(P, sp, 0); r0 += 2 * kSoftWarps * 32 / WI_D)
-            merge_some<kSoftWarps * 32>(P, sp, c0, 0, r0);
+            for (int r0 = 0; r0 < tile_rows(P, sp, 0); r0 += 2 * kSoftWarps * 32 / WI_D)
+              merge_some<kSoftWarps * 32>(P, sp, c0, 0, r0);
+          }
         }
       } else if (part && w.b0 == 0 && tid == 0) {
         split = true;
@@ -1022,11 +1102,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
   }
 }
 
-// The merge as a kernel of its own: a block takes 32 rows of one cut item.  What counts is latency.  Up to kMergeWide
-// parts are read with a lane to a row, as they were written, every load issued before the first is used, and turned in
-// shared memory for the way out; more parts eight rows at a time.
+// The merge as a kernel of its own: a block takes 32 rows of one cut item.  What counts is latency.  The rows are turned
+// in shared memory for the way out; where there are few, more threads share one.
 constexpr int kMergeRows = 32;
-constexpr int kMergeWide = 4;
+
+// Row base + lane of the tile, eight columns to a warp, to `to` in bf16.
+template <bool ONCE>
+__device__ __forceinline__ void merge_row(const Params& P, const Split& sp, int c0, int t, int base, bf16* to) {
+  const int r = base + (threadIdx.x & 31), warp = threadIdx.x >> 5;
+  const Merged<8> y = merge_wide<8, kRows, 2, ONCE>(P, sp, c0, t, r, warp * 8);
+  uint4 x;
+  x.x = pack2(y.acc[0], y.acc[1]);
+  x.y = pack2(y.acc[2], y.acc[3]);
+  x.z = pack2(y.acc[4], y.acc[5]);
+  x.w = pack2(y.acc[6], y.acc[7]);
+  *reinterpret_cast<uint4*>(to) = x;
+  if (P.a.lse && warp == 0 && r < tile_rows(P, sp, t))
+    P.a.lse[place_of(P, sp, t, r)] = y.L == 0.f ? -INFINITY : y.M * kLn2 + logf(y.L);
+}
+
+__device__ __noinline__ void merge_row_of_many(const Params& P, const Split& sp, int c0, int t, int base, bf16* to) {
+  merge_row<false>(P, sp, c0, t, base, to);
+}
 
 __global__ void __launch_bounds__(kMergeThreads, 2) k_paged_merge(const __grid_constant__ Params P) {
   __shared__ __align__(16) bf16 turn[kMergeRows][WI_D + 8];
@@ -1034,55 +1131,24 @@ __global__ void __launch_bounds__(kMergeThreads, 2) k_paged_merge(const __grid_c
   const int c0 = blockIdx.x;
   const Split sp = P.splits[c0];
   if (sp.last < 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, parts = sp.last - c0 + 1;
   const int t = blockIdx.y / (kRows / kMergeRows), base = blockIdx.y % (kRows / kMergeRows) * kMergeRows;
   const int rows = tile_rows(P, sp, t);
   if (base >= rows) return;
-  if (parts > kMergeWide) {
-    for (int r0 = base; r0 < rows && r0 < base + kMergeRows; r0 += 2 * kMergeThreads / WI_D)
-      merge_some<kMergeThreads>(P, sp, c0, t, r0);
+  bf16* const to = &turn[threadIdx.x & 31][(threadIdx.x >> 5) * 8];  // (rows behind the last are read, and not stored)
+  if (sp.last - c0 < kWideParts) {
+    merge_row<true>(P, sp, c0, t, base, to);
+  } else if (rows - base <= kFewRows) {
+    for (int r0 = base; r0 < rows; r0 += 2 * kMergeThreads / WI_D) merge_some<kMergeThreads>(P, sp, c0, t, r0);
     return;
+  } else {
+    merge_row_of_many(P, sp, c0, t, base, to);
   }
-  const int r = base + lane, d0 = warp * 8;  // sixteen warps take eight columns each
-  float m[kMergeWide], l[kMergeWide], o[kMergeWide][8];
-#pragma unroll
-  for (int i = 0; i < kMergeWide; ++i) {
-    m[i] = -INFINITY;
-    l[i] = 0.f;
-    if (i < parts) {
-      const float* p = part_of(P, c0, i);
-      m[i] = __ldcg(p + P.parts.m(t, r));
-      l[i] = __ldcg(p + P.parts.l(t, r));
-#pragma unroll
-      for (int k = 0; k < 8; ++k) o[i][k] = __ldcg(p + P.parts.o(t, d0 + k, r));
-    }
-  }
-  float M = m[0], L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 1; i < kMergeWide; ++i) M = fmaxf(M, m[i]);
-  const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-  for (int i = 0; i < kMergeWide; ++i)
-    if (i < parts) {
-      const float f = ex2(m[i] - ref);
-      L += l[i] * f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] += o[i][k] * f;
-    }
-  const float inv = L == 0.f ? 0.f : 1.f / L;
-  uint4 x;
-  x.x = pack2(acc[0] * inv, acc[1] * inv);
-  x.y = pack2(acc[2] * inv, acc[3] * inv);
-  x.z = pack2(acc[4] * inv, acc[5] * inv);
-  x.w = pack2(acc[6] * inv, acc[7] * inv);
-  *reinterpret_cast<uint4*>(&turn[lane][d0]) = x;
   __syncthreads();
   static_assert(kMergeThreads / 32 * 8 == WI_D && kMergeThreads / 16 == kMergeRows, "thread maps");
   const int q = threadIdx.x >> 4, c = (threadIdx.x & 15) * 8;  // sixteen threads store a row
   if (base + q < rows)
     *reinterpret_cast<uint4*>(static_cast<bf16*>(P.a.out) + place_of(P, sp, t, base + q) * WI_D + c) =
         *reinterpret_cast<const uint4*>(&turn[q][c]);
-  if (P.a.lse && warp == 0 && r < rows) P.a.lse[place_of(P, sp, t, r)] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
 }
 
 }  // namespace
@@ -1106,11 +1172,12 @@ cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a
   // a box of a block lies inside one page: the largest power of two that divides the page, 128 at most
   P.box = g.page & -g.page;
   if (P.box > kRows) P.box = kRows;
-  const bool here = (long long)a.n_tokens * g.G <= kMergeHere;
+  const long long rows_here = (long long)a.n_tokens * g.G;
+  const bool here = rows_here <= kMergeHere;
   P.tickets = here ? static_cast<unsigned*>(scratch) : nullptr;
   P.splits = reinterpret_cast<Split*>(static_cast<char*>(scratch) + kPagedTicketBytes);
   P.parts = {reinterpret_cast<float*>(static_cast<char*>(scratch) + kPagedTicketBytes + kSplitBytes),
-             here ? kMergeHere : kRows, here ? 1 : 2};
+             rows_here <= kFewRows ? kFewRows : here ? kMergeHere : kRows, here ? 1 : 2};
   P.err = err;
   CUtensorMap map_q, map_k, map_v;
   const unsigned long long rows = (unsigned long long)g.n_pages * g.Hkv * g.page;

@@ -1093,3 +1093,14 @@ def test_largest_batch(wi):
             bound = (2.0 ** -7 + 2.0 ** -11) * (p @ np.abs(V[:see])) + 1e-6
             assert (np.abs(out[qs[b] + i] - p @ V[:see]) <= bound).all(), b
     pc.free()
+
+
+@pytest.mark.parametrize("hq,hkv,new,kv", [
+    (32, 8, [5], [305]), (32, 8, [1], [512]), (32, 8, [1], [513]), (32, 8, [8], [512]), (32, 8, [8], [514]),   # one request whole and cut
+    (64, 64, [1], [300]), (200, 200, [2], [400]), (8, 1, [4], [6000]), (28, 4, [4], [5000]), (4, 1, [8], [20000]),
+    (32, 8, [2, 3, 0, 1], [900, 4000, 0, 9]), (6, 2, [1] * 10, [700] * 10), (32, 8, [8], [1]),       # 32 rows and fewer
+    (32, 8, [9], [300]), (4, 1, [9], [20000]), (28, 4, [5, 30, 1], [4000, 9000, 3000]), (8, 8, [33], [7000]),  # and more
+    (4, 2, [130, 17, 2], [5000, 2500, 9000])])
+def test_attention_parts_of_few_and_many_rows(wi, hq, hkv, new, kv):
+    """Items cut into a few or dozens of parts, of one to 128 rows, merged in the kernel or by one of its own."""
+    attention_case(wi, hq, hkv, 16, new, [max(a, b) for a, b in zip(kv, new)], seed=sum(kv) + sum(new))
