@@ -1104,3 +1104,12 @@ def test_largest_batch(wi):
 def test_attention_parts_of_few_and_many_rows(wi, hq, hkv, new, kv):
     """Items cut into a few or dozens of parts, of one to 128 rows, merged in the kernel or by one of its own."""
     attention_case(wi, hq, hkv, 16, new, [max(a, b) for a, b in zip(kv, new)], seed=sum(kv) + sum(new))
+
+
+@pytest.mark.parametrize("hq,hkv,new,kv", [
+    (32, 8, [1] * 32, [700] * 32), (32, 8, [1] * 33, [700] * 33), (28, 4, [1] * 18, [2500] * 18), (12, 2, [1] * 21, [1500] * 21),
+    (4, 1, [20] + [0] * 19, [6000] + [0] * 19), (4, 1, [0] * 5 + [30, 2] + [0] * 25, [50] * 5 + [9000, 4000] + [0] * 25),
+    (8, 2, [3, 0, 5, 0, 1, 0, 2, 1, 0, 0, 4, 0], [2000] * 12), (1, 1, [1] * 128, [500] * 128), (1, 1, [128] + [0] * 127, [3000] + [0] * 127)])
+def test_attention_no_more_tokens_than_requests(wi, hq, hkv, new, kv):
+    """Steps of single tokens, and calls that look like one by their sizes while some requests have several tokens."""
+    attention_case(wi, hq, hkv, 16, new, kv, seed=sum(kv) + len(new))
