@@ -42,8 +42,8 @@
 // the end of the item then adds to the rows that do see them.
 //
 // What bounds it, 32 query and 8 kv heads on one GB300.  Chunks: the tensor
-// pipe, 72% active while a CTA runs; 2048 tokens behind 14K positions 316 us,
-// 1630 TFLOP/s, 0.87 of the measured bf16 peak (behind 129K 2.7 - 2.9 ms, 0.81
+// pipe, 72% active while a CTA runs; 2048 tokens behind 14K positions 318 us,
+// 1620 TFLOP/s, 0.86 of the measured bf16 peak (behind 129K 2.7 - 2.9 ms, 0.81
 // - 0.86; run for seconds, under the power cap, 3.1 - 3.3 ms).  Each role is
 // kept short: one thread computing the operands of tcgen05.mma under a branch
 // took 3345 of 4230 cycles a block (hence mma_bf16_warp), a maximum of every
