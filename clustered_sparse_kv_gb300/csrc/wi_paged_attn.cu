@@ -42,8 +42,8 @@
 // the end of the item then adds to the rows that do see them.
 //
 // What bounds it, 32 query and 8 kv heads on one GB300.  Chunks: the tensor
-// pipe, 72% active while a CTA runs; 2048 tokens behind 14K positions 318 us,
-// 1620 TFLOP/s, 0.86 of the measured bf16 peak (behind 129K 2.7 - 2.9 ms, 0.81
+// pipe, 72% active while a CTA runs; 2048 tokens behind 14K positions 316 - 322 us,
+// 1600 - 1630 TFLOP/s, 0.85 - 0.87 of the measured bf16 peak (behind 129K 2.7 - 2.9 ms, 0.81
 // - 0.86; run for seconds, under the power cap, 3.1 - 3.3 ms).  Each role is
 // kept short: one thread computing the operands of tcgen05.mma under a branch
 // took 3345 of 4230 cycles a block (hence mma_bf16_warp), a maximum of every
@@ -130,8 +130,9 @@ struct Smem {
   int spare;
   Cursor start;             // of the run
   Req req;                  // start.b's
+  Req reqs[kSoftWarps];     // of the softmax warps' segments
   float xch[2][2][kRows];   // maximum and sum of a row, from chain to chain: [chain][m, l]
-  unsigned char pad[3 * 1024 - (4 * kStages + 9) * 8 - 4 - 32 - 4 - kThreads / 32 * 8 - 24 - 20 - 16 - 4 * kRows * 4];
+  unsigned char pad[3 * 1024 - (4 * kStages + 9) * 8 - 4 - 32 - 4 - kThreads / 32 * 8 - 24 - 20 - 16 - 4 * kRows * 4 - kSoftWarps * 16];
   unsigned char q[2][kTileBytes];          // [k half][128 rows][128 B]
   unsigned char ring[kStages][kTileBytes]; // [group of 8 rows][k half][8 rows][128 B]
 };
@@ -234,7 +235,6 @@ struct Walk : Cursor {
     tp = 2 * P.tq;
     set(q);
   }
-  __device__ __forceinline__ Walk(const Params& P, const Cursor& c) : Walk(P, c, load_req(P, c.b)) {}
   __device__ __forceinline__ void set(const Req& q) {
     r = q;
     p0 = (long long)r.kv - r.n;
@@ -661,22 +661,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     uint32_t s_par = 0, o_par0 = 0, o_par1 = 0;
     bool ok = true;  // after one timed-out wait the warp waits no more and writes nothing, but meets every barrier
     bool split = false;  // the run's last item goes on in the next CTA
-    // Only the cursor lives through a segment's blocks, beside the scores; the rest is worked out again behind them.
-    Cursor cur = sm.start;
-    for (int seg = 0;; ++seg) {
-      int nb, step, from, base, limit, whole;
-      {
-        Walk w(P, cur);
-        if (!w.next(P)) break;
-        cur = w;
-        const int own_tile = w.single ? 0 : chain, ti = w.tile * w.tp + own_tile * P.tq + tok;
-        limit = tok < P.tq && ti < w.r.n ? (int)(w.p0 + ti) : -1;     // the last position that the row sees
-        whole = (int)(w.p0 + w.tile * w.tp + own_tile * P.tq);       // ... that all rows of the tile see
-        nb = w.nb;
-        step = w.single ? 2 : 1;
-        from = w.single ? chain : 0;
-        base = w.b0 * kRows;
-      }
+    // Only the cursor and what the blocks need live through a segment, beside the scores; the rest is worked out again
+    // behind them, from the request as the warp keeps it in shared memory.  The next segment begins with the walk that
+    // ended the last one (64 single tokens over 1000 positions: 76.0 us with the request read at both ends, now 72.9).
+    Cursor cur;
+    int nb, step, from, base, limit, whole;
+    auto begin = [&](Walk& w) {
+      const bool more = w.next(P);
+      cur = w;
+      if (lane == 0) sm.reqs[warp] = w.r;
+      __syncwarp();
+      const int own_tile = w.single ? 0 : chain, ti = w.tile * w.tp + own_tile * P.tq + tok;
+      limit = tok < P.tq && ti < w.r.n ? (int)(w.p0 + ti) : -1;     // the last position that the row sees
+      whole = (int)(w.p0 + w.tile * w.tp + own_tile * P.tq);       // ... that all rows of the tile see
+      nb = w.nb;
+      step = w.single ? 2 : 1;
+      from = w.single ? chain : 0;
+      base = w.b0 * kRows;
+      return more;
+    };
+    bool more;
+    {
+      Walk w(P, sm.start, sm.req);
+      more = begin(w);
+    }
+    for (int seg = 0; more; ++seg) {
       float m = -INFINITY, l = 0.f;  // the row's reference maximum and its sum
       for (int j = from; j < nb; j += step) {
         if (ok) ok = mbar_wait(&sm.s_full[chain], s_par, P.err);
@@ -745,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       }
 
       // ---- the segment's end: maximum and sum over both chains where they had one tile, then O
-      Walk w(P, cur);
+      Walk w(P, cur, sm.reqs[warp]);
       w.next(P);
       const int own_tile = w.single ? 0 : chain, ti = w.tile * w.tp + own_tile * P.tq + tok;
       const bool live = tok < P.tq && ti < w.r.n;
@@ -849,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       }
       if (w.single) soft_barrier();  // both chains' O, maxima and sums have been read
       w.advance();
-      cur = w;
+      more = begin(w);
     }
     if (tid == 0 && !split) P.splits[blockIdx.x].last = -1;
   } else if (warp == kSoftWarps) {
