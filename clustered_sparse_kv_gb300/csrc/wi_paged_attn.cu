@@ -740,8 +740,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
           weights(b[1], ts + 48, ref, sum);
           const uint64_t both = add2(sum[0], sum[1]);
           const float z = lo_of(both) + hi_of(both);
-          // (a row that had seen nothing takes its reference from the first block that it sees something of)
-          grown = !(z <= kAgain) || (m == -INFINITY && z > 0.f);
+          // (a row without a reference, every score so far minus infinity, looks for one in each block that it sees
+          // something of: against 0 its weights might all vanish)
+          grown = !(z <= kAgain) || (seen >= 0 && m == -INFINITY);
           if (again || !__any_sync(0xffffffffu, grown)) {
             l += z;
             break;

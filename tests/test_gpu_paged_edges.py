@@ -1,0 +1,69 @@
+"""Corners of the paged cache on the GPU: scores of minus infinity, rows that no token owns, bad offsets, handles and
+streams.  Tolerances as tests/test_gpu_paged.py derives them."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged
+from test_gpu_paged import DEV, bf, f64, i32, lay_out
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def wi():
+    import clustered_sparse_kv_gb300 as m
+    return m
+
+
+# ------------------------------------------------------------ scores of minus infinity ----
+
+@pytest.mark.parametrize("hq,hkv,batch,new,kv,hidden", [
+    (4, 1, 1, 1, 380, 128),        # one tile, whole: the first block of one of its two chains
+    (4, 1, 1, 1, 380, 256),        # ... of both
+    (4, 1, 1, 40, 900, 128),       # two tiles, a block to a CTA
+    (4, 1, 200, 40, 900, 128),     # two tiles, whole and cut at any block
+    (4, 1, 200, 40, 900, 300),
+    (8, 2, 1, 1, 20000, 12000),    # one tile, cut into many parts, some of which see nothing else
+    (8, 2, 40, 1, 20000, 12000),   # ... into parts of several blocks
+    (4, 1, 30, 300, 3000, 1500),   # several pairs of tiles
+    (7, 1, 150, 20, 700, 300),     # rows that no token owns in every tile
+    (4, 1, 100, 300, 300, 128),    # rows that see hidden positions only: as if they saw nothing
+])
+def test_attention_behind_scores_of_minus_infinity(wi, hq, hkv, batch, new, kv, hidden):
+    """Keys with an element of minus infinity at positions 0 .. hidden - 1, which every query weights with nothing, and
+    logits around -100 behind them: far below what 32 bits hold as a weight on their own.  The requests of a call are
+    alike and share their pages."""
+    rng = np.random.default_rng(kv + hidden)
+    page = 16
+    table, n_pages = lay_out([kv], page, rng)
+    base = rng.normal(size=128)
+    base[5] = 0.0
+    base *= np.sqrt(128) / np.linalg.norm(base)
+    q = np.broadcast_to(base * 3, (new, hq, 128)) + 0.3 * rng.normal(size=(new, hq, 128))
+    q[..., 5] = 1.0
+    rows = -base * 2.95 + 0.3 * rng.normal(size=(hkv, kv, 128))     # 3 * -2.95 * 128 / sqrt(128) = -100
+    rows[:, :hidden, 5] = -np.inf
+    rows[:, hidden:, 5] = 0.0
+    Kp, Vp = np.zeros((n_pages, hkv, page, 128)), rng.normal(size=(n_pages, hkv, page, 128))
+    for p in range(kv):
+        Kp[table[0, p // page], :, p % page] = rows[:, p]
+    (q, Q), (k, K), (v, V) = bf(q), bf(Kp), bf(Vp)
+    pc = wi.PagedCache(wi.make_paged_config(hq, hkv, page, n_pages, batch, table.shape[1]))
+    lse = torch.empty((batch * new, hq), device=DEV)
+    out = pc.attention(q.repeat(batch, 1, 1), k, v, i32(table.repeat(batch, 0)), i32(np.arange(batch + 1) * new),
+                       i32([kv] * batch), lse=lse)
+    pc.check()
+    pc.free()
+    out, lse = f64(out).reshape(batch, new, hq, 128), f64(lse).reshape(batch, new, hq)
+    ref, rlse, spread = paged.attention(Q, K, V, table, [0, new], [kv])
+    finite = np.where(np.isfinite(K), K, 0)
+    top = np.linalg.norm(Q, axis=-1) * np.sqrt((finite ** 2).sum(-1).max()) / np.sqrt(128)
+    ds = 128 * 2.0 ** -24 * top + 2.0 ** -20
+    tol = 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -7) * spread * (2.0 ** -8 + 2 * ds + kv * 2.0 ** -23)[..., None]
+    assert (np.abs(out - ref) <= tol).all()
+    none = np.arange(new) + kv - new < hidden
+    assert (ref[none] == 0).all() and (rlse[none] == -np.inf).all() and (lse[:, none] == -np.inf).all()
+    assert (rlse[~none] < -80).all()
+    ltol = ds + kv * 2.0 ** -24 + 2.0 ** -22 * np.abs(np.where(np.isfinite(rlse), rlse, 0)) + 2.0 ** -20
+    assert (np.abs(lse[:, ~none] - rlse[~none]) <= ltol[~none]).all()
