@@ -740,9 +740,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
           weights(b[1], ts + 48, ref, sum);
           const uint64_t both = add2(sum[0], sum[1]);
           const float z = lo_of(both) + hi_of(both);
-          // (a row without a reference, every score so far minus infinity, looks for one in each block that it sees
-          // something of: against 0 its weights might all vanish)
-          grown = !(z <= kAgain) || (seen >= 0 && m == -INFINITY);
+          // A row without a reference (every score so far minus infinity) looks for one in each block that it sees
+          // something of: against 0 its weights might all vanish.  A row that sees nothing of the block, or that no token
+          // owns, asks for nothing, whatever its query holds.
+          grown = seen >= 0 && (!(z <= kAgain) || m == -INFINITY);
           if (again || !__any_sync(0xffffffffu, grown)) {
             l += z;
             break;

@@ -67,3 +67,38 @@ def test_attention_behind_scores_of_minus_infinity(wi, hq, hkv, batch, new, kv, 
     assert (rlse[~none] < -80).all()
     ltol = ds + kv * 2.0 ** -24 + 2.0 ** -22 * np.abs(np.where(np.isfinite(rlse), rlse, 0)) + 2.0 ** -20
     assert (np.abs(lse[:, ~none] - rlse[~none]) <= ltol[~none]).all()
+
+
+# ------------------------------------------------------------ rows that no token owns ----
+
+def test_attention_does_not_wait_for_rows_that_no_token_owns(wi):
+    """NaN in the queries behind the last token: the same bits in the tokens' rows, and no block of theirs done twice
+    (2040 tokens behind 14K positions took 1.4 times as long, 446 us to 320)."""
+    rng = np.random.default_rng(50)
+    hq, hkv, page, new, kv, n = 32, 8, 128, 2040, 16384, 2048
+    table, n_pages = lay_out([kv], page, rng)
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(50)
+    k, v, q = (torch.randn(s, generator=gen, device=DEV, dtype=torch.bfloat16)
+               for s in ((n_pages, hkv, page, 128), (n_pages, hkv, page, 128), (n, hq, 128)))
+    pc = wi.PagedCache(wi.make_paged_config(hq, hkv, page, n_pages, 1, table.shape[1]))
+    args = (k, v, i32(table), i32([0, new]), i32([kv]))
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    qs = [q.clone(), q.clone()]
+    qs[0][new:] = 0
+    qs[1][new:] = float("nan")
+    times = [[], []]
+    for turn in range(12):
+        for s in range(2):
+            e = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+            e[0].record()
+            for _ in range(5):
+                pc.attention(qs[s], *args, out=outs[s])
+            e[1].record()
+            torch.cuda.synchronize()
+            times[s].append(e[0].elapsed_time(e[1]))
+    pc.check()
+    pc.free()
+    assert torch.equal(outs[0], outs[1]) and (outs[0][new:] == 0).all()
+    zero, nan = (float(np.median(t[2:])) for t in times)
+    assert nan < 1.2 * zero, (zero, nan)
