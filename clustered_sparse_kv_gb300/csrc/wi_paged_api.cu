@@ -129,6 +129,13 @@ int geom_from_config(const wi_paged_config* c, WiPagedGeom* g) {
   return WI_OK;
 }
 
+// Zeros, there when the call returns: a memset is queued on the default stream, which the streams of later calls need
+// not wait for.
+cudaError_t clear(void* p, size_t bytes) {
+  const cudaError_t e = cudaMemset(p, 0, bytes);
+  return e != cudaSuccess ? e : cudaStreamSynchronize(cudaStreamLegacy);
+}
+
 void destroy(wi_paged* pc) {
   if (pc->err) cudaFree(pc->err);
   if (pc->scratch) cudaFree(pc->scratch);
@@ -151,7 +158,7 @@ int create_impl(const wi_paged_config* cfg, wi_paged** out) {
   pc->sms = sms;
   if (cudaMalloc(reinterpret_cast<void**>(&pc->err), 4) != cudaSuccess ||
       cudaMalloc(&pc->scratch, wi_paged_attention_scratch(sms)) != cudaSuccess ||
-      cudaMemset(pc->err, 0, 4) != cudaSuccess || cudaMemset(pc->scratch, 0, kPagedTicketBytes) != cudaSuccess) {
+      clear(pc->err, 4) != cudaSuccess || clear(pc->scratch, kPagedTicketBytes) != cudaSuccess) {
     cudaGetLastError();
     destroy(pc);
     return fail(WI_ENOMEM, "device allocation failed");
@@ -180,8 +187,8 @@ int wi_paged_check(wi_paged* pc) {
   int herr = 0;
   WI_CUDA(cudaMemcpy(&herr, pc->err, 4, cudaMemcpyDeviceToHost));
   if (!herr) return WI_OK;
-  WI_CUDA(cudaMemset(pc->err, 0, 4));
-  if (herr & WI_DEVERR_MBAR_TIMEOUT) WI_CUDA(cudaMemset(pc->scratch, 0, kPagedTicketBytes));  // tickets left behind
+  WI_CUDA(clear(pc->err, 4));
+  if (herr & WI_DEVERR_MBAR_TIMEOUT) WI_CUDA(clear(pc->scratch, kPagedTicketBytes));  // tickets left behind
   return fail(WI_EDEVICE, "paged cache (flags 0x%x):%s%s%s%s", herr,
               herr & WI_DEVERR_BAD_PAGE ? " a page or slot outside the pool;" : "",
               herr & WI_DEVERR_BAD_LENGTH ? " a length or offset out of range;" : "",

@@ -423,7 +423,8 @@ typedef struct {
   const double* inv_freq; /* host, rotary_dim / 2 angles per position (radians), copied; NULL if none */
 } wi_paged_config;
 
-/* Make a handle on the current device (allocates the attention's scratch, about 270 KB per SM). */
+/* Make a handle on the current device (allocates the attention's scratch, about 270 KB per SM, and waits for the
+ * default stream, on which it is cleared: the handle may be used on any stream at once). */
 int wi_paged_create(const wi_paged_config* cfg, wi_paged** out);
 
 /* Synchronise the device and report what kernels of this handle's calls found wrong

@@ -102,3 +102,47 @@ def test_attention_does_not_wait_for_rows_that_no_token_owns(wi):
     assert torch.equal(outs[0], outs[1]) and (outs[0][new:] == 0).all()
     zero, nan = (float(np.median(t[2:])) for t in times)
     assert nan < 1.2 * zero, (zero, nan)
+
+
+# ------------------------------------------------------------ handles and streams ----
+
+def test_a_new_cache_is_ready_for_every_stream(wi):
+    """A cache made while the default stream is busy, over memory that was not zero, and used at once on a stream that
+    does not wait for the default one: its tickets and error word are clear when the call that makes it returns."""
+    rng = np.random.default_rng(51)
+    kv, side = 20000, torch.cuda.Stream()
+    table, n_pages = lay_out([kv], 16, rng)
+    q, k, v = (bf(rng.normal(size=s))[0] for s in ((1, 8, 128), (n_pages, 2, 16, 128), (n_pages, 2, 16, 128)))
+    args = (q, k, v, i32(table), i32([0, 1]), i32([kv]))
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    dirt = torch.full((1 << 26,), -1, dtype=torch.int32, device=DEV)
+    torch.cuda.synchronize()
+    del dirt
+    torch.cuda.empty_cache()
+    torch.cuda._sleep(400_000_000)          # about 0.2 s of work on the default stream
+    pc = wi.PagedCache(wi.make_paged_config(8, 2, 16, n_pages, 1, table.shape[1]))
+    assert torch.cuda.default_stream().query()   # what clears them stands behind that work, and has been waited for
+    pc.attention(*args, out=outs[0], stream=side)
+    side.synchronize()
+    pc.check()
+    pc.attention(*args, out=outs[1])
+    pc.check()
+    pc.free()
+    assert torch.equal(*outs) and (outs[0] != 0).any()
+
+
+def test_a_reported_error_is_cleared_before_the_next_call(wi):
+    """The check that reports an error clears it before it returns: one that a call on another stream meets right
+    behind it is kept."""
+    pc = wi.PagedCache(wi.make_paged_config(1, 1, 16, 4, 1, 4))
+    side = torch.cuda.Stream()
+    k, out = (torch.ones((4, 1, 16, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    v, out2 = k.clone(), out.clone()
+    bad, kv = i32([[0, 9, 9, 9]]), i32([64])
+    for _ in range(20):
+        for stream in (None, side):
+            pc.gather(k, v, bad, kv, 0, out.view(1, 1, 1, 64, 128), out2.view(1, 1, 1, 64, 128), stream=stream)
+            with pytest.raises(wi.WiError, match="page or slot"):
+                pc.check()
+    pc.check()
+    pc.free()
