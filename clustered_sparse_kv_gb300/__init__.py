@@ -145,7 +145,10 @@ def _new_on(stream, shape, dtype, device, make=torch.empty):
     if stream is None:
         return make(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
+        # handles 0 and 1 are the default stream, which torch does not take as an external one (0 gives a stream of
+        # its pool, which the call's stream does not wait for)
+        h = int(stream)
+        stream = torch.cuda.ExternalStream(h, device) if h > 1 else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return make(shape, dtype=dtype, device=device)
 

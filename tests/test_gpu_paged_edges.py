@@ -146,3 +146,35 @@ def test_a_reported_error_is_cleared_before_the_next_call(wi):
                 pc.check()
     pc.check()
     pc.free()
+
+
+def test_outputs_are_made_on_the_stream_that_a_handle_names(wi):
+    """An output that a call makes itself belongs to the call's stream, given as an object or as a handle; 0 is the
+    default stream, also while another one is current."""
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    for stream, want in ((None, 0), (0, 0), (1, 0), (torch.cuda.default_stream(), 0), (side, side.cuda_stream),
+                         (side.cuda_stream, side.cuda_stream)):
+        made = []
+
+        def make(shape, dtype, device):
+            made.append(torch.cuda.current_stream().cuda_stream)
+            return torch.empty(shape, dtype=dtype, device=device)
+
+        wi._new_on(stream, (4,), torch.float32, torch.device(DEV), make)
+        if stream is not None:
+            with torch.cuda.stream(other):
+                wi._new_on(stream, (4,), torch.float32, torch.device(DEV), make)
+        assert made == [want] * len(made), (stream, made, want)
+    rng = np.random.default_rng(52)
+    table, n_pages = lay_out([700], 16, rng)
+    q, k, v = (bf(rng.normal(size=s))[0] for s in ((40, 8, 128), (n_pages, 2, 16, 128), (n_pages, 2, 16, 128)))
+    pc = wi.PagedCache(wi.make_paged_config(8, 2, 16, n_pages, 1, table.shape[1]))
+    args = (q, k, v, i32(table), i32([0, 30]), i32([700]))
+    want = pc.attention(*args)
+    for stream in (0, 1, side.cuda_stream):
+        torch.cuda.synchronize()
+        got = pc.attention(*args, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    pc.check()
+    pc.free()
