@@ -100,6 +100,10 @@ struct Reader {
     if (ok && rows < batch) fail("block_table must have a row for each of the " + std::to_string(batch) + " requests");
     return static_cast<int32_t*>(data("block_table", o, kInt32, {rows, c->max_pages}));
   }
+  // Sizes that the C ABI takes as int.
+  void fits(const char* what, int64_t n) {
+    if (n > INT32_MAX) fail(std::string(what) + " must be below 2^31 (got " + std::to_string(n) + ")");
+  }
   int32_t* ints(const char* name, PyObject* o, int64_t n) { return static_cast<int32_t*>(data(name, o, kInt32, {n})); }
 };
 
@@ -161,8 +165,8 @@ PyObject* tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int32_t *table = r.table(a[5], b), *kv = r.ints("kv_len", a[6], b), *start = r.ints("q_start", a[7], b + 1),
             *slots = r.ints("slots", a[8], t), *pos = r.ints("positions", a[9], t), *out = r.ints("n_free_out", a[10], 1);
     void* stream = stream_of(a[11], r);
+    r.fits("the requests", b), r.fits("the free pages", cap), r.fits("the tokens", t);
     if (!r.ok) return nullptr;
-    if (b > INT32_MAX || cap > INT32_MAX || t > INT32_MAX) return PyLong_FromLong(WI_EINVAL);
     int rc;
     Py_BEGIN_ALLOW_THREADS rc = wi_paged_tables(c->handle, (int)b, ctx, fresh, pages, left, (int)cap, table, kv, start,
                                                 slots, pos, (int)t, out, stream);
@@ -189,8 +193,8 @@ PyObject* write(PyObject*, PyObject* const* a, Py_ssize_t n) {
          *qo = r.data("q_out", a[8], kBf16, {t, c->hq, kD});
     const void *wq = r.data("q_weight", a[9], kBf16, {kD}, true), *wk = r.data("k_weight", a[10], kBf16, {kD}, true);
     void* stream = stream_of(a[11], r);
+    r.fits("the tokens", t);
     if (!r.ok) return nullptr;
-    if (t > INT32_MAX) return PyLong_FromLong(WI_EINVAL);
     int rc;
     Py_BEGIN_ALLOW_THREADS rc =
         wi_paged_write(c->handle, (int)t, q, qs, k, ks, v, vs, wq, wk, pos, slots, qo, kp, vp, stream);
@@ -212,8 +216,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* out = r.data("out", a[7], kBf16, {t, c->hq, kD});
     float* lse = static_cast<float*>(r.data("lse", a[8], kFp32, {t, c->hq}, true));
     void* stream = stream_of(a[9], r);
+    r.fits("the tokens", t), r.fits("the requests", b);
     if (!r.ok) return nullptr;
-    if (t > INT32_MAX || b > INT32_MAX) return PyLong_FromLong(WI_EINVAL);
     int rc;
     Py_BEGIN_ALLOW_THREADS rc =
         wi_paged_attention(c->handle, (int)b, (int)t, q, kp, vp, table, start, kv, out, lse, stream);
@@ -243,8 +247,8 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void *ko = r.data("k_out", a[6], kBf16, {b, layers, c->hkv, rows, kD}),
          *vo = r.data("v_out", a[7], kBf16, {b, layers, c->hkv, rows, kD});
     void* stream = stream_of(a[8], r);
+    r.fits("the requests", b), r.fits("the layers", layers);
     if (!r.ok) return nullptr;
-    if (b > INT32_MAX || layers > INT32_MAX) return PyLong_FromLong(WI_EINVAL);
     int rc;
     Py_BEGIN_ALLOW_THREADS rc =
         wi_paged_gather(c->handle, (int)b, (int)layers, kp, vp, table, kv, pos0, rows, ko, vo, stream);

@@ -213,6 +213,7 @@ int wi_paged_tables(wi_paged* pc, int batch, const int32_t* ctx_len, const int32
   if (rc != WI_OK) return rc;
   if (batch < 1 || batch > pc->g.max_batch) return bad_batch(pc, batch);
   if (n_tokens < 0 || free_cap < 0) return fail(WI_EINVAL, "n_tokens and free_cap must be >= 0");
+  if (n_tokens > kPagedMaxTokens) return fail(WI_EUNSUPPORTED, "n_tokens must be <= %d (got %d)", kPagedMaxTokens, n_tokens);
   if (!ctx_len || !new_len || !n_free || !block_table || !kv_len || !q_start || !n_free_out ||
       (free_cap > 0 && !free_pages) || (n_tokens > 0 && (!slots || !positions)))
     return fail(WI_EINVAL, "a table pointer is NULL");

@@ -178,3 +178,29 @@ def test_outputs_are_made_on_the_stream_that_a_handle_names(wi):
         assert torch.equal(got, want)
     pc.check()
     pc.free()
+
+
+# ------------------------------------------------------------ refusals ----
+
+def test_tables_refuse_more_tokens_than_a_step_may_have(wi):
+    """The limit of a step is the same for the tables as for the calls that use them; nothing is written."""
+    pc = wi.PagedCache(wi.make_paged_config(1, 1, 16, 8, 2, 4))
+    most = 1 << 24
+    one = lambda: i32([0])  # noqa: E731
+    table, kv, start, left = i32([[-1] * 4]), one(), i32([5, 5]), one()
+    free = i32(range(8))
+    for n, error in ((most + 1, wi.WiError), ((1 << 31) - 1, wi.WiError), (1 << 31, ValueError)):
+        slots, pos = (torch.empty(n, dtype=torch.int32, device=DEV) for _ in range(2))
+        slots[:40] = 7
+        with pytest.raises(error, match="tokens"):
+            pc.tables(one(), i32([20]), free, i32([8]), table, kv, start, slots, pos, left)
+        assert (slots[:40] == 7).all() and (start == 5).all() and (table == -1).all()
+        del slots, pos
+    slots, pos = (torch.full((most,), 7, dtype=torch.int32, device=DEV) for _ in range(2))
+    pc.tables(one(), i32([20]), free, i32([8]), table, kv, start, slots, pos, left)
+    pc.check()
+    assert table[0].tolist() == [7, 6, -1, -1] and start.tolist() == [0, 20] and left.tolist() == [6]
+    assert slots[:20].tolist() == [7 * 16 + i for i in range(16)] + [6 * 16 + i for i in range(4)]
+    assert (slots[20:] == -1).all() and (pos[20:] == -1).all() and pos[:20].tolist() == list(range(20))
+    pc.free()
+    torch.cuda.empty_cache()
