@@ -522,6 +522,48 @@ __device__ __noinline__ void merge_tile(const Params& P, const Split& sp, int c0
   if (P.a.lse && d0 == 0) P.a.lse[at] = x.L == 0.f ? -INFINITY : x.M * kLn2 + logf(x.L);
 }
 
+// What a place where q_start falls adds to the units: more than any grid takes, and 4096 of them fit 64 bits beside the
+// most units that a call can have (2^51).
+constexpr long long kFalls = 1LL << 50;
+
+// The requests in front of the first place where q_start falls.  Those behind it may claim rows of the ones in front of
+// it: they have no tokens.
+__device__ __noinline__ int requests_in_order(const Params& P) {
+  int b = 0;
+  while (b < P.a.batch && P.a.q_start[b + 1] >= P.a.q_start[b]) ++b;
+  return b;
+}
+
+// Units of the requests [rb0, rb1) of this thread, of the threads in front of it, and of all: what the kernel's start
+// works out in line, once more for calls that are not in order (a loop around that code took 1% of single tokens' time).
+struct Share {
+  long long mine, before, total;
+};
+__device__ __noinline__ Share share_of(const Params& P, Smem& sm, int rb0, int rb1) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tp = 2 * P.tq;
+  Share x = {0, 0, 0};
+  for (int b = rb0; b < rb1; ++b) {
+    const Req r = load_req(P, b);
+    if (r.n == 0) continue;
+    const long long p0 = (long long)r.kv - r.n;
+    x.mine += P.Hkv * (units_before(p0, tp, (r.n + tp - 1) / tp - 1) + kLead + blocks_to(p0, r.n));
+  }
+  x.before = x.mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, x.before, o);
+    if (lane >= o) x.before += t;
+  }
+  __syncthreads();  // every warp has read the sums that stood there
+  if (lane == 31) sm.scan[warp] = x.before;
+  __syncthreads();
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) x.before += x.total;
+    x.total += sm.scan[w];
+  }
+  x.before -= x.mine;
+  return x;
+}
+
 __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_constant__ CUtensorMap map_q,
                                                                 const __grid_constant__ CUtensorMap map_k,
                                                                 const __grid_constant__ CUtensorMap map_v,
@@ -573,13 +615,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
 
   // ---- this CTA's run of units
   const int per = (P.a.batch + kThreads - 1) / kThreads;
-  const int rb0 = min(tid * per, P.a.batch), rb1 = min(rb0 + per, P.a.batch);
+  const int rb0 = min(tid * per, P.a.batch);
+  int rb1 = min(rb0 + per, P.a.batch);
   const int tp = 2 * P.tq;
   long long mine = 0, cost = 0;  // cost: of one kv head of the last request looked at
   Req r = {0, 0, 0, 1};
   for (int b = rb0; b < rb1; ++b) {
     r = load_req(P, b);
-    if (!r.ok && blockIdx.x == 0) atomicOr(P.err, WI_DEVERR_BAD_LENGTH);
+    if (!r.ok) {
+      if (blockIdx.x == 0) atomicOr(P.err, WI_DEVERR_BAD_LENGTH);
+      if (P.a.q_start[b + 1] < r.s0) mine += kFalls;
+    }
     if (r.n == 0) continue;
     const int tiles = (r.n + tp - 1) / tp;
     cost = units_before((long long)r.kv - r.n, tp, tiles - 1) + kLead + blocks_to((long long)r.kv - r.n, r.n);
@@ -602,10 +648,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     total += sm.scan[w];
   }
   before -= mine;
-  // (lengths that add up to more than a run can count, through pages shared by many requests: nothing is done)
-  if (total > (long long)gridDim.x * 0x3fffffff) {
+  // q_start falls somewhere, or lengths add up to more than a run can count (through pages shared by many requests)
+  const long long most = (long long)gridDim.x * 0x3fffffff;
+  if (total > most) {
     if (blockIdx.x == 0 && tid == 0) atomicOr(P.err, WI_DEVERR_BAD_LENGTH);
-    total = 0;
+    rb1 = min(rb1, requests_in_order(P));
+    const Share x = share_of(P, sm, rb0, rb1);
+    mine = x.mine;
+    before = x.before;
+    total = x.total > most ? 0 : x.total;  // too much still: nothing is done
   }
   int ctas = (int)min((long long)gridDim.x, total);
   if (P.tickets && P.a.batch == 1 && ctas > P.Hkv && total <= (long long)P.Hkv * (kLead + kWhole)) ctas = P.Hkv;

@@ -485,7 +485,8 @@ int wi_paged_write(wi_paged* pc, int n_tokens, const void* q, long long q_stride
  * Attention of a step's tokens over the cache (their own keys and values
  * already written).  q: device bf16 [n_tokens][n_q_heads][128], normed and
  * rotated; q_start [batch + 1] and kv_len [batch] as wi_paged_tables writes
- * them.  Token i of request b sits at position kv_len[b] - (tokens of b) + i
+ * them: where an entry of q_start lies below the one before it, the request that ends there and all behind it have no
+ * tokens (and an error bit is set).  Token i of request b sits at position kv_len[b] - (tokens of b) + i
  * and sees positions 0 .. its own: out = softmax(q K^T / sqrt(128)) V, bf16
  * [n_tokens][n_q_heads][128]; lse (fp32 [n_tokens][n_q_heads], may be NULL)
  * the natural logarithm of the row's sum of exponentials.  A token whose

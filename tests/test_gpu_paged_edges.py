@@ -204,3 +204,33 @@ def test_tables_refuse_more_tokens_than_a_step_may_have(wi):
     assert (slots[20:] == -1).all() and (pos[20:] == -1).all() and pos[:20].tolist() == list(range(20))
     pc.free()
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("start,good", [
+    ([0, 5, 2, 5], 1),                  # request 2 alone would be fine, and write rows of request 0
+    ([0, 5, 7, 3, 10, 12], 2),
+    ([0, 12, 0, 12, 0, 12], 1),         # every other request claims all rows
+    ([5, 4, 4, 12], 0),
+    ([0, 3, 3, 12, 11], 3),
+    ([0] + [6, 2] * 250, 1),            # in another thread's share of the requests
+    ([0] * 450 + [7, 1, 9], 450),
+])
+def test_attention_keeps_requests_apart_where_offsets_fall(wi, start, good):
+    """The requests in front of a falling offset are answered as if they were the whole call; rows of none behind it."""
+    rng = np.random.default_rng(53)
+    n, batch = 12, len(start) - 1
+    table, n_pages = lay_out([300], 16, rng)
+    q, k, v = (bf(rng.normal(size=s))[0] for s in ((n, 8, 128), (n_pages, 2, 16, 128), (n_pages, 2, 16, 128)))
+    pc = wi.PagedCache(wi.make_paged_config(8, 2, 16, n_pages, max(batch, 1), table.shape[1]))
+    table, kv = i32(table.repeat(batch, 0)), i32([300] * batch)
+    outs, lses = ([torch.full(s, 7.0, dtype=t, device=DEV) for _ in range(2)]
+                  for s, t in (((n, 8, 128), torch.bfloat16), ((n, 8), torch.float32)))
+    if good:
+        pc.attention(q, k, v, table, i32(start[:good + 1]), kv[:good].contiguous(), out=outs[0], lse=lses[0])
+        pc.check()
+    pc.attention(q, k, v, table, i32(start), kv, out=outs[1], lse=lses[1])
+    with pytest.raises(wi.WiError, match="length"):
+        pc.check()
+    assert torch.equal(*outs) and torch.equal(*lses)
+    assert (outs[1][start[good]:] == 7).all() and (outs[1][start[0]:start[good]] != 7).any(-1).all()
+    pc.free()
