@@ -21,7 +21,6 @@ if not os.path.exists(_LIB_PATH):
     raise ImportError(f"{_LIB_PATH} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
 
 lib = ctypes.CDLL(_LIB_PATH)
-from . import _paged  # noqa: E402  (the paged cache's argument checks; built with the library)
 
 WI_OK, WI_EINVAL, WI_ENOMEM, WI_ECUDA, WI_EUNSUPPORTED, WI_EDEVICE, WI_EFULL = 0, -1, -2, -3, -4, -5, -6
 _NAMES = {-1: "WI_EINVAL", -2: "WI_ENOMEM", -3: "WI_ECUDA", -4: "WI_EUNSUPPORTED", -5: "WI_EDEVICE",
@@ -470,6 +469,13 @@ class PagedCache:
 
     def __init__(self, cfg: wi_paged_config):
         self.handle = None
+        # the calls' argument checks, built against this Python's torch: the rest of the package does without them
+        try:
+            from . import _paged
+        except ImportError as e:
+            raise ImportError("the paged cache's _paged.so is missing or was built for another Python or torch: build it "
+                              "with `python -c 'import __graft_entry__ as g; g.build()'`") from e
+        self._calls = _paged
         h = _vp()
         _check(lib.wi_paged_create(ctypes.byref(cfg), ctypes.byref(h)))
         self.handle = h.value
@@ -487,8 +493,8 @@ class PagedCache:
     def tables(self, ctx_len, new_len, free_pages, n_free, block_table, kv_len, q_start, slots, positions,
                n_free_out, stream=None):
         """Pages, slots and positions of a step (wi_paged_tables); every argument an int32 tensor."""
-        rc = _paged.tables(self._ctx, ctx_len, new_len, free_pages, n_free, block_table, kv_len, q_start, slots,
-                           positions, n_free_out, self._on(stream))
+        rc = self._calls.tables(self._ctx, ctx_len, new_len, free_pages, n_free, block_table, kv_len, q_start, slots,
+                                positions, n_free_out, self._on(stream))
         if rc:
             _check(rc)
 
@@ -499,8 +505,8 @@ class PagedCache:
         k_pages and v_pages are [n][n_kv_heads][128]."""
         if q_out is None:
             q_out = _new_on(stream, (q.shape[0], self.n_q_heads, 128), q.dtype, q.device)
-        rc = _paged.write(self._ctx, q, k, v, positions, slots, k_pages, v_pages, q_out, q_weight, k_weight,
-                          self._on(stream))
+        rc = self._calls.write(self._ctx, q, k, v, positions, slots, k_pages, v_pages, q_out, q_weight, k_weight,
+                               self._on(stream))
         if rc:
             _check(rc)
         return q_out
@@ -510,7 +516,8 @@ class PagedCache:
         (rows behind the last request are zero if out was not given)."""
         if out is None:
             out = _new_on(stream, (q.shape[0], self.n_q_heads, 128), q.dtype, q.device, torch.zeros)
-        rc = _paged.attention(self._ctx, q, k_pages, v_pages, block_table, q_start, kv_len, out, lse, self._on(stream))
+        rc = self._calls.attention(self._ctx, q, k_pages, v_pages, block_table, q_start, kv_len, out, lse,
+                                   self._on(stream))
         if rc:
             _check(rc)
         return out
@@ -518,7 +525,7 @@ class PagedCache:
     def gather(self, k_pages, v_pages, block_table, kv_len, pos0, k_out, v_out, stream=None):
         """Rows [pos0, pos0 + n) of every request to k_out, v_out [batch][layers][n_kv_heads][n][128]
         (wi_paged_gather).  k_pages, v_pages: one pool, or [layers] of them."""
-        rc = _paged.gather(self._ctx, k_pages, v_pages, block_table, kv_len, pos0, k_out, v_out, self._on(stream))
+        rc = self._calls.gather(self._ctx, k_pages, v_pages, block_table, kv_len, pos0, k_out, v_out, self._on(stream))
         if rc:
             _check(rc)
         return k_out, v_out
