@@ -17,6 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libwaveindex.so")
 EXT = os.path.join(PKG, "_paged.so")
+STAMP = os.path.join(BUILD, "paged_binding.stamp")  # what EXT was built against
 
 SOURCES = ["wi_api.cu", "wi_build.cu", "wi_decode.cu", "wi_dense.cu", "wi_assign_tc.cu", "wi_noalloc.cu",
            "wi_grow.cu", "wi_tier.cu", "wi_selftest.cu", "wi_paged_api.cu", "wi_paged.cu", "wi_paged_attn.cu"]
@@ -35,6 +36,27 @@ def nvcc() -> str:
 def _deps_mtime() -> float:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
     return max(os.path.getmtime(f) for f in files)
+
+
+def _torch_of_this_python() -> str:
+    """The Python and the torch that the extension module reads the insides of."""
+    import importlib.metadata
+    import importlib.util
+    import sys
+
+    spec = importlib.util.find_spec("torch")
+    return f"{sys.version} | torch {importlib.metadata.version('torch')} in {spec.origin if spec else None}\n"
+
+
+def is_current() -> bool:
+    """Whether both files are there, newer than their sources, and the extension module fits this Python and torch."""
+    if not all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, EXT)):
+        return False
+    try:
+        with open(STAMP) as f:
+            return f.read() == _torch_of_this_python()
+    except OSError:
+        return False
 
 
 def _run(what: str, cmd: list[str]):
@@ -64,10 +86,12 @@ def _link_ext(obj: str):
                                *[f"-L{d}" for d in dirs], *[f"-Wl,-rpath,{d}" for d in dirs], "-ltorch_python",
                                "-ltorch_cpu", "-lc10"])
     os.replace(tmp, EXT)
+    with open(STAMP, "w") as f:
+        f.write(_torch_of_this_python())
 
 
 def build(force: bool = False, verbose: bool = False, extra: list[str] | None = None) -> str:
-    if not force and all(os.path.exists(f) and os.path.getmtime(f) >= _deps_mtime() for f in (LIB, EXT)):
+    if not force and is_current():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()

@@ -1,4 +1,5 @@
-"""The paged cache's extension module is loaded by the paged cache alone (no GPU needed)."""
+"""The paged cache's extension module is loaded by the paged cache alone, and built again for another torch (no GPU
+needed)."""
 import os
 import subprocess
 import sys
@@ -26,3 +27,20 @@ except ImportError as e:
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0 and "said so" in r.stdout, r.stdout + r.stderr
+
+
+def test_another_torch_or_python_means_another_build(monkeypatch, tmp_path):
+    """Files newer than every source are kept only while the extension module's Python and torch are those of now."""
+    b = __graft_entry__._load_build_module()
+    b.build()
+    assert b.is_current()
+    for name in ("LIB", "EXT", "STAMP"):
+        f = tmp_path / name
+        f.write_text(open(b.STAMP).read() if name == "STAMP" else "")
+        monkeypatch.setattr(b, name, str(f))
+    assert b.is_current()
+    monkeypatch.setattr(b, "_torch_of_this_python", lambda: "3.12 | torch 0.0")
+    assert not b.is_current()
+    monkeypatch.undo()
+    monkeypatch.setattr(b, "STAMP", str(tmp_path / "none"))
+    assert not b.is_current()
