@@ -9,6 +9,7 @@ library has not been built, importing this package raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -139,16 +140,23 @@ def _stream(stream):
     return int(stream)
 
 
-def _new_on(stream, shape, dtype, device, make=torch.empty):
-    """A tensor made on `stream`, so that nothing enqueued elsewhere still uses its memory."""
+def _on_stream(stream, device):
+    """A block whose torch calls go to `stream` (None: the current one)."""
     if stream is None:
-        return make(shape, dtype=dtype, device=device)
+        return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
         # handles 0 and 1 are the default stream, which torch does not take as an external one (0 gives a stream of
         # its pool, which the call's stream does not wait for)
         h = int(stream)
         stream = torch.cuda.ExternalStream(h, device) if h > 1 else torch.cuda.default_stream(device)
-    with torch.cuda.stream(stream):
+    return torch.cuda.stream(stream)
+
+
+def _new_on(stream, shape, dtype, device, make=torch.empty):
+    """A tensor made on `stream`, so that nothing enqueued elsewhere still uses its memory."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with _on_stream(stream, device):
         return make(shape, dtype=dtype, device=device)
 
 
@@ -372,10 +380,16 @@ class WaveIndex:
         """Build from prompts prefilled into a paged cache: gathers positions [0, n_ctx) of every
         request into contiguous tensors that the index owns (the pages may be given back once the
         build has run) and clusters them.  k_pages, v_pages: cfg.layers pools; kv_len: device int32
-        [cfg.batch], each at least n_ctx."""
+        [cfg.batch], each at least n_ctx (ValueError; this reads them, so it waits for `stream`).  A bad
+        page in the block table is reported by cache.check(), as for the gather."""
         shape = (cfg.batch, cfg.layers, cfg.n_kv_heads, cfg.n_ctx, 128)
         k, v = (_new_on(stream, shape, torch.bfloat16, k_pages.device) for _ in range(2))
         cache.gather(k_pages, v_pages, block_table, kv_len, 0, k, v, stream)
+        with _on_stream(stream, k.device):
+            lengths = kv_len.tolist()
+        for b, n in enumerate(lengths):
+            if not cfg.n_ctx <= n <= cache.max_pages * cache.page_size:
+                raise ValueError(f"kv_len[{b}] must be at least n_ctx = {cfg.n_ctx} and fit the block table (got {n})")
         return cls.build(cfg, k, v, init_centroids, stream)
 
     def decode(self, q: torch.Tensor, k_new=None, v_new=None, out=None, stream=None) -> torch.Tensor:

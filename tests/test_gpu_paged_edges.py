@@ -234,3 +234,55 @@ def test_attention_keeps_requests_apart_where_offsets_fall(wi, start, good):
     assert torch.equal(*outs) and torch.equal(*lses)
     assert (outs[1][start[good]:] == 7).all() and (outs[1][start[0]:start[good]] != 7).any(-1).all()
     pc.free()
+
+
+# ------------------------------------------------------------ from pages to an index ----
+
+@pytest.mark.parametrize("layers", [1, 3])
+def test_index_from_the_pages_of_several_layers(wi, layers):
+    """An index built from the pages decodes as one built from the same rows laid out by hand."""
+    rng = np.random.default_rng(54 + layers)
+    batch, hq, hkv, page, n = 2, 8, 2, 16, 1024
+    kv = [1100, 1024]
+    table, n_pages = lay_out(kv, page, rng)
+    pools = [bf(rng.normal(size=(layers, n_pages, hkv, page, 128)))[0] for _ in range(2)]
+    rows = [torch.stack([torch.stack([torch.cat([pool[a, int(table[b, j])] for j in range(n // page)], 1)
+                                      for a in range(layers)]) for b in range(batch)]) for pool in pools]
+    pc = wi.PagedCache(wi.make_paged_config(hq, hkv, page, n_pages, batch, table.shape[1]))
+    cfg = wi.make_config(batch, layers, hq, hkv, n, seg_len=512, clusters_per_seg=32, iters=2, budget_k=8)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ix = wi.WaveIndex.build_paged(cfg, pc, *pools, i32(table), i32(kv), stream=side)
+    torch.cuda.synchronize()
+    pc.check()
+    iy = wi.WaveIndex.build(cfg, *rows)
+    q = bf(rng.normal(size=(batch, layers, hq, 128)))[0]
+    a, b = ix.decode(q), iy.decode(q)
+    assert torch.equal(a, b) and a.isfinite().all() and (a != 0).any()
+    for x in (ix, iy):
+        x.check()
+        x.free()
+    pc.free()
+
+
+@pytest.mark.parametrize("kv", [[1024, 1023], [0, 1024], [-1, 1024], [1024, 3000]])
+@pytest.mark.parametrize("on", ["current", "side"])
+def test_index_from_pages_wants_every_position(wi, kv, on):
+    """A prompt shorter than the index's context, or longer than its row of pages, is no index over zeros."""
+    rng = np.random.default_rng(55)
+    hkv, page, n = 2, 16, 1024
+    table, n_pages = lay_out([1100, 1100], page, rng)
+    pools = [bf(rng.normal(size=(n_pages, hkv, page, 128)))[0] for _ in range(2)]
+    pc = wi.PagedCache(wi.make_paged_config(8, hkv, page, n_pages, 2, table.shape[1]))
+    cfg = wi.make_config(2, 1, 8, hkv, n, seg_len=512, clusters_per_seg=32, iters=2, budget_k=8)
+    lengths, late, table = i32([1024, 1024]), i32(kv), i32(table)
+    stream = torch.cuda.Stream() if on == "side" else torch.cuda.current_stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):      # the lengths come late, on the call's stream
+        torch.cuda._sleep(20_000_000)
+        lengths.copy_(late)
+    short = next(b for b, x in enumerate(kv) if not n <= x <= table.shape[1] * page)
+    with pytest.raises(ValueError, match=rf"kv_len\[{short}\].*got {kv[short]}"):
+        wi.WaveIndex.build_paged(cfg, pc, *pools, table, lengths, stream=stream)
+    torch.cuda.synchronize()
+    pc.free()
