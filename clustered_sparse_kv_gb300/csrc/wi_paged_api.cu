@@ -77,6 +77,13 @@ int enter(const wi_paged* pc) {
   return WI_OK;
 }
 
+// A call's status.  A launch that fails leaves its error for the next call that asks for the last one: it is taken away.
+int launched(const char* what, cudaError_t e) {
+  if (e == cudaSuccess) return WI_OK;
+  cudaGetLastError();
+  return fail(WI_ECUDA, "paged %s launch: %s", what, cudaGetErrorString(e));
+}
+
 int bad_batch(const wi_paged* pc, int batch) {
   return fail(WI_EINVAL, "batch (%d) must be in [1, %d]", batch, pc->g.max_batch);
 }
@@ -228,9 +235,7 @@ int wi_paged_tables(wi_paged* pc, int batch, const int32_t* ctx_len, const int32
   if (clash(outs, in)) return fail(WI_EINVAL, "an output shares memory with an input or another output");
   const WiPagedTables a = {ctx_len, new_len, free_pages, n_free,    block_table, kv_len,  q_start,
                            slots,   positions, n_free_out, batch, free_cap,    n_tokens};
-  const cudaError_t e = wi_launch_paged_tables(pc->g, a, pc->sms, pc->err, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return fail(WI_ECUDA, "paged tables launch: %s", cudaGetErrorString(e));
-  return WI_OK;
+  return launched("tables", wi_launch_paged_tables(pc->g, a, pc->sms, pc->err, static_cast<cudaStream_t>(stream)));
 }
 
 int wi_paged_write(wi_paged* pc, int n_tokens, const void* q, long long q_stride, const void* k, long long k_stride,
@@ -263,9 +268,7 @@ int wi_paged_write(wi_paged* pc, int n_tokens, const void* q, long long q_stride
                            "tokens are contiguous)");
   const WiPagedWrite a = {q,     k,     v,       q_stride, k_stride, v_stride, q_weight, k_weight, positions,
                           slots, q_out, k_pages, v_pages,  n_tokens};
-  const cudaError_t e = wi_launch_paged_write(g, a, pc->sms, pc->err, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return fail(WI_ECUDA, "paged write launch: %s", cudaGetErrorString(e));
-  return WI_OK;
+  return launched("write", wi_launch_paged_write(g, a, pc->sms, pc->err, static_cast<cudaStream_t>(stream)));
 }
 
 int wi_paged_attention(wi_paged* pc, int batch, int n_tokens, const void* q, const void* k_pages,
@@ -290,9 +293,8 @@ int wi_paged_attention(wi_paged* pc, int batch, int n_tokens, const void* q, con
   const Span outs[2] = {{out, qb}, {lse, 4LL * n_tokens * g.Hq}};
   if (clash(outs, in)) return fail(WI_EINVAL, "out or lse shares memory with an input or with the other");
   const WiPagedAttn a = {q, k_pages, v_pages, block_table, q_start, kv_len, out, lse, batch, n_tokens};
-  const cudaError_t e = wi_launch_paged_attention(pc->g, a, pc->sms, pc->scratch, pc->err, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return fail(WI_ECUDA, "paged attention launch: %s", cudaGetErrorString(e));
-  return WI_OK;
+  return launched("attention", wi_launch_paged_attention(pc->g, a, pc->sms, pc->scratch, pc->err,
+                                                         static_cast<cudaStream_t>(stream)));
 }
 
 int wi_paged_gather(wi_paged* pc, int batch, int layers, const void* k_pages, const void* v_pages,
@@ -320,9 +322,7 @@ int wi_paged_gather(wi_paged* pc, int batch, int layers, const void* k_pages, co
   const Span outs[2] = {{k_out, ob}, {v_out, ob}};
   if (clash(outs, in)) return fail(WI_EINVAL, "k_out or v_out shares memory with an input or with the other");
   const WiPagedGather a = {k_pages, v_pages, block_table, kv_len, k_out, v_out, batch, layers, pos0, n};
-  const cudaError_t e = wi_launch_paged_gather(g, a, pc->err, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return fail(WI_ECUDA, "paged gather launch: %s", cudaGetErrorString(e));
-  return WI_OK;
+  return launched("gather", wi_launch_paged_gather(g, a, pc->err, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -286,3 +286,47 @@ def test_index_from_pages_wants_every_position(wi, kv, on):
         wi.WaveIndex.build_paged(cfg, pc, *pools, table, lengths, stream=stream)
     torch.cuda.synchronize()
     pc.free()
+
+
+# ------------------------------------------------------------ failed launches ----
+
+@pytest.mark.parametrize("call", ["tables", "write", "attention", "gather"])
+def test_a_launch_that_fails_leaves_nothing_behind(wi, call):
+    """A call on the default stream while a stream that waits for it is captured cannot be launched: it says so, and the
+    next call of the library, which has nothing to do with it, is fine."""
+    import ctypes
+
+    cu = ctypes.CDLL("libcuda.so.1")
+    pc = wi.PagedCache(wi.make_paged_config(4, 2, 16, 8, 1, 4))
+    bf16 = dict(dtype=torch.bfloat16, device=DEV)
+    q, kn = torch.zeros((1, 4, 128), **bf16), torch.zeros((1, 2, 128), **bf16)
+    vn, qo, out = kn.clone(), q.clone(), q.clone()
+    pools = [torch.zeros((8, 2, 16, 128), **bf16) for _ in range(2)]
+    rows = [torch.zeros((1, 1, 2, 4, 128), **bf16) for _ in range(2)]
+    table, one, start = i32([[0, 1, 2, 3]]), [i32([1]) for _ in range(8)], i32([0, 1])
+    free = i32([4, 5])
+    cfg = wi.make_config(1, 1, 4, 2, 1024, seg_len=512, clusters_per_seg=32)
+    keys = torch.zeros((1, 1, 2, 1024, 128), **bf16)
+    mu = torch.zeros((2, 64, 128), **bf16)
+    run = {"tables": lambda s: pc.tables(one[0], one[1], free, one[2], table, one[3], start, one[4], one[5], one[6], stream=s),
+           "write": lambda s: pc.write(q, kn, vn, one[0], one[1], *pools, qo, stream=s),
+           "attention": lambda s: pc.attention(q, *pools, table, start, one[0], out=out, stream=s),
+           "gather": lambda s: pc.gather(*pools, table, one[0], 0, *rows, stream=s)}[call]
+    run(None)
+    wi.wi_init_centroids(cfg, keys, mu)
+    torch.cuda.synchronize()
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert cu.cuStreamCreate(ctypes.byref(stream), 0) == 0
+    assert cu.cuStreamBeginCapture_v2(stream, 0) == 0
+    try:
+        with pytest.raises(wi.WiError, match=f"paged {call} launch"):
+            run(0)
+    finally:
+        cu.cuStreamEndCapture(stream, ctypes.byref(graph))     # the capture is lost with the refused call
+        if graph.value:
+            cu.cuGraphDestroy(graph)
+        assert cu.cuStreamDestroy_v2(stream) == 0
+    wi.wi_init_centroids(cfg, keys, mu)
+    run(None)
+    pc.check()
+    pc.free()
