@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(kWrThreads, 6) k_paged_write(const __grid_cons
     if (turned) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        // the product's low 64 bits are the fraction of a turn; signed, it is the angle in [-1/2, 1/2) turns
+        // the product's low 64 bits are the fraction of a turn; signed, it is the angle in [-1/2, 1/2) turns, rounded to
+        // fp32 here (by at most 2^-26 of a turn, next to half turns)
         const long long a = (long long)(R.turn[4 * l + 2 * row1 + i] * (unsigned long long)pos);
         sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &s[i], &c[i]);  // 2^-31: half turns
         c[i] *= R.scale;

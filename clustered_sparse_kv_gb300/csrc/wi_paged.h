@@ -27,7 +27,8 @@ constexpr int kPagedMaxBatch = 4096;
 constexpr int kPagedMaxTokens = 1 << 24;  // of a step
 
 // Rotation of a head's pairs: the angle of pair i at position p is p * turn[i] / 2^64 turns, so the whole
-// turns drop out of a 64-bit product and nothing is lost at far positions.
+// turns drop out of a 64-bit product, and a far position's angle is as good as a near one's: known to 2^-31 of a turn, then
+// rounded to fp32.
 struct WiRope {
   unsigned long long turn[64];
   float scale;       // on cosine and sine

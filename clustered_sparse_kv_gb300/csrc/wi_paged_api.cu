@@ -88,6 +88,19 @@ int bad_batch(const wi_paged* pc, int batch) {
   return fail(WI_EINVAL, "batch (%d) must be in [1, %d]", batch, pc->g.max_batch);
 }
 
+// The fraction of a turn that x radians are, in 2^-64 turns: x / 2 pi in two doubles (one alone is off by up to 2^-55 of a
+// turn, which a position of 2^31 makes 2^-24), each without its whole turns, which are no rotation.
+unsigned long long turn_of(double x) {
+  constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;  // 1 / 2 pi
+  const double a = x * hi, b = std::fma(x, lo, std::fma(x, hi, -a));
+  auto fraction = [](double v) {
+    v -= std::rint(v);  // exact
+    const unsigned long long m = (unsigned long long)std::ldexp(std::fabs(v), 64);  // 2^63 at most
+    return v < 0 ? 0ull - m : m;
+  };
+  return fraction(a) + fraction(b);
+}
+
 int geom_from_config(const wi_paged_config* c, WiPagedGeom* g) {
   if (!c) return fail(WI_EINVAL, "config is NULL");
   if (c->n_q_heads < 1 || c->n_kv_heads < 1 || c->n_q_heads % c->n_kv_heads)
@@ -127,11 +140,8 @@ int geom_from_config(const wi_paged_config* c, WiPagedGeom* g) {
   g->rope.rotary = c->rotary_dim;
   g->rope.interleaved = c->interleaved;
   for (int i = 0; i < c->rotary_dim / 2; ++i) {
-    const double f = c->inv_freq[i] / 6.283185307179586476925286766559;  // turns per position
-    if (!std::isfinite(f)) return fail(WI_EINVAL, "inv_freq[%d] is not finite", i);
-    const double part = f - std::floor(f);  // whole turns per position are no rotation
-    // a double's 53 bits fit the 64-bit fraction; 1.0 (a tiny negative f) is a whole turn again
-    g->rope.turn[i] = part >= 1.0 ? 0ull : (unsigned long long)std::ldexp(part, 64);
+    if (!std::isfinite(c->inv_freq[i])) return fail(WI_EINVAL, "inv_freq[%d] is not finite", i);
+    g->rope.turn[i] = turn_of(c->inv_freq[i]);
   }
   return WI_OK;
 }

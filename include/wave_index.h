@@ -467,7 +467,8 @@ int wi_paged_tables(wi_paged* pc, int batch, const int32_t* ctx_len, const int32
  * q and k: x * rsqrt(mean(x^2) + eps) * weight with q_weight / k_weight device
  * bf16 [128] (NULL: no norm), then each pair (a, b) of the rotated part by the
  * angle positions[t] * inv_freq[i]: (a cos - b sin, b cos + a sin).  All in
- * fp32 (the angle exact to 2^-32 of a turn at any position), rounded once.
+ * fp32, rounded once; the angle (in half a turn either way) is off by at most
+ * 2^-31 of a turn and 2^-24 of itself, at any position.
  * Queries go to q_out [n_tokens][n_q_heads][128] (q itself if
  * q_stride = n_q_heads * 128; outputs share no memory otherwise, WI_EINVAL),
  * keys and values to slot slots[t] of the pools.

@@ -330,3 +330,63 @@ def test_a_launch_that_fails_leaves_nothing_behind(wi, call):
     run(None)
     pc.check()
     pc.free()
+
+
+# ------------------------------------------------------------ angles of far positions ----
+
+def test_write_knows_the_angles_of_far_positions(wi):
+    """At position 2^31 - 1 and frequencies whose angle lies within 2e-6 of a quarter turn, (1, 0) turns to (+-2e-6 or
+    less, +-1): the first element's bf16 digits show the angle to about 2^-30 of a turn.  The frequencies are such that
+    their quotient by 2 pi, rounded to a double, would be off by 24 * 2^-32 of a turn there or more, while the angle's own
+    rounding to fp32 is at most 1.5 * 2^-32."""
+    from fractions import Fraction
+
+    turn = Fraction(2 * 3141592653589793238462643383279502884197169399375105820974944, 10 ** 60)
+    rng = np.random.default_rng(56)
+    p, freq, want = 2 ** 31 - 1, [], []
+    while len(freq) < 64:
+        k, quarter = int(rng.integers(1, p // 8)), int(rng.choice([-1, 1]))
+        f = float((k * turn + quarter * turn / 4 + Fraction(rng.uniform(2e-7, 2e-6) * rng.choice([-1, 1]))) / p)
+        exact = Fraction(f) * p / turn
+        exact -= round(exact)                                    # turns in [-1/2, 1/2]
+        units = int(np.floor(float(exact * 2 ** 32)))
+        rounded = float(f / (2 * np.pi))
+        near = Fraction(rounded) * p
+        near -= round(near)
+        if abs(int(np.float32(units)) - units) <= 1.5 and abs(near - exact) * 2 ** 32 >= 24:
+            freq.append(f)
+            want.append((float(np.cos(float(exact * turn))), quarter))
+    want = np.array(want)
+    x = torch.zeros((1, 3, 128), dtype=torch.bfloat16, device=DEV)
+    x[..., :64] = 1
+    pc = wi.PagedCache(wi.make_paged_config(1, 1, 16, 1, 1, 1, inv_freq=freq))
+    pools = [torch.zeros((1, 1, 16, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    out = f64(pc.write(x[:, :1], x[:, 1:2], x[:, 2:], i32([p]), i32([0]), *pools))[0, 0]
+    pc.check()
+    pc.free()
+    # half a step of bf16, cosine and product in fp32 (2^-21 of the value), and of the angle: 1 for the product's dropped
+    # bits, 1.5 for its rounding, 0.5 for the frequency, in 2^-32 turns
+    tol = (2.0 ** -8 + 2.0 ** -21) * np.abs(want[:, 0]) + 3 * 2.0 ** -32 * 2 * np.pi
+    assert (np.abs(out[:64] - want[:, 0]) <= tol).all(), (np.abs(out[:64] - want[:, 0]) / tol).max()
+    assert (out[64:] == want[:, 1]).all()
+
+
+def test_write_turns_backwards(wi):
+    """Negative frequencies turn as positive ones mirrored, tiny ones (whose fraction of a turn is next to a whole) too."""
+    rng = np.random.default_rng(57)
+    n, freq = 40, [float(f) for f in 10.0 ** rng.uniform(-22, 0.7, size=64)]
+    x = bf(rng.normal(size=(n, 3, 128)))[0]
+    pos, slots = i32(rng.integers(0, 2 ** 31 - 1, n)), i32(range(n))
+    got = []
+    for sign in (1, -1):
+        pc = wi.PagedCache(wi.make_paged_config(1, 1, 16, 3, 1, 1, inv_freq=[sign * f for f in freq]))
+        pools = [torch.zeros((3, 1, 16, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        y = x if sign > 0 else torch.cat([x[..., 64:], x[..., :64]], -1)      # (a, b) as (b, a): the other way round
+        got.append(f64(pc.write(y[:, :1], y[:, 1:2], y[:, 2:], pos, slots, *pools)))
+        pc.check()
+        pc.free()
+    a, b = got[0], np.concatenate([got[1][..., 64:], got[1][..., :64]], -1)
+    size = np.abs(f64(x[:, :1]))
+    size = np.concatenate([size[..., :64] + size[..., 64:]] * 2, -1)
+    # each is off by half a step of bf16 and 2^-23 of |a| + |b| (angles of 2^-26 turns, products and sums in fp32)
+    assert (np.abs(a - b) <= 2.0 ** -7 * np.abs(a) + 2.0 ** -19 * size + 2.0 ** -133).all()
