@@ -82,6 +82,13 @@ constexpr int kLead = 4;
 // One request of few rows is not cut up to this many blocks: a merge costs 4 us, a block behind the first 0.7 (five
 // tokens over 305 positions 10.6 us whole, 12.4 cut; one over 500 11.3 and 12.1, over 800 15.7 and 12.9).
 constexpr int kWhole = 4;
+// Blocks that one segment has at most: what a CTA has of a longer item is added up in fp32 by its softmax warps, one
+// segment after the other (a segment costs 5 us, 2048 blocks 1400).  The tensor cores' own additions cut bits off: equal
+// weights over values of one sign came out 0.02% too small after 2^18 positions without a break, 0.3% after 2^20, 0.9% after
+// 2^21, and a sum of 2^26 took no more.  The kernel has an instance of its own (LONG) for caches whose requests can be that
+// long: the few instructions more at a segment's end cost single tokens over short contexts 4% (64 over 1000 positions
+// 75.2 us, 72.4 without), chunks 1%.
+constexpr int kLongest = 2048;
 // A row's weights are 2^(score - m) with m the row's maximum in the first block of its part, which no later block needs
 // to know its own maximum for: only when a block's weights add up to more than this (one of them is 2^9 at least), or to
 // no number, the block is done again with the maximum so far, and O rescaled.  Weights below 2^16 cost neither bf16 nor
@@ -225,6 +232,7 @@ __device__ __forceinline__ long long quot(long long a, long long b) {
 }
 
 // The run, one item's part after the other.
+template <bool LONG>
 struct Walk : Cursor {
   Req r;
   int tp, tiles;
@@ -256,6 +264,7 @@ struct Walk : Cursor {
       single = cnt <= P.tq;
       nblk = blocks_to(p0, (long long)tile * tp + cnt);
       took = min(nblk + kLead - at, left);
+      if (LONG) took = min(took, kLead + kLongest);
       b0 = max(0, at - kLead);
       nb = max(0, at + took - kLead) - b0;
       if (nb > 0) return true;
@@ -522,6 +531,31 @@ __device__ __noinline__ void merge_tile(const Params& P, const Split& sp, int c0
   if (P.a.lse && d0 == 0) P.a.lse[at] = x.L == 0.f ? -INFINITY : x.M * kLn2 + logf(x.L);
 }
 
+// What a CTA's earlier segments of an item left in the scratch, added to a row's O in tensor memory (columns [ca, cb) at
+// `to`; with `join`, of both chains, whose factors are f0 and f1).  Returns the row's new maximum and sum.
+__device__ __noinline__ float2 add_earlier(const Params& P, const float* src, int t, int row, bool live, float m, float l,
+                                           uint32_t to, int ca, int cb, bool join, float f0, float f1) {
+  const float pm = live ? __ldcg(src + P.parts.m(t, row)) : -INFINITY, pl = live ? __ldcg(src + P.parts.l(t, row)) : 0.f;
+  const float top = fmaxf(m, pm), ref = top == -INFINITY ? 0.f : top, f = ex2(m - ref), g = ex2(pm - ref);
+#pragma unroll 1
+  for (int c = ca; c < cb; c += 16) {
+    uint32_t a[16], b[16];
+    __syncwarp();
+    tmem_ld16_nowait(to + c, a);
+    tmem_ld16_nowait(to + (join ? WI_D : 0) + c, b);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float o = __uint_as_float(a[i]);
+      if (join) o = o * f0 + __uint_as_float(b[i]) * f1;
+      a[i] = __float_as_uint(live ? o * f + __ldcg(src + P.parts.o(t, c + i, row)) * g : o);
+    }
+    tmem_st16_nowait(to + c, a);
+  }
+  tmem_wait_st();
+  return make_float2(top, l * f + pl * g);
+}
+
 // What a place where q_start falls adds to the units: more than any grid takes, and 4096 of them fit 64 bits beside the
 // most units that a call can have (2^51).
 constexpr long long kFalls = 1LL << 50;
@@ -564,6 +598,7 @@ __device__ __noinline__ Share share_of(const Params& P, Smem& sm, int rb0, int r
   return x;
 }
 
+template <bool LONG>
 __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_constant__ CUtensorMap map_q,
                                                                 const __grid_constant__ CUtensorMap map_k,
                                                                 const __grid_constant__ CUtensorMap map_v,
@@ -718,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     // ended the last one (64 single tokens over 1000 positions: 76.0 us with the request read at both ends, now 72.9).
     Cursor cur;
     int nb, step, from, base, limit, whole;
-    auto begin = [&](Walk& w) {
+    auto begin = [&](Walk<LONG>& w) {
       const bool more = w.next(P);
       cur = w;
       if (lane == 0) sm.reqs[warp] = w.r;
@@ -734,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     };
     bool more;
     {
-      Walk w(P, sm.start, sm.req);
+      Walk<LONG> w(P, sm.start, sm.req);
       more = begin(w);
     }
     for (int seg = 0; more; ++seg) {
@@ -808,12 +843,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       }
 
       // ---- the segment's end: maximum and sum over both chains where they had one tile, then O
-      Walk w(P, cur, sm.reqs[warp]);
+      Walk<LONG> w(P, cur, sm.reqs[warp]);
       w.next(P);
       const int own_tile = w.single ? 0 : chain, ti = w.tile * w.tp + own_tile * P.tq + tok;
       const bool live = tok < P.tq && ti < w.r.n;
       const bool both = !w.single || w.nb > 1;  // chain 1 had blocks
-      const bool part = w.b0 > 0 || w.nb < w.nblk;
+      bool part = w.b0 > 0 || w.nb < w.nblk, begun = w.b0 == 0, goes_on = false, join = w.single && both;
       if (ok && (w.single || chain == 0)) ok = mbar_wait(&sm.o_full[0], o_par0, P.err);
       if (ok && both && (w.single || chain == 1)) ok = mbar_wait(&sm.o_full[1], o_par1, P.err);
       o_par0 ^= 1;
@@ -832,12 +867,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         l = sm.xch[0][1][row] * f0 + sm.xch[1][1][row] * f1;
       }
       const long long at = (long long)(w.r.s0 + ti) * P.Hq + w.kh * P.G + head;
-      const int slot = 2 * (int)blockIdx.x + (w.b0 == 0 ? 1 : 0);
+      const uint32_t to = tmem + lanes + 256u + (w.single ? 0u : (uint32_t)chain * WI_D);
+      const int ca = w.single ? 64 * chain : 0, cb = w.single ? ca + 64 : WI_D;  // the columns that this thread takes
+      if (LONG && w.nblk > kLongest) {  // maybe not the CTA's first segment of the item, or not its last
+        const int spent = sm.start.left - w.left;
+        begun = spent >= w.at - kLead;
+        part = !begun || w.b0 + w.nb < w.nblk;
+        goes_on = w.b0 + w.nb < w.nblk && w.took < w.left;
+        if (w.at > 0 && spent > 0) {
+          const float2 x = add_earlier(P, P.parts.slot(2 * (int)blockIdx.x + begun), own_tile, row, live, m, l, to, ca, cb,
+                                       join, f0, f1);
+          m = x.x;
+          l = x.y;
+          join = false;
+          if (w.single) soft_barrier();  // both threads of a row have read its maximum and sum
+        }
+      }
+      const int slot = 2 * (int)blockIdx.x + (begun ? 1 : 0);
       float* dst = P.parts.slot(slot);
       const bool poison = *reinterpret_cast<volatile int*>(&sm.poison[seg & 7]) == seg + 1;
       const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
-      const uint32_t to = tmem + lanes + 256u + (w.single ? 0u : (uint32_t)chain * WI_D);
-      const int ca = w.single ? 64 * chain : 0, cb = w.single ? ca + 64 : WI_D;  // the columns that this thread takes
 #pragma unroll 1
       for (int c = ca; c < cb; c += 16) {
         __syncwarp();
@@ -847,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         float o[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(raw_o[i]);
-        if (w.single && both) {
+        if (join) {
           tmem_ld16_nowait(to + WI_D + c, raw_o);
           tmem_wait_ld();
 #pragma unroll
@@ -883,7 +932,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         }
       }
       tc_fence_before();  // O is read: the next segment may write it
-      if (part && P.tickets) {
+      if (LONG && goes_on) {
+        // the rest of the item's end is for the last segment that the CTA has of it
+      } else if (part && P.tickets) {
         const long long item = sm.run_end - w.left - w.at + kLead;  // the unit of the item's first block
         const int c0 = cta_of(item, sm.total, sm.ctas), c1 = cta_of(item + w.nblk - 1, sm.total, sm.ctas);
         soft_barrier();  // then thread 0's release covers what all of them stored
@@ -905,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
               merge_some<kSoftWarps * 32>(P, sp, c0, 0, r0);
           }
         }
-      } else if (part && w.b0 == 0 && tid == 0) {
+      } else if (part && begun && tid == 0) {
         split = true;
         P.splits[blockIdx.x] = {w.r.s0 + w.tile * w.tp, w.kh, w.cnt,
                                 cta_of(sm.run_end - w.left - w.at + kLead + w.nblk - 1, sm.total, sm.ctas)};
@@ -916,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     }
     if (tid == 0 && !split) P.splits[blockIdx.x].last = -1;
   } else if (warp == kSoftWarps) {
-    Walk w(P, sm.start, sm.req);
+    Walk<LONG> w(P, sm.start, sm.req);
     // ---------------- TMA: queries, keys, values
     const uint32_t on = elect_one();
     const int boxes = kRows / P.box;  // boxes of a block, one lane finds the page of each
@@ -994,7 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     for (int s = 0; s < filled; ++s)  // the last use of each stage: this turn's in front of `at`, else the turn before
       mbar_wait(&sm.full[s], s < at.s ? at.par : at.par ^ 1u, P.err);
   } else if (warp == kSoftWarps + 1) {
-    Walk w(P, sm.start, sm.req);
+    Walk<LONG> w(P, sm.start, sm.req);
     // ---------------- tensor cores: one lane issues, the whole warp computes what it issues
     {
       const uint32_t on = elect_one();
@@ -1111,7 +1162,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       mbar_wait(&sm.drained, 0, P.err);
     }
   } else {
-    Walk w(P, sm.start, sm.req);
+    Walk<LONG> w(P, sm.start, sm.req);
     // ---------------- clean the value rows of blocks that not every row sees whole
     const int fixer = warp - kSoftWarps - 2;
     Ring at;                     // the ring stage of the next block in turn
@@ -1249,11 +1300,13 @@ cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a
       !wi_encode_pages_sw128(&map_k, a.k_pages, rows, (unsigned)P.box) ||
       !wi_encode_pages_sw128(&map_v, a.v_pages, rows, (unsigned)P.box))
     return cudaErrorInvalidValue;
-  static int smem_set[kWiSmemDevices] = {};
-  cudaError_t e = wi_ensure_smem(k_paged_attention, sizeof(Smem), smem_set);
+  static int smem_set[2][kWiSmemDevices] = {};
+  const bool is_long = (long long)g.max_pages * g.page > (long long)kLongest * kRows;
+  auto* kernel = is_long ? k_paged_attention<true> : k_paged_attention<false>;
+  cudaError_t e = wi_ensure_smem(kernel, sizeof(Smem), smem_set[is_long]);
   if (e != cudaSuccess) return e;
   const int grid = sms < kPagedMaxSms ? sms : kPagedMaxSms;
-  if ((e = wi_launch_chained(k_paged_attention, dim3((unsigned)grid), kThreads, sizeof(Smem), st, map_q, map_k, map_v,
+  if ((e = wi_launch_chained(kernel, dim3((unsigned)grid), kThreads, sizeof(Smem), st, map_q, map_k, map_v,
                              P)) != cudaSuccess)
     return e;
   if (here) return cudaSuccess;

@@ -495,7 +495,8 @@ int wi_paged_write(wi_paged* pc, int n_tokens, const void* q, long long q_stride
  * nothing: out 0, lse -infinity.  Rows at and behind q_start[batch] stay as
  * they were.  What lies in the pools beyond a request's kv_len, or at
  * positions that a token does not see, has no influence, not even infinities
- * or NaN.  Fp32 accumulation and softmax; the weights are rounded to bf16 for
+ * or NaN.  Fp32 accumulation (the tensor cores' over 2^18 positions at most,
+ * then added up in turn) and softmax; the weights are rounded to bf16 for
  * the product with V (the row's sum is of the unrounded ones).  Same inputs,
  * same bits.  Single tokens and chunks may be mixed freely in one call.
  */

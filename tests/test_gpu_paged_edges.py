@@ -390,3 +390,83 @@ def test_write_turns_backwards(wi):
     size = np.concatenate([size[..., :64] + size[..., 64:]] * 2, -1)
     # each is off by half a step of bf16 and 2^-23 of |a| + |b| (angles of 2^-26 turns, products and sums in fp32)
     assert (np.abs(a - b) <= 2.0 ** -7 * np.abs(a) + 2.0 ** -19 * size + 2.0 ** -133).all()
+
+
+# ------------------------------------------------------------ contexts of millions of positions ----
+
+def repeated(kv, rng, rows=1024):
+    """Block table of a long request over a pool of few pages of 128, each position's row, and the rows' counts in front
+    of positions [kv - tail, kv)."""
+    table = rng.integers(0, rows // 128, -(-kv // 128))
+    row = (table[:, None] * 128 + np.arange(128)).reshape(-1)[:kv]
+    return table, row
+
+
+@pytest.mark.parametrize("hq,hkv,new,kv", [
+    (8, 2, [1] * 80, [1 << 20] * 80),                          # one tile, whole in their CTAs, segment after segment
+    (4, 1, [1], [(1 << 26) - 77]),                             # cut: every CTA has more than a segment of it
+    (4, 1, [40], [(1 << 26) - 77]),                            # two tiles, cut
+    (4, 1, [40] * 200, [(1 << 19) + 300] * 200),               # two tiles, whole or cut anywhere
+    (8, 1, [1, 33, 2, 0, 16, 1, 70], [1 << 23, 3 << 20, 900, 5, (1 << 22) + 1, 7 << 20, 555555]),
+])
+def test_attention_over_millions_of_positions(wi, hq, hkv, new, kv):
+    """Long contexts over few distinct rows, which the 64-bit softmax counts instead of adding them one by one."""
+    rng = np.random.default_rng(58)
+    unique, tables = {}, []
+    for n in kv:
+        if n not in unique:
+            unique[n] = repeated(n, rng)
+        tables.append(unique[n][0])
+    width = max(len(t) for t in tables)
+    table = np.zeros((len(kv), width), np.int64)
+    for b, t in enumerate(tables):
+        table[b, :len(t)] = t
+    start = np.concatenate([[0], np.cumsum(new)])
+    n = int(start[-1])
+    (q, Q), (k, K), (v, V) = (bf(rng.normal(size=s)) for s in ((n, hq, 128), (8, hkv, 128, 128), (8, hkv, 128, 128)))
+    pc = wi.PagedCache(wi.make_paged_config(hq, hkv, 128, 8, len(kv), width))
+    lse = torch.empty((n, hq), device=DEV)
+    args = (q, k, v, i32(table), i32(start), i32(kv))
+    out = pc.attention(*args, lse=lse)
+    pc.check()
+    again = pc.attention(*args)
+    pc.check()
+    pc.free()
+    assert torch.equal(out, again)
+    out, lse = f64(out), f64(lse)
+    K, V = (x.transpose(1, 0, 2, 3).reshape(hkv, -1, 128) for x in (K, V))
+    for b in range(len(kv)):
+        if b >= 8 and b % 37:       # requests alike: some are enough
+            continue
+        row = unique[kv[b]][1]
+        counts = np.bincount(row[:max(kv[b] - new[b], 0)], minlength=1024).astype(np.float64)
+        for i in range(new[b]):
+            p, t = kv[b] - new[b] + i, start[b] + i
+            counts[row[p]] += 1
+            for h in range(hq):
+                x = K[h // (hq // hkv)] @ Q[t, h] / np.sqrt(128)
+                w = counts * np.exp(x - x.max())
+                z = w.sum()
+                ref, spread = w / z @ V[h // (hq // hkv)], w / z @ np.abs(V[h // (hq // hkv)])
+                # weights and result rounded to bf16, 2^-8 each; a score of at most 40 off by 128 * 2^-24 * 40 < 2^-11,
+                # twice; a segment's 2^14 additions of sixteen positions' products, each in up to four steps that lose
+                # less than 2^-23 of a sum that is half as large on average, 2^-8; its 2^11 sums of a row, less
+                assert (np.abs(out[t, h] - ref) <= 2.0 ** -8 * np.abs(ref) + (3 * 2.0 ** -8) * spread).all()
+                assert abs(lse[t, h] - (np.log(z) + x.max())) <= 2.0 ** -11 + 2.0 ** -12
+
+
+def test_attention_adds_long_contexts_up_in_parts(wi):
+    """Equal scores over values of one sign: what the additions lose does not grow with the context (in one sum, 2^23
+    positions came out 2.2% too small).  A bf16 rounding, and the additions' 2^-8 as above."""
+    rng = np.random.default_rng(59)
+    kv, batch = 1 << 23, 2 * 152
+    table, row = repeated(kv, rng)
+    v, V = bf(rng.uniform(0.5, 1.5, size=(8, 1, 128, 128)))
+    k = torch.zeros_like(v)
+    pc = wi.PagedCache(wi.make_paged_config(1, 1, 128, 8, batch, len(table)))
+    q = torch.zeros((batch, 1, 128), dtype=torch.bfloat16, device=DEV)
+    out = pc.attention(q, k, v, i32(table)[None].repeat(batch, 1), i32(range(batch + 1)), i32([kv] * batch))
+    pc.check()
+    pc.free()
+    ref = np.bincount(row, minlength=1024) / kv @ V.reshape(1024, 128)
+    assert (np.abs(f64(out) - ref) <= 2.0 ** -7 * ref).all()
