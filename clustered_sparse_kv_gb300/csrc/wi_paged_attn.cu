@@ -89,6 +89,8 @@ constexpr int kWhole = 4;
 // long: the few instructions more at a segment's end cost single tokens over short contexts 4% (64 over 1000 positions
 // 75.2 us, 72.4 without), chunks 1%.
 constexpr int kLongest = 2048;
+// Cycles that a block may take (1500 do), for the waits that may last through a run of a LONG instance.
+constexpr long long kBlockCycles = 1 << 14;
 // A row's weights are 2^(score - m) with m the row's maximum in the first block of its part, which no later block needs
 // to know its own maximum for: only when a block's weights add up to more than this (one of them is 2^9 at least), or to
 // no number, the block is done again with the maximum so far, and O rescaled.  Weights below 2^16 cost neither bf16 nor
@@ -1176,8 +1178,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       for (int j = 0; j < w.nb; ++j, at.step(j + ahead - 1 < w.nb ? 2 : 1)) {
         if (j < from) continue;
         const int s = at.s;
-        // only once the copy has been asked for does the stage's phase stand at this use
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.to_fix[s], (fix_par >> s) & 1u, P.err)))) break;
+        // only once the copy has been asked for does the stage's phase stand at this use (these warps are there as soon as
+        // they have cleaned what comes before, maybe a whole run ahead)
+        const long long limit = kMbarWaitCycles + (LONG ? sm.start.left * kBlockCycles : 0);
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.to_fix[s], (fix_par >> s) & 1u, P.err, limit)))) break;
         fix_par ^= 1u << s;
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[s], at.par, P.err)))) break;
         const int k0 = (w.b0 + j) * kRows, seen = w.r.kv - k0;  // rows of the block that the request holds

@@ -34,15 +34,16 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 }
 
 // Wait until the phase with the given parity has completed.  The wait is
-// bounded: after about 2^31 SM cycles (~1 s) without completion it records
-// WI_DEVERR_MBAR_TIMEOUT and returns false, so no kernel can spin forever.
+// bounded: after about 2^31 SM cycles (~1 s; `limit`, where the wait may take
+// longer in earnest) without completion it records WI_DEVERR_MBAR_TIMEOUT and
+// returns false, so no kernel can spin forever.
 constexpr long long kMbarWaitCycles = 1LL << 31;
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* err) {
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* err, long long limit = kMbarWaitCycles) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 0u && clock64() - t0 > kMbarWaitCycles) break;
+    if ((i & 255u) == 0u && clock64() - t0 > limit) break;
   }
   atomicOr(err, WI_DEVERR_MBAR_TIMEOUT);
   return false;

@@ -470,3 +470,19 @@ def test_attention_adds_long_contexts_up_in_parts(wi):
     pc.free()
     ref = np.bincount(row, minlength=1024) / kv @ V.reshape(1024, 128)
     assert (np.abs(f64(out) - ref) <= 2.0 ** -7 * ref).all()
+
+
+def test_attention_over_a_quarter_of_a_billion_positions(wi):
+    """Two million blocks of one item in a CTA, nearly three seconds: longer than a wait is given.  One page holds every
+    position; with equal scores and powers of two as values every sum is exact."""
+    kv, n = 1 << 28, 256 * torch.cuda.get_device_properties(0).multi_processor_count
+    pc = wi.PagedCache(wi.make_paged_config(1, 1, 128, 1, 1, kv // 128))
+    k = torch.zeros((1, 1, 128, 128), dtype=torch.bfloat16, device=DEV)
+    v = bf(np.broadcast_to(2.0 ** (np.arange(128) % 4), k.shape))[0]
+    q = torch.zeros((n, 1, 128), dtype=torch.bfloat16, device=DEV)
+    lse = torch.zeros((n, 1), device=DEV)
+    out = pc.attention(q, k, v, torch.zeros((1, kv // 128), dtype=torch.int32, device=DEV), i32([0, n]), i32([kv]), lse=lse)
+    pc.check()
+    pc.free()
+    assert (out == v[0, 0, 0]).all()
+    assert (lse - 28 * np.log(2)).abs().max() < 2.0 ** -12       # the rows see 2^28 positions and up to n fewer
