@@ -479,7 +479,8 @@ class PagedCache:
 
     Made on the current CUDA device; tensors are the caller's, on that device, bf16 ones as
     torch.bfloat16 or their int16 bit patterns.  One layer's pools are
-    k_pages, v_pages [n_pages][n_kv_heads][page_size][128]."""
+    k_pages, v_pages [n_pages][n_kv_heads][page_size][128].  The attention calls of one cache
+    share its scratch: order them (one stream)."""
 
     def __init__(self, cfg: wi_paged_config):
         self.handle = None
@@ -515,8 +516,8 @@ class PagedCache:
     def write(self, q, k, v, positions, slots, k_pages, v_pages, q_out=None, q_weight=None, k_weight=None,
               stream=None):
         """Norms and rotation of q and k, keys and values into the pools (wi_paged_write); returns q_out
-        [n][n_q_heads][128].  q, k, v: [n][heads][128], views of a fused projection allowed.  slots None:
-        k_pages and v_pages are [n][n_kv_heads][128]."""
+        [n][n_q_heads][128] (rows of padding tokens are not written).  q, k, v: [n][heads][128], views of a
+        fused projection allowed.  slots None: k_pages and v_pages are [n][n_kv_heads][128]."""
         if q_out is None:
             q_out = _new_on(stream, (q.shape[0], self.n_q_heads, 128), q.dtype, q.device)
         rc = self._calls.write(self._ctx, q, k, v, positions, slots, k_pages, v_pages, q_out, q_weight, k_weight,

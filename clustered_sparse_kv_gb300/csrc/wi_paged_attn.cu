@@ -44,8 +44,8 @@
 // What bounds it, 32 query and 8 kv heads on one GB300.  Chunks: the tensor
 // pipe, 72% active while a CTA runs; 2048 tokens behind 14K positions 316 -
 // 322 us, 1600 - 1630 TFLOP/s, 0.85 - 0.87 of the measured bf16 peak (behind
-// 129K 2.7 - 2.9 ms, 0.81 - 0.86; run for seconds, under the power cap, 3.1 -
-// 3.3 ms).  Each role is kept short: one thread computing the operands of
+// 129K, call after call under the power cap, 3.1 - 3.4 ms, 0.75 - 0.82 of the
+// sustained peak; a few calls alone 2.7 - 2.9).  Each role is kept short: one thread computing the operands of
 // tcgen05.mma under a branch took 3345 of 4230 cycles a block (hence
 // mma_bf16_warp), a maximum of every block and two threads to a row 1750
 // cycles of softmax where 1100 do.  The code's size matters as much: loops
@@ -80,7 +80,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 439, 444 us at 1, 2, 3, 4, 6 in an earlier form; longer contexts and single tokens do not care).
 constexpr int kLead = 4;
 // One request of few rows is not cut up to this many blocks: a merge costs 4 us, a block behind the first 0.7 (five
-// tokens over 305 positions 10.6 us whole, 12.4 cut; one over 500 11.3 and 12.1, over 800 15.7 and 12.9).
+// tokens over 305 positions 10.6 us whole, 12.4 cut; one over 500 11.3 and 12.1, over 800 15.7 and 12.9).  Several
+// requests are: as many equal runs as there are items are whole items only where all requests are as long as each other
+// (two of four tokens over 305 11.0 us, 12.1 cut), and elsewhere are cut all the same, into fewer parts (four tokens over
+// 100 and over 500 16.8 us, 12.0 cut; single tokens over 50, 500, 300 and 200 18.8 and 13.5).
 constexpr int kWhole = 4;
 // Blocks that one segment has at most: what a CTA has of a longer item is added up in fp32 by its softmax warps, one
 // segment after the other (a segment costs 5 us, 2048 blocks 1400).  The tensor cores' own additions cut bits off: equal
@@ -200,9 +203,10 @@ __device__ __forceinline__ int blocks_to(long long p0, long long end) {
   return e <= kRows ? 1 : (int)((e + kRows - 1) / kRows);
 }
 
-// Sum over i < n of floor((a i + b) / 128), a, b >= 0: whole multiples of the divisor m are taken out of a and b, and
-// what is left counts lattice points under a line, which is the same problem with a and m exchanged (n <= 2^19, so
-// that after the first step everything but the sum fits 32 bits).
+// Sum over i < n of floor((a i + b) / 128), a, b >= 0, by the steps of Euclid's algorithm on a and the divisor m (the
+// known way to a floor sum): whole multiples of m are taken out of a and b, and what is left counts lattice points under
+// a line, which is the same problem with a and m exchanged (n <= 2^19, so that after the first step everything but the
+// sum fits 32 bits).
 __device__ long long floor_sum(int n, int a, long long b) {
   if (n <= 0) return 0;
   long long s = (long long)n * (n - 1) / 2 * (a >> 7) + n * (b >> 7);
@@ -348,7 +352,11 @@ __device__ __forceinline__ float top_score(const uint32_t (&s)[2][32]) {
   return fmaxf(max3(t[0], t[1], max3(t[2], t[3], -INFINITY)), -INFINITY);
 }
 
-// 32 scores to weights 2^(score * log2(e) / sqrt(128) - ref): added to `sum`, and as bf16 to 16 columns of P.
+// 32 scores to weights 2^(score * log2(e) / sqrt(128) - ref): added to `sum`, and as bf16 to 16 columns of P.  The
+// tensor cores take both operands of a product in one type and the values are bf16, so the weights are too, the one
+// rounding before the output's; a second product with what the rounding leaves would be half as much tensor work again.
+// Against 64 bits the output is 1.6e-3 - 1.8e-3 off (relative 2-norm), as it is with fp32 weights to within 5e-5: its own
+// rounding is most of it.
 __device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t tp, float ref, uint64_t (&sum)[2]) {
   const uint64_t scale2 = pair(kScaleLog2, kScaleLog2), ref2 = pair(-ref, -ref);
   uint32_t p[16];
@@ -696,6 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     total = x.total > most ? 0 : x.total;  // too much still: nothing is done
   }
   int ctas = (int)min((long long)gridDim.x, total);
+  // (see kWhole: the items of one request are alike, so that a run per kv head is an item)
   if (P.tickets && P.a.batch == 1 && ctas > P.Hkv && total <= (long long)P.Hkv * (kLead + kWhole)) ctas = P.Hkv;
   if ((int)blockIdx.x >= ctas) {  // fewer units than CTAs (the whole CTA leaves)
     if (tid == 0) P.splits[blockIdx.x].last = -1;

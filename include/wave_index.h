@@ -402,10 +402,13 @@ void wi_lru_free(void* policy);
  * they use it: a bad value is never followed, sets a bit that
  * wi_paged_check reports, and leaves the outputs of the request it belongs to
  * unspecified but inside their buffers.
- * Limits: at most 2^24 tokens in a step (WI_EUNSUPPORTED).
+ * Limits (WI_EUNSUPPORTED): 2^24 tokens in a step, 1024 query heads, and those
+ * below.  No output shares memory with an input or another output (WI_EINVAL;
+ * wi_paged_write has one exception).
  * A handle owns the attention's scratch and the error word and belongs to the
  * device that was current when it was made (WI_EINVAL on another): order the
- * attention calls on one handle (one stream); the other calls may overlap.
+ * attention calls on one handle (one stream; graphs that hold them one behind
+ * the other, too); the other calls may overlap.
  */
 typedef struct wi_paged wi_paged; /* opaque, library-owned */
 
@@ -510,6 +513,7 @@ int wi_paged_attention(wi_paged* pc, int batch, int n_tokens, const void* q, con
  * page_size * 128 elements into k_pages / v_pages), to k_out and v_out: device
  * bf16 [batch][layers][n_kv_heads][n][128], as wi_build_index takes them, and with n = 1
  * wi_decode_step's k_new and v_new.  Positions at or beyond kv_len[b] become zeros.
+ * layers <= 65536 (WI_EINVAL), batch * layers * n_kv_heads * n < 2^37.
  */
 int wi_paged_gather(wi_paged* pc, int batch, int layers, const void* k_pages, const void* v_pages,
                     const int32_t* block_table, const int32_t* kv_len, long long pos0, long long n, void* k_out,
