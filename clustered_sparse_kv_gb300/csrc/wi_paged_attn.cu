@@ -45,12 +45,12 @@
 // pipe, 72% active while a CTA runs; 2048 tokens behind 14K positions 316 -
 // 322 us, 1600 - 1630 TFLOP/s, 0.85 - 0.87 of the measured bf16 peak (behind
 // 129K, call after call under the power cap, 3.1 - 3.4 ms, 0.75 - 0.82 of the
-// sustained peak; a few calls alone 2.7 - 2.9).  Each role is kept short: one thread computing the operands of
-// tcgen05.mma under a branch took 3345 of 4230 cycles a block (hence
-// mma_bf16_warp), a maximum of every block and two threads to a row 1750
-// cycles of softmax where 1100 do.  The code's size matters as much: loops
-// that were unrolled further, or a form of its own for tiles of few rows,
-// slowed every other loop of the kernel.
+// sustained peak; a few calls alone 2.7 - 2.9).  Each role is kept short: one
+// thread computing the operands of tcgen05.mma under a branch took 3345 of
+// 4230 cycles a block (hence mma_bf16_warp), a maximum of every block and two
+// threads to a row 1750 cycles of softmax where 1100 do.  The code's size
+// matters as much: loops that were unrolled further, or a form of its own for
+// tiles of few rows, slowed every other loop of the kernel.
 // Single tokens: HBM; 131K positions in pages of 16 in 90 - 98 us, 5.5 - 6.0
 // TB/s, of which the start takes 6, the reads 70 (7.6 TB/s) and the merge of
 // twenty parts per head 5.

@@ -472,6 +472,44 @@ def test_attention_adds_long_contexts_up_in_parts(wi):
     assert (np.abs(f64(out) - ref) <= 2.0 ** -7 * ref).all()
 
 
+@pytest.mark.parametrize("hq,new", [(1, 300), (4, 40)])
+def test_attention_poison_where_a_long_context_is_cut(wi, hq, new):
+    """Infinite and NaN values on both sides of position 2^18, where the first 2048 blocks end, in the middle of the
+    tokens' own positions: they reach the tokens that see them, in their two elements, and no others."""
+    rng = np.random.default_rng(60)
+    kv, batch, at = (1 << 18) + new // 2, 100, ((1 << 18) - 9, (1 << 18) + 3)
+    table, row = repeated(kv, rng)
+    table[-4:] = [8, 9, 10, 11]                 # the last blocks' pages are used once
+    row = (table[:, None] * 128 + np.arange(128)).reshape(-1)[:kv]
+    K, V = rng.normal(size=(12, 1, 128, 128)), rng.normal(size=(12, 1, 128, 128))
+    flat = V.reshape(-1, 128)
+    flat[row[at[0]], 9], flat[row[at[1]], 70] = np.inf, np.nan
+    (q, Q), (k, K), (v, V) = bf(rng.normal(size=(new, hq, 128))), bf(K), bf(V)
+    pc = wi.PagedCache(wi.make_paged_config(hq, 1, 128, 12, batch, len(table)))
+    out = pc.attention(q.repeat(batch, 1, 1), k, v, i32(table)[None].repeat(batch, 1), i32(np.arange(batch + 1) * new),
+                       i32([kv] * batch))
+    pc.check()
+    pc.free()
+    out = f64(out).reshape(batch, new, hq, 128)
+    K, V = K.reshape(-1, 128), V.reshape(-1, 128)
+    clean = np.where(np.isfinite(V), V, 0)
+    counts = np.bincount(row[:kv - new], minlength=12 * 128).astype(np.float64)
+    for i in range(new):
+        p = kv - new + i
+        counts[row[p]] += 1
+        x = Q[i] @ K.T / np.sqrt(128)
+        w = counts * np.exp(x - x.max(1, keepdims=True))
+        w /= w.sum(1, keepdims=True)
+        ref, spread = w @ clean, w @ np.abs(clean)
+        got = out[:, i]
+        if p >= at[0]:
+            assert (got[..., 9] == np.inf).all(), i
+        if p >= at[1]:
+            assert np.isnan(got[..., 70]).all(), i
+        fine = np.ones(128, bool)
+        fine[[9] * (p >= at[0]) + [70] * (p >= at[1])] = False
+        assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + 3 * 2.0 ** -8 * spread)[..., fine].all(), i
+
 def test_attention_over_a_quarter_of_a_billion_positions(wi):
     """Two million blocks of one item in a CTA, nearly three seconds: longer than a wait is given.  One page holds every
     position; with equal scores and powers of two as values every sum is exact."""
