@@ -93,6 +93,10 @@ _SIGS = {
     "wi_paged_write": [_vp, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
     "wi_paged_attention": [_vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
     "wi_paged_gather": [_vp, _i32, _i32, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp],
+    "wi_paged_axes": [_vp, _i32, _vp],
+    "wi_paged_write8": [_vp, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "wi_paged_attention8": [_vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "wi_paged_gather8": [_vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _vp],
     "wi_lru_round": [_vp, _vp, ctypes.c_int, ctypes.c_longlong, _vp, _vp, _ip, _vp, _vp, _ip],
 }
 for _name, _args in _SIGS.items():
@@ -376,15 +380,21 @@ class WaveIndex:
 
     @classmethod
     def build_paged(cls, cfg: wi_config, cache: "PagedCache", k_pages, v_pages, block_table, kv_len,
-                    init_centroids=None, stream=None):
+                    init_centroids=None, stream=None, k_scales=None, v_scales=None):
         """Build from prompts prefilled into a paged cache: gathers positions [0, n_ctx) of every
         request into contiguous tensors that the index owns (the pages may be given back once the
         build has run) and clusters them.  k_pages, v_pages: cfg.layers pools; kv_len: device int32
         [cfg.batch], each at least n_ctx (ValueError; this reads them, so it waits for `stream`).  A bad
-        page in the block table is reported by cache.check(), as for the gather."""
+        page in the block table is reported by cache.check(), as for the gather.  With k_scales and v_scales
+        the pools are those of gather8, and the index is built from what they stand for."""
+        if (k_scales is None) != (v_scales is None):
+            raise ValueError("k_scales and v_scales are given together")
         shape = (cfg.batch, cfg.layers, cfg.n_kv_heads, cfg.n_ctx, 128)
         k, v = (_new_on(stream, shape, torch.bfloat16, k_pages.device) for _ in range(2))
-        cache.gather(k_pages, v_pages, block_table, kv_len, 0, k, v, stream)
+        if k_scales is None:
+            cache.gather(k_pages, v_pages, block_table, kv_len, 0, k, v, stream)
+        else:
+            cache.gather8(k_pages, v_pages, k_scales, v_scales, block_table, kv_len, 0, k, v, stream)
         with _on_stream(stream, k.device):
             lengths = kv_len.tolist()
         for b, n in enumerate(lengths):
@@ -480,10 +490,21 @@ class PagedCache:
     Made on the current CUDA device; tensors are the caller's, on that device, bf16 ones as
     torch.bfloat16 or their int16 bit patterns.  One layer's pools are
     k_pages, v_pages [n_pages][n_kv_heads][page_size][128].  The attention calls of one cache
-    share its scratch: order them (one stream)."""
+    share its scratch: order them (one stream).
 
-    def __init__(self, cfg: wi_paged_config):
+    axes: the axis of each of the rotation's rotary_dim // 2 pairs, numbers from 0 (time, height, width, say;
+    wi_paged_axes); `positions` of the writes is then [max(axes) + 1][n].
+
+    write8, attention8 and gather8 are the calls of the same name over pools in 8 bits: k_pages, v_pages
+    torch.float8_e4m3fn [n_pages][n_kv_heads][page_size][128] and k_scales, v_scales torch.float8_e8m0fnu
+    [n_pages][n_kv_heads][page_size // 16] (or the bit patterns of either as torch.uint8)."""
+
+    def __init__(self, cfg: wi_paged_config, axes=None):
         self.handle = None
+        axes = None if axes is None else [int(a) for a in axes]
+        if axes is not None and (len(axes) != max(cfg.rotary_dim, 0) // 2 or not axes or min(axes) < 0):
+            raise ValueError(f"axes must have rotary_dim // 2 = {max(cfg.rotary_dim, 0) // 2} values, one at least and "
+                             f"none negative (got {axes})")
         # the calls' argument checks, built against this Python's torch: the rest of the package does without them
         try:
             from . import _paged
@@ -499,8 +520,13 @@ class PagedCache:
         self.n_q_heads, self.n_kv_heads = cfg.n_q_heads, cfg.n_kv_heads
         self.page_size, self.n_pages = cfg.page_size, cfg.n_pages
         self.max_batch, self.max_pages = cfg.max_batch, cfg.max_pages
+        self.n_axes = 1
+        if axes is not None:
+            n = max(axes) + 1
+            _check(lib.wi_paged_axes(self.handle, n, (ctypes.c_int * len(axes))(*axes)))
+            self.n_axes = n
         self._ctx = _paged.context(self.handle, self.device, cfg.n_q_heads, cfg.n_kv_heads, cfg.page_size, cfg.n_pages,
-                                   cfg.max_pages)
+                                   cfg.max_pages, self.n_axes)
 
     def _on(self, stream):
         return _raw_stream(self.device) if stream is None else _stream(stream)
@@ -517,7 +543,8 @@ class PagedCache:
               stream=None):
         """Norms and rotation of q and k, keys and values into the pools (wi_paged_write); returns q_out
         [n][n_q_heads][128] (rows of padding tokens are not written).  q, k, v: [n][heads][128], views of a
-        fused projection allowed.  slots None: k_pages and v_pages are [n][n_kv_heads][128]."""
+        fused projection allowed.  positions: [n], or [n_axes][n] where the cache has axes.  slots None: k_pages
+        and v_pages are [n][n_kv_heads][128]."""
         if q_out is None:
             q_out = _new_on(stream, (q.shape[0], self.n_q_heads, 128), q.dtype, q.device)
         rc = self._calls.write(self._ctx, q, k, v, positions, slots, k_pages, v_pages, q_out, q_weight, k_weight,
@@ -541,6 +568,37 @@ class PagedCache:
         """Rows [pos0, pos0 + n) of every request to k_out, v_out [batch][layers][n_kv_heads][n][128]
         (wi_paged_gather).  k_pages, v_pages: one pool, or [layers] of them."""
         rc = self._calls.gather(self._ctx, k_pages, v_pages, block_table, kv_len, pos0, k_out, v_out, self._on(stream))
+        if rc:
+            _check(rc)
+        return k_out, v_out
+
+    def write8(self, q, k, v, positions, slots, k_pages, v_pages, k_scales, v_scales, q_out=None, q_weight=None,
+               k_weight=None, stream=None):
+        """write into pools in 8 bits (wi_paged_write8); returns q_out.  The tokens that share a group of sixteen
+        slots have to follow one another, in rising slots without a gap."""
+        if q_out is None:
+            q_out = _new_on(stream, (q.shape[0], self.n_q_heads, 128), q.dtype, q.device)
+        rc = self._calls.write8(self._ctx, q, k, v, positions, slots, k_pages, v_pages, k_scales, v_scales, q_out,
+                                q_weight, k_weight, self._on(stream))
+        if rc:
+            _check(rc)
+        return q_out
+
+    def attention8(self, q, k_pages, v_pages, k_scales, v_scales, block_table, q_start, kv_len, out=None, lse=None,
+                   stream=None):
+        """attention over pools in 8 bits (wi_paged_attention8)."""
+        if out is None:
+            out = _new_on(stream, (q.shape[0], self.n_q_heads, 128), q.dtype, q.device, torch.zeros)
+        rc = self._calls.attention8(self._ctx, q, k_pages, v_pages, k_scales, v_scales, block_table, q_start, kv_len,
+                                    out, lse, self._on(stream))
+        if rc:
+            _check(rc)
+        return out
+
+    def gather8(self, k_pages, v_pages, k_scales, v_scales, block_table, kv_len, pos0, k_out, v_out, stream=None):
+        """gather from pools in 8 bits to bf16 rows (wi_paged_gather8)."""
+        rc = self._calls.gather8(self._ctx, k_pages, v_pages, k_scales, v_scales, block_table, kv_len, pos0, k_out,
+                                 v_out, self._on(stream))
         if rc:
             _check(rc)
         return k_out, v_out

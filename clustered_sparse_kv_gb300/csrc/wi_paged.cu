@@ -195,8 +195,9 @@ __device__ __forceinline__ uint64_t swap2(uint64_t x) {
   return pair2(v.y, v.x);
 }
 
-// INTER: pairs (2i, 2i + 1).  FULL: the whole head is rotated (no lane holds elements that are only scaled).
-template <bool INTER, bool FULL>
+// INTER: pairs (2i, 2i + 1).  FULL: the whole head is rotated (no lane holds elements that are only scaled).  AXES: a
+// pair's position is that of its axis; a lane asks for those of its two pairs beside the token's first.
+template <bool INTER, bool FULL, bool AXES>
 __global__ void __launch_bounds__(kWrThreads, 6) k_paged_write(const __grid_constant__ WiPagedWrite A,
                                                               const __grid_constant__ WiRope R, int Hq, int Hkv, int page,
                                                               int n_slots, float eps, int parts, int* err) {
@@ -235,6 +236,11 @@ __global__ void __launch_bounds__(kWrThreads, 6) k_paged_write(const __grid_cons
 #pragma unroll
   for (int s = 0; s < kWrStages - 1; ++s) fetch(part + s * parts, s);
   const int pos = A.positions[t];
+  int at[2] = {0, 0};
+  if (AXES && turned) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) at[i] = A.positions[(long long)R.axis[4 * l + 2 * row1 + i] * A.n_tokens + t];
+  }
   int slot = A.slots ? A.slots[t] : t;
   if (pos < 0) {  // padding
     asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives its warp
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(kWrThreads, 6) k_paged_write(const __grid_cons
       for (int i = 0; i < 2; ++i) {
         // the product's low 64 bits are the fraction of a turn; signed, it is the angle in [-1/2, 1/2) turns, rounded to
         // fp32 here (by at most 2^-26 of a turn, next to half turns)
-        const long long a = (long long)(R.turn[4 * l + 2 * row1 + i] * (unsigned long long)pos);
+        const long long a = (long long)(R.turn[4 * l + 2 * row1 + i] * (unsigned long long)(AXES ? at[i] : pos));
         sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &s[i], &c[i]);  // 2^-31: half turns
         c[i] *= R.scale;
         s[i] *= R.scale;
@@ -479,8 +485,11 @@ cudaError_t wi_launch_paged_write(const WiPagedGeom& g, const WiPagedWrite& a, i
   if (parts > batches) parts = batches;
   const long long grid = (parts * a.n_tokens + kWrThreads / 32 - 1) / (kWrThreads / 32);
   const bool full = g.rope.rotary == WI_D;
-  auto* kernel = g.rope.interleaved ? (full ? k_paged_write<true, true> : k_paged_write<true, false>)
-                                    : (full ? k_paged_write<false, true> : k_paged_write<false, false>);
+  auto* kernel = g.rope.axes > 1
+                     ? (g.rope.interleaved ? (full ? k_paged_write<true, true, true> : k_paged_write<true, false, true>)
+                                           : (full ? k_paged_write<false, true, true> : k_paged_write<false, false, true>))
+                     : (g.rope.interleaved ? (full ? k_paged_write<true, true, false> : k_paged_write<true, false, false>)
+                                           : (full ? k_paged_write<false, true, false> : k_paged_write<false, false, false>));
   return wi_launch_chained(kernel, dim3((unsigned)grid), kWrThreads, 0, st, a, g.rope, g.Hq, g.Hkv, g.page,
                            g.n_pages * g.page, g.eps, (int)parts, err);
 }

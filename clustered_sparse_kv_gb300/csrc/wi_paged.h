@@ -34,7 +34,10 @@ struct WiRope {
   float scale;       // on cosine and sine
   int rotary;        // rotated elements, a multiple of 8
   int interleaved;
+  int axes;          // positions of a token: 1, or as many as its pairs turn by
+  unsigned char axis[64];  // the one that pair i turns by
 };
+constexpr int kPagedMaxAxes = 4;
 
 // Geometry of a paged cache, derived from wi_paged_config.
 struct WiPagedGeom {
@@ -77,6 +80,17 @@ struct WiPagedWrite {
 };
 cudaError_t wi_launch_paged_write(const WiPagedGeom& g, const WiPagedWrite& a, int sms, int* err, cudaStream_t st);
 
+// Pools in 8 bits: e4m3 values, and a power of two (its exponent + 127 in a byte) for every kGroup positions of a head.
+constexpr int kGroup = 16;
+constexpr int kScaleBias = 127, kScaleLowest = -64;
+struct WiPagedScales {
+  unsigned char* k;
+  unsigned char* v;
+};
+// w's k_out and v_out are the 8-bit pools.
+cudaError_t wi_launch_paged_write8(const WiPagedGeom& g, const WiPagedWrite& w, const WiPagedScales& s, int sms, int* err,
+                                   cudaStream_t st);
+
 struct WiPagedGather {
   const void* k_pages;
   const void* v_pages;
@@ -88,6 +102,8 @@ struct WiPagedGather {
   long long pos0, n;
 };
 cudaError_t wi_launch_paged_gather(const WiPagedGeom& g, const WiPagedGather& a, int* err, cudaStream_t st);
+cudaError_t wi_launch_paged_gather8(const WiPagedGeom& g, const WiPagedGather& a, const WiPagedScales& s, int* err,
+                                    cudaStream_t st);
 
 struct WiPagedAttn {
   const void* q;
@@ -107,3 +123,5 @@ constexpr size_t kPagedTicketBytes = kPagedMaxSms * 4;  // at the start of the s
 size_t wi_paged_attention_scratch(int sms);
 cudaError_t wi_launch_paged_attention(const WiPagedGeom& g, const WiPagedAttn& a, int sms, void* scratch, int* err,
                                       cudaStream_t st);
+cudaError_t wi_launch_paged_attention8(const WiPagedGeom& g, const WiPagedAttn& a, const WiPagedScales& s, int sms,
+                                       void* scratch, int* err, cudaStream_t st);

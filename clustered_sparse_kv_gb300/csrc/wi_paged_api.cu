@@ -66,6 +66,9 @@ bool clash(const Span (&outs)[N], const Span (&ins)[M]) {
 }
 
 long long pool_bytes(const WiPagedGeom& g) { return (long long)g.n_pages * g.Hkv * g.page * WI_D * 2; }
+// ... of 8-bit pools, and of their scales
+long long pool8_bytes(const WiPagedGeom& g) { return (long long)g.n_pages * g.Hkv * g.page * WI_D; }
+long long scale_bytes(const WiPagedGeom& g) { return (long long)g.n_pages * g.Hkv * (g.page / kGroup); }
 
 // What every call checks first: the handle, and that its device is the current one.
 int enter(const wi_paged* pc) {
@@ -139,6 +142,7 @@ int geom_from_config(const wi_paged_config* c, WiPagedGeom* g) {
   g->rope.scale = (float)c->rope_scale;
   g->rope.rotary = c->rotary_dim;
   g->rope.interleaved = c->interleaved;
+  g->rope.axes = 1;
   for (int i = 0; i < c->rotary_dim / 2; ++i) {
     if (!std::isfinite(c->inv_freq[i])) return fail(WI_EINVAL, "inv_freq[%d] is not finite", i);
     g->rope.turn[i] = turn_of(c->inv_freq[i]);
@@ -213,6 +217,20 @@ int wi_paged_check(wi_paged* pc) {
               herr & WI_DEVERR_MBAR_TIMEOUT ? " a wait timed out;" : "");
 }
 
+int wi_paged_axes(wi_paged* pc, int n_axes, const int32_t* axis) {
+  wi_set_error("");
+  if (!pc) return fail(WI_EINVAL, "paged cache handle is NULL");
+  WiRope& r = pc->g.rope;
+  if (n_axes < 1 || n_axes > kPagedMaxAxes) return fail(WI_EINVAL, "n_axes (%d) must be in [1, %d]", n_axes, kPagedMaxAxes);
+  if (n_axes > 1 && !axis && r.rotary > 0) return fail(WI_EINVAL, "axis is NULL");
+  for (int i = 0; n_axes > 1 && i < r.rotary / 2; ++i)
+    if (axis[i] < 0 || axis[i] >= n_axes)
+      return fail(WI_EINVAL, "axis[%d] (%d) must be in [0, %d)", i, axis[i], n_axes);
+  for (int i = 0; i < r.rotary / 2; ++i) r.axis[i] = n_axes > 1 ? (unsigned char)axis[i] : 0;
+  r.axes = n_axes;
+  return WI_OK;
+}
+
 void wi_paged_free(wi_paged* pc) {
   if (!pc) return;
   int dev = -1;
@@ -248,10 +266,11 @@ int wi_paged_tables(wi_paged* pc, int batch, const int32_t* ctx_len, const int32
   return launched("tables", wi_launch_paged_tables(pc->g, a, pc->sms, pc->err, static_cast<cudaStream_t>(stream)));
 }
 
-int wi_paged_write(wi_paged* pc, int n_tokens, const void* q, long long q_stride, const void* k, long long k_stride,
-                   const void* v, long long v_stride, const void* q_weight, const void* k_weight,
-                   const int32_t* positions, const int32_t* slots, void* q_out, void* k_pages, void* v_pages,
-                   void* stream) {
+// The write's checks: into bf16 pools or rows, or with scales into 8-bit pools.
+static int write_any(wi_paged* pc, int n_tokens, const void* q, long long q_stride, const void* k, long long k_stride,
+                     const void* v, long long v_stride, const void* q_weight, const void* k_weight,
+                     const int32_t* positions, const int32_t* slots, void* q_out, void* k_pages, void* v_pages,
+                     const WiPagedScales* scales, void* stream) {
   const int rc = enter(pc);
   if (rc != WI_OK) return rc;
   const WiPagedGeom& g = pc->g;
@@ -267,23 +286,47 @@ int wi_paged_write(wi_paged* pc, int n_tokens, const void* q, long long q_stride
   const long long qw = (long long)g.Hq * WI_D, kw = (long long)g.Hkv * WI_D;
   if (n_tokens > 1 && (q_stride < qw || k_stride < kw || v_stride < kw || q_stride % 8 || k_stride % 8 || v_stride % 8))
     return fail(WI_EINVAL, "token strides must be multiples of 8 and at least a token's heads");
-  const long long n1 = n_tokens - 1, kb = slots ? pool_bytes(g) : 2 * kw * n_tokens;
+  if (scales && (!slots || !scales->k || !scales->v)) return fail(WI_EINVAL, "slots, k_scales and v_scales must be non-NULL");
+  if (scales && (misaligned(scales->k, 16) || misaligned(scales->v, 16)))
+    return fail(WI_EINVAL, "the scales must be 16-byte aligned");
+  const long long n1 = n_tokens - 1, kb = scales ? pool8_bytes(g) : slots ? pool_bytes(g) : 2 * kw * n_tokens;
+  const long long sb = scales ? scale_bytes(g) : 0;
   const bool in_place = q_out == q && (n_tokens == 1 || q_stride == qw);
   const Span in[7] = {{in_place ? nullptr : q, 2 * (n1 * q_stride + qw)}, {k, 2 * (n1 * k_stride + kw)},
                       {v, 2 * (n1 * v_stride + kw)}, {q_weight, 2 * WI_D}, {k_weight, 2 * WI_D},
-                      {positions, 4LL * n_tokens}, {slots, 4LL * n_tokens}};
-  const Span outs[3] = {{q_out, 2 * qw * n_tokens}, {k_pages, kb}, {v_pages, kb}};
+                      {positions, 4LL * g.rope.axes * n_tokens}, {slots, 4LL * n_tokens}};
+  const Span outs[5] = {{q_out, 2 * qw * n_tokens}, {k_pages, kb}, {v_pages, kb}, {scales ? scales->k : nullptr, sb},
+                        {scales ? scales->v : nullptr, sb}};
   if (clash(outs, in))
     return fail(WI_EINVAL, "an output shares memory with an input or another output (q_out may be q itself where q's "
                            "tokens are contiguous)");
   const WiPagedWrite a = {q,     k,     v,       q_stride, k_stride, v_stride, q_weight, k_weight, positions,
                           slots, q_out, k_pages, v_pages,  n_tokens};
+  if (scales)
+    return launched("write8", wi_launch_paged_write8(g, a, *scales, pc->sms, pc->err, static_cast<cudaStream_t>(stream)));
   return launched("write", wi_launch_paged_write(g, a, pc->sms, pc->err, static_cast<cudaStream_t>(stream)));
 }
 
-int wi_paged_attention(wi_paged* pc, int batch, int n_tokens, const void* q, const void* k_pages,
-                       const void* v_pages, const int32_t* block_table, const int32_t* q_start,
-                       const int32_t* kv_len, void* out, float* lse, void* stream) {
+int wi_paged_write(wi_paged* pc, int n_tokens, const void* q, long long q_stride, const void* k, long long k_stride,
+                   const void* v, long long v_stride, const void* q_weight, const void* k_weight,
+                   const int32_t* positions, const int32_t* slots, void* q_out, void* k_pages, void* v_pages,
+                   void* stream) {
+  return write_any(pc, n_tokens, q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, positions, slots, q_out,
+                   k_pages, v_pages, nullptr, stream);
+}
+
+int wi_paged_write8(wi_paged* pc, int n_tokens, const void* q, long long q_stride, const void* k, long long k_stride,
+                    const void* v, long long v_stride, const void* q_weight, const void* k_weight,
+                    const int32_t* positions, const int32_t* slots, void* q_out, void* k_pages, void* v_pages,
+                    void* k_scales, void* v_scales, void* stream) {
+  const WiPagedScales s = {static_cast<unsigned char*>(k_scales), static_cast<unsigned char*>(v_scales)};
+  return write_any(pc, n_tokens, q, q_stride, k, k_stride, v, v_stride, q_weight, k_weight, positions, slots, q_out,
+                   k_pages, v_pages, &s, stream);
+}
+
+static int attention_any(wi_paged* pc, int batch, int n_tokens, const void* q, const void* k_pages, const void* v_pages,
+                         const WiPagedScales* scales, const int32_t* block_table, const int32_t* q_start,
+                         const int32_t* kv_len, void* out, float* lse, void* stream) {
   const int rc = enter(pc);
   if (rc != WI_OK) return rc;
   if (batch < 1 || batch > pc->g.max_batch) return bad_batch(pc, batch);
@@ -297,19 +340,40 @@ int wi_paged_attention(wi_paged* pc, int batch, int n_tokens, const void* q, con
   if (misaligned(block_table, 4) || misaligned(q_start, 4) || misaligned(kv_len, 4) || misaligned(lse, 4))
     return fail(WI_EINVAL, "the tables and lse must be 4-byte aligned");
   const WiPagedGeom& g = pc->g;
+  if (scales && (!scales->k || !scales->v)) return fail(WI_EINVAL, "k_scales and v_scales must be non-NULL");
+  if (scales && (misaligned(scales->k, 16) || misaligned(scales->v, 16)))
+    return fail(WI_EINVAL, "the scales must be 16-byte aligned");
   const long long qb = 2LL * n_tokens * g.Hq * WI_D;
-  const Span in[6] = {{q, qb}, {k_pages, pool_bytes(g)}, {v_pages, pool_bytes(g)}, {block_table, 4LL * batch * g.max_pages},
-                      {q_start, 4LL * (batch + 1)}, {kv_len, 4LL * batch}};
+  const long long kb = scales ? pool8_bytes(g) : pool_bytes(g), sb = scales ? scale_bytes(g) : 0;
+  const Span in[8] = {{q, qb}, {k_pages, kb}, {v_pages, kb}, {block_table, 4LL * batch * g.max_pages},
+                      {q_start, 4LL * (batch + 1)}, {kv_len, 4LL * batch}, {scales ? scales->k : nullptr, sb},
+                      {scales ? scales->v : nullptr, sb}};
   const Span outs[2] = {{out, qb}, {lse, 4LL * n_tokens * g.Hq}};
   if (clash(outs, in)) return fail(WI_EINVAL, "out or lse shares memory with an input or with the other");
   const WiPagedAttn a = {q, k_pages, v_pages, block_table, q_start, kv_len, out, lse, batch, n_tokens};
-  return launched("attention", wi_launch_paged_attention(pc->g, a, pc->sms, pc->scratch, pc->err,
-                                                         static_cast<cudaStream_t>(stream)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (scales)
+    return launched("attention8", wi_launch_paged_attention8(g, a, *scales, pc->sms, pc->scratch, pc->err, st));
+  return launched("attention", wi_launch_paged_attention(g, a, pc->sms, pc->scratch, pc->err, st));
 }
 
-int wi_paged_gather(wi_paged* pc, int batch, int layers, const void* k_pages, const void* v_pages,
-                    const int32_t* block_table, const int32_t* kv_len, long long pos0, long long n, void* k_out,
-                    void* v_out, void* stream) {
+int wi_paged_attention(wi_paged* pc, int batch, int n_tokens, const void* q, const void* k_pages,
+                       const void* v_pages, const int32_t* block_table, const int32_t* q_start,
+                       const int32_t* kv_len, void* out, float* lse, void* stream) {
+  return attention_any(pc, batch, n_tokens, q, k_pages, v_pages, nullptr, block_table, q_start, kv_len, out, lse, stream);
+}
+
+int wi_paged_attention8(wi_paged* pc, int batch, int n_tokens, const void* q, const void* k_pages,
+                        const void* v_pages, const void* k_scales, const void* v_scales, const int32_t* block_table,
+                        const int32_t* q_start, const int32_t* kv_len, void* out, float* lse, void* stream) {
+  const WiPagedScales s = {static_cast<unsigned char*>(const_cast<void*>(k_scales)),
+                           static_cast<unsigned char*>(const_cast<void*>(v_scales))};
+  return attention_any(pc, batch, n_tokens, q, k_pages, v_pages, &s, block_table, q_start, kv_len, out, lse, stream);
+}
+
+static int gather_any(wi_paged* pc, int batch, int layers, const void* k_pages, const void* v_pages,
+                      const WiPagedScales* scales, const int32_t* block_table, const int32_t* kv_len, long long pos0,
+                      long long n, void* k_out, void* v_out, void* stream) {
   const int rc = enter(pc);
   if (rc != WI_OK) return rc;
   const WiPagedGeom& g = pc->g;
@@ -326,13 +390,33 @@ int wi_paged_gather(wi_paged* pc, int batch, int layers, const void* k_pages, co
   if (misaligned(k_pages, 16) || misaligned(v_pages, 16) || misaligned(k_out, 16) || misaligned(v_out, 16))
     return fail(WI_EINVAL, "the pools, k_out and v_out must be 16-byte aligned");
   if (misaligned(block_table, 4) || misaligned(kv_len, 4)) return fail(WI_EINVAL, "the tables must be 4-byte aligned");
+  if (scales && (!scales->k || !scales->v)) return fail(WI_EINVAL, "k_scales and v_scales must be non-NULL");
+  if (scales && (misaligned(scales->k, 16) || misaligned(scales->v, 16)))
+    return fail(WI_EINVAL, "the scales must be 16-byte aligned");
   const long long ob = 2LL * batch * layers * g.Hkv * n * WI_D;
-  const Span in[4] = {{k_pages, layers * pool_bytes(g)}, {v_pages, layers * pool_bytes(g)},
-                      {block_table, 4LL * batch * g.max_pages}, {kv_len, 4LL * batch}};
+  const long long kb = layers * (scales ? pool8_bytes(g) : pool_bytes(g)), sb = scales ? layers * scale_bytes(g) : 0;
+  const Span in[6] = {{k_pages, kb}, {v_pages, kb}, {block_table, 4LL * batch * g.max_pages}, {kv_len, 4LL * batch},
+                      {scales ? scales->k : nullptr, sb}, {scales ? scales->v : nullptr, sb}};
   const Span outs[2] = {{k_out, ob}, {v_out, ob}};
   if (clash(outs, in)) return fail(WI_EINVAL, "k_out or v_out shares memory with an input or with the other");
   const WiPagedGather a = {k_pages, v_pages, block_table, kv_len, k_out, v_out, batch, layers, pos0, n};
-  return launched("gather", wi_launch_paged_gather(g, a, pc->err, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (scales) return launched("gather8", wi_launch_paged_gather8(g, a, *scales, pc->err, st));
+  return launched("gather", wi_launch_paged_gather(g, a, pc->err, st));
+}
+
+int wi_paged_gather(wi_paged* pc, int batch, int layers, const void* k_pages, const void* v_pages,
+                    const int32_t* block_table, const int32_t* kv_len, long long pos0, long long n, void* k_out,
+                    void* v_out, void* stream) {
+  return gather_any(pc, batch, layers, k_pages, v_pages, nullptr, block_table, kv_len, pos0, n, k_out, v_out, stream);
+}
+
+int wi_paged_gather8(wi_paged* pc, int batch, int layers, const void* k_pages, const void* v_pages,
+                     const void* k_scales, const void* v_scales, const int32_t* block_table, const int32_t* kv_len,
+                     long long pos0, long long n, void* k_out, void* v_out, void* stream) {
+  const WiPagedScales s = {static_cast<unsigned char*>(const_cast<void*>(k_scales)),
+                           static_cast<unsigned char*>(const_cast<void*>(v_scales))};
+  return gather_any(pc, batch, layers, k_pages, v_pages, &s, block_table, kv_len, pos0, n, k_out, v_out, stream);
 }
 
 }  // extern "C"

@@ -430,6 +430,17 @@ typedef struct {
  * default stream, on which it is cleared: the handle may be used on any stream at once). */
 int wi_paged_create(const wi_paged_config* cfg, wi_paged** out);
 
+/*
+ * Positions of several axes (time, height and width of a picture's or a video's
+ * tokens): pair i of the rotation turns by the position on axis[i].  axis: host
+ * int32 [rotary_dim / 2], each in [0, n_axes), copied; n_axes in 1 .. 4, where 1
+ * (as after wi_paged_create) takes axis away again.  From then on `positions` of
+ * wi_paged_write and wi_paged_write8 is [n_axes][n_tokens].  A token whose first
+ * axis' position is negative is padding; on other axes negative positions turn the
+ * other way.  Calls that are in a graph keep the axes they were captured with.
+ */
+int wi_paged_axes(wi_paged* pc, int n_axes, const int32_t* axis);
+
 /* Synchronise the device and report what kernels of this handle's calls found wrong
  * since the last check: WI_OK, or WI_EDEVICE with a message. */
 int wi_paged_check(wi_paged* pc);
@@ -518,6 +529,53 @@ int wi_paged_attention(wi_paged* pc, int batch, int n_tokens, const void* q, con
 int wi_paged_gather(wi_paged* pc, int batch, int layers, const void* k_pages, const void* v_pages,
                     const int32_t* block_table, const int32_t* kv_len, long long pos0, long long n, void* k_out,
                     void* v_out, void* stream);
+
+/*
+ * The paged cache in 8 bits: half the memory, and half of what attention reads.
+ * k_pages and v_pages are e4m3 [n_pages][n_kv_heads][page_size][128] (sign, 4
+ * exponent bits of bias 7, 3 mantissa bits; largest 448; all ones is NaN, there
+ * is no infinity), k_scales and v_scales [n_pages][n_kv_heads][page_size / 16]
+ * bytes, one for every group of sixteen positions of a head: byte x is the factor
+ * 2^(x - 127) on the group's values.  Device, 16-byte aligned; tables, lengths and
+ * slots are those of the bf16 pools.
+ *
+ * wi_paged_write8 is wi_paged_write into such pools (slots are needed).  What a
+ * slot gets is the fp32 key or value over its group's scale, rounded to the
+ * nearest e4m3 (ties to even; infinities and NaN become NaN).  A group's scale is
+ * the smallest power of two, 2^-64 at least, with which its largest finite value
+ * is 448 at most; so no value saturates, and a value keeps four significant bits
+ * unless it is below 2^-6 of the scale.  It is worked out from what the call
+ * writes and, where the call's first slot of the group is not the group's first,
+ * from the scale that stands there: where that is larger it stays, else the rows
+ * in front of the call's are rounded again to the new one, which loses nothing
+ * but what falls below 2^-6 of it.  A group whose first slot the call writes
+ * begins anew; rows behind the call's last stay as they were.  Tokens of one
+ * call that share a group have to follow one another, in rising slots without a
+ * gap (as wi_paged_tables gives them): otherwise that group's contents are
+ * unspecified.
+ */
+int wi_paged_write8(wi_paged* pc, int n_tokens, const void* q, long long q_stride, const void* k, long long k_stride,
+                    const void* v, long long v_stride, const void* q_weight, const void* k_weight,
+                    const int32_t* positions, const int32_t* slots, void* q_out, void* k_pages, void* v_pages,
+                    void* k_scales, void* v_scales, void* stream);
+
+/*
+ * wi_paged_attention over 8-bit pools: the same tables, rows and masks, with keys and values that are a pool's
+ * values times their group's scale.  What lies at positions that a token does not see has no influence, NaN and
+ * scales included.  Queries and the softmax lose nothing to the 8 bits; the weights are held to 2^-10 of themselves or
+ * better for the product with V.
+ */
+int wi_paged_attention8(wi_paged* pc, int batch, int n_tokens, const void* q, const void* k_pages,
+                        const void* v_pages, const void* k_scales, const void* v_scales, const int32_t* block_table,
+                        const int32_t* q_start, const int32_t* kv_len, void* out, float* lse, void* stream);
+
+/*
+ * wi_paged_gather from 8-bit pools: k_out and v_out are bf16, value times scale (exact, unless it leaves bf16's range).
+ * Layer l's scales start l * n_pages * n_kv_heads * page_size / 16 bytes into k_scales / v_scales.
+ */
+int wi_paged_gather8(wi_paged* pc, int batch, int layers, const void* k_pages, const void* v_pages,
+                     const void* k_scales, const void* v_scales, const int32_t* block_table, const int32_t* kv_len,
+                     long long pos0, long long n, void* k_out, void* v_out, void* stream);
 
 /* Error-path testing: with the environment variable WI_FAIL_ALLOC_AT=n (n >= 1),
  * the n-th device allocation made for any index fails as out-of-memory; the

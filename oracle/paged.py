@@ -99,3 +99,59 @@ def gather(pools, table, kv_len, pos0, n):
                 r = rows_of(pools[layer], table[b], h, int(kv))[pos0:pos0 + n]
                 out[b, layer, h, :len(r)] = r
     return out
+
+
+# ------------------------------------------------------------------ in 8 bits ----
+#
+# A pool in 8 bits is (values [n_pages][n_kv_heads][page][128], exponents [n_pages][n_kv_heads][page // 16]): a row is
+# its values times 2 ** exponent of its group of sixteen positions.
+
+GROUP = 16
+LOWEST = -64   # the smallest exponent
+
+
+def e4m3(x):
+    """The nearest number of four significant bits at 2^-6 or above, multiple of 2^-9 below that (ties to even)."""
+    x = np.asarray(x, np.float64)
+    _, e = np.frexp(np.where(np.isfinite(x), x, 0.0))
+    step = np.ldexp(1.0, np.maximum(e, -5) - 4)
+    with np.errstate(invalid="ignore"):
+        return np.where(np.isfinite(x), np.rint(x / step) * step, np.nan)
+
+
+def exponent(top):
+    """The smallest exponent e >= LOWEST with top <= 448 * 2^e."""
+    e = LOWEST
+    while top > np.ldexp(448.0, e):
+        e += 1
+    return e
+
+
+def append8(values, exps, x, slots):
+    """The pool (values, exps) after the rows x [token][n_kv_heads][128] came to their slots (-1: nowhere)."""
+    values, exps = np.array(values, np.float64), np.array(exps, np.int64)
+    page = values.shape[2]
+    groups = {}
+    for t, s in enumerate(slots):
+        if s >= 0:
+            groups.setdefault(int(s) // GROUP, []).append((int(s) % GROUP, t))
+    for g, rows in groups.items():
+        at, sub = divmod(g, page // GROUP)
+        begin = min(o for o, _ in rows)
+        here = slice(sub * GROUP, (sub + 1) * GROUP)
+        for h in range(values.shape[1]):
+            new = np.array([x[t, h] for _, t in rows])
+            e = exponent(np.abs(new[np.isfinite(new)]).max(initial=0.0))
+            if begin > 0:
+                e = max(e, int(exps[at, h, sub]))
+                held = values[at, h, here][:begin]
+                values[at, h, here][:begin] = e4m3(np.ldexp(held, int(exps[at, h, sub]) - e))
+            exps[at, h, sub] = e
+            for (o, _), row in zip(rows, new):
+                values[at, h, sub * GROUP + o] = e4m3(np.ldexp(row, -e))
+    return values, exps
+
+
+def widened(values, exps):
+    """The rows that a pool in 8 bits stands for."""
+    return np.ldexp(np.asarray(values, np.float64), np.repeat(np.asarray(exps, np.int64), GROUP, axis=-1)[..., None])
