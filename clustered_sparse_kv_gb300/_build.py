@@ -21,7 +21,7 @@ STAMP = os.path.join(BUILD, "paged_binding.stamp")  # what EXT was built against
 
 SOURCES = ["wi_api.cu", "wi_build.cu", "wi_decode.cu", "wi_dense.cu", "wi_assign_tc.cu", "wi_noalloc.cu",
            "wi_grow.cu", "wi_tier.cu", "wi_selftest.cu", "wi_paged_api.cu", "wi_paged.cu", "wi_paged_attn.cu",
-           "wi_paged8.cu", "wi_paged8_attn.cu"]
+           "wi_paged8.cu", "wi_paged8_attn.cu", "wi_paged8_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

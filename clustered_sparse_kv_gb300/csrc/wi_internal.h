@@ -62,6 +62,8 @@ bool wi_encode_rows_sw128(CUtensorMap* map, const void* base, unsigned long long
 // group, column half, group), box = box_rows / 8 whole groups, 128-byte swizzle.  A box lands as
 // [group][column half][8 rows][128 B], so one copy brings rows whole, and every group lies 2048 bytes from the next.
 bool wi_encode_pages_sw128(CUtensorMap* map, const void* base, unsigned long long rows, unsigned box_rows);
+// 2-D map over rows of 128 bytes, box_rows of them at a time, 128-byte swizzle.
+bool wi_encode_bytes_sw128(CUtensorMap* map, const void* base, unsigned long long rows, unsigned box_rows);
 // 3-D bf16 tensor map over [tokens][heads][128], box = 64 columns x box_heads x box_tokens, 128-byte swizzle.
 bool wi_encode_heads_sw128(CUtensorMap* map, const void* base, unsigned long long tokens, unsigned heads,
                            unsigned box_heads, unsigned box_tokens);

@@ -1,0 +1,8 @@
+// wi_paged8.h -- host-side declarations shared by the sources of the attention in 8 bits.
+#pragma once
+#include "wi_paged.h"
+
+// Whether a call's tiles have few rows, as single tokens' have.
+bool wi_paged_few(const WiPagedGeom& g, const WiPagedAttn& a);
+cudaError_t wi_launch_paged_few(const WiPagedGeom& g, const WiPagedAttn& a, const WiPagedScales& s, int sms, void* scratch,
+                                int* err, cudaStream_t st);

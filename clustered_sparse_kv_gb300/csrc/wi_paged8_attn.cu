@@ -10,6 +10,7 @@
 #include "wi_e4m3.cuh"
 #include "wi_internal.h"
 #include "wi_paged.h"
+#include "wi_paged8.h"
 #include "wi_pipe.cuh"
 
 namespace {
@@ -154,6 +155,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_paged_attention8(WiPagedAttn A,
 
 cudaError_t wi_launch_paged_attention8(const WiPagedGeom& g, const WiPagedAttn& a, const WiPagedScales& s, int sms,
                                        void* scratch, int* err, cudaStream_t st) {
+  if (wi_paged_few(g, a)) return wi_launch_paged_few(g, a, s, sms, scratch, err, st);
   return wi_launch_chained(k_paged_attention8, dim3((unsigned)(a.n_tokens * (long long)g.Hkv)), 32 * kWarps, 0, st, a, s,
                            g.Hq, g.Hkv, g.G, g.page, g.n_pages, g.max_pages, err);
 }

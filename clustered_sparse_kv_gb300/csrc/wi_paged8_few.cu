@@ -1,0 +1,710 @@
+// wi_paged8_few.cu -- attention over the paged cache in 8 bits where a tile has few rows: single tokens above all.
+//
+// The products are turned, so that the 128 rows of a tensor-core tile are the
+// block's 128 positions, and then a head's 128 elements, with the few queries
+// as columns:
+//   S^T [position][row] = K Q^T       A = K as it lies in the cache, B = Q
+//   O^T [element][row] += V^T P^T     A = V as it lies (M-major), B = P
+// both in e4m3, which keys and values are held in.  Queries and weights are
+// not, and are sums of e4m3 pieces.  A bf16 query is a first piece of four
+// significant bits and a rest of four, exactly (over the row's largest element;
+// what is below 2^-18 of that may be lost), so Q has two columns per row and S
+// is added up.  A weight has four pieces with a column, and so a sum in tensor
+// memory, each: columns cost next to nothing here, and each piece has its own
+// power of two, so that together they hold twelve bits of a weight down to 2^-9
+// and no less than 2^-28 of the largest (a sink of attention may weigh a
+// million times more than what is left of the row).
+//
+// A thread of the four softmax warps has one position: its group's two scales,
+// its score of every row, and its weights' pieces, which it stores as one or
+// two 16-byte pieces of B.  The value's scale 2^e goes into the weight,
+// p' = 2^(score + e - m), and out of the sum, l += p' 2^-e; m is a row's
+// reference, near the largest score + e so far.  It moves only when a weight
+// would pass 448 (every thread asks, by one barrier a block): then O is
+// rescaled and the block done with the new one.
+//
+// One warp brings the blocks by TMA into rings of three keys' and three values'
+// blocks, with the groups' scales beside the values; one issues the products.
+// Two CTAs share an SM, so that one's start and end lie behind the other's
+// reads.  Runs of units, and parts that the last CTA of an item adds up, as in
+// the bf16 attention.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstddef>
+
+#include "wi_common.cuh"
+#include "wi_e4m3.cuh"
+#include "wi_internal.h"
+#include "wi_paged.h"
+#include "wi_paged8.h"
+#include "wi_paged_walk.cuh"
+#include "wi_pipe.cuh"
+#include "wi_tc.cuh"
+
+namespace {
+
+constexpr int kStages = 3;
+constexpr int kBlockBytes = kRows * WI_D;  // of keys or of values
+constexpr int kSoftWarps = 4;
+constexpr int kSoftThreads = 32 * kSoftWarps;
+constexpr int kThreads = kSoftThreads + 64;
+constexpr int kLead = 2;    // units in front of an item's blocks, for what its start and end cost
+constexpr int kLeast = 4;   // units of a run
+// Blocks after which the tensor cores' sums are added up in fp32: their additions cut bits off.
+constexpr int kFlush = 1024;
+constexpr int kPieces = 4;
+constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
+constexpr float kLn2 = 0.6931471805599453f;
+// A new reference makes the row's largest weight 2^2; it is taken where one passes 2^8.5, or where a score is so far above
+// it (through values of a tiny scale) that the sum might leave fp32.
+constexpr float kTop = 2.f, kMost = 8.5f, kFar = 64.f, kFarMost = 80.f;
+
+// What the pieces of a weight are multiplied by, one on top of the other: the first three take four bits each, the last
+// one what is too small for them.
+__device__ __forceinline__ constexpr float step_of(int piece) { return piece == kPieces - 1 ? 256.f : 16.f; }
+__device__ __forceinline__ constexpr float size_of(int piece) {
+  return piece == 0 ? 1.f : piece == 1 ? 1.f / 16 : piece == 2 ? 1.f / 256 : 1.f / 65536;
+}
+
+// RP: rows of a tile.
+template <int RP>
+struct Smem {
+  static constexpr int kQCols = 16;            // two columns per row, sixteen at least
+  static constexpr int kPCols = kPieces * RP;
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  // Of two buffers each, block n's in n & 1: who waits for block n's has seen that of block n - 2 (S of a block is issued
+  // behind O of the one two before it), so that a phase's parity says which it is.
+  uint64_t q_full, s_full[2], p_ready[2], o_done[2], drained;
+  uint32_t tmem_base;
+  int last;                     // this CTA merges the item that it just added to
+  int poison;                   // number + 1 of the last segment with a NaN value that not every row sees
+  int mask[kSoftWarps];         // rows that take a new reference
+  long long scan[kThreads / 32];
+  Run run;
+  float q_scale[RP];
+  float xch[kSoftWarps][RP];
+  float sum[kSoftWarps][RP];
+  float scale[kStages][2][kRows / kGroup];  // 2^e of the keys' groups; e of the values'
+  float factor[32][RP];         // of the parts that are added up
+  float joined[3][RP];
+  alignas(1024) unsigned char q[kQCols * WI_D];      // K-major, 128-byte swizzle
+  unsigned char p[2][kPCols * kRows];                // [16 columns][position][16 B]
+  alignas(1024) unsigned char k[kStages][kBlockBytes];
+  unsigned char v[kStages][kBlockBytes];
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory"); }
+// Whether any of the softmax threads says so.
+__device__ __forceinline__ bool soft_any(bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)x), "n"(kSoftThreads)
+      : "memory");
+  return any != 0;
+}
+
+// One pass over the pieces of RP weights: word w of piece i holds rows 4w .. 4w + 3.
+template <int RP>
+__device__ __forceinline__ void split(float (&x)[RP], uint32_t (&out)[kPieces][RP / 4]) {
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+#pragma unroll
+    for (int w = 0; w < RP / 4; ++w) {
+      float* y = x + 4 * w;
+      const uint32_t a = e4m3x2_of(y[0], y[1]), b = e4m3x2_of(y[2], y[3]);
+      out[i][w] = a | b << 16;
+      if (i + 1 < kPieces) {
+        const float2 fa = e4m3x2_to_f32x2(a), fb = e4m3x2_to_f32x2(b);
+        y[0] = (y[0] - fa.x) * step_of(i + 1);
+        y[1] = (y[1] - fa.y) * step_of(i + 1);
+        y[2] = (y[2] - fb.x) * step_of(i + 1);
+        y[3] = (y[3] - fb.y) * step_of(i + 1);
+      }
+    }
+  }
+}
+
+struct Few {
+  Params P;
+  WiPagedScales s;
+};
+
+// The queries of a segment's tile as e4m3 pieces, two rows of shared memory each.  A row of infinities or NaN gets a scale
+// that is no number, and so do all its scores.
+template <int RP, typename W>
+__device__ __forceinline__ void load_queries(const Params& P, Smem<RP>& sm, const W& w) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int r = warp; r < RP; r += kSoftWarps) {
+    const int tok = r / P.G, ti = w.tile * w.tp + tok;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (tok < P.tq && ti < w.r.n)
+      load_bf16x4(static_cast<const bf16*>(P.a.q) + ((long long)(w.r.s0 + ti) * P.Hq + w.kh * P.G + r - tok * P.G) * WI_D + 4 * lane, x);
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) top = max(top, __float_as_uint(x[c]) & 0x7fffffffu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    // the row's largest element lies in [128, 256): e is its exponent less 7, within what 2^-e can be
+    const int e = min(max((int)(top >> 23) - 127 - 7, -126), 126);
+    const float f = pow2(-e);
+    float y[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) y[c] = top < 0x7f800000u ? x[c] * f : 0.f;
+    const uint32_t a = e4m3x2_of(y[0], y[1]), b = e4m3x2_of(y[2], y[3]);
+    const float2 fa = e4m3x2_to_f32x2(a), fb = e4m3x2_to_f32x2(b);
+    const uint32_t rest = e4m3x4_of(y[0] - fa.x, y[1] - fa.y, y[2] - fb.x, y[3] - fb.y);
+    const uint32_t chunk = lane >> 2, in = (lane & 3) * 4;
+    *reinterpret_cast<uint32_t*>(sm.q + r * WI_D + ((chunk ^ (r & 7)) << 4) + in) = a | b << 16;
+    *reinterpret_cast<uint32_t*>(sm.q + (RP + r) * WI_D + ((chunk ^ ((RP + r) & 7)) << 4) + in) = rest;
+    if (lane == 0) sm.q_scale[r] = top < 0x7f800000u ? pow2(e) * kScaleLog2 : __uint_as_float(0x7fc00000u);
+  }
+}
+
+// out and lse of an item that was cut between CTAs, added up in CTA order: thread d has column d of every row.
+template <int RP>
+__device__ __noinline__ void join_parts(const Params& P, Smem<RP>& sm, const Split& sp, int c0) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, parts = sp.last - c0 + 1;
+  auto part = [&](int i) -> const float* { return P.parts.slot(2 * (c0 + i) + (i == 0 ? 1 : 0)); };
+  float acc[RP];
+#pragma unroll
+  for (int r = 0; r < RP; ++r) acc[r] = 0.f;
+  if (tid < RP) {
+    sm.joined[0][tid] = -INFINITY;
+    sm.joined[1][tid] = 0.f;
+  }
+  soft_barrier();
+  for (int i0 = 0; i0 < parts; i0 += 32) {
+#pragma unroll
+    for (int r = warp; r < RP; r += kSoftWarps) {  // a warp has a row's factors, a lane a part's
+      float m = -INFINITY, l = 0.f;
+      if (i0 + lane < parts) {
+        m = __ldcg(part(i0 + lane) + r);
+        l = __ldcg(part(i0 + lane) + RP + r);
+      }
+      const float old = sm.joined[0][r], top = fmaxf(old, warp_max(m)), ref = top == -INFINITY ? 0.f : top;
+      const float f = ex2(m - ref), back = ex2(old - ref), z = warp_sum(f * l);
+      sm.factor[lane][r] = f;
+      __syncwarp();
+      if (lane == 0) {
+        sm.joined[0][r] = top;
+        sm.joined[1][r] = sm.joined[1][r] * back + z;
+        sm.joined[2][r] = back;
+      }
+    }
+    soft_barrier();
+#pragma unroll
+    for (int r = 0; r < RP; ++r) acc[r] *= sm.joined[2][r];
+    const int n = min(32, parts - i0);
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float4* o = reinterpret_cast<const float4*>(part(i0 + i) + (2 + tid) * RP);
+#pragma unroll
+      for (int q = 0; q < RP / 4; ++q) {
+        const float4 x = __ldcg(o + q);
+        acc[4 * q] += x.x * sm.factor[i][4 * q];
+        acc[4 * q + 1] += x.y * sm.factor[i][4 * q + 1];
+        acc[4 * q + 2] += x.z * sm.factor[i][4 * q + 2];
+        acc[4 * q + 3] += x.w * sm.factor[i][4 * q + 3];
+      }
+    }
+    soft_barrier();  // the factors are read
+  }
+#pragma unroll
+  for (int r = 0; r < RP; ++r) {
+    const int tok = r / P.G;
+    if (tok >= P.tq || tok >= sp.cnt) break;
+    const long long at = (long long)(sp.row0 + tok) * P.Hq + sp.kh * P.G + r - tok * P.G;
+    const float l = sm.joined[1][r];
+    static_cast<bf16*>(P.a.out)[at * WI_D + tid] = __float2bfloat16_rn(l == 0.f ? 0.f : acc[r] / l);
+    if (P.a.lse && tid == r) P.a.lse[at] = l == 0.f ? -INFINITY : sm.joined[0][r] * kLn2 + logf(l);
+  }
+}
+
+template <int RP>
+__global__ void __launch_bounds__(kThreads, 2) k_paged_attention8_few(const __grid_constant__ CUtensorMap map_k,
+                                                                     const __grid_constant__ CUtensorMap map_v,
+                                                                     const __grid_constant__ Few F) {
+  using Sm = Smem<RP>;
+  using Walk = WalkOver<kLead, 1, 0>;
+  const Params& P = F.P;
+  extern __shared__ __align__(1024) unsigned char raw[];
+  pdl_trigger();
+  Sm& sm = *reinterpret_cast<Sm*>(raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (smem_addr(raw) & 1023u) {  // the swizzled tiles need 1024-byte alignment; never run misaligned
+    if (tid == 0) atomicOr(P.err, WI_DEVERR_BAD_ROW);
+    return;
+  }
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sm.k_full[s], 1);
+      mbar_init(&sm.k_empty[s], 1);
+      mbar_init(&sm.v_full[s], 1);
+      mbar_init(&sm.v_empty[s], 1);
+    }
+    mbar_init(&sm.q_full, kSoftWarps);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sm.s_full[t], 1);
+      mbar_init(&sm.p_ready[t], kSoftWarps);
+      mbar_init(&sm.o_done[t], 1);
+    }
+    mbar_init(&sm.drained, 1);
+    sm.poison = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  constexpr uint32_t kCols = 64;  // S twice (16 columns), O
+  if (warp == kSoftWarps + 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem_base)),
+                 "n"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == kSoftWarps && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
+  }
+  for (int i = tid; i < Sm::kQCols * WI_D / 16; i += kThreads)  // columns that no query has: zero
+    reinterpret_cast<uint4*>(sm.q)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  pdl_wait();
+  tc_fence_before();
+  const bool any = find_run<kLead, 1, kThreads>(P, kLeast, sm.scan, &sm.run);  // (with a barrier of all threads)
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;  // S at columns 0 and 16, O at 32
+  if (!any) {  // the whole CTA leaves
+    if (warp == kSoftWarps + 1)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kCols) : "memory");
+    return;
+  }
+
+  if (warp < kSoftWarps) {
+    // ---------------- softmax: a thread per position, then per element
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    bool ok = true;  // after one timed-out wait the warp waits no more and writes nothing, but meets every barrier
+    int n = 0;       // blocks so far
+    Walk w(P, sm.run.start, sm.run.req);
+    bool more = w.next(P);
+    auto ask = [&] {  // the queries of the segment: the products of the one before are done with theirs
+      load_queries<RP>(P, sm, w);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full);
+    };
+    if (more) ask();
+    soft_barrier();
+    for (int seg = 0; more; ++seg) {
+      float m[RP], l[RP], acc[RP], l_sum[RP], q_scale[RP];
+      int lim[RP];  // the last position that a row sees; of no token: -1
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        m[r] = -INFINITY;
+        l[r] = acc[r] = l_sum[r] = 0.f;
+        const int tok = r / P.G, ti = w.tile * w.tp + tok;
+        lim[r] = tok < P.tq && ti < w.r.n ? (int)(w.p0 + ti) : -1;
+        q_scale[r] = sm.q_scale[r];
+      }
+      const int whole = w.first_pos();  // the last position that all rows see
+      for (int j = 0; j < w.nb; ++j, ++n) {
+        const int st = n % kStages, buf = n & 1;
+        if (ok) ok = mbar_wait(&sm.s_full[buf], (n >> 1) & 1, P.err);
+        if (ok) ok = mbar_wait(&sm.v_full[st], (n / kStages) & 1, P.err);
+        tc_fence_after();
+        float s[RP], y[RP];
+        {
+          uint32_t a[2 * RP];
+          if (RP == 4)
+            tmem_ld8_nowait(tmem + lanes + buf * 16, reinterpret_cast<uint32_t(&)[8]>(a));
+          else
+            tmem_ld16_nowait(tmem + lanes + buf * 16, reinterpret_cast<uint32_t(&)[16]>(a));
+          tmem_wait_ld();
+#pragma unroll
+          for (int r = 0; r < RP; ++r) s[r] = (__uint_as_float(a[r]) + __uint_as_float(a[RP + r])) * q_scale[r];
+        }
+        const float k_scale = sm.scale[st][0][tid / kGroup], v_exp = sm.scale[st][1][tid / kGroup];
+        const int pos = (w.b0 + j) * kRows + tid;
+        const bool fresh = j % kFlush == 0;  // O begins anew with this block
+        if (fresh && j > 0) {
+          if (ok) ok = mbar_wait(&sm.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, P.err);
+          tc_fence_after();
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+            for (int q = 0; q < RP; q += 4) {
+              uint32_t a[4];
+              tmem_ld4_nowait(tmem + lanes + 32 + i * RP + q, a);
+              tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 4; ++c) acc[q + c] += __uint_as_float(a[c]) * size_of(i);
+            }
+#pragma unroll
+          for (int r = 0; r < RP; ++r) {  // the sum so far, apart from what is to come
+            l_sum[r] += l[r];
+            l[r] = 0.f;
+          }
+        }
+        bool grown = false;
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          s[r] = pos <= lim[r] ? s[r] * k_scale : -INFINITY;
+          y[r] = s[r] + v_exp;
+          grown |= y[r] - m[r] > kMost || s[r] - m[r] > kFarMost;
+        }
+        if (soft_any(grown)) {
+          uint32_t mine = 0;
+#pragma unroll
+          for (int r = 0; r < RP; ++r) {
+            if (y[r] - m[r] > kMost || s[r] - m[r] > kFarMost) mine |= 1u << r;
+            const float top = warp_max(fmaxf(y[r] - kTop, s[r] - kFar));
+            if (lane == 0) sm.xch[warp][r] = top;
+          }
+          mine = __reduce_or_sync(0xffffffffu, mine);
+          if (lane == 0) sm.mask[warp] = (int)mine;
+          soft_barrier();
+          const int rows = sm.mask[0] | sm.mask[1] | sm.mask[2] | sm.mask[3];
+          float f[RP];
+#pragma unroll
+          for (int r = 0; r < RP; ++r) {  // the other rows keep theirs
+            const float top = fmaxf(fmaxf(sm.xch[0][r], sm.xch[1][r]), fmaxf(sm.xch[2][r], sm.xch[3][r]));
+            f[r] = 1.f;
+            if (rows >> r & 1) {
+              f[r] = ex2(m[r] - fmaxf(m[r], top));
+              m[r] = fmaxf(m[r], top);
+            }
+            l[r] *= f[r];
+            l_sum[r] *= f[r];
+            acc[r] *= f[r];
+          }
+          if (!fresh) {
+            if (ok) ok = mbar_wait(&sm.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, P.err);
+            tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+              for (int q = 0; q < RP; q += 4) {
+                uint32_t a[4];
+                tmem_ld4_nowait(tmem + lanes + 32 + i * RP + q, a);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) a[c] = __float_as_uint(__uint_as_float(a[c]) * f[q + c]);
+                tmem_st4_nowait(tmem + lanes + 32 + i * RP + q, a);
+              }
+            tmem_wait_st();
+          }
+          soft_barrier();  // maxima and masks are read
+        }
+        const float back = pow2(-(int)v_exp);
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          y[r] = ex2(y[r] - (m[r] == -INFINITY ? 0.f : m[r]));
+          l[r] += y[r] * back;
+        }
+        uint32_t b[kPieces][RP / 4];
+        split<RP>(y, b);
+        if (RP == 4) {
+          *reinterpret_cast<uint4*>(sm.p[buf] + 16 * tid) = make_uint4(b[0][0], b[1][0], b[2][0], b[3][0]);
+        } else {
+          uint4* const to = reinterpret_cast<uint4*>(sm.p[buf] + 16 * tid);
+          to[0] = make_uint4(b[0][0], b[0][RP / 4 - 1], b[1][0], b[1][RP / 4 - 1]);
+          to[kRows] = make_uint4(b[2][0], b[2][RP / 4 - 1], b[3][0], b[3][RP / 4 - 1]);
+        }
+        if (pos > whole) {
+          // A value that not every row sees: 0 * NaN is NaN inside the product, so rows behind the request's end are zeroed,
+          // and so are NaN elements, which the end of the segment adds to the rows that see them.
+          uint4* const v = reinterpret_cast<uint4*>(sm.v[st]) + tid * (WI_D / 16);
+          bool found = false;
+#pragma unroll
+          for (int c = 0; c < WI_D / 16; ++c) {
+            uint4 x = v[c];
+            uint32_t e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              // bit 7 of the bytes whose other bits are all ones
+              const uint32_t nan = ((e[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              if (pos >= w.r.kv) {
+                e[k] = 0;
+              } else if (nan) {
+                e[k] &= ~((nan >> 7) * 0xffu);
+                found = true;
+              }
+            }
+            v[c] = make_uint4(e[0], e[1], e[2], e[3]);
+          }
+          if (found) *reinterpret_cast<volatile int*>(&sm.poison) = seg + 1;
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_ready[buf]);
+      }
+
+      // ---- the segment's end
+      const Walk done = w;
+      w.advance();
+      more = w.next(P);
+      soft_barrier();  // the queries' scales are read
+      if (more) ask();
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        l[r] = warp_sum(l[r] + l_sum[r]);
+        if (lane == 0) sm.sum[warp][r] = l[r];
+      }
+      if (ok) ok = mbar_wait(&sm.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, P.err);
+      tc_fence_after();
+      {
+        uint32_t a[kPieces][RP];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+          for (int q = 0; q < RP; q += 4)
+            tmem_ld4_nowait(tmem + lanes + 32 + i * RP + q, reinterpret_cast<uint32_t(&)[4]>(a[i][q]));
+        tmem_wait_ld();
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+#pragma unroll
+          for (int i = kPieces - 1; i >= 0; --i) acc[r] += __uint_as_float(a[i][r]) * size_of(i);
+        }
+      }
+      tc_fence_before();  // O is read: the next segment may write it
+      soft_barrier();
+#pragma unroll
+      for (int r = 0; r < RP; ++r) l[r] = (sm.sum[0][r] + sm.sum[1][r]) + (sm.sum[2][r] + sm.sum[3][r]);
+      if (*reinterpret_cast<volatile int*>(&sm.poison) == seg + 1) {
+        const int from = max(max(whole + 1, 0), done.b0 * kRows), to = min((done.b0 + done.nb) * kRows, done.r.kv);
+#pragma unroll 1
+        for (int p = from; p < to; ++p) {
+          const int i = p / P.page, pg = P.a.block_table[(long long)done.b * P.max_pages + i];
+          if (pg < 0 || pg >= P.n_pages) continue;
+          const unsigned char v = static_cast<const unsigned char*>(
+              P.a.v_pages)[(((long long)pg * P.Hkv + done.kh) * P.page + (p - i * P.page)) * WI_D + tid];
+          if ((v & 0x7f) == 0x7f) {
+#pragma unroll
+            for (int r = 0; r < RP; ++r)
+              if (p <= lim[r]) acc[r] = __uint_as_float(0x7fc00000u);
+          }
+        }
+      }
+      const bool part = done.b0 > 0 || done.nb < done.nblk;
+      if (!part) {
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          const int tok = r / P.G, ti = done.tile * done.tp + tok;
+          if (!ok || tok >= P.tq || ti >= done.r.n) break;
+          const long long at = (long long)(done.r.s0 + ti) * P.Hq + done.kh * P.G + r - tok * P.G;
+          static_cast<bf16*>(P.a.out)[at * WI_D + tid] = __float2bfloat16_rn(l[r] == 0.f ? 0.f : acc[r] / l[r]);
+          if (P.a.lse && tid == r) P.a.lse[at] = l[r] == 0.f ? -INFINITY : m[r] * kLn2 + logf(l[r]);
+        }
+      } else {
+        float* const dst = P.parts.slot(2 * (int)blockIdx.x + (done.b0 == 0 ? 1 : 0));
+#pragma unroll
+        for (int q = 0; q < RP; q += 4)
+          __stcg(reinterpret_cast<float4*>(dst + (2 + tid) * RP + q), make_float4(acc[q], acc[q + 1], acc[q + 2], acc[q + 3]));
+#pragma unroll
+        for (int r = 0; r < RP; ++r)
+          if (tid == r) {
+            __stcg(dst + r, m[r]);
+            __stcg(dst + RP + r, l[r]);
+          }
+        const long long item = sm.run.end - done.left - done.at + kLead;  // the unit of the item's first block
+        const int c0 = cta_of(item, sm.run.total, sm.run.ctas), c1 = cta_of(item + done.nblk - 1, sm.run.total, sm.run.ctas);
+        soft_barrier();  // then thread 0's release covers what all of them stored
+        if (tid == 0) {
+          sm.last = 0;
+          if (ok && ticket_acq_rel(P.tickets + c0) == (unsigned)(c1 - c0)) {
+            P.tickets[c0] = 0;
+            sm.last = 1;
+          }
+        }
+        soft_barrier();
+        if (sm.last) join_parts<RP>(P, sm, {done.r.s0 + done.tile * done.tp, done.kh, done.cnt, c1}, c0);
+      }
+      soft_barrier();  // what the threads share is read, and the next segment's queries have their scales
+    }
+  } else if (warp == kSoftWarps) {
+    // ---------------- TMA: keys, values, and the scales of their groups
+    Walk w(P, sm.run.start, sm.run.req);
+    const uint32_t on = elect_one();
+    const int per = P.box / kGroup;  // groups of a box; one lane finds the page of each group
+    constexpr int kGroups = kRows / kGroup;
+    int n = 0, asked[2] = {0, 0};  // blocks done with, blocks of keys and of values that were asked for
+    bool ok = true;
+    for (; ok && w.next(P); w.advance()) {
+      constexpr int kNone = -0x7fffffff - 1;  // behind the request's end
+      auto page_of = [&](int j) -> int {
+        const int p = (w.b0 + j) * kRows + lane * kGroup;
+        if (j >= w.nb || lane >= kGroups || p >= w.r.kv) return kNone;
+        return P.a.block_table[(long long)w.b * P.max_pages + p / P.page];
+      };
+      // a group's (row of the pool, scales), from its page; a bad page is page 0
+      auto row_of = [&](int pg, int j) -> int {
+        if (pg == kNone) return -1;
+        if (pg < 0 || pg >= P.n_pages) {
+          atomicOr(P.err, WI_DEVERR_BAD_PAGE);
+          pg = 0;
+        }
+        return (pg * P.Hkv + w.kh) * P.page + ((w.b0 + j) * kRows + lane * kGroup) % P.page;
+      };
+      auto scales_of = [&](int row) -> uint32_t {
+        return row < 0 ? kScaleBias * 0x101u : (uint32_t)F.s.k[row / kGroup] | (uint32_t)F.s.v[row / kGroup] << 8;
+      };
+      // pages are looked up three blocks ahead, scales two
+      int g2 = page_of(2), g3;
+      int r0 = row_of(page_of(0), 0), r1 = row_of(page_of(1), 1), r2;
+      uint32_t e0 = scales_of(r0), e1 = scales_of(r1), e2;
+      for (int j = 0; j < w.nb; ++j, ++n) {
+        g3 = page_of(j + 3);
+        r2 = row_of(g2, j + 2);
+        e2 = scales_of(r2);
+        const int st = n % kStages;
+        const uint32_t par = ((uint32_t)(n / kStages) & 1u) ^ 1u;
+        // boxes behind the request's end are left out: always the last ones
+        const int groups = __popc(__ballot_sync(0xffffffffu, r0 >= 0)), boxes = (groups + per - 1) / per;
+        const uint32_t bytes = (uint32_t)(boxes * P.box) * WI_D;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          uint64_t* const full = v ? &sm.v_full[st] : &sm.k_full[st];
+          if (ok && n >= kStages) ok = mbar_wait(v ? &sm.v_empty[st] : &sm.k_empty[st], par, P.err);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = smem_addr(v ? sm.v[st] : sm.k[st]);
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d_warp(on, dst + (uint32_t)(i * P.box) * WI_D, v ? &map_v : &map_k, 0,
+                             __shfl_sync(0xffffffffu, r0, i * per), full);
+          if (v && lane < kGroups) {  // behind the copies: the scales may still be on their way here
+            sm.scale[st][0][lane] = pow2(scale_exponent((unsigned char)(e0 & 0xff)));
+            sm.scale[st][1][lane] = (float)scale_exponent((unsigned char)(e0 >> 8));
+          }
+          __syncwarp();
+          if (on) mbar_arrive_expect_tx(full, bytes);  // the stage's one arrival: it is full when the bytes are there
+          ++asked[v];
+        }
+        if (!ok) break;
+        r0 = r1;
+        e0 = e1;
+        r1 = r2;
+        e1 = e2;
+        g2 = g3;
+      }
+    }
+    // no copy is in flight when the CTA's shared memory goes (after a timed-out wait nobody may have waited for them)
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+      for (int s = 0; s < kStages && s < asked[v]; ++s)  // each stage's last use
+        mbar_wait(v ? &sm.v_full[s] : &sm.k_full[s], (uint32_t)((asked[v] - 1 - s) / kStages) & 1u, P.err);
+  } else {
+    // ---------------- tensor cores: one lane issues, the whole warp computes what it issues
+    Walk w(P, sm.run.start, sm.run.req);
+    const uint32_t on = elect_one();
+    constexpr uint32_t idesc_s = make_idesc_e4m3(kRows, Sm::kQCols);
+    constexpr uint32_t idesc_o = make_idesc_e4m3(WI_D, Sm::kPCols) | kIdescMMajorA | kIdescNMajorB;
+    // P without a swizzle: 128 bytes from eight positions to the next, 2048 from sixteen columns to the next
+    constexpr uint32_t kPHi = (2048u >> 4) | (1u << 14), kPLo = (128u >> 4) << 16;
+    auto all_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, P.err));
+    };
+    bool ok = true;
+    auto scores = [&](int n) -> bool {
+      const int st = n % kStages, buf = n & 1;
+      if (!all_wait(&sm.k_full[st], (uint32_t)(n / kStages) & 1u)) return false;
+      tc_fence_after();
+      const uint32_t d = __shfl_sync(0xffffffffu, tmem + (uint32_t)buf * 16, 0);
+      const uint32_t a = __shfl_sync(0xffffffffu, desc_lo_kmajor(smem_addr(sm.k[st])), 0);
+      const uint32_t b = __shfl_sync(0xffffffffu, desc_lo_kmajor(smem_addr(sm.q)), 0);
+#pragma unroll
+      for (int kk = 0; kk < WI_D / 32; ++kk)
+        mma_e4m3_warp(on, d, a + kk * 2, desc_hi_sw128(1024), b + kk * 2, desc_hi_sw128(1024), idesc_s, kk > 0);
+      mma_commit_warp(on, &sm.s_full[buf]);
+      mma_commit_warp(on, &sm.k_empty[st]);
+      return true;
+    };
+    int n = 0;
+    for (int seg = 0; ok && w.next(P); ++seg, w.advance()) {
+      if (!(ok = all_wait(&sm.q_full, seg & 1))) break;
+      tc_fence_after();
+      if (!(ok = scores(n))) break;
+      for (int j = 0; j < w.nb; ++j, ++n) {
+        if (j + 1 < w.nb && !(ok = scores(n + 1))) break;
+        const int st = n % kStages, buf = n & 1;
+        if (!(ok = all_wait(&sm.p_ready[buf], (uint32_t)(n >> 1) & 1u))) break;
+        if (!(ok = all_wait(&sm.v_full[st], (uint32_t)(n / kStages) & 1u))) break;
+        tc_fence_after();
+        const uint32_t d = __shfl_sync(0xffffffffu, tmem + 32u, 0);
+        const uint32_t a = __shfl_sync(0xffffffffu, desc_lo_kmajor(smem_addr(sm.v[st])), 0);
+        const uint32_t b = __shfl_sync(0xffffffffu, (smem_addr(sm.p[buf]) >> 4) | kPLo, 0);
+        const uint32_t add = __shfl_sync(0xffffffffu, (uint32_t)(j % kFlush != 0), 0);
+#pragma unroll
+        for (int kk = 0; kk < kRows / 32; ++kk)
+          mma_e4m3_warp(on, d, a + kk * (32 * WI_D / 16), desc_hi_sw128(1024), b + kk * 32, kPHi, idesc_o, kk > 0 ? 1u : add);
+        mma_commit_warp(on, &sm.v_empty[st]);
+        mma_commit_warp(on, &sm.o_done[buf]);
+      }
+    }
+    // every product is done before the tensor memory goes
+    mma_commit_warp(on, &sm.drained);
+    mbar_wait(&sm.drained, 0, P.err);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kSoftWarps + 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kCols) : "memory");
+  }
+}
+
+template <int RP>
+cudaError_t launch(const Few& F, const CUtensorMap& map_k, const CUtensorMap& map_v, int grid, cudaStream_t st) {
+  static int smem_set[kWiSmemDevices] = {};
+  auto* kernel = k_paged_attention8_few<RP>;
+  static_assert(offsetof(Smem<RP>, q) % 1024 == 0 && offsetof(Smem<RP>, k) % 1024 == 0, "tiles must start 1024-byte aligned");
+  static_assert(2 * (sizeof(Smem<RP>) + 1024) <= 228 * 1024, "two CTAs to an SM");
+  const cudaError_t e = wi_ensure_smem(kernel, sizeof(Smem<RP>), smem_set);
+  if (e != cudaSuccess) return e;
+  return wi_launch_chained(kernel, dim3((unsigned)grid), kThreads, sizeof(Smem<RP>), st, map_k, map_v, F);
+}
+
+}  // namespace
+
+bool wi_paged_few(const WiPagedGeom& g, const WiPagedAttn& a) {
+  const int tq = (g.G <= 4 ? 4 : 8) / g.G;
+  return a.n_tokens <= (long long)a.batch * tq;
+}
+
+cudaError_t wi_launch_paged_few(const WiPagedGeom& g, const WiPagedAttn& a, const WiPagedScales& s, int sms, void* scratch,
+                                int* err, cudaStream_t st) {
+  const int rp = g.G <= 4 ? 4 : 8;
+  Few F;
+  Params& P = F.P;
+  F.s = s;
+  P.a = a;
+  P.Hq = g.Hq;
+  P.Hkv = g.Hkv;
+  P.G = g.G;
+  P.tq = rp / g.G;
+  P.page = g.page;
+  P.n_pages = g.n_pages;
+  P.max_pages = g.max_pages;
+  // a box of a block lies inside one page: the largest power of two that divides the page, 128 at most
+  P.box = g.page & -g.page;
+  if (P.box > kRows) P.box = kRows;
+  P.splits = nullptr;
+  P.tickets = static_cast<unsigned*>(scratch);
+  P.parts = {reinterpret_cast<float*>(static_cast<char*>(scratch) + kPagedTicketBytes), rp, 1};
+  P.err = err;
+  CUtensorMap map_k, map_v;
+  const unsigned long long rows = (unsigned long long)g.n_pages * g.Hkv * g.page;
+  if (!wi_encode_bytes_sw128(&map_k, a.k_pages, rows, (unsigned)P.box) ||
+      !wi_encode_bytes_sw128(&map_v, a.v_pages, rows, (unsigned)P.box))
+    return cudaErrorInvalidValue;
+  const int grid = 2 * sms < kPagedMaxSms ? 2 * sms : kPagedMaxSms;
+  return rp == 4 ? launch<4>(F, map_k, map_v, grid, st) : launch<8>(F, map_k, map_v, grid, st);
+}

@@ -62,12 +62,12 @@
 #include "wi_common.cuh"
 #include "wi_internal.h"
 #include "wi_paged.h"
+#include "wi_paged_walk.cuh"
 #include "wi_pipe.cuh"
 #include "wi_tc.cuh"
 
 namespace {
 
-constexpr int kRows = 128;                     // rows of a tile, and positions of a block
 constexpr int kStages = 5;
 constexpr int kTileBytes = kRows * WI_D * 2;   // 32 KB: two halves of 64 columns
 constexpr int kHalfBytes = kTileBytes / 2;
@@ -100,33 +100,14 @@ constexpr long long kBlockCycles = 1 << 14;
 // fp32 any precision.
 constexpr float kAgain = 65536.f;
 
-// A partial result: m, then l, of every row, then O, column-major (a thread owns a row, so column-major stores of a
-// warp are contiguous).  Two tiles of 128 rows, or, where a call has no more, one of kMergeHere or kFewRows: those of
+template <bool LONG>
+using Walk = WalkOver<kLead, 2, LONG ? kLongest : 0>;
+
+// A partial result holds two tiles of 128 rows, or, where a call has no more, one of kMergeHere or kFewRows: those of
 // all CTAs lie within 5 or 1.3 MB then, which a merge reads with fewer address translations.
 constexpr int kFewRows = 8;
 constexpr int kMergeHere = 32;  // rows per kv head of a call up to which the attention kernel merges itself
-struct Parts {
-  float* base;
-  int rows, tiles;
-  __device__ __forceinline__ float* slot(int i) const {
-    return base + (long long)i * (tiles * rows * (2 + WI_D));
-  }
-  __device__ __forceinline__ int m(int t, int r) const { return t * rows + r; }
-  __device__ __forceinline__ int l(int t, int r) const { return (tiles + t) * rows + r; }
-  __device__ __forceinline__ int o(int t, int d, int r) const { return (2 * tiles + t * WI_D + d) * rows + r; }
-};
 constexpr size_t kPartBytes = 2 * kRows * (2 + WI_D) * 4;
-
-// Request b as the kernel reads it; a request with impossible numbers has no tokens (CTA 0 reports it).
-struct Req {
-  int s0, n, kv, ok;
-};
-
-// Where a CTA stands in its run: request, kv head, tile pair, the next unit of that item (its first kLead units stand
-// for no block), and the units of the run still to come.
-struct Cursor {
-  int b, kh, tile, at, left;
-};
 
 struct Smem {
   uint64_t full[kStages], empty[kStages];
@@ -169,131 +150,6 @@ struct Ring {
       par ^= 1;
     }
   }
-};
-
-// An item that CTA c begins and others go on with: what the merge needs of it.  last < 0: there is none.
-struct Split {
-  int row0, kh, cnt, last;  // first token (row of q), kv head, tokens, the item's last CTA
-};
-
-struct Params {
-  WiPagedAttn a;
-  int Hq, Hkv, G, tq;       // tq = tokens per tile
-  int page, n_pages, max_pages, box;
-  Parts parts;
-  Split* splits;
-  unsigned* tickets;        // of the items, at the CTA that begins each; zero between calls; null: k_paged_merge merges
-  int* err;
-};
-
-__device__ __forceinline__ Req load_req(const Params& P, int b) {
-  Req r;
-  r.s0 = P.a.q_start[b];
-  const int s1 = P.a.q_start[b + 1];
-  r.kv = P.a.kv_len[b];
-  r.ok = r.s0 >= 0 && s1 >= r.s0 && s1 <= P.a.n_tokens && r.kv >= 0 && (long long)r.kv <= (long long)P.max_pages * P.page;
-  r.n = r.ok ? s1 - r.s0 : 0;
-  return r;
-}
-
-// Blocks of the tile pair that ends before token `end` of a request whose token 0 sits at p0: at least one,
-// so that rows that see nothing are visited too.
-__device__ __forceinline__ int blocks_to(long long p0, long long end) {
-  const long long e = p0 + end;
-  return e <= kRows ? 1 : (int)((e + kRows - 1) / kRows);
-}
-
-// Sum over i < n of floor((a i + b) / 128), a, b >= 0, by the steps of Euclid's algorithm on a and the divisor m (the
-// known way to a floor sum): whole multiples of m are taken out of a and b, and what is left counts lattice points under
-// a line, which is the same problem with a and m exchanged (n <= 2^19, so that after the first step everything but the
-// sum fits 32 bits).
-__device__ long long floor_sum(int n, int a, long long b) {
-  if (n <= 0) return 0;
-  long long s = (long long)n * (n - 1) / 2 * (a >> 7) + n * (b >> 7);
-  uint32_t k = (uint32_t)n, m = 128, u = (uint32_t)a & 127u, v = (uint32_t)b & 127u;
-  for (;;) {
-    const uint32_t y = u * k + v;
-    if (y < m) return s;
-    k = y / m;
-    v = y % m;
-    const uint32_t t = u;
-    u = m;
-    m = t;
-    s += (long long)k * (k - 1) / 2 * (u / m) + (long long)k * (v / m);
-    u %= m;
-    v %= m;
-  }
-}
-
-// Units of the first `m` tile pairs (none of them the last one, which may be shorter).
-__device__ long long units_before(long long p0, int tp, int m) {
-  long long z = 0;  // pairs that end at or before position 0: one block each
-  if (p0 < 0) z = min(-p0 / tp, (long long)m);
-  return z + floor_sum((int)(m - z), tp, p0 + (z + 1) * tp + kRows - 1) + (long long)kLead * m;
-}
-
-// a / b; 64-bit division only where 32 bits do not do.
-__device__ __forceinline__ long long quot(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
-
-// The run, one item's part after the other.
-template <bool LONG>
-struct Walk : Cursor {
-  Req r;
-  int tp, tiles;
-  // the current segment: what the run holds of one item
-  int cnt, single, nblk, b0, nb, took;   // tokens, one tile, blocks of the item, first block, blocks, units
-  long long p0;           // position of the request's token 0
-
-  __device__ __forceinline__ Walk(const Params& P, const Cursor& c, const Req& q) : Cursor(c) {
-    tp = 2 * P.tq;
-    set(q);
-  }
-  __device__ __forceinline__ void set(const Req& q) {
-    r = q;
-    p0 = (long long)r.kv - r.n;
-    tiles = (r.n + tp - 1) / tp;
-  }
-  // The next segment of the run that has blocks; false at the run's end.
-  __device__ __forceinline__ bool next(const Params& P) {
-    while (left > 0) {
-      while (tile >= tiles) {   // past the request's last pair: next kv head, next request with tokens
-        tile = 0;
-        if (r.n == 0 || ++kh == P.Hkv) {
-          kh = 0;
-          if (++b >= P.a.batch) return false;
-          set(load_req(P, b));
-        }
-      }
-      cnt = min(tp, r.n - tile * tp);
-      single = cnt <= P.tq;
-      nblk = blocks_to(p0, (long long)tile * tp + cnt);
-      took = min(nblk + kLead - at, left);
-      if (LONG) took = min(took, kLead + kLongest);
-      b0 = max(0, at - kLead);
-      nb = max(0, at + took - kLead) - b0;
-      if (nb > 0) return true;
-      advance();
-    }
-    return false;
-  }
-  __device__ __forceinline__ void advance() {
-    left -= took;
-    at += took;
-    if (at >= nblk + kLead) {
-      at = 0;
-      ++tile;
-    }
-  }
-  __device__ __forceinline__ int first_pos() const { return (int)(p0 + (long long)tile * tp); }
-  // The item's first block that not all of its rows see whole.
-  __device__ __forceinline__ int first_fix() const {
-    const int f = first_pos();
-    return f < 0 ? 0 : (f + 1) / kRows;
-  }
-  // The first position whose value row is cleaned: what all rows see stays as it is, in whole groups of eight.
-  __device__ __forceinline__ int first_clean() const { return max(0, first_pos() + 1) & ~7; }
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -394,11 +250,6 @@ __device__ __forceinline__ void add_poison(const Params& P, int b, int kh, int f
       if (nonfinite16(w >> 16)) o[2 * i + 1] += bf16_hi(w);
     }
   }
-}
-
-// The CTA whose run holds unit u of `total`, cut into `ctas` runs.
-__device__ __forceinline__ int cta_of(long long u, long long total, int ctas) {
-  return (int)quot((u + 1) * ctas - 1, total);
 }
 
 // ---- merge of an item that was cut between CTAs
@@ -566,18 +417,6 @@ __device__ __noinline__ float2 add_earlier(const Params& P, const float* src, in
   return make_float2(top, l * f + pl * g);
 }
 
-// What a place where q_start falls adds to the units: more than any grid takes, and 4096 of them fit 64 bits beside the
-// most units that a call can have (2^51).
-constexpr long long kFalls = 1LL << 50;
-
-// The requests in front of the first place where q_start falls.  Those behind it may claim rows of the ones in front of
-// it: they have no tokens.
-__device__ __noinline__ int requests_in_order(const Params& P) {
-  int b = 0;
-  while (b < P.a.batch && P.a.q_start[b + 1] >= P.a.q_start[b]) ++b;
-  return b;
-}
-
 // Units of the requests [rb0, rb1) of this thread, of the threads in front of it, and of all: what the kernel's start
 // works out in line, once more for calls that are not in order (a loop around that code took 1% of single tokens' time).
 struct Share {
@@ -590,7 +429,7 @@ __device__ __noinline__ Share share_of(const Params& P, Smem& sm, int rb0, int r
     const Req r = load_req(P, b);
     if (r.n == 0) continue;
     const long long p0 = (long long)r.kv - r.n;
-    x.mine += P.Hkv * (units_before(p0, tp, (r.n + tp - 1) / tp - 1) + kLead + blocks_to(p0, r.n));
+    x.mine += P.Hkv * (units_before<kLead>(p0, tp, (r.n + tp - 1) / tp - 1) + kLead + blocks_to(p0, r.n));
   }
   x.before = x.mine;
   for (int o = 1; o < 32; o <<= 1) {
@@ -673,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     }
     if (r.n == 0) continue;
     const int tiles = (r.n + tp - 1) / tp;
-    cost = units_before((long long)r.kv - r.n, tp, tiles - 1) + kLead + blocks_to((long long)r.kv - r.n, r.n);
+    cost = units_before<kLead>((long long)r.kv - r.n, tp, tiles - 1) + kLead + blocks_to((long long)r.kv - r.n, r.n);
     mine += P.Hkv * cost;
   }
   long long before = mine;
@@ -720,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       if (r.n == 0) continue;
       const int tiles = (r.n + tp - 1) / tp;
       const long long p0 = (long long)r.kv - r.n;
-      if (per > 1) cost = units_before(p0, tp, tiles - 1) + kLead + blocks_to(p0, r.n);
+      if (per > 1) cost = units_before<kLead>(p0, tp, tiles - 1) + kLead + blocks_to(p0, r.n);
       if (rem >= cost * P.Hkv) {
         rem -= cost * P.Hkv;
         continue;
@@ -730,9 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       int lo = 0, hi = tiles - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (units_before(p0, tp, mid) <= rem) lo = mid; else hi = mid - 1;
+        if (units_before<kLead>(p0, tp, mid) <= rem) lo = mid; else hi = mid - 1;
       }
-      if (lo > 0) rem -= units_before(p0, tp, lo);
+      if (lo > 0) rem -= units_before<kLead>(p0, tp, lo);
       sm.start = {b, kh, lo, (int)rem, (int)(u1 - u0)};
       sm.req = r;
       sm.run_end = u1;

@@ -44,6 +44,17 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// A 2-D box by the lane with on != 0 (every lane runs the setup, as for mma_bf16_warp).
+__device__ __forceinline__ void tma_load_2d_warp(uint32_t on, uint32_t dst, const CUtensorMap* map, int x, int y,
+                                                 uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar)), "r"(on)
+      : "memory");
+}
+
 // A 4-D box by the lane with on != 0 (every lane runs the setup, as for mma_bf16_warp).
 __device__ __forceinline__ void tma_load_4d_warp(uint32_t on, uint32_t dst, const CUtensorMap* map, int x, int y, int z,
                                                  int w, uint64_t* bar) {
@@ -108,6 +119,28 @@ __device__ __forceinline__ void mma_bf16_ta_warp(uint32_t on, uint32_t tmem_d, u
       : "memory");
 }
 
+// Instruction descriptor, kind::f8f6f4: fp32 accumulator, e4m3 A and B (types 0).
+__host__ __device__ constexpr uint32_t make_idesc_e4m3(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// ... bit of an A operand whose M elements are contiguous (M-major); kIdescNMajorB is B's.  With the 128-byte swizzle a
+// row of 128 such elements takes the descriptor words of a K-major one.
+constexpr uint32_t kIdescMMajorA = 1u << 15;
+
+// D (+)= A B of e4m3 operands in shared memory, issued by the lane with on != 0 (see mma_bf16_warp).
+__device__ __forceinline__ void mma_e4m3_warp(uint32_t on, uint32_t tmem_d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                              uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %7, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %6};\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(a_hi), "r"(b_hi), "r"(on)
+      : "memory");
+}
+
 // mma_commit by the lane with on != 0.
 __device__ __forceinline__ void mma_commit_warp(uint32_t on, uint64_t* bar) {
   asm volatile(
@@ -156,6 +189,25 @@ __device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t (&r)[1
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+
+// 8 consecutive 32-bit accumulator columns, likewise.
+__device__ __forceinline__ void tmem_ld8_nowait(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+// 4 consecutive columns from and to this warp's 32 TMEM lanes, likewise.
+__device__ __forceinline__ void tmem_ld4_nowait(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st4_nowait(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3])
+               : "memory");
 }
 
 // 16 registers to 16 consecutive 32-bit columns of this warp's 32 TMEM lanes
