@@ -82,11 +82,12 @@ struct Smem {
   int mask[kSoftWarps];         // rows that take a new reference
   long long scan[kThreads / 32];
   Run run;
+  alignas(8) unsigned char next[kSoftWarps][sizeof(WalkOver<kLead, 1, 0>)];  // a softmax warp's segment behind this one
   float q_scale[RP];
   float xch[kSoftWarps][RP];
   float sum[kSoftWarps][RP];
   float scale[kStages][2][kRows / kGroup];  // 2^e of the keys' groups; e of the values'
-  float factor[32][RP];         // of the parts that are added up
+  alignas(16) float factor[64][RP];  // of the parts that are added up
   float joined[3][RP];
   alignas(1024) unsigned char q[kQCols * WI_D];      // K-major, 128-byte swizzle
   unsigned char p[2][kPCols * kRows];                // [16 columns][position][16 B]
@@ -138,85 +139,122 @@ struct Few {
   WiPagedScales s;
 };
 
-// The queries of a segment's tile as e4m3 pieces, two rows of shared memory each.  A row of infinities or NaN gets a scale
-// that is no number, and so do all its scores.
-template <int RP, typename W>
-__device__ __forceinline__ void load_queries(const Params& P, Smem<RP>& sm, const W& w) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int r = warp; r < RP; r += kSoftWarps) {
-    const int tok = r / P.G, ti = w.tile * w.tp + tok;
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (tok < P.tq && ti < w.r.n)
-      load_bf16x4(static_cast<const bf16*>(P.a.q) + ((long long)(w.r.s0 + ti) * P.Hq + w.kh * P.G + r - tok * P.G) * WI_D + 4 * lane, x);
-    uint32_t top = 0;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) top = max(top, __float_as_uint(x[c]) & 0x7fffffffu);
-    top = __reduce_max_sync(0xffffffffu, top);
-    // the row's largest element lies in [128, 256): e is its exponent less 7, within what 2^-e can be
-    const int e = min(max((int)(top >> 23) - 127 - 7, -126), 126);
-    const float f = pow2(-e);
-    float y[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) y[c] = top < 0x7f800000u ? x[c] * f : 0.f;
-    const uint32_t a = e4m3x2_of(y[0], y[1]), b = e4m3x2_of(y[2], y[3]);
-    const float2 fa = e4m3x2_to_f32x2(a), fb = e4m3x2_to_f32x2(b);
-    const uint32_t rest = e4m3x4_of(y[0] - fa.x, y[1] - fa.y, y[2] - fb.x, y[3] - fb.y);
-    const uint32_t chunk = lane >> 2, in = (lane & 3) * 4;
-    *reinterpret_cast<uint32_t*>(sm.q + r * WI_D + ((chunk ^ (r & 7)) << 4) + in) = a | b << 16;
-    *reinterpret_cast<uint32_t*>(sm.q + (RP + r) * WI_D + ((chunk ^ ((RP + r) & 7)) << 4) + in) = rest;
-    if (lane == 0) sm.q_scale[r] = top < 0x7f800000u ? pow2(e) * kScaleLog2 : __uint_as_float(0x7fc00000u);
-  }
-}
-
-// out and lse of an item that was cut between CTAs, added up in CTA order: thread d has column d of every row.
+// A segment's queries, rows warp, warp + 4 of the tile, four elements to a lane.
 template <int RP>
-__device__ __noinline__ void join_parts(const Params& P, Smem<RP>& sm, const Split& sp, int c0) {
+struct Queries {
+  uint2 x[RP / kSoftWarps];
+  template <typename W>
+  __device__ __forceinline__ void ask(const Params& P, const W& w) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int k = 0; k < RP / kSoftWarps; ++k) {
+      const int r = warp + k * kSoftWarps, tok = r / P.G, ti = w.tile * w.tp + tok;
+      x[k] = make_uint2(0u, 0u);
+      if (tok < P.tq && ti < w.r.n)
+        x[k] = ldg_u2(static_cast<const bf16*>(P.a.q) +
+                      ((long long)(w.r.s0 + ti) * P.Hq + w.kh * P.G + r - tok * P.G) * WI_D + 4 * lane);
+    }
+  }
+  // ... to shared memory as e4m3 pieces, two rows each.  A row of infinities or NaN gets a scale that is no number, and so
+  // do all its scores.
+  __device__ __forceinline__ void put(Smem<RP>& sm) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int k = 0; k < RP / kSoftWarps; ++k) {
+      const int r = warp + k * kSoftWarps;
+      float v[4];
+      unpack_bf16x4(x[k], v);
+      uint32_t top = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) top = max(top, __float_as_uint(v[c]) & 0x7fffffffu);
+      top = __reduce_max_sync(0xffffffffu, top);
+      // the row's largest element lies in [128, 256): e is its exponent less 7, within what 2^-e can be
+      const int e = min(max((int)(top >> 23) - 127 - 7, -126), 126);
+      const float f = pow2(-e);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = top < 0x7f800000u ? v[c] * f : 0.f;
+      const uint32_t a = e4m3x2_of(v[0], v[1]), b = e4m3x2_of(v[2], v[3]);
+      const float2 fa = e4m3x2_to_f32x2(a), fb = e4m3x2_to_f32x2(b);
+      const uint32_t rest = e4m3x4_of(v[0] - fa.x, v[1] - fa.y, v[2] - fb.x, v[3] - fb.y);
+      const uint32_t chunk = lane >> 2, in = (lane & 3) * 4;
+      *reinterpret_cast<uint32_t*>(sm.q + r * WI_D + ((chunk ^ (r & 7)) << 4) + in) = a | b << 16;
+      *reinterpret_cast<uint32_t*>(sm.q + (RP + r) * WI_D + ((chunk ^ ((RP + r) & 7)) << 4) + in) = rest;
+      if (lane == 0) sm.q_scale[r] = top < 0x7f800000u ? pow2(e) * kScaleLog2 : __uint_as_float(0x7fc00000u);
+    }
+  }
+};
+
+// out and lse of an item that was cut between CTAs, added up in CTA order: thread d has column d of every row.  An SM comes
+// here once a call, so the code is cold, and what counts is how little of it there is: the parts' columns come to shared
+// memory by a short loop of asynchronous copies, `room` parts at a time (38 parts 8.2 us with unrolled loads to registers,
+// 2.1 of which went by before the last load was issued).
+constexpr int kJoin = 64;  // parts at a time, at most
+template <int RP>
+__device__ __noinline__ void join_parts(const Params& P, Smem<RP>& sm, const Split& sp, int c0, unsigned char* buf, int room) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, parts = sp.last - c0 + 1;
-  auto part = [&](int i) -> const float* { return P.parts.slot(2 * (c0 + i) + (i == 0 ? 1 : 0)); };
-  float acc[RP];
+  constexpr int kRecord = RP * WI_D * 4, kVec = RP / 4;  // bytes of a part's columns; pieces of a thread's
+  const long long stride = P.parts.slot(2) - P.parts.slot(0);
+  const float* const base = P.parts.slot(2 * c0);
+  auto part = [&](int i) -> const float* { return base + i * stride + (i == 0 ? stride / 2 : 0); };
+  float acc[RP], M[RP / kSoftWarps], L[RP / kSoftWarps];  // M, L: of this warp's rows
 #pragma unroll
   for (int r = 0; r < RP; ++r) acc[r] = 0.f;
-  if (tid < RP) {
-    sm.joined[0][tid] = -INFINITY;
-    sm.joined[1][tid] = 0.f;
-  }
-  soft_barrier();
-  for (int i0 = 0; i0 < parts; i0 += 32) {
 #pragma unroll
-    for (int r = warp; r < RP; r += kSoftWarps) {  // a warp has a row's factors, a lane a part's
-      float m = -INFINITY, l = 0.f;
-      if (i0 + lane < parts) {
-        m = __ldcg(part(i0 + lane) + r);
-        l = __ldcg(part(i0 + lane) + RP + r);
-      }
-      const float old = sm.joined[0][r], top = fmaxf(old, warp_max(m)), ref = top == -INFINITY ? 0.f : top;
-      const float f = ex2(m - ref), back = ex2(old - ref), z = warp_sum(f * l);
-      sm.factor[lane][r] = f;
-      __syncwarp();
+  for (int k = 0; k < RP / kSoftWarps; ++k) {
+    M[k] = -INFINITY;
+    L[k] = 0.f;
+  }
+#pragma unroll 1
+  for (int i0 = 0; i0 < parts; i0 += room) {
+    const int n = min(room, parts - i0);
+    const uint32_t to = smem_addr(buf) + tid * 16;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const float* from = part(i0 + i) + (2 + tid) * RP;
+#pragma unroll
+      for (int q = 0; q < kVec; ++q)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * kRecord + q * (kRecord / kVec)), "l"(from + 4 * q)
+                     : "memory");
+    }
+    if (i0 > 0) soft_barrier();  // the factors before are read
+#pragma unroll
+    for (int k = 0; k < RP / kSoftWarps; ++k) {  // a warp has a row's factors, a lane two parts'
+      const int r = warp + k * kSoftWarps;
+      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (32 * h + lane < n) {
+          m[h] = __ldcg(part(i0 + 32 * h + lane) + r);
+          l[h] = __ldcg(part(i0 + 32 * h + lane) + RP + r);
+        }
+      const float top = fmaxf(M[k], warp_max(fmaxf(m[0], m[1]))), ref = top == -INFINITY ? 0.f : top;
+      const float back = ex2(M[k] - ref), f0 = ex2(m[0] - ref), f1 = ex2(m[1] - ref);
+      L[k] = L[k] * back + warp_sum(f0 * l[0] + f1 * l[1]);
+      M[k] = top;
+      sm.factor[lane][r] = f0;
+      sm.factor[32 + lane][r] = f1;
       if (lane == 0) {
-        sm.joined[0][r] = top;
-        sm.joined[1][r] = sm.joined[1][r] * back + z;
+        sm.joined[0][r] = M[k];
+        sm.joined[1][r] = L[k];
         sm.joined[2][r] = back;
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // a thread reads what it asked for itself
     soft_barrier();
 #pragma unroll
     for (int r = 0; r < RP; ++r) acc[r] *= sm.joined[2][r];
-    const int n = min(32, parts - i0);
-#pragma unroll 8
+#pragma unroll 2
     for (int i = 0; i < n; ++i) {
-      const float4* o = reinterpret_cast<const float4*>(part(i0 + i) + (2 + tid) * RP);
 #pragma unroll
-      for (int q = 0; q < RP / 4; ++q) {
-        const float4 x = __ldcg(o + q);
-        acc[4 * q] += x.x * sm.factor[i][4 * q];
-        acc[4 * q + 1] += x.y * sm.factor[i][4 * q + 1];
-        acc[4 * q + 2] += x.z * sm.factor[i][4 * q + 2];
-        acc[4 * q + 3] += x.w * sm.factor[i][4 * q + 3];
+      for (int q = 0; q < kVec; ++q) {
+        const float4 x = *reinterpret_cast<const float4*>(buf + tid * 16 + i * kRecord + q * (kRecord / kVec));
+        const float4 f = *reinterpret_cast<const float4*>(&sm.factor[i][4 * q]);
+        acc[4 * q] += x.x * f.x;
+        acc[4 * q + 1] += x.y * f.y;
+        acc[4 * q + 2] += x.z * f.z;
+        acc[4 * q + 3] += x.w * f.w;
       }
     }
-    soft_barrier();  // the factors are read
   }
 #pragma unroll
   for (int r = 0; r < RP; ++r) {
@@ -293,13 +331,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention8_few(const __gr
     int n = 0;       // blocks so far
     Walk w(P, sm.run.start, sm.run.req);
     bool more = w.next(P);
-    auto ask = [&] {  // the queries of the segment: the products of the one before are done with theirs
-      load_queries<RP>(P, sm, w);
+    Queries<RP> queries;
+    auto put = [&] {  // once the products of the segment before are done with theirs
+      queries.put(sm);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_full);
     };
-    if (more) ask();
+    if (more) {
+      queries.ask(P, w);
+      put();
+    }
     soft_barrier();
     for (int seg = 0; more; ++seg) {
       float m[RP], l[RP], acc[RP], l_sum[RP], q_scale[RP];
@@ -313,6 +355,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention8_few(const __gr
         q_scale[r] = sm.q_scale[r];
       }
       const int whole = w.first_pos();  // the last position that all rows see
+      {  // the next segment, and its queries on their way
+        Walk next = w;
+        next.advance();
+        more = next.next(P);
+        if (more) queries.ask(P, next);
+        if (lane == 0) *reinterpret_cast<Walk*>(sm.next[warp]) = next;
+        __syncwarp();
+      }
       for (int j = 0; j < w.nb; ++j, ++n) {
         const int st = n % kStages, buf = n & 1;
         if (ok) ok = mbar_wait(&sm.s_full[buf], (n >> 1) & 1, P.err);
@@ -448,10 +498,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention8_few(const __gr
 
       // ---- the segment's end
       const Walk done = w;
-      w.advance();
-      more = w.next(P);
+      w = *reinterpret_cast<const Walk*>(sm.next[warp]);
+      __syncwarp();
       soft_barrier();  // the queries' scales are read
-      if (more) ask();
+      if (more) put();
 #pragma unroll
       for (int r = 0; r < RP; ++r) {
         l[r] = warp_sum(l[r] + l_sum[r]);
@@ -524,7 +574,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention8_few(const __gr
           }
         }
         soft_barrier();
-        if (sm.last) join_parts<RP>(P, sm, {done.r.s0 + done.tile * done.tp, done.kh, done.cnt, c1}, c0);
+        if (sm.last) {
+          // behind the CTA's last segment the rings are free, else what the weights took
+          constexpr int kRings = 2 * kStages * kBlockBytes / (RP * WI_D * 4);
+          static_assert(kRings <= kJoin, "a lane has two parts");
+          join_parts<RP>(P, sm, {done.r.s0 + done.tile * done.tp, done.kh, done.cnt, c1}, c0, more ? sm.p[0] : sm.k[0],
+                         more ? (int)(sizeof(sm.p) / (RP * WI_D * 4)) : kRings);
+        }
       }
       soft_barrier();  // what the threads share is read, and the next segment's queries have their scales
     }
@@ -532,41 +588,52 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention8_few(const __gr
     // ---------------- TMA: keys, values, and the scales of their groups
     Walk w(P, sm.run.start, sm.run.req);
     const uint32_t on = elect_one();
-    const int per = P.box / kGroup;  // groups of a box; one lane finds the page of each group
-    constexpr int kGroups = kRows / kGroup;
+    const int per = P.box / kGroup;  // groups of a box
+    constexpr int kGroups = kRows / kGroup, kBatch = 32 / kGroups;
     int n = 0, asked[2] = {0, 0};  // blocks done with, blocks of keys and of values that were asked for
     bool ok = true;
     for (; ok && w.next(P); w.advance()) {
+      // The pages and scales of four blocks at a time, a lane to a group: pages are looked up two batches ahead and scales
+      // one, so that no block waits for a look-up.
       constexpr int kNone = -0x7fffffff - 1;  // behind the request's end
-      auto page_of = [&](int j) -> int {
-        const int p = (w.b0 + j) * kRows + lane * kGroup;
-        if (j >= w.nb || lane >= kGroups || p >= w.r.kv) return kNone;
+      auto page_of = [&](int batch) -> int {
+        const int j = batch * kBatch + lane / kGroups, p = (w.b0 + j) * kRows + lane % kGroups * kGroup;
+        if (j >= w.nb || p >= w.r.kv) return kNone;
         return P.a.block_table[(long long)w.b * P.max_pages + p / P.page];
       };
-      // a group's (row of the pool, scales), from its page; a bad page is page 0
-      auto row_of = [&](int pg, int j) -> int {
+      // a group's row of the pool, from its page; a bad page is page 0
+      auto row_of = [&](int pg, int batch) -> int {
         if (pg == kNone) return -1;
         if (pg < 0 || pg >= P.n_pages) {
           atomicOr(P.err, WI_DEVERR_BAD_PAGE);
           pg = 0;
         }
-        return (pg * P.Hkv + w.kh) * P.page + ((w.b0 + j) * kRows + lane * kGroup) % P.page;
+        return (pg * P.Hkv + w.kh) * P.page + ((w.b0 + batch * kBatch) * kRows + lane * kGroup) % P.page;
       };
       auto scales_of = [&](int row) -> uint32_t {
         return row < 0 ? kScaleBias * 0x101u : (uint32_t)F.s.k[row / kGroup] | (uint32_t)F.s.v[row / kGroup] << 8;
       };
-      // pages are looked up three blocks ahead, scales two
-      int g2 = page_of(2), g3;
-      int r0 = row_of(page_of(0), 0), r1 = row_of(page_of(1), 1), r2;
-      uint32_t e0 = scales_of(r0), e1 = scales_of(r1), e2;
+      int page = page_of(0), row = 0, row_next = 0;
+      uint32_t e = 0, e_next = 0;
+      {
+        const int ahead = page_of(1);
+        row_next = row_of(page, 0);
+        e_next = scales_of(row_next);
+        page = ahead;
+      }
       for (int j = 0; j < w.nb; ++j, ++n) {
-        g3 = page_of(j + 3);
-        r2 = row_of(g2, j + 2);
-        e2 = scales_of(r2);
-        const int st = n % kStages;
+        if (j % kBatch == 0) {
+          row = row_next;
+          e = e_next;
+          row_next = row_of(page, j / kBatch + 1);
+          e_next = scales_of(row_next);
+          page = page_of(j / kBatch + 2);
+        }
+        const int st = n % kStages, first = j % kBatch * kGroups;  // first: the lane of the block's first group
         const uint32_t par = ((uint32_t)(n / kStages) & 1u) ^ 1u;
         // boxes behind the request's end are left out: always the last ones
-        const int groups = __popc(__ballot_sync(0xffffffffu, r0 >= 0)), boxes = (groups + per - 1) / per;
+        const int groups = __popc(__ballot_sync(0xffffffffu, row >= 0) >> first & ((1u << kGroups) - 1));
+        const int boxes = (groups + per - 1) / per;
         const uint32_t bytes = (uint32_t)(boxes * P.box) * WI_D;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
@@ -579,21 +646,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention8_few(const __gr
           const uint32_t dst = smem_addr(v ? sm.v[st] : sm.k[st]);
           for (int i = 0; i < boxes; ++i)
             tma_load_2d_warp(on, dst + (uint32_t)(i * P.box) * WI_D, v ? &map_v : &map_k, 0,
-                             __shfl_sync(0xffffffffu, r0, i * per), full);
-          if (v && lane < kGroups) {  // behind the copies: the scales may still be on their way here
-            sm.scale[st][0][lane] = pow2(scale_exponent((unsigned char)(e0 & 0xff)));
-            sm.scale[st][1][lane] = (float)scale_exponent((unsigned char)(e0 >> 8));
+                             __shfl_sync(0xffffffffu, row, first + i * per), full);
+          if (v && lane / kGroups == j % kBatch) {  // behind the copies: the scales may still be on their way here
+            sm.scale[st][0][lane % kGroups] = pow2(scale_exponent((unsigned char)(e & 0xff)));
+            sm.scale[st][1][lane % kGroups] = (float)scale_exponent((unsigned char)(e >> 8));
           }
           __syncwarp();
           if (on) mbar_arrive_expect_tx(full, bytes);  // the stage's one arrival: it is full when the bytes are there
           ++asked[v];
         }
         if (!ok) break;
-        r0 = r1;
-        e0 = e1;
-        r1 = r2;
-        e1 = e2;
-        g2 = g3;
       }
     }
     // no copy is in flight when the CTA's shared memory goes (after a timed-out wait nobody may have waited for them)
