@@ -1,153 +1,768 @@
-// wi_paged8_attn.cu -- attention of new tokens over the paged cache in 8 bits.
+// wi_paged8_attn.cu -- attention of new tokens over the paged cache in 8 bits, on tiles of 128 rows.
 //
 // out = softmax(q K^T / sqrt(128)) V over the positions a token sees, K and V
-// the pools' values times their group's scale.  A CTA takes one token and one
-// kv head: its warps take every fourth run of 32 positions, a lane a key, for
-// the scores of the head's queries, and then a lane four columns of the values.
+// the pools' values times their group's scale.  Rows, items, runs and the two
+// softmax chains are those of the bf16 attention (wi_paged_attn.cu); what
+// differs is how the operands reach the tensor cores.
+//
+// S = Q K^T in e4m3: keys as they lie in the cache, queries as two e4m3 pieces, a
+// first one of four significant bits and the rest of four, which a bf16 query is
+// exactly (over the row's largest element; what is below 2^-18 of that may be
+// lost).  Two products of half the time each, so S costs what it does in bf16, and
+// no key is ever widened.  A column's scale is its group's: a score is
+// S 2^(e_row + e_group), one multiplier per sixteen columns.
+//
+// O += P V in f16: e4m3 pieces of P would lose what weighs less than 2^-18 of the
+// row's largest, which a sink of attention makes most of the row, and three of
+// them would cost more than bf16 does.  So two warps widen a block's values (a
+// conversion of two values an instruction, exact) on their way from the copy's
+// stage to the product's, once for both chains.  The value's scale goes into
+// the weight, p' = 2^(score + e - m), and out of the row's sum, l += p' 2^-e.
+//
+// Warps of a CTA (384 threads):
+//   0-3, 4-7  softmax, one thread per row of chain 0 / chain 1; they also cut the
+//             queries of their tile into pieces
+//   8         TMA: key and value blocks, box by box, and their groups' scales
+//   9         issues tcgen05.mma
+//   10-11     widen the values, and clean what not every row sees
+#include <cuda.h>
 #include <cuda_runtime.h>
+
+#include <cstddef>
 
 #include "wi_common.cuh"
 #include "wi_e4m3.cuh"
 #include "wi_internal.h"
 #include "wi_paged.h"
 #include "wi_paged8.h"
+#include "wi_paged_merge.cuh"
+#include "wi_paged_walk.cuh"
 #include "wi_pipe.cuh"
+#include "wi_tc.cuh"
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kMaxG = 8;
+constexpr int kKStages = 3, kVStages = 2, kWStages = 2, kScaleSlots = 8;
+constexpr int kBlockBytes = kRows * WI_D;       // a block of keys or values in 8 bits, a piece of a tile's queries
+constexpr int kWideBytes = kRows * WI_D * 2;    // a block of values in f16: [group of 8 rows][half of 64 columns][8][128 B]
+constexpr int kSoftWarps = 8;
+constexpr int kThreads = 32 * (kSoftWarps + 4);
+constexpr int kWideWarps = 2;
+constexpr int kGroups = kRows / kGroup;         // of a block
 constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
-constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kLead = 4;                        // units in front of an item's blocks, for what its start and end cost
+constexpr int kWhole = 4;                       // blocks up to which one request's items of few rows are not cut
+// Blocks that one segment has at most: the tensor cores' additions cut bits off, so longer sums are added up in fp32.
+constexpr int kLongest = 2048;
+// A reference makes the row's largest weight 2^4: f16 holds a weight to 11 bits down to 2^-18 of that, and no less than
+// 2^-29 of it.  A row takes a new one when a block's weights add up to more than f16 takes, or its sum (through values
+// of a tiny scale) to more than kFarMost.
+constexpr float kTop = 4.f, kAgain = 60000.f, kFar = 64.f, kFarMost = 0x1p90f;
 
-__global__ void __launch_bounds__(32 * kWarps) k_paged_attention8(WiPagedAttn A, WiPagedScales S, int Hq, int Hkv, int G,
-                                                                  int page, int n_pages, int max_pages, int* err) {
-  __shared__ float q[kMaxG][WI_D];
-  __shared__ float part[kWarps][kMaxG][WI_D + 2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_trigger();
-  pdl_wait();
-  const int t = blockIdx.x / Hkv, kh = blockIdx.x - t * Hkv;
-  int b = 0, s0 = 0, n = 0, kv = 0;
-  bool found = false;
-  for (; b < A.batch; ++b) {
-    s0 = A.q_start[b];
-    const int s1 = A.q_start[b + 1];
-    if (s1 < s0) {
-      if (blockIdx.x == 0 && tid == 0) atomicOr(err, WI_DEVERR_BAD_LENGTH);
-      break;
-    }
-    kv = A.kv_len[b];
-    const bool ok = s0 >= 0 && s1 <= A.n_tokens && kv >= 0 && (long long)kv <= (long long)max_pages * page;
-    if (!ok && blockIdx.x == 0 && tid == 0) atomicOr(err, WI_DEVERR_BAD_LENGTH);
-    if (t >= s0 && t < s1 && !found) {
-      if (!ok) return;
-      n = s1 - s0;
-      found = true;
-      if (blockIdx.x != 0) break;
-    }
-    if (found) continue;
-  }
-  if (!found) return;
-  // (block 0 went on to look at every request: its own again)
-  if (blockIdx.x == 0) {
-    for (b = 0; !(A.q_start[b] <= t && t < A.q_start[b + 1]); ++b) {
-    }
-    s0 = A.q_start[b];
-    n = A.q_start[b + 1] - s0;
-    kv = A.kv_len[b];
-  }
-  const int end = (int)((long long)kv - n + (t - s0)) + 1;  // positions that the token sees: 0 or less, none
-  for (int i = tid; i < G * WI_D; i += 32 * kWarps)
-    q[i / WI_D][i % WI_D] = __bfloat162float(static_cast<const bf16*>(A.q)[((long long)t * Hq + kh * G) * WI_D + i]) * kScaleLog2;
-  __syncthreads();
-  float m[kMaxG], z[kMaxG], acc[kMaxG][4];
+template <bool LONG>
+using Walk = WalkOver<kLead, 2, LONG ? kLongest : 0>;
+
+struct Smem {
+  uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], w_full[kWStages], w_empty[kWStages];
+  uint64_t scale_full[kScaleSlots];
+  uint64_t q_full, s_full[2], p_ready[2], o_full[2], drained;
+  uint32_t tmem_base;
+  int last;                 // this CTA merges the item that it just added to
+  int poison[8];            // segment number + 1 of the last segment (modulo 8) with a NaN value
+  long long scan[kThreads / 32];
+  Run run;
+  Req reqs[kSoftWarps];     // of the softmax warps' segments
+  // of a block's groups: 2^e of the keys, e of the values, 2^-e of the values.  A slot is written again eight blocks on,
+  // behind the scores of the block three before that, which come behind the weights of this one.
+  alignas(16) float scale[kScaleSlots][3][kGroups];
+  float q_scale[2][kRows];
+  float xch[2][2][kRows];   // maximum and sum of a row, from chain to chain: [chain][m, l]
+  alignas(1024) unsigned char q[2][2][kBlockBytes];   // [tile][piece]
+  unsigned char k[kKStages][kBlockBytes];
+  unsigned char v[kVStages][kBlockBytes];
+  unsigned char w[kWStages][kWideBytes];
+};
+static_assert(offsetof(Smem, q) % 1024 == 0, "tiles must start 1024-byte aligned");
+static_assert(sizeof(Smem) <= 232448, "shared memory");
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 w = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&w);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 w = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&w);
+}
+
+__device__ __forceinline__ void soft_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kSoftWarps * 32) : "memory"); }
+
+// Scores behind column `seen` of 64 are not seen.
+__device__ __forceinline__ void mask_scores(uint32_t (&s)[2][32], int seen) {
 #pragma unroll
-  for (int g = 0; g < kMaxG; ++g) {
-    m[g] = -INFINITY;
-    z[g] = 0.f;
+  for (int i = 0; i < 64; ++i)
+    if (i > seen) s[i >> 5][i & 31] = 0xFF800000u;  // -infinity
+}
+
+// The reference that 64 scores ask for: the largest score + e less kTop, and the largest score less kFar.
+__device__ __forceinline__ float top_of(const uint32_t (&s)[2][32], const float* scale, float q_scale) {
+  float best = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[g][c] = 0.f;
+  for (int g = 0; g < 4; ++g) {
+    const uint32_t* x = s[g >> 1] + (g & 1) * 16;
+    float t = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+#pragma unroll
+    for (int i = 2; i < 16; i += 2) t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+    t *= q_scale * scale[g];
+    best = max3(best, t + (scale[kGroups + g] - kTop), t - kFar);
   }
-  for (int p0 = warp * 32; p0 < end; p0 += 32 * kWarps) {
-    const int p = p0 + lane;
-    long long row = -1;
-    float x[kMaxG];
+  return best;
+}
+
+// 32 scores, two groups of columns, to weights 2^(score + e - ref): added to `sum`, and over the values' scale to `low`, and
+// as f16 to 16 columns of P.
+__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t tp, const float* scale, float q_scale, float ref,
+                                        uint64_t& sum, uint64_t& low) {
+  uint32_t p[16];
 #pragma unroll
-    for (int g = 0; g < kMaxG; ++g) x[g] = 0.f;
-    float vscale = 0.f;
-    if (p < end) {
-      const int j = p / page;
-      int pg = A.block_table[(long long)b * max_pages + j];
-      if (pg < 0 || pg >= n_pages) {
-        atomicOr(err, WI_DEVERR_BAD_PAGE);
-        pg = 0;
+  for (int g = 0; g < 2; ++g) {
+    const float f = q_scale * scale[g], e = scale[kGroups + g] - ref, back = scale[2 * kGroups + g];
+    const uint64_t f2 = pair(f, f), e2 = pair(e, e);
+    uint64_t z = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint64_t x = fma2(pair(s[16 * g + 2 * i], s[16 * g + 2 * i + 1]), f2, e2);
+      const float a = ex2(lo_of(x)), b = ex2(hi_of(x));
+      z = i == 0 ? pair(a, b) : add2(z, pair(a, b));
+      p[8 * g + i] = pack_f16(a, b);
+    }
+    sum = add2(sum, z);
+    low = fma2(z, pair(back, back), low);
+  }
+  tmem_st16_nowait(tp, p);
+}
+
+// A row's query as two e4m3 pieces, to row `row` of a tile's two; the factor of its scores.  A row of infinities or NaN gets
+// one that is no number, a row of no token pieces of zeros.
+__device__ __forceinline__ float put_query(const uint4* from, bool live, unsigned char* to, int row) {
+  uint32_t top = 0;
+  if (live) {
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const uint4 x = __ldg(from + c);
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+    }
+    top = max(top & 0xffffu, top >> 16);
+  }
+  const bool good = live && top < 0x7f80u;
+  // the row's largest element lies in [128, 256)
+  const int e = min(max((int)(top >> 7) - 127 - 7, -126), 126);
+  const float f = pow2(-e);
+#pragma unroll 2
+  for (int c = 0; c < 8; ++c) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 x = good ? __ldg(from + 2 * c + h) : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float y0 = bf16_lo(w[2 * k]) * f, y1 = bf16_hi(w[2 * k]) * f, y2 = bf16_lo(w[2 * k + 1]) * f,
+                    y3 = bf16_hi(w[2 * k + 1]) * f;
+        const uint32_t a = e4m3x2_of(y0, y1), b = e4m3x2_of(y2, y3);
+        const float2 fa = e4m3x2_to_f32x2(a), fb = e4m3x2_to_f32x2(b);
+        hi[2 * h + k] = a | b << 16;
+        lo[2 * h + k] = e4m3x4_of(y0 - fa.x, y1 - fa.y, y2 - fb.x, y3 - fb.y);
       }
-      const long long head = (long long)pg * Hkv + kh;
-      row = head * page + (p - j * page);
-      const long long group = head * (page / kGroup) + (p - j * page) / kGroup;
-      const float kscale = pow2(scale_exponent(S.k[group]));
-      vscale = pow2(scale_exponent(S.v[group]));
-      const uint4* k = static_cast<const uint4*>(A.k_pages) + row * 8;
-      for (int c = 0; c < 8; ++c) {
-        const uint4 w = k[c];
-        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+    }
+    unsigned char* const at = to + row * WI_D + ((c ^ (row & 7)) << 4);
+    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(at + kBlockBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  return !live ? 1.f : good ? pow2(e) * kScaleLog2 : __uint_as_float(0x7fc00000u);
+}
+
+// The NaN values that a row sees at positions [from, to), where they were taken out, to 16 columns of its O.
+__device__ __forceinline__ void add_poison(const Params& P, int b, int kh, int from, int to, int limit, int c0,
+                                           float (&o)[16]) {
+  const int end = min(to, limit + 1);
+#pragma unroll 1
+  for (int p = from; p < end; ++p) {
+    const int j = p / P.page, pg = P.a.block_table[(long long)b * P.max_pages + j];
+    if (pg < 0 || pg >= P.n_pages) continue;
+    const unsigned char* v = static_cast<const unsigned char*>(P.a.v_pages) +
+                             (((long long)pg * P.Hkv + kh) * P.page + (p - j * P.page)) * WI_D + c0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 v = e4m3x2_to_f32x2(e[i >> 1] >> (16 * (i & 1)) & 0xffffu);
-          const int d = c * 16 + 2 * i;
-          for (int g = 0; g < G; ++g) x[g] += q[g][d] * v.x + q[g][d + 1] * v.y;
+    for (int i = 0; i < 16; ++i)
+      if ((v[i] & 0x7f) == 0x7f) o[i] = __uint_as_float(0x7fc00000u);
+  }
+}
+
+struct Rows8 {
+  Params P;
+  WiPagedScales s;
+};
+
+template <bool LONG>
+__global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_constant__ CUtensorMap map_k,
+                                                                 const __grid_constant__ CUtensorMap map_v,
+                                                                 const __grid_constant__ Rows8 A) {
+  const Params& P = A.P;
+  extern __shared__ __align__(1024) unsigned char raw[];
+  pdl_trigger();  // the next kernel may take the SMs as they fall free; it waits for this grid before it reads
+  Smem& sm = *reinterpret_cast<Smem*>(raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (smem_addr(raw) & 1023u) {  // the swizzled tiles need 1024-byte alignment; never run misaligned
+    if (tid == 0) atomicOr(P.err, WI_DEVERR_BAD_ROW);
+    return;
+  }
+  if (tid == 0) {
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(&sm.k_full[s], 1);
+      mbar_init(&sm.k_empty[s], 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(&sm.v_full[s], 1);
+      mbar_init(&sm.v_empty[s], kWideWarps);
+    }
+    for (int s = 0; s < kWStages; ++s) {
+      mbar_init(&sm.w_full[s], kWideWarps);
+      mbar_init(&sm.w_empty[s], 1);
+    }
+    for (int s = 0; s < kScaleSlots; ++s) mbar_init(&sm.scale_full[s], 1);
+    mbar_init(&sm.q_full, kSoftWarps);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sm.s_full[t], 1);
+      mbar_init(&sm.p_ready[t], kSoftWarps / 2);
+      mbar_init(&sm.o_full[t], 1);
+    }
+    mbar_init(&sm.drained, 1);
+    for (int i = 0; i < 8; ++i) sm.poison[i] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kSoftWarps + 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == kSoftWarps && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
+  }
+  pdl_wait();
+  tc_fence_before();
+  const bool any = find_run<kLead, 2, kThreads>(P, 1, P.tickets ? kLead + kWhole : 0, sm.scan, &sm.run);  // (with a barrier of all threads)
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;  // S0, S1 at columns 0, 128; O0, O1 at 256, 384
+  if (!any) {  // the whole CTA leaves
+    if (tid == 0) P.splits[blockIdx.x].last = -1;
+    if (warp == kSoftWarps + 1)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    return;
+  }
+
+  // a softmax lane holds a row of scores; the registers that the other warps do not need go to those
+  // (208 * 8 + 88 * 4 = 168 * 12, what the launch has)
+  if (warp < kSoftWarps)
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  else
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp < kSoftWarps) {
+    // ---------------- softmax
+    const int chain = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + (uint32_t)chain * kRows;
+    const int tok = (row * ((65536 + P.G - 1) / P.G)) >> 16, head = row - tok * P.G;
+    uint32_t s_par = 0, o_par0 = 0, o_par1 = 0;
+    bool ok = true;  // after one timed-out wait the warp waits no more and writes nothing, but meets every barrier
+    bool split = false;  // the run's last item goes on in the next CTA
+    // Only the cursor and what the blocks need live through a segment, beside the scores; the rest is worked out again
+    // behind them, from the request as the warp keeps it in shared memory.
+    Cursor cur;
+    int nb, step, from, base, limit, whole, n0 = 0;  // n0: blocks of the segments before
+    float q_scale = 1.f;
+    auto begin = [&](Walk<LONG>& w) {
+      const bool more = w.next(P);
+      cur = w;
+      if (lane == 0) sm.reqs[warp] = w.r;
+      __syncwarp();
+      const int own_tile = w.single ? 0 : chain, ti = w.tile * w.tp + own_tile * P.tq + tok;
+      const bool live = more && tok < P.tq && ti < w.r.n;
+      limit = live ? (int)(w.p0 + ti) : -1;                        // the last position that the row sees
+      whole = (int)(w.p0 + w.tile * w.tp + own_tile * P.tq);       // ... that all rows of the tile see
+      nb = w.nb;
+      step = w.single ? 2 : 1;
+      from = w.single ? chain : 0;
+      base = w.b0 * kRows;
+      if (!more) return false;
+      // the tile's queries: the products that read the ones before are done (O is)
+      if (!w.single || chain == 0)
+        sm.q_scale[chain][row] = put_query(
+            reinterpret_cast<const uint4*>(static_cast<const bf16*>(P.a.q) +
+                                           ((long long)(w.r.s0 + ti) * P.Hq + w.kh * P.G + head) * WI_D),
+            live, sm.q[chain][0], row);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_full);
+      if (w.single) soft_barrier();  // both chains have the one tile
+      q_scale = sm.q_scale[own_tile][row];
+      return true;
+    };
+    cur = sm.run.start;
+    if (lane == 0) sm.reqs[warp] = sm.run.req;
+    __syncwarp();
+    for (int seg = 0;; ++seg) {
+      {
+        Walk<LONG> w(P, cur, sm.reqs[warp]);
+        if (!begin(w)) break;
+      }
+      float m = -INFINITY, l = 0.f;  // the row's reference and its sum
+      for (int j = from; j < nb; j += step) {
+        const int slot = (n0 + j) % kScaleSlots;
+        if (ok) ok = mbar_wait(&sm.scale_full[slot], ((n0 + j) / kScaleSlots) & 1, P.err);
+        if (ok) ok = mbar_wait(&sm.s_full[chain], s_par, P.err);
+        s_par ^= 1;
+        tc_fence_after();
+        const float* const scale = sm.scale[slot][0];
+        // The second half of the scores comes while the first is worked on; P then takes the place of the first half,
+        // which stays in registers, so that the block can be done again.
+        uint32_t a[2][32], b[2][32];
+        tmem_ld32_nowait(ts, a[0]);
+        tmem_ld32_nowait(ts + 32, a[1]);
+        tmem_wait_ld();
+        tmem_ld32_nowait(ts + 64, b[0]);
+        tmem_ld32_nowait(ts + 96, b[1]);
+        const bool masked = base + j * kRows + kRows - 1 > whole;
+        const int seen = limit - base - j * kRows;  // the row sees columns 0 .. seen of this block
+        if (masked) mask_scores(a, seen);
+        bool again = j == from, grown = again;  // grown: this row takes a new reference (other rows keep theirs)
+        for (;;) {
+          if (again) {  // the first block, or the reference is far too small
+            tmem_wait_st();
+            tmem_wait_ld();
+            tmem_ld32_nowait(ts + 64, b[0]);
+            tmem_ld32_nowait(ts + 96, b[1]);
+            tmem_wait_ld();
+            if (masked) mask_scores(b, seen - 64);
+            const float top = grown ? max3(m, top_of(a, scale, q_scale), top_of(b, scale + 4, q_scale)) : m;
+            if (j != from) {
+              // the chain's products so far are done: S of this block was issued behind them
+              const float f = m == top ? 1.f : ex2(m - top);
+              l *= f;
+              const uint32_t to = tmem + lanes + 256u + (uint32_t)chain * WI_D;
+#pragma unroll 1
+              for (int c = 0; c < 8; ++c) {
+                uint32_t o[16];
+                tmem_ld16_nowait(to + 16 * c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st16_nowait(to + 16 * c, o);
+              }
+            }
+            m = top;
+          }
+          const float ref = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 2^-inf = 0
+          uint64_t sum = 0ull, low = 0ull;
+          weights(a[0], ts, scale, q_scale, ref, sum, low);
+          weights(a[1], ts + 16, scale + 2, q_scale, ref, sum, low);
+          tmem_wait_ld();
+          if (masked && !again) mask_scores(b, seen - 64);
+          weights(b[0], ts + 32, scale + 4, q_scale, ref, sum, low);
+          weights(b[1], ts + 48, scale + 6, q_scale, ref, sum, low);
+          const float z = lo_of(sum) + hi_of(sum), zl = lo_of(low) + hi_of(low);
+          // A row without a reference (every score so far minus infinity) looks for one in each block that it sees
+          // something of: against 0 its weights might all vanish.  A row that sees nothing of the block, or that no token
+          // owns, asks for nothing.
+          grown = seen >= 0 && (!(z <= kAgain) || !(zl <= kFarMost) || m == -INFINITY);
+          if (again || !__any_sync(0xffffffffu, grown)) {
+            l += zl;
+            break;
+          }
+          again = true;
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_ready[chain]);
+      }
+
+      // ---- the segment's end: maximum and sum over both chains where they had one tile, then O
+      Walk<LONG> w(P, cur, sm.reqs[warp]);
+      w.next(P);
+      const int own_tile = w.single ? 0 : chain, ti = w.tile * w.tp + own_tile * P.tq + tok;
+      const bool live = tok < P.tq && ti < w.r.n;
+      const bool both = !w.single || w.nb > 1;  // chain 1 had blocks
+      bool part = w.b0 > 0 || w.nb < w.nblk, begun = w.b0 == 0, goes_on = false, join = w.single && both;
+      if (ok && (w.single || chain == 0)) ok = mbar_wait(&sm.o_full[0], o_par0, P.err);
+      if (ok && both && (w.single || chain == 1)) ok = mbar_wait(&sm.o_full[1], o_par1, P.err);
+      o_par0 ^= 1;
+      if (both) o_par1 ^= 1;
+      tc_fence_after();
+      float f0 = 1.f, f1 = 0.f;
+      if (w.single) {
+        sm.xch[chain][0][row] = m;
+        sm.xch[chain][1][row] = l;
+        soft_barrier();
+        const float m0 = sm.xch[0][0][row], m1 = sm.xch[1][0][row];
+        m = fmaxf(m0, m1);
+        const float ref = m == -INFINITY ? 0.f : m;
+        f0 = ex2(m0 - ref);
+        f1 = ex2(m1 - ref);
+        l = sm.xch[0][1][row] * f0 + sm.xch[1][1][row] * f1;
+      }
+      const long long at = (long long)(w.r.s0 + ti) * P.Hq + w.kh * P.G + head;
+      const uint32_t to = tmem + lanes + 256u + (w.single ? 0u : (uint32_t)chain * WI_D);
+      const int ca = w.single ? 64 * chain : 0, cb = w.single ? ca + 64 : WI_D;  // the columns that this thread takes
+      if (LONG && w.nblk > kLongest) {  // maybe not the CTA's first segment of the item, or not its last
+        const int spent = sm.run.start.left - w.left;
+        begun = spent >= w.at - kLead;
+        part = !begun || w.b0 + w.nb < w.nblk;
+        goes_on = w.b0 + w.nb < w.nblk && w.took < w.left;
+        if (w.at > 0 && spent > 0) {
+          const float2 x = add_earlier(P, P.parts.slot(2 * (int)blockIdx.x + begun), own_tile, row, live, m, l, to, ca, cb,
+                                       join, f0, f1);
+          m = x.x;
+          l = x.y;
+          join = false;
+          if (w.single) soft_barrier();  // both threads of a row have read its maximum and sum
         }
       }
+      const int slot = 2 * (int)blockIdx.x + (begun ? 1 : 0);
+      float* dst = P.parts.slot(slot);
+      const bool poison = *reinterpret_cast<volatile int*>(&sm.poison[seg & 7]) == seg + 1;
+      const float inv = part ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+#pragma unroll 1
+      for (int c = ca; c < cb; c += 16) {
+        __syncwarp();
+        uint32_t raw_o[16];
+        tmem_ld16_nowait(to + c, raw_o);
+        tmem_wait_ld();
+        float o[16];
 #pragma unroll
-      for (int g = 0; g < kMaxG; ++g) x[g] *= kscale;
+        for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(raw_o[i]);
+        if (join) {
+          tmem_ld16_nowait(to + WI_D + c, raw_o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = o[i] * f0 + __uint_as_float(raw_o[i]) * f1;
+        }
+        if (poison && live)
+          add_poison(P, w.b, w.kh, max(max(w.b0, w.first_fix()) * kRows, w.first_clean()),
+                     min((w.b0 + w.nb) * kRows, w.r.kv), limit, c, o);
+        if (ok && live) {
+          if (part) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) __stcg(dst + P.parts.o(own_tile, c + i, row), o[i]);
+          } else {
+            uint4* q = reinterpret_cast<uint4*>(static_cast<bf16*>(P.a.out) + at * WI_D + c);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              q[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+          }
+        }
+      }
+      if (ok && live && (chain == 0 || !w.single)) {
+        if (part) {
+          __stcg(dst + P.parts.m(own_tile, row), m);
+          __stcg(dst + P.parts.l(own_tile, row), l);
+        } else if (P.a.lse) {
+          P.a.lse[at] = l == 0.f ? -INFINITY : m * kLn2 + logf(l);
+        }
+      }
+      tc_fence_before();  // O is read: the next segment may write it
+      if (LONG && goes_on) {
+        // the rest of the item's end is for the last segment that the CTA has of it
+      } else if (part && P.tickets) {
+        const long long item = sm.run.end - w.left - w.at + kLead;  // the unit of the item's first block
+        const int c0 = cta_of(item, sm.run.total, sm.run.ctas), c1 = cta_of(item + w.nblk - 1, sm.run.total, sm.run.ctas);
+        soft_barrier();  // then thread 0's release covers what all of them stored
+        if (tid == 0) {
+          sm.last = 0;
+          if (ok && ticket_acq_rel(P.tickets + c0) == (unsigned)(c1 - c0)) {
+            P.tickets[c0] = 0;
+            sm.last = 1;
+          }
+        }
+        soft_barrier();
+        if (sm.last) {
+          const Split sp = {w.r.s0 + w.tile * w.tp, w.kh, w.cnt, c1};
+          if (P.parts.rows > kFewRows) {
+            merge_tile<kSoftWarps>(P, sp, c0);
+          } else {
+#pragma unroll 1
+            for (int r0 = 0; r0 < tile_rows(P, sp, 0); r0 += 2 * kSoftWarps * 32 / WI_D)
+              merge_some<kSoftWarps * 32>(P, sp, c0, 0, r0);
+          }
+        }
+      } else if (part && begun && tid == 0) {
+        split = true;
+        P.splits[blockIdx.x] = {w.r.s0 + w.tile * w.tp, w.kh, w.cnt,
+                                cta_of(sm.run.end - w.left - w.at + kLead + w.nblk - 1, sm.run.total, sm.run.ctas)};
+      }
+      if (w.single) soft_barrier();  // both chains' O, maxima and sums have been read
+      n0 += w.nb;
+      w.advance();
+      cur = w;
     }
-#pragma unroll
-    for (int g = 0; g < kMaxG; ++g) {
-      if (p >= end) x[g] = -INFINITY;
-      const float top = fmaxf(m[g], warp_max(x[g])), ref = top == -INFINITY ? 0.f : top;
-      const float f = exp2f(m[g] - ref);
-      m[g] = top;
-      x[g] = exp2f(x[g] - ref);
-      z[g] = z[g] * f + warp_sum(x[g]);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[g][c] *= f;
+    if (tid == 0 && !split) P.splits[blockIdx.x].last = -1;
+  } else if (warp == kSoftWarps) {
+    // ---------------- TMA: keys, values, and the scales of their groups
+    Walk<LONG> w(P, sm.run.start, sm.run.req);
+    const uint32_t on = elect_one();
+    const int per = P.box / kGroup;  // groups of a box
+    constexpr int kBatch = 32 / kGroups;
+    int nk = 0, nv = 0;  // blocks of keys and of values that were asked for
+    bool ok = true;
+    for (; ok && w.next(P); w.advance()) {
+      // The pages and scales of four blocks at a time, a lane to a group: pages are looked up two batches ahead and scales
+      // one, so that no block waits for a look-up.
+      constexpr int kNone = -0x7fffffff - 1;  // behind the request's end
+      auto page_of = [&](int batch) -> int {
+        const int j = batch * kBatch + lane / kGroups, p = (w.b0 + j) * kRows + lane % kGroups * kGroup;
+        if (j >= w.nb || p >= w.r.kv) return kNone;
+        return P.a.block_table[(long long)w.b * P.max_pages + p / P.page];
+      };
+      // a group's row of the pool, from its page; a bad page is page 0
+      auto row_of = [&](int pg, int batch) -> int {
+        if (pg == kNone) return -1;
+        if (pg < 0 || pg >= P.n_pages) {
+          atomicOr(P.err, WI_DEVERR_BAD_PAGE);
+          pg = 0;
+        }
+        return (pg * P.Hkv + w.kh) * P.page + ((w.b0 + batch * kBatch) * kRows + lane * kGroup) % P.page;
+      };
+      auto scales_of = [&](int row) -> uint32_t {
+        return row < 0 ? kScaleBias * 0x101u : (uint32_t)A.s.k[row / kGroup] | (uint32_t)A.s.v[row / kGroup] << 8;
+      };
+      auto fill = [&](const CUtensorMap* map, unsigned char* to, uint64_t* full, uint64_t* empty, int stages, int n, int row,
+                      int j) -> bool {
+        bool got = true;
+        if (n >= stages) got = mbar_wait(empty, ((uint32_t)(n / stages) & 1u) ^ 1u, P.err);
+        if (!__all_sync(0xffffffffu, got)) return false;
+        const int first = j % kBatch * kGroups;  // the lane of the block's first group
+        // boxes behind the request's end are left out: always the last ones
+        const int groups = __popc(__ballot_sync(0xffffffffu, row >= 0) >> first & ((1u << kGroups) - 1));
+        const int boxes = (groups + per - 1) / per;
+        if (on) mbar_arrive_expect_tx(full, (uint32_t)(boxes * P.box) * WI_D);
+        __syncwarp();
+        const uint32_t dst = smem_addr(to);
+        for (int i = 0; i < boxes; ++i)
+          tma_load_2d_warp(on, dst + (uint32_t)(i * P.box) * WI_D, map, 0, __shfl_sync(0xffffffffu, row, first + i * per), full);
+        return true;
+      };
+      const int ahead = w.single ? 2 : 1;
+      // the batch that keys are asked for from (rows and scales), and the one that values are, which may lie behind it
+      int page, row = 0, row_next, row_v = 0;
+      uint32_t e = 0, e_next;
+      {
+        const int g0 = page_of(0);
+        page = page_of(1);
+        row_next = row_of(g0, 0);
+        e_next = scales_of(row_next);
+      }
+      auto keys = [&](int j) -> bool {
+        if (j % kBatch == 0) {
+          row_v = row;
+          row = row_next;
+          e = e_next;
+          row_next = row_of(page, j / kBatch + 1);
+          e_next = scales_of(row_next);
+          page = page_of(j / kBatch + 2);
+        }
+        const int st = nk % kKStages, slot = nk % kScaleSlots;
+        if (!fill(&map_k, sm.k[st], &sm.k_full[st], &sm.k_empty[st], kKStages, nk, row, j)) return false;
+        if (lane / kGroups == j % kBatch) {
+          const int ev = scale_exponent((unsigned char)(e >> 8));
+          sm.scale[slot][0][lane % kGroups] = pow2(scale_exponent((unsigned char)(e & 0xff)));
+          sm.scale[slot][1][lane % kGroups] = (float)ev;
+          sm.scale[slot][2][lane % kGroups] = pow2(-ev);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.scale_full[slot]);
+        ++nk;
+        return true;
+      };
+      ok = keys(0);
+      if (ok && ahead == 2 && w.nb > 1) ok = keys(1);
+      for (int j = 0; ok && j < w.nb; ++j) {
+        const int st = nv % kVStages, kj = min(j + ahead - 1, w.nb - 1);  // the last block whose keys were asked for
+        ok = fill(&map_v, sm.v[st], &sm.v_full[st], &sm.v_empty[st], kVStages, nv, j / kBatch == kj / kBatch ? row : row_v, j);
+        if (!ok) break;
+        ++nv;
+        if (j + ahead < w.nb) ok = keys(j + ahead);
+      }
     }
-    for (int i = 0; i < 32 && p0 + i < end; ++i) {
-      const long long r = __shfl_sync(0xffffffffu, row, i);
-      const float f = __shfl_sync(0xffffffffu, vscale, i);
-      const uint32_t w = static_cast<const uint32_t*>(A.v_pages)[r * 32 + lane];
-      const float2 a = e4m3x2_to_f32x2(w & 0xffffu), c = e4m3x2_to_f32x2(w >> 16);
-      const float v[4] = {a.x * f, a.y * f, c.x * f, c.y * f};
+    // no copy is in flight when the CTA's shared memory goes (after a timed-out wait nobody may have waited for them)
+    for (int s = 0; s < kKStages && s < nk; ++s) mbar_wait(&sm.k_full[s], (uint32_t)((nk - 1 - s) / kKStages) & 1u, P.err);
+    for (int s = 0; s < kVStages && s < nv; ++s) mbar_wait(&sm.v_full[s], (uint32_t)((nv - 1 - s) / kVStages) & 1u, P.err);
+  } else if (warp == kSoftWarps + 1) {
+    // ---------------- tensor cores: one lane issues, the whole warp computes what it issues
+    Walk<LONG> w(P, sm.run.start, sm.run.req);
+    const uint32_t on = elect_one();
+    constexpr uint32_t idesc_s = make_idesc_e4m3(kRows, kRows);
+    constexpr uint32_t idesc_o = make_idesc_f16(kRows, WI_D) | kIdescNMajorB;
+    int nk = 0, nw = 0;  // blocks of keys and of values taken
+    uint32_t p_par = 0;
+    bool ok = true;
+    auto all_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, P.err));
+    };
+    auto take_keys = [&]() -> bool {
+      if (!all_wait(&sm.k_full[nk % kKStages], (uint32_t)(nk / kKStages) & 1u)) return false;
+      tc_fence_after();
+      return true;
+    };
+    auto scores = [&](int t, int q) {
+      const uint32_t d = __shfl_sync(0xffffffffu, tmem + (uint32_t)t * kRows, 0);
+      const uint32_t a0 = __shfl_sync(0xffffffffu, desc_lo_kmajor(smem_addr(sm.q[q][0])), 0);
+      const uint32_t b0 = __shfl_sync(0xffffffffu, desc_lo_kmajor(smem_addr(sm.k[nk % kKStages])), 0);
 #pragma unroll
-      for (int g = 0; g < kMaxG; ++g) {
-        const float y = __shfl_sync(0xffffffffu, x[g], i);
+      for (int kk = 0; kk < 2 * WI_D / 32; ++kk)  // the first pieces, then the rest
+        mma_e4m3_warp(on, d, a0 + (kk >> 2) * (kBlockBytes / 16) + (kk & 3) * 2, desc_hi_sw128(1024), b0 + (kk & 3) * 2,
+                      desc_hi_sw128(1024), idesc_s, kk > 0);
+      mma_commit_warp(on, &sm.s_full[t]);
+    };
+    auto keys_done = [&] { mma_commit_warp(on, &sm.k_empty[nk % kKStages]); ++nk; };
+    auto values = [&](int t, bool add) {
+      const uint32_t p = __shfl_sync(0xffffffffu, tmem + (uint32_t)t * kRows, 0);
+      const uint32_t b0 = __shfl_sync(0xffffffffu, desc_lo_nmajor(smem_addr(sm.w[nw % kWStages]), 1024), 0);
+      const uint32_t more = __shfl_sync(0xffffffffu, (uint32_t)add, 0);
+      const uint32_t d = __shfl_sync(0xffffffffu, tmem + 256u + (uint32_t)t * WI_D, 0);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[g][k] += y * v[k];
+      for (int kk = 0; kk < kRows / 16; ++kk)
+        mma_bf16_ta_warp(on, d, p + (uint32_t)kk * 8, b0 + (uint32_t)kk * (4096 / 16), desc_hi_sw128(2048), idesc_o,
+                         kk > 0 ? 1u : more);
+    };
+    auto weights_ready = [&](int t) -> bool {
+      if (!all_wait(&sm.p_ready[t], (p_par >> t) & 1u)) return false;
+      p_par ^= 1u << t;
+      tc_fence_after();
+      return true;
+    };
+    for (int seg = 0; ok && w.next(P); ++seg, w.advance()) {
+      if (!(ok = all_wait(&sm.q_full, seg & 1))) break;
+      tc_fence_after();
+      if (!(ok = take_keys())) break;
+      scores(0, 0);
+      if (w.single) {
+        keys_done();
+        if (w.nb > 1) {
+          if (!(ok = take_keys())) break;
+          scores(1, 0);
+          keys_done();
+        }
+      } else {
+        scores(1, 1);
+        keys_done();
+      }
+      for (int j = 0; j < w.nb; ++j) {
+        if (!(ok = all_wait(&sm.w_full[nw % kWStages], (uint32_t)(nw / kWStages) & 1u))) break;
+        if (w.single) {
+          const int t = j & 1;
+          if (!(ok = weights_ready(t))) break;
+          values(t, j >= 2);
+          mma_commit_warp(on, &sm.w_empty[nw % kWStages]);
+          if (j + 2 >= w.nb) {
+            mma_commit_warp(on, &sm.o_full[t]);
+          } else {
+            if (!(ok = take_keys())) break;
+            scores(t, 0);
+            keys_done();
+          }
+        } else {
+          const bool more = j + 1 < w.nb;
+          if (!(ok = weights_ready(0))) break;
+          values(0, j > 0);
+          if (more) {
+            if (!(ok = take_keys())) break;
+            scores(0, 0);
+          } else {
+            mma_commit_warp(on, &sm.o_full[0]);
+          }
+          if (!(ok = weights_ready(1))) break;
+          values(1, j > 0);
+          mma_commit_warp(on, &sm.w_empty[nw % kWStages]);
+          if (more) {
+            scores(1, 1);
+            keys_done();
+          } else {
+            mma_commit_warp(on, &sm.o_full[1]);
+          }
+        }
+        ++nw;
+      }
+    }
+    // every product is done before the tensor memory goes
+    mma_commit_warp(on, &sm.drained);
+    mbar_wait(&sm.drained, 0, P.err);
+  } else {
+    // ---------------- values to f16; in blocks that not every row sees whole, what lies behind the request's end is
+    // zeroed, and so are NaN elements (0 * NaN is NaN inside the product), which the end of the item adds to the rows that
+    // see them
+    Walk<LONG> w(P, sm.run.start, sm.run.req);
+    const int half = warp - kSoftWarps - 2;
+    const int r8 = lane & 7, c0 = lane >> 3;  // a lane's row of a group of eight, and its first 16-byte piece
+    int n = 0;
+    bool ok = true;
+    for (int seg = 0; ok && w.next(P); ++seg, w.advance()) {
+      const int fix = w.first_fix() - w.b0;
+      for (int j = 0; j < w.nb; ++j, ++n) {
+        const int st = n % kVStages, to = n % kWStages;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.v_full[st], (uint32_t)(n / kVStages) & 1u, P.err)))) break;
+        if (n >= kWStages &&
+            !(ok = __all_sync(0xffffffffu, mbar_wait(&sm.w_empty[to], ((uint32_t)(n / kWStages) & 1u) ^ 1u, P.err))))
+          break;
+        const unsigned char* const v = sm.v[st] + r8 * WI_D;
+        unsigned char* const o = sm.w[to] + r8 * 128;
+        const int k0 = (w.b0 + j) * kRows, seen = w.r.kv - k0, clean = w.first_clean() - k0;
+        bool found = false;
+#pragma unroll 4
+        for (int i = half; i < kRows / 8 * 2; i += kWideWarps) {  // group of eight rows, half of their pieces
+          const int g = i >> 1, c = c0 + (i & 1) * 4;
+          const uint4 x = *reinterpret_cast<const uint4*>(v + g * 1024 + ((c ^ r8) << 4));
+          uint32_t e[4] = {x.x, x.y, x.z, x.w};
+          if (j >= fix && 8 * g + r8 >= clean) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t nan = ((e[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // of bytes whose other bits are all ones
+              if (8 * g + r8 >= seen) {
+                e[k] = 0;
+              } else if (nan) {
+                e[k] &= ~((nan >> 7) * 0xffu);
+                found = true;
+              }
+            }
+          }
+          uint32_t h[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            h[2 * k] = e4m3x2_to_f16x2(e[k] & 0xffffu);
+            h[2 * k + 1] = e4m3x2_to_f16x2(e[k] >> 16);
+          }
+          // columns 16 c .. 16 c + 15: two pieces of the half's eight
+          unsigned char* const d = o + g * 2048 + (c >> 2) * 1024;
+          const int p = (c & 3) * 2;
+          *reinterpret_cast<uint4*>(d + ((p ^ r8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(d + (((p + 1) ^ r8) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        if (found) *reinterpret_cast<volatile int*>(&sm.poison[seg & 7]) = seg + 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sm.w_full[to]);
+          mbar_arrive(&sm.v_empty[st]);
+        }
       }
     }
   }
-#pragma unroll
-  for (int g = 0; g < kMaxG; ++g) {
-    if (g >= G) break;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) part[warp][g][4 * lane + c] = acc[g][c];
-    part[warp][g][WI_D] = m[g];
-    part[warp][g][WI_D + 1] = z[g];
-  }
+  tc_fence_before();
   __syncthreads();
-  for (int g = 0; g < G; ++g) {
-    float top = -INFINITY, sum = 0.f, o = 0.f;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part[w][g][WI_D]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2f(part[w][g][WI_D] - ref);
-      sum += f * part[w][g][WI_D + 1];
-      o += f * part[w][g][tid];
-    }
-    const long long at = (long long)t * Hq + kh * G + g;
-    static_cast<bf16*>(A.out)[at * WI_D + tid] = __float2bfloat16_rn(sum == 0.f ? 0.f : o / sum);
-    if (A.lse && tid == 0) A.lse[at] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+  if (warp == kSoftWarps + 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
   }
 }
 
@@ -156,6 +771,40 @@ __global__ void __launch_bounds__(32 * kWarps) k_paged_attention8(WiPagedAttn A,
 cudaError_t wi_launch_paged_attention8(const WiPagedGeom& g, const WiPagedAttn& a, const WiPagedScales& s, int sms,
                                        void* scratch, int* err, cudaStream_t st) {
   if (wi_paged_few(g, a)) return wi_launch_paged_few(g, a, s, sms, scratch, err, st);
-  return wi_launch_chained(k_paged_attention8, dim3((unsigned)(a.n_tokens * (long long)g.Hkv)), 32 * kWarps, 0, st, a, s,
-                           g.Hq, g.Hkv, g.G, g.page, g.n_pages, g.max_pages, err);
+  Rows8 A;
+  Params& P = A.P;
+  A.s = s;
+  P.a = a;
+  P.Hq = g.Hq;
+  P.Hkv = g.Hkv;
+  P.G = g.G;
+  P.tq = kRows / g.G;
+  P.page = g.page;
+  P.n_pages = g.n_pages;
+  P.max_pages = g.max_pages;
+  // a box of a block lies inside one page: the largest power of two that divides the page, 128 at most
+  P.box = g.page & -g.page;
+  if (P.box > kRows) P.box = kRows;
+  const long long rows_here = (long long)a.n_tokens * g.G;
+  const bool here = rows_here <= kMergeHere;
+  P.tickets = here ? static_cast<unsigned*>(scratch) : nullptr;
+  P.splits = reinterpret_cast<Split*>(static_cast<char*>(scratch) + kPagedTicketBytes);
+  P.parts = {reinterpret_cast<float*>(static_cast<char*>(scratch) + kPagedTicketBytes + kSplitBytes),
+             rows_here <= kFewRows ? kFewRows : here ? kMergeHere : kRows, here ? 1 : 2};
+  P.err = err;
+  CUtensorMap map_k, map_v;
+  const unsigned long long rows = (unsigned long long)g.n_pages * g.Hkv * g.page;
+  if (!wi_encode_bytes_sw128(&map_k, a.k_pages, rows, (unsigned)P.box) ||
+      !wi_encode_bytes_sw128(&map_v, a.v_pages, rows, (unsigned)P.box))
+    return cudaErrorInvalidValue;
+  static int smem_set[2][kWiSmemDevices] = {};
+  const bool is_long = (long long)g.max_pages * g.page > (long long)kLongest * kRows;
+  auto* kernel = is_long ? k_paged_attention8<true> : k_paged_attention8<false>;
+  cudaError_t e = wi_ensure_smem(kernel, sizeof(Smem), smem_set[is_long]);
+  if (e != cudaSuccess) return e;
+  const int grid = sms < kPagedMaxSms ? sms : kPagedMaxSms;
+  if ((e = wi_launch_chained(kernel, dim3((unsigned)grid), kThreads, sizeof(Smem), st, map_k, map_v, A)) != cudaSuccess)
+    return e;
+  if (here) return cudaSuccess;
+  return wi_launch_chained(k_paged_merge, dim3((unsigned)grid, 2 * kRows / kMergeRows), kMergeThreads, 0, st, P);
 }

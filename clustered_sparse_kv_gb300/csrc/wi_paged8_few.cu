@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention8_few(const __gr
   fence_proxy_async_smem();
   pdl_wait();
   tc_fence_before();
-  const bool any = find_run<kLead, 1, kThreads>(P, kLeast, sm.scan, &sm.run);  // (with a barrier of all threads)
+  const bool any = find_run<kLead, 1, kThreads>(P, kLeast, 0, sm.scan, &sm.run);  // (with a barrier of all threads)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;  // S at columns 0 and 16, O at 32
   if (!any) {  // the whole CTA leaves

@@ -190,9 +190,10 @@ struct Run {
 };
 
 // This CTA's run of the call's units: equal ones, `least` units at least (a run of a few units would spend more on joining
-// its part with the others than on the part).  False, for the whole CTA, where it has none.
+// its part with the others than on the part); where there is one request, whose items are alike, and they have no more than
+// `whole` units, each of them is a run.  False, for the whole CTA, where it has none.
 template <int LEAD, int TILES, int THREADS>
-__device__ __forceinline__ bool find_run(const Params& P, int least, long long* scan, Run* run) {
+__device__ __forceinline__ bool find_run(const Params& P, int least, int whole, long long* scan, Run* run) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tp = TILES * P.tq;
   const int per = (P.a.batch + THREADS - 1) / THREADS;
   const int rb0 = min(tid * per, P.a.batch);
@@ -236,7 +237,8 @@ __device__ __forceinline__ bool find_run(const Params& P, int least, long long* 
     rb1 = min(rb1, requests_in_order(P));
     __syncthreads();  // the sums are read
   }
-  const int ctas = (int)min((long long)gridDim.x, quot(total + least - 1, least));
+  int ctas = (int)min((long long)gridDim.x, quot(total + least - 1, least));
+  if (P.a.batch == 1 && ctas > P.Hkv && total <= (long long)P.Hkv * whole) ctas = P.Hkv;
   if ((int)blockIdx.x >= ctas) return false;
   const long long u0 = quot(total * blockIdx.x, ctas), u1 = quot(total * (blockIdx.x + 1), ctas);
   if (u0 >= before && u0 < before + mine) {  // one thread's requests hold the run's first unit

@@ -28,6 +28,11 @@ __host__ __device__ constexpr uint32_t make_idesc(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+// ... with f16 A and B (types 0).
+__host__ __device__ constexpr uint32_t make_idesc_f16(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
@@ -106,7 +111,7 @@ __device__ __forceinline__ void mma_bf16_warp(uint32_t on, uint32_t tmem_d, uint
       : "memory");
 }
 
-// The same with A (K-major, two bf16 to a 32-bit column) in tensor memory.
+// The same with A (K-major, two bf16, or f16 by its descriptor, to a 32-bit column) in tensor memory.
 __device__ __forceinline__ void mma_bf16_ta_warp(uint32_t on, uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo,
                                                  uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
