@@ -103,8 +103,24 @@ __device__ __forceinline__ void mask_scores(uint32_t (&s)[2][32], int seen) {
     if (i > seen) s[i >> 5][i & 31] = 0xFF800000u;  // -infinity
 }
 
+// A block's scales as a row takes them, read before its scores are there: the factor of a score, the value's exponent, and
+// its power of two's inverse.
+struct Scales {
+  float f[kGroups], e[kGroups], back[kGroups];
+  __device__ __forceinline__ void load(const float (&from)[3][kGroups], float q_scale) {
+#pragma unroll
+    for (int g = 0; g < kGroups; g += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(&from[0][g]), y = *reinterpret_cast<const float4*>(&from[1][g]),
+                   z = *reinterpret_cast<const float4*>(&from[2][g]);
+      f[g] = x.x * q_scale, f[g + 1] = x.y * q_scale, f[g + 2] = x.z * q_scale, f[g + 3] = x.w * q_scale;
+      e[g] = y.x, e[g + 1] = y.y, e[g + 2] = y.z, e[g + 3] = y.w;
+      back[g] = z.x, back[g + 1] = z.y, back[g + 2] = z.z, back[g + 3] = z.w;
+    }
+  }
+};
+
 // The reference that 64 scores ask for: the largest score + e less kTop, and the largest score less kFar.
-__device__ __forceinline__ float top_of(const uint32_t (&s)[2][32], const float* scale, float q_scale) {
+__device__ __forceinline__ float top_of(const uint32_t (&s)[2][32], const Scales& x8, int g0) {
   float best = -INFINITY;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
@@ -112,20 +128,20 @@ __device__ __forceinline__ float top_of(const uint32_t (&s)[2][32], const float*
     float t = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
     for (int i = 2; i < 16; i += 2) t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-    t *= q_scale * scale[g];
-    best = max3(best, t + (scale[kGroups + g] - kTop), t - kFar);
+    t *= x8.f[g0 + g];
+    best = max3(best, t + (x8.e[g0 + g] - kTop), t - kFar);
   }
   return best;
 }
 
 // 32 scores, two groups of columns, to weights 2^(score + e - ref): added to `sum`, and over the values' scale to `low`, and
 // as f16 to 16 columns of P.
-__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t tp, const float* scale, float q_scale, float ref,
+__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t tp, const Scales& x8, int g0, float ref,
                                         uint64_t& sum, uint64_t& low) {
   uint32_t p[16];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const float f = q_scale * scale[g], e = scale[kGroups + g] - ref, back = scale[2 * kGroups + g];
+    const float f = x8.f[g0 + g], e = x8.e[g0 + g] - ref, back = x8.back[g0 + g];
     const uint64_t f2 = pair(f, f), e2 = pair(e, e);
     uint64_t z = 0;
 #pragma unroll
@@ -320,10 +336,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
       for (int j = from; j < nb; j += step) {
         const int slot = (n0 + j) % kScaleSlots;
         if (ok) ok = mbar_wait(&sm.scale_full[slot], ((n0 + j) / kScaleSlots) & 1, P.err);
+        Scales x8;
+        x8.load(sm.scale[slot], q_scale);
         if (ok) ok = mbar_wait(&sm.s_full[chain], s_par, P.err);
         s_par ^= 1;
         tc_fence_after();
-        const float* const scale = sm.scale[slot][0];
         // The second half of the scores comes while the first is worked on; P then takes the place of the first half,
         // which stays in registers, so that the block can be done again.
         uint32_t a[2][32], b[2][32];
@@ -344,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
             tmem_ld32_nowait(ts + 96, b[1]);
             tmem_wait_ld();
             if (masked) mask_scores(b, seen - 64);
-            const float top = grown ? max3(m, top_of(a, scale, q_scale), top_of(b, scale + 4, q_scale)) : m;
+            const float top = grown ? max3(m, top_of(a, x8, 0), top_of(b, x8, 4)) : m;
             if (j != from) {
               // the chain's products so far are done: S of this block was issued behind them
               const float f = m == top ? 1.f : ex2(m - top);
@@ -364,12 +381,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
           }
           const float ref = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 2^-inf = 0
           uint64_t sum = 0ull, low = 0ull;
-          weights(a[0], ts, scale, q_scale, ref, sum, low);
-          weights(a[1], ts + 16, scale + 2, q_scale, ref, sum, low);
+          weights(a[0], ts, x8, 0, ref, sum, low);
+          weights(a[1], ts + 16, x8, 2, ref, sum, low);
           tmem_wait_ld();
           if (masked && !again) mask_scores(b, seen - 64);
-          weights(b[0], ts + 32, scale + 4, q_scale, ref, sum, low);
-          weights(b[1], ts + 48, scale + 6, q_scale, ref, sum, low);
+          weights(b[0], ts + 32, x8, 4, ref, sum, low);
+          weights(b[1], ts + 48, x8, 6, ref, sum, low);
           const float z = lo_of(sum) + hi_of(sum), zl = lo_of(low) + hi_of(low);
           // A row without a reference (every score so far minus infinity) looks for one in each block that it sees
           // something of: against 0 its weights might all vanish.  A row that sees nothing of the block, or that no token
@@ -719,34 +736,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
         unsigned char* const o = sm.w[to] + r8 * 128;
         const int k0 = (w.b0 + j) * kRows, seen = w.r.kv - k0, clean = w.first_clean() - k0;
         bool found = false;
-#pragma unroll 4
-        for (int i = half; i < kRows / 8 * 2; i += kWideWarps) {  // group of eight rows, half of their pieces
-          const int g = i >> 1, c = c0 + (i & 1) * 4;
-          const uint4 x = *reinterpret_cast<const uint4*>(v + g * 1024 + ((c ^ r8) << 4));
-          uint32_t e[4] = {x.x, x.y, x.z, x.w};
-          if (j >= fix && 8 * g + r8 >= clean) {
+        // a warp takes one half of a row's pieces, eight groups of rows at a time: all their loads in front of the first store
+        const int c = c0 + half * 4, piece = (c & 3) * 2;
+#pragma unroll 1
+        for (int g0 = 0; g0 < kRows / 8; g0 += 8) {
+          uint4 x[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t nan = ((e[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // of bytes whose other bits are all ones
-              if (8 * g + r8 >= seen) {
-                e[k] = 0;
-              } else if (nan) {
-                e[k] &= ~((nan >> 7) * 0xffu);
-                found = true;
+          for (int g = 0; g < 8; ++g) x[g] = *reinterpret_cast<const uint4*>(v + (g0 + g) * 1024 + ((c ^ r8) << 4));
+          if (j >= fix) {
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              const int r = 8 * (g0 + g) + r8;
+              if (r < clean) continue;
+              uint32_t e[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t nan = ((e[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // of bytes whose other bits are all ones
+                if (r >= seen) {
+                  e[k] = 0;
+                } else if (nan) {
+                  e[k] &= ~((nan >> 7) * 0xffu);
+                  found = true;
+                }
               }
+              x[g] = make_uint4(e[0], e[1], e[2], e[3]);
             }
           }
-          uint32_t h[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            h[2 * k] = e4m3x2_to_f16x2(e[k] & 0xffffu);
-            h[2 * k + 1] = e4m3x2_to_f16x2(e[k] >> 16);
+          for (int g = 0; g < 8; ++g) {
+            // columns 16 c .. 16 c + 15: two pieces of the half's eight
+            unsigned char* const d = o + (g0 + g) * 2048 + (c >> 2) * 1024;
+            *reinterpret_cast<uint4*>(d + ((piece ^ r8) << 4)) =
+                make_uint4(e4m3x2_to_f16x2(x[g].x & 0xffffu), e4m3x2_to_f16x2(x[g].x >> 16),
+                           e4m3x2_to_f16x2(x[g].y & 0xffffu), e4m3x2_to_f16x2(x[g].y >> 16));
+            *reinterpret_cast<uint4*>(d + (((piece + 1) ^ r8) << 4)) =
+                make_uint4(e4m3x2_to_f16x2(x[g].z & 0xffffu), e4m3x2_to_f16x2(x[g].z >> 16),
+                           e4m3x2_to_f16x2(x[g].w & 0xffffu), e4m3x2_to_f16x2(x[g].w >> 16));
           }
-          // columns 16 c .. 16 c + 15: two pieces of the half's eight
-          unsigned char* const d = o + g * 2048 + (c >> 2) * 1024;
-          const int p = (c & 3) * 2;
-          *reinterpret_cast<uint4*>(d + ((p ^ r8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(d + (((p + 1) ^ r8) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
         if (found) *reinterpret_cast<volatile int*>(&sm.poison[seg & 7]) = seg + 1;
         fence_proxy_async_smem();
