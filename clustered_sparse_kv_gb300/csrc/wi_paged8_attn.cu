@@ -74,7 +74,11 @@ struct Smem {
   Req reqs[kSoftWarps];     // of the softmax warps' segments
   // of a block's groups: 2^e of the keys, e of the values, 2^-e of the values.  A slot is written again eight blocks on,
   // behind the scores of the block three before that, which come behind the weights of this one.
-  alignas(16) float scale[kScaleSlots][3][kGroups];
+  struct Slot {
+    float2 k[kGroups], e[kGroups];  // (the same number twice)
+    float back[kGroups];
+  };
+  alignas(16) Slot scale[kScaleSlots];
   float q_scale[2][kRows];
   float xch[2][2][kRows];   // maximum and sum of a row, from chain to chain: [chain][m, l]
   alignas(1024) unsigned char q[2][2][kBlockBytes];   // [tile][piece]
@@ -103,24 +107,20 @@ __device__ __forceinline__ void mask_scores(uint32_t (&s)[2][32], int seen) {
     if (i > seen) s[i >> 5][i & 31] = 0xFF800000u;  // -infinity
 }
 
-// A block's scales as a row takes them, read before its scores are there: the factor of a score, the value's exponent, and
-// its power of two's inverse.
+// The scales of two of a block's groups as the weights take them, asked for one step ahead of their use: of the keys and the
+// values' exponents twice, for packed arithmetic, and the inverse of the values'.
 struct Scales {
-  float f[kGroups], e[kGroups], back[kGroups];
-  __device__ __forceinline__ void load(const float (&from)[3][kGroups], float q_scale) {
-#pragma unroll
-    for (int g = 0; g < kGroups; g += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(&from[0][g]), y = *reinterpret_cast<const float4*>(&from[1][g]),
-                   z = *reinterpret_cast<const float4*>(&from[2][g]);
-      f[g] = x.x * q_scale, f[g + 1] = x.y * q_scale, f[g + 2] = x.z * q_scale, f[g + 3] = x.w * q_scale;
-      e[g] = y.x, e[g + 1] = y.y, e[g + 2] = y.z, e[g + 3] = y.w;
-      back[g] = z.x, back[g + 1] = z.y, back[g + 2] = z.z, back[g + 3] = z.w;
-    }
+  ulonglong2 k, e;
+  float2 back;
+  __device__ __forceinline__ void load(const Smem::Slot& from, int g0) {
+    k = *reinterpret_cast<const ulonglong2*>(&from.k[g0]);
+    e = *reinterpret_cast<const ulonglong2*>(&from.e[g0]);
+    back = *reinterpret_cast<const float2*>(&from.back[g0]);
   }
 };
 
 // The reference that 64 scores ask for: the largest score + e less kTop, and the largest score less kFar.
-__device__ __forceinline__ float top_of(const uint32_t (&s)[2][32], const Scales& x8, int g0) {
+__device__ __forceinline__ float top_of(const uint32_t (&s)[2][32], const Smem::Slot& x8, int g0, float q_scale) {
   float best = -INFINITY;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
@@ -128,31 +128,32 @@ __device__ __forceinline__ float top_of(const uint32_t (&s)[2][32], const Scales
     float t = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
     for (int i = 2; i < 16; i += 2) t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-    t *= x8.f[g0 + g];
-    best = max3(best, t + (x8.e[g0 + g] - kTop), t - kFar);
+    t *= x8.k[g0 + g].x * q_scale;
+    best = max3(best, t + (x8.e[g0 + g].x - kTop), t - kFar);
   }
   return best;
 }
 
 // 32 scores, two groups of columns, to weights 2^(score + e - ref): added to `sum`, and over the values' scale to `low`, and
 // as f16 to 16 columns of P.
-__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t tp, const Scales& x8, int g0, float ref,
-                                        uint64_t& sum, uint64_t& low) {
+__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t tp, const Scales& x8, uint64_t q2, uint64_t ref2,
+                                        float& sum, float& low) {
   uint32_t p[16];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const float f = x8.f[g0 + g], e = x8.e[g0 + g] - ref, back = x8.back[g0 + g];
-    const uint64_t f2 = pair(f, f), e2 = pair(e, e);
-    uint64_t z = 0;
+    const uint64_t f2 = mul2(g ? x8.k.y : x8.k.x, q2), e2 = add2(g ? x8.e.y : x8.e.x, ref2);
+    uint64_t z[2];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint64_t x = fma2(pair(s[16 * g + 2 * i], s[16 * g + 2 * i + 1]), f2, e2);
       const float a = ex2(lo_of(x)), b = ex2(hi_of(x));
-      z = i == 0 ? pair(a, b) : add2(z, pair(a, b));
+      z[i & 1] = i < 2 ? pair(a, b) : add2(z[i & 1], pair(a, b));
       p[8 * g + i] = pack_f16(a, b);
     }
-    sum = add2(sum, z);
-    low = fma2(z, pair(back, back), low);
+    const uint64_t z2 = add2(z[0], z[1]);
+    const float zs = lo_of(z2) + hi_of(z2);
+    sum += zs;
+    low += zs * (g ? x8.back.y : x8.back.x);
   }
   tmem_st16_nowait(tp, p);
 }
@@ -211,6 +212,34 @@ __device__ __forceinline__ void add_poison(const Params& P, int b, int kh, int f
     for (int i = 0; i < 16; ++i)
       if ((v[i] & 0x7f) == 0x7f) o[i] = __uint_as_float(0x7fc00000u);
   }
+}
+
+// Rows [from, 128) of a block of values as they came: those behind the request's end (row `seen` of the block) are zeroed, and
+// so are NaN elements, which `flag` is told of.  One half of every row by each of two warps, the half that it widens.
+__device__ __noinline__ void clean_values(unsigned char* v, int lane, int half, int from, int seen, int* flag, int mark) {
+  bool found = false;
+  for (int i = max(from, 0) * (WI_D / 32) + lane; i < kRows * (WI_D / 32); i += 32) {
+    const int r = i / (WI_D / 32), c = i % (WI_D / 32) + half * (WI_D / 32);
+    uint4* const at = reinterpret_cast<uint4*>(v + r * WI_D + ((c ^ (r & 7)) << 4));
+    if (r >= seen) {
+      *at = make_uint4(0u, 0u, 0u, 0u);
+      continue;
+    }
+    const uint4 x = *at;
+    uint32_t e[4] = {x.x, x.y, x.z, x.w}, any = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t nan = ((e[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // of bytes whose other bits are all ones
+      any |= nan;
+      e[k] &= ~((nan >> 7) * 0xffu);
+    }
+    if (any) {
+      *at = make_uint4(e[0], e[1], e[2], e[3]);
+      found = true;
+    }
+  }
+  if (found) *reinterpret_cast<volatile int*>(flag) = mark;
+  __syncwarp();
 }
 
 struct Rows8 {
@@ -337,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
         const int slot = (n0 + j) % kScaleSlots;
         if (ok) ok = mbar_wait(&sm.scale_full[slot], ((n0 + j) / kScaleSlots) & 1, P.err);
         Scales x8;
-        x8.load(sm.scale[slot], q_scale);
+        x8.load(sm.scale[slot], 0);
         if (ok) ok = mbar_wait(&sm.s_full[chain], s_par, P.err);
         s_par ^= 1;
         tc_fence_after();
@@ -351,52 +380,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
         tmem_ld32_nowait(ts + 96, b[1]);
         const bool masked = base + j * kRows + kRows - 1 > whole;
         const int seen = limit - base - j * kRows;  // the row sees columns 0 .. seen of this block
-        if (masked) mask_scores(a, seen);
-        bool again = j == from, grown = again;  // grown: this row takes a new reference (other rows keep theirs)
-        for (;;) {
-          if (again) {  // the first block, or the reference is far too small
-            tmem_wait_st();
-            tmem_wait_ld();
-            tmem_ld32_nowait(ts + 64, b[0]);
-            tmem_ld32_nowait(ts + 96, b[1]);
-            tmem_wait_ld();
-            if (masked) mask_scores(b, seen - 64);
-            const float top = grown ? max3(m, top_of(a, x8, 0), top_of(b, x8, 4)) : m;
-            if (j != from) {
-              // the chain's products so far are done: S of this block was issued behind them
-              const float f = m == top ? 1.f : ex2(m - top);
-              l *= f;
-              const uint32_t to = tmem + lanes + 256u + (uint32_t)chain * WI_D;
-#pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
-                uint32_t o[16];
-                tmem_ld16_nowait(to + 16 * c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tmem_st16_nowait(to + 16 * c, o);
-              }
-            }
-            m = top;
-          }
+        // Weights of the four quarters; whether the row's reference is too small for them.  A row without a reference (every
+        // score so far minus infinity) looks for one in each block that it sees something of: against 0 its weights might all
+        // vanish.  A row that sees nothing of the block, or that no token owns, asks for nothing.
+        float zl;
+        auto all_weights = [&](bool mask_rest) -> bool {
           const float ref = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 2^-inf = 0
-          uint64_t sum = 0ull, low = 0ull;
-          weights(a[0], ts, x8, 0, ref, sum, low);
-          weights(a[1], ts + 16, x8, 2, ref, sum, low);
+          const uint64_t ref2 = pair(-ref, -ref), q2 = pair(q_scale, q_scale);
+          float z = zl = 0.f;
+          Scales y8;
+          y8.load(sm.scale[slot], 2);
+          weights(a[0], ts, x8, q2, ref2, z, zl);
+          x8.load(sm.scale[slot], 4);
+          weights(a[1], ts + 16, y8, q2, ref2, z, zl);
+          y8.load(sm.scale[slot], 6);
           tmem_wait_ld();
-          if (masked && !again) mask_scores(b, seen - 64);
-          weights(b[0], ts + 32, x8, 4, ref, sum, low);
-          weights(b[1], ts + 48, x8, 6, ref, sum, low);
-          const float z = lo_of(sum) + hi_of(sum), zl = lo_of(low) + hi_of(low);
-          // A row without a reference (every score so far minus infinity) looks for one in each block that it sees
-          // something of: against 0 its weights might all vanish.  A row that sees nothing of the block, or that no token
-          // owns, asks for nothing.
-          grown = seen >= 0 && (!(z <= kAgain) || !(zl <= kFarMost) || m == -INFINITY);
-          if (again || !__any_sync(0xffffffffu, grown)) {
-            l += zl;
-            break;
+          if (mask_rest) mask_scores(b, seen - 64);
+          weights(b[0], ts + 32, x8, q2, ref2, z, zl);
+          weights(b[1], ts + 48, y8, q2, ref2, z, zl);
+          return seen >= 0 && (!(z <= kAgain) || !(zl <= kFarMost) || m == -INFINITY);
+        };
+        // Most blocks are seen whole by every row and fit their references: their code stands on its own, without a jump (with
+        // the rest in the same loop, jumped over, a block took 1740 cycles here, 290 of them before its first weight).
+        const bool first = j == from;
+        bool grown = first, again = first;
+        if (__builtin_expect(!(masked || first), 1)) {
+          grown = all_weights(false);
+          again = __any_sync(0xffffffffu, grown);
+          if (!again) l += zl;
+        }
+        if (__builtin_expect(masked || again, 0)) {
+          if (masked) mask_scores(a, seen);
+          for (;;) {
+            if (again) {  // the first block, or the reference is far too small; grown: of this row (other rows keep theirs)
+              tmem_wait_st();
+              tmem_wait_ld();
+              tmem_ld32_nowait(ts + 64, b[0]);
+              tmem_ld32_nowait(ts + 96, b[1]);
+              tmem_wait_ld();
+              if (masked) mask_scores(b, seen - 64);
+              const float top =
+                  grown ? max3(m, top_of(a, sm.scale[slot], 0, q_scale), top_of(b, sm.scale[slot], 4, q_scale)) : m;
+              if (!first) {
+                // the chain's products so far are done: S of this block was issued behind them
+                const float f = m == top ? 1.f : ex2(m - top);
+                l *= f;
+                const uint32_t to = tmem + lanes + 256u + (uint32_t)chain * WI_D;
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                  uint32_t o[16];
+                  tmem_ld16_nowait(to + 16 * c, o);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                  tmem_st16_nowait(to + 16 * c, o);
+                }
+              }
+              m = top;
+            }
+            x8.load(sm.scale[slot], 0);
+            grown = all_weights(masked && !again);
+            if (again || !__any_sync(0xffffffffu, grown)) {
+              l += zl;
+              break;
+            }
+            again = true;
           }
-          again = true;
         }
         tmem_wait_st();
         tc_fence_before();
@@ -593,9 +642,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
         if (!fill(&map_k, sm.k[st], &sm.k_full[st], &sm.k_empty[st], kKStages, nk, row, j)) return false;
         if (lane / kGroups == j % kBatch) {
           const int ev = scale_exponent((unsigned char)(e >> 8));
-          sm.scale[slot][0][lane % kGroups] = pow2(scale_exponent((unsigned char)(e & 0xff)));
-          sm.scale[slot][1][lane % kGroups] = (float)ev;
-          sm.scale[slot][2][lane % kGroups] = pow2(-ev);
+          const float ks = pow2(scale_exponent((unsigned char)(e & 0xff)));
+          sm.scale[slot].k[lane % kGroups] = make_float2(ks, ks);
+          sm.scale[slot].e[lane % kGroups] = make_float2((float)ev, (float)ev);
+          sm.scale[slot].back[lane % kGroups] = pow2(-ev);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.scale_full[slot]);
@@ -721,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
     // see them
     Walk<LONG> w(P, sm.run.start, sm.run.req);
     const int half = warp - kSoftWarps - 2;
-    const int r8 = lane & 7, c0 = lane >> 3;  // a lane's row of a group of eight, and its first 16-byte piece
+    const int r8 = lane & 7, c = (lane >> 3) + 4 * half, piece = (c & 3) * 2;  // a lane's row of a group, and piece of the row
     int n = 0;
     bool ok = true;
     for (int seg = 0; ok && w.next(P); ++seg, w.advance()) {
@@ -732,40 +782,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
         if (n >= kWStages &&
             !(ok = __all_sync(0xffffffffu, mbar_wait(&sm.w_empty[to], ((uint32_t)(n / kWStages) & 1u) ^ 1u, P.err))))
           break;
-        const unsigned char* const v = sm.v[st] + r8 * WI_D;
-        unsigned char* const o = sm.w[to] + r8 * 128;
-        const int k0 = (w.b0 + j) * kRows, seen = w.r.kv - k0, clean = w.first_clean() - k0;
-        bool found = false;
-        // a warp takes one half of a row's pieces, eight groups of rows at a time: all their loads in front of the first store
-        const int c = c0 + half * 4, piece = (c & 3) * 2;
+        if (j >= fix) clean_values(sm.v[st], lane, half, w.first_clean() - (w.b0 + j) * kRows, w.r.kv - (w.b0 + j) * kRows,
+                                   &sm.poison[seg & 7], seg + 1);
+        const unsigned char* const v = sm.v[st] + r8 * WI_D + ((c ^ r8) << 4);
+        unsigned char* const o = sm.w[to] + (c >> 2) * 1024 + r8 * 128;
+        // a warp takes one half of a row's pieces, four groups of rows at a time: all their loads in front of the first store
 #pragma unroll 1
-        for (int g0 = 0; g0 < kRows / 8; g0 += 8) {
-          uint4 x[8];
+        for (int g0 = 0; g0 < kRows / 8; g0 += 4) {
+          uint4 x[4];
 #pragma unroll
-          for (int g = 0; g < 8; ++g) x[g] = *reinterpret_cast<const uint4*>(v + (g0 + g) * 1024 + ((c ^ r8) << 4));
-          if (j >= fix) {
+          for (int g = 0; g < 4; ++g) x[g] = *reinterpret_cast<const uint4*>(v + (g0 + g) * 1024);
 #pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              const int r = 8 * (g0 + g) + r8;
-              if (r < clean) continue;
-              uint32_t e[4] = {x[g].x, x[g].y, x[g].z, x[g].w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t nan = ((e[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // of bytes whose other bits are all ones
-                if (r >= seen) {
-                  e[k] = 0;
-                } else if (nan) {
-                  e[k] &= ~((nan >> 7) * 0xffu);
-                  found = true;
-                }
-              }
-              x[g] = make_uint4(e[0], e[1], e[2], e[3]);
-            }
-          }
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
+          for (int g = 0; g < 4; ++g) {
             // columns 16 c .. 16 c + 15: two pieces of the half's eight
-            unsigned char* const d = o + (g0 + g) * 2048 + (c >> 2) * 1024;
+            unsigned char* const d = o + (g0 + g) * 2048;
             *reinterpret_cast<uint4*>(d + ((piece ^ r8) << 4)) =
                 make_uint4(e4m3x2_to_f16x2(x[g].x & 0xffffu), e4m3x2_to_f16x2(x[g].x >> 16),
                            e4m3x2_to_f16x2(x[g].y & 0xffffu), e4m3x2_to_f16x2(x[g].y >> 16));
@@ -774,7 +804,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
                            e4m3x2_to_f16x2(x[g].w & 0xffffu), e4m3x2_to_f16x2(x[g].w >> 16));
           }
         }
-        if (found) *reinterpret_cast<volatile int*>(&sm.poison[seg & 7]) = seg + 1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
