@@ -4,39 +4,44 @@
 #include "wi_common.cuh"
 #include "wi_e4m3.cuh"
 #include "wi_paged.h"
+#include "wi_paged_write.cuh"
 #include "wi_pipe.cuh"
 
 namespace {
 
-// ------------------------------------------------------------------- append
+// -------------------------------------------------------------------- write
 //
-// A group of sixteen positions of a head has one scale, so its new rows are
-// looked at together: a run is what a call writes of one group, tokens that
-// follow one another in rising slots, and a warp takes a run's rows of one
-// head's keys or values into registers (sixteen lanes hold a row of 128
-// elements, eight each), norms and turns the keys, reduces their largest
-// value, and rounds.  Where the group's scale grows the rows in front of the run
-// are rounded again.  A CTA takes the runs that begin in its tile of tokens,
-// one after the other, with the rotation's cosines and sines of a run's rows in
-// shared memory for all heads.
-constexpr int kApThreads = 128;
+// One launch, two kinds of CTAs.  The queries go as in the bf16 write, a warp to
+// heads of one token.  Keys and values: a group of sixteen positions of a head has
+// one scale, so its new rows are looked at together.  A run is what a call writes
+// of one group, tokens that follow one another in rising slots; a warp takes a
+// run's rows of one head's keys or values into registers (sixteen lanes hold a row
+// of 128 elements, eight each), norms and turns the keys, reduces their largest
+// value, and rounds.  Where the group's scale grows the rows in front of the run are
+// rounded again.  A CTA takes the runs that begin in its tile of tokens, one after
+// the other, with the rotation's cosines and sines of a run's rows in shared memory
+// for all heads of keys.
 constexpr int kApTile = 16;  // tokens of a tile, where there are many
 
+struct Append {
+  int tile;          // tokens of a tile
+  int ctas;          // CTAs of keys and values
+  int parts;         // ... of a tile's keys, and as many of its values
+};
+
 template <bool INTER>
-__global__ void __launch_bounds__(kApThreads) k_paged_append8(const __grid_constant__ WiPagedWrite A, WiPagedScales S,
-                                                             const __grid_constant__ WiRope R, int Hkv, int page,
-                                                             int n_slots, float eps, int tile, int* err) {
-  __shared__ float2 turns[kGroup][WI_D / 2];
+__device__ __forceinline__ void append_rows(const WiPagedWrite& A, const WiPagedScales& S, const WiRope& R, int Hkv, int page,
+                                            int n_slots, float eps, const Append& G, float2 (*turns)[WI_D / 2], int* err) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane & 15, row1 = lane >> 4;
-  pdl_trigger();
-  pdl_wait();
+  const int tile = G.tile, which = blockIdx.x % (2 * G.parts);  // keys' CTAs of the tile, then values'
+  const bool is_key = which < G.parts;
   // lane i has the slot of token t0 - 1 + i: the tile's, the one before it, and what a run may have behind it
-  const long long t0 = (long long)blockIdx.x * tile;
+  const long long t0 = (long long)(blockIdx.x / (2 * G.parts)) * tile;
   const long long mine = t0 - 1 + lane;
   int slot = -1;
   if (mine >= 0 && mine < A.n_tokens && A.positions[mine] >= 0) slot = A.slots[mine];
   if (slot >= n_slots) {
-    if (lane > 0 && lane <= tile) atomicOr(err, WI_DEVERR_BAD_PAGE);
+    if (lane > 0 && lane <= tile && which == 0) atomicOr(err, WI_DEVERR_BAD_PAGE);
     slot = -1;
   }
   const int before = __shfl_up_sync(0xffffffffu, slot, 1);
@@ -51,9 +56,9 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append8(const __grid_const
     const int len = at < 31 ? __ffs(~(follow >> (at + 1))) : 1;  // rows of the run: kGroup at most
     const int first = __shfl_sync(0xffffffffu, slot, at), off = first % kGroup;
     const long long t = t0 - 1 + at;
-    if (half) {
+    if (is_key && half) {
       __syncthreads();  // the last run's are read
-      for (int i = tid; i < len * half; i += kApThreads) {
+      for (int i = tid; i < len * half; i += kWrThreads) {
         const int r = i / half, p = i - r * half;
         const int pos = A.positions[(long long)R.axis[p] * A.n_tokens + t + r];
         // the product's low 64 bits are the fraction of a turn, as in the bf16 write
@@ -65,9 +70,7 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append8(const __grid_const
       __syncthreads();
     }
     const int pg = first / page, row = first - pg * page;
-    for (int u = blockIdx.y * (kApThreads / 32) + warp; u < 2 * Hkv; u += gridDim.y * (kApThreads / 32)) {
-      const bool is_key = u < Hkv;
-      const int h = is_key ? u : u - Hkv;
+    for (int h = (is_key ? which : which - G.parts) * (kWrThreads / 32) + warp; h < Hkv; h += G.parts * (kWrThreads / 32)) {
       const int ea = is_key ? o0 : 8 * l, eb = is_key ? o1 : 8 * l + 4;  // this lane's elements of a row
       const bf16* from = (is_key ? static_cast<const bf16*>(A.k) + t * A.k_stride : static_cast<const bf16*>(A.v) + t * A.v_stride) +
                          h * WI_D;
@@ -185,6 +188,27 @@ __global__ void __launch_bounds__(kApThreads) k_paged_append8(const __grid_const
   }
 }
 
+// INTER, FULL, AXES: as in the bf16 write.
+template <bool INTER, bool FULL, bool AXES>
+__global__ void __launch_bounds__(kWrThreads, 4) k_paged_write8(const __grid_constant__ WiPagedWrite A,
+                                                               const WiPagedScales S, const __grid_constant__ WiRope R,
+                                                               int Hq, int Hkv, int page, int n_slots, float eps, int parts,
+                                                               const Append G, int* err) {
+  __shared__ __align__(16) unsigned char rows[kWrThreads / 32][kWrStages * kWrBatch];
+  static_assert(sizeof(rows) >= kGroup * (WI_D / 2) * sizeof(float2), "the cosines and sines of a run");
+  pdl_trigger();
+  pdl_wait();
+  if ((int)blockIdx.x < G.ctas) {
+    append_rows<INTER>(A, S, R, Hkv, page, n_slots, eps, G, reinterpret_cast<float2(*)[WI_D / 2]>(rows), err);
+  } else {
+    WiPagedWrite Q = A;  // no keys and values, so no slots either
+    Q.slots = nullptr;
+    write_rows<INTER, FULL, AXES>(Q, R, Hq, 0, page, n_slots, eps, parts,
+                                  (long long)(blockIdx.x - G.ctas) * (kWrThreads / 32) + (threadIdx.x >> 5),
+                                  rows[threadIdx.x >> 5], err);
+  }
+}
+
 // ------------------------------------------------------------------- gather
 //
 // Eight lanes move one row: sixteen values each, to thirty-two bytes of bf16.
@@ -276,19 +300,25 @@ __global__ void __launch_bounds__(kGaThreads) k_paged_gather8(WiPagedGather A, W
 
 cudaError_t wi_launch_paged_write8(const WiPagedGeom& g, const WiPagedWrite& w, const WiPagedScales& s, int sms, int* err,
                                    cudaStream_t st) {
-  // the queries by the bf16 write, which is told of no kv heads
-  WiPagedGeom queries = g;
-  queries.Hkv = 0;
-  WiPagedWrite a = w;
-  a.slots = nullptr;
-  const cudaError_t e = wi_launch_paged_write(queries, a, sms, err, st);
-  if (e != cudaSuccess) return e;
-  const int per = kApThreads / 32, units = (2 * g.Hkv + per - 1) / per;
-  const int tile = (long long)w.n_tokens * units > 16LL * sms ? kApTile : 1;
-  const unsigned tiles = (unsigned)((w.n_tokens + tile - 1) / tile);
-  auto* kernel = g.rope.interleaved ? k_paged_append8<true> : k_paged_append8<false>;
-  return wi_launch_chained(kernel, dim3(tiles, (unsigned)units), kApThreads, 0, st, w, s, g.rope, g.Hkv, g.page,
-                           g.n_pages * g.page, g.eps, tile, err);
+  constexpr int kWarps = kWrThreads / 32;
+  Append G;
+  G.parts = (g.Hkv + kWarps - 1) / kWarps;
+  // tiles of one token where that gives no more CTAs than the machine holds at once
+  G.tile = 2LL * w.n_tokens * G.parts > 4LL * sms ? kApTile : 1;
+  const long long ctas = 2LL * G.parts * ((w.n_tokens + G.tile - 1) / G.tile);
+  const int batches = (g.Hq + 7) / 8;
+  long long parts = ((long long)kWrPerSm * sms + w.n_tokens - 1) / w.n_tokens;  // as in the bf16 write
+  if (parts > batches) parts = batches;
+  const long long grid = ctas + (parts * w.n_tokens + kWarps - 1) / kWarps;
+  if (grid > 2147483647LL) return cudaErrorInvalidConfiguration;
+  G.ctas = (int)ctas;
+  const bool full = g.rope.rotary == WI_D, axes = g.rope.axes > 1, inter = g.rope.interleaved;
+  auto* kernel = axes ? (inter ? (full ? k_paged_write8<true, true, true> : k_paged_write8<true, false, true>)
+                               : (full ? k_paged_write8<false, true, true> : k_paged_write8<false, false, true>))
+                      : (inter ? (full ? k_paged_write8<true, true, false> : k_paged_write8<true, false, false>)
+                               : (full ? k_paged_write8<false, true, false> : k_paged_write8<false, false, false>));
+  return wi_launch_chained(kernel, dim3((unsigned)grid), kWrThreads, 0, st, w, s, g.rope, g.Hq, g.Hkv, g.page,
+                           g.n_pages * g.page, g.eps, (int)parts, G, err);
 }
 
 cudaError_t wi_launch_paged_gather8(const WiPagedGeom& g, const WiPagedGather& a, const WiPagedScales& s, int* err,
