@@ -14,14 +14,16 @@ namespace {
 // One launch, two kinds of CTAs.  The queries go as in the bf16 write, a warp to
 // heads of one token.  Keys and values: a group of sixteen positions of a head has
 // one scale, so its new rows are looked at together.  A run is what a call writes
-// of one group, tokens that follow one another in rising slots; a warp takes a
+// of one group, tokens that follow one another in rising slots; two warps take a
 // run's rows of one head's keys or values into registers (sixteen lanes hold a row
-// of 128 elements, eight each), norms and turns the keys, reduces their largest
-// value, and rounds.  Where the group's scale grows the rows in front of the run are
-// rounded again.  A CTA takes the runs that begin in its tile of tokens, one after
-// the other, with the rotation's cosines and sines of a run's rows in shared memory
-// for all heads of keys.
-constexpr int kApTile = 16;  // tokens of a tile, where there are many
+// of 128 elements, eight each), norm and turn the keys, find their largest value
+// (the one exchange between them), and round.  Where the group's scale grows the
+// rows in front of the run are rounded again.  A CTA takes the runs that begin in its
+// tile of tokens, one after the other, with the rotation's cosines and sines of a
+// run's rows in shared memory for its heads of keys; the first head's rows are asked
+// for before those are worked out.
+constexpr int kApTile = 16;   // tokens of a tile, where there are many
+constexpr int kApHeads = 2;   // heads that a CTA has at once
 
 struct Append {
   int tile;          // tokens of a tile
@@ -29,19 +31,30 @@ struct Append {
   int parts;         // ... of a tile's keys, and as many of its values
 };
 
-template <bool INTER>
-__device__ __forceinline__ void append_rows(const WiPagedWrite& A, const WiPagedScales& S, const WiRope& R, int Hkv, int page,
-                                            int n_slots, float eps, const Append& G, float2 (*turns)[WI_D / 2], int* err) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane & 15, row1 = lane >> 4;
-  const int tile = G.tile, which = blockIdx.x % (2 * G.parts);  // keys' CTAs of the tile, then values'
-  const bool is_key = which < G.parts;
+// A run's rotation: cosine, sine and minus sine of a pair and row.
+struct Turns {
+  float c[kGroup][WI_D / 2], s[kGroup][WI_D / 2], n[kGroup][WI_D / 2];
+};
+
+template <bool INTER, bool KEY>
+__device__ __forceinline__ void append_rows(const WiPagedWrite& A, unsigned char* const scales, const WiRope& R, int Hkv,
+                                            int page, int n_slots, float eps, const Append& G, int which, Turns& turns,
+                                            uint32_t (*tops)[kWrThreads / 32], int* err) {
+  constexpr int kRows = kGroup / 4;  // rows of a lane
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, l = lane & 15;
+  const int row1 = 2 * (warp & 1) + (lane >> 4);  // rows row1, row1 + 4, ..
+  const int tile = G.tile;
   // lane i has the slot of token t0 - 1 + i: the tile's, the one before it, and what a run may have behind it
   const long long t0 = (long long)(blockIdx.x / (2 * G.parts)) * tile;
   const long long mine = t0 - 1 + lane;
   int slot = -1;
-  if (mine >= 0 && mine < A.n_tokens && A.positions[mine] >= 0) slot = A.slots[mine];
+  if (mine >= 0 && mine < A.n_tokens) {
+    const int pos = A.positions[mine];
+    slot = A.slots[mine];
+    if (pos < 0) slot = -1;
+  }
   if (slot >= n_slots) {
-    if (lane > 0 && lane <= tile && which == 0) atomicOr(err, WI_DEVERR_BAD_PAGE);
+    if (KEY && which == 0 && lane > 0 && lane <= tile) atomicOr(err, WI_DEVERR_BAD_PAGE);
     slot = -1;
   }
   const int before = __shfl_up_sync(0xffffffffu, slot, 1);
@@ -49,15 +62,46 @@ __device__ __forceinline__ void append_rows(const WiPagedWrite& A, const WiPaged
   uint32_t starts = __ballot_sync(0xffffffffu, begins && lane > 0 && lane <= tile);
   const uint32_t follow = __ballot_sync(0xffffffffu, slot >= 0 && !begins);
   const int half = R.rotary >> 1;
-  const bool turned = INTER ? 8 * l < R.rotary : 4 * l < half;
-  const int o0 = !INTER && turned ? 4 * l : 8 * l, o1 = !INTER && turned ? 4 * l + half : 8 * l + 4;
+  const bool turned = KEY && (INTER ? 8 * l < R.rotary : 4 * l < half);
+  const int ea = KEY && !INTER && turned ? 4 * l : 8 * l, eb = KEY && !INTER && turned ? 4 * l + half : 8 * l + 4;
+  const bf16* const w = KEY ? static_cast<const bf16*>(A.k_weight) : nullptr;
+  uint64_t wa[2], wb[2];
+  if (KEY && w) {
+    const uint2 x = ldg_u2(w + ea), y = ldg_u2(w + eb);
+    wa[0] = unpack2(x.x), wa[1] = unpack2(x.y), wb[0] = unpack2(y.x), wb[1] = unpack2(y.y);
+  }
+  const long long step = KEY ? A.k_stride : A.v_stride;
+  int turn = 0;  // of the exchange between two warps
   for (; starts; starts &= starts - 1) {
     const int at = __ffs(starts) - 1;
     const int len = at < 31 ? __ffs(~(follow >> (at + 1))) : 1;  // rows of the run: kGroup at most
     const int first = __shfl_sync(0xffffffffu, slot, at), off = first % kGroup;
     const long long t = t0 - 1 + at;
-    if (is_key && half) {
-      __syncthreads();  // the last run's are read
+    const int pg = first / page, row = first - pg * page;
+    uint2 raw[kRows][2];
+    int was = -128;
+    const int h0 = which * kApHeads;
+    auto fetch = [&](int h) {
+      const bf16* from = static_cast<const bf16*>(KEY ? A.k : A.v) + t * step + h * WI_D;
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        raw[k][0] = raw[k][1] = make_uint2(0u, 0u);
+        if (h < Hkv && 4 * k + row1 < len) {
+          if (KEY) {
+            raw[k][0] = ldg_u2(from + (4 * k + row1) * step + ea);
+            raw[k][1] = ldg_u2(from + (4 * k + row1) * step + eb);
+          } else {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(from + (4 * k + row1) * step + ea));
+            raw[k][0] = make_uint2(x.x, x.y);
+            raw[k][1] = make_uint2(x.z, x.w);
+          }
+        }
+      }
+      if (off > 0 && h < Hkv) was = scale_exponent(scales[((long long)pg * Hkv + h) * (page / kGroup) + row / kGroup]);
+    };
+    fetch(h0 + (warp >> 1));
+    if (KEY && half) {
+      if (turn) __syncthreads();  // the last run's are read
       for (int i = tid; i < len * half; i += kWrThreads) {
         const int r = i / half, p = i - r * half;
         const int pos = A.positions[(long long)R.axis[p] * A.n_tokens + t + r];
@@ -65,101 +109,99 @@ __device__ __forceinline__ void append_rows(const WiPagedWrite& A, const WiPaged
         const long long a = (long long)(R.turn[p] * (unsigned long long)pos);
         float c, s;
         sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &s, &c);
-        turns[r][p] = make_float2(c * R.scale, s * R.scale);
+        turns.c[r][p] = c * R.scale;
+        turns.s[r][p] = s * R.scale;
+        turns.n[r][p] = -s * R.scale;
       }
       __syncthreads();
     }
-    const int pg = first / page, row = first - pg * page;
-    for (int h = (is_key ? which : which - G.parts) * (kWrThreads / 32) + warp; h < Hkv; h += G.parts * (kWrThreads / 32)) {
-      const int ea = is_key ? o0 : 8 * l, eb = is_key ? o1 : 8 * l + 4;  // this lane's elements of a row
-      const bf16* from = (is_key ? static_cast<const bf16*>(A.k) + t * A.k_stride : static_cast<const bf16*>(A.v) + t * A.v_stride) +
-                         h * WI_D;
-      const long long step = is_key ? A.k_stride : A.v_stride;
+    for (int hp = h0; hp < Hkv; hp += G.parts * kApHeads, ++turn) {  // (the same turns for all warps)
+      const int h = hp + (warp >> 1);
+      uint64_t a[kRows][2], b[kRows][2];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          a[k][c] = unpack2(c ? raw[k][0].y : raw[k][0].x);
+          b[k][c] = unpack2(c ? raw[k][1].y : raw[k][1].x);
+        }
+      const int held = was;  // exponent of the scale that the rows in front of the run have
+      if (hp + G.parts * kApHeads < Hkv) fetch(h + G.parts * kApHeads);
+      if (KEY && w) {
+        // the four rows' sums of squares are reduced together, a quarter of the lanes ending with each
+        float v[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          const float2 ss = unpair(fma2(a[k][0], a[k][0], fma2(a[k][1], a[k][1], fma2(b[k][0], b[k][0], mul2(b[k][1], b[k][1])))));
+          v[k] = ss.x + ss.y;
+        }
+        const bool up8 = l & 8, up4 = l & 4;
+        float k0 = up8 ? v[2] : v[0], k1 = up8 ? v[3] : v[1];
+        k0 += __shfl_xor_sync(0xffffffffu, up8 ? v[0] : v[2], 8);
+        k1 += __shfl_xor_sync(0xffffffffu, up8 ? v[1] : v[3], 8);
+        float r = (up4 ? k1 : k0) + __shfl_xor_sync(0xffffffffu, up4 ? k0 : k1, 4);
+        r += __shfl_xor_sync(0xffffffffu, r, 2);
+        r += __shfl_xor_sync(0xffffffffu, r, 1);
+        r = rsqrtf(r * (1.f / WI_D) + eps);
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          const float inv = __shfl_sync(0xffffffffu, r, (lane & 16) + 4 * k);
+          const uint64_t f = pair2(inv, inv);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            a[k][c] = mul2(mul2(a[k][c], f), wa[c]);
+            b[k][c] = mul2(mul2(b[k][c], f), wb[c]);
+          }
+        }
+      }
+      if (turned) {
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          const int r = 4 * k + row1;
+          if (r >= len) continue;
+          const float4 c4 = *reinterpret_cast<const float4*>(&turns.c[r][4 * l]), s4 = *reinterpret_cast<const float4*>(&turns.s[r][4 * l]);
+          const float4 n4 = *reinterpret_cast<const float4*>(&turns.n[r][4 * l]);
+          if (INTER) {  // both words hold whole pairs
+            a[k][0] = fma2(a[k][0], pair2(c4.x, c4.x), mul2(swap2(a[k][0]), pair2(n4.x, s4.x)));
+            a[k][1] = fma2(a[k][1], pair2(c4.y, c4.y), mul2(swap2(a[k][1]), pair2(n4.y, s4.y)));
+            b[k][0] = fma2(b[k][0], pair2(c4.z, c4.z), mul2(swap2(b[k][0]), pair2(n4.z, s4.z)));
+            b[k][1] = fma2(b[k][1], pair2(c4.w, c4.w), mul2(swap2(b[k][1]), pair2(n4.w, s4.w)));
+          } else {
+            const uint64_t c2[2] = {pair2(c4.x, c4.y), pair2(c4.z, c4.w)}, s2[2] = {pair2(s4.x, s4.y), pair2(s4.z, s4.w)};
+            const uint64_t n2[2] = {pair2(n4.x, n4.y), pair2(n4.z, n4.w)};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint64_t x = a[k][c];
+              a[k][c] = fma2(x, c2[c], mul2(b[k][c], n2[c]));
+              b[k][c] = fma2(b[k][c], c2[c], mul2(x, s2[c]));
+            }
+          }
+        }
+      }
+      auto largest = [&](bool finite) -> uint32_t {
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < kRows; ++k)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 x = unpair(c < 2 ? a[k][c & 1] : b[k][c & 1]);
+            const uint32_t u = __float_as_uint(x.x) & 0x7fffffffu, v = __float_as_uint(x.y) & 0x7fffffffu;
+            top = max(top, finite && u >= 0x7f800000u ? 0u : u);
+            top = max(top, finite && v >= 0x7f800000u ? 0u : v);
+          }
+        return __reduce_max_sync(0xffffffffu, top);
+      };
+      uint32_t top = largest(false);
+      if (top >= 0x7f800000u) top = largest(true);  // the largest finite value
+      if (lane == 0) tops[turn & 1][warp] = top;
+      __syncthreads();  // (the other of the two is free again: what was there was read in front of the barrier before)
+      if (h >= Hkv) continue;
+      const int e = max(scale_needed(max(tops[turn & 1][warp], tops[turn & 1][warp ^ 1])), held);
       unsigned char* const to =
-          static_cast<unsigned char*>(is_key ? A.k_out : A.v_out) + (((long long)pg * Hkv + h) * page + row - off) * WI_D;
-      unsigned char* const scale =
-          (is_key ? S.k : S.v) + ((long long)pg * Hkv + h) * (page / kGroup) + row / kGroup;
-      float x[kGroup / 2][8];
-      uint2 raw[kGroup / 2][2];
-#pragma unroll
-      for (int k = 0; k < kGroup / 2; ++k) {
-        raw[k][0] = raw[k][1] = make_uint2(0u, 0u);
-        if (2 * k + row1 < len) {
-          raw[k][0] = ldg_u2(from + (2 * k + row1) * step + ea);
-          raw[k][1] = ldg_u2(from + (2 * k + row1) * step + eb);
-        }
-      }
-      const int was = off > 0 ? scale_exponent(*scale) : -128;
-      float wa[4] = {1.f, 1.f, 1.f, 1.f}, wb[4] = {1.f, 1.f, 1.f, 1.f};
-      const bf16* w = static_cast<const bf16*>(A.k_weight);
-      if (is_key && w) {
-        load_bf16x4(w + ea, wa);
-        load_bf16x4(w + eb, wb);
-      }
-      uint32_t top = 0;
-#pragma unroll
-      for (int k = 0; k < kGroup / 2; ++k) {
-        float a[4], b[4];
-        unpack_bf16x4(raw[k][0], a);
-        unpack_bf16x4(raw[k][1], b);
-        if (is_key) {
-          if (w) {
-            float ss = 0.f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) ss += a[c] * a[c] + b[c] * b[c];
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float inv = rsqrtf(ss * (1.f / WI_D) + eps);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              a[c] *= inv * wa[c];
-              b[c] *= inv * wb[c];
-            }
-          }
-          if (turned && 2 * k + row1 < len) {
-            const float2* f = turns[2 * k + row1] + 4 * l;
-            if (INTER) {
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const float a0 = a[2 * c], b0 = b[2 * c];
-                a[2 * c] = a0 * f[c].x - a[2 * c + 1] * f[c].y;
-                a[2 * c + 1] = a[2 * c + 1] * f[c].x + a0 * f[c].y;
-                b[2 * c] = b0 * f[2 + c].x - b[2 * c + 1] * f[2 + c].y;
-                b[2 * c + 1] = b[2 * c + 1] * f[2 + c].x + b0 * f[2 + c].y;
-              }
-            } else {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float a0 = a[c];
-                a[c] = a0 * f[c].x - b[c] * f[c].y;
-                b[c] = b[c] * f[c].x + a0 * f[c].y;
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          x[k][c] = a[c];
-          x[k][4 + c] = b[c];
-          top = max(top, max(__float_as_uint(a[c]) & 0x7fffffffu, __float_as_uint(b[c]) & 0x7fffffffu));
-        }
-      }
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (top >= 0x7f800000u) {  // the largest finite value
-        top = 0;
-#pragma unroll
-        for (int k = 0; k < kGroup / 2; ++k)
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const uint32_t v = __float_as_uint(x[k][c]) & 0x7fffffffu;
-            top = max(top, v >= 0x7f800000u ? 0u : v);
-          }
-        top = __reduce_max_sync(0xffffffffu, top);
-      }
-      const int e = max(scale_needed(top), was);
-      if (off > 0 && e > was) {  // the rows in front are rounded again
-        const float f = pow2(max(was - e, -30));  // (2^-30 takes the largest value to nothing)
-        for (int r = row1; r < off; r += 2) {
+          static_cast<unsigned char*>(KEY ? A.k_out : A.v_out) + (((long long)pg * Hkv + h) * page + row - off) * WI_D;
+      if (off > 0 && e > held) {  // the rows in front are rounded again
+        const float f = pow2(max(held - e, -30));  // (2^-30 takes the largest value to nothing)
+        for (int r = row1; r < off; r += 4) {
           uint2* p = reinterpret_cast<uint2*>(to + r * WI_D + 8 * l);
           const uint2 v = *p;
           uint32_t n[2];
@@ -172,17 +214,27 @@ __device__ __forceinline__ void append_rows(const WiPagedWrite& A, const WiPaged
           *p = make_uint2(n[0], n[1]);
         }
       }
-      if (lane == 0) *scale = (unsigned char)(e + kScaleBias);
+      if (lane == 0 && !(warp & 1))
+        scales[((long long)pg * Hkv + h) * (page / kGroup) + row / kGroup] = (unsigned char)(e + kScaleBias);
       const float f = pow2(-e);
+      const uint64_t f2 = pair2(f, f);
 #pragma unroll
-      for (int k = 0; k < kGroup / 2; ++k) {
-        if (2 * k + row1 >= len) continue;
-        float y[8];
+      for (int k = 0; k < kRows; ++k) {
+        if (4 * k + row1 >= len) continue;
+        uint32_t y[2];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) y[c] = fmaf(x[k][c], 0.f, x[k][c] * f);  // an infinity becomes NaN
-        unsigned char* const d = to + (off + 2 * k + row1) * WI_D;
-        *reinterpret_cast<uint32_t*>(d + ea) = e4m3x4_of(y[0], y[1], y[2], y[3]);
-        *reinterpret_cast<uint32_t*>(d + eb) = e4m3x4_of(y[4], y[5], y[6], y[7]);
+        for (int c = 0; c < 2; ++c) {
+          const uint64_t x0 = c ? b[k][0] : a[k][0], x1 = c ? b[k][1] : a[k][1];
+          const float2 y0 = unpair(fma2(x0, 0ull, mul2(x0, f2))), y1 = unpair(fma2(x1, 0ull, mul2(x1, f2)));  // an infinity becomes NaN
+          y[c] = e4m3x4_of(y0.x, y0.y, y1.x, y1.y);
+        }
+        unsigned char* const d = to + (off + 4 * k + row1) * WI_D;
+        if (KEY) {
+          *reinterpret_cast<uint32_t*>(d + ea) = y[0];
+          *reinterpret_cast<uint32_t*>(d + eb) = y[1];
+        } else {
+          *reinterpret_cast<uint2*>(d + ea) = make_uint2(y[0], y[1]);
+        }
       }
     }
   }
@@ -190,16 +242,22 @@ __device__ __forceinline__ void append_rows(const WiPagedWrite& A, const WiPaged
 
 // INTER, FULL, AXES: as in the bf16 write.
 template <bool INTER, bool FULL, bool AXES>
-__global__ void __launch_bounds__(kWrThreads, 4) k_paged_write8(const __grid_constant__ WiPagedWrite A,
+__global__ void __launch_bounds__(kWrThreads, 6) k_paged_write8(const __grid_constant__ WiPagedWrite A,
                                                                const WiPagedScales S, const __grid_constant__ WiRope R,
                                                                int Hq, int Hkv, int page, int n_slots, float eps, int parts,
                                                                const Append G, int* err) {
   __shared__ __align__(16) unsigned char rows[kWrThreads / 32][kWrStages * kWrBatch];
-  static_assert(sizeof(rows) >= kGroup * (WI_D / 2) * sizeof(float2), "the cosines and sines of a run");
+  __shared__ uint32_t tops[2][kWrThreads / 32];
+  static_assert(sizeof(rows) >= sizeof(Turns), "the cosines and sines of a run");
   pdl_trigger();
   pdl_wait();
   if ((int)blockIdx.x < G.ctas) {
-    append_rows<INTER>(A, S, R, Hkv, page, n_slots, eps, G, reinterpret_cast<float2(*)[WI_D / 2]>(rows), err);
+    const int which = blockIdx.x % (2 * G.parts);  // a tile's CTAs of keys, then of values
+    Turns& turns = *reinterpret_cast<Turns*>(rows);
+    if (which < G.parts)
+      append_rows<INTER, true>(A, S.k, R, Hkv, page, n_slots, eps, G, which, turns, tops, err);
+    else
+      append_rows<false, false>(A, S.v, R, Hkv, page, n_slots, eps, G, which - G.parts, turns, tops, err);
   } else {
     WiPagedWrite Q = A;  // no keys and values, so no slots either
     Q.slots = nullptr;
@@ -302,9 +360,13 @@ cudaError_t wi_launch_paged_write8(const WiPagedGeom& g, const WiPagedWrite& w, 
                                    cudaStream_t st) {
   constexpr int kWarps = kWrThreads / 32;
   Append G;
-  G.parts = (g.Hkv + kWarps - 1) / kWarps;
-  // tiles of one token where that gives no more CTAs than the machine holds at once
-  G.tile = 2LL * w.n_tokens * G.parts > 4LL * sms ? kApTile : 1;
+  // a CTA per token and two heads where the machine holds them all at once, else per sixteen tokens and four heads
+  G.parts = (g.Hkv + kApHeads - 1) / kApHeads;
+  G.tile = 1;
+  if (2LL * w.n_tokens * G.parts > 6LL * sms) {
+    G.parts = (G.parts + 1) / 2;
+    G.tile = kApTile;
+  }
   const long long ctas = 2LL * G.parts * ((w.n_tokens + G.tile - 1) / G.tile);
   const int batches = (g.Hq + 7) / 8;
   long long parts = ((long long)kWrPerSm * sms + w.n_tokens - 1) / w.n_tokens;  // as in the bf16 write
