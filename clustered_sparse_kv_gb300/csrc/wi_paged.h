@@ -102,7 +102,7 @@ struct WiPagedGather {
   long long pos0, n;
 };
 cudaError_t wi_launch_paged_gather(const WiPagedGeom& g, const WiPagedGather& a, int* err, cudaStream_t st);
-cudaError_t wi_launch_paged_gather8(const WiPagedGeom& g, const WiPagedGather& a, const WiPagedScales& s, int* err,
+cudaError_t wi_launch_paged_gather8(const WiPagedGeom& g, const WiPagedGather& a, const WiPagedScales& s, int sms, int* err,
                                     cudaStream_t st);
 
 struct WiPagedAttn {

@@ -71,6 +71,11 @@ __device__ __forceinline__ void append_rows(const WiPagedWrite& A, unsigned char
     wa[0] = unpack2(x.x), wa[1] = unpack2(x.y), wb[0] = unpack2(y.x), wb[1] = unpack2(y.y);
   }
   const long long step = KEY ? A.k_stride : A.v_stride;
+  // A thread works out the angles of one pair (the table of them is in constant memory, where 32 addresses take 32 turns: read
+  // per angle, it made the keys four fifths of the kernel).
+  const int p = tid % (WI_D / 2);
+  const unsigned long long one_turn = KEY && p < half ? R.turn[p] : 0;
+  const int32_t* const at_axis = A.positions + (KEY && p < half ? (long long)R.axis[p] * A.n_tokens : 0);
   int turn = 0;  // of the exchange between two warps
   for (; starts; starts &= starts - 1) {
     const int at = __ffs(starts) - 1;
@@ -102,11 +107,10 @@ __device__ __forceinline__ void append_rows(const WiPagedWrite& A, unsigned char
     fetch(h0 + (warp >> 1));
     if (KEY && half) {
       if (turn) __syncthreads();  // the last run's are read
-      for (int i = tid; i < len * half; i += kWrThreads) {
-        const int r = i / half, p = i - r * half;
-        const int pos = A.positions[(long long)R.axis[p] * A.n_tokens + t + r];
+      for (int r = tid / (WI_D / 2); p < half && r < len; r += kWrThreads / (WI_D / 2)) {
+        const int pos = at_axis[t + r];
         // the product's low 64 bits are the fraction of a turn, as in the bf16 write
-        const long long a = (long long)(R.turn[p] * (unsigned long long)pos);
+        const long long a = (long long)(one_turn * (unsigned long long)pos);
         float c, s;
         sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &s, &c);
         turns.c[r][p] = c * R.scale;
@@ -269,10 +273,13 @@ __global__ void __launch_bounds__(kWrThreads, 6) k_paged_write8(const __grid_con
 
 // ------------------------------------------------------------------- gather
 //
-// Eight lanes move one row: sixteen values each, to thirty-two bytes of bf16.
-constexpr int kGaThreads = 256;
-constexpr int kGaRows = 4;
-constexpr int kGaStep = kGaThreads / 8;
+// Sixteen lanes move one row, eight values each, so that what they store is whole sectors in a row (137 us with eight lanes
+// of sixteen values).
+constexpr int kGaThreads = 128;
+// Rows of a thread, where there are many (a 131K prompt of 8 kv heads 131.8 us with four, 128.1 with five, 164 with eight).
+constexpr int kGaMany = 5;
+constexpr int kGaLanes = 16;
+constexpr int kGaStep = kGaThreads / kGaLanes;
 
 __device__ __forceinline__ long long quot(long long a, int b) {
   return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
@@ -285,22 +292,23 @@ __device__ __forceinline__ uint2 widen(uint32_t w, float f) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
+template <int kGaRows>
 __global__ void __launch_bounds__(kGaThreads) k_paged_gather8(WiPagedGather A, WiPagedScales S, long long rows, int Hkv,
                                                              int page, int n_pages, int max_pages, int* err) {
   pdl_trigger();
   pdl_wait();
-  const int l = threadIdx.x & 7, most = max_pages * page, n = (int)A.n;
+  const int l = threadIdx.x % kGaLanes, most = max_pages * page, n = (int)A.n;
   const long long r0 = (long long)blockIdx.x * (kGaStep * kGaRows);
   const long long u0 = quot(r0, n);
-  const unsigned i0 = (unsigned)(r0 - u0 * n) + (threadIdx.x >> 3);
+  const unsigned i0 = (unsigned)(r0 - u0 * n) + (threadIdx.x / kGaLanes);
   long long cur = -1, pool = 0;  // the unit of the last row, and the pages in front of its layer's pool
   int b = 0, h = 0, len = 0, flags = 0;
-  uint4 kr[kGaRows], vr[kGaRows];
+  uint2 kr[kGaRows], vr[kGaRows];
   unsigned char ks[kGaRows], vs[kGaRows];
 #pragma unroll
   for (int k = 0; k < kGaRows; ++k) {
-    const long long r = r0 + (threadIdx.x >> 3) + k * kGaStep;
-    kr[k] = vr[k] = make_uint4(0u, 0u, 0u, 0u);
+    const long long r = r0 + (threadIdx.x / kGaLanes) + k * kGaStep;
+    kr[k] = vr[k] = make_uint2(0u, 0u);
     ks[k] = vs[k] = kScaleBias;
     if (r >= rows) continue;
     unsigned i = i0 + k * kGaStep;
@@ -328,9 +336,9 @@ __global__ void __launch_bounds__(kGaThreads) k_paged_gather8(WiPagedGather A, W
         flags |= WI_DEVERR_BAD_PAGE;
       } else {
         const long long head = (pool + pg) * Hkv + h;
-        const long long src = (head * page + (p - j * page)) * 8 + l;
-        kr[k] = __ldcg(static_cast<const uint4*>(A.k_pages) + src);
-        vr[k] = __ldcg(static_cast<const uint4*>(A.v_pages) + src);
+        const long long src = (head * page + (p - j * page)) * kGaLanes + l;
+        kr[k] = __ldcg(static_cast<const uint2*>(A.k_pages) + src);
+        vr[k] = __ldcg(static_cast<const uint2*>(A.v_pages) + src);
         const long long group = head * (page / kGroup) + (p - j * page) / kGroup;
         ks[k] = S.k[group];
         vs[k] = S.v[group];
@@ -339,16 +347,14 @@ __global__ void __launch_bounds__(kGaThreads) k_paged_gather8(WiPagedGather A, W
   }
 #pragma unroll
   for (int k = 0; k < kGaRows; ++k) {
-    const long long r = r0 + (threadIdx.x >> 3) + k * kGaStep;
+    const long long r = r0 + (threadIdx.x / kGaLanes) + k * kGaStep;
     if (r >= rows) continue;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const uint4 x = c ? vr[k] : kr[k];
+      const uint2 x = c ? vr[k] : kr[k];
       const float f = pow2(scale_exponent(c ? vs[k] : ks[k]));
-      const uint2 y0 = widen(x.x, f), y1 = widen(x.y, f), y2 = widen(x.z, f), y3 = widen(x.w, f);
-      uint4* const to = static_cast<uint4*>(c ? A.v_out : A.k_out) + r * 16 + 2 * l;
-      to[0] = make_uint4(y0.x, y0.y, y1.x, y1.y);
-      to[1] = make_uint4(y2.x, y2.y, y3.x, y3.y);
+      const uint2 y0 = widen(x.x, f), y1 = widen(x.y, f);
+      static_cast<uint4*>(c ? A.v_out : A.k_out)[r * kGaLanes + l] = make_uint4(y0.x, y0.y, y1.x, y1.y);
     }
   }
   if (flags && l == 0) atomicOr(err, flags);
@@ -360,11 +366,12 @@ cudaError_t wi_launch_paged_write8(const WiPagedGeom& g, const WiPagedWrite& w, 
                                    cudaStream_t st) {
   constexpr int kWarps = kWrThreads / 32;
   Append G;
-  // a CTA per token and two heads where the machine holds them all at once, else per sixteen tokens and four heads
+  // a CTA per token and two heads where the machine holds them all at once, else per sixteen tokens and eight heads (8192
+  // tokens of 8 kv heads 32.8 us; with two and four heads to a CTA, each with the angles to work out, 39.5 and 35.2)
   G.parts = (g.Hkv + kApHeads - 1) / kApHeads;
   G.tile = 1;
   if (2LL * w.n_tokens * G.parts > 6LL * sms) {
-    G.parts = (G.parts + 1) / 2;
+    G.parts = (g.Hkv + 7) / 8;
     G.tile = kApTile;
   }
   const long long ctas = 2LL * G.parts * ((w.n_tokens + G.tile - 1) / G.tile);
@@ -383,11 +390,13 @@ cudaError_t wi_launch_paged_write8(const WiPagedGeom& g, const WiPagedWrite& w, 
                            g.n_pages * g.page, g.eps, (int)parts, G, err);
 }
 
-cudaError_t wi_launch_paged_gather8(const WiPagedGeom& g, const WiPagedGather& a, const WiPagedScales& s, int* err,
+cudaError_t wi_launch_paged_gather8(const WiPagedGeom& g, const WiPagedGather& a, const WiPagedScales& s, int sms, int* err,
                                     cudaStream_t st) {
-  const int per = kGaStep * kGaRows;
-  const long long rows = (long long)a.batch * a.layers * g.Hkv * a.n, grid = (rows + per - 1) / per;
+  const long long rows = (long long)a.batch * a.layers * g.Hkv * a.n;
+  // a row to a thread where the machine holds them all at once, else four
+  const int each = rows <= 16LL * sms * kGaStep ? 1 : kGaMany, per = kGaStep * each;
+  const long long grid = (rows + per - 1) / per;
   if (grid > 2147483647LL) return cudaErrorInvalidConfiguration;
-  return wi_launch_chained(k_paged_gather8, dim3((unsigned)grid), kGaThreads, 0, st, a, s, rows, g.Hkv, g.page, g.n_pages,
-                           g.max_pages, err);
+  return wi_launch_chained(each == 1 ? k_paged_gather8<1> : k_paged_gather8<kGaMany>, dim3((unsigned)grid), kGaThreads, 0, st,
+                           a, s, rows, g.Hkv, g.page, g.n_pages, g.max_pages, err);
 }

@@ -401,7 +401,7 @@ static int gather_any(wi_paged* pc, int batch, int layers, const void* k_pages, 
   if (clash(outs, in)) return fail(WI_EINVAL, "k_out or v_out shares memory with an input or with the other");
   const WiPagedGather a = {k_pages, v_pages, block_table, kv_len, k_out, v_out, batch, layers, pos0, n};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (scales) return launched("gather8", wi_launch_paged_gather8(g, a, *scales, pc->err, st));
+  if (scales) return launched("gather8", wi_launch_paged_gather8(g, a, *scales, pc->sms, pc->err, st));
   return launched("gather", wi_launch_paged_gather(g, a, pc->err, st));
 }
 
