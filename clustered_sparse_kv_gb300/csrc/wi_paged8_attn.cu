@@ -65,13 +65,14 @@ using Walk = WalkOver<kLead, 2, LONG ? kLongest : 0>;
 struct Smem {
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], w_full[kWStages], w_empty[kWStages];
   uint64_t scale_full[kScaleSlots];
-  uint64_t q_full, s_full[2], p_ready[2], o_full[2], drained;
+  uint64_t q_raw, q_empty, q_full;  // the queries as they are have come; nobody reads their pieces any more; the pieces are there
+  uint64_t s_full[2], p_ready[2], o_full[2], drained;
   uint32_t tmem_base;
   int last;                 // this CTA merges the item that it just added to
   int poison[8];            // segment number + 1 of the last segment (modulo 8) with a NaN value
   long long scan[kThreads / 32];
   Run run;
-  Req reqs[kSoftWarps];     // of the softmax warps' segments
+  Req reqs[2][kSoftWarps];  // of the softmax warps' segments, this one's and the next one's in turn
   // of a block's groups: 2^e of the keys, e of the values, 2^-e of the values.  A slot is written again eight blocks on,
   // behind the scores of the block three before that, which come behind the weights of this one.
   struct Slot {
@@ -81,7 +82,7 @@ struct Smem {
   alignas(16) Slot scale[kScaleSlots];
   float q_scale[2][kRows];
   float xch[2][2][kRows];   // maximum and sum of a row, from chain to chain: [chain][m, l]
-  alignas(1024) unsigned char q[2][2][kBlockBytes];   // [tile][piece]
+  alignas(1024) unsigned char q[2][2][kBlockBytes];   // [tile][piece]; before that [tile][half of 64 columns] in bf16
   unsigned char k[kKStages][kBlockBytes];
   unsigned char v[kVStages][kBlockBytes];
   unsigned char w[kWStages][kWideBytes];
@@ -158,40 +159,41 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t tp, co
   tmem_st16_nowait(tp, p);
 }
 
-// A row's query as two e4m3 pieces, to row `row` of a tile's two; the factor of its scores.  A row of infinities or NaN gets
-// one that is no number, a row of no token pieces of zeros.
-__device__ __forceinline__ float put_query(const uint4* from, bool live, unsigned char* to, int row) {
+// A row of a tile's queries, from the bf16 in `tile` (as TMA brings them) to two e4m3 pieces in the same place, once all rows
+// are read (`barrier`: of the tile's 128 threads); the factor of its scores.  A row of infinities or NaN gets one that is no
+// number, a row of no token pieces of zeros.
+__device__ __forceinline__ float cut_query(unsigned char* tile, bool live, int row, int barrier) {
+  uint4 x[16];
   uint32_t top = 0;
-  if (live) {
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const uint4 x = __ldg(from + c);
-      top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-    }
-    top = max(top & 0xffffu, top >> 16);
+  for (int c = 0; c < 16; ++c) {
+    x[c] = *reinterpret_cast<const uint4*>(tile + (c >> 3) * kBlockBytes + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+    const uint32_t m = 0x7fff7fffu;
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[c].x & m, x[c].y & m), __vmaxu2(x[c].z & m, x[c].w & m)));
   }
+  asm volatile("bar.sync %0, 128;" ::"r"(barrier) : "memory");
+  top = max(top & 0xffffu, top >> 16);
   const bool good = live && top < 0x7f80u;
   // the row's largest element lies in [128, 256)
   const int e = min(max((int)(top >> 7) - 127 - 7, -126), 126);
-  const float f = pow2(-e);
-#pragma unroll 2
+  const float f = good ? pow2(-e) : 0.f;
+#pragma unroll
   for (int c = 0; c < 8; ++c) {
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint4 x = good ? __ldg(from + 2 * c + h) : make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      const uint32_t w[4] = {x[2 * c + h].x, x[2 * c + h].y, x[2 * c + h].z, x[2 * c + h].w};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const float y0 = bf16_lo(w[2 * k]) * f, y1 = bf16_hi(w[2 * k]) * f, y2 = bf16_lo(w[2 * k + 1]) * f,
                     y3 = bf16_hi(w[2 * k + 1]) * f;
         const uint32_t a = e4m3x2_of(y0, y1), b = e4m3x2_of(y2, y3);
         const float2 fa = e4m3x2_to_f32x2(a), fb = e4m3x2_to_f32x2(b);
-        hi[2 * h + k] = a | b << 16;
-        lo[2 * h + k] = e4m3x4_of(y0 - fa.x, y1 - fa.y, y2 - fb.x, y3 - fb.y);
+        hi[2 * h + k] = good ? a | b << 16 : 0u;
+        lo[2 * h + k] = good ? e4m3x4_of(y0 - fa.x, y1 - fa.y, y2 - fb.x, y3 - fb.y) : 0u;
       }
     }
-    unsigned char* const at = to + row * WI_D + ((c ^ (row & 7)) << 4);
+    unsigned char* const at = tile + row * WI_D + ((c ^ (row & 7)) << 4);
     *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(at + kBlockBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
@@ -248,7 +250,8 @@ struct Rows8 {
 };
 
 template <bool LONG>
-__global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_constant__ CUtensorMap map_k,
+__global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_constant__ CUtensorMap map_q,
+                                                                 const __grid_constant__ CUtensorMap map_k,
                                                                  const __grid_constant__ CUtensorMap map_v,
                                                                  const __grid_constant__ Rows8 A) {
   const Params& P = A.P;
@@ -274,6 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
       mbar_init(&sm.w_empty[s], 1);
     }
     for (int s = 0; s < kScaleSlots; ++s) mbar_init(&sm.scale_full[s], 1);
+    mbar_init(&sm.q_raw, 1);
+    mbar_init(&sm.q_empty, 1);
     mbar_init(&sm.q_full, kSoftWarps);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm.s_full[t], 1);
@@ -290,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (warp == kSoftWarps && lane == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
   }
@@ -325,41 +331,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
     // behind them, from the request as the warp keeps it in shared memory.
     Cursor cur;
     int nb, step, from, base, limit, whole, n0 = 0;  // n0: blocks of the segments before
-    float q_scale = 1.f;
-    auto begin = [&](Walk<LONG>& w) {
-      const bool more = w.next(P);
-      cur = w;
-      if (lane == 0) sm.reqs[warp] = w.r;
-      __syncwarp();
-      const int own_tile = w.single ? 0 : chain, ti = w.tile * w.tp + own_tile * P.tq + tok;
-      const bool live = more && tok < P.tq && ti < w.r.n;
-      limit = live ? (int)(w.p0 + ti) : -1;                        // the last position that the row sees
-      whole = (int)(w.p0 + w.tile * w.tp + own_tile * P.tq);       // ... that all rows of the tile see
-      nb = w.nb;
-      step = w.single ? 2 : 1;
-      from = w.single ? chain : 0;
-      base = w.b0 * kRows;
-      if (!more) return false;
-      // the tile's queries: the products that read the ones before are done (O is)
-      if (!w.single || chain == 0)
-        sm.q_scale[chain][row] = put_query(
-            reinterpret_cast<const uint4*>(static_cast<const bf16*>(P.a.q) +
-                                           ((long long)(w.r.s0 + ti) * P.Hq + w.kh * P.G + head) * WI_D),
-            live, sm.q[chain][0], row);
+    // The queries of segment `seg`, before the end of the one in front of it: its first scores are worked out meanwhile.
+    auto queries = [&](const Walk<LONG>& w, int seg) {
+      if (ok) ok = mbar_wait(&sm.q_raw, seg & 1, P.err);
+      if (!w.single || chain == 0) {
+        const int ti = w.tile * w.tp + chain * P.tq + tok;
+        sm.q_scale[chain][row] = cut_query(sm.q[chain][0], tok < P.tq && ti < w.r.n, row, 2 + chain);
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.q_full);
-      if (w.single) soft_barrier();  // both chains have the one tile
-      q_scale = sm.q_scale[own_tile][row];
-      return true;
     };
-    cur = sm.run.start;
-    if (lane == 0) sm.reqs[warp] = sm.run.req;
-    __syncwarp();
-    for (int seg = 0;; ++seg) {
+    bool more;
+    {
+      Walk<LONG> w(P, sm.run.start, sm.run.req);
+      more = w.next(P);
+      cur = w;
+      if (lane == 0) sm.reqs[0][warp] = w.r;
+      __syncwarp();
+      if (more) queries(w, 0);
+    }
+    for (int seg = 0; more; ++seg) {
+      float q_scale;
       {
-        Walk<LONG> w(P, cur, sm.reqs[warp]);
-        if (!begin(w)) break;
+        Walk<LONG> w(P, cur, sm.reqs[seg & 1][warp]);
+        w.next(P);
+        const int own_tile = w.single ? 0 : chain, ti = w.tile * w.tp + own_tile * P.tq + tok;
+        limit = tok < P.tq && ti < w.r.n ? (int)(w.p0 + ti) : -1;    // the last position that the row sees
+        whole = (int)(w.p0 + w.tile * w.tp + own_tile * P.tq);       // ... that all rows of the tile see
+        nb = w.nb;
+        step = w.single ? 2 : 1;
+        from = w.single ? chain : 0;
+        base = w.b0 * kRows;
+        if (w.single) soft_barrier();  // both chains have the one tile
+        q_scale = sm.q_scale[own_tile][row];
       }
       float m = -INFINITY, l = 0.f;  // the row's reference and its sum
       for (int j = from; j < nb; j += step) {
@@ -454,8 +459,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
       }
 
       // ---- the segment's end: maximum and sum over both chains where they had one tile, then O
-      Walk<LONG> w(P, cur, sm.reqs[warp]);
+      Walk<LONG> w(P, cur, sm.reqs[seg & 1][warp]);
       w.next(P);
+      {
+        Walk<LONG> next = w;
+        next.advance();
+        more = next.next(P);
+        cur = next;
+        if (lane == 0) sm.reqs[seg + 1 & 1][warp] = next.r;
+        __syncwarp();
+        if (w.single) soft_barrier();  // both chains have read their factors of the tile's queries
+        if (more) queries(next, seg + 1);
+      }
       const int own_tile = w.single ? 0 : chain, ti = w.tile * w.tp + own_tile * P.tq + tok;
       const bool live = tok < P.tq && ti < w.r.n;
       const bool both = !w.single || w.nb > 1;  // chain 1 had blocks
@@ -570,8 +585,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
       }
       if (w.single) soft_barrier();  // both chains' O, maxima and sums have been read
       n0 += w.nb;
-      w.advance();
-      cur = w;
     }
     if (tid == 0 && !split) P.splits[blockIdx.x].last = -1;
   } else if (warp == kSoftWarps) {
@@ -580,7 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
     const uint32_t on = elect_one();
     const int per = P.box / kGroup;  // groups of a box
     constexpr int kBatch = 32 / kGroups;
-    int nk = 0, nv = 0;  // blocks of keys and of values that were asked for
+    const uint32_t q_half = (uint32_t)(P.tq * P.G) * 128u;
+    int nk = 0, nv = 0, nq = 0;  // blocks of keys and of values, and queries that were asked for
     bool ok = true;
     for (; ok && w.next(P); w.advance()) {
       // The pages and scales of four blocks at a time, a lane to a group: pages are looked up two batches ahead and scales
@@ -619,6 +633,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
           tma_load_2d_warp(on, dst + (uint32_t)(i * P.box) * WI_D, map, 0, __shfl_sync(0xffffffffu, row, first + i * per), full);
         return true;
       };
+      // queries, once the scores of the segment before have read theirs
+      if (nq > 0) ok = mbar_wait(&sm.q_empty, (uint32_t)(nq - 1) & 1u, P.err);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        const int n = w.single ? 1 : 2;
+        mbar_arrive_expect_tx(&sm.q_raw, 2u * q_half * n);
+        for (int t = 0; t < n; ++t) {
+          const int tk = w.r.s0 + w.tile * w.tp + t * P.tq;
+          tma_load_3d(sm.q[t][0], &map_q, 0, w.kh * P.G, tk, &sm.q_raw);
+          tma_load_3d(sm.q[t][1], &map_q, 64, w.kh * P.G, tk, &sm.q_raw);
+        }
+      }
+      ++nq;
       const int ahead = w.single ? 2 : 1;
       // the batch that keys are asked for from (rows and scales), and the one that values are, which may lie behind it
       int page, row = 0, row_next, row_v = 0;
@@ -663,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
       }
     }
     // no copy is in flight when the CTA's shared memory goes (after a timed-out wait nobody may have waited for them)
+    if (nq > 0) mbar_wait(&sm.q_raw, (uint32_t)(nq - 1) & 1u, P.err);
     for (int s = 0; s < kKStages && s < nk; ++s) mbar_wait(&sm.k_full[s], (uint32_t)((nk - 1 - s) / kKStages) & 1u, P.err);
     for (int s = 0; s < kVStages && s < nv; ++s) mbar_wait(&sm.v_full[s], (uint32_t)((nv - 1 - s) / kVStages) & 1u, P.err);
   } else if (warp == kSoftWarps + 1) {
@@ -725,6 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
         scores(1, 1);
         keys_done();
       }
+      if (w.nb <= (w.single ? 2 : 1)) mma_commit_warp(on, &sm.q_empty);
       for (int j = 0; j < w.nb; ++j) {
         if (!(ok = all_wait(&sm.w_full[nw % kWStages], (uint32_t)(nw / kWStages) & 1u))) break;
         if (w.single) {
@@ -738,6 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
             if (!(ok = take_keys())) break;
             scores(t, 0);
             keys_done();
+            if (j + 3 >= w.nb) mma_commit_warp(on, &sm.q_empty);
           }
         } else {
           const bool more = j + 1 < w.nb;
@@ -755,6 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
           if (more) {
             scores(1, 1);
             keys_done();
+            if (j + 2 >= w.nb) mma_commit_warp(on, &sm.q_empty);
           } else {
             mma_commit_warp(on, &sm.o_full[1]);
           }
@@ -847,9 +881,11 @@ cudaError_t wi_launch_paged_attention8(const WiPagedGeom& g, const WiPagedAttn& 
   P.parts = {reinterpret_cast<float*>(static_cast<char*>(scratch) + kPagedTicketBytes + kSplitBytes),
              rows_here <= kFewRows ? kFewRows : here ? kMergeHere : kRows, here ? 1 : 2};
   P.err = err;
-  CUtensorMap map_k, map_v;
+  CUtensorMap map_q, map_k, map_v;
   const unsigned long long rows = (unsigned long long)g.n_pages * g.Hkv * g.page;
-  if (!wi_encode_bytes_sw128(&map_k, a.k_pages, rows, (unsigned)P.box) ||
+  if (!wi_encode_heads_sw128(&map_q, a.q, (unsigned long long)a.n_tokens, (unsigned)g.Hq, (unsigned)g.G,
+                             (unsigned)P.tq) ||
+      !wi_encode_bytes_sw128(&map_k, a.k_pages, rows, (unsigned)P.box) ||
       !wi_encode_bytes_sw128(&map_v, a.v_pages, rows, (unsigned)P.box))
     return cudaErrorInvalidValue;
   static int smem_set[2][kWiSmemDevices] = {};
@@ -858,7 +894,7 @@ cudaError_t wi_launch_paged_attention8(const WiPagedGeom& g, const WiPagedAttn& 
   cudaError_t e = wi_ensure_smem(kernel, sizeof(Smem), smem_set[is_long]);
   if (e != cudaSuccess) return e;
   const int grid = sms < kPagedMaxSms ? sms : kPagedMaxSms;
-  if ((e = wi_launch_chained(kernel, dim3((unsigned)grid), kThreads, sizeof(Smem), st, map_k, map_v, A)) != cudaSuccess)
+  if ((e = wi_launch_chained(kernel, dim3((unsigned)grid), kThreads, sizeof(Smem), st, map_q, map_k, map_v, A)) != cudaSuccess)
     return e;
   if (here) return cudaSuccess;
   return wi_launch_chained(k_paged_merge, dim3((unsigned)grid, 2 * kRows / kMergeRows), kMergeThreads, 0, st, P);
