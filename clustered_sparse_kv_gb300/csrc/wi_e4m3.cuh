@@ -21,6 +21,11 @@ __device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
   asm("{\n\t.reg .b16 x;\n\tcvt.rn.satfinite.e4m3x2.f32 x, %2, %1;\n\tcvt.u32.u16 %0, x;\n\t}" : "=r"(w) : "f"(lo), "f"(hi));
   return w;
 }
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
+  uint32_t w;
+  asm("{\n\t.reg .b16 x;\n\tcvt.rn.satfinite.e4m3x2.f16x2 x, %1;\n\tcvt.u32.u16 %0, x;\n\t}" : "=r"(w) : "r"(h));
+  return w;
+}
 __device__ __forceinline__ uint32_t e4m3x4_of(float a, float b, float c, float d) {
   return e4m3x2_of(a, b) | e4m3x2_of(c, d) << 16;
 }

@@ -7,7 +7,7 @@
 //
 // S = Q K^T in e4m3: keys as they lie in the cache, queries as two e4m3 pieces, a
 // first one of four significant bits and the rest of four, which a bf16 query is
-// exactly (over the row's largest element; what is below 2^-18 of that may be
+// exactly (over the row's largest element; what is below 2^-17 of that may be
 // lost).  Two products of half the time each, so S costs what it does in bf16, and
 // no key is ever widened.  A column's scale is its group's: a score is
 // S 2^(e_row + e_group), one multiplier per sixteen columns.
@@ -159,45 +159,85 @@ __device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t tp, co
   tmem_st16_nowait(tp, p);
 }
 
-// A row of a tile's queries, from the bf16 in `tile` (as TMA brings them) to two e4m3 pieces in the same place, once all rows
-// are read (`barrier`: of the tile's 128 threads); the factor of its scores.  A row of infinities or NaN gets one that is no
-// number, a row of no token pieces of zeros.
-__device__ __forceinline__ float cut_query(unsigned char* tile, bool live, int row, int barrier) {
-  uint4 x[16];
-  uint32_t top = 0;
+// Sixteen elements of a query, in two words of e4m3 pieces each.  Through f16: scaled by the row's power of two, it holds a
+// bf16 element whole, down to 2^-24.
+__device__ __forceinline__ void cut16(const uint4& x, const uint4& y, float f, uint4* hi, uint4* lo) {
+  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  uint32_t h[4], r[4];
 #pragma unroll
-  for (int c = 0; c < 16; ++c) {
-    x[c] = *reinterpret_cast<const uint4*>(tile + (c >> 3) * kBlockBytes + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-    const uint32_t m = 0x7fff7fffu;
-    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[c].x & m, x[c].y & m), __vmaxu2(x[c].z & m, x[c].w & m)));
+  for (int k = 0; k < 4; ++k) {
+    uint32_t p[2], q[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t v = pack_f16(bf16_lo(w[2 * k + c]) * f, bf16_hi(w[2 * k + c]) * f);
+      p[c] = e4m3x2_of_f16x2(v);
+      const uint32_t back = e4m3x2_to_f16x2(p[c]);
+      const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&back));
+      q[c] = e4m3x2_of_f16x2(*reinterpret_cast<const uint32_t*>(&d));
+    }
+    h[k] = __byte_perm(p[0], p[1], 0x5410);
+    r[k] = __byte_perm(q[0], q[1], 0x5410);
   }
-  asm volatile("bar.sync %0, 128;" ::"r"(barrier) : "memory");
+  *hi = make_uint4(h[0], h[1], h[2], h[3]);
+  *lo = make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// A row of a tile's queries, from the bf16 in `tile` (as TMA brings them: two halves of 64 columns, rows of 128 bytes) to two
+// e4m3 pieces in the same place; a row's pieces lie where its own elements lay.  Returns the factor of its scores.  A row of
+// infinities or NaN gets one that is no number, a row of no token pieces of zeros.  Short loops: the code is cold when a
+// segment ends (unrolled it took 5300 cycles).
+__device__ __forceinline__ float cut_query(unsigned char* tile, bool live, int row) {
+  unsigned char* const first = tile + row * WI_D;
+  unsigned char* const second = first + kBlockBytes;
+  const int turn = (row & 7) << 4;
+  uint32_t top = 0;
+#pragma unroll 2
+  for (int c = 0; c < 8; ++c) {
+    const int at = (c << 4) ^ turn;  // (without the swizzle's turn, all rows from the same banks)
+    const uint4 x = *reinterpret_cast<const uint4*>(first + at), y = *reinterpret_cast<const uint4*>(second + at);
+    const uint32_t m = 0x7fff7fffu;
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m)));
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(y.x & m, y.y & m), __vmaxu2(y.z & m, y.w & m)));
+  }
   top = max(top & 0xffffu, top >> 16);
   const bool good = live && top < 0x7f80u;
   // the row's largest element lies in [128, 256)
   const int e = min(max((int)(top >> 7) - 127 - 7, -126), 126);
-  const float f = good ? pow2(-e) : 0.f;
+  const float f = pow2(-e);
+  uint4 rest[8];  // the second half, which the first half's pieces would run over
 #pragma unroll
+  for (int c = 0; c < 8; ++c) rest[c] = *reinterpret_cast<const uint4*>(second + ((c << 4) ^ turn));
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
   for (int c = 0; c < 8; ++c) {
-    uint32_t hi[4], lo[4];
+    uint4 x, y, hi, lo;
+    if (c < 4) {
+      x = *reinterpret_cast<const uint4*>(first + ((2 * c << 4) ^ turn));
+      y = *reinterpret_cast<const uint4*>(first + ((2 * c + 1 << 4) ^ turn));
+    } else {
+      x = rest[0];
+      y = rest[1];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t w[4] = {x[2 * c + h].x, x[2 * c + h].y, x[2 * c + h].z, x[2 * c + h].w};
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float y0 = bf16_lo(w[2 * k]) * f, y1 = bf16_hi(w[2 * k]) * f, y2 = bf16_lo(w[2 * k + 1]) * f,
-                    y3 = bf16_hi(w[2 * k + 1]) * f;
-        const uint32_t a = e4m3x2_of(y0, y1), b = e4m3x2_of(y2, y3);
-        const float2 fa = e4m3x2_to_f32x2(a), fb = e4m3x2_to_f32x2(b);
-        hi[2 * h + k] = good ? a | b << 16 : 0u;
-        lo[2 * h + k] = good ? e4m3x4_of(y0 - fa.x, y1 - fa.y, y2 - fb.x, y3 - fb.y) : 0u;
-      }
+      for (int k = 0; k < 6; ++k) rest[k] = rest[k + 2];
     }
-    unsigned char* const at = tile + row * WI_D + ((c ^ (row & 7)) << 4);
-    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(at + kBlockBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    cut16(x, y, f, &hi, &lo);
+    *reinterpret_cast<uint4*>(first + ((c << 4) ^ turn)) = good ? hi : none;
+    *reinterpret_cast<uint4*>(second + ((c << 4) ^ turn)) = good ? lo : none;
   }
   return !live ? 1.f : good ? pow2(e) * kScaleLog2 : __uint_as_float(0x7fc00000u);
+}
+
+// 32 bytes to global memory, by one instruction where they are a sector: a thread's row is not its neighbours', so that every
+// store instruction of a warp takes 32 turns.
+__device__ __forceinline__ void store32(void* to, const uint32_t (&x)[8]) {
+  if (reinterpret_cast<uintptr_t>(to) & 31) {
+    static_cast<uint4*>(to)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    static_cast<uint4*>(to)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
 }
 
 // The NaN values that a row sees at positions [from, to), where they were taken out, to 16 columns of its O.
@@ -336,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
       if (ok) ok = mbar_wait(&sm.q_raw, seg & 1, P.err);
       if (!w.single || chain == 0) {
         const int ti = w.tile * w.tp + chain * P.tq + tok;
-        sm.q_scale[chain][row] = cut_query(sm.q[chain][0], tok < P.tq && ti < w.r.n, row, 2 + chain);
+        sm.q_scale[chain][row] = cut_query(sm.q[chain][0], tok < P.tq && ti < w.r.n, row);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -536,12 +576,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
 #pragma unroll
             for (int i = 0; i < 16; ++i) __stcg(dst + P.parts.o(own_tile, c + i, row), o[i]);
           } else {
-            uint4* q = reinterpret_cast<uint4*>(static_cast<bf16*>(P.a.out) + at * WI_D + c);
+            uint32_t x[8];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-              q[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                                pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+            for (int i = 0; i < 8; ++i) x[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
+            store32(static_cast<bf16*>(P.a.out) + at * WI_D + c, x);
           }
         }
       }

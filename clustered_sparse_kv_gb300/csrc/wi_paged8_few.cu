@@ -8,7 +8,7 @@
 // both in e4m3, which keys and values are held in.  Queries and weights are
 // not, and are sums of e4m3 pieces.  A bf16 query is a first piece of four
 // significant bits and a rest of four, exactly (over the row's largest element;
-// what is below 2^-18 of that may be lost), so Q has two columns per row and S
+// what is below 2^-17 of that may be lost), so Q has two columns per row and S
 // is added up.  A weight has four pieces with a column, and so a sum in tensor
 // memory, each: columns cost next to nothing here, and each piece has its own
 // power of two, so that together they hold twelve bits of a weight down to 2^-9

@@ -5,9 +5,10 @@ terms of a rotated pair).  A value in 8 bits is off by at most half a step, 2^-4
 that is more; keys also by 2^-19 of |a| + |b| in front of the rounding.  Values (not rotated), copies and scales of values
 are equal; a key's scale is that of its group's largest key, known to 2^-18.
 Attention, on the pools' own bytes: a bf16 output is off by at most 2^-8 of itself; its weights by 2^-10, that is 2^-10 of
-sum w|v|; a score is an fp32 dot of 128 products of the key with a query of which 2^-18 of its largest element may be
-missing: off by 128 * 2^-24 of |q||k| / sqrt(128) and 2^-18 of max|q| |k|, and its weight by as much, once itself and once
-through the sum; weights below 2^-27 of the row's largest may be missing, and the sums over n positions are fp32: n * 2^-24.
+sum w|v|; a score is an fp32 dot of 128 products of the key with a query whose elements are known to 2^-17 of its largest
+(two e4m3 pieces, the largest element scaled to 2^7 .. 2^8: half the smallest step, 2^-10, over 2^7): off by 128 * 2^-24 of
+|q||k| / sqrt(128) and by sqrt(128) 2^-17 max|q| |k| / sqrt(128), and its weight by as much, once itself and once through the
+sum; weights below 2^-27 of the row's largest may be missing, and the sums over n positions are fp32: n * 2^-24.
 lse: the score's error, and n * 2^-24 of the sum.
 """
 import numpy as np
@@ -314,7 +315,7 @@ def compare(got, gl, Q, K, V, table, q_start, kv):
     held = [paged.rows_of(K, table[b], h, int(n)) for b, n in enumerate(kv) for h in range(K.shape[1])]
     kmax = max([np.linalg.norm(np.where(np.isfinite(x), x, 0), axis=-1).max(initial=0.0) for x in held])
     qn, qm = np.linalg.norm(Q[live], axis=-1), np.abs(Q[live]).max(-1, initial=0.0)
-    ds = 128 * 2.0 ** -24 * qn * kmax / np.sqrt(128) + 2.0 ** -18 * qm * kmax + 2.0 ** -20
+    ds = 128 * 2.0 ** -24 * qn * kmax / np.sqrt(128) + 2.0 ** -17 * qm * kmax + 2.0 ** -20
     most = max([1, *kv])
     tol = (2.0 ** -8 * np.abs(ref[live]) +
            (1 + 2.0 ** -7) * spread[live] * (2.0 ** -10 + 2 * ds + 2 * most * 2.0 ** -24)[..., None] + 2.0 ** -80)
