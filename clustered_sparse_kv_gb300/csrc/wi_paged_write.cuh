@@ -62,6 +62,18 @@ __device__ __forceinline__ uint64_t swap2(uint64_t x) {
   return pair2(v.y, v.x);
 }
 
+// A launch parameter by its generic address: as constant memory, which the compiler would read it as, it takes a turn for
+// each of a warp's 32 addresses.
+__device__ __forceinline__ void load_turns(const unsigned long long* p, unsigned long long (&x)[2]) {
+  asm("ld.u64 %0, [%1];" : "=l"(x[0]) : "l"(p));
+  asm("ld.u64 %0, [%1];" : "=l"(x[1]) : "l"(p + 1));
+}
+__device__ __forceinline__ unsigned load_axes(const unsigned char* p) {
+  unsigned short x;
+  asm("ld.u16 %0, [%1];" : "=h"(x) : "l"(p));
+  return x;
+}
+
 // INTER: pairs (2i, 2i + 1).  FULL: the whole head is rotated (no lane holds elements that are only scaled).  AXES: a
 // pair's position is that of its axis; a lane asks for those of its two pairs beside the token's first.
 // A warp's unit of work: `parts` units per token, each with every parts-th batch; `mine`: its kWrStages batches of shared
@@ -100,9 +112,14 @@ __device__ __forceinline__ void write_rows(const WiPagedWrite& A, const WiRope& 
   for (int s = 0; s < kWrStages - 1; ++s) fetch(part + s * parts, s);
   const int pos = A.positions[t];
   int at[2] = {0, 0};
-  if (AXES && turned) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) at[i] = A.positions[(long long)R.axis[4 * l + 2 * row1 + i] * A.n_tokens + t];
+  unsigned long long turn[2] = {0ull, 0ull};  // of this lane's two pairs
+  if (turned) {
+    load_turns(&R.turn[4 * l + 2 * row1], turn);
+    if (AXES) {
+      const unsigned both = load_axes(&R.axis[4 * l + 2 * row1]);
+      at[0] = A.positions[(long long)(both & 0xffu) * A.n_tokens + t];
+      at[1] = A.positions[(long long)(both >> 8) * A.n_tokens + t];
+    }
   }
   int slot = A.slots ? A.slots[t] : t;
   if (pos < 0) {  // padding
@@ -123,7 +140,7 @@ __device__ __forceinline__ void write_rows(const WiPagedWrite& A, const WiRope& 
       for (int i = 0; i < 2; ++i) {
         // the product's low 64 bits are the fraction of a turn; signed, it is the angle in [-1/2, 1/2) turns, rounded to
         // fp32 here (by at most 2^-26 of a turn, next to half turns)
-        const long long a = (long long)(R.turn[4 * l + 2 * row1 + i] * (unsigned long long)(AXES ? at[i] : pos));
+        const long long a = (long long)(turn[i] * (unsigned long long)(AXES ? at[i] : pos));
         sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &s[i], &c[i]);  // 2^-31: half turns
         c[i] *= R.scale;
         s[i] *= R.scale;
