@@ -49,6 +49,7 @@ constexpr int kSoftWarps = 8;
 constexpr int kThreads = 32 * (kSoftWarps + 4);
 constexpr int kWideWarps = 2;
 constexpr int kGroups = kRows / kGroup;         // of a block
+constexpr int kHalf = kRows / 2;                // positions of a step: the first half's product runs while the second half's weights are worked out
 constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
 constexpr int kLead = 4;                        // units in front of an item's blocks, for what its start and end cost
 constexpr int kWhole = 4;                       // blocks up to which one request's items of few rows are not cut
@@ -66,7 +67,9 @@ struct Smem {
   uint64_t k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages], w_full[kWStages], w_empty[kWStages];
   uint64_t scale_full[kScaleSlots];
   uint64_t q_raw, q_empty, q_full;  // the queries as they are have come; nobody reads their pieces any more; the pieces are there
-  uint64_t s_full[2], p_ready[2], o_full[2], drained;
+  // Of a chain: a block's scores are there; the weights of half of it are; the first half's product is done.
+  uint64_t s_full[2], p_ready[2][2], pv_done[2];
+  uint64_t o_full[2], drained;
   uint32_t tmem_base;
   int last;                 // this CTA merges the item that it just added to
   int poison[8];            // segment number + 1 of the last segment (modulo 8) with a NaN value
@@ -322,7 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
     mbar_init(&sm.q_full, kSoftWarps);
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm.s_full[t], 1);
-      mbar_init(&sm.p_ready[t], kSoftWarps / 2);
+      for (int h = 0; h < 2; ++h) mbar_init(&sm.p_ready[t][h], kSoftWarps / 2);
+      mbar_init(&sm.pv_done[t], 1);
       mbar_init(&sm.o_full[t], 1);
     }
     mbar_init(&sm.drained, 1);
@@ -410,92 +414,83 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
       for (int j = from; j < nb; j += step) {
         const int slot = (n0 + j) % kScaleSlots;
         if (ok) ok = mbar_wait(&sm.scale_full[slot], ((n0 + j) / kScaleSlots) & 1, P.err);
-        Scales x8;
-        x8.load(sm.scale[slot], 0);
-        if (ok) ok = mbar_wait(&sm.s_full[chain], s_par, P.err);
-        s_par ^= 1;
-        tc_fence_after();
-        // The second half of the scores comes while the first is worked on; P then takes the place of the first half,
-        // which stays in registers, so that the block can be done again.
-        uint32_t a[2][32], b[2][32];
-        tmem_ld32_nowait(ts, a[0]);
-        tmem_ld32_nowait(ts + 32, a[1]);
-        tmem_wait_ld();
-        tmem_ld32_nowait(ts + 64, b[0]);
-        tmem_ld32_nowait(ts + 96, b[1]);
-        const bool masked = base + j * kRows + kRows - 1 > whole;
-        const int seen = limit - base - j * kRows;  // the row sees columns 0 .. seen of this block
-        // Weights of the four quarters; whether the row's reference is too small for them.  A row without a reference (every
-        // score so far minus infinity) looks for one in each block that it sees something of: against 0 its weights might all
-        // vanish.  A row that sees nothing of the block, or that no token owns, asks for nothing.
-        float zl;
-        auto all_weights = [&](bool mask_rest) -> bool {
-          const float ref = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 2^-inf = 0
-          const uint64_t ref2 = pair(-ref, -ref), q2 = pair(q_scale, q_scale);
-          float z = zl = 0.f;
-          Scales y8;
-          y8.load(sm.scale[slot], 2);
-          weights(a[0], ts, x8, q2, ref2, z, zl);
-          x8.load(sm.scale[slot], 4);
-          weights(a[1], ts + 16, y8, q2, ref2, z, zl);
-          y8.load(sm.scale[slot], 6);
-          tmem_wait_ld();
-          if (mask_rest) mask_scores(b, seen - 64);
-          weights(b[0], ts + 32, x8, q2, ref2, z, zl);
-          weights(b[1], ts + 48, y8, q2, ref2, z, zl);
-          return seen >= 0 && (!(z <= kAgain) || !(zl <= kFarMost) || m == -INFINITY);
-        };
-        // Most blocks are seen whole by every row and fit their references: their code stands on its own, without a jump (with
-        // the rest in the same loop, jumped over, a block took 1740 cycles here, 290 of them before its first weight).
-        const bool first = j == from;
-        bool grown = first, again = first;
-        if (__builtin_expect(!(masked || first), 1)) {
-          grown = all_weights(false);
-          again = __any_sync(0xffffffffu, grown);
-          if (!again) l += zl;
-        }
-        if (__builtin_expect(masked || again, 0)) {
-          if (masked) mask_scores(a, seen);
-          for (;;) {
-            if (again) {  // the first block, or the reference is far too small; grown: of this row (other rows keep theirs)
-              tmem_wait_st();
-              tmem_wait_ld();
-              tmem_ld32_nowait(ts + 64, b[0]);
-              tmem_ld32_nowait(ts + 96, b[1]);
-              tmem_wait_ld();
-              if (masked) mask_scores(b, seen - 64);
-              const float top =
-                  grown ? max3(m, top_of(a, sm.scale[slot], 0, q_scale), top_of(b, sm.scale[slot], 4, q_scale)) : m;
-              if (!first) {
-                // the chain's products so far are done: S of this block was issued behind them
-                const float f = m == top ? 1.f : ex2(m - top);
-                l *= f;
-                const uint32_t to = tmem + lanes + 256u + (uint32_t)chain * WI_D;
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
-                  uint32_t o[16];
-                  tmem_ld16_nowait(to + 16 * c, o);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                  tmem_st16_nowait(to + 16 * c, o);
-                }
-              }
-              m = top;
-            }
-            x8.load(sm.scale[slot], 0);
-            grown = all_weights(masked && !again);
-            if (again || !__any_sync(0xffffffffu, grown)) {
-              l += zl;
-              break;
-            }
-            again = true;
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t tsh = ts + (uint32_t)half * kHalf;
+          Scales x8, y8;
+          x8.load(sm.scale[slot], 4 * half);
+          if (ok && half == 0) ok = mbar_wait(&sm.s_full[chain], s_par, P.err);
+          tc_fence_after();
+          // P takes the place of the scores, which stay in registers, so that the half can be done again.
+          uint32_t a[2][32];
+          tmem_ld32_nowait(tsh, a[0]);
+          tmem_ld32_nowait(tsh + 32, a[1]);
+          tmem_wait_ld();
+          const int k0 = base + j * kRows + half * kHalf;
+          const bool masked = k0 + kHalf - 1 > whole;
+          const int seen = limit - k0;  // the row sees columns 0 .. seen of this half
+          // Weights of the two quarters; whether the row's reference is too small for them.  A row without a reference (every
+          // score so far minus infinity) looks for one in each half that it sees something of: against 0 its weights might
+          // all vanish.  A row that sees nothing of the half, or that no token owns, asks for nothing.
+          float zl;
+          auto all_weights = [&]() -> bool {
+            const float ref = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 2^-inf = 0
+            const uint64_t ref2 = pair(-ref, -ref), q2 = pair(q_scale, q_scale);
+            float z = zl = 0.f;
+            y8.load(sm.scale[slot], 4 * half + 2);
+            weights(a[0], tsh, x8, q2, ref2, z, zl);
+            weights(a[1], tsh + 16, y8, q2, ref2, z, zl);
+            return seen >= 0 && (!(z <= kAgain) || !(zl <= kFarMost) || m == -INFINITY);
+          };
+          // Most halves are seen whole by every row and fit their references: their code stands on its own, without a jump
+          // (with the rest in the same loop, jumped over, a block took 1740 cycles here, 290 of them before its first weight).
+          const bool first = j == from && half == 0;
+          bool grown = first, again = first;
+          if (__builtin_expect(!(masked || first), 1)) {
+            grown = all_weights();
+            again = __any_sync(0xffffffffu, grown);
+            if (!again) l += zl;
           }
+          if (__builtin_expect(masked || again, 0)) {
+            if (masked) mask_scores(a, seen);
+            for (;;) {
+              if (again) {  // the first half, or the reference is far too small; grown: of this row (other rows keep theirs)
+                tmem_wait_st();
+                const float top = grown ? fmaxf(m, top_of(a, sm.scale[slot], 4 * half, q_scale)) : m;
+                if (!first) {
+                  // once the chain's products so far are done (those of earlier blocks are: these scores came behind them)
+                  if (ok && half == 1) ok = mbar_wait(&sm.pv_done[chain], s_par, P.err);
+                  tc_fence_after();
+                  const float f = m == top ? 1.f : ex2(m - top);
+                  l *= f;
+                  const uint32_t to = tmem + lanes + 256u + (uint32_t)chain * WI_D;
+#pragma unroll 1
+                  for (int c = 0; c < 8; ++c) {
+                    uint32_t o[16];
+                    tmem_ld16_nowait(to + 16 * c, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    tmem_st16_nowait(to + 16 * c, o);
+                  }
+                }
+                m = top;
+              }
+              x8.load(sm.scale[slot], 4 * half);
+              grown = all_weights();
+              if (again || !__any_sync(0xffffffffu, grown)) {
+                l += zl;
+                break;
+              }
+              again = true;
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_ready[chain][half]);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_ready[chain]);
+        s_par ^= 1;
       }
 
       // ---- the segment's end: maximum and sum over both chains where they had one tile, then O
@@ -740,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
     const uint32_t on = elect_one();
     constexpr uint32_t idesc_s = make_idesc_e4m3(kRows, kRows);
     constexpr uint32_t idesc_o = make_idesc_f16(kRows, WI_D) | kIdescNMajorB;
-    int nk = 0, nw = 0;  // blocks of keys and of values taken
+    int nk = 0, nw = 0;  // blocks of keys and of values done with
     uint32_t p_par = 0;
     bool ok = true;
     auto all_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -751,6 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
       tc_fence_after();
       return true;
     };
+    // chain t's scores of a block, of the queries of tile q.  (In two products of 64 keys, the second behind the first half's
+    // weights, a block takes 3600 cycles: a product of 64 columns costs what one of 128 does.)
     auto scores = [&](int t, int q) {
       const uint32_t d = __shfl_sync(0xffffffffu, tmem + (uint32_t)t * kRows, 0);
       const uint32_t a0 = __shfl_sync(0xffffffffu, desc_lo_kmajor(smem_addr(sm.q[q][0])), 0);
@@ -762,73 +759,55 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
       mma_commit_warp(on, &sm.s_full[t]);
     };
     auto keys_done = [&] { mma_commit_warp(on, &sm.k_empty[nk % kKStages]); ++nk; };
-    auto values = [&](int t, bool add) {
-      const uint32_t p = __shfl_sync(0xffffffffu, tmem + (uint32_t)t * kRows, 0);
-      const uint32_t b0 = __shfl_sync(0xffffffffu, desc_lo_nmajor(smem_addr(sm.w[nw % kWStages]), 1024), 0);
+    // ... and the product of half of its weights, once they are there
+    auto values = [&](int t, int half, bool add) -> bool {
+      const uint32_t bit = (uint32_t)(t * 2 + half);
+      if (!all_wait(&sm.p_ready[t][half], (p_par >> bit) & 1u)) return false;
+      p_par ^= 1u << bit;
+      tc_fence_after();
+      const uint32_t p = __shfl_sync(0xffffffffu, tmem + (uint32_t)t * kRows + (uint32_t)half * kHalf, 0);
+      const uint32_t b0 = __shfl_sync(
+          0xffffffffu, desc_lo_nmajor(smem_addr(sm.w[nw % kWStages]) + (uint32_t)half * kHalf * WI_D * 2, 1024), 0);
       const uint32_t more = __shfl_sync(0xffffffffu, (uint32_t)add, 0);
       const uint32_t d = __shfl_sync(0xffffffffu, tmem + 256u + (uint32_t)t * WI_D, 0);
 #pragma unroll
-      for (int kk = 0; kk < kRows / 16; ++kk)
+      for (int kk = 0; kk < kHalf / 16; ++kk)
         mma_bf16_ta_warp(on, d, p + (uint32_t)kk * 8, b0 + (uint32_t)kk * (4096 / 16), desc_hi_sw128(2048), idesc_o,
                          kk > 0 ? 1u : more);
-    };
-    auto weights_ready = [&](int t) -> bool {
-      if (!all_wait(&sm.p_ready[t], (p_par >> t) & 1u)) return false;
-      p_par ^= 1u << t;
-      tc_fence_after();
+      if (half == 0) mma_commit_warp(on, &sm.pv_done[t]);
       return true;
     };
     for (int seg = 0; ok && w.next(P); ++seg, w.advance()) {
       if (!(ok = all_wait(&sm.q_full, seg & 1))) break;
       tc_fence_after();
       if (!(ok = take_keys())) break;
+      const int ahead = w.single ? 2 : 1;
       scores(0, 0);
-      if (w.single) {
-        keys_done();
-        if (w.nb > 1) {
-          if (!(ok = take_keys())) break;
-          scores(1, 0);
-          keys_done();
-        }
-      } else {
-        scores(1, 1);
+      if (!w.single) scores(1, 1);
+      keys_done();
+      if (w.single && w.nb > 1) {
+        if (!(ok = take_keys())) break;
+        scores(1, 0);
         keys_done();
       }
-      if (w.nb <= (w.single ? 2 : 1)) mma_commit_warp(on, &sm.q_empty);
-      for (int j = 0; j < w.nb; ++j) {
+      if (w.nb <= ahead) mma_commit_warp(on, &sm.q_empty);
+      for (int j = 0; ok && j < w.nb; ++j) {
         if (!(ok = all_wait(&sm.w_full[nw % kWStages], (uint32_t)(nw / kWStages) & 1u))) break;
-        if (w.single) {
-          const int t = j & 1;
-          if (!(ok = weights_ready(t))) break;
-          values(t, j >= 2);
-          mma_commit_warp(on, &sm.w_empty[nw % kWStages]);
-          if (j + 2 >= w.nb) {
+        const bool more = j + ahead < w.nb;
+        const int t0 = w.single ? j & 1 : 0, t1 = w.single ? t0 : 1;  // the chains that have the block
+#pragma unroll 1
+        for (int t = t0; t <= t1; ++t) {
+          if (!(ok = values(t, 0, j >= ahead) && values(t, 1, true))) break;
+          if (t == t1) mma_commit_warp(on, &sm.w_empty[nw % kWStages]);
+          if (!more) {
             mma_commit_warp(on, &sm.o_full[t]);
-          } else {
-            if (!(ok = take_keys())) break;
-            scores(t, 0);
-            keys_done();
-            if (j + 3 >= w.nb) mma_commit_warp(on, &sm.q_empty);
+            continue;
           }
-        } else {
-          const bool more = j + 1 < w.nb;
-          if (!(ok = weights_ready(0))) break;
-          values(0, j > 0);
-          if (more) {
-            if (!(ok = take_keys())) break;
-            scores(0, 0);
-          } else {
-            mma_commit_warp(on, &sm.o_full[0]);
-          }
-          if (!(ok = weights_ready(1))) break;
-          values(1, j > 0);
-          mma_commit_warp(on, &sm.w_empty[nw % kWStages]);
-          if (more) {
-            scores(1, 1);
+          if (t == t0 && !(ok = take_keys())) break;
+          scores(t, w.single ? 0 : t);
+          if (t == t1) {
             keys_done();
-            if (j + 2 >= w.nb) mma_commit_warp(on, &sm.q_empty);
-          } else {
-            mma_commit_warp(on, &sm.o_full[1]);
+            if (j + ahead + 1 >= w.nb) mma_commit_warp(on, &sm.q_empty);
           }
         }
         ++nw;
