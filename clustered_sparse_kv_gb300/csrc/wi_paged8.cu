@@ -276,10 +276,12 @@ __global__ void __launch_bounds__(kWrThreads, 6) k_paged_write8(const __grid_con
 // Sixteen lanes move one row, eight values each, so that what they store is whole sectors in a row (137 us with eight lanes
 // of sixteen values).
 constexpr int kGaThreads = 128;
-// Rows of a thread, where there are many (a 131K prompt of 8 kv heads 131.8 us with four, 128.1 with five, 164 with eight).
-constexpr int kGaMany = 5;
+// Rows of a thread, where there are many (a 131K prompt of 8 kv heads 126.2 us with four, 127.8, 129.7 and 130.2 with five, six
+// and eight); one where the machine holds them all at once (sixteen requests' rows 2.6 us, 4.4 with four).
+constexpr int kGaMany = 4;
 constexpr int kGaLanes = 16;
 constexpr int kGaStep = kGaThreads / kGaLanes;
+static_assert(kGaStep <= kGroup, "a step is less than a page");
 
 __device__ __forceinline__ long long quot(long long a, int b) {
   return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
@@ -302,21 +304,22 @@ __global__ void __launch_bounds__(kGaThreads) k_paged_gather8(WiPagedGather A, W
   const long long u0 = quot(r0, n);
   const unsigned i0 = (unsigned)(r0 - u0 * n) + (threadIdx.x / kGaLanes);
   long long cur = -1, pool = 0;  // the unit of the last row, and the pages in front of its layer's pool
-  int b = 0, h = 0, len = 0, flags = 0;
+  int b = 0, h = 0, len = 0, flags = 0, j = 0, off = 0;
+  unsigned i = i0;
+  long long u = u0;
   uint2 kr[kGaRows], vr[kGaRows];
   unsigned char ks[kGaRows], vs[kGaRows];
 #pragma unroll
-  for (int k = 0; k < kGaRows; ++k) {
+  for (int k = 0; k < kGaRows; ++k, i += kGaStep, off += kGaStep) {
     const long long r = r0 + (threadIdx.x / kGaLanes) + k * kGaStep;
     kr[k] = vr[k] = make_uint2(0u, 0u);
     ks[k] = vs[k] = kScaleBias;
     if (r >= rows) continue;
-    unsigned i = i0 + k * kGaStep;
-    long long u = u0;
     if (i >= (unsigned)n) {
       u += i / (unsigned)n;
       i %= (unsigned)n;
     }
+    const int p = (int)A.pos0 + (int)i;
     if (u != cur) {
       cur = u;
       const long long bl = quot(u, Hkv);
@@ -328,20 +331,23 @@ __global__ void __launch_bounds__(kGaThreads) k_paged_gather8(WiPagedGather A, W
         flags |= WI_DEVERR_BAD_LENGTH;
         len = 0;
       }
+      j = p / page;
+      off = p - j * page;
+    } else if (off >= page) {  // a step is less than a page
+      ++j;
+      off -= page;
     }
-    const int p = (int)A.pos0 + (int)i, j = p / page;
     const int pg = A.block_table[(long long)b * max_pages + j];  // on its way beside the length: j < max_pages always
     if (p < len) {
       if (pg < 0 || pg >= n_pages) {
         flags |= WI_DEVERR_BAD_PAGE;
       } else {
         const long long head = (pool + pg) * Hkv + h;
-        const long long src = (head * page + (p - j * page)) * kGaLanes + l;
-        kr[k] = __ldcg(static_cast<const uint2*>(A.k_pages) + src);
-        vr[k] = __ldcg(static_cast<const uint2*>(A.v_pages) + src);
-        const long long group = head * (page / kGroup) + (p - j * page) / kGroup;
-        ks[k] = S.k[group];
-        vs[k] = S.v[group];
+        const long long row = head * page + off;
+        kr[k] = __ldcg(static_cast<const uint2*>(A.k_pages) + row * kGaLanes + l);
+        vr[k] = __ldcg(static_cast<const uint2*>(A.v_pages) + row * kGaLanes + l);
+        ks[k] = S.k[row / kGroup];  // (a page is whole groups)
+        vs[k] = S.v[row / kGroup];
       }
     }
   }
