@@ -22,7 +22,12 @@ namespace {
 // tile of tokens, one after the other, with the rotation's cosines and sines of a
 // run's rows in shared memory for its heads of keys; the first head's rows are asked
 // for before those are worked out.
-constexpr int kApTile = 16;   // tokens of a tile, where there are many
+// 8192 tokens of 32 + 8 + 8 heads: 32.1 us, 5.8 TB/s; instruction issue (67% of the
+// slots while busy) and the start and end bound it, as the bf16 write.  The queries
+// alone take 26.3.  In a launch of their own behind the queries' the keys and values
+// made it 75.7 us; in the same one, a warp to a run's rows of a head 50.6, two warps
+// and packed arithmetic 40.5, angles a pair to a thread 32.7.
+constexpr int kApTile = 16;   // tokens of a tile, at most
 constexpr int kApHeads = 2;   // heads that a CTA has at once
 
 struct Append {
@@ -372,13 +377,18 @@ cudaError_t wi_launch_paged_write8(const WiPagedGeom& g, const WiPagedWrite& w, 
                                    cudaStream_t st) {
   constexpr int kWarps = kWrThreads / 32;
   Append G;
-  // a CTA per token and two heads where the machine holds them all at once, else per sixteen tokens and eight heads (8192
-  // tokens of 8 kv heads 32.8 us; with two and four heads to a CTA, each with the angles to work out, 39.5 and 35.2)
+  // A CTA takes a tile's runs one after the other, so a tile of single tokens costs as many times a run; a tile inside a chunk
+  // has one, whose angles its heads share.  Few tokens: a CTA per token and two heads, though most of them find that no run
+  // begins with theirs (256 single tokens of 8 kv heads 8.4 us, 18.3 by tiles of four; 584 of five requests 6.5 and 12.6, 500 of
+  // one 9.1 and 6.9).  As many as a call may have single ones: tiles of four, four heads (1000 single tokens 24.4 us, 127.6 by
+  // tiles of sixteen; twenty chunks of 100 12.1 and 19.8).  More: tiles of sixteen, eight heads (8192 tokens 31.9 us, 40.4 by
+  // tiles of four).
   G.parts = (g.Hkv + kApHeads - 1) / kApHeads;
   G.tile = 1;
-  if (2LL * w.n_tokens * G.parts > 6LL * sms) {
-    G.parts = (g.Hkv + 7) / 8;
-    G.tile = kApTile;
+  if (2LL * w.n_tokens * G.parts > 48LL * sms) {
+    const bool chunks = w.n_tokens > kPagedMaxBatch;
+    G.parts = chunks ? (g.Hkv + 7) / 8 : (g.Hkv + 3) / 4;
+    G.tile = chunks ? kApTile : 4;
   }
   const long long ctas = 2LL * G.parts * ((w.n_tokens + G.tile - 1) / G.tile);
   const int batches = (g.Hq + 7) / 8;

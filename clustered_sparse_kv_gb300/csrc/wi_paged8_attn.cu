@@ -25,6 +25,22 @@
 //   8         TMA: key and value blocks, box by box, and their groups' scales
 //   9         issues tcgen05.mma
 //   10-11     widen the values, and clean what not every row sees
+// A chain's weights of a block come in two halves of 64 positions, so that the
+// first half's product with the values runs while the second half's weights are
+// worked out; O then waits for half a product and the next scores.
+//
+// What bounds it, 32 query and 8 kv heads on one GB300: the chain of scores,
+// weights and product of either tile between two of its turns on the tensor
+// cores, which are active 57% of the time (2048 tokens behind 14K positions 403
+// us, 1270 TFLOP/s; behind 129K 3.1 - 3.2 ms; 8192 fresh tokens 467 us).  Of 3050
+// cycles a block takes, a chain spends 1600 on weights (2 x 670 where the other
+// chain does not want the special function units too) and 1400 waiting: 770 for the
+// tensor cores, the rest for barriers.  A segment's start and end cost 10000 cycles
+// (queries cut into pieces 4000 of them, outputs stored row by row 4500).
+// The way here, 2048 tokens behind 14K unless said: two warps widening a word at a
+// time 498 us, all loads in front of the stores 455; scales read ahead of the
+// scores 456 (behind 129K 3.41 ms, 3.74 before); blocks that need no mask and no new
+// reference in code of their own 424; queries by TMA, cut by a short loop 406.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

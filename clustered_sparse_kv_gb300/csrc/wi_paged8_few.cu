@@ -28,6 +28,16 @@
 // Two CTAs share an SM, so that one's start and end lie behind the other's
 // reads.  Runs of units, and parts that the last CTA of an item adds up, as in
 // the bf16 attention.
+//
+// What bounds it, 32 query and 8 kv heads on one GB300: HBM.  One token over 131K
+// positions in 54 us: 6 until the first scores (lengths, tables, first copies), 38
+// for 268 MB (7.1 TB/s), then the slowest CTA, and 5 for the parts; 64 single tokens
+// over 100 - 8000 positions 69 us, of which 50 are the reads.  A block of 128
+// positions costs a CTA 650 cycles of weights, and HBM gives two CTAs one every
+// 1400.  With one CTA to an SM 91 and 122 us (its stages do not matter); with pages
+// and scales looked up a block ahead, not four, 68 and 81; with three CTAs of two
+// stages 56 and 69; with a block's values asked for before the scales of the block in
+// front are stored, the short cases 0.6 us more.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -190,7 +200,7 @@ struct Queries {
 // out and lse of an item that was cut between CTAs, added up in CTA order: thread d has column d of every row.  An SM comes
 // here once a call, so the code is cold, and what counts is how little of it there is: the parts' columns come to shared
 // memory by a short loop of asynchronous copies, `room` parts at a time (38 parts 8.2 us with unrolled loads to registers,
-// 2.1 of which went by before the last load was issued).
+// 2.1 of which went by before the last load was issued; 4 so).
 constexpr int kJoin = 64;  // parts at a time, at most
 template <int RP>
 __device__ __noinline__ void join_parts(const Params& P, Smem<RP>& sm, const Split& sp, int c0, unsigned char* buf, int room) {

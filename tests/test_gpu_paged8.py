@@ -188,6 +188,14 @@ def test_write8_many_tokens(wi, ctx):
     write8_case(wi, [3000], [ctx], 2, 2, 32, seed=4, norm=False, rotary=64, hole=1232 - ctx)
 
 
+def test_write8_every_size_of_tile(wi):
+    """Single tokens and chunks by tiles of one, four and sixteen tokens (8 kv heads and 152 SMs: to 912, to 4096, above)."""
+    write8_case(wi, [1] * 300, list(range(300)), 8, 8, 16, seed=20)
+    write8_case(wi, [1] * 1000, [i % 50 for i in range(1000)], 8, 8, 16, seed=21)
+    write8_case(wi, [1] * 500 + [700, 3, 40] + [1] * 99, [i % 33 for i in range(602)], 8, 8, 16, seed=22, pad=3)
+    write8_case(wi, [1] * 400 + [3000, 17, 1000] + [2] * 99, [i % 33 for i in range(502)], 8, 8, 16, seed=23)
+
+
 @pytest.mark.parametrize("hole", [0, 15, 16, 31, 39])
 def test_write8_token_without_a_slot(wi, hole):
     """A token without a slot, the first or the last of its group: the rest of the group is written without it."""
