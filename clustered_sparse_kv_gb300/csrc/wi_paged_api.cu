@@ -287,8 +287,6 @@ static int write_any(wi_paged* pc, int n_tokens, const void* q, long long q_stri
   if (n_tokens > 1 && (q_stride < qw || k_stride < kw || v_stride < kw || q_stride % 8 || k_stride % 8 || v_stride % 8))
     return fail(WI_EINVAL, "token strides must be multiples of 8 and at least a token's heads");
   if (scales && (!slots || !scales->k || !scales->v)) return fail(WI_EINVAL, "slots, k_scales and v_scales must be non-NULL");
-  if (scales && (misaligned(scales->k, 16) || misaligned(scales->v, 16)))
-    return fail(WI_EINVAL, "the scales must be 16-byte aligned");
   const long long n1 = n_tokens - 1, kb = scales ? pool8_bytes(g) : slots ? pool_bytes(g) : 2 * kw * n_tokens;
   const long long sb = scales ? scale_bytes(g) : 0;
   const bool in_place = q_out == q && (n_tokens == 1 || q_stride == qw);
@@ -341,8 +339,6 @@ static int attention_any(wi_paged* pc, int batch, int n_tokens, const void* q, c
     return fail(WI_EINVAL, "the tables and lse must be 4-byte aligned");
   const WiPagedGeom& g = pc->g;
   if (scales && (!scales->k || !scales->v)) return fail(WI_EINVAL, "k_scales and v_scales must be non-NULL");
-  if (scales && (misaligned(scales->k, 16) || misaligned(scales->v, 16)))
-    return fail(WI_EINVAL, "the scales must be 16-byte aligned");
   const long long qb = 2LL * n_tokens * g.Hq * WI_D;
   const long long kb = scales ? pool8_bytes(g) : pool_bytes(g), sb = scales ? scale_bytes(g) : 0;
   const Span in[8] = {{q, qb}, {k_pages, kb}, {v_pages, kb}, {block_table, 4LL * batch * g.max_pages},
@@ -383,16 +379,15 @@ static int gather_any(wi_paged* pc, int batch, int layers, const void* k_pages, 
   if (pos0 < 0 || n < 0 || pos0 > most || n > most - pos0)
     return fail(WI_EINVAL, "positions [pos0, pos0 + n) must lie in [0, max_pages * page_size = %lld)", most);
   if (n == 0) return WI_OK;
-  if ((double)batch * layers * g.Hkv * (double)n >= 137438953472.0)  // 64 rows a block, 2^31 blocks
-    return fail(WI_EUNSUPPORTED, "batch * layers * n_kv_heads * n must be < 2^37");
+  const int rows_log2 = scales ? 36 : 37;  // 32 or 64 rows a block, 2^31 blocks
+  if ((double)batch * layers * g.Hkv * (double)n >= std::ldexp(1.0, rows_log2))
+    return fail(WI_EUNSUPPORTED, "batch * layers * n_kv_heads * n must be < 2^%d", rows_log2);
   if (!k_pages || !v_pages || !block_table || !kv_len || !k_out || !v_out)
     return fail(WI_EINVAL, "the pools, block_table, kv_len, k_out and v_out must be non-NULL");
   if (misaligned(k_pages, 16) || misaligned(v_pages, 16) || misaligned(k_out, 16) || misaligned(v_out, 16))
     return fail(WI_EINVAL, "the pools, k_out and v_out must be 16-byte aligned");
   if (misaligned(block_table, 4) || misaligned(kv_len, 4)) return fail(WI_EINVAL, "the tables must be 4-byte aligned");
   if (scales && (!scales->k || !scales->v)) return fail(WI_EINVAL, "k_scales and v_scales must be non-NULL");
-  if (scales && (misaligned(scales->k, 16) || misaligned(scales->v, 16)))
-    return fail(WI_EINVAL, "the scales must be 16-byte aligned");
   const long long ob = 2LL * batch * layers * g.Hkv * n * WI_D;
   const long long kb = layers * (scales ? pool8_bytes(g) : pool_bytes(g)), sb = scales ? layers * scale_bytes(g) : 0;
   const Span in[6] = {{k_pages, kb}, {v_pages, kb}, {block_table, 4LL * batch * g.max_pages}, {kv_len, 4LL * batch},

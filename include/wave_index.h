@@ -536,8 +536,8 @@ int wi_paged_gather(wi_paged* pc, int batch, int layers, const void* k_pages, co
  * exponent bits of bias 7, 3 mantissa bits; largest 448; all ones is NaN, there
  * is no infinity), k_scales and v_scales [n_pages][n_kv_heads][page_size / 16]
  * bytes, one for every group of sixteen positions of a head: byte x is the factor
- * 2^(x - 127) on the group's values.  Device, 16-byte aligned; tables, lengths and
- * slots are those of the bf16 pools.
+ * 2^(x - 127) on the group's values.  Device, the pools 16-byte aligned; tables,
+ * lengths and slots are those of the bf16 pools.
  *
  * wi_paged_write8 is wi_paged_write into such pools (slots are needed).  What a
  * slot gets is the fp32 key or value over its group's scale, rounded to the
