@@ -35,7 +35,10 @@
 // us, 1270 TFLOP/s; behind 129K 3.1 - 3.2 ms; 8192 fresh tokens 467 us).  Of 3050
 // cycles a block takes, a chain spends 1600 on weights (2 x 670 where the other
 // chain does not want the special function units too) and 1400 waiting: 770 for the
-// tensor cores, the rest for barriers.  A segment's start and end cost 10000 cycles
+// tensor cores, the rest for barriers.  Shared memory, at 128 bytes a cycle, is in
+// use for 2180 of them: operands 1540, copies and widening 640.  (The second half's
+// weights through it, to let the next scores in beside them: 420 us for 403.)
+// A segment's start and end cost 10000 cycles
 // (queries cut into pieces 4000 of them, outputs stored row by row 4500).
 // The way here, 2048 tokens behind 14K unless said: two warps widening a word at a
 // time 498 us, all loads in front of the stores 455; scales read ahead of the
