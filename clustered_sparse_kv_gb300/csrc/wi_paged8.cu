@@ -41,6 +41,103 @@ struct Turns {
   float c[kGroup][WI_D / 2], s[kGroup][WI_D / 2], n[kGroup][WI_D / 2];
 };
 
+// Eight elements of a row, as a lane holds them: the first and the second of its pairs (or eight that follow one another).
+struct Eight {
+  uint64_t a[2], b[2];
+  __device__ __forceinline__ void from(const uint2 (&raw)[2]) {
+    a[0] = unpack2(raw[0].x), a[1] = unpack2(raw[0].y), b[0] = unpack2(raw[1].x), b[1] = unpack2(raw[1].y);
+  }
+  __device__ __forceinline__ float squares() const {
+    const float2 ss = unpair(fma2(a[0], a[0], fma2(a[1], a[1], fma2(b[0], b[0], mul2(b[1], b[1])))));
+    return ss.x + ss.y;
+  }
+  __device__ __forceinline__ void norm(float inv, const Eight& w) {
+    const uint64_t f = pair2(inv, inv);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      a[c] = mul2(mul2(a[c], f), w.a[c]);
+      b[c] = mul2(mul2(b[c], f), w.b[c]);
+    }
+  }
+  template <bool INTER>
+  __device__ __forceinline__ void turn(const Turns& t, int r, int l) {
+    const float4 c4 = *reinterpret_cast<const float4*>(&t.c[r][4 * l]), s4 = *reinterpret_cast<const float4*>(&t.s[r][4 * l]);
+    const float4 n4 = *reinterpret_cast<const float4*>(&t.n[r][4 * l]);
+    if (INTER) {  // both words hold whole pairs
+      a[0] = fma2(a[0], pair2(c4.x, c4.x), mul2(swap2(a[0]), pair2(n4.x, s4.x)));
+      a[1] = fma2(a[1], pair2(c4.y, c4.y), mul2(swap2(a[1]), pair2(n4.y, s4.y)));
+      b[0] = fma2(b[0], pair2(c4.z, c4.z), mul2(swap2(b[0]), pair2(n4.z, s4.z)));
+      b[1] = fma2(b[1], pair2(c4.w, c4.w), mul2(swap2(b[1]), pair2(n4.w, s4.w)));
+    } else {
+      const uint64_t c2[2] = {pair2(c4.x, c4.y), pair2(c4.z, c4.w)}, s2[2] = {pair2(s4.x, s4.y), pair2(s4.z, s4.w)};
+      const uint64_t n2[2] = {pair2(n4.x, n4.y), pair2(n4.z, n4.w)};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint64_t x = a[c];
+        a[c] = fma2(x, c2[c], mul2(b[c], n2[c]));
+        b[c] = fma2(b[c], c2[c], mul2(x, s2[c]));
+      }
+    }
+  }
+  // The bits of the largest absolute value, or of the largest finite one.
+  __device__ __forceinline__ uint32_t largest(bool finite) const {
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float2 x = unpair(c < 2 ? a[c & 1] : b[c & 1]);
+      const uint32_t u = __float_as_uint(x.x) & 0x7fffffffu, v = __float_as_uint(x.y) & 0x7fffffffu;
+      top = max(top, finite && u >= 0x7f800000u ? 0u : u);
+      top = max(top, finite && v >= 0x7f800000u ? 0u : v);
+    }
+    return top;
+  }
+  // Times f as e4m3, to elements ea and eb of a row.
+  template <bool KEY>
+  __device__ __forceinline__ void store(unsigned char* row, int ea, int eb, float f) const {
+    const uint64_t f2 = pair2(f, f);
+    uint32_t y[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint64_t x0 = c ? b[0] : a[0], x1 = c ? b[1] : a[1];
+      const float2 y0 = unpair(fma2(x0, 0ull, mul2(x0, f2))), y1 = unpair(fma2(x1, 0ull, mul2(x1, f2)));  // an infinity becomes NaN
+      y[c] = e4m3x4_of(y0.x, y0.y, y1.x, y1.y);
+    }
+    if (KEY) {
+      *reinterpret_cast<uint32_t*>(row + ea) = y[0];
+      *reinterpret_cast<uint32_t*>(row + eb) = y[1];
+    } else {
+      *reinterpret_cast<uint2*>(row + ea) = make_uint2(y[0], y[1]);
+    }
+  }
+};
+
+// A lane's eight elements of a row of the input.
+template <bool KEY>
+__device__ __forceinline__ void load_eight(const bf16* row, int ea, int eb, uint2 (&raw)[2]) {
+  if (KEY) {
+    raw[0] = ldg_u2(row + ea);
+    raw[1] = ldg_u2(row + eb);
+  } else {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + ea));
+    raw[0] = make_uint2(x.x, x.y);
+    raw[1] = make_uint2(x.z, x.w);
+  }
+}
+
+// Eight values in the cache rounded again, to a scale that is 1 / f as large.
+__device__ __forceinline__ void round_again(unsigned char* at, float f) {
+  uint2* const p = reinterpret_cast<uint2*>(at);
+  const uint2 v = *p;
+  uint32_t n[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const uint32_t y = c ? v.y : v.x;
+    const float2 p0 = e4m3x2_to_f32x2(y & 0xffffu), p1 = e4m3x2_to_f32x2(y >> 16);
+    n[c] = e4m3x4_of(p0.x * f, p0.y * f, p1.x * f, p1.y * f);
+  }
+  *p = make_uint2(n[0], n[1]);
+}
+
 template <bool INTER, bool KEY>
 __device__ __forceinline__ void append_rows(const WiPagedWrite& A, unsigned char* const scales, const WiRope& R, int Hkv,
                                             int page, int n_slots, float eps, const Append& G, int which, Turns& turns,
@@ -70,10 +167,10 @@ __device__ __forceinline__ void append_rows(const WiPagedWrite& A, unsigned char
   const bool turned = KEY && (INTER ? 8 * l < R.rotary : 4 * l < half);
   const int ea = KEY && !INTER && turned ? 4 * l : 8 * l, eb = KEY && !INTER && turned ? 4 * l + half : 8 * l + 4;
   const bf16* const w = KEY ? static_cast<const bf16*>(A.k_weight) : nullptr;
-  uint64_t wa[2], wb[2];
+  Eight w8;
   if (KEY && w) {
-    const uint2 x = ldg_u2(w + ea), y = ldg_u2(w + eb);
-    wa[0] = unpack2(x.x), wa[1] = unpack2(x.y), wb[0] = unpack2(y.x), wb[1] = unpack2(y.y);
+    const uint2 x[2] = {ldg_u2(w + ea), ldg_u2(w + eb)};
+    w8.from(x);
   }
   const long long step = KEY ? A.k_stride : A.v_stride;
   // A thread works out the angles of one pair (the table of them is in constant memory, where 32 addresses take 32 turns: read
@@ -81,6 +178,70 @@ __device__ __forceinline__ void append_rows(const WiPagedWrite& A, unsigned char
   const int p = tid % (WI_D / 2);
   const unsigned long long one_turn = KEY && p < half ? R.turn[p] : 0;
   const int32_t* const at_axis = A.positions + (KEY && p < half ? (long long)R.axis[p] * A.n_tokens : 0);
+  // ... of row r, for token t
+  auto angle = [&](int r, long long t) {
+    const int pos = at_axis[t];
+    // the product's low 64 bits are the fraction of a turn, as in the bf16 write
+    const long long a = (long long)(one_turn * (unsigned long long)pos);
+    float c, s;
+    sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &s, &c);
+    turns.c[r][p] = c * R.scale;
+    turns.s[r][p] = s * R.scale;
+    turns.n[r][p] = -s * R.scale;
+  };
+  if (((starts << 1) & follow) == 0 && starts) {
+    // Single tokens, each a run of its own: sixteen lanes to a token's head, the tile's tokens at once.
+    if (KEY && half) {
+      for (int r = tid / (WI_D / 2); p < half && r < tile; r += kWrThreads / (WI_D / 2))
+        if (starts >> (r + 1) & 1) angle(r, t0 + r);
+      __syncthreads();
+    }
+    // the CTA's heads: kApHeads of every G.parts * kApHeads
+    const int sets = (Hkv - which * kApHeads + G.parts * kApHeads - 1) / (G.parts * kApHeads), jobs = tile * sets * kApHeads;
+    for (int j0 = 2 * warp; j0 < jobs; j0 += kWrThreads / 16) {
+      const int job = j0 + (lane >> 4), r = job % tile, hs = job / tile;
+      const int h = (hs / kApHeads * G.parts + which) * kApHeads + hs % kApHeads;
+      const int at = __shfl_sync(0xffffffffu, slot, r + 1), off = at % kGroup;
+      const bool live = job < jobs && h < Hkv && (starts >> (r + 1) & 1);
+      const int pg = at / page, row = at - pg * page;
+      const long long head = (long long)pg * Hkv + h;
+      unsigned char* const scale = scales + head * (page / kGroup) + row / kGroup;
+      uint2 raw[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
+      int held = -128;
+      if (live) {
+        load_eight<KEY>(static_cast<const bf16*>(KEY ? A.k : A.v) + (t0 + r) * step + h * WI_D, ea, eb, raw);
+        if (off > 0) held = scale_exponent(*scale);
+      }
+      Eight x;
+      x.from(raw);
+      if (KEY && w) {
+        float v = x.squares();
+#pragma unroll
+        for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        x.norm(rsqrtf(v * (1.f / WI_D) + eps), w8);
+      }
+      if (turned && live) x.template turn<INTER>(turns, r, l);
+      auto largest = [&](bool finite) -> uint32_t {
+        uint32_t top = x.largest(finite);
+#pragma unroll
+        for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        return top;
+      };
+      uint32_t top = largest(false);
+      if (__any_sync(0xffffffffu, top >= 0x7f800000u)) top = largest(true);
+      __syncwarp();  // all have the old scale
+      if (!live) continue;
+      const int e = max(scale_needed(top), held);
+      unsigned char* const to = static_cast<unsigned char*>(KEY ? A.k_out : A.v_out) + (head * page + row - off) * WI_D;
+      if (off > 0 && e > held) {
+        const float f = pow2(max(held - e, -30));
+        for (int i = 0; i < off; ++i) round_again(to + i * WI_D + 8 * l, f);
+      }
+      if (l == 0) *scale = (unsigned char)(e + kScaleBias);
+      x.template store<KEY>(to + off * WI_D, ea, eb, pow2(-e));
+    }
+    return;
+  }
   int turn = 0;  // of the exchange between two warps
   for (; starts; starts &= starts - 1) {
     const int at = __ffs(starts) - 1;
@@ -96,54 +257,28 @@ __device__ __forceinline__ void append_rows(const WiPagedWrite& A, unsigned char
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
         raw[k][0] = raw[k][1] = make_uint2(0u, 0u);
-        if (h < Hkv && 4 * k + row1 < len) {
-          if (KEY) {
-            raw[k][0] = ldg_u2(from + (4 * k + row1) * step + ea);
-            raw[k][1] = ldg_u2(from + (4 * k + row1) * step + eb);
-          } else {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(from + (4 * k + row1) * step + ea));
-            raw[k][0] = make_uint2(x.x, x.y);
-            raw[k][1] = make_uint2(x.z, x.w);
-          }
-        }
+        if (h < Hkv && 4 * k + row1 < len) load_eight<KEY>(from + (4 * k + row1) * step, ea, eb, raw[k]);
       }
       if (off > 0 && h < Hkv) was = scale_exponent(scales[((long long)pg * Hkv + h) * (page / kGroup) + row / kGroup]);
     };
     fetch(h0 + (warp >> 1));
     if (KEY && half) {
       if (turn) __syncthreads();  // the last run's are read
-      for (int r = tid / (WI_D / 2); p < half && r < len; r += kWrThreads / (WI_D / 2)) {
-        const int pos = at_axis[t + r];
-        // the product's low 64 bits are the fraction of a turn, as in the bf16 write
-        const long long a = (long long)(one_turn * (unsigned long long)pos);
-        float c, s;
-        sincospif((float)(int)(a >> 32) * 4.656612873077393e-10f, &s, &c);
-        turns.c[r][p] = c * R.scale;
-        turns.s[r][p] = s * R.scale;
-        turns.n[r][p] = -s * R.scale;
-      }
+      for (int r = tid / (WI_D / 2); p < half && r < len; r += kWrThreads / (WI_D / 2)) angle(r, t + r);
       __syncthreads();
     }
     for (int hp = h0; hp < Hkv; hp += G.parts * kApHeads, ++turn) {  // (the same turns for all warps)
       const int h = hp + (warp >> 1);
-      uint64_t a[kRows][2], b[kRows][2];
+      Eight x[kRows];
 #pragma unroll
-      for (int k = 0; k < kRows; ++k)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          a[k][c] = unpack2(c ? raw[k][0].y : raw[k][0].x);
-          b[k][c] = unpack2(c ? raw[k][1].y : raw[k][1].x);
-        }
+      for (int k = 0; k < kRows; ++k) x[k].from(raw[k]);
       const int held = was;  // exponent of the scale that the rows in front of the run have
       if (hp + G.parts * kApHeads < Hkv) fetch(h + G.parts * kApHeads);
       if (KEY && w) {
         // the four rows' sums of squares are reduced together, a quarter of the lanes ending with each
         float v[kRows];
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-          const float2 ss = unpair(fma2(a[k][0], a[k][0], fma2(a[k][1], a[k][1], fma2(b[k][0], b[k][0], mul2(b[k][1], b[k][1])))));
-          v[k] = ss.x + ss.y;
-        }
+        for (int k = 0; k < kRows; ++k) v[k] = x[k].squares();
         const bool up8 = l & 8, up4 = l & 4;
         float k0 = up8 ? v[2] : v[0], k1 = up8 ? v[3] : v[1];
         k0 += __shfl_xor_sync(0xffffffffu, up8 ? v[0] : v[2], 8);
@@ -153,51 +288,17 @@ __device__ __forceinline__ void append_rows(const WiPagedWrite& A, unsigned char
         r += __shfl_xor_sync(0xffffffffu, r, 1);
         r = rsqrtf(r * (1.f / WI_D) + eps);
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-          const float inv = __shfl_sync(0xffffffffu, r, (lane & 16) + 4 * k);
-          const uint64_t f = pair2(inv, inv);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            a[k][c] = mul2(mul2(a[k][c], f), wa[c]);
-            b[k][c] = mul2(mul2(b[k][c], f), wb[c]);
-          }
-        }
+        for (int k = 0; k < kRows; ++k) x[k].norm(__shfl_sync(0xffffffffu, r, (lane & 16) + 4 * k), w8);
       }
       if (turned) {
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-          const int r = 4 * k + row1;
-          if (r >= len) continue;
-          const float4 c4 = *reinterpret_cast<const float4*>(&turns.c[r][4 * l]), s4 = *reinterpret_cast<const float4*>(&turns.s[r][4 * l]);
-          const float4 n4 = *reinterpret_cast<const float4*>(&turns.n[r][4 * l]);
-          if (INTER) {  // both words hold whole pairs
-            a[k][0] = fma2(a[k][0], pair2(c4.x, c4.x), mul2(swap2(a[k][0]), pair2(n4.x, s4.x)));
-            a[k][1] = fma2(a[k][1], pair2(c4.y, c4.y), mul2(swap2(a[k][1]), pair2(n4.y, s4.y)));
-            b[k][0] = fma2(b[k][0], pair2(c4.z, c4.z), mul2(swap2(b[k][0]), pair2(n4.z, s4.z)));
-            b[k][1] = fma2(b[k][1], pair2(c4.w, c4.w), mul2(swap2(b[k][1]), pair2(n4.w, s4.w)));
-          } else {
-            const uint64_t c2[2] = {pair2(c4.x, c4.y), pair2(c4.z, c4.w)}, s2[2] = {pair2(s4.x, s4.y), pair2(s4.z, s4.w)};
-            const uint64_t n2[2] = {pair2(n4.x, n4.y), pair2(n4.z, n4.w)};
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint64_t x = a[k][c];
-              a[k][c] = fma2(x, c2[c], mul2(b[k][c], n2[c]));
-              b[k][c] = fma2(b[k][c], c2[c], mul2(x, s2[c]));
-            }
-          }
-        }
+        for (int k = 0; k < kRows; ++k)
+          if (4 * k + row1 < len) x[k].template turn<INTER>(turns, 4 * k + row1, l);
       }
       auto largest = [&](bool finite) -> uint32_t {
         uint32_t top = 0;
 #pragma unroll
-        for (int k = 0; k < kRows; ++k)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float2 x = unpair(c < 2 ? a[k][c & 1] : b[k][c & 1]);
-            const uint32_t u = __float_as_uint(x.x) & 0x7fffffffu, v = __float_as_uint(x.y) & 0x7fffffffu;
-            top = max(top, finite && u >= 0x7f800000u ? 0u : u);
-            top = max(top, finite && v >= 0x7f800000u ? 0u : v);
-          }
+        for (int k = 0; k < kRows; ++k) top = max(top, x[k].largest(finite));
         return __reduce_max_sync(0xffffffffu, top);
       };
       uint32_t top = largest(false);
@@ -210,41 +311,14 @@ __device__ __forceinline__ void append_rows(const WiPagedWrite& A, unsigned char
           static_cast<unsigned char*>(KEY ? A.k_out : A.v_out) + (((long long)pg * Hkv + h) * page + row - off) * WI_D;
       if (off > 0 && e > held) {  // the rows in front are rounded again
         const float f = pow2(max(held - e, -30));  // (2^-30 takes the largest value to nothing)
-        for (int r = row1; r < off; r += 4) {
-          uint2* p = reinterpret_cast<uint2*>(to + r * WI_D + 8 * l);
-          const uint2 v = *p;
-          uint32_t n[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint32_t y = c ? v.y : v.x;
-            const float2 p0 = e4m3x2_to_f32x2(y & 0xffffu), p1 = e4m3x2_to_f32x2(y >> 16);
-            n[c] = e4m3x4_of(p0.x * f, p0.y * f, p1.x * f, p1.y * f);
-          }
-          *p = make_uint2(n[0], n[1]);
-        }
+        for (int r = row1; r < off; r += 4) round_again(to + r * WI_D + 8 * l, f);
       }
       if (lane == 0 && !(warp & 1))
         scales[((long long)pg * Hkv + h) * (page / kGroup) + row / kGroup] = (unsigned char)(e + kScaleBias);
       const float f = pow2(-e);
-      const uint64_t f2 = pair2(f, f);
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        if (4 * k + row1 >= len) continue;
-        uint32_t y[2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint64_t x0 = c ? b[k][0] : a[k][0], x1 = c ? b[k][1] : a[k][1];
-          const float2 y0 = unpair(fma2(x0, 0ull, mul2(x0, f2))), y1 = unpair(fma2(x1, 0ull, mul2(x1, f2)));  // an infinity becomes NaN
-          y[c] = e4m3x4_of(y0.x, y0.y, y1.x, y1.y);
-        }
-        unsigned char* const d = to + (off + 4 * k + row1) * WI_D;
-        if (KEY) {
-          *reinterpret_cast<uint32_t*>(d + ea) = y[0];
-          *reinterpret_cast<uint32_t*>(d + eb) = y[1];
-        } else {
-          *reinterpret_cast<uint2*>(d + ea) = make_uint2(y[0], y[1]);
-        }
-      }
+      for (int k = 0; k < kRows; ++k)
+        if (4 * k + row1 < len) x[k].template store<KEY>(to + (off + 4 * k + row1) * WI_D, ea, eb, f);
     }
   }
 }
