@@ -1,6 +1,8 @@
 // wi_paged8.cu -- the paged cache in 8 bits: writes and gather.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "wi_common.cuh"
 #include "wi_e4m3.cuh"
 #include "wi_paged.h"
@@ -21,7 +23,9 @@ namespace {
 // rows in front of the run are rounded again.  A CTA takes the runs that begin in its
 // tile of tokens, one after the other, with the rotation's cosines and sines of a
 // run's rows in shared memory for its heads of keys; the first head's rows are asked
-// for before those are worked out.
+// for before those are worked out.  Runs of four tokens at most, as decoding gives,
+// go sixteen lanes to a run's rows of a head, the tile's at once (1000 single tokens
+// 8.2 us, 24.3 one run after the other).
 // 8192 tokens of 32 + 8 + 8 heads: 32.1 us, 5.8 TB/s; instruction issue (67% of the
 // slots while busy) and the start and end bound it, as the bf16 write.  The queries
 // alone take 26.3.  In a launch of their own behind the queries' the keys and values
@@ -29,6 +33,7 @@ namespace {
 // and packed arithmetic 40.5, angles a pair to a thread 32.7.
 constexpr int kApTile = 16;   // tokens of a tile, at most
 constexpr int kApHeads = 2;   // heads that a CTA has at once
+constexpr int kShort = 4;     // tokens of a short run, at most
 
 struct Append {
   int tile;          // tokens of a tile
@@ -36,9 +41,10 @@ struct Append {
   int parts;         // ... of a tile's keys, and as many of its values
 };
 
-// A run's rotation: cosine, sine and minus sine of a pair and row.
+// The rotation of a run, or of a tile's short ones: cosine, sine and minus sine of a pair and row.
 struct Turns {
-  float c[kGroup][WI_D / 2], s[kGroup][WI_D / 2], n[kGroup][WI_D / 2];
+  static constexpr int kRows = kApTile + kShort - 1;
+  float c[kRows][WI_D / 2], s[kRows][WI_D / 2], n[kRows][WI_D / 2];
 };
 
 // Eight elements of a row, as a lane holds them: the first and the second of its pairs (or eight that follow one another).
@@ -189,40 +195,54 @@ __device__ __forceinline__ void append_rows(const WiPagedWrite& A, unsigned char
     turns.s[r][p] = s * R.scale;
     turns.n[r][p] = -s * R.scale;
   };
-  if (((starts << 1) & follow) == 0 && starts) {
-    // Single tokens, each a run of its own: sixteen lanes to a token's head, the tile's tokens at once.
+  // Runs of N tokens at most: sixteen lanes to a run's rows of a head, the tile's runs at once.
+  auto short_runs = [&](auto longest) {
+    constexpr int N = decltype(longest)::value;
     if (KEY && half) {
-      for (int r = tid / (WI_D / 2); p < half && r < tile; r += kWrThreads / (WI_D / 2))
-        if (starts >> (r + 1) & 1) angle(r, t0 + r);
+      for (int r = tid / (WI_D / 2); p < half && r < tile + N - 1; r += kWrThreads / (WI_D / 2))
+        if ((N == 1 ? starts : starts | follow) >> (r + 1) & 1) angle(r, t0 + r);
       __syncthreads();
     }
     // the CTA's heads: kApHeads of every G.parts * kApHeads
-    const int sets = (Hkv - which * kApHeads + G.parts * kApHeads - 1) / (G.parts * kApHeads), jobs = tile * sets * kApHeads;
+    const int sets = (Hkv - which * kApHeads + G.parts * kApHeads - 1) / (G.parts * kApHeads);
+    const int runs = __popc(starts), jobs = runs * sets * kApHeads;
+    int nth = 0;  // lane i: where run i starts
+    uint32_t left = starts;
+    for (int i = 0; i < runs; ++i, left &= left - 1)
+      if (i == lane) nth = __ffs(left) - 1;
     for (int j0 = 2 * warp; j0 < jobs; j0 += kWrThreads / 16) {
-      const int job = j0 + (lane >> 4), r = job % tile, hs = job / tile;
+      const int job = j0 + (lane >> 4), hs = job / runs, r = __shfl_sync(0xffffffffu, nth, job - hs * runs) - 1;
       const int h = (hs / kApHeads * G.parts + which) * kApHeads + hs % kApHeads;
       const int at = __shfl_sync(0xffffffffu, slot, r + 1), off = at % kGroup;
-      const bool live = job < jobs && h < Hkv && (starts >> (r + 1) & 1);
+      const int len = job < jobs && h < Hkv ? (N == 1 ? 1 : __ffs(~(follow >> (r + 2)))) : 0;
       const int pg = at / page, row = at - pg * page;
       const long long head = (long long)pg * Hkv + h;
       unsigned char* const scale = scales + head * (page / kGroup) + row / kGroup;
-      uint2 raw[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
+      uint2 raw[N][2];
       int held = -128;
-      if (live) {
-        load_eight<KEY>(static_cast<const bf16*>(KEY ? A.k : A.v) + (t0 + r) * step + h * WI_D, ea, eb, raw);
-        if (off > 0) held = scale_exponent(*scale);
-      }
-      Eight x;
-      x.from(raw);
-      if (KEY && w) {
-        float v = x.squares();
+      const bf16* const from = static_cast<const bf16*>(KEY ? A.k : A.v) + (t0 + r) * step + h * WI_D;
 #pragma unroll
-        for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        x.norm(rsqrtf(v * (1.f / WI_D) + eps), w8);
+      for (int k = 0; k < N; ++k) {
+        raw[k][0] = raw[k][1] = make_uint2(0u, 0u);
+        if (k < len) load_eight<KEY>(from + k * step, ea, eb, raw[k]);
       }
-      if (turned && live) x.template turn<INTER>(turns, r, l);
+      if (len && off > 0) held = scale_exponent(*scale);
+      Eight x[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        x[k].from(raw[k]);
+        if (KEY && w) {
+          float v = x[k].squares();
+#pragma unroll
+          for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          x[k].norm(rsqrtf(v * (1.f / WI_D) + eps), w8);
+        }
+        if (turned && k < len) x[k].template turn<INTER>(turns, r + k, l);
+      }
       auto largest = [&](bool finite) -> uint32_t {
-        uint32_t top = x.largest(finite);
+        uint32_t top = x[0].largest(finite);
+#pragma unroll
+        for (int k = 1; k < N; ++k) top = max(top, x[k].largest(finite));
 #pragma unroll
         for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         return top;
@@ -230,7 +250,7 @@ __device__ __forceinline__ void append_rows(const WiPagedWrite& A, unsigned char
       uint32_t top = largest(false);
       if (__any_sync(0xffffffffu, top >= 0x7f800000u)) top = largest(true);
       __syncwarp();  // all have the old scale
-      if (!live) continue;
+      if (!len) continue;
       const int e = max(scale_needed(top), held);
       unsigned char* const to = static_cast<unsigned char*>(KEY ? A.k_out : A.v_out) + (head * page + row - off) * WI_D;
       if (off > 0 && e > held) {
@@ -238,10 +258,23 @@ __device__ __forceinline__ void append_rows(const WiPagedWrite& A, unsigned char
         for (int i = 0; i < off; ++i) round_again(to + i * WI_D + 8 * l, f);
       }
       if (l == 0) *scale = (unsigned char)(e + kScaleBias);
-      x.template store<KEY>(to + off * WI_D, ea, eb, pow2(-e));
+      const float f = pow2(-e);
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (k < len) x[k].template store<KEY>(to + (off + k) * WI_D, ea, eb, f);
     }
-    return;
+  };
+  const uint32_t longer = starts & follow >> 1 & follow >> 2 & follow >> 3 & follow >> 4;
+  static_assert(kShort == 4, "longer: of more tokens than that");
+  starts &= ~longer;
+  if (starts) {
+    if (!(starts & follow >> 1))
+      short_runs(std::integral_constant<int, 1>());
+    else
+      short_runs(std::integral_constant<int, kShort>());
+    if (longer) __syncthreads();  // the short runs' cosines and sines are read
   }
+  starts = longer;
   int turn = 0;  // of the exchange between two warps
   for (; starts; starts &= starts - 1) {
     const int at = __ffs(starts) - 1;
@@ -331,7 +364,7 @@ __global__ void __launch_bounds__(kWrThreads, 6) k_paged_write8(const __grid_con
                                                                const Append G, int* err) {
   __shared__ __align__(16) unsigned char rows[kWrThreads / 32][kWrStages * kWrBatch];
   __shared__ uint32_t tops[2][kWrThreads / 32];
-  static_assert(sizeof(rows) >= sizeof(Turns), "the cosines and sines of a run");
+  static_assert(sizeof(rows) >= sizeof(Turns) && kApTile >= kGroup, "the cosines and sines of a run");
   pdl_trigger();
   pdl_wait();
   if ((int)blockIdx.x < G.ctas) {
@@ -451,20 +484,29 @@ cudaError_t wi_launch_paged_write8(const WiPagedGeom& g, const WiPagedWrite& w, 
                                    cudaStream_t st) {
   constexpr int kWarps = kWrThreads / 32;
   Append G;
-  // A CTA takes a tile's runs one after the other, so a tile of single tokens costs as many times a run; a tile inside a chunk
-  // has one, whose angles its heads share.  Few tokens: a CTA per token and two heads, though most of them find that no run
-  // begins with theirs (256 single tokens of 8 kv heads 8.4 us, 18.3 by tiles of four; 584 of five requests 6.5 and 12.6, 500 of
-  // one 9.1 and 6.9).  As many as a call may have single ones: tiles of four, four heads (1000 single tokens 24.4 us, 127.6 by
-  // tiles of sixteen; twenty chunks of 100 12.1 and 19.8).  More: tiles of sixteen, eight heads (8192 tokens 31.9 us, 40.4 by
-  // tiles of four).
-  G.parts = (g.Hkv + kApHeads - 1) / kApHeads;
-  G.tile = 1;
-  if (2LL * w.n_tokens * G.parts > 48LL * sms) {
-    const bool chunks = w.n_tokens > kPagedMaxBatch;
-    G.parts = chunks ? (g.Hkv + 7) / 8 : (g.Hkv + 3) / 4;
-    G.tile = chunks ? kApTile : 4;
+  // A CTA takes a tile's long runs one after the other and its short ones at once, kApHeads heads after the other.  Small tiles
+  // of few heads spread few tokens over the machine; large ones share a run's angles between heads, and what is known of a tile
+  // between its runs.  8 kv heads: up to half an SM's tokens, one to a tile (16 single tokens 3.0 us, 3.8 by fours); fours while
+  // all CTAs run at once (256 single tokens 4.7, 5.9 by eights; 500 of one request 5.9, 7.2 by more fours); eights up to the
+  // tokens that a call may have of single ones (500 requests' four 10.7 us, 13.0 by fours, 12.7 by sixteens; 4000 single ones 23.5
+  // and 26.2), with four heads where two would not run at once (600 tokens of 200 requests 7.1 with two, 8.5 with four); sixteens
+  // of eight heads for chunks (8192 tokens 32.2 us, 40.8 by fours).
+  const int two = (g.Hkv + kApHeads - 1) / kApHeads;
+  auto ctas_of = [&](int tile, int parts) { return 2LL * parts * ((w.n_tokens + tile - 1) / tile); };
+  const long long at_once = 6LL * sms;
+  G.parts = two;
+  if (ctas_of(1, two) <= 4LL * sms) {
+    G.tile = 1;
+  } else if (ctas_of(4, two) <= at_once) {
+    G.tile = 4;
+  } else if (w.n_tokens <= kPagedMaxBatch) {
+    G.tile = 8;
+    if (ctas_of(8, two) > at_once) G.parts = (g.Hkv + 3) / 4;
+  } else {
+    G.tile = kApTile;
+    G.parts = (g.Hkv + 7) / 8;
   }
-  const long long ctas = 2LL * G.parts * ((w.n_tokens + G.tile - 1) / G.tile);
+  const long long ctas = ctas_of(G.tile, G.parts);
   const int batches = (g.Hq + 7) / 8;
   long long parts = ((long long)kWrPerSm * sms + w.n_tokens - 1) / w.n_tokens;  // as in the bf16 write
   if (parts > batches) parts = batches;

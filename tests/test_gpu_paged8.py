@@ -189,7 +189,7 @@ def test_write8_many_tokens(wi, ctx):
 
 
 def test_write8_every_size_of_tile(wi):
-    """Single tokens and chunks by tiles of one, four and sixteen tokens (8 kv heads and 152 SMs: to 912, to 4096, above)."""
+    """Single tokens and chunks, of few tokens to more than 4096, which tiles of several sizes take."""
     write8_case(wi, [1] * 300, list(range(300)), 8, 8, 16, seed=20)
     write8_case(wi, [1] * 1000, [i % 50 for i in range(1000)], 8, 8, 16, seed=21)
     write8_case(wi, [1] * 500 + [700, 3, 40] + [1] * 99, [i % 33 for i in range(602)], 8, 8, 16, seed=22, pad=3)

@@ -9,7 +9,7 @@ import torch
 
 from oracle import paged
 from test_gpu_paged import DEV, bf, f64, freqs, i32, lay_out
-from test_gpu_paged8 import compare, exps8, random_pool, upload, values8
+from test_gpu_paged8 import compare, exps8, random_pool, upload, values8, write8_case
 
 pytestmark = pytest.mark.gpu
 
@@ -109,6 +109,51 @@ def test_write8_with_queries_in_place(wi, n):
     assert pc.write8(q, k, v, i32(at), slots, *args, q_out=q) is q
     pc.check()
     assert torch.equal(q, want)
+    pc.free()
+
+
+@pytest.mark.parametrize("total,longest", [(40, 6), (330, 3), (330, 9), (1300, 7), (4700, 5), (4700, 40)])
+@pytest.mark.parametrize("hq,hkv", [(8, 8), (6, 3), (2, 1)])
+def test_write8_short_and_long_runs_together(wi, total, longest, hq, hkv):
+    """Runs of up to four tokens go another way than longer ones, also in one tile; a request's tokens may be cut anywhere by
+    their groups."""
+    rng = np.random.default_rng(total + longest)
+    new = []
+    while sum(new) < total:
+        new.append(int(rng.integers(1, longest + 1)))
+    axis = [i % 2 for i in range(32)] if hkv == 3 else None
+    write8_case(wi, new, rng.integers(0, 50, len(new)).tolist(), hq, hkv, 16 if hkv == 1 else 48, rotary=64 if hkv == 3 else 128,
+                interleaved=hkv == 1, norm=hkv != 1, axis=axis, seed=total, pad=2)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4])
+@pytest.mark.parametrize("off", [0, 1, 7, 11])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_write8_short_runs_are_the_longer_ones(wi, rows, off, interleaved):
+    """A short run's rows and scale are, bit for bit, those of the same run with rows of zeros behind it: infinities, NaN,
+    zeros and very different sizes among them, and rows in front that are rounded again."""
+    rng = np.random.default_rng(78)
+    hq, hkv, page, requests = 4, 4, 16, 12
+    long = 5 if off + 5 <= 16 else 16 - off
+    x, _ = bf(rng.normal(size=(requests, long, hq + 2 * hkv, 128)) * 2.0 ** rng.integers(-40, 40, (requests, 1, 1, 1)))
+    x[:, rows:] = 0
+    for b, odd in ((1, float("inf")), (2, -float("inf")), (3, float("nan")), (4, 0.0), (5, 2.0 ** -130), (6, 3e38)):
+        x[b, rng.integers(rows), hq:, rng.integers(128)] = odd
+    x[7] = float("nan")
+    pc = wi.PagedCache(wi.make_paged_config(hq, hkv, page, requests, requests, 1, inv_freq=freqs(128), interleaved=interleaved))
+    pools = [random_pool(rng, requests, hkv, page) for _ in range(2)]
+    got = []
+    for n in (rows, long):
+        (k, ks), (v, vs) = (upload(p) for p in pools)
+        at = (off + np.arange(n))[None].repeat(requests, 0)
+        slots = at + 16 * np.arange(requests)[:, None]
+        y = x[:, :n].reshape(-1, hq + 2 * hkv, 128).contiguous()
+        pc.write8(*split(y, hq, hkv), i32(at.reshape(-1)), i32(slots.reshape(-1)), k, v, ks, vs, q_weight=ones8(128),
+                  k_weight=ones8(128))
+        pc.check()
+        got.append([t.view(torch.uint8) for t in (k[:, :, :off + rows], v[:, :, :off + rows], ks, vs)])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
     pc.free()
 
 
