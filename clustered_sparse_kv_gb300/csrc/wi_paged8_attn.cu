@@ -31,8 +31,8 @@
 //
 // What bounds it, 32 query and 8 kv heads on one GB300: the chain of scores,
 // weights and product of either tile between two of its turns on the tensor
-// cores, which are active 57% of the time (2048 tokens behind 14K positions 403
-// us, 1270 TFLOP/s; behind 129K 3.1 - 3.2 ms; 8192 fresh tokens 467 us).  Of 3050
+// cores, which are active 57% of the time (2048 tokens behind 14K positions 396
+// us, 1290 TFLOP/s; behind 129K 3.1 - 3.2 ms; 8192 fresh tokens 462 us).  Of 3050
 // cycles a block takes, a chain spends 1600 on weights (2 x 670 where the other
 // chain does not want the special function units too) and 1400 waiting: 770 for the
 // tensor cores, the rest for barriers.  Shared memory, at 128 bytes a cycle, is in
@@ -43,7 +43,8 @@
 // The way here, 2048 tokens behind 14K unless said: two warps widening a word at a
 // time 498 us, all loads in front of the stores 455; scales read ahead of the
 // scores 456 (behind 129K 3.41 ms, 3.74 before); blocks that need no mask and no new
-// reference in code of their own 424; queries by TMA, cut by a short loop 406.
+// reference in code of their own 424; queries by TMA, cut by a short loop 406; what a
+// product needs made ready in front of the wait for its weights 396 (403).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -780,15 +781,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
     auto keys_done = [&] { mma_commit_warp(on, &sm.k_empty[nk % kKStages]); ++nk; };
     // ... and the product of half of its weights, once they are there
     auto values = [&](int t, int half, bool add) -> bool {
-      const uint32_t bit = (uint32_t)(t * 2 + half);
-      if (!all_wait(&sm.p_ready[t][half], (p_par >> bit) & 1u)) return false;
-      p_par ^= 1u << bit;
-      tc_fence_after();
       const uint32_t p = __shfl_sync(0xffffffffu, tmem + (uint32_t)t * kRows + (uint32_t)half * kHalf, 0);
       const uint32_t b0 = __shfl_sync(
           0xffffffffu, desc_lo_nmajor(smem_addr(sm.w[nw % kWStages]) + (uint32_t)half * kHalf * WI_D * 2, 1024), 0);
       const uint32_t more = __shfl_sync(0xffffffffu, (uint32_t)add, 0);
       const uint32_t d = __shfl_sync(0xffffffffu, tmem + 256u + (uint32_t)t * WI_D, 0);
+      const uint32_t bit = (uint32_t)(t * 2 + half);
+      if (!all_wait(&sm.p_ready[t][half], (p_par >> bit) & 1u)) return false;
+      p_par ^= 1u << bit;
+      tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < kHalf / 16; ++kk)
         mma_bf16_ta_warp(on, d, p + (uint32_t)kk * 8, b0 + (uint32_t)kk * (4096 / 16), desc_hi_sw128(2048), idesc_o,
