@@ -64,6 +64,9 @@ constexpr int kLead = 2;    // units in front of an item's blocks, for what its 
 // (one token over 300 positions 8.9 us whole, 11.6 cut; over 1000 13.6 whole, and cut 11.9, 12.3, 13.3 with runs of 1, 2, 4 at
 // least; over 8000 14.9, 14.5, 15.5).
 constexpr int kLeast = 2, kWhole = 4;
+// What the largest item may have above an equal run, where each item is a run (30 single tokens over 300 - 700 positions 14.6 us
+// whole, 21.1 cut; ten over 300 - 900 13.8 cut, 13.4 with eight, but sixteen over 2000 25.0 with sixteen, 23.6 cut).
+constexpr int kSlack = 4;
 // Blocks after which the tensor cores' sums are added up in fp32: their additions cut bits off.
 constexpr int kFlush = 1024;
 constexpr int kPieces = 4;
@@ -93,7 +96,7 @@ struct Smem {
   int last;                     // this CTA merges the item that it just added to
   int poison;                   // number + 1 of the last segment with a NaN value that not every row sees
   int mask[kSoftWarps];         // rows that take a new reference
-  long long scan[kThreads / 32];
+  long long scan[2 * (kThreads / 32)];
   Run run;
   alignas(8) unsigned char next[kSoftWarps][sizeof(WalkOver<kLead, 1, 0>)];  // a softmax warp's segment behind this one
   float q_scale[RP];
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention8_few(const __gr
   fence_proxy_async_smem();
   pdl_wait();
   tc_fence_before();
-  const bool any = find_run<kLead, 1, kThreads>(P, kLeast, kLead + kWhole, sm.scan, &sm.run);  // (with a barrier of all threads)
+  const bool any = find_run<kLead, 1, kThreads>(P, kLeast, kLead + kWhole, kSlack, sm.scan, &sm.run);  // (with a barrier of all threads)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;  // S at columns 0 and 16, O at 32
   if (!any) {  // the whole CTA leaves

@@ -189,11 +189,32 @@ struct Run {
   int ctas;              // CTAs with units
 };
 
+// The run that is item i of those of requests [b0, b1): all of it.  Called by one thread.
+template <int LEAD>
+__device__ __noinline__ void own_item(const Params& P, int tp, int b0, int b1, int i, Run* run) {
+  for (int b = b0; b < b1; ++b) {
+    const Req r = load_req(P, b);
+    const int tiles = (r.n + tp - 1) / tp;
+    if (i >= tiles * P.Hkv) {
+      i -= tiles * P.Hkv;
+      continue;
+    }
+    const int kh = i / tiles, tile = i - kh * tiles;
+    const int units = LEAD + blocks_to((long long)r.kv - r.n, min((long long)(tile + 1) * tp, (long long)r.n));
+    run->start = {b, kh, tile, 0, units};
+    run->req = r;
+    run->end = run->total = units;
+    run->ctas = 1;
+    return;
+  }
+}
+
 // This CTA's run of the call's units: equal ones, `least` units at least (a run of a few units would spend more on joining
 // its part with the others than on the part); where there is one request, whose items are alike, and they have no more than
-// `whole` units, each of them is a run.  False, for the whole CTA, where it has none.
+// `whole` units, each of them is a run.  So it is of several requests with no more items than CTAs, the largest of which has no
+// more than `slack` units more than an equal run.  False, for the whole CTA, where it has none.  scan: two numbers per warp.
 template <int LEAD, int TILES, int THREADS>
-__device__ __forceinline__ bool find_run(const Params& P, int least, int whole, long long* scan, Run* run) {
+__device__ __forceinline__ bool find_run(const Params& P, int least, int whole, int slack, long long* scan, Run* run) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tp = TILES * P.tq;
   const int per = (P.a.batch + THREADS - 1) / THREADS;
   const int rb0 = min(tid * per, P.a.batch);
@@ -201,9 +222,10 @@ __device__ __forceinline__ bool find_run(const Params& P, int least, int whole, 
   // more than a run can count, through q_start that falls somewhere or pages shared by many requests
   const long long most = (long long)gridDim.x * 0x3fffffff;
   long long mine, before, total, cost = 0;  // cost: of one kv head of the last request looked at
+  long long items, largest;  // this thread's; its largest, in units
   Req r = {0, 0, 0, 1};
   for (int again = 0;; ++again) {
-    mine = total = 0;
+    mine = total = items = largest = 0;
     for (int b = rb0; b < rb1; ++b) {
       r = load_req(P, b);
       if (!r.ok && !again) {
@@ -212,8 +234,17 @@ __device__ __forceinline__ bool find_run(const Params& P, int least, int whole, 
       }
       if (r.n == 0) continue;
       const long long p0 = (long long)r.kv - r.n;
-      cost = units_before<LEAD>(p0, tp, (r.n + tp - 1) / tp - 1) + LEAD + blocks_to(p0, r.n);
+      const long long last = LEAD + blocks_to(p0, r.n);
+      cost = units_before<LEAD>(p0, tp, (r.n + tp - 1) / tp - 1) + last;
       mine += P.Hkv * cost;
+      items += P.Hkv * ((r.n + tp - 1) / tp);
+      largest = max(largest, last);
+    }
+    if (P.a.batch > 1) {
+      // of a warp: the largest item, and the items unless they are more than there are CTAs anyway
+      const uint32_t units = __reduce_max_sync(0xffffffffu, (uint32_t)largest);
+      const uint32_t count = __reduce_add_sync(0xffffffffu, (uint32_t)min(items, 1LL << 16));
+      if (lane == 0) reinterpret_cast<uint2*>(scan)[THREADS / 32 + warp] = make_uint2(units, count);
     }
     before = mine;
 #pragma unroll
@@ -239,6 +270,24 @@ __device__ __forceinline__ bool find_run(const Params& P, int least, int whole, 
   }
   int ctas = (int)min((long long)gridDim.x, quot(total + least - 1, least));
   if (P.a.batch == 1 && ctas > P.Hkv && total <= (long long)P.Hkv * whole) ctas = P.Hkv;
+  if (P.a.batch > 1) {
+    const uint2 x = lane < THREADS / 32 ? reinterpret_cast<const uint2*>(scan)[THREADS / 32 + lane] : make_uint2(0u, 0u);
+    const uint32_t most_units = __reduce_max_sync(0xffffffffu, x.x), all = __reduce_add_sync(0xffffffffu, x.y);
+    if (all <= gridDim.x && total > 0 && ((long long)most_units - slack) * ctas <= total) {  // item i is CTA i's
+      if (blockIdx.x >= all) return false;
+      long long first = items;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, first, o);
+        if (lane >= o) first += t;
+      }
+      const int before_warp = (int)__reduce_add_sync(0xffffffffu, lane < warp ? x.y : 0u);
+      const int i = (int)(blockIdx.x - before_warp - (first - items));
+      if (i >= 0 && i < items) own_item<LEAD>(P, tp, rb0, rb1, i, run);
+      __syncthreads();
+      return true;
+    }
+  }
   if ((int)blockIdx.x >= ctas) return false;
   const long long u0 = quot(total * blockIdx.x, ctas), u1 = quot(total * (blockIdx.x + 1), ctas);
   if (u0 >= before && u0 < before + mine) {  // one thread's requests hold the run's first unit

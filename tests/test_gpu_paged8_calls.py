@@ -208,6 +208,34 @@ def test_requests_that_share_pages(wi, new):
     pc.free()
 
 
+@pytest.mark.parametrize("batch,where,new,kv", [
+    (30, range(30), 1, (300, 700)), (2, range(2), 1, (1, 2)), (38, range(38), 1, (900, 1100)),      # an item to a CTA
+    (300, (3, 77, 78, 299), 1, (500, 520)), (4000, (0, 1999, 3999), 1, (100, 4000)),                # few of many requests
+    (300, (3, 77, 78, 299), 5, (500, 520)), (16, range(16), 4, (1900, 2100)), (4000, (5, 3999), 90, (90, 700)),
+    (20, range(20), 16, (16, 16)), (6, range(6), 33, (30, 800)), (3, range(3), 200, (200, 300))])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (7, 1), (8, 8)])
+def test_requests_whole_in_their_ctas(wi, batch, where, new, kv, hq, hkv):
+    """Batches with fewer items than CTAs, of lengths alike or not; requests without tokens between them; twice the same."""
+    rng = np.random.default_rng(batch + new)
+    page, counts = 16, np.zeros(batch, int)
+    counts[list(where)] = new
+    lengths = np.where(counts > 0, rng.integers(kv[0], kv[1] + 1, batch), rng.integers(0, 40, batch))
+    table, n_pages = lay_out(lengths.tolist(), page, rng)
+    start = np.concatenate([[0], np.cumsum(counts)])
+    pools = [random_pool(rng, n_pages, hkv, page) for _ in range(2)]
+    (k, ks), (v, vs) = (upload(p) for p in pools)
+    pc = wi.PagedCache(wi.make_paged_config(hq, hkv, page, n_pages, batch, table.shape[1]))
+    q, Q = bf(rng.normal(size=(int(start[-1]), hq, 128)))
+    lse = torch.empty((len(q), hq), device=DEV)
+    args = (q, k, v, ks, vs, i32(table), i32(start), i32(lengths))
+    out = pc.attention8(*args, lse=lse)
+    again = pc.attention8(*args)
+    pc.check()
+    assert torch.equal(out, again)
+    compare(f64(out), f64(lse), Q, *(paged.widened(*p) for p in pools), table, start, lengths)
+    pc.free()
+
+
 def test_no_tokens_and_no_rows(wi):
     pc = wi.PagedCache(wi.make_paged_config(4, 2, 16, 4, 2, 2, inv_freq=freqs(128)), axes=[i % 3 for i in range(64)])
     rng = np.random.default_rng(76)
