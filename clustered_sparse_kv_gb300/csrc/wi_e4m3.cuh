@@ -11,6 +11,16 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
   asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(w));
   return h;
 }
+// Eight of them, the halves of a word named as they are (masked and shifted out of it, an instruction each in front of a
+// conversion, a tile's attention took 1.1% more).
+__device__ __forceinline__ uint4 e4m3x8_to_f16x8(uint32_t a, uint32_t b) {
+  uint4 h;
+  asm("{\n\t.reg .b16 p, q, r, s;\n\tmov.b32 {p, q}, %4;\n\tmov.b32 {r, s}, %5;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, p;\n\tcvt.rn.f16x2.e4m3x2 %1, q;\n\tcvt.rn.f16x2.e4m3x2 %2, r;\n\tcvt.rn.f16x2.e4m3x2 %3, s;\n\t}"
+      : "=r"(h.x), "=r"(h.y), "=r"(h.z), "=r"(h.w)
+      : "r"(a), "r"(b));
+  return h;
+}
 __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t w) {
   const uint32_t h = e4m3x2_to_f16x2(w);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));

@@ -31,8 +31,8 @@
 //
 // What bounds it, 32 query and 8 kv heads on one GB300: the chain of scores,
 // weights and product of either tile between two of its turns on the tensor
-// cores, which are active 57% of the time (2048 tokens behind 14K positions 396
-// us, 1290 TFLOP/s; behind 129K 3.1 - 3.2 ms; 8192 fresh tokens 462 us).  Of 3050
+// cores, which are active 57% of the time (2048 tokens behind 14K positions 392
+// us, 1300 TFLOP/s; behind 129K 3.1 - 3.2 ms; 8192 fresh tokens 457 us).  Of 3050
 // cycles a block takes, a chain spends 1600 on weights (2 x 670 where the other
 // chain does not want the special function units too) and 1400 waiting: 770 for the
 // tensor cores, the rest for barriers.  Shared memory, at 128 bytes a cycle, is in
@@ -870,12 +870,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
           for (int g = 0; g < 4; ++g) {
             // columns 16 c .. 16 c + 15: two pieces of the half's eight
             unsigned char* const d = o + (g0 + g) * 2048;
-            *reinterpret_cast<uint4*>(d + ((piece ^ r8) << 4)) =
-                make_uint4(e4m3x2_to_f16x2(x[g].x & 0xffffu), e4m3x2_to_f16x2(x[g].x >> 16),
-                           e4m3x2_to_f16x2(x[g].y & 0xffffu), e4m3x2_to_f16x2(x[g].y >> 16));
-            *reinterpret_cast<uint4*>(d + (((piece + 1) ^ r8) << 4)) =
-                make_uint4(e4m3x2_to_f16x2(x[g].z & 0xffffu), e4m3x2_to_f16x2(x[g].z >> 16),
-                           e4m3x2_to_f16x2(x[g].w & 0xffffu), e4m3x2_to_f16x2(x[g].w >> 16));
+            *reinterpret_cast<uint4*>(d + ((piece ^ r8) << 4)) = e4m3x8_to_f16x8(x[g].x, x[g].y);
+            *reinterpret_cast<uint4*>(d + (((piece + 1) ^ r8) << 4)) = e4m3x8_to_f16x8(x[g].z, x[g].w);
           }
         }
         fence_proxy_async_smem();
