@@ -252,9 +252,6 @@ def prepare(case, seed):
         shape = (case["batch"], case["layers"], case["hkv"], case["rows"], D)
         for name in ("k", "v"):
             s[name + "_pages"], s[name + "_scales"] = _pool8(n_pages, case["hkv"], page, gen, case["layers"])
-        if own:  # the handle's tables have to reach as far as the rows asked for, which may be more than any request has
-            wide = max(0, _up(case["rows"], page) - table.shape[1])
-            table = torch.nn.functional.pad(table, (0, wide), value=-1)
         s.update(block_table=table, kv_len=_ints(kv), pos0=min(kv) - min(min(kv), case["rows"]),
                  k_out=torch.zeros(shape, device="cuda", dtype=torch.bfloat16),
                  v_out=torch.zeros(shape, device="cuda", dtype=torch.bfloat16),
