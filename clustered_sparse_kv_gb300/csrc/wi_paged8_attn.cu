@@ -102,7 +102,8 @@ struct Smem {
   // of a block's groups: 2^e of the keys, e of the values, 2^-e of the values.  A slot is written again eight blocks on,
   // behind the scores of the block three before that, which come behind the weights of this one.
   struct Slot {
-    float2 k[kGroups], e[kGroups];  // (the same number twice)
+    float k[kGroups];
+    float2 e[kGroups];  // (the same number twice)
     float back[kGroups];
   };
   alignas(16) Slot scale[kScaleSlots];
@@ -134,17 +135,26 @@ __device__ __forceinline__ void mask_scores(uint32_t (&s)[2][32], int seen) {
     if (i > seen) s[i >> 5][i & 31] = 0xFF800000u;  // -infinity
 }
 
-// The scales of two of a block's groups as the weights take them, asked for one step ahead of their use: of the keys and the
+// The scales of two of a block's groups as the weights take them, asked for one step ahead of their use: of the keys, the
 // values' exponents twice, for packed arithmetic, and the inverse of the values'.
 struct Scales {
-  ulonglong2 k, e;
-  float2 back;
+  ulonglong2 e;
+  float2 k, back;
   __device__ __forceinline__ void load(const Smem::Slot& from, int g0) {
-    k = *reinterpret_cast<const ulonglong2*>(&from.k[g0]);
+    k = *reinterpret_cast<const float2*>(&from.k[g0]);
     e = *reinterpret_cast<const ulonglong2*>(&from.e[g0]);
     back = *reinterpret_cast<const float2*>(&from.back[g0]);
   }
 };
+
+// What a group's scores are multiplied by: its keys' scale times the row's factor, which may leave fp32 together (a row of
+// zeros over a group of zeros).  No less than the smallest normal number: a score that small is nothing, but 0 would make NaN of
+// the scores that stand at minus infinity.  A row's factor that is no number stays none.
+__device__ __forceinline__ float factor_of(float k_scale, float q_scale) {
+  float f;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(k_scale * q_scale), "f"(0x1p-126f));
+  return f;
+}
 
 // The reference that 64 scores ask for: the largest score + e less kTop, and the largest score less kFar.
 __device__ __forceinline__ float top_of(const uint32_t (&s)[2][32], const Smem::Slot& x8, int g0, float q_scale) {
@@ -155,7 +165,7 @@ __device__ __forceinline__ float top_of(const uint32_t (&s)[2][32], const Smem::
     float t = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
     for (int i = 2; i < 16; i += 2) t = max3(t, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-    t *= x8.k[g0 + g].x * q_scale;
+    t *= factor_of(x8.k[g0 + g], q_scale);
     best = max3(best, t + (x8.e[g0 + g].x - kTop), t - kFar);
   }
   return best;
@@ -163,12 +173,13 @@ __device__ __forceinline__ float top_of(const uint32_t (&s)[2][32], const Smem::
 
 // 32 scores, two groups of columns, to weights 2^(score + e - ref): added to `sum`, and over the values' scale to `low`, and
 // as f16 to 16 columns of P.
-__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t tp, const Scales& x8, uint64_t q2, uint64_t ref2,
+__device__ __forceinline__ void weights(const uint32_t (&s)[32], uint32_t tp, const Scales& x8, float q_scale, uint64_t ref2,
                                         float& sum, float& low) {
   uint32_t p[16];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const uint64_t f2 = mul2(g ? x8.k.y : x8.k.x, q2), e2 = add2(g ? x8.e.y : x8.e.x, ref2);
+    const float f = factor_of(g ? x8.k.y : x8.k.x, q_scale);
+    const uint64_t f2 = pair(f, f), e2 = add2(g ? x8.e.y : x8.e.x, ref2);
     uint64_t z[2];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -458,11 +469,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
           float zl;
           auto all_weights = [&]() -> bool {
             const float ref = m == -INFINITY ? 0.f : m;  // nothing seen so far: every weight is 2^-inf = 0
-            const uint64_t ref2 = pair(-ref, -ref), q2 = pair(q_scale, q_scale);
+            const uint64_t ref2 = pair(-ref, -ref);
             float z = zl = 0.f;
             y8.load(sm.scale[slot], 4 * half + 2);
-            weights(a[0], tsh, x8, q2, ref2, z, zl);
-            weights(a[1], tsh + 16, y8, q2, ref2, z, zl);
+            weights(a[0], tsh, x8, q_scale, ref2, z, zl);
+            weights(a[1], tsh + 16, y8, q_scale, ref2, z, zl);
             return seen >= 0 && (!(z <= kAgain) || !(zl <= kFarMost) || m == -INFINITY);
           };
           // Most halves are seen whole by every row and fit their references: their code stands on its own, without a jump
@@ -728,8 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention8(const __grid_c
         if (!fill(&map_k, sm.k[st], &sm.k_full[st], &sm.k_empty[st], kKStages, nk, row, j)) return false;
         if (lane / kGroups == j % kBatch) {
           const int ev = scale_exponent((unsigned char)(e >> 8));
-          const float ks = pow2(scale_exponent((unsigned char)(e & 0xff)));
-          sm.scale[slot].k[lane % kGroups] = make_float2(ks, ks);
+          sm.scale[slot].k[lane % kGroups] = pow2(scale_exponent((unsigned char)(e & 0xff)));
           sm.scale[slot].e[lane % kGroups] = make_float2((float)ev, (float)ev);
           sm.scale[slot].back[lane % kGroups] = pow2(-ev);
         }

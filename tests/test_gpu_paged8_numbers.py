@@ -1,0 +1,81 @@
+"""Numbers at the ends of what the paged cache in 8 bits holds: queries of nothing, scales far apart, weights far below the
+row's largest, sums over long contexts.  Tolerances as tests/test_gpu_paged8.py derives them, unless said."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged
+from test_gpu_paged import DEV, bf, f64, i32, lay_out
+from test_gpu_paged8 import as_scales, as_values, compare, exps8, random_pool, upload, values8
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def wi():
+    import clustered_sparse_kv_gb300 as m
+    return m
+
+
+def attend(wi, Q, pools, table, start, kv, page):
+    """out and lse of attention8 in 64 bits; queries in bf16, pools as (values, exponents)."""
+    n, hq = Q.shape[:2]
+    (k, ks), (v, vs) = pools
+    pc = wi.PagedCache(wi.make_paged_config(hq, k.shape[1], page, k.shape[0], len(kv), table.shape[1]))
+    out = torch.full((n, hq, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((n, hq), 7.0, device=DEV)
+    pc.attention8(Q, k, v, ks, vs, i32(table), i32(start), i32(kv), out=out, lse=lse)
+    pc.check()
+    pc.free()
+    return f64(out), f64(lse)
+
+
+# ------------------------------------------------------------ queries of nothing ----
+
+@pytest.mark.parametrize("new,ctx", [([1], [40]), ([40], [0]), ([40], [75]), ([7, 1, 100], [0, 30, 300]), ([300], [0])])
+def test_attention8_of_zeros_that_were_written(wi, new, ctx):
+    """A call on zeroed rows, as a warm-up's or a padded batch's: groups of zero keys have the smallest scale, and every row is
+    the mean of the values that it sees."""
+    rng = np.random.default_rng(70)
+    hq, hkv, page = 8, 2, 16
+    kv = [c + n for c, n in zip(ctx, new)]
+    table, n_pages = lay_out(kv, page, rng)
+    start = np.concatenate([[0], np.cumsum(new)])
+    pc = wi.PagedCache(wi.make_paged_config(hq, hkv, page, n_pages, len(kv), table.shape[1]))
+    pools = [torch.zeros((n_pages, hkv, page, 128), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    pools += [torch.zeros((n_pages, hkv, 1), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    at = np.concatenate([np.arange(n) for n in kv])          # everything that is cached, in one write
+    who = np.repeat(np.arange(len(kv)), kv)
+    slots = table[who, at // page] * page + at % page
+    zeros = torch.zeros((len(at), hq, 128), dtype=torch.bfloat16, device=DEV)
+    v, V = bf(rng.normal(size=(len(at), hkv, 128)))
+    q = pc.write8(zeros, zeros[:, :hkv], v, i32(at), i32(slots), *pools)
+    assert (exps8(pools[2])[table[table >= 0]] == paged.LOWEST).all()
+    q = q[:start[-1]].contiguous()
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full(q.shape[:2], 7.0, device=DEV)
+    pc.attention8(q, *pools, i32(table), i32(start), i32(kv), out=out, lse=lse)
+    pc.check()
+    pc.free()
+    K, V = (paged.widened(values8(p), exps8(s)) for p, s in (pools[::2], pools[1::2]))
+    compare(f64(out), f64(lse), f64(q), K, V, table, start, kv)
+
+
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -126, 2.0 ** -100, 2.0 ** -60, 2.0 ** -15, 1.0])
+@pytest.mark.parametrize("exps", [[-64], [-127], [-127, 0], [-64, -22, 3]])
+@pytest.mark.parametrize("new,kv", [([50], [50]), ([50, 3, 200], [300, 3, 333]), ([1, 1], [100, 130])])
+def test_attention8_of_small_queries_over_small_scales(wi, size, exps, new, kv):
+    """Factors of a score that vanish: the row's and the group's together leave fp32, in groups that a row sees and in those
+    that it does not.  Rows of zeros beside others."""
+    rng = np.random.default_rng(71)
+    hq, hkv, page = 8, 2, 32
+    table, n_pages = lay_out(kv, page, rng)
+    start = np.concatenate([[0], np.cumsum(new)])
+    Q = rng.normal(size=(start[-1], hq, 128)) * size
+    Q[::3, ::2] = 0
+    q, Q = bf(Q)
+    values = [paged.e4m3(rng.normal(size=(n_pages, hkv, page, 128)) * 50) for _ in range(2)]
+    e = rng.choice(exps, (n_pages, hkv, page // 16))
+    pools = [(values[0], e), (values[1], np.full_like(e, -6))]
+    out, lse = attend(wi, q, [upload(p) for p in pools], table, start, kv, page)
+    compare(out, lse, Q, *(paged.widened(*p) for p in pools), table, start, kv)
