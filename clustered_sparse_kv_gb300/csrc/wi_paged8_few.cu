@@ -9,15 +9,15 @@
 // not, and are sums of e4m3 pieces.  A bf16 query is a first piece of four
 // significant bits and a rest of four, exactly (over the row's largest element;
 // what is below 2^-17 of that may be lost), so Q has two columns per row and S
-// is added up.  A weight has four pieces with a column, and so a sum in tensor
-// memory, each: columns cost next to nothing here, and each piece has its own
-// power of two, so that together they hold twelve bits of a weight down to 2^-9
-// and no less than 2^-28 of the largest (a sink of attention may weigh a
-// million times more than what is left of the row).
+// is added up.  A weight has six pieces of four bits with a column, and so a sum
+// in tensor memory, each: columns cost next to nothing here, and each piece has
+// its own power of two, so that together they hold a weight to 2^-33 of the
+// largest, or to fp32 (a sink of attention may weigh many million times more
+// than what is left of the row).
 //
 // A thread of the four softmax warps has one position: its group's two scales,
-// its score of every row, and its weights' pieces, which it stores as one or
-// two 16-byte pieces of B.  The value's scale 2^e goes into the weight,
+// its score of every row, and its weights' pieces, which it stores as two or
+// three 16-byte pieces of B.  The value's scale 2^e goes into the weight,
 // p' = 2^(score + e - m), and out of the sum, l += p' 2^-e; m is a row's
 // reference, near the largest score + e so far.  It moves only when a weight
 // would pass 448 (every thread asks, by one barrier a block): then O is
@@ -69,25 +69,25 @@ constexpr int kLeast = 2, kWhole = 4;
 constexpr int kSlack = 4;
 // Blocks after which the tensor cores' sums are added up in fp32: their additions cut bits off.
 constexpr int kFlush = 1024;
-constexpr int kPieces = 4;
+constexpr int kPieces = 6;
 constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
 constexpr float kLn2 = 0.6931471805599453f;
-// A new reference makes the row's largest weight 2^2; it is taken where one passes 2^8.5, or where a score is so far above
-// it (through values of a tiny scale) that the sum might leave fp32.
-constexpr float kTop = 2.f, kMost = 8.5f, kFar = 64.f, kFarMost = 80.f;
+// A new reference makes the row's largest weight 2^3 (for values' scales of 2^-64 or more); it is taken where one passes
+// 2^8.5, or where a score is so far above it (through values of a tiny scale) that the sum might leave fp32.
+constexpr float kTop = 3.f, kMost = 8.5f, kFar = 64.f + kTop, kFarMost = 80.f;
 
-// What the pieces of a weight are multiplied by, one on top of the other: the first three take four bits each, the last
-// one what is too small for them.
-__device__ __forceinline__ constexpr float step_of(int piece) { return piece == kPieces - 1 ? 256.f : 16.f; }
-__device__ __forceinline__ constexpr float size_of(int piece) {
-  return piece == 0 ? 1.f : piece == 1 ? 1.f / 16 : piece == 2 ? 1.f / 256 : 1.f / 65536;
-}
+// A piece takes four bits, so that what it leaves, times kStep, is a piece again; the last one is known to 2^-10, 2^-30 of
+// a weight's own units.
+constexpr float kStep = 16.f;
+__device__ __forceinline__ constexpr float size_of(int piece) { return piece == 0 ? 1.f : size_of(piece - 1) / kStep; }
 
 // RP: rows of a tile.
 template <int RP>
 struct Smem {
   static constexpr int kQCols = 16;            // two columns per row, sixteen at least
-  static constexpr int kPCols = kPieces * RP;
+  static constexpr int kPCols = (kPieces * RP + 15) / 16 * 16;
+  static constexpr int kRings = 2 * kStages * kBlockBytes / (RP * WI_D * 4);  // parts that fit the rings at a time
+  static constexpr int kJoin = (kRings + 31) / 32 * 32;
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   // Of two buffers each, block n's in n & 1: who waits for block n's has seen that of block n - 2 (S of a block is issued
   // behind O of the one two before it), so that a phase's parity says which it is.
@@ -103,7 +103,7 @@ struct Smem {
   float xch[kSoftWarps][RP];
   float sum[kSoftWarps][RP];
   float scale[kStages][2][kRows / kGroup];  // 2^e of the keys' groups; e of the values'
-  alignas(16) float factor[64][RP];  // of the parts that are added up
+  alignas(16) float factor[kJoin][RP];  // of the parts that are added up
   float joined[3][RP];
   alignas(1024) unsigned char q[kQCols * WI_D];      // K-major, 128-byte swizzle
   unsigned char p[2][kPCols * kRows];                // [16 columns][position][16 B]
@@ -141,12 +141,27 @@ __device__ __forceinline__ void split(float (&x)[RP], uint32_t (&out)[kPieces][R
       out[i][w] = a | b << 16;
       if (i + 1 < kPieces) {
         const float2 fa = e4m3x2_to_f32x2(a), fb = e4m3x2_to_f32x2(b);
-        y[0] = (y[0] - fa.x) * step_of(i + 1);
-        y[1] = (y[1] - fa.y) * step_of(i + 1);
-        y[2] = (y[2] - fb.x) * step_of(i + 1);
-        y[3] = (y[3] - fb.y) * step_of(i + 1);
+        y[0] = (y[0] - fa.x) * kStep;
+        y[1] = (y[1] - fa.y) * kStep;
+        y[2] = (y[2] - fb.x) * kStep;
+        y[3] = (y[3] - fb.y) * kStep;
       }
     }
+  }
+}
+
+// The pieces' sums of this thread's element, the smallest first, to acc.
+template <int RP>
+__device__ __forceinline__ void add_pieces(uint32_t from, float (&acc)[RP]) {
+  float size = size_of(kPieces - 1);
+#pragma unroll 1
+  for (int i = kPieces - 1; i >= 0; --i, size *= kStep) {
+    uint32_t a[RP];
+#pragma unroll
+    for (int q = 0; q < RP; q += 4) tmem_ld4_nowait(from + i * RP + q, reinterpret_cast<uint32_t(&)[4]>(a[q]));
+    tmem_wait_ld();
+#pragma unroll
+    for (int r = 0; r < RP; ++r) acc[r] += __uint_as_float(a[r]) * size;
   }
 }
 
@@ -204,7 +219,6 @@ struct Queries {
 // here once a call, so the code is cold, and what counts is how little of it there is: the parts' columns come to shared
 // memory by a short loop of asynchronous copies, `room` parts at a time (38 parts 8.2 us with unrolled loads to registers,
 // 2.1 of which went by before the last load was issued; 4 so).
-constexpr int kJoin = 64;  // parts at a time, at most
 template <int RP>
 __device__ __noinline__ void join_parts(const Params& P, Smem<RP>& sm, const Split& sp, int c0, unsigned char* buf, int room) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, parts = sp.last - c0 + 1;
@@ -234,11 +248,13 @@ __device__ __noinline__ void join_parts(const Params& P, Smem<RP>& sm, const Spl
     }
     if (i0 > 0) soft_barrier();  // the factors before are read
 #pragma unroll
-    for (int k = 0; k < RP / kSoftWarps; ++k) {  // a warp has a row's factors, a lane two parts'
+    for (int k = 0; k < RP / kSoftWarps; ++k) {  // a warp has a row's factors, a lane one or two parts'
       const int r = warp + k * kSoftWarps;
+      constexpr int kEach = Smem<RP>::kJoin / 32;
+      static_assert(kEach <= 2, "m and l");
       float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < kEach; ++h)
         if (32 * h + lane < n) {
           m[h] = __ldcg(part(i0 + 32 * h + lane) + r);
           l[h] = __ldcg(part(i0 + 32 * h + lane) + RP + r);
@@ -248,7 +264,7 @@ __device__ __noinline__ void join_parts(const Params& P, Smem<RP>& sm, const Spl
       L[k] = L[k] * back + warp_sum(f0 * l[0] + f1 * l[1]);
       M[k] = top;
       sm.factor[lane][r] = f0;
-      sm.factor[32 + lane][r] = f1;
+      if (kEach > 1) sm.factor[(kEach - 1) * 32 + lane][r] = f1;
       if (lane == 0) {
         sm.joined[0][r] = M[k];
         sm.joined[1][r] = L[k];
@@ -315,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention8_few(const __gr
     sm.poison = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  constexpr uint32_t kCols = 64;  // S twice (16 columns), O
+  constexpr uint32_t kCols = 32 + Sm::kPCols <= 64 ? 64 : 128;  // S twice (16 columns), O
   if (warp == kSoftWarps + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem_base)),
                  "n"(kCols)
@@ -401,16 +417,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention8_few(const __gr
         if (fresh && j > 0) {
           if (ok) ok = mbar_wait(&sm.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, P.err);
           tc_fence_after();
-#pragma unroll
-          for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-            for (int q = 0; q < RP; q += 4) {
-              uint32_t a[4];
-              tmem_ld4_nowait(tmem + lanes + 32 + i * RP + q, a);
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < 4; ++c) acc[q + c] += __uint_as_float(a[c]) * size_of(i);
-            }
+          add_pieces<RP>(tmem + lanes + 32, acc);
 #pragma unroll
           for (int r = 0; r < RP; ++r) {  // the sum so far, apart from what is to come
             l_sum[r] += l[r];
@@ -475,13 +482,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention8_few(const __gr
         }
         uint32_t b[kPieces][RP / 4];
         split<RP>(y, b);
-        if (RP == 4) {
-          *reinterpret_cast<uint4*>(sm.p[buf] + 16 * tid) = make_uint4(b[0][0], b[1][0], b[2][0], b[3][0]);
-        } else {
-          uint4* const to = reinterpret_cast<uint4*>(sm.p[buf] + 16 * tid);
-          to[0] = make_uint4(b[0][0], b[0][RP / 4 - 1], b[1][0], b[1][RP / 4 - 1]);
-          to[kRows] = make_uint4(b[2][0], b[2][RP / 4 - 1], b[3][0], b[3][RP / 4 - 1]);
-        }
+        // piece i, words of four rows, one behind the other; no piece: zero
+        auto word = [&](int i) -> uint32_t { return i < kPieces * RP / 4 ? b[i / (RP / 4)][i % (RP / 4)] : 0u; };
+#pragma unroll
+        for (int c = 0; c < Sm::kPCols / 16; ++c)
+          reinterpret_cast<uint4*>(sm.p[buf] + 16 * tid)[c * kRows] =
+              make_uint4(word(4 * c), word(4 * c + 1), word(4 * c + 2), word(4 * c + 3));
         if (pos > whole) {
           // A value that not every row sees: 0 * NaN is NaN inside the product, so rows behind the request's end are zeroed,
           // and so are NaN elements, which the end of the segment adds to the rows that see them.
@@ -525,20 +531,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention8_few(const __gr
       }
       if (ok) ok = mbar_wait(&sm.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, P.err);
       tc_fence_after();
-      {
-        uint32_t a[kPieces][RP];
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-          for (int q = 0; q < RP; q += 4)
-            tmem_ld4_nowait(tmem + lanes + 32 + i * RP + q, reinterpret_cast<uint32_t(&)[4]>(a[i][q]));
-        tmem_wait_ld();
-#pragma unroll
-        for (int r = 0; r < RP; ++r) {
-#pragma unroll
-          for (int i = kPieces - 1; i >= 0; --i) acc[r] += __uint_as_float(a[i][r]) * size_of(i);
-        }
-      }
+      add_pieces<RP>(tmem + lanes + 32, acc);
       tc_fence_before();  // O is read: the next segment may write it
       soft_barrier();
 #pragma unroll
@@ -592,10 +585,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_paged_attention8_few(const __gr
         soft_barrier();
         if (sm.last) {
           // behind the CTA's last segment the rings are free, else what the weights took
-          constexpr int kRings = 2 * kStages * kBlockBytes / (RP * WI_D * 4);
-          static_assert(kRings <= kJoin, "a lane has two parts");
           join_parts<RP>(P, sm, {done.r.s0 + done.tile * done.tp, done.kh, done.cnt, c1}, c0, more ? sm.p[0] : sm.k[0],
-                         more ? (int)(sizeof(sm.p) / (RP * WI_D * 4)) : kRings);
+                         more ? (int)(sizeof(sm.p) / (RP * WI_D * 4)) : Sm::kRings);
         }
       }
       soft_barrier();  // what the threads share is read, and the next segment's queries have their scales

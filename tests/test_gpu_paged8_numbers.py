@@ -79,3 +79,41 @@ def test_attention8_of_small_queries_over_small_scales(wi, size, exps, new, kv):
     pools = [(values[0], e), (values[1], np.full_like(e, -6))]
     out, lse = attend(wi, q, [upload(p) for p in pools], table, start, kv, page)
     compare(out, lse, Q, *(paged.widened(*p) for p in pools), table, start, kv)
+
+
+# ------------------------------------------------------------ weights far below the largest ----
+
+def behind_a_sink(wi, hq, tokens, requests, where):
+    """One position of value 0, which weighs e^gap as much as any other, all alike and of value 1: what is left of a row is a
+    multiple of one weight, whose rounding shows as it is.  Gaps from 0.3 to 18 (2^26) in steps that fall between rounding
+    points, one for every row."""
+    rng = np.random.default_rng(72)
+    kv, page = 20000 + tokens, 16
+    table, n_pages = lay_out([kv], page, rng)
+    n = tokens * requests
+    gaps = np.linspace(0.3, 18.0, n * hq).reshape(n, hq)
+    base = np.sqrt(18.0 * np.sqrt(128) / 128)                   # of the sink's key: q . k = gap * sqrt(128)
+    k0 = paged.e4m3(np.full(128, base * 64)) / 64
+    q, Q = bf(np.broadcast_to((gaps * np.sqrt(128) / k0.sum())[..., None], (n, hq, 128)))
+    pools = [(np.zeros((n_pages, 1, page, 128)), np.full((n_pages, 1, 1), -6)) for _ in range(2)]
+    pools[1][0][table[0]] = 64
+    pools[0][0][table[0, where // page], 0, where % page] = k0 * 64
+    pools[1][0][table[0, where // page], 0, where % page] = 0
+    start, lengths = np.arange(requests + 1) * tokens, [kv] * requests
+    out, lse = attend(wi, q, [upload(p) for p in pools], np.repeat(table, requests, 0), start, lengths, page)
+    gap = Q[..., 0] * k0.sum() / np.sqrt(128)
+    others = kv - tokens + np.tile(np.arange(tokens), requests)[:, None]      # positions beside the sink
+    ref = others / (others + np.exp(gap))
+    # A weight is known to 2^-11 of itself or 2^-33 of the row's largest.  A score, of products that are all alike and exact in
+    # pieces, is off by 128 * 2^-24 of itself, and its weight by as much; the tensor cores' 160 blocks of eight additions by 2^-23
+    # each; a power of two and the sums of the weights by 2^-17; the output is rounded to bf16, 2^-8.
+    tol = 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -33 * np.exp(gap) + 2 * 128 * 2.0 ** -24 * gap + 160 * 8 * 2.0 ** -23 + 2.0 ** -17
+    err = np.abs(out / ref[..., None] - 1)
+    assert (err <= tol[..., None]).all(), (err / tol[..., None]).max()
+    assert (np.abs(lse - np.log(others + np.exp(gap))) <= 2.0 ** -11).all()
+
+
+@pytest.mark.parametrize("where", [0, 3000, 19990])
+@pytest.mark.parametrize("hq", [4, 8])
+def test_attention8_weights_behind_a_sink_single_tokens(wi, hq, where):
+    behind_a_sink(wi, hq, 1, 44, where)
