@@ -76,12 +76,15 @@ constexpr int kLead = 4;                        // units in front of an item's b
 // 37.8 us whole, 46.1 cut; eight requests' sixteen over 500 - 1500 25.3 cut, 28.1 with a slack of sixteen).
 constexpr int kSlack = 8;
 constexpr int kWhole = 4;                       // blocks up to which one request's items of few rows are not cut
-// Blocks that one segment has at most: the tensor cores' additions cut bits off, so longer sums are added up in fp32.
+// Blocks that one segment has at most: the tensor cores' additions cut bits off, so longer sums are added up in fp32.  Sums of
+// numbers of one sign come out too small by 3e-4 of themselves after 1024 blocks, by 7e-4 after 2048 and more (with 512 at most
+// 1.6e-4, and 2048 tokens behind 129K 3170 us for 3120; with 256 6e-5 and 3240).
 constexpr int kLongest = 2048;
-// A reference makes the row's largest weight 2^4: f16 holds a weight to 11 bits down to 2^-18 of that, and no less than
-// 2^-29 of it.  A row takes a new one when a block's weights add up to more than f16 takes, or its sum (through values
-// of a tiny scale) to more than kFarMost.
-constexpr float kTop = 4.f, kAgain = 60000.f, kFar = 64.f, kFarMost = 0x1p90f;
+// A reference makes the row's largest weight 2^4 (for values' scales of 2^-64 or more): f16 holds a weight to 2^-11 of itself
+// down to 2^-18 of that, and to 2^-29 of it below.  A row takes a new one when half a block's weights add up to more than f16
+// takes, or its sum (through values of a tiny scale) to more than kFarMost.  A larger first weight would hold more and leave
+// less room above it, and new references cost time: seven mixed requests 173 us, with 2^5 178, with 2^6 183, with 2^8 201.
+constexpr float kTop = 4.f, kAgain = 60000.f, kFar = 64.f + kTop, kFarMost = 0x1p90f;
 
 template <bool LONG>
 using Walk = WalkOver<kLead, 2, LONG ? kLongest : 0>;

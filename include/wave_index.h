@@ -562,8 +562,13 @@ int wi_paged_write8(wi_paged* pc, int n_tokens, const void* q, long long q_strid
 /*
  * wi_paged_attention over 8-bit pools: the same tables, rows and masks, with keys and values that are a pool's
  * values times their group's scale.  What lies at positions that a token does not see has no influence, NaN and
- * scales included.  Queries and the softmax lose nothing to the 8 bits; the weights are held to 2^-10 of themselves or
- * better for the product with V.
+ * scales included.  Queries and weights are not rounded to 8 bits: a query's elements are held to 2^-17 of the largest
+ * of their head (bf16's own bits down to 2^-9 of it); a weight, for the product with V, to 2^-11 of itself or to 2^-29
+ * of the row's largest, whichever is more (2^-33 in calls of single tokens; where values' scales differ, weights times
+ * scales are meant, and scales of 2^-64 or more).  The sum over the positions is an fp32 one whose additions cut bits
+ * off: over a million positions of values of one sign it comes out up to 2^-10 of itself too small.  lse and the sum
+ * that divides have every weight down to 2^-30 of the largest in fp32, as long as the scales of the values that a row
+ * sees lie within 2^100 of each other.
  */
 int wi_paged_attention8(wi_paged* pc, int batch, int n_tokens, const void* q, const void* k_pages,
                         const void* v_pages, const void* k_scales, const void* v_scales, const int32_t* block_table,

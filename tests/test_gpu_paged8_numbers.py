@@ -83,10 +83,11 @@ def test_attention8_of_small_queries_over_small_scales(wi, size, exps, new, kv):
 
 # ------------------------------------------------------------ weights far below the largest ----
 
-def behind_a_sink(wi, hq, tokens, requests, where):
+def behind_a_sink(wi, hq, tokens, requests, where, least):
     """One position of value 0, which weighs e^gap as much as any other, all alike and of value 1: what is left of a row is a
     multiple of one weight, whose rounding shows as it is.  Gaps from 0.3 to 18 (2^26) in steps that fall between rounding
-    points, one for every row."""
+    points, one for every row.  As many requests as leave their runs whole: a part that does not hold the sink would hold its
+    weights better."""
     rng = np.random.default_rng(72)
     kv, page = 20000 + tokens, 16
     table, n_pages = lay_out([kv], page, rng)
@@ -104,10 +105,10 @@ def behind_a_sink(wi, hq, tokens, requests, where):
     gap = Q[..., 0] * k0.sum() / np.sqrt(128)
     others = kv - tokens + np.tile(np.arange(tokens), requests)[:, None]      # positions beside the sink
     ref = others / (others + np.exp(gap))
-    # A weight is known to 2^-11 of itself or 2^-33 of the row's largest.  A score, of products that are all alike and exact in
+    # A weight is known to 2^-11 of itself or to `least` of the row's largest.  A score, of products that are all alike and exact in
     # pieces, is off by 128 * 2^-24 of itself, and its weight by as much; the tensor cores' 160 blocks of eight additions by 2^-23
     # each; a power of two and the sums of the weights by 2^-17; the output is rounded to bf16, 2^-8.
-    tol = 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -33 * np.exp(gap) + 2 * 128 * 2.0 ** -24 * gap + 160 * 8 * 2.0 ** -23 + 2.0 ** -17
+    tol = 2.0 ** -8 + 2.0 ** -11 + least * np.exp(gap) + 2 * 128 * 2.0 ** -24 * gap + 160 * 8 * 2.0 ** -23 + 2.0 ** -17
     err = np.abs(out / ref[..., None] - 1)
     assert (err <= tol[..., None]).all(), (err / tol[..., None]).max()
     assert (np.abs(lse - np.log(others + np.exp(gap))) <= 2.0 ** -11).all()
@@ -116,4 +117,12 @@ def behind_a_sink(wi, hq, tokens, requests, where):
 @pytest.mark.parametrize("where", [0, 3000, 19990])
 @pytest.mark.parametrize("hq", [4, 8])
 def test_attention8_weights_behind_a_sink_single_tokens(wi, hq, where):
-    behind_a_sink(wi, hq, 1, 44, where)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    behind_a_sink(wi, hq, 1, 2 * sms, where, 2.0 ** -33)
+
+
+@pytest.mark.parametrize("where", [0, 3000, 19990])
+@pytest.mark.parametrize("hq,tokens", [(4, 44), (8, 3), (1, 200)])
+def test_attention8_weights_behind_a_sink_chunks(wi, hq, tokens, where):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    behind_a_sink(wi, hq, tokens, sms, where, 2.0 ** -29)
