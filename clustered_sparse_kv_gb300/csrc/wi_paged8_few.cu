@@ -67,8 +67,9 @@ constexpr int kLeast = 2, kWhole = 4;
 // What the largest item may have above an equal run, where each item is a run (30 single tokens over 300 - 700 positions 14.6 us
 // whole, 21.1 cut; ten over 300 - 900 13.8 cut, 13.4 with eight, but sixteen over 2000 25.0 with sixteen, 23.6 cut).
 constexpr int kSlack = 4;
-// Blocks after which the tensor cores' sums are added up in fp32: their additions cut bits off.
-constexpr int kFlush = 1024;
+// Blocks after which the tensor cores' sums are added up in fp32: their additions cut bits off.  Sums of numbers of one sign
+// come out too small by 1.4e-5 of themselves (by 1e-4 with 1024); reading them costs less than a block.
+constexpr int kFlush = 256;
 constexpr int kPieces = 6;
 constexpr float kScaleLog2 = 0.08838834764831845f * 1.4426950408889634f;  // log2(e) / sqrt(128)
 constexpr float kLn2 = 0.6931471805599453f;

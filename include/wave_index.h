@@ -566,7 +566,8 @@ int wi_paged_write8(wi_paged* pc, int n_tokens, const void* q, long long q_strid
  * of their head (bf16's own bits down to 2^-9 of it); a weight, for the product with V, to 2^-11 of itself or to 2^-29
  * of the row's largest, whichever is more (2^-33 in calls of single tokens; where values' scales differ, weights times
  * scales are meant, and scales of 2^-64 or more).  The sum over the positions is an fp32 one whose additions cut bits
- * off: over a million positions of values of one sign it comes out up to 2^-10 of itself too small.  lse and the sum
+ * off: over many positions of values of one sign it comes out up to 2^-10 of itself too small (2^-16 in calls of single
+ * tokens).  lse and the sum
  * that divides have every weight down to 2^-30 of the largest in fp32, as long as the scales of the values that a row
  * sees lie within 2^100 of each other.
  */

@@ -126,3 +126,24 @@ def test_attention8_weights_behind_a_sink_single_tokens(wi, hq, where):
 def test_attention8_weights_behind_a_sink_chunks(wi, hq, tokens, where):
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     behind_a_sink(wi, hq, tokens, sms, where, 2.0 ** -29)
+
+
+# ------------------------------------------------------------ sums over long contexts ----
+
+def test_attention8_single_tokens_sums_of_one_sign(wi):
+    """What the tensor cores' additions cut off, over 2^18 positions in one CTA's run, on the average over many rows: less than
+    an addition's 2^-23 of the sum for each of the 256 blocks of four that are added up there."""
+    rng = np.random.default_rng(73)
+    kv, batch = 1 << 18, 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    pages = rng.integers(0, 8, kv // 128)
+    q, Q = bf(rng.normal(size=(batch, 1, 128)))
+    pools = [(paged.e4m3(rng.normal(size=(8, 1, 128, 128)) * 64), np.full((8, 1, 8), -6)),
+             (paged.e4m3(rng.uniform(48, 80, size=(8, 1, 128, 128))), np.full((8, 1, 8), -6))]
+    out, _ = attend(wi, q, [upload(p) for p in pools], np.repeat(pages[None], batch, 0), np.arange(batch + 1), [kv] * batch, 128)
+    K, V = (paged.widened(*p).reshape(-1, 128) for p in pools)
+    x = Q[:, 0] @ K.T / np.sqrt(128)
+    w = np.repeat(np.bincount(pages, minlength=8), 128) * np.exp(x - x.max(1, keepdims=True))
+    ref = w / w.sum(1, keepdims=True) @ V
+    # 39000 elements, of which a few in a hundred round the other way by 2^-8: their mean is known to 2^-16
+    bias = ((out[:, 0] - f64(torch.from_numpy(ref).bfloat16())) / ref).mean()
+    assert abs(bias) <= 256 * 4 * 2.0 ** -23 + 2.0 ** -16, bias
