@@ -493,7 +493,7 @@ class PagedCache:
     share its scratch: order them (one stream).
 
     axes: the axis of each of the rotation's rotary_dim // 2 pairs, numbers from 0 (time, height, width, say;
-    wi_paged_axes); `positions` of the writes is then [max(axes) + 1][n].
+    wi_paged_axes); `positions` of the writes is then [max(axes) + 1][n] (with one axis [n] as well).
 
     write8, attention8 and gather8 are the calls of the same name over pools in 8 bits: k_pages, v_pages
     torch.float8_e4m3fn [n_pages][n_kv_heads][page_size][128] and k_scales, v_scales torch.float8_e8m0fnu

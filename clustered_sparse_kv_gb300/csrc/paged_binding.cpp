@@ -113,11 +113,13 @@ struct Reader {
     *k = data("k_scales", ko, kE8m0, s);
     *v = data("v_scales", vo, kE8m0, s);
   }
-  // positions [n], or [axes][n]
+  // positions [axes][n]; of one axis [n] too
   int32_t* places(PyObject* o, int64_t n) {
     const int64_t shape[] = {c->axes, n};
+    const at::Tensor* t = c->axes > 1 ? nullptr : tensor("positions", o);
+    const bool axes = c->axes > 1 || (t && t->dim() == 2);
     return static_cast<int32_t*>(
-        data("positions", o, kInt32, c->axes > 1 ? at::IntArrayRef(shape, 2) : at::IntArrayRef(shape + 1, 1)));
+        data("positions", o, kInt32, axes ? at::IntArrayRef(shape, 2) : at::IntArrayRef(shape + 1, 1)));
   }
   // Sizes that the C ABI takes as int.
   void fits(const char* what, int64_t n) {
