@@ -567,9 +567,11 @@ int wi_paged_write8(wi_paged* pc, int n_tokens, const void* q, long long q_strid
  * of the row's largest, whichever is more (2^-33 in calls of single tokens; where values' scales differ, weights times
  * scales are meant, and scales of 2^-64 or more).  The sum over the positions is an fp32 one whose additions cut bits
  * off: over many positions of values of one sign it comes out up to 2^-10 of itself too small (2^-16 in calls of single
- * tokens).  lse and the sum
- * that divides have every weight down to 2^-30 of the largest in fp32, as long as the scales of the values that a row
- * sees lie within 2^100 of each other.
+ * tokens).  lse and the sum that divides have every weight down to 2^-30 of the largest in fp32, as long as the scales
+ * of the values that a row sees lie within 2^100 of each other.
+ * A call of no more tokens than requests (n_q_heads / n_kv_heads = 2: twice, 1: four times as many) is one of single
+ * tokens: how the requests share the tokens does not change what it gives, but a chunk reads its context once for every
+ * token (two, four) there.  Requests without tokens are better left out of a call that has a chunk.
  */
 int wi_paged_attention8(wi_paged* pc, int batch, int n_tokens, const void* q, const void* k_pages,
                         const void* v_pages, const void* k_scales, const void* v_scales, const int32_t* block_table,
