@@ -575,7 +575,8 @@ class PagedCache:
     def write8(self, q, k, v, positions, slots, k_pages, v_pages, k_scales, v_scales, q_out=None, q_weight=None,
                k_weight=None, stream=None):
         """write into pools in 8 bits (wi_paged_write8); returns q_out.  The tokens that share a group of sixteen
-        slots have to follow one another, in rising slots without a gap."""
+        slots have to follow one another, in rising slots without a gap.  Where such a group's scale grows, what it
+        held before is rounded again: order the calls that read it before or behind this one, on other streams too."""
         if q_out is None:
             q_out = _new_on(stream, (q.shape[0], self.n_q_heads, 128), q.dtype, q.device)
         rc = self._calls.write8(self._ctx, q, k, v, positions, slots, k_pages, v_pages, k_scales, v_scales, q_out,

@@ -553,6 +553,11 @@ int wi_paged_gather(wi_paged* pc, int batch, int layers, const void* k_pages, co
  * call that share a group have to follow one another, in rising slots without a
  * gap (as wi_paged_tables gives them): otherwise that group's contents are
  * unspecified.
+ * Unlike wi_paged_write, which touches the call's slots alone, a call may so
+ * change values and scales that earlier ones wrote (of a group that it adds to,
+ * the values in front of its own first, then the scale): what reads that group,
+ * as attention or a gather of the same request, has to be ordered before the
+ * call or behind it, on other streams with an event.
  */
 int wi_paged_write8(wi_paged* pc, int n_tokens, const void* q, long long q_stride, const void* k, long long k_stride,
                     const void* v, long long v_stride, const void* q_weight, const void* k_weight,
