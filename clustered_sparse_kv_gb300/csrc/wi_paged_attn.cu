@@ -113,15 +113,10 @@ struct Smem {
   int last;                 // this CTA merges the item that it just added to
   int poison[8];            // segment number + 1 of the last segment (modulo 8) with an infinite or NaN value
   long long scan[kThreads / 32];
-  long long run_end, total;  // the unit behind this CTA's run, all units
-  int ctas;                 // CTAs with units
-  int spare;
-  Cursor start;             // of the run
-  Req req;                  // start.b's
+  Run run;
   Req reqs[kSoftWarps];     // of the softmax warps' segments
   float xch[2][2][kRows];   // maximum and sum of a row, from chain to chain: [chain][m, l]
-  unsigned char pad[3 * 1024 - (4 * kStages + 9) * 8 - 4 - 32 - 4 - kThreads / 32 * 8 - 24 - 20 - 16 - 4 * kRows * 4 - kSoftWarps * 16];
-  unsigned char q[2][kTileBytes];          // [k half][128 rows][128 B]
+  alignas(1024) unsigned char q[2][kTileBytes];          // [k half][128 rows][128 B]
   unsigned char ring[kStages][kTileBytes]; // [group of 8 rows][k half][8 rows][128 B]
 };
 static_assert(offsetof(Smem, q) == 3 * 1024, "tiles must start 1024-byte aligned");
@@ -214,28 +209,15 @@ __device__ __forceinline__ void add_poison(const Params& P, int b, int kh, int f
 struct Share {
   long long mine, before, total;
 };
-__device__ __noinline__ Share share_of(const Params& P, Smem& sm, int rb0, int rb1) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tp = 2 * P.tq;
+__device__ __noinline__ Share share_of(const Params& P, long long* scan, int rb0, int rb1) {
+  const int tp = 2 * P.tq;
   Share x = {0, 0, 0};
   for (int b = rb0; b < rb1; ++b) {
     const Req r = load_req(P, b);
-    if (r.n == 0) continue;
-    const long long p0 = (long long)r.kv - r.n;
-    x.mine += P.Hkv * (units_before<kLead>(p0, tp, (r.n + tp - 1) / tp - 1) + kLead + blocks_to(p0, r.n));
-  }
-  x.before = x.mine;
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, x.before, o);
-    if (lane >= o) x.before += t;
+    if (r.n > 0) x.mine += P.Hkv * units_of<kLead>(r, tp);
   }
   __syncthreads();  // every warp has read the sums that stood there
-  if (lane == 31) sm.scan[warp] = x.before;
-  __syncthreads();
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w == warp) x.before += x.total;
-    x.total += sm.scan[w];
-  }
-  x.before -= x.mine;
+  add_up<kThreads>(x.mine, scan, x.before, x.total);
   return x;
 }
 
@@ -303,33 +285,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       if (P.a.q_start[b + 1] < r.s0) mine += kFalls;
     }
     if (r.n == 0) continue;
-    const int tiles = (r.n + tp - 1) / tp;
-    cost = units_before<kLead>((long long)r.kv - r.n, tp, tiles - 1) + kLead + blocks_to((long long)r.kv - r.n, r.n);
+    cost = units_of<kLead>(r, tp);
     mine += P.Hkv * cost;
   }
-  long long before = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long t = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += t;
-  }
-  if (lane == 31) sm.scan[warp] = before;
+  long long before, total;
   tc_fence_before();
-  __syncthreads();
+  add_up<kThreads>(mine, sm.scan, before, total);
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;  // S0, S1 at columns 0, 128; O0, O1 at 256, 384
-  long long total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w == warp) before += total;
-    total += sm.scan[w];
-  }
-  before -= mine;
   // q_start falls somewhere, or lengths add up to more than a run can count (through pages shared by many requests)
   const long long most = (long long)gridDim.x * 0x3fffffff;
   if (total > most) {
     if (blockIdx.x == 0 && tid == 0) atomicOr(P.err, WI_DEVERR_BAD_LENGTH);
     rb1 = min(rb1, requests_in_order(P));
-    const Share x = share_of(P, sm, rb0, rb1);
+    const Share x = share_of(P, sm.scan, rb0, rb1);
     mine = x.mine;
     before = x.before;
     total = x.total > most ? 0 : x.total;  // too much still: nothing is done
@@ -344,34 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     return;
   }
   const long long u0 = quot(total * blockIdx.x, ctas), u1 = quot(total * (blockIdx.x + 1), ctas);
-  if (u0 >= before && u0 < before + mine) {  // one thread's requests hold the run's first unit
-    long long rem = u0 - before;
-    for (int b = rb0; b < rb1; ++b) {
-      if (per > 1) r = load_req(P, b);  // else the one request is at hand
-      if (r.n == 0) continue;
-      const int tiles = (r.n + tp - 1) / tp;
-      const long long p0 = (long long)r.kv - r.n;
-      if (per > 1) cost = units_before<kLead>(p0, tp, tiles - 1) + kLead + blocks_to(p0, r.n);
-      if (rem >= cost * P.Hkv) {
-        rem -= cost * P.Hkv;
-        continue;
-      }
-      const int kh = (int)quot(rem, cost);
-      rem -= cost * kh;
-      int lo = 0, hi = tiles - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (units_before<kLead>(p0, tp, mid) <= rem) lo = mid; else hi = mid - 1;
-      }
-      if (lo > 0) rem -= units_before<kLead>(p0, tp, lo);
-      sm.start = {b, kh, lo, (int)rem, (int)(u1 - u0)};
-      sm.req = r;
-      sm.run_end = u1;
-      sm.total = total;
-      sm.ctas = ctas;
-      break;
-    }
-  }
+  if (u0 >= before && u0 < before + mine)  // (where each thread has one request, that is at hand)
+    begin_run<kLead>(P, tp, rb0, rb1, per == 1, r, cost, before, u0, u1, total, ctas, &sm.run);
   __syncthreads();
 
   // a softmax lane holds a row of scores; the registers that the other warps do not need go to those
@@ -411,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     };
     bool more;
     {
-      Walk<LONG> w(P, sm.start, sm.req);
+      Walk<LONG> w(P, sm.run.start, sm.run.req);
       more = begin(w);
     }
     for (int seg = 0; more; ++seg) {
@@ -512,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       const uint32_t to = tmem + lanes + 256u + (w.single ? 0u : (uint32_t)chain * WI_D);
       const int ca = w.single ? 64 * chain : 0, cb = w.single ? ca + 64 : WI_D;  // the columns that this thread takes
       if (LONG && w.nblk > kLongest) {  // maybe not the CTA's first segment of the item, or not its last
-        const int spent = sm.start.left - w.left;
+        const int spent = sm.run.start.left - w.left;
         begun = spent >= w.at - kLead;
         part = !begun || w.b0 + w.nb < w.nblk;
         goes_on = w.b0 + w.nb < w.nblk && w.took < w.left;
@@ -577,8 +520,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       if (LONG && goes_on) {
         // the rest of the item's end is for the last segment that the CTA has of it
       } else if (part && P.tickets) {
-        const long long item = sm.run_end - w.left - w.at + kLead;  // the unit of the item's first block
-        const int c0 = cta_of(item, sm.total, sm.ctas), c1 = cta_of(item + w.nblk - 1, sm.total, sm.ctas);
+        const long long item = sm.run.end - w.left - w.at + kLead;  // the unit of the item's first block
+        const int c0 = cta_of(item, sm.run.total, sm.run.ctas), c1 = cta_of(item + w.nblk - 1, sm.run.total, sm.run.ctas);
         soft_barrier();  // then thread 0's release covers what all of them stored
         if (tid == 0) {
           sm.last = 0;
@@ -601,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       } else if (part && begun && tid == 0) {
         split = true;
         P.splits[blockIdx.x] = {w.r.s0 + w.tile * w.tp, w.kh, w.cnt,
-                                cta_of(sm.run_end - w.left - w.at + kLead + w.nblk - 1, sm.total, sm.ctas)};
+                                cta_of(sm.run.end - w.left - w.at + kLead + w.nblk - 1, sm.run.total, sm.run.ctas)};
       }
       if (w.single) soft_barrier();  // both chains' O, maxima and sums have been read
       w.advance();
@@ -609,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     }
     if (tid == 0 && !split) P.splits[blockIdx.x].last = -1;
   } else if (warp == kSoftWarps) {
-    Walk<LONG> w(P, sm.start, sm.req);
+    Walk<LONG> w(P, sm.run.start, sm.run.req);
     // ---------------- TMA: queries, keys, values
     const uint32_t on = elect_one();
     const int boxes = kRows / P.box;  // boxes of a block, one lane finds the page of each
@@ -687,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
     for (int s = 0; s < filled; ++s)  // the last use of each stage: this turn's in front of `at`, else the turn before
       mbar_wait(&sm.full[s], s < at.s ? at.par : at.par ^ 1u, P.err);
   } else if (warp == kSoftWarps + 1) {
-    Walk<LONG> w(P, sm.start, sm.req);
+    Walk<LONG> w(P, sm.run.start, sm.run.req);
     // ---------------- tensor cores: one lane issues, the whole warp computes what it issues
     {
       const uint32_t on = elect_one();
@@ -804,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
       mbar_wait(&sm.drained, 0, P.err);
     }
   } else {
-    Walk<LONG> w(P, sm.start, sm.req);
+    Walk<LONG> w(P, sm.run.start, sm.run.req);
     // ---------------- clean the value rows of blocks that not every row sees whole
     const int fixer = warp - kSoftWarps - 2;
     Ring at;                     // the ring stage of the next block in turn
@@ -820,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged_attention(const __grid_co
         const int s = at.s;
         // only once the copy has been asked for does the stage's phase stand at this use (these warps are there as soon as
         // they have cleaned what comes before, maybe a whole run ahead)
-        const long long limit = kMbarWaitCycles + (LONG ? sm.start.left * kBlockCycles : 0);
+        const long long limit = kMbarWaitCycles + (LONG ? sm.run.start.left * kBlockCycles : 0);
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.to_fix[s], (fix_par >> s) & 1u, P.err, limit)))) break;
         fix_par ^= 1u << s;
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[s], at.par, P.err)))) break;

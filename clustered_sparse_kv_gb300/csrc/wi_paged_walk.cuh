@@ -189,6 +189,66 @@ struct Run {
   int ctas;              // CTAs with units
 };
 
+// Units of one kv head of a request.
+template <int LEAD>
+__device__ __forceinline__ long long units_of(const Req& r, int tp) {
+  const long long p0 = (long long)r.kv - r.n;
+  return units_before<LEAD>(p0, tp, (r.n + tp - 1) / tp - 1) + LEAD + blocks_to(p0, r.n);
+}
+
+// What the threads in front of this one have, and all of them.  With a barrier of all THREADS; scan: a number per warp.
+template <int THREADS>
+__device__ __forceinline__ void add_up(long long mine, long long* scan, long long& before, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += t;
+  }
+  if (lane == 31) scan[warp] = before;
+  __syncthreads();
+  total = 0;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w == warp) before += total;
+    total += scan[w];
+  }
+  before -= mine;
+}
+
+// The run of units [u0, u1), by the one thread whose requests [rb0, rb1) hold u0; `before` units in front of those.  One
+// request: r, of `cost` units per kv head.
+template <int LEAD>
+__device__ __forceinline__ void begin_run(const Params& P, int tp, int rb0, int rb1, bool one, Req r, long long cost,
+                                          long long before, long long u0, long long u1, long long total, int ctas, Run* run) {
+  long long rem = u0 - before;
+  for (int b = rb0; b < rb1; ++b) {
+    if (!one) r = load_req(P, b);
+    if (r.n == 0) continue;
+    const int tiles = (r.n + tp - 1) / tp;
+    const long long p0 = (long long)r.kv - r.n;
+    if (!one) cost = units_of<LEAD>(r, tp);
+    if (rem >= cost * P.Hkv) {
+      rem -= cost * P.Hkv;
+      continue;
+    }
+    const int kh = (int)quot(rem, cost);
+    rem -= cost * kh;
+    int lo = 0, hi = tiles - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (units_before<LEAD>(p0, tp, mid) <= rem) lo = mid; else hi = mid - 1;
+    }
+    if (lo > 0) rem -= units_before<LEAD>(p0, tp, lo);
+    run->start = {b, kh, lo, (int)rem, (int)(u1 - u0)};
+    run->req = r;
+    run->end = u1;
+    run->total = total;
+    run->ctas = ctas;
+    break;
+  }
+}
+
 // The run that is item i of those of requests [b0, b1): all of it.  Called by one thread.
 template <int LEAD>
 __device__ __noinline__ void own_item(const Params& P, int tp, int b0, int b1, int i, Run* run) {
@@ -225,7 +285,7 @@ __device__ __forceinline__ bool find_run(const Params& P, int least, int whole, 
   long long items, largest;  // this thread's; its largest, in units
   Req r = {0, 0, 0, 1};
   for (int again = 0;; ++again) {
-    mine = total = items = largest = 0;
+    mine = items = largest = 0;
     for (int b = rb0; b < rb1; ++b) {
       r = load_req(P, b);
       if (!r.ok && !again) {
@@ -233,12 +293,10 @@ __device__ __forceinline__ bool find_run(const Params& P, int least, int whole, 
         if (P.a.q_start[b + 1] < r.s0) mine += kFalls;
       }
       if (r.n == 0) continue;
-      const long long p0 = (long long)r.kv - r.n;
-      const long long last = LEAD + blocks_to(p0, r.n);
-      cost = units_before<LEAD>(p0, tp, (r.n + tp - 1) / tp - 1) + last;
+      cost = units_of<LEAD>(r, tp);
       mine += P.Hkv * cost;
       items += P.Hkv * ((r.n + tp - 1) / tp);
-      largest = max(largest, last);
+      largest = max(largest, (long long)LEAD + blocks_to((long long)r.kv - r.n, r.n));
     }
     if (P.a.batch > 1) {
       // of a warp: the largest item, and the items unless they are more than there are CTAs anyway
@@ -246,19 +304,7 @@ __device__ __forceinline__ bool find_run(const Params& P, int least, int whole, 
       const uint32_t count = __reduce_add_sync(0xffffffffu, (uint32_t)min(items, 1LL << 16));
       if (lane == 0) reinterpret_cast<uint2*>(scan)[THREADS / 32 + warp] = make_uint2(units, count);
     }
-    before = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += t;
-    }
-    if (lane == 31) scan[warp] = before;
-    __syncthreads();
-    for (int w = 0; w < THREADS / 32; ++w) {
-      if (w == warp) before += total;
-      total += scan[w];
-    }
-    before -= mine;
+    add_up<THREADS>(mine, scan, before, total);
     if (total <= most) break;
     if (blockIdx.x == 0 && tid == 0) atomicOr(P.err, WI_DEVERR_BAD_LENGTH);
     if (again) {  // too much still: nothing is done
@@ -290,34 +336,8 @@ __device__ __forceinline__ bool find_run(const Params& P, int least, int whole, 
   }
   if ((int)blockIdx.x >= ctas) return false;
   const long long u0 = quot(total * blockIdx.x, ctas), u1 = quot(total * (blockIdx.x + 1), ctas);
-  if (u0 >= before && u0 < before + mine) {  // one thread's requests hold the run's first unit
-    long long rem = u0 - before;
-    for (int b = rb0; b < rb1; ++b) {
-      if (per > 1) r = load_req(P, b);  // else the one request is at hand
-      if (r.n == 0) continue;
-      const int tiles = (r.n + tp - 1) / tp;
-      const long long p0 = (long long)r.kv - r.n;
-      if (per > 1) cost = units_before<LEAD>(p0, tp, tiles - 1) + LEAD + blocks_to(p0, r.n);
-      if (rem >= cost * P.Hkv) {
-        rem -= cost * P.Hkv;
-        continue;
-      }
-      const int kh = (int)quot(rem, cost);
-      rem -= cost * kh;
-      int lo = 0, hi = tiles - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (units_before<LEAD>(p0, tp, mid) <= rem) lo = mid; else hi = mid - 1;
-      }
-      if (lo > 0) rem -= units_before<LEAD>(p0, tp, lo);
-      run->start = {b, kh, lo, (int)rem, (int)(u1 - u0)};
-      run->req = r;
-      run->end = u1;
-      run->total = total;
-      run->ctas = ctas;
-      break;
-    }
-  }
+  if (u0 >= before && u0 < before + mine)  // (where each thread has one request, that is at hand)
+    begin_run<LEAD>(P, tp, rb0, rb1, per == 1, r, cost, before, u0, u1, total, ctas, run);
   __syncthreads();
   return true;
 }
