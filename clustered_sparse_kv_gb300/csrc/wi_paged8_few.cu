@@ -30,11 +30,11 @@
 // the bf16 attention.
 //
 // What bounds it, 32 query and 8 kv heads on one GB300: HBM.  One token over 131K
-// positions in 54 us: 6 until the first scores (lengths, tables, first copies), 38
+// positions in 55 us: 6 until the first scores (lengths, tables, first copies), 38
 // for 268 MB (7.1 TB/s), then the slowest CTA, and 5 for the parts; 64 single tokens
-// over 100 - 8000 positions 69 us, of which 50 are the reads.  A block of 128
-// positions costs a CTA 650 cycles of weights, and HBM gives two CTAs one every
-// 1400.  With one CTA to an SM 91 and 122 us (its stages do not matter); with pages
+// over 100 - 8000 positions 70 us, of which 50 are the reads.  A block of 128
+// positions costs a CTA 700 cycles of weights (1000 with eight rows; with four pieces
+// 600 and 880, and 54 and 69 us), and HBM gives two CTAs one every 1400.  With one CTA to an SM 91 and 122 us (its stages do not matter); with pages
 // and scales looked up a block ahead, not four, 68 and 81; with three CTAs of two
 // stages 56 and 69; with a block's values asked for before the scales of the block in
 // front are stored, the short cases 0.6 us more.
